@@ -1,0 +1,594 @@
+// attention.cu -- attention of a few query rows per key/value head over the paged 8-bit
+// cache: single tokens, draft tokens, short chunks.
+//
+// Bound: the codes, 2 head_dim bytes per key and key/value head, read once for all query
+// rows of that head.  The keys of all sequences and heads form one list of 64-key tiles that
+// is cut evenly over the CTAs, whatever the sequences' lengths; a CTA's share of one head's
+// keys is a piece.  A CTA's warps take a piece's tiles in turn, each with its own ring of
+// bulk copies (a page's keys or values of one head are contiguous), its own running maximum
+// and sum and its own outputs; they are joined through shared memory at the end of the
+// piece.  A head that is cut joins its pieces through the handle's workspace: every CTA has
+// at most two unfinished pieces (its first and its last), the CTA that arrives last adds
+// them in order, so the result does not depend on the schedule.
+//
+// Products on the tensor cores (m16n8k16, fp16 operands, fp32 sums): codes - 128 are exact
+// in fp16; a query row and a row of probabilities take two of the MMA's 16 rows each, the
+// rounded value and what the rounding left (22 bits), so 8 rows fill a tile at no cost over
+// one-term operands.  Both operands' summed axes are permuted so that a lane reads 16
+// consecutive bytes of a key (of a channel of the values) at a time and the scores leave
+// the first product in the layout that the second one takes.
+#include <algorithm>
+
+#include "q4lin_internal.h"
+#include "serving.cuh"
+
+namespace q4lin {
+namespace {
+using namespace ptx;
+using namespace serving;
+
+constexpr int kTile = 64;        // keys per tile
+constexpr int kRows = 8;         // query rows per MMA tile (two of its 16 rows each)
+constexpr int kSlots = 3;        // half tiles (keys or values) in a warp's ring
+constexpr int kMaxBatch = 2048;  // sequences per launch
+constexpr float kShift = 14.f;   // probabilities are kept as 2^14 p: fp16's range downwards
+constexpr int64_t kDrainNs = 4000000000LL;
+
+__host__ __device__ constexpr int warps_of(int D) { return D == 256 ? 4 : 8; }
+__host__ __device__ constexpr int ctas_of(int D, int RT) { return D == 64 && RT == 1 ? 2 : 1; }
+
+struct SplitArgs {
+    q4lin_kv_cache_t cache;
+    q4lin_attention_t a;
+    int page_shift;
+    int64_t rows_max;
+    int q_vec;
+    float* ws;
+    int* tickets;
+    int* status;
+    int64_t wait_ns;
+};
+
+// Per query row of a piece.
+struct RowInfo {
+    float factor;        // of the MMA's scores, without the keys' scale, in powers of two
+    int limit, low;      // keys [low, limit] are seen
+    int64_t index;       // token * heads + head, or -1
+};
+
+template <int D, int RT>
+struct Shared {
+    static constexpr int W = warps_of(D);
+    uint4 q[RT][D / 16][32];  // A fragments
+    RowInfo row[RT * kRows];
+    float m[W][RT * kRows], l[W][RT * kRows];
+    uint64_t full[W][kSlots];
+    int prefix[kMaxBatch + 1];
+    int sums[W];
+    int limit_min, low_max;
+    int failed, last;
+};
+
+struct Sequence {
+    int tq, len, tile0, tiles, row_tiles;
+};
+
+// What one sequence asks of this kernel; nothing where its indices are bad or its rows are
+// too many for it.
+template <int RT>
+__device__ __forceinline__ Sequence sequence_of(const SplitArgs& g, int64_t b, bool* bad) {
+    Sequence s;
+    const int64_t o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1);
+    const int64_t group = g.a.heads / g.cache.kv_heads;
+    s.len = __ldg(g.a.lengths + b);
+    s.tq = (int)(o1 - o0);
+    *bad = o0 < 0 || o1 < o0 || o1 > g.a.tokens || s.tq > g.a.max_query ||
+           (int64_t)s.len > g.cache.pages_per_sequence << g.page_shift ||
+           (g.a.rope.cos && s.len > g.a.rope.positions);
+    if (*bad || s.tq * group > g.rows_max) s.tq = 0;
+    if (s.len < 0) s.len = 0;
+    const int64_t first = g.a.window > 0 ? (int64_t)s.len - s.tq - g.a.window + 1 : 0;
+    s.tile0 = first > 0 ? (int)(first / kTile) : 0;
+    s.tiles = max((s.len + kTile - 1) / kTile - s.tile0, 1);
+    s.row_tiles = (int)((s.tq * group + RT * kRows - 1) / (RT * kRows));
+    return s;
+}
+
+// Four channels of a query row: the joined sums o and l, both as 2^kShift p, over the maximum
+// `base` (a power of two's exponent).
+__device__ __forceinline__ void emit(const SplitArgs& g, int64_t index, int D, int d, float4 o, float l,
+                                     float base) {
+    if (index < 0) return;
+    const float inv = l != 0.f ? 1.f / l : 0.f;  // l == 0: the row sees no key
+    const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    if (g.a.dtype == Q4LIN_DTYPE_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + index * D + d) =
+            make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D + d) =
+            make_uint2(to_16x2(v[0], v[1], g.a.dtype), to_16x2(v[2], v[3], g.a.dtype));
+    if (d == 0 && g.a.lse) g.a.lse[index] = l != 0.f ? (base + lg2(l) - kShift) * kLn2 : -INFINITY;
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_split_kernel(const SplitArgs g) {
+    constexpr int W = warps_of(D), T = 32 * W, R = RT * kRows;
+    constexpr int kNt = D / 8;
+    constexpr uint32_t kHalf = kTile * D;  // bytes of a tile's keys (values)
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared<D, RT> S;
+    const uint32_t ring = (smem_u32(smem_raw) + 127u) & ~127u;
+    float* merge = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));  // [W][R][D]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
+    const q4lin_kv_cache_t& C = g.cache;
+    const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads), ps = g.page_shift;
+    const int ppt = kTile >> ps;  // pages per tile
+
+    // ---- the list of tiles: an inclusive scan over the sequences
+    if (tid == 0) {
+        S.prefix[0] = 0;
+        S.failed = 0;
+        for (int w = 0; w < W; ++w)
+            for (int s = 0; s < kSlots; ++s) mbar_init(smem_u32(&S.full[w][s]), 1);
+        mbar_init_fence();
+    }
+    const int batch = (int)C.batch;
+    int carry = 0;
+    for (int b0 = 0; b0 < batch; b0 += T) {
+        const int b = b0 + tid;
+        int v = 0;
+        if (b < batch) {
+            bool bad;
+            const Sequence s = sequence_of<RT>(g, b, &bad);
+            v = s.tiles * s.row_tiles * Hkv;
+            if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += n;
+        }
+        __syncthreads();
+        if (lane == 31) S.sums[warp] = v;
+        __syncthreads();
+        int before = carry;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) before += S.sums[w];
+            carry += S.sums[w];
+        }
+        if (b < batch) S.prefix[b + 1] = before + v;
+    }
+    __syncthreads();
+    const int total = carry;
+    // Shares of at least a tile per warp.
+    const int share = max(W, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    const int64_t begin = (int64_t)blockIdx.x * share;
+    const int end = (int)min((int64_t)total, begin + share);
+    if (begin >= end) return;
+    uint32_t phase = 0;  // parity bit of each slot's next wait
+
+    for (int pos = (int)begin; pos < end;) {
+        // ---- the piece: tiles [k0, k0 + n) of row tile rt of head h of sequence b
+        int lo = 0, hi = batch;  // prefix[lo] <= pos < prefix[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (S.prefix[mid] <= pos)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int b = lo;
+        bool bad;
+        const Sequence s = sequence_of<RT>(g, b, &bad);
+        const int local = pos - S.prefix[b], seg = local / s.tiles;
+        const int k0 = local - seg * s.tiles, h = seg / s.row_tiles, rt0 = seg - h * s.row_tiles;
+        const int n = min(s.tiles - k0, end - pos);
+        const int seg_begin = pos - k0;  // first tile of the whole head in the list
+        pos += n;
+        const int64_t o0 = __ldg(g.a.offsets + b);
+
+        // ---- queries: rotated, scaled to fp16's upper range by a power of two, split
+        if (tid == 0) S.limit_min = INT_MAX, S.low_max = 0;
+        __syncthreads();
+        constexpr int kUnitsRow = D / 8;               // lanes per row (8 channels each)
+        constexpr int kPer = T / kUnitsRow;            // rows in flight
+        for (int r0 = 0; r0 < R; r0 += kPer) {
+            const int r = r0 + tid / kUnitsRow, u = tid % kUnitsRow;
+            const int row = rt0 * R + r;
+            const bool in = r < R && row < s.tq * group;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            const int token = in ? row / group : 0, head = h * group + (in ? row - token * group : 0);
+            const int position = s.len - s.tq + token;
+            bool turned;
+            int cl, ch;
+            rope_channels(g.a.rope, u, &turned, &cl, &ch);
+            if (in) {
+                const int64_t e = (o0 + token) * g.a.q_token_stride + head * g.a.q_head_stride;
+                load_four(g.a.query, g.a.dtype, e + cl, g.q_vec, x);
+                load_four(g.a.query, g.a.dtype, e + ch, g.q_vec, x + 4);
+                if (turned && position >= 0) rope_unit(g.a.rope, position, u, x);
+            }
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+#pragma unroll
+            for (int o = kUnitsRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            // 2^up brings the row's largest |x| to [2^14, 2^15); its exponent is kept within
+            // what both 2^up and 2^-up can hold.
+            const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
+            const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+            const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+            if (r < R) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int d = w ? ch : cl;  // channels d .. d + 3
+                    uint4 f;
+                    split_f16(x[4 * w] * up, x[4 * w + 1] * up, &f.x, &f.y);
+                    split_f16(x[4 * w + 2] * up, x[4 * w + 3] * up, &f.z, &f.w);
+                    S.q[r / kRows][(d / 64) * 4 + (d % 16) / 4][(r % kRows) * 4 + (d % 64) / 16] = f;
+                }
+                if (u == 0) {
+                    RowInfo i;
+                    i.factor = g.a.scale * kLog2e * down;
+                    i.limit = in && position >= 0 ? (g.a.causal ? position : s.len - 1) : -1;
+                    if (in && !g.a.causal) i.limit = s.len - 1;
+                    const int64_t low = g.a.window > 0 ? (int64_t)position - g.a.window + 1 : 0;
+                    i.low = low > 0 ? (int)low : 0;
+                    i.index = in ? (o0 + token) * g.a.heads + head : -1;
+                    S.row[r] = i;
+                    if (in) {
+                        atomicMin(&S.limit_min, i.limit);
+                        atomicMax(&S.low_max, i.low);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+
+        // ---- this warp's tiles
+        const int cnt = s.len > 0 && n > warp ? (n - warp + W - 1) / W : 0;
+        const int first = s.tile0 + k0 + warp;  // its tiles: first, first + W, ...
+        const int32_t* table = C.page_table + b * C.table_stride;
+        const uint32_t page_bytes = (uint32_t)(D << ps);
+        const int pages = (s.len + (1 << ps) - 1) >> ps;
+        // Pages of the next 32 / ppt tiles: lane i holds page (i % ppt) of tile i / ppt.
+        int ids = 0;
+        auto fetch_ids = [&](int i) {
+            const int tile = first + (i + lane / ppt) * W, p = tile * ppt + lane % ppt;
+            ids = -1;
+            if (i + lane / ppt < cnt && p < pages) {
+                ids = __ldg(table + p);
+                if (ids < 0 || ids >= C.num_pages) {
+                    atomicCAS(g.status, 0, kStatusIndex);
+                    ids = 0;  // read something of the cache rather than nothing
+                }
+            }
+        };
+        const int batch_tiles = 32 / ppt;
+        int issued = 0;
+        // Half tile u (keys of tile u / 2, then its values) into its slot of the ring.
+        auto issue = [&]() {
+            if (issued >= 2 * cnt) return;
+            const int i = issued >> 1, slot = issued % kSlots;
+            if ((issued & 1) == 0 && i % batch_tiles == 0) fetch_ids(i);
+            const int id = __shfl_sync(0xffffffffu, ids, (i % batch_tiles) * ppt + lane % ppt);
+            const bool mine = lane < ppt && id >= 0;
+            const int count = __popc(__ballot_sync(0xffffffffu, mine));
+            const uint32_t bar = smem_u32(&S.full[warp][slot]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * page_bytes);
+            __syncwarp();
+            if (mine) {
+                const uint8_t* base = issued & 1 ? C.v_codes : C.k_codes;
+                bulk_load(ring + (uint32_t)(warp * kSlots + slot) * kHalf + lane * page_bytes,
+                          base + ((int64_t)id * Hkv + h) * page_bytes, page_bytes, bar);
+            }
+            ++issued;
+        };
+        // The scales of this lane's 16 keys of tile i (one page each).
+        float sk_next = 0.f, sv_next = 0.f;
+        auto fetch_scales = [&](int i) {
+            const int p = (first + i * W) * ppt + ((t * 16) >> ps);
+            sk_next = sv_next = 0.f;
+            if (i < cnt && p < pages) {
+                int id = __ldg(table + p);
+                if (id < 0 || id >= C.num_pages) id = 0;
+                sk_next = __ldg(C.k_scales + (int64_t)id * Hkv + h);
+                sv_next = __ldg(C.v_scales + (int64_t)id * Hkv + h);
+            }
+        };
+
+        float O[RT][kNt][2], m_run[RT], l_run[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            m_run[rt] = -INFINITY, l_run[rt] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kNt; ++i) O[rt][i][0] = O[rt][i][1] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) issue();
+        fetch_scales(0);
+        int waited = 0;
+        bool ok = true;
+        auto await = [&]() {
+            const int slot = waited % kSlots;
+            const uint32_t bar = smem_u32(&S.full[warp][slot]);
+            const bool done = wait_bounded(bar, (phase >> slot) & 1u, g.wait_ns, &S.failed);
+            ok = __all_sync(0xffffffffu, done);
+            if (ok) phase ^= 1u << slot, ++waited;
+        };
+        const RowInfo* rows = S.row;
+        const int limit_min = S.limit_min, low_max = S.low_max;
+
+        for (int i = 0; i < cnt; ++i) {
+            const float sk = sk_next, sv = sv_next;
+            fetch_scales(i + 1);
+            const int key0 = (first + i * W) * kTile + t * 16;  // first of this lane's 16 keys
+            // ---- scores: 8 column tiles of 8 keys; key of column c of tile j:
+            // (c / 2) 16 + 2 j + c % 2, so that this lane's are key0 .. key0 + 15
+            uint32_t slot_at = ring + (uint32_t)(warp * kSlots + waited % kSlots) * kHalf;
+            await();
+            if (!ok) break;
+            float sc[RT][8][4];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[rt][j][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint4 qf[RT][4];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) qf[rt][k] = S.q[rt][4 * c + k][lane];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int key = (gq >> 1) * 16 + 2 * j + (gq & 1);
+                    const uint4 w = ld_shared_v4(slot_at + (uint32_t)(key * D + c * 64 + t * 16));
+                    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t b0, b1;
+                        codes_f16(words[k], &b0, &b1);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) mma_f16(sc[rt][j], qf[rt][k], b0, b1);
+                    }
+                }
+            }
+            __syncwarp();
+            issue();  // the slot of the keys is free
+
+            // ---- softmax: running maximum and sum; weights of the values, two fp16 terms
+            float sv_max = sv;
+            if (ppt > 1) {
+                sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, 1));
+                sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, 2));
+            }
+            const float ratio = ppt > 1 ? (sv_max > 0.f ? __fdividef(sv, sv_max) : 0.f) : 1.f;
+            const int tile_key = (first + i * W) * kTile;
+            const bool inside = tile_key >= low_max && tile_key + kTile - 1 <= limit_min;
+            uint4 pf[RT][4];
+            float alpha[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const RowInfo& row = rows[rt * kRows + gq];
+                const float f = row.factor * sk;
+                float p[8][2], mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) p[j][e] = (sc[rt][j][e] + sc[rt][j][2 + e]) * f;
+                if (!inside) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + 2 * j + e;
+                            if (key < row.low || key > row.limit) p[j][e] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(p[j][0], p[j][1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                mx = fmaxf(mx, m_run[rt]);
+                const float base = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing yet
+                alpha[rt] = ex2(m_run[rt] - base);
+                m_run[rt] = mx;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        p[j][e] = ex2(p[j][e] - base + kShift);
+                        sum += p[j][e];
+                        p[j][e] *= ratio;
+                    }
+                l_run[rt] = fmaf(l_run[rt], alpha[rt], sum);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    split_f16(p[2 * k][0], p[2 * k][1], &pf[rt][k].x, &pf[rt][k].y);
+                    split_f16(p[2 * k + 1][0], p[2 * k + 1][1], &pf[rt][k].z, &pf[rt][k].w);
+                }
+            }
+
+            // ---- outputs: channel tile nt of 8, the tile's 64 keys in 4 steps
+            slot_at = ring + (uint32_t)(warp * kSlots + waited % kSlots) * kHalf;
+            await();
+            if (!ok) break;
+            const uint32_t v_at = slot_at + (uint32_t)((((t * 16) >> ps) * (D << ps)) + ((t * 16) & ((1 << ps) - 1)) + (gq << ps));
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+                const uint4 w = ld_shared_v4(v_at + (uint32_t)((nt * 8) << ps));
+                const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                float acc[RT][4];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[rt][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t b0, b1;
+                    codes_f16(words[k], &b0, &b1);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) mma_f16(acc[rt], pf[rt][k], b0, b1);
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        O[rt][nt][e] = fmaf(acc[rt][e] + acc[rt][2 + e], sv_max, O[rt][nt][e] * alpha[rt]);
+            }
+            __syncwarp();
+            issue();
+        }
+        if (!ok && lane == 0) record_failure(g.status, &S.failed);
+        // Copies still in flight (only after a failed wait) must land before the CTA leaves.
+        for (; waited < issued; ++waited) {
+            const int slot = waited % kSlots;
+            wait_bounded(smem_u32(&S.full[warp][slot]), (phase >> slot) & 1u, kDrainNs, nullptr);
+            phase ^= 1u << slot;
+        }
+
+        // ---- join the warps: the ring holds nothing any more.  (After a failed wait, too: the
+        // tickets have to come out even; the outputs are undefined then.)
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float l = l_run[rt];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int r = rt * kRows + gq;
+            if (t == 0) S.m[warp][r] = m_run[rt], S.l[warp][r] = l;
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt)
+                *reinterpret_cast<float2*>(merge + ((size_t)warp * R + r) * D + nt * 8 + 2 * t) =
+                    make_float2(O[rt][nt][0], O[rt][nt][1]);
+        }
+        __syncthreads();
+        const bool whole = n == s.tiles;
+        // Partial pieces: slot 0 for the CTA's first (begun by an earlier CTA), 1 for its last.
+        constexpr int kPart = R * (D + 2);
+        float* part = g.ws + ((int64_t)blockIdx.x * 2 + (k0 == 0)) * kPart;
+        constexpr int kQuads = R * D / 4;
+        for (int i = tid; i < kQuads; i += T) {
+            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < W; ++w) mx = fmaxf(mx, S.m[w][r]);
+            const float base = mx == -INFINITY ? 0.f : mx;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float c = ex2(S.m[w][r] - base);
+                const float4 v = *reinterpret_cast<const float4*>(merge + ((size_t)w * R + r) * D + d);
+                o.x = fmaf(v.x, c, o.x), o.y = fmaf(v.y, c, o.y);
+                o.z = fmaf(v.z, c, o.z), o.w = fmaf(v.w, c, o.w);
+                l = fmaf(S.l[w][r], c, l);
+            }
+            if (!whole) {
+                *reinterpret_cast<float4*>(part + r * D + d) = o;
+                if (d == 0) part[R * D + r] = mx, part[R * D + R + r] = l;
+                continue;
+            }
+            emit(g, S.row[r].index, D, d, o, l, base);
+        }
+        if (!whole) {
+            // The CTAs that share this head's keys: c0 .. c1.
+            const int c0 = seg_begin / share, c1 = (seg_begin + s.tiles - 1) / share;
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();
+                S.last = atomicAdd(g.tickets + c0, 1) == c1 - c0;
+                __threadfence();
+                if (S.last) g.tickets[c0] = 0;
+            }
+            __syncthreads();
+            if (S.last) {
+                for (int i = tid; i < kQuads; i += T) {
+                    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+                    const int64_t index = S.row[r].index;
+                    if (index < 0) continue;
+                    float mx = -INFINITY;
+                    for (int c = c0; c <= c1; ++c)
+                        mx = fmaxf(mx, __ldcg(g.ws + ((int64_t)c * 2 + (c == c0)) * kPart + R * D + r));
+                    const float base = mx == -INFINITY ? 0.f : mx;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float l = 0.f;
+#pragma unroll 4
+                    for (int c = c0; c <= c1; ++c) {
+                        const float* src = g.ws + ((int64_t)c * 2 + (c == c0)) * kPart;
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
+                        const float k = ex2(__ldcg(src + R * D + r) - base);
+                        o.x = fmaf(v.x, k, o.x), o.y = fmaf(v.y, k, o.y);
+                        o.z = fmaf(v.z, k, o.z), o.w = fmaf(v.w, k, o.w);
+                        l = fmaf(__ldcg(src + R * D + R + r), k, l);
+                    }
+                    emit(g, index, D, d, o, l, base);
+                }
+            }
+        }
+        // The next piece's copies write where the joined outputs were.
+        fence_async_shared();
+        __syncthreads();
+    }
+}
+
+template <int D, int RT>
+cudaError_t launch(const SplitArgs& g, int64_t grid, cudaStream_t stream) {
+    constexpr int bytes = warps_of(D) * kSlots * kTile * D + 128;
+    const cudaError_t e = kernel_smem_once<attention_split_kernel<D, RT>>(bytes);
+    if (e != cudaSuccess) return e;
+    attention_split_kernel<D, RT><<<(unsigned)grid, 32 * warps_of(D), bytes, stream>>>(g);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
+                                   int64_t rows_max, const LaunchCtx& c) {
+    const int64_t group = a.heads / cache.kv_heads;
+    const int64_t rows = std::min(rows_max, a.max_query * group);
+    const int D = (int)cache.head_dim;
+    const bool two = rows > kRows && D != 256;
+    const int R = two ? 2 * kRows : kRows;
+    cudaError_t err = cudaSuccess;
+    // Sequences in groups that the kernel's list holds.
+    for (int64_t b = 0; b < cache.batch && err == cudaSuccess; b += kMaxBatch) {
+        SplitArgs g;
+        g.cache = cache;
+        g.a = a;
+        g.cache.batch = std::min<int64_t>(kMaxBatch, cache.batch - b);
+        g.cache.page_table += b * cache.table_stride;
+        g.a.offsets += b;
+        g.a.lengths += b;
+        g.page_shift = cache.page_size == 16 ? 4 : cache.page_size == 32 ? 5 : 6;
+        g.rows_max = rows_max;
+        g.q_vec = reinterpret_cast<uintptr_t>(a.query) % (4 * dtype_size(a.dtype)) == 0 &&
+                  a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;
+        g.ws = c.ws;
+        g.tickets = c.tickets;
+        g.status = c.status_word;
+        g.wait_ns = c.wait_limit_ns;
+        // No more CTAs than tiles of the longest possible list; one or two per SM.
+        const int64_t tiles = (cache.pages_per_sequence * cache.page_size + kTile - 1) / kTile;
+        const int64_t row_tiles = std::min((a.tokens * group + R - 1) / R + g.cache.batch,
+                                           ((rows + R - 1) / R) * g.cache.batch);
+        const int64_t grid = std::max<int64_t>(
+            1, std::min<int64_t>((int64_t)c.sm_count * ctas_of(D, two ? 2 : 1),
+                                 (tiles * row_tiles * cache.kv_heads + warps_of(D) - 1) / warps_of(D)));
+        switch (D) {
+            case 64: err = two ? launch<64, 2>(g, grid, c.stream) : launch<64, 1>(g, grid, c.stream); break;
+            case 128: err = two ? launch<128, 2>(g, grid, c.stream) : launch<128, 1>(g, grid, c.stream); break;
+            default: err = launch<256, 1>(g, grid, c.stream); break;
+        }
+    }
+    return err;
+}
+
+}  // namespace q4lin

@@ -15,30 +15,18 @@
 
 #include <new>
 
+#include "handle.h"
 #include "q4lin_internal.h"
-
-struct q4lin_handle {
-    int device = 0;
-    int sm_count = 0;
-    int max_smem_optin = 0;
-    int force_path = Q4LIN_PATH_AUTO;
-    int even_high = 0;
-    int pdl = 0;
-    int64_t wait_limit = 0;  // ns; 0: default
-    int tc_skip_first_copy = 0;
-    int tc_f16 = 0;
-    int tc_small_operands = 0;
-    int* d_status = nullptr;
-    float* d_ws = nullptr;     // split-K partial sums
-    int* d_tickets = nullptr;  // split-K row-block counters (zero between launches)
-};
 
 namespace {
 
-constexpr int64_t kDefaultWaitLimit = 2000000000LL;  // 2 s of GPU global time
-// Scratch of a handle: partial sums of split-K launches and their row-block counters.
-constexpr int64_t kWsFloats = 1 << 24;   // 64 MiB (split-K partials; the fp16 copy of x)
-constexpr int64_t kTickets = 1 << 14;    // 64 KiB
+using q4lin::DeviceGuard;
+using q4lin::kDefaultWaitLimit;
+using q4lin::kTickets;
+using q4lin::kWsFloats;
+using q4lin::make_ctx;
+using q4lin::mul_ok;
+using q4lin::overlaps;
 
 // M-dispatch between the CUDA-core kernels (the row-streaming kernel, which re-reads the
 // weights for every 4 activation rows, so its time grows with M, and the TMA-fed multi-row
@@ -95,31 +83,6 @@ bool tc_small_preferred(const q4lin::Problem& p, const q4lin::LaunchCtx& c) {
     return blocks >= 100;
 }
 
-class DeviceGuard {
-   public:
-    explicit DeviceGuard(int device) {
-        if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
-        if (prev_ != device) ok_ = cudaSetDevice(device) == cudaSuccess;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev_ >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev_) cudaSetDevice(prev_);
-    }
-    bool ok() const { return ok_; }
-
-   private:
-    int prev_ = -1;
-    bool ok_ = true;
-};
-
-bool mul_ok(int64_t a, int64_t b, int64_t* r) { return !__builtin_mul_overflow(a, b, r); }
-
-bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-    if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
-}
-
 // Validation shared by q4lin_run and q4lin_plan.  On success fills `p` (except the
 // out pointer for plan) and returns Q4LIN_OK; M == 0 or N == 0 is reported via *empty.
 q4lin_status_t validate(q4lin_handle_t h, const float* x, const uint8_t* qweight,
@@ -163,24 +126,6 @@ q4lin_status_t validate(q4lin_handle_t h, const float* x, const uint8_t* qweight
     p->scale_f16 = scale_dtype == Q4LIN_SCALE_F16;
     p->even_high = h->even_high;
     return Q4LIN_OK;
-}
-
-q4lin::LaunchCtx make_ctx(q4lin_handle_t h, cudaStream_t stream) {
-    q4lin::LaunchCtx c;
-    c.stream = stream;
-    c.sm_count = h->sm_count;
-    c.max_smem_optin = h->max_smem_optin;
-    c.pdl = h->pdl;
-    c.status_word = h->d_status;
-    c.wait_limit_ns = h->wait_limit > 0 ? h->wait_limit : kDefaultWaitLimit;
-    c.tc_skip_first_copy = h->tc_skip_first_copy;
-    c.tc_f16 = h->tc_f16;
-    c.tc_small_operands = h->tc_small_operands;
-    c.ws = h->d_ws;
-    c.ws_floats = kWsFloats;
-    c.tickets = h->d_tickets;
-    c.ticket_count = kTickets;
-    return c;
 }
 
 // Which kernel family runs the problem.

@@ -8,6 +8,8 @@
 
 #include <atomic>
 
+#include "../../include/q4lin.h"
+
 namespace q4lin {
 
 // Function attributes belong to the function's instance in one device's context: a kernel
@@ -146,5 +148,16 @@ bool tc_small_uses_bf16(const Problem& p, const LaunchCtx& c);
 // items fit one wave, within the handle's split-K workspace and tickets.
 int tc_small_parts(const Problem& p, const LaunchCtx& c);
 cudaError_t tc_small_launch(const Problem& p, const LaunchCtx& c);
+
+// Operators around the linears, on arguments that the host layer (operators.cpp) has
+// validated.  What they read on the device (indices) they check there.
+cudaError_t kv_append_launch(const q4lin_kv_cache_t& cache, const q4lin_kv_append_t& a,
+                             const LaunchCtx& c);
+// attention.cu: keys split evenly over the SMs; sequences of up to `rows_max` query rows
+// per key/value head (a row: one query token of one head).
+cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
+                                   int64_t rows_max, const LaunchCtx& c);
+cudaError_t logprobs_launch(const q4lin_logprobs_t& a, const LaunchCtx& c);
+cudaError_t logprobs_backward_launch(const q4lin_logprobs_backward_t& a, const LaunchCtx& c);
 
 }  // namespace q4lin

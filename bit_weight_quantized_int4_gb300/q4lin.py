@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq4lin.so")
 if not os.path.exists(_LIB_PATH):
@@ -53,6 +53,10 @@ Q4LIN_KERNEL_TC_SMALL_BF16 = 9
 KERNEL_NAMES = {0: "none", 1: "gemv_tma", 2: "multirow", 3: "rowstream", 4: "generic",
                 5: "tc", 6: "tc_f16", 7: "gemv_tma_fixed", 8: "tc_small", 9: "tc_small_bf16"}
 
+Q4LIN_DTYPE_F32 = 0
+Q4LIN_DTYPE_F16 = 1
+Q4LIN_DTYPE_BF16 = 2
+
 Q4LIN_OPT_FORCE_PATH = 1
 Q4LIN_OPT_NIBBLE_EVEN_HIGH = 2
 Q4LIN_OPT_WAIT_LIMIT = 3
@@ -84,6 +88,54 @@ _lib.q4lin_run_backward_dx.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64
 _lib.q4lin_run_backward_dx.restype = _i32
 _lib.q4lin_run_requant.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp]
 _lib.q4lin_run_requant.restype = _i32
+
+
+class q4lin_kv_cache_t(ctypes.Structure):
+    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp),
+                ("page_table", _vp), ("num_pages", _i64), ("kv_heads", _i64),
+                ("page_size", _i64), ("head_dim", _i64), ("batch", _i64),
+                ("pages_per_sequence", _i64), ("table_stride", _i64)]
+
+
+class q4lin_rope_t(ctypes.Structure):
+    _fields_ = [("cos", _vp), ("sin", _vp), ("positions", _i64), ("rotated", _i64),
+                ("interleaved", _i32)]
+
+
+class q4lin_kv_append_t(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_token_stride", _i64), ("k_head_stride", _i64),
+                ("v_token_stride", _i64), ("v_head_stride", _i64), ("dtype", _i32),
+                ("tokens", _i64), ("offsets", _vp), ("starts", _vp), ("rope", q4lin_rope_t)]
+
+
+class q4lin_attention_t(ctypes.Structure):
+    _fields_ = [("query", _vp), ("q_token_stride", _i64), ("q_head_stride", _i64), ("out", _vp),
+                ("lse", _vp), ("dtype", _i32), ("tokens", _i64), ("heads", _i64),
+                ("max_query", _i64), ("offsets", _vp), ("lengths", _vp),
+                ("scale", ctypes.c_float), ("causal", _i32), ("window", _i64),
+                ("rope", q4lin_rope_t)]
+
+
+class q4lin_logprobs_t(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("row_stride", _i64), ("dtype", _i32), ("rows", _i64),
+                ("vocabulary", _i64), ("tokens", _vp), ("logprob", _vp), ("entropy", _vp),
+                ("lse", _vp), ("top", _i64), ("top_tokens", _vp), ("top_logprobs", _vp)]
+
+
+class q4lin_logprobs_backward_t(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("row_stride", _i64), ("dtype", _i32), ("rows", _i64),
+                ("vocabulary", _i64), ("tokens", _vp), ("lse", _vp), ("entropy", _vp),
+                ("d_logprob", _vp), ("d_entropy", _vp), ("d_logits", _vp),
+                ("d_row_stride", _i64)]
+
+
+for _name, _types in (("q4lin_run_kv_append", (q4lin_kv_cache_t, q4lin_kv_append_t)),
+                      ("q4lin_run_attention", (q4lin_kv_cache_t, q4lin_attention_t)),
+                      ("q4lin_run_logprobs", (q4lin_logprobs_t,)),
+                      ("q4lin_run_logprobs_backward", (q4lin_logprobs_backward_t,))):
+    _f = getattr(_lib, _name)
+    _f.argtypes = [_vp, *(ctypes.POINTER(t) for t in _types), _vp]
+    _f.restype = _i32
 _lib.q4lin_plan.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32,
                             ctypes.POINTER(_i32)]
 _lib.q4lin_plan.restype = _i32
@@ -200,6 +252,26 @@ def q4lin_check_device_status(handle, stream):
     return st, code.value
 
 
+def q4lin_run_kv_append(handle, cache, args, stream) -> int:
+    """cache: q4lin_kv_cache_t; args: q4lin_kv_append_t (pointers as integers)."""
+    return _lib.q4lin_run_kv_append(handle, cache, args, stream)
+
+
+def q4lin_run_attention(handle, cache, args, stream) -> int:
+    """cache: q4lin_kv_cache_t; args: q4lin_attention_t."""
+    return _lib.q4lin_run_attention(handle, cache, args, stream)
+
+
+def q4lin_run_logprobs(handle, args, stream) -> int:
+    """args: q4lin_logprobs_t."""
+    return _lib.q4lin_run_logprobs(handle, args, stream)
+
+
+def q4lin_run_logprobs_backward(handle, args, stream) -> int:
+    """args: q4lin_logprobs_backward_t."""
+    return _lib.q4lin_run_logprobs_backward(handle, args, stream)
+
+
 # ---------------------------------------------------------------- torch convenience
 class Handle:
     """Owns a q4lin handle for one CUDA device."""
@@ -285,3 +357,212 @@ def plan_kernel(handle: Handle, x, qweight, scales, bias, group_size: int, out) 
     if st != Q4LIN_OK:
         raise Q4LinError(st, "q4lin_plan_kernel")
     return KERNEL_NAMES[kernel]
+
+
+# ------------------------------------------------- operators around the linears (torch)
+def _dtype_code(t, what):
+    code = {"torch.float32": Q4LIN_DTYPE_F32, "torch.float16": Q4LIN_DTYPE_F16,
+            "torch.bfloat16": Q4LIN_DTYPE_BF16}.get(str(t.dtype))
+    if code is None:
+        raise ValueError(f"{what} must be float32, float16 or bfloat16")
+    return code
+
+
+def _check_device(handle, *tensors):
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != handle.device):
+            raise ValueError(f"every tensor must be on the handle's device, cuda:{handle.device}")
+
+
+def _check_vector(t, n, kind, what):
+    """A contiguous one-dimensional tensor of n int32 ("int32") or float32 values."""
+    if str(t.dtype) != "torch." + kind or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {kind} [{n}] tensor")
+    return t.data_ptr()
+
+
+def _check_heads(t, what):
+    """[tokens, heads, head_dim] with contiguous channels."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous channels")
+
+
+def _stream_of(stream, t) -> int:
+    if stream is not None:
+        return stream
+    import torch
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _rope_args(rope, interleaved):
+    if rope is None:
+        return q4lin_rope_t()
+    cos, sin = rope
+    for t in rope:
+        if str(t.dtype) != "torch.float32" or t.dim() != 2 or not t.is_contiguous() \
+                or t.shape != cos.shape:
+            raise ValueError("rope must be two contiguous float32 [positions, rotated / 2] tensors")
+    return q4lin_rope_t(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1],
+                        int(interleaved))
+
+
+class KVCache:
+    """The tensors of a paged 8-bit key/value cache (q4lin_kv_cache_t).
+
+    k_codes uint8 [num_pages, kv_heads, page_size, head_dim], v_codes uint8 [num_pages,
+    kv_heads, head_dim, page_size], k_scales and v_scales float32 [num_pages, kv_heads],
+    page_table int32 [batch, pages per sequence].  The tensors stay the caller's; the page
+    table's contents may change between calls."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, page_table):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim]")
+        pages, heads, page, dim = k_codes.shape
+        for t, shape, kind, what in ((k_codes, (pages, heads, page, dim), "uint8", "k_codes"),
+                                     (v_codes, (pages, heads, dim, page), "uint8", "v_codes"),
+                                     (k_scales, (pages, heads), "float32", "k_scales"),
+                                     (v_scales, (pages, heads), "float32", "v_scales")):
+            if tuple(t.shape) != shape or str(t.dtype) != "torch." + kind or not t.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous {kind} {list(shape)} tensor")
+        if page_table.dim() != 2 or str(page_table.dtype) != "torch.int32" or \
+                (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be an int32 [batch, pages] tensor with contiguous rows")
+        if len({t.device for t in (k_codes, k_scales, v_codes, v_scales, page_table)}) != 1:
+            raise ValueError("a cache's tensors must be on one device")
+        self.k_codes, self.k_scales = k_codes, k_scales
+        self.v_codes, self.v_scales = v_codes, v_scales
+        self.page_table = page_table
+        batch, width = page_table.shape
+        stride = page_table.stride(0) if batch > 1 else width
+        self.args = q4lin_kv_cache_t(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                     v_scales.data_ptr(), page_table.data_ptr(), pages, heads, page,
+                                     dim, batch, width, stride)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, page_table):
+        """A cache with nothing in it, on the page table's device."""
+        import torch
+        new = lambda *shape: torch.full(shape, 128, dtype=torch.uint8, device=page_table.device)
+        scales = lambda: torch.zeros(num_pages, kv_heads, device=page_table.device)
+        return cls(new(num_pages, kv_heads, page_size, head_dim), scales(),
+                   new(num_pages, kv_heads, head_dim, page_size), scales(), page_table)
+
+
+def kv_append(handle: Handle, cache: KVCache, k, v, offsets, starts, rope=None,
+              interleaved: bool = False, stream=None) -> None:
+    """Append k (rotated by rope = (cos, sin) on the way) and v, [tokens, kv_heads, head_dim]
+    each and possibly slices of a larger tensor, to the cache: rows offsets[b] ..
+    offsets[b + 1] become tokens starts[b], starts[b] + 1, ... of sequence b."""
+    c = cache.args
+    _check_device(handle, cache.k_codes, k, v, offsets, starts, *(rope or ()))
+    _check_heads(k, "k")
+    if k.shape != v.shape or k.shape[1] != c.kv_heads or k.shape[2] != c.head_dim or \
+            v.dtype != k.dtype:
+        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one type, as the cache")
+    _check_heads(v, "v")
+    args = q4lin_kv_append_t(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0),
+                             v.stride(1), _dtype_code(k, "k"), k.shape[0],
+                             _check_vector(offsets, c.batch + 1, "int32", "offsets"),
+                             _check_vector(starts, c.batch, "int32", "starts"),
+                             _rope_args(rope, interleaved))
+    st = _lib.q4lin_run_kv_append(handle.ptr, c, args, _stream_of(stream, k))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st, "q4lin_run_kv_append")
+
+
+def attention(handle: Handle, cache: KVCache, query, offsets, lengths, scale: float,
+              max_query: Optional[int] = None, rope=None, interleaved: bool = False,
+              causal: bool = True, window: int = 0, out=None, lse=None, stream=None):
+    """Attention of query [tokens, heads, head_dim] over the cache (q4lin_run_attention).
+    lengths[b] counts sequence b's tokens in the cache, those of its queries included;
+    max_query: no sequence has more query tokens (default: all of them).  Returns (out, lse):
+    out like query, lse float32 [tokens, heads]."""
+    import torch
+    c = cache.args
+    _check_device(handle, cache.k_codes, query, offsets, lengths, out, lse, *(rope or ()))
+    _check_heads(query, "query")
+    tokens, heads, dim = query.shape
+    if dim != c.head_dim or heads % c.kv_heads:
+        raise ValueError("query must be [tokens, heads, head_dim], heads a multiple of kv_heads")
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=query.dtype, device=query.device)
+    elif out.shape != query.shape or out.dtype != query.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous, with the query's shape and type")
+    if lse is None:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=query.device)
+    elif tuple(lse.shape) != (tokens, heads) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
+    args = q4lin_attention_t(query.data_ptr(), query.stride(0), query.stride(1), out.data_ptr(),
+                             lse.data_ptr(), _dtype_code(query, "query"), tokens, heads,
+                             tokens if max_query is None else max_query,
+                             _check_vector(offsets, c.batch + 1, "int32", "offsets"),
+                             _check_vector(lengths, c.batch, "int32", "lengths"), scale,
+                             int(causal), window, _rope_args(rope, interleaved))
+    st = _lib.q4lin_run_attention(handle.ptr, c, args, _stream_of(stream, query))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st, "q4lin_run_attention")
+    return out, lse
+
+
+class LogProbs(NamedTuple):
+    """Results of logprobs: float32 [rows] each; the top alternatives (None without any) as
+    int32 and float32 [rows, top], largest first."""
+    logprob: object
+    entropy: object
+    lse: object
+    top_tokens: object
+    top_logprobs: object
+
+
+def _check_logits(t, what):
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{what} must be [rows, vocabulary] with contiguous rows")
+
+
+def logprobs(handle: Handle, logits, tokens=None, top: int = 0, stream=None) -> LogProbs:
+    """Log probability of tokens (int32 [rows], -1 for none), entropy, log-sum-exp and the
+    `top` most likely tokens of each row of logits (q4lin_run_logprobs)."""
+    import torch
+    _check_device(handle, logits, tokens)
+    _check_logits(logits, "logits")
+    rows, vocabulary = logits.shape
+    small = torch.empty((3, rows), dtype=torch.float32, device=logits.device)
+    logprob, entropy, lse = small.unbind()
+    ids = best = None
+    if top:
+        ids = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
+        best = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
+    args = q4lin_logprobs_t(
+        logits.data_ptr(), logits.stride(0), _dtype_code(logits, "logits"), rows, vocabulary,
+        None if tokens is None else _check_vector(tokens, rows, "int32", "tokens"),
+        logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top, _ptr(ids), _ptr(best))
+    st = _lib.q4lin_run_logprobs(handle.ptr, args, _stream_of(stream, logits))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st, "q4lin_run_logprobs")
+    return LogProbs(logprob, entropy, lse, ids, best)
+
+
+def logprobs_backward(handle: Handle, logits, tokens, lse, entropy, d_logprob=None,
+                      d_entropy=None, out=None, stream=None):
+    """Gradient for the logits of logprobs' logprob and entropy, given theirs (float32 [rows]
+    or None for zeros) and the lse and entropy that logprobs returned.  out may be the logits
+    themselves."""
+    import torch
+    _check_device(handle, logits, tokens, lse, entropy, d_logprob, d_entropy, out)
+    _check_logits(logits, "logits")
+    rows, vocabulary = logits.shape
+    if out is None:
+        out = torch.empty((rows, vocabulary), dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the logits' shape and type")
+    _check_logits(out, "out")
+    vector = lambda t, kind, what: None if t is None else _check_vector(t, rows, kind, what)
+    args = q4lin_logprobs_backward_t(
+        logits.data_ptr(), logits.stride(0), _dtype_code(logits, "logits"), rows, vocabulary,
+        vector(tokens, "int32", "tokens"), vector(lse, "float32", "lse"),
+        vector(entropy, "float32", "entropy"), vector(d_logprob, "float32", "d_logprob"),
+        vector(d_entropy, "float32", "d_entropy"), out.data_ptr(), out.stride(0))
+    st = _lib.q4lin_run_logprobs_backward(handle.ptr, args, _stream_of(stream, logits))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st, "q4lin_run_logprobs_backward")
+    return out

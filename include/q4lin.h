@@ -262,6 +262,165 @@ Q4LIN_API q4lin_status_t q4lin_run_requant(q4lin_handle_t handle, const float* l
                                            int64_t K, int64_t group_size, int scale_dtype,
                                            void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Operators around the linears: a paged 8-bit key/value cache, attention over it, and the
+ * log probabilities of the vocabulary head's output with their gradient.
+ *
+ * Every index array (page table, offsets, starts, lengths, tokens) is read on the device
+ * only.  An index that points outside its array (a page >= num_pages or < 0, a position
+ * past the page table or the rotation table, offsets that decrease or pass `tokens`, a
+ * token >= vocabulary) makes the kernel leave out what it would have touched and record
+ * code 4 in the handle's status word; nothing out of range is read or written. */
+
+/* Element type of keys, values, queries, attention outputs and logits. */
+typedef enum { Q4LIN_DTYPE_F32 = 0, Q4LIN_DTYPE_F16 = 1, Q4LIN_DTYPE_BF16 = 2 } q4lin_dtype_t;
+
+/* A key/value cache in pages of page_size tokens.  A code c (one byte) of page p and head h
+ * stands for (c - 128) * scale[p, h]; codes are 1..255.
+ *   k_codes   uint8 [num_pages, kv_heads, page_size, head_dim], 16-byte aligned
+ *   v_codes   uint8 [num_pages, kv_heads, head_dim, page_size], 16-byte aligned (values
+ *             are kept transposed within a page, so that both products of the attention
+ *             read 16 consecutive bytes along the axis that they sum over)
+ *   k_scales, v_scales  float32 [num_pages, kv_heads]
+ *   page_table int32 [batch, table_stride]: entry (b, j) is the page of tokens
+ *             [j * page_size, (j + 1) * page_size) of sequence b, j < pages_per_sequence.
+ *             Entries past a sequence's length are not read (they may be -1).
+ * page_size: 16, 32 or 64.  head_dim: 64, 128 or 256.  A page belongs to one sequence
+ * while that sequence is appended to (full pages may be shared). */
+typedef struct q4lin_kv_cache {
+    uint8_t* k_codes;
+    float* k_scales;
+    uint8_t* v_codes;
+    float* v_scales;
+    const int32_t* page_table;
+    int64_t num_pages, kv_heads, page_size, head_dim;
+    int64_t batch, pages_per_sequence, table_stride;
+} q4lin_kv_cache_t;
+
+/* Position rotation of the first `rotated` channels (a multiple of 8, at most head_dim) of a
+ * head; cos and sin are float32 [positions, rotated / 2], contiguous, indexed by the
+ * token's position in its sequence.  With i < rotated / 2, the pair (a, b) of channels
+ * (i, i + rotated / 2), or (2i, 2i + 1) when interleaved is 1, becomes
+ * (a cos - b sin, b cos + a sin).  cos == NULL: no rotation. */
+typedef struct q4lin_rope {
+    const float* cos;
+    const float* sin;
+    int64_t positions, rotated;
+    int interleaved;
+} q4lin_rope_t;
+
+typedef struct q4lin_kv_append {
+    const void* k; /* [tokens, kv_heads, head_dim], channels contiguous */
+    const void* v;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride; /* elements */
+    int dtype;              /* q4lin_dtype_t of k and v */
+    int64_t tokens;         /* new tokens of all sequences */
+    const int32_t* offsets; /* [batch + 1]: sequence b's are rows offsets[b] .. offsets[b+1] */
+    const int32_t* starts;  /* [batch]: tokens that sequence b holds before the call */
+    q4lin_rope_t rope;      /* of the keys */
+} q4lin_kv_append_t;
+
+/* Append keys (rotated on the way) and values to the cache.
+ *
+ * For each page that receives tokens and each head, with amax the largest finite |x| of
+ * the new tokens in that page (keys after the rotation, in fp32) and s0 the page's scale
+ * if it holds earlier tokens of the sequence, else 0:
+ *   s    = max(s0, amax * fl(1/127))          (a scale below 2^-126 is 0)
+ *   code = clamp(rint(x * fl(1/s)), -127, 127) + 128, or 128 when s is 0
+ * and where s > s0 > 0 the page's earlier codes are rounded again,
+ *   code = rint((code - 128) * fl(s0/s)) + 128.
+ * rint rounds half to even, and every product, sum and quotient is rounded to fp32 once, in
+ * the order written, so the bytes are determined by the inputs.  An infinity becomes 1 or
+ * 255, a NaN 128, and either records code 3 in the status word.  The caller keeps the
+ * lengths: sequence b holds starts[b] + offsets[b+1] - offsets[b] tokens afterwards.
+ * k and v may be slices of one larger array (strides).  tokens == 0 or batch == 0 is
+ * Q4LIN_OK (nothing runs).  No input may overlap the cache. */
+Q4LIN_API q4lin_status_t q4lin_run_kv_append(q4lin_handle_t handle,
+                                             const q4lin_kv_cache_t* cache,
+                                             const q4lin_kv_append_t* args, void* stream);
+
+typedef struct q4lin_attention {
+    const void* query; /* [tokens, heads, head_dim], channels contiguous */
+    int64_t q_token_stride, q_head_stride; /* elements */
+    void* out;              /* [tokens, heads, head_dim], contiguous, of the query's type */
+    float* lse;             /* [tokens, heads], or NULL */
+    int dtype;              /* q4lin_dtype_t of query and out */
+    int64_t tokens, heads;  /* heads: a multiple of kv_heads */
+    int64_t max_query;      /* no sequence has more query tokens than this (<= tokens) */
+    const int32_t* offsets; /* [batch + 1], as in q4lin_kv_append_t */
+    const int32_t* lengths; /* [batch]: tokens in the cache, those of the queries included */
+    float scale;            /* of the scores, usually 1 / sqrt(head_dim) */
+    int causal;             /* 1: a query sees keys up to its own position; 0: all of them */
+    int64_t window;         /* > 0: only the last `window` of those (its own included); 0: off */
+    q4lin_rope_t rope;      /* of the queries (the keys were rotated when appended) */
+} q4lin_attention_t;
+
+/* Attention of queries over the cache.  Query i of the t = offsets[b+1] - offsets[b] of
+ * sequence b has position q = lengths[b] - t + i, and reads the keys j < lengths[b] with
+ * j <= q (causal) and j > q - window (window > 0); head h reads key/value head
+ * h / (heads / kv_heads):
+ *   x_j = scale * sum_d q_d K[j,d],  out_d = sum_j e^(x_j) V[j,d] / sum_j e^(x_j),
+ *   lse = ln sum_j e^(x_j).
+ * A query that sees no key (an empty sequence, a negative position) gets out = 0 and
+ * lse = -infinity.  Codes are exact in the tensor cores' fp16 operands; queries and
+ * probabilities enter them as two fp16 terms (22 bits; one term, 11 bits, for the
+ * probabilities and queries of 16-bit prompts, see below), and everything is summed in fp32.
+ * Sequences with many query rows go through a tcgen05 kernel, the others through one that
+ * splits the keys evenly over the SMs (partial results joined in a fixed order through the
+ * handle's workspace), so a batch may mix prompts and single tokens.  tokens == 0 or
+ * batch == 0 is Q4LIN_OK.  Sequences of more than max_query tokens record code 4, and
+ * their outputs are not written. */
+Q4LIN_API q4lin_status_t q4lin_run_attention(q4lin_handle_t handle,
+                                             const q4lin_kv_cache_t* cache,
+                                             const q4lin_attention_t* args, void* stream);
+
+typedef struct q4lin_logprobs {
+    const void* logits; /* [rows, vocabulary], entries of a row contiguous */
+    int64_t row_stride; /* elements */
+    int dtype;          /* q4lin_dtype_t of the logits */
+    int64_t rows, vocabulary;
+    const int32_t* tokens; /* [rows]; -1: no token (its log probability is 0); may be NULL */
+    float* logprob;        /* [rows], or NULL */
+    float* entropy;        /* [rows], or NULL */
+    float* lse;            /* [rows], or NULL */
+    int64_t top;           /* alternatives, 0..32 and <= vocabulary */
+    int32_t* top_tokens;   /* [rows, top] (NULL when top is 0) */
+    float* top_logprobs;   /* [rows, top] (NULL when top is 0) */
+} q4lin_logprobs_t;
+
+/* Of each row x of logits, in one pass: lse = ln sum_v e^(x_v), logprob = x_token - lse,
+ * entropy = -sum_v p_v ln p_v with p = e^(x - lse), and the `top` largest entries in
+ * descending order (equal ones: lowest index first) with their log probabilities.
+ * -infinity stands for an excluded entry (p = 0, no part in the entropy).  A row of
+ * nothing else has lse = -infinity, logprob and top_logprobs -infinity and entropy 0.  A
+ * row with a NaN or a +infinity has lse NaN or +infinity, and entropy NaN; the order of
+ * the top entries takes a NaN as the largest. */
+Q4LIN_API q4lin_status_t q4lin_run_logprobs(q4lin_handle_t handle, const q4lin_logprobs_t* args,
+                                            void* stream);
+
+typedef struct q4lin_logprobs_backward {
+    const void* logits; /* as in q4lin_logprobs_t */
+    int64_t row_stride;
+    int dtype;
+    int64_t rows, vocabulary;
+    const int32_t* tokens;  /* [rows], or NULL when d_logprob is NULL */
+    const float* lse;       /* [rows], as q4lin_run_logprobs wrote it */
+    const float* entropy;   /* [rows], ditto (may be NULL when d_entropy is NULL) */
+    const float* d_logprob; /* [rows], or NULL for zeros */
+    const float* d_entropy; /* [rows], or NULL for zeros */
+    void* d_logits;         /* [rows, vocabulary], of the logits' type */
+    int64_t d_row_stride;   /* elements */
+} q4lin_logprobs_backward_t;
+
+/* Gradient of q4lin_run_logprobs' logprob and entropy for the logits:
+ *   d_x_v = d_logprob (1[v = token] - p_v) - d_entropy p_v (ln p_v + entropy).
+ * Entries with p = 0 get 0 (beyond the token's term).  A row with token -1 has no logprob
+ * term; a row whose lse is -infinity gets zeros.  d_logits may be the logits' own array
+ * (same pointer and stride), else it must not overlap any input. */
+Q4LIN_API q4lin_status_t q4lin_run_logprobs_backward(q4lin_handle_t handle,
+                                                     const q4lin_logprobs_backward_t* args,
+                                                     void* stream);
+
 /* The path q4lin_run would take for these arguments (no launch, no device access);
  * *path_out receives a q4lin_path_t other than AUTO.  Same validation and status codes
  * as q4lin_run.  For M == 0 or N == 0, *path_out is Q4LIN_PATH_AUTO (nothing runs). */
@@ -307,7 +466,8 @@ Q4LIN_API q4lin_status_t q4lin_get_option(q4lin_handle_t handle, int option,
 /* Read and clear the handle's device status word after synchronizing `stream`.
  * *code_out = 0 if no kernel recorded a problem since the last call; otherwise the
  * first recorded code (1 = a bounded device-side wait ran out; 2 = a value outside the
- * fp16 range on the fp16 tensor-core path).
+ * fp16 range on the fp16 tensor-core path; 3 = a non-finite key or value was appended to a
+ * cache; 4 = an index outside its array, see the operators around the linears).
  * The word is shared by every call on the handle.
  * Returns Q4LIN_ERR_TIMEOUT when the code is non-zero, Q4LIN_OK otherwise. */
 Q4LIN_API q4lin_status_t q4lin_check_device_status(q4lin_handle_t handle, void* stream,

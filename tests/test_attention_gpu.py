@@ -1,0 +1,279 @@
+"""Attention over the paged 8-bit cache against float64.
+
+Tolerance of a row: the query's two fp16 terms leave 2^-22 of its largest element, so a score
+is off by at most 2^-21 S, S = scale sum |q k| (doubled for the fp32 sums), the weights
+relatively by twice that, and the weights' own terms, exponentials and sums add 2^-19 at
+most for these lengths.  The outputs are means of values no larger than A, so they are off by
+A (2^-19 S + 2^-18); then comes the rounding to the output's type."""
+import numpy as np
+import pytest
+
+from tests import _operators as ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def handle():
+    from bit_weight_quantized_int4_gb300 import q4lin
+    h = q4lin.Handle(0)
+    yield h
+    h.close()
+
+
+def status(handle):
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    return q4lin.q4lin_check_device_status(handle.ptr, torch.cuda.current_stream().cuda_stream)[1]
+
+
+def check(out, lse, want, dtype):
+    ref, ref_lse, vmax, smax = want
+    bound = (vmax * (2.0**-19 * smax + 2.0**-18))[..., None] + ops.ROUND[dtype] * np.abs(ref) + ops.TINY[dtype]
+    err = np.abs(ops.to_host(out) - ref)
+    assert np.all(err <= bound), f"out: {np.max(err / bound):.3g} times the tolerance"
+    got = ops.to_host(lse)
+    empty = np.isneginf(ref_lse)
+    assert np.array_equal(np.isneginf(got), empty)
+    err = np.abs(got[~empty] - ref_lse[~empty])
+    bound = (2.0**-20 * smax + 2.0**-20 + 2.0**-22 * np.abs(np.where(empty, 0, ref_lse)))[~empty]
+    assert np.all(err <= bound), f"lse: {np.max(err / bound):.3g} times the tolerance"
+
+
+def run(handle, lengths, counts, heads, kv_heads, page, dim, dtype, rotated=None, interleaved=False,
+        causal=True, window=0, seed=0, gain=1.5, q=None, **more):
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(seed + dim + page + sum(lengths))
+    host = ops.Cache(rng, lengths, kv_heads, page, dim)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    if q is None:
+        q = ops.to_device((rng.standard_normal((offsets[-1], heads, dim)) * gain).astype(np.float32), dtype)
+    rotated = dim if rotated is None else rotated
+    rope = ops.rope_tables(rng, max(max(lengths), 1), rotated) if rotated else None
+    scale = 1 / np.sqrt(dim)
+    out, lse = q4lin.attention(handle, host.device(), q, ops.to_device(offsets),
+                               ops.to_device(np.array(lengths, np.int32)), scale,
+                               rope=None if rope is None else tuple(map(ops.to_device, rope)),
+                               interleaved=interleaved, causal=causal, window=window, **more)
+    want = ops.attention(host, ops.to_host(q), offsets, lengths, float(np.float32(scale)), rope,
+                         interleaved, causal, window)
+    return out, lse, want, dtype
+
+
+SINGLE = [
+    # lengths, heads, kv heads, page, dim, dtype
+    ([1], 1, 1, 16, 64, "f32"),
+    ([2], 4, 1, 64, 128, "f32"),
+    ([63, 64, 65], 4, 2, 64, 128, "f32"),
+    ([15, 16, 17, 33], 6, 2, 16, 64, "bf16"),
+    ([511, 512, 513, 700], 8, 2, 32, 128, "f16"),
+    ([701], 32, 8, 16, 64, "f32"),
+    ([4097, 1, 900, 0, 31], 8, 8, 64, 64, "f32"),
+    ([1300, 77], 14, 2, 32, 128, "bf16"),
+    ([650, 3], 8, 1, 16, 256, "f32"),
+    ([300], 12, 1, 64, 128, "f32"),
+    ([200, 210], 34, 2, 64, 64, "f16"),
+    ([9000], 4, 4, 64, 128, "f32"),
+    ([i * 7 % 130 for i in range(300)], 2, 1, 16, 64, "f32"),
+]
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,page,dim,dtype", SINGLE)
+def test_one_token(handle, lengths, heads, kv_heads, page, dim, dtype):
+    check(*run(handle, lengths, [1] * len(lengths), heads, kv_heads, page, dim, dtype, max_query=1))
+    assert status(handle) == 0
+
+
+SEVERAL = [
+    # lengths, query tokens, heads, kv heads, page, dim, dtype, causal, window
+    ([5], [5], 4, 2, 16, 64, "f32", True, 0),
+    ([70, 9, 128], [3, 0, 5], 4, 1, 32, 128, "f32", True, 0),
+    ([70, 9, 128], [3, 2, 5], 4, 1, 32, 128, "bf16", False, 0),
+    ([200, 130], [17, 4], 6, 2, 64, 128, "f16", True, 50),
+    ([100, 3, 0], [2, 5, 2], 2, 2, 16, 64, "f32", True, 0),   # queries before the sequence: empty rows
+    ([100, 3], [2, 5], 2, 2, 16, 64, "f32", True, 1),
+    ([333], [70], 7, 1, 64, 256, "f32", True, 100),
+    ([333], [70], 8, 2, 64, 128, "f32", False, 33),
+    ([260, 40, 600], [150, 1, 90], 4, 2, 16, 128, "bf16", True, 0),
+    ([260, 40, 600], [150, 1, 90], 4, 2, 64, 64, "f32", True, 0),
+    ([400], [400], 3, 1, 32, 64, "f16", True, 0),
+    ([129], [129], 2, 1, 64, 128, "f32", True, 0),
+    ([640, 2], [200, 2], 5, 1, 64, 128, "f32", True, 64),
+]
+
+
+@pytest.mark.parametrize("lengths,counts,heads,kv_heads,page,dim,dtype,causal,window", SEVERAL)
+def test_several_tokens(handle, lengths, counts, heads, kv_heads, page, dim, dtype, causal, window):
+    check(*run(handle, lengths, counts, heads, kv_heads, page, dim, dtype, causal=causal, window=window))
+    assert status(handle) == 0
+
+
+@pytest.mark.parametrize("rotated,interleaved", [(0, False), (32, False), (32, True), (128, True)])
+def test_rotation(handle, rotated, interleaved):
+    check(*run(handle, [100, 40], [1, 3], 4, 2, 32, 128, "f32", rotated=rotated, interleaved=interleaved))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 40.0])
+def test_tiny_and_large_scores(handle, dtype, size):
+    """Scores all alike, and one weight that takes everything."""
+    check(*run(handle, [150], [2], 4, 2, 16, 64, dtype, gain=size))
+
+
+def test_slices_of_one_projection(handle):
+    import torch
+    wide = torch.randn(3, 1 + 8 * 64 + 64, device="cuda")
+    for shift in (0, 1, 4):
+        q = wide[:, shift:shift + 512].unflatten(1, (8, 64))
+        check(*run(handle, [50, 20], [2, 1], 8, 2, 16, 64, "f32", q=q))
+
+
+def test_results_do_not_depend_on_the_rest_of_the_batch_or_the_run(handle):
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(4)
+    host = ops.Cache(rng, [3000, 50, 700], 2, 64, 128)
+    cache = host.device()
+    q = torch.randn(3, 8, 128, device="cuda")
+    o, n = (ops.to_device(np.array(a, np.int32)) for a in ([0, 1, 2, 3], [3000, 50, 700]))
+    first = q4lin.attention(handle, cache, q, o, n, 0.1, max_query=1)
+    for _ in range(5):
+        again = q4lin.attention(handle, cache, q, o, n, 0.1, max_query=1)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("counts", [[1], [200]])
+def test_a_nan_stays_in_its_row_and_unseen_pages_are_not_read(handle, counts):
+    """A NaN in one query; NaN scales of pages that no sequence has."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(11)
+    host = ops.Cache(rng, [230], 2, 64, 128)
+    used = host.table[0, :4]
+    for s in (host.ks, host.vs):
+        spare = np.setdiff1d(np.arange(host.total), used)
+        s[spare] = np.nan
+    q = torch.randn(counts[0], 4, 128, device="cuda")
+    q[0, 1, 7] = float("nan")
+    offsets = np.array([0, counts[0]], np.int32)
+    out, lse = q4lin.attention(handle, host.device(), q, ops.to_device(offsets),
+                               ops.to_device(np.array([230], np.int32)), 0.1)
+    bad = torch.isnan(out).any(-1)
+    want = torch.zeros_like(bad)
+    want[0, 1] = True
+    assert torch.equal(bad, want) and torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    q[0, 1, 7] = 0
+    ref = ops.attention(host, ops.to_host(q), offsets, [230], float(np.float32(0.1)))
+    ok = ~want.cpu().numpy()
+    err = np.abs(ops.to_host(out) - ref[0])[ok]
+    assert np.all(err <= (ref[2] * (2.0**-19 * ref[3] + 2.0**-18))[ok][:, None] + 1e-7)
+
+
+def test_masked_places_may_hold_anything(handle):
+    """Bytes of a page past the sequence's end change nothing."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(12)
+    host = ops.Cache(rng, [70], 1, 64, 64)
+    q = torch.randn(70, 2, 64, device="cuda")
+    results = []
+    for fill in (0, 255):
+        last = host.table[0, 1]
+        host.k[last, 0, 6:] = fill
+        host.v[last, 0, :, 6:] = fill
+        cache = host.device()
+        for n in (1, 70):
+            results.append(q4lin.attention(handle, cache, q[:n], ops.to_device(np.array([0, n], np.int32)),
+                                           ops.to_device(np.array([70], np.int32)), 0.125)[0])
+    assert torch.equal(results[0], results[2]) and torch.equal(results[1], results[3])
+
+
+def test_append_then_attend(handle):
+    """The two together, token by token, against attention over unquantised keys."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(13)
+    table = ops.to_device(np.arange(8, dtype=np.int32).reshape(2, 4))
+    cache = q4lin.KVCache.empty(8, 2, 16, 64, table)
+    rope = tuple(map(ops.to_device, ops.rope_tables(rng, 64, 64)))
+    offsets = ops.to_device(np.array([0, 1, 2], np.int32))
+    x = rng.standard_normal((3, 40, 2, 2, 64)).astype(np.float32)  # k, v, q of each step
+    k_all, v_all = [], []
+    for i in range(40):
+        k, v, q = (ops.to_device(x[j, i]) for j in range(3))
+        at = torch.full((2,), i, dtype=torch.int32, device="cuda")
+        q4lin.kv_append(handle, cache, k, v, offsets, at, rope=rope)
+        out, _ = q4lin.attention(handle, cache, q, offsets, at + 1, 0.125, max_query=1, rope=rope)
+        position = np.full(2, i)
+        host_rope = tuple(t.cpu().numpy() for t in rope)
+        k_all.append(ops.rotate(x[0, i], position, host_rope, False))
+        v_all.append(x[1, i])
+        qr = ops.rotate(x[2, i], position, host_rope, False)
+        for b in range(2):
+            for h in range(2):
+                kk, vv = np.array(k_all)[:, b, h], np.array(v_all)[:, b, h]
+                p = np.exp(0.125 * kk @ qr[b, h])
+                ref = p @ vv / p.sum()
+                # A code is within half a step, and each growth of the scale adds half of one:
+                # some steps of 1/127 of the largest element, which are averaged.
+                assert np.max(np.abs(ops.to_host(out)[b, h] - ref)) < 0.1
+    assert status(handle) == 0
+
+
+def test_indices_out_of_range_are_reported(handle):
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(14)
+    host = ops.Cache(rng, [100], 1, 64, 64, spare=0)
+    q = torch.randn(2, 2, 64, device="cuda")
+    for table, lengths, offsets, most in (([[0, 9]], [100], [0, 2], 2), ([[0, -1]], [100], [0, 2], 2),
+                                          ([[0, 1]], [129], [0, 2], 2), ([[0, 1]], [100], [0, 3], 2),
+                                          ([[0, 1]], [100], [0, 2], 1), ([[0, 1]], [100], [1, 0], 2)):
+        host.table = np.array(table, np.int32)
+        q4lin.attention(handle, host.device(), q, ops.to_device(np.array(offsets, np.int32)),
+                        ops.to_device(np.array(lengths, np.int32)), 0.1, max_query=most)
+        assert status(handle) == 4
+
+
+def test_other_stream_and_nothing_to_do(handle):
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    host = ops.Cache(np.random.default_rng(15), [100], 1, 64, 64)
+    cache, q = host.device(), torch.randn(1, 2, 64, device="cuda")
+    o, n = (ops.to_device(np.array(a, np.int32)) for a in ([0, 1], [100]))
+    want = q4lin.attention(handle, cache, q, o, n, 0.1)[0]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    out = torch.full_like(q, 7.0)
+    stream.wait_stream(torch.cuda.current_stream())
+    q4lin.attention(handle, cache, q, o, n, 0.1, out=out, stream=stream.cuda_stream)
+    stream.synchronize()
+    assert torch.equal(out, want)
+    empty, _ = q4lin.attention(handle, cache, q[:0], o, n, 0.1)
+    assert empty.shape == (0, 2, 64)
+
+
+def test_refusals(handle):
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    cache = ops.Cache(np.random.default_rng(16), [100], 2, 64, 64).device()
+    q = torch.randn(1, 4, 64, device="cuda")
+    o, n = (ops.to_device(np.array(a, np.int32)) for a in ([0, 1], [100]))
+    for change in (dict(query=q[:, :3]), dict(query=q[..., :32]), dict(query=q.double()), dict(offsets=n),
+                   dict(lengths=n.long()), dict(out=q.half()), dict(lse=q[..., 0].half()),
+                   dict(query=q.transpose(1, 2)), dict(query=q.cpu())):
+        args = dict(dict(query=q, offsets=o, lengths=n), **change)
+        with pytest.raises(ValueError):
+            q4lin.attention(handle, cache, scale=0.1, **args)
+    inv = q4lin.Q4LIN_ERR_INVALID_ARG
+    for change in (dict(window=-1), dict(max_query=0), dict(causal=2), dict(out=q)):
+        with pytest.raises(q4lin.Q4LinError) as e:
+            q4lin.attention(handle, cache, q, o, n, 0.1, **change)
+        assert e.value.status == inv
+    wide = q4lin.q4lin_kv_cache_t.from_buffer_copy(cache.args)
+    wide.pages_per_sequence = wide.table_stride = 1 << 40
+    a = q4lin.q4lin_attention_t(q.data_ptr(), 256, 64, torch.empty_like(q).data_ptr(), None, 0, 1, 4, 1,
+                                o.data_ptr(), n.data_ptr(), 0.1, 1, 0, q4lin.q4lin_rope_t())
+    assert q4lin.q4lin_run_attention(handle.ptr, wide, a, 0) == q4lin.Q4LIN_ERR_TOO_LARGE
+    assert q4lin.q4lin_run_attention(handle.ptr, cache.args, None, 0) == inv
+    torch.cuda.synchronize()
