@@ -1,0 +1,585 @@
+// attention_prompt.cu -- attention of many query rows per key/value head over the paged 8-bit
+// cache (prompts and their chunks), on the tcgen05 tensor cores.
+//
+// A row is one query token of one head; the heads that share a key/value head are rows of one
+// list (token-major), so grouped heads fill the MMA's 128 rows and share the keys.  A CTA
+// takes two tiles of 128 rows and walks over 128 keys at a time:
+//   dequantizing warps  codes from global memory into fp16 K and V tiles in shared memory
+//                       (code - 128 is exact in fp16; both are stored with the axis that the
+//                       product sums over contiguous, 128-byte swizzled),
+//   one issuing thread  S = Q K^T into tensor memory, then O += P V with P read from there,
+//   softmax warps       one thread per row: the running maximum and sum in fp32, the weights
+//                       back into tensor memory over the scores that they came from.
+// The two tiles take turns: one's products run while the other's softmax does.
+//
+// The pages' scales stay out of the operands: a key page's multiplies its columns of S, a
+// value page's (over the largest of the walk) joins the exponent of its weights.  O is
+// only rescaled when a row's maximum has grown by 2^8 since the last time, which fp16's range
+// leaves room for.  Queries and weights enter as QT and PT fp16 terms, the rounded value and
+// what the rounding left (22 bits), each term a product of its own: two of both in general; a
+// weight of a bf16 output takes one (its 11 bits are finer than the output's 8), and bf16
+// queries that are not rotated are exact in one.
+//
+// Bound: the products (4 head_dim flops a pair and term) together with the exponentials
+// (16 a clock and SM against 128 x 128 products in 8 clocks).
+#include <algorithm>
+
+#include "q4lin_internal.h"
+#include "serving.cuh"
+
+namespace q4lin {
+namespace {
+using namespace ptx;
+using namespace serving;
+
+constexpr int kQ = 128;     // rows per tile (MMA M = lanes of tensor memory)
+constexpr int kKeys = 128;  // keys per step
+constexpr int kSoftWarps = 8, kDeqWarps = 4;
+constexpr int kThreads = 32 * (kSoftWarps + kDeqWarps + 1);
+constexpr int kScaleSlots = 4;
+constexpr float kBase = 7.f;    // weights are kept as 2^7 p ...
+constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
+constexpr float kLeastRatio = 5.421010862427522e-20f;  // 2^-64
+constexpr int64_t kDrainNs = 4000000000LL;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScoreCol = 256;  // O of the two tiles in columns 0 and 128, S from here
+
+struct PromptArgs {
+    q4lin_kv_cache_t cache;
+    q4lin_attention_t a;
+    int page_shift;
+    int64_t rows_min;  // sequences of more rows than this per key/value head are taken
+    int q_vec;
+    int* status;
+    int64_t wait_ns;
+};
+
+template <int D, int QT>
+struct Layout {
+    static constexpr int kBlock = 128 * 128;           // 128 rows of 128 bytes
+    static constexpr int kBlocks = D / 64;             // of a Q or K tile
+    static constexpr int kStages = QT == 1 ? 2 : 1;  // of K and V tiles
+    static constexpr uint32_t q = 0;                                        // [tile][term][block]
+    static constexpr uint32_t k = q + 2 * QT * kBlocks * kBlock;         // [stage][block]
+    static constexpr uint32_t v = k + kStages * kBlocks * kBlock;           // [stage][2 x D rows of 128 B]
+    static constexpr uint32_t bytes = v + kStages * 2 * D * 128;
+};
+
+struct PromptShared {
+    float factor[2 * kQ];
+    float k_scale[kScaleSlots][8], v_log[kScaleSlots][8], v_inv[kScaleSlots][8];  // of 16 keys each
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+    float v_max[kThreads / 32];
+    int sums[kThreads / 32];
+    int found_b, found_tile, failed;
+    uint32_t tmem;
+};
+
+// D (tensor memory) (+)= A B^T, both fp16 operands from shared memory.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// 16 columns of this warp's lanes, without waiting for completion.
+__device__ __forceinline__ void tmem_st16_async(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Byte of 16-byte chunk `chunk` of row `row` in a 128-byte-swizzled block.
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
+    return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+template <int D, int QT, int PT>
+__global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const PromptArgs g) {
+    using L = Layout<D, QT>;
+    constexpr int ST = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PromptShared S;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
+    const q4lin_kv_cache_t& C = g.cache;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ps = g.page_shift;
+    const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads);
+    const int h = (int)(blockIdx.x % Hkv);
+    const int64_t want = blockIdx.x / Hkv;  // which tile pair of the whole call
+
+    // ---- the CTA's sequence and tile pair: a scan over the sequences
+    if (tid == 0) S.found_b = -1, S.failed = 0;
+    int64_t carry = 0;
+    for (int64_t b0 = 0; b0 < C.batch; b0 += kThreads) {
+        const int64_t b = b0 + tid;
+        int v = 0;
+        if (b < C.batch) {
+            const int64_t o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1);
+            const int64_t len = __ldg(g.a.lengths + b), rows = (o1 - o0) * group;
+            const bool bad = o0 < 0 || o1 < o0 || o1 > g.a.tokens || o1 - o0 > g.a.max_query ||
+                             len > C.pages_per_sequence << ps || (g.a.rope.cos && len > g.a.rope.positions);
+            if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
+            if (!bad && rows > g.rows_min) v = (int)((rows + 2 * kQ - 1) / (2 * kQ));
+        }
+        int sum = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += n;
+        }
+        __syncthreads();
+        if (lane == 31) S.sums[warp] = sum;
+        __syncthreads();
+        int64_t before = carry;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += S.sums[w];
+            carry += S.sums[w];
+        }
+        before += sum - v;
+        if (v && want >= before && want < before + v) {
+            S.found_b = (int)b;
+            S.found_tile = (int)(v - 1 - (want - before));  // the longest walks first
+        }
+    }
+    __syncthreads();
+    if (S.found_b < 0) return;
+    const int64_t b = S.found_b;
+    const int64_t o0 = __ldg(g.a.offsets + b);
+    const int tq = (int)(__ldg(g.a.offsets + b + 1) - o0), len = max(__ldg(g.a.lengths + b), 0);
+    const int rows = tq * group, row0 = S.found_tile * 2 * kQ;
+    const int row_end = min(rows, row0 + 2 * kQ);
+    const bool two = row_end - row0 > kQ;
+    // Steps over keys [128 step0, 128 step1).
+    const int first_pos = len - tq + row0 / group, last_pos = len - tq + (row_end - 1) / group;
+    const int last_key = g.a.causal ? last_pos : len - 1;
+    const int64_t low64 = g.a.window > 0 ? (int64_t)first_pos - g.a.window + 1 : 0;
+    const int step0 = low64 > 0 ? (int)(low64 / kKeys) : 0;
+    const int step1 = last_key < 0 || len == 0 ? step0 : max(step0, last_key / kKeys + 1);
+    const int n = step1 - step0;
+    const int32_t* table = C.page_table + b * C.table_stride;
+    const int pages = (len + (1 << ps) - 1) >> ps;
+
+    // ---- prologue: barriers, tensor memory, the largest value scale, queries
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&S.k_full[s]), 32 * kDeqWarps);
+            mbar_init(smem_u32(&S.v_full[s]), 32 * kDeqWarps);
+            mbar_init(smem_u32(&S.k_empty[s]), 1);
+            mbar_init(smem_u32(&S.v_empty[s]), 1);
+            mbar_init(smem_u32(&S.s_full[s]), 1);
+            mbar_init(smem_u32(&S.p_full[s]), kQ);
+            mbar_init(smem_u32(&S.o_full[s]), 1);
+        }
+        mbar_init_fence();
+    }
+    if (warp == kSoftWarps + kDeqWarps) tmem_alloc(smem_u32(&S.tmem), kTmemCols);
+    float v_max = 0.f;
+    for (int p = ((step0 * kKeys) >> ps) + tid; p < min(pages, (step1 * kKeys) >> ps); p += kThreads) {
+        const int id = __ldg(table + p);
+        if (id < 0 || id >= C.num_pages)
+            atomicCAS(g.status, 0, kStatusIndex);
+        else
+            v_max = fmaxf(v_max, __ldg(C.v_scales + (int64_t)id * Hkv + h));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, o));
+    if (lane == 0) S.v_max[warp] = v_max;
+    {
+        constexpr int kUnitsRow = D / 8, kPer = kThreads / kUnitsRow;  // 16 or 8 lanes a row
+        const int u = tid % kUnitsRow;
+        bool turned;
+        int cl, ch;
+        rope_channels(g.a.rope, u, &turned, &cl, &ch);
+        for (int r0 = 0; r0 < 2 * kQ; r0 += kPer) {
+            const int r = r0 + tid / kUnitsRow, row = row0 + r;
+            const bool in = r < 2 * kQ && row < row_end;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            const int token = in ? row / group : 0, head = h * group + (in ? row - token * group : 0);
+            if (in) {
+                const int64_t e = (o0 + token) * g.a.q_token_stride + head * g.a.q_head_stride;
+                load_four(g.a.query, g.a.dtype, e + cl, g.q_vec, x);
+                load_four(g.a.query, g.a.dtype, e + ch, g.q_vec, x + 4);
+                const int position = len - tq + token;
+                if (turned && position >= 0) rope_unit(g.a.rope, position, u, x);
+            }
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+#pragma unroll
+            for (int o = kUnitsRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            // 2^up brings the row's largest |x| to [2^14, 2^15); the scale's sign goes with it,
+            // so that larger scores stay larger after the factor.
+            const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
+            const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), g.a.scale);
+            const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+            if (r < 2 * kQ) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split_f16(x[2 * e] * up, x[2 * e + 1] * up, &hi[e], &lo[e]);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int d = w ? ch : cl;  // channels d .. d + 3: half a 16-byte chunk
+                    const uint32_t at = L::q + (uint32_t)((r / kQ) * QT * L::kBlocks + d / 64) * L::kBlock +
+                                        swizzled(r % kQ, (d % 64) / 8) + (d % 8) * 2;
+                    *reinterpret_cast<uint2*>(gbase + at) = make_uint2(hi[2 * w], hi[2 * w + 1]);
+                    if (QT == 2)
+                        *reinterpret_cast<uint2*>(gbase + at + L::kBlocks * L::kBlock) =
+                            make_uint2(lo[2 * w], lo[2 * w + 1]);
+                }
+                if (u == 0) S.factor[r] = fabsf(g.a.scale) * kLog2e * down;
+            }
+        }
+    }
+    fence_async_shared();  // the queries are read by the tensor cores
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    float v_ref = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) v_ref = fmaxf(v_ref, S.v_max[w]);
+    if (!(v_ref > 0.f)) v_ref = 1.f;  // values that are all zero
+    volatile int* failed = &S.failed;
+    auto bar = [](uint64_t& x) { return smem_u32(&x); };
+    auto wait = [&](uint64_t& x, uint32_t parity) {
+        if (wait_bounded(bar(x), parity, g.wait_ns, failed)) return true;
+        record_failure(g.status, failed);
+        return false;
+    };
+
+    if (warp < kSoftWarps) {
+        // -------------------------------------------------------------- softmax
+        const int tile = warp >> 2;
+        const int r = tile * kQ + (warp & 3) * 32 + lane, row = row0 + r;
+        const bool in = row < row_end;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + kScoreCol + tile * kKeys, o_at = tmem + lanes + tile * 128;
+        const int token = row / group, position = len - tq + token;
+        const int limit = !in ? -1 : g.a.causal ? position : len - 1;
+        const int64_t low = g.a.window > 0 ? max((int64_t)0, (int64_t)position - g.a.window + 1) : 0;
+        const float factor = S.factor[r];
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        const int steps = tile == 0 || two ? n : 0;
+        for (int i = 0; i < steps; ++i) {
+            ok = __all_sync(0xffffffffu, wait(S.s_full[tile], i & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const int key0 = (step0 + i) * kKeys, slot = i % kScaleSlots;
+            const int hi = min(limit - key0, kKeys), lo = (int)(low > key0 ? min(low - key0, (int64_t)kKeys) : 0);
+            // Columns [lo, hi] of the step are seen; all of them in most steps.
+            const bool part = __any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0);
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(s_at + 32 * c, x);
+                if (part) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e > hi || 32 * c + e < lo) x[e] = 0xFF800000u;
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float mx = __uint_as_float(x[16 * half]);
+#pragma unroll
+                    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(x[16 * half + e]));
+                    const float f = factor * S.k_scale[slot][2 * c + half];
+                    top = fmaxf(top, mx == -INFINITY ? mx : mx * f);
+                }
+            }
+            if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                // Some row's maximum grew too far: O and l over to the new one.  (The product
+                // that read the last weights is complete: this step's scores came after it.)
+                const float now = fmaxf(m, top);
+                const float alpha = now == -INFINITY ? 1.f : ex2(m - now);
+                m = now, l *= alpha;
+                if (i > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(o_at + 32 * c, x);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+                        tmem_st32_async(o_at + 32 * c, x);
+                    }
+                }
+            }
+            const float origin = kBase - (m == -INFINITY ? 0.f : m);
+            uint32_t rest[PT == 2 ? 64 : 1];
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c) {
+                uint32_t x[32], p[16];
+                tmem_ld32(s_at + 32 * c, x);
+                if (part) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e > hi || 32 * c + e < lo) x[e] = 0xFF800000u;
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int at = 2 * c + half;
+                    const float f = factor * S.k_scale[slot][at], off = origin + S.v_log[slot][at];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float a = __uint_as_float(x[16 * half + e]), b2 = __uint_as_float(x[16 * half + e + 1]);
+                        const float pa = ex2(a == -INFINITY ? a : fmaf(a, f, off));
+                        const float pb = ex2(b2 == -INFINITY ? b2 : fmaf(b2, f, off));
+                        sum += pa + pb;
+                        const int w = 8 * half + e / 2;
+                        if (PT == 2) {
+                            split_f16(pa, pb, &p[w], &rest[16 * c + w]);
+                        } else {
+                            const __half2 v = __floats2half2_rn(pa, pb);
+                            p[w] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                    }
+                    l = fmaf(sum, S.v_inv[slot][at], l);
+                }
+                tmem_st16_async(s_at + 16 * c, p);  // over scores that have been read
+            }
+            if (PT == 2) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_st16_async(s_at + 64 + 16 * c, rest + (PT == 2 ? 16 * c : 0));
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(S.p_full[tile]));
+        }
+        if (ok && steps > 0) {
+            ok = __all_sync(0xffffffffu, wait(S.o_full[tile], 0));
+            tc_fence_after();
+        }
+        if (ok) {
+            const int64_t index = (o0 + token) * g.a.heads + h * group + (row - token * group);
+            const float inv = l != 0.f ? v_ref / l : 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                __syncwarp();  // the load is the whole warp's
+                if (steps > 0) tmem_ld32(o_at + 32 * c, x);
+                if (!in) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = l != 0.f ? __float_as_uint(__uint_as_float(x[e]) * inv) : 0u;
+                if (g.a.dtype == Q4LIN_DTYPE_F32) {
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<float*>(g.a.out) + index * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        out[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                } else {
+                    uint2* out =
+                        reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        out[e] = make_uint2(
+                            to_16x2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), g.a.dtype),
+                            to_16x2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3]), g.a.dtype));
+                }
+            }
+            if (in && g.a.lse) g.a.lse[index] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l) - kBase) * kLn2 : -INFINITY;
+        }
+    } else if (warp < kSoftWarps + kDeqWarps) {
+        // ------------------------------------------------ codes into fp16 tiles
+        const int t = tid - 32 * kSoftWarps;
+        constexpr int kPieces = kKeys * D / 16 / (32 * kDeqWarps);  // 16-byte pieces per thread
+        constexpr int kRowPieces = D / 16;
+        const int page_pieces = (D << ps) / 16, slot_pieces = (1 << ps) / 16;
+        uint4 kreg[kPieces], vreg[kPieces];
+        const uint4 zero = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        auto page_of = [&](int i, int token) {  // page id of a key of step i, -1 past the end
+            const int p = ((step0 + i) * kKeys + token) >> ps;
+            if (i >= n || p >= pages) return -1;
+            const int id = __ldg(table + p);
+            return id < 0 || id >= C.num_pages ? 0 : id;
+        };
+        auto load_k = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                const int p = t + 32 * kDeqWarps * j, token = p / kRowPieces, c = p % kRowPieces;
+                const int id = page_of(i, token);
+                kreg[j] = id < 0 ? zero
+                                 : __ldg(reinterpret_cast<const uint4*>(
+                                       C.k_codes + (((int64_t)id * Hkv + h) << ps) * D +
+                                       (token & ((1 << ps) - 1)) * D + c * 16));
+            }
+        };
+        auto load_v = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                const int p = t + 32 * kDeqWarps * j, pg = p / page_pieces, rem = p % page_pieces;
+                const int id = page_of(i, pg << ps);
+                vreg[j] = id < 0 ? zero
+                                 : __ldg(reinterpret_cast<const uint4*>(
+                                       C.v_codes + (((int64_t)id * Hkv + h) << ps) * D + rem * 16));
+            }
+        };
+        // 16 codes as two 16-byte chunks of fp16, chunks 2 c and 2 c + 1 of the row.
+        auto put = [&](uint32_t block, int row, int c, const uint4& w, int odd) {
+            uint32_t f[8];
+            codes_f16(w.x, &f[0], &f[1]);
+            codes_f16(w.y, &f[2], &f[3]);
+            codes_f16(w.z, &f[4], &f[5]);
+            codes_f16(w.w, &f[6], &f[7]);
+            const uint32_t a = block + swizzled(row, 2 * c), b2 = block + swizzled(row, 2 * c + 1);
+            if (odd) {  // the order of the two stores keeps a quarter-warp off its own banks
+                st_shared_v4(b2, f[4], f[5], f[6], f[7]);
+                st_shared_v4(a, f[0], f[1], f[2], f[3]);
+            } else {
+                st_shared_v4(a, f[0], f[1], f[2], f[3]);
+                st_shared_v4(b2, f[4], f[5], f[6], f[7]);
+            }
+        };
+        load_k(0);
+        load_v(0);
+        for (int i = 0; i < n; ++i) {
+            const int st = i % ST;
+            const uint32_t again = (uint32_t)(i / ST - 1) & 1u;
+            float ks = 0.f, vs = 0.f;
+            if (t < 8) {
+                const int id = page_of(i, t * 16);
+                if (id >= 0) {
+                    ks = __ldg(C.k_scales + (int64_t)id * Hkv + h);
+                    vs = __ldg(C.v_scales + (int64_t)id * Hkv + h);
+                }
+            }
+            if (i >= ST && !wait(S.k_empty[st], again)) break;
+            if (t < 8) {
+                // Far below fp16's range a weight is 0 in the product; in l it counts.
+                const float ratio = fmaxf(vs / v_ref, kLeastRatio);
+                const int slot = i % kScaleSlots;
+                S.k_scale[slot][t] = ks, S.v_log[slot][t] = lg2(ratio), S.v_inv[slot][t] = 1.f / ratio;
+            }
+            const uint32_t kt = base + L::k + (uint32_t)(st * L::kBlocks) * L::kBlock;
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                const int p = t + 32 * kDeqWarps * j, token = p / kRowPieces, c = p % kRowPieces;
+                put(kt + (uint32_t)(c / 4) * L::kBlock, token, c % 4, kreg[j], (c / 4) & 1);
+            }
+            fence_async_shared();
+            mbar_arrive(bar(S.k_full[st]));
+            load_k(i + 1);
+            if (i >= ST && !wait(S.v_empty[st], again)) break;
+            const uint32_t vt = base + L::v + (uint32_t)st * (2 * D * 128);
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                const int p = t + 32 * kDeqWarps * j, pg = p / page_pieces, rem = p % page_pieces;
+                const int d = rem / slot_pieces, key = (pg << ps) + (rem % slot_pieces) * 16;
+                put(vt + (uint32_t)(key / 64) * (D * 128), d, (key % 64) / 16, vreg[j], 0);
+            }
+            fence_async_shared();
+            mbar_arrive(bar(S.v_full[st]));
+            load_v(i + 1);
+        }
+    } else if (lane == 0 && n > 0) {
+        // ------------------------------------------------------------ MMA issue
+        const uint32_t idesc_s = f16_idesc(kQ, kKeys), idesc_o = f16_idesc(kQ, D);
+        auto scores = [&](int tile, int st) {
+#pragma unroll
+            for (int term = 0; term < QT; ++term)
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t a = sw128_desc(base + L::q + (uint32_t)((tile * QT + term) * L::kBlocks + kk / 4) * L::kBlock) + 2 * (kk % 4);
+                    const uint64_t b2 = sw128_desc(base + L::k + (uint32_t)(st * L::kBlocks + kk / 4) * L::kBlock) + 2 * (kk % 4);
+                    mma_f16_ss(tmem + kScoreCol + tile * kKeys, a, b2, idesc_s, term + kk > 0);
+                }
+            mma_commit(bar(S.s_full[tile]));
+        };
+        auto outputs = [&](int tile, int st, int i) {
+#pragma unroll
+            for (int term = 0; term < PT; ++term)
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk) {
+                    const uint64_t b2 = sw128_desc(base + L::v + (uint32_t)st * (2 * D * 128) + (uint32_t)(kk / 4) * (D * 128)) + 2 * (kk % 4);
+                    mma_f16_ts(tmem + tile * 128, tmem + kScoreCol + tile * kKeys + term * 64 + 8 * kk, b2, idesc_o,
+                               i > 0 || term + kk > 0);
+                }
+        };
+        bool ok = wait(S.k_full[0], 0);
+        if (ok) {
+            tc_fence_after();
+            scores(0, 0);
+            if (two) scores(1, 0);
+            mma_commit(bar(S.k_empty[0]));
+        }
+        for (int i = 0; ok && i < n; ++i) {
+            const int st = i % ST, next = (i + 1) % ST;
+            const uint32_t par = (uint32_t)(i / ST) & 1u, npar = (uint32_t)((i + 1) / ST) & 1u;
+            const bool more = i + 1 < n;
+            if (!(ok = wait(S.v_full[st], par) && wait(S.p_full[0], i & 1))) break;
+            tc_fence_after();
+            outputs(0, st, i);
+            if (more) {
+                if (!(ok = wait(S.k_full[next], npar))) break;
+                tc_fence_after();
+                scores(0, next);
+            }
+            if (two) {
+                if (!(ok = wait(S.p_full[1], i & 1))) break;
+                tc_fence_after();
+                outputs(1, st, i);
+            }
+            mma_commit(bar(S.v_empty[st]));
+            if (more) {
+                if (two) scores(1, next);
+                mma_commit(bar(S.k_empty[next]));
+            }
+        }
+        // Everything issued has completed when these arrive; tensor memory is freed after.
+        mma_commit(bar(S.o_full[0]));
+        mma_commit(bar(S.o_full[1]));
+        wait_bounded(bar(S.o_full[1]), 0, kDrainNs, nullptr);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps + kDeqWarps) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, int QT, int PT>
+cudaError_t launch(const PromptArgs& g, int64_t grid, cudaStream_t stream) {
+    constexpr int bytes = Layout<D, QT>::bytes + 1024;
+    static_assert(bytes + sizeof(PromptShared) <= 227 * 1024, "shared memory of one SM");
+    // One CTA holds an SM (it takes all of its tensor memory).
+    constexpr int asked = bytes > 116 * 1024 ? bytes : 116 * 1024;
+    const cudaError_t e = kernel_smem_once<attention_prompt_kernel<D, QT, PT>>(asked);
+    if (e != cudaSuccess) return e;
+    attention_prompt_kernel<D, QT, PT><<<(unsigned)grid, kThreads, asked, stream>>>(g);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attention_prompt_eligible(const q4lin_kv_cache_t& cache) { return cache.head_dim <= 128; }
+
+cudaError_t attention_prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
+                                    int64_t rows_min, const LaunchCtx& c) {
+    PromptArgs g;
+    g.cache = cache;
+    g.a = a;
+    g.page_shift = cache.page_size == 16 ? 4 : cache.page_size == 32 ? 5 : 6;
+    g.rows_min = rows_min;
+    g.q_vec = reinterpret_cast<uintptr_t>(a.query) % (4 * dtype_size(a.dtype)) == 0 &&
+              a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;
+    g.status = c.status_word;
+    g.wait_ns = c.wait_limit_ns;
+    // Tile pairs of all sequences at most: each taken one has more than rows_min rows.
+    const int64_t rows = a.tokens * (a.heads / cache.kv_heads);
+    const int64_t pairs = rows / (2 * kQ) + std::min(cache.batch, rows / (rows_min + 1));
+    const int64_t grid = std::max<int64_t>(1, pairs) * cache.kv_heads;
+    // One term where it is exact (see the head of this file).
+    if (a.dtype == Q4LIN_DTYPE_BF16 && !a.rope.cos)
+        return cache.head_dim == 64 ? launch<64, 1, 1>(g, grid, c.stream) : launch<128, 1, 1>(g, grid, c.stream);
+    if (a.dtype == Q4LIN_DTYPE_BF16)
+        return cache.head_dim == 64 ? launch<64, 2, 1>(g, grid, c.stream) : launch<128, 2, 1>(g, grid, c.stream);
+    return cache.head_dim == 64 ? launch<64, 2, 2>(g, grid, c.stream) : launch<128, 2, 2>(g, grid, c.stream);
+}
+
+}  // namespace q4lin

@@ -20,6 +20,7 @@ struct q4lin_handle {
     int tc_skip_first_copy = 0;
     int tc_f16 = 0;
     int tc_small_operands = 0;
+    int64_t attention_split_rows = 0;  // 0: the measured rule
     int* d_status = nullptr;
     float* d_ws = nullptr;     // split-K partial sums
     int* d_tickets = nullptr;  // split-K row-block counters (zero between launches)

@@ -13,6 +13,10 @@ using q4lin::overlaps;
 
 namespace {
 
+// Query rows (tokens x heads) per key/value head up to which a sequence's attention goes
+// through the kernel that splits the keys.
+constexpr int64_t kSplitRows = 64;
+
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 bool known_dtype(int dtype) { return dtype >= Q4LIN_DTYPE_F32 && dtype <= Q4LIN_DTYPE_BF16; }
 int64_t size_of(int dtype) { return dtype == Q4LIN_DTYPE_F32 ? 4 : 2; }
@@ -161,8 +165,16 @@ q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cac
     args.max_query = max_query;
     DeviceGuard g(h->device);
     if (!g.ok()) return Q4LIN_ERR_CUDA;
-    return finish(q4lin::attention_split_launch(*cache, args, INT64_MAX,
-                                                make_ctx(h, static_cast<cudaStream_t>(stream))));
+    const q4lin::LaunchCtx c = make_ctx(h, static_cast<cudaStream_t>(stream));
+    const int64_t split_rows = h->attention_split_rows > 0 ? h->attention_split_rows : kSplitRows;
+    if (max_query * group <= split_rows || !q4lin::attention_prompt_eligible(*cache))
+        return finish(q4lin::attention_split_launch(*cache, args, INT64_MAX, c));
+    // One sequence goes to the prompts' kernel whatever its length; of several, each kernel
+    // takes its own (lengths are on the device).
+    if (cache->batch == 1) return finish(q4lin::attention_prompt_launch(*cache, args, 0, c));
+    const cudaError_t err = q4lin::attention_prompt_launch(*cache, args, split_rows, c);
+    if (err != cudaSuccess) return finish(err);
+    return finish(q4lin::attention_split_launch(*cache, args, split_rows, c));
 }
 
 q4lin_status_t q4lin_run_logprobs(q4lin_handle_t h, const q4lin_logprobs_t* a, void* stream) {

@@ -495,6 +495,10 @@ q4lin_status_t q4lin_set_option(q4lin_handle_t h, int option, int64_t value) {
             if (value < 0 || value > 2) return Q4LIN_ERR_INVALID_ARG;
             h->tc_small_operands = (int)value;
             return Q4LIN_OK;
+        case Q4LIN_OPT_ATTENTION_SPLIT_ROWS:
+            if (value < 0) return Q4LIN_ERR_INVALID_ARG;
+            h->attention_split_rows = value;
+            return Q4LIN_OK;
         default:
             return Q4LIN_ERR_INVALID_ARG;
     }
@@ -512,6 +516,7 @@ q4lin_status_t q4lin_get_option(q4lin_handle_t h, int option, int64_t* value) {
         case Q4LIN_OPT_TC_SKIP_FIRST_COPY: *value = h->tc_skip_first_copy; return Q4LIN_OK;
         case Q4LIN_OPT_TC_F16: *value = h->tc_f16; return Q4LIN_OK;
         case Q4LIN_OPT_TC_SMALL_OPERANDS: *value = h->tc_small_operands; return Q4LIN_OK;
+        case Q4LIN_OPT_ATTENTION_SPLIT_ROWS: *value = h->attention_split_rows; return Q4LIN_OK;
         default: return Q4LIN_ERR_INVALID_ARG;
     }
 }

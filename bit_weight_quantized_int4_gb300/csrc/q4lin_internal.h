@@ -157,6 +157,10 @@ cudaError_t kv_append_launch(const q4lin_kv_cache_t& cache, const q4lin_kv_appen
 // per key/value head (a row: one query token of one head).
 cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
                                    int64_t rows_max, const LaunchCtx& c);
+// attention_prompt.cu: sequences of more than `rows_min` query rows per key/value head.
+bool attention_prompt_eligible(const q4lin_kv_cache_t& cache);
+cudaError_t attention_prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
+                                    int64_t rows_min, const LaunchCtx& c);
 cudaError_t logprobs_launch(const q4lin_logprobs_t& a, const LaunchCtx& c);
 cudaError_t logprobs_backward_launch(const q4lin_logprobs_backward_t& a, const LaunchCtx& c);
 

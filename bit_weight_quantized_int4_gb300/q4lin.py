@@ -64,6 +64,7 @@ Q4LIN_OPT_PDL = 4
 Q4LIN_OPT_TC_SKIP_FIRST_COPY = 5
 Q4LIN_OPT_TC_F16 = 6
 Q4LIN_OPT_TC_SMALL_OPERANDS = 7
+Q4LIN_OPT_ATTENTION_SPLIT_ROWS = 8
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 

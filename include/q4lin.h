@@ -125,7 +125,11 @@ typedef enum {
      * path's 4e-3 * sum|x*w| bar, and bf16 keeps fp32's exponent range.  0 (default): bf16
      * where it applies and the matrix has >= 100 blocks of 128 rows (measured faster there),
      * else tf32; 1: tf32 always; 2: bf16 wherever it applies. */
-    Q4LIN_OPT_TC_SMALL_OPERANDS = 7
+    Q4LIN_OPT_TC_SMALL_OPERANDS = 7,
+    /* Query rows (tokens x heads of one key/value head) up to which a sequence's attention
+     * goes through the kernel that splits the keys over the SMs; longer ones go through the
+     * prompts' tcgen05 kernel (head_dim 64 and 128).  0 (default): the measured crossover. */
+    Q4LIN_OPT_ATTENTION_SPLIT_ROWS = 8
 } q4lin_option_t;
 
 /* Create a handle for CUDA device `device`.  Queries the SM count and shared-memory
@@ -276,7 +280,7 @@ Q4LIN_API q4lin_status_t q4lin_run_requant(q4lin_handle_t handle, const float* l
 typedef enum { Q4LIN_DTYPE_F32 = 0, Q4LIN_DTYPE_F16 = 1, Q4LIN_DTYPE_BF16 = 2 } q4lin_dtype_t;
 
 /* A key/value cache in pages of page_size tokens.  A code c (one byte) of page p and head h
- * stands for (c - 128) * scale[p, h]; codes are 1..255.
+ * stands for (c - 128) * scale[p, h], scale >= 0.
  *   k_codes   uint8 [num_pages, kv_heads, page_size, head_dim], 16-byte aligned
  *   v_codes   uint8 [num_pages, kv_heads, head_dim, page_size], 16-byte aligned (values
  *             are kept transposed within a page, so that both products of the attention
@@ -362,12 +366,14 @@ typedef struct q4lin_attention {
  *   x_j = scale * sum_d q_d K[j,d],  out_d = sum_j e^(x_j) V[j,d] / sum_j e^(x_j),
  *   lse = ln sum_j e^(x_j).
  * A query that sees no key (an empty sequence, a negative position) gets out = 0 and
- * lse = -infinity.  Codes are exact in the tensor cores' fp16 operands; queries and
- * probabilities enter them as two fp16 terms (22 bits; one term, 11 bits, for the
- * probabilities and queries of 16-bit prompts, see below), and everything is summed in fp32.
- * Sequences with many query rows go through a tcgen05 kernel, the others through one that
- * splits the keys evenly over the SMs (partial results joined in a fixed order through the
- * handle's workspace), so a batch may mix prompts and single tokens.  tokens == 0 or
+ * lse = -infinity; a query with a NaN or an infinity gets NaN.  Codes are exact in the
+ * tensor cores' fp16 operands; queries and probabilities enter them as two fp16 terms (22
+ * bits), and everything is summed in fp32.  Sequences with many query rows go through a
+ * tcgen05 kernel (whose bfloat16 outputs take probabilities of one fp16 term, 11 bits, and
+ * which reads values relative to the largest value scale that its tile of queries sees),
+ * the others through one that splits the keys evenly over the SMs (partial
+ * results joined in a fixed order through the handle's workspace), so a batch may mix
+ * prompts and single tokens (Q4LIN_OPT_ATTENTION_SPLIT_ROWS).  tokens == 0 or
  * batch == 0 is Q4LIN_OK.  Sequences of more than max_query tokens record code 4, and
  * their outputs are not written. */
 Q4LIN_API q4lin_status_t q4lin_run_attention(q4lin_handle_t handle,

@@ -29,7 +29,8 @@ def status(handle):
 
 def check(out, lse, want, dtype):
     ref, ref_lse, vmax, smax = want
-    bound = (vmax * (2.0**-19 * smax + 2.0**-18))[..., None] + ops.ROUND[dtype] * np.abs(ref) + ops.TINY[dtype]
+    one_term = 2.0**-11 if dtype == "bf16" else 0.0
+    bound = (vmax * (2.0**-19 * smax + 2.0**-18 + one_term))[..., None] + ops.ROUND[dtype] * np.abs(ref) + ops.TINY[dtype]
     err = np.abs(ops.to_host(out) - ref)
     assert np.all(err <= bound), f"out: {np.max(err / bound):.3g} times the tolerance"
     got = ops.to_host(lse)
@@ -106,6 +107,50 @@ SEVERAL = [
 def test_several_tokens(handle, lengths, counts, heads, kv_heads, page, dim, dtype, causal, window):
     check(*run(handle, lengths, counts, heads, kv_heads, page, dim, dtype, causal=causal, window=window))
     assert status(handle) == 0
+
+
+PROMPTS = [
+    # lengths, query tokens, heads, kv heads, page, dim, dtype, causal, window
+    ([1], [1], 1, 1, 16, 64, "f32", True, 0),
+    ([5], [5], 4, 2, 64, 128, "f32", True, 0),
+    ([130, 9, 128], [3, 0, 5], 4, 1, 32, 128, "bf16", True, 0),
+    ([129, 300], [129, 2], 3, 1, 16, 128, "f16", True, 0),
+    ([200, 130], [17, 4], 6, 2, 64, 64, "bf16", False, 50),
+    ([700, 3, 0], [90, 5, 2], 7, 1, 32, 128, "f32", True, 100),
+    ([400], [400], 3, 1, 64, 64, "f32", True, 0),
+    ([513], [513], 2, 2, 16, 64, "bf16", True, 0),
+    ([640, 2], [200, 2], 5, 1, 64, 128, "bf16", True, 64),
+    ([3], [7], 2, 1, 64, 128, "f32", True, 0),
+    ([1500], [40], 8, 1, 32, 128, "f16", False, 0),
+]
+
+
+@pytest.mark.parametrize("lengths,counts,heads,kv_heads,page,dim,dtype,causal,window", PROMPTS)
+def test_prompt_kernel(handle, lengths, counts, heads, kv_heads, page, dim, dtype, causal, window):
+    """Every size through the prompts' kernel, then the same call by the other one."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    try:
+        for rows in (1, 1 << 40):
+            handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, rows)
+            check(*run(handle, lengths, counts, heads, kv_heads, page, dim, dtype, causal=causal, window=window))
+            assert status(handle) == 0
+    finally:
+        handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
+
+
+def test_values_of_very_different_pages(handle):
+    """Pages whose values are 2^12 apart, and one of zeros: rows that see only small ones."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(17)
+    host = ops.Cache(rng, [256], 1, 64, 128)
+    for i, s in enumerate((2.0**-12, 0.0, 1.0, 2.0**-12)):
+        host.vs[host.table[0, i]] = s
+    offsets = np.array([0, 256], np.int32)
+    q = torch.randn(256, 2, 128, device="cuda")
+    out, lse = q4lin.attention(handle, host.device(), q, ops.to_device(offsets),
+                               ops.to_device(np.array([256], np.int32)), 0.1)
+    check(out, lse, ops.attention(host, ops.to_host(q), offsets, [256], float(np.float32(0.1))), "f32")
 
 
 @pytest.mark.parametrize("rotated,interleaved", [(0, False), (32, False), (32, True), (128, True)])
