@@ -34,11 +34,16 @@ using namespace serving;
 
 constexpr int kQ = 128;     // rows per tile (MMA M = lanes of tensor memory)
 constexpr int kKeys = 128;  // keys per step
-constexpr int kSoftWarps = 8, kDeqWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kDeqWarps + 1);
+// Four warpgroups: two of softmax, one that widens codes, one whose first warp issues MMAs.
+constexpr int kSoftWarps = 8, kDeqWarps = 4, kWarps = 16, kThreads = 32 * kWarps;
+// Registers of their threads: launched with 128 each, 512 a column of four threads.
+constexpr int kSoftRegs = 184, kDeqRegs = 96, kIssueRegs = 48;
+static_assert(2 * kSoftRegs + kDeqRegs + kIssueRegs <= 4 * 128, "registers of the launch");
 constexpr int kScaleSlots = 4;
 constexpr float kBase = 7.f;    // weights are kept as 2^7 p ...
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
+// A score's factor is at least this, so that a masked score (-infinity) stays one.
+constexpr float kLeastFactor = 1e-37f;
 constexpr float kLeastRatio = 5.421010862427522e-20f;  // 2^-64
 constexpr int64_t kDrainNs = 4000000000LL;
 constexpr uint32_t kTmemCols = 512;
@@ -58,19 +63,21 @@ template <int D, int QT>
 struct Layout {
     static constexpr int kBlock = 128 * 128;           // 128 rows of 128 bytes
     static constexpr int kBlocks = D / 64;             // of a Q or K tile
-    static constexpr int kStages = QT == 1 ? 2 : 1;  // of K and V tiles
+    // Stages of K and V tiles: what fits (with two terms of 128 channels, one of K).
+    static constexpr int kStages = QT == 2 && D == 128 ? 1 : 2;
+    static constexpr int vStages = 2;
     static constexpr uint32_t q = 0;                                        // [tile][term][block]
     static constexpr uint32_t k = q + 2 * QT * kBlocks * kBlock;         // [stage][block]
     static constexpr uint32_t v = k + kStages * kBlocks * kBlock;           // [stage][2 x D rows of 128 B]
-    static constexpr uint32_t bytes = v + kStages * 2 * D * 128;
+    static constexpr uint32_t bytes = v + vStages * 2 * D * 128;
 };
 
 struct PromptShared {
     float factor[2 * kQ];
     float k_scale[kScaleSlots][8], v_log[kScaleSlots][8], v_inv[kScaleSlots][8];  // of 16 keys each
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
-    float v_max[kThreads / 32];
-    int sums[kThreads / 32];
+    float v_max[kWarps];
+    int sums[kWarps];
     int found_b, found_tile, failed;
     uint32_t tmem;
 };
@@ -83,16 +90,50 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, u
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// 16 columns of this warp's lanes, without waiting for completion.
-__device__ __forceinline__ void tmem_st16_async(uint32_t addr, const uint32_t* r) {
+// 8 or 16 columns of this warp's lanes, without waiting for completion.
+__device__ __forceinline__ void tmem_st8_async(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16_async(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+// 64 columns of this warp's lanes; the load and its wait are one statement, so that no use of
+// the registers is scheduled between them.
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t* r) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// A value that the compiler computes with anew where it stands: what it would otherwise keep
+// for a whole loop (an address for every piece of a tile) does not fit the registers.
+__device__ __forceinline__ void fresh(uint32_t& x) { asm volatile("" : "+r"(x)); }
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
+// 16 bytes, issued where it stands (a plain load may sink to its use, behind the waits).
+__device__ __forceinline__ void ld_codes(const uint8_t* p, uint4& v) {
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+}
 // Byte of 16-byte chunk `chunk` of row `row` in a 128-byte-swizzled block.
 __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
     return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
@@ -101,7 +142,7 @@ __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
 template <int D, int QT, int PT>
 __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const PromptArgs g) {
     using L = Layout<D, QT>;
-    constexpr int ST = L::kStages;
+    constexpr int KS = L::kStages, VS = L::vStages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PromptShared S;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -136,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         if (lane == 31) S.sums[warp] = sum;
         __syncthreads();
         int64_t before = carry;
-        for (int w = 0; w < kThreads / 32; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += S.sums[w];
             carry += S.sums[w];
         }
@@ -244,18 +285,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     const uint32_t tmem = S.tmem;
     float v_ref = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v_ref = fmaxf(v_ref, S.v_max[w]);
+    for (int w = 0; w < kWarps; ++w) v_ref = fmaxf(v_ref, S.v_max[w]);
     if (!(v_ref > 0.f)) v_ref = 1.f;  // values that are all zero
     volatile int* failed = &S.failed;
     auto bar = [](uint64_t& x) { return smem_u32(&x); };
+    // In line (a call would tie the warpgroups' registers together), bounded as everywhere.
+    auto wait_for = [&](uint64_t& x, uint32_t parity, int64_t limit, const volatile int* stop) {
+        if (mbar_try_wait(bar(x), parity)) return true;
+        const uint64_t t0 = global_timer();
+        while (!mbar_try_wait(bar(x), parity))
+            if ((stop && *stop) || (int64_t)(global_timer() - t0) > limit) return false;
+        return true;
+    };
     auto wait = [&](uint64_t& x, uint32_t parity) {
-        if (wait_bounded(bar(x), parity, g.wait_ns, failed)) return true;
+        if (wait_for(x, parity, g.wait_ns, failed)) return true;
         record_failure(g.status, failed);
         return false;
     };
 
     if (warp < kSoftWarps) {
         // -------------------------------------------------------------- softmax
+        more_registers<kSoftRegs>();
         const int tile = warp >> 2;
         const int r = tile * kQ + (warp & 3) * 32 + lane, row = row0 + r;
         const bool in = row < row_end;
@@ -274,26 +324,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             tc_fence_after();
             const int key0 = (step0 + i) * kKeys, slot = i % kScaleSlots;
             const int hi = min(limit - key0, kKeys), lo = (int)(low > key0 ? min(low - key0, (int64_t)kKeys) : 0);
+            uint32_t x[kKeys];
+            tmem_ld64(s_at, x);
+            tmem_ld64(s_at + 64, x + 64);
             // Columns [lo, hi] of the step are seen; all of them in most steps.
-            const bool part = __any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0);
+            if (__any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0)) {
+#pragma unroll
+                for (int e = 0; e < kKeys; ++e)
+                    if (e > hi || e < lo) x[e] = 0xFF800000u;
+            }
             float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c) {
-                uint32_t x[32];
-                tmem_ld32(s_at + 32 * c, x);
-                if (part) {
+            for (int c = 0; c < 8; ++c) {
+                float mx = max3(__uint_as_float(x[16 * c]), __uint_as_float(x[16 * c + 1]), __uint_as_float(x[16 * c + 2]));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e > hi || 32 * c + e < lo) x[e] = 0xFF800000u;
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float mx = __uint_as_float(x[16 * half]);
-#pragma unroll
-                    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(x[16 * half + e]));
-                    const float f = factor * S.k_scale[slot][2 * c + half];
-                    top = fmaxf(top, mx == -INFINITY ? mx : mx * f);
-                }
+                for (int e = 3; e < 15; e += 2)
+                    mx = max3(mx, __uint_as_float(x[16 * c + e]), __uint_as_float(x[16 * c + e + 1]));
+                mx = fmaxf(mx, __uint_as_float(x[16 * c + 15]));
+                top = fmaxf(top, mx * fmaxf(factor * S.k_scale[slot][c], kLeastFactor));
             }
             if (__any_sync(0xffffffffu, top > m + kSlack)) {
                 // Some row's maximum grew too far: O and l over to the new one.  (The product
@@ -303,52 +351,37 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                 m = now, l *= alpha;
                 if (i > 0) {
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t x[32];
-                        tmem_ld32(o_at + 32 * c, x);
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t y[16];
+                        tmem_ld16(o_at + 16 * c, y);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-                        tmem_st32_async(o_at + 32 * c, x);
+                        for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+                        tmem_st16_async(o_at + 16 * c, y);
                     }
                 }
             }
             const float origin = kBase - (m == -INFINITY ? 0.f : m);
-            uint32_t rest[PT == 2 ? 64 : 1];
 #pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c) {
-                uint32_t x[32], p[16];
-                tmem_ld32(s_at + 32 * c, x);
-                if (part) {
+            for (int c = 0; c < 8; ++c) {
+                const float f = fmaxf(factor * S.k_scale[slot][c], kLeastFactor), off = origin + S.v_log[slot][c];
+                const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+                float2 sum = make_float2(0.f, 0.f);
+                uint32_t p[8], rest[8];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e > hi || 32 * c + e < lo) x[e] = 0xFF800000u;
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int at = 2 * c + half;
-                    const float f = factor * S.k_scale[slot][at], off = origin + S.v_log[slot][at];
-                    float sum = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float a = __uint_as_float(x[16 * half + e]), b2 = __uint_as_float(x[16 * half + e + 1]);
-                        const float pa = ex2(a == -INFINITY ? a : fmaf(a, f, off));
-                        const float pb = ex2(b2 == -INFINITY ? b2 : fmaf(b2, f, off));
-                        sum += pa + pb;
-                        const int w = 8 * half + e / 2;
-                        if (PT == 2) {
-                            split_f16(pa, pb, &p[w], &rest[16 * c + w]);
-                        } else {
-                            const __half2 v = __floats2half2_rn(pa, pb);
-                            p[w] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
+                for (int e = 0; e < 8; ++e) {
+                    float2 y = ffma2(make_float2(__uint_as_float(x[16 * c + 2 * e]), __uint_as_float(x[16 * c + 2 * e + 1])), f2, off2);
+                    y.x = ex2(y.x), y.y = ex2(y.y);
+                    sum = fadd2(sum, y);
+                    if (PT == 2) {
+                        split_f16(y.x, y.y, &p[e], &rest[e]);
+                    } else {
+                        const __half2 v = __floats2half2_rn(y.x, y.y);
+                        p[e] = *reinterpret_cast<const uint32_t*>(&v);
                     }
-                    l = fmaf(sum, S.v_inv[slot][at], l);
                 }
-                tmem_st16_async(s_at + 16 * c, p);  // over scores that have been read
-            }
-            if (PT == 2) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_st16_async(s_at + 64 + 16 * c, rest + (PT == 2 ? 16 * c : 0));
+                l = fmaf(sum.x + sum.y, S.v_inv[slot][c], l);
+                tmem_st8_async(s_at + 8 * c, p);  // over the scores
+                if (PT == 2) tmem_st8_async(s_at + 64 + 8 * c, rest);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -388,37 +421,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         }
     } else if (warp < kSoftWarps + kDeqWarps) {
         // ------------------------------------------------ codes into fp16 tiles
-        const int t = tid - 32 * kSoftWarps;
-        constexpr int kPieces = kKeys * D / 16 / (32 * kDeqWarps);  // 16-byte pieces per thread
+        fewer_registers<kDeqRegs>();
+        const uint32_t t = tid - 32 * kSoftWarps;
+        constexpr uint32_t kPieces = kKeys * D / 16 / (32 * kDeqWarps);  // 16-byte pieces per thread
         constexpr int kRowPieces = D / 16;
-        const int page_pieces = (D << ps) / 16, slot_pieces = (1 << ps) / 16;
+        // Piece j of a thread, p = t + 128 j: 16 channels of key p / (D / 16), or 16 keys of
+        // a channel, page by page.  Either way it lies in group p / D of 16 keys.
+        constexpr int kLogD = D == 64 ? 6 : 7;
+        const int page_shift = kLogD + ps - 4;
+        const uint32_t page_pieces = 1u << page_shift, slot_pieces = 1u << ps >> 4;
         uint4 kreg[kPieces], vreg[kPieces];
-        const uint4 zero = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        auto page_of = [&](int i, int token) {  // page id of a key of step i, -1 past the end
-            const int p = ((step0 + i) * kKeys + token) >> ps;
-            if (i >= n || p >= pages) return -1;
+        // Page of group `lane` of 16 keys of step i, -1 past the end.
+        auto fetch_ids = [&](int i) {
+            const int p = ((step0 + i) * kKeys + lane * 16) >> ps;
+            if (lane >= 8 || i >= n || p >= pages) return -1;
             const int id = __ldg(table + p);
             return id < 0 || id >= C.num_pages ? 0 : id;
         };
-        auto load_k = [&](int i) {
+        auto load = [&](const uint8_t* codes, int ids, uint4* reg) {
+            uint32_t tl = t;
+            fresh(tl);
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                const int p = t + 32 * kDeqWarps * j, token = p / kRowPieces, c = p % kRowPieces;
-                const int id = page_of(i, token);
-                kreg[j] = id < 0 ? zero
-                                 : __ldg(reinterpret_cast<const uint4*>(
-                                       C.k_codes + (((int64_t)id * Hkv + h) << ps) * D +
-                                       (token & ((1 << ps) - 1)) * D + c * 16));
-            }
-        };
-        auto load_v = [&](int i) {
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-                const int p = t + 32 * kDeqWarps * j, pg = p / page_pieces, rem = p % page_pieces;
-                const int id = page_of(i, pg << ps);
-                vreg[j] = id < 0 ? zero
-                                 : __ldg(reinterpret_cast<const uint4*>(
-                                       C.v_codes + (((int64_t)id * Hkv + h) << ps) * D + rem * 16));
+                const uint32_t p = tl + 32 * kDeqWarps * j;
+                const int id = __shfl_sync(0xffffffffu, ids, p / D);
+                const uint32_t at = (p & page_pieces - 1) * 16;
+                reg[j] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+                if (id >= 0) ld_codes(codes + (((int64_t)id * Hkv + h) << ps) * D + at, reg[j]);
             }
         };
         // 16 codes as two 16-byte chunks of fp16, chunks 2 c and 2 c + 1 of the row.
@@ -437,105 +466,121 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                 st_shared_v4(b2, f[4], f[5], f[6], f[7]);
             }
         };
-        load_k(0);
-        load_v(0);
+        int ids = fetch_ids(0), ids_next = fetch_ids(1);
+        load(C.k_codes, ids, kreg);
+        load(C.v_codes, ids, vreg);
         for (int i = 0; i < n; ++i) {
-            const int st = i % ST;
-            const uint32_t again = (uint32_t)(i / ST - 1) & 1u;
+            const int kst = i % KS, vst = i % VS;
             float ks = 0.f, vs = 0.f;
-            if (t < 8) {
-                const int id = page_of(i, t * 16);
-                if (id >= 0) {
-                    ks = __ldg(C.k_scales + (int64_t)id * Hkv + h);
-                    vs = __ldg(C.v_scales + (int64_t)id * Hkv + h);
-                }
+            if (ids >= 0 && t < 8) {
+                ks = __ldg(C.k_scales + (int64_t)ids * Hkv + h);
+                vs = __ldg(C.v_scales + (int64_t)ids * Hkv + h);
             }
-            if (i >= ST && !wait(S.k_empty[st], again)) break;
+            ids = ids_next, ids_next = fetch_ids(i + 2);
+            if (i >= KS && !__all_sync(0xffffffffu, wait(S.k_empty[kst], (uint32_t)(i / KS - 1) & 1u))) break;
             if (t < 8) {
                 // Far below fp16's range a weight is 0 in the product; in l it counts.
                 const float ratio = fmaxf(vs / v_ref, kLeastRatio);
                 const int slot = i % kScaleSlots;
                 S.k_scale[slot][t] = ks, S.v_log[slot][t] = lg2(ratio), S.v_inv[slot][t] = 1.f / ratio;
             }
-            const uint32_t kt = base + L::k + (uint32_t)(st * L::kBlocks) * L::kBlock;
+            const uint32_t kt = base + L::k + (uint32_t)(kst * L::kBlocks) * L::kBlock;
+            uint32_t tk = t;
+            fresh(tk);
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                const int p = t + 32 * kDeqWarps * j, token = p / kRowPieces, c = p % kRowPieces;
+                const uint32_t p = tk + 32 * kDeqWarps * j, token = p / kRowPieces, c = p % kRowPieces;
                 put(kt + (uint32_t)(c / 4) * L::kBlock, token, c % 4, kreg[j], (c / 4) & 1);
             }
             fence_async_shared();
-            mbar_arrive(bar(S.k_full[st]));
-            load_k(i + 1);
-            if (i >= ST && !wait(S.v_empty[st], again)) break;
-            const uint32_t vt = base + L::v + (uint32_t)st * (2 * D * 128);
+            mbar_arrive(bar(S.k_full[kst]));
+            load(C.k_codes, ids, kreg);
+            if (i >= VS && !__all_sync(0xffffffffu, wait(S.v_empty[vst], (uint32_t)(i / VS - 1) & 1u))) break;
+            const uint32_t vt = base + L::v + (uint32_t)vst * (2 * D * 128);
+            uint32_t tv = t;
+            fresh(tv);
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                const int p = t + 32 * kDeqWarps * j, pg = p / page_pieces, rem = p % page_pieces;
-                const int d = rem / slot_pieces, key = (pg << ps) + (rem % slot_pieces) * 16;
+                // (The divisors are powers of two that depend on the page size.)
+                const uint32_t p = tv + 32 * kDeqWarps * j, pg = p >> page_shift, rem = p & page_pieces - 1;
+                const uint32_t d = rem >> ps - 4, key = (pg << ps) + (rem & slot_pieces - 1) * 16;
                 put(vt + (uint32_t)(key / 64) * (D * 128), d, (key % 64) / 16, vreg[j], 0);
             }
             fence_async_shared();
-            mbar_arrive(bar(S.v_full[st]));
-            load_v(i + 1);
+            mbar_arrive(bar(S.v_full[vst]));
+            load(C.v_codes, ids, vreg);
         }
-    } else if (lane == 0 && n > 0) {
+    } else {
         // ------------------------------------------------------------ MMA issue
-        const uint32_t idesc_s = f16_idesc(kQ, kKeys), idesc_o = f16_idesc(kQ, D);
-        auto scores = [&](int tile, int st) {
+        fewer_registers<kIssueRegs>();
+        if (warp == kSoftWarps + kDeqWarps && lane == 0 && n > 0) {
+            const uint32_t idesc_s = f16_idesc(kQ, kKeys), idesc_o = f16_idesc(kQ, D);
+            // Low words of the descriptors; 32 bytes along a swizzled row are 2 in their address
+            // field, a block of 64 channels (keys) is kBlock / 16 (the high words are all alike).
+            const uint64_t desc0 = sw128_desc(base);
+            const uint32_t high = (uint32_t)(desc0 >> 32), low0 = (uint32_t)desc0;
+            auto desc = [&](uint32_t low_word) { return (uint64_t)high << 32 | low_word; };
+            auto scores = [&](int tile, int st) {
+                uint32_t k_low = low0 + ((L::k + (uint32_t)(st * L::kBlocks) * L::kBlock) >> 4);
+                uint32_t q_low = low0 + ((L::q + (uint32_t)(tile * QT * L::kBlocks) * L::kBlock) >> 4);
+                const uint32_t d = tmem + kScoreCol + tile * kKeys;
+                fresh(k_low), fresh(q_low);
+#pragma unroll 1
+                for (int term = 0; term < QT; ++term, q_low += L::kBlocks * L::kBlock >> 4)
 #pragma unroll
-            for (int term = 0; term < QT; ++term)
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t at = (uint32_t)(kk / 4) * (L::kBlock >> 4) + 2 * (kk % 4);
+                        mma_f16_ss(d, desc(q_low + at), desc(k_low + at), idesc_s, term + kk > 0);
+                    }
+                mma_commit(bar(S.s_full[tile]));
+            };
+            auto outputs = [&](int tile, int st, int i) {
+                uint32_t v_low = low0 + ((L::v + (uint32_t)st * (2 * D * 128)) >> 4);
+                uint32_t p_at = tmem + kScoreCol + tile * kKeys;
+                fresh(v_low), fresh(p_at);
+#pragma unroll 1
+                for (int term = 0; term < PT; ++term, p_at += 64)
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t a = sw128_desc(base + L::q + (uint32_t)((tile * QT + term) * L::kBlocks + kk / 4) * L::kBlock) + 2 * (kk % 4);
-                    const uint64_t b2 = sw128_desc(base + L::k + (uint32_t)(st * L::kBlocks + kk / 4) * L::kBlock) + 2 * (kk % 4);
-                    mma_f16_ss(tmem + kScoreCol + tile * kKeys, a, b2, idesc_s, term + kk > 0);
-                }
-            mma_commit(bar(S.s_full[tile]));
-        };
-        auto outputs = [&](int tile, int st, int i) {
-#pragma unroll
-            for (int term = 0; term < PT; ++term)
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk) {
-                    const uint64_t b2 = sw128_desc(base + L::v + (uint32_t)st * (2 * D * 128) + (uint32_t)(kk / 4) * (D * 128)) + 2 * (kk % 4);
-                    mma_f16_ts(tmem + tile * 128, tmem + kScoreCol + tile * kKeys + term * 64 + 8 * kk, b2, idesc_o,
-                               i > 0 || term + kk > 0);
-                }
-        };
-        bool ok = wait(S.k_full[0], 0);
-        if (ok) {
-            tc_fence_after();
-            scores(0, 0);
-            if (two) scores(1, 0);
-            mma_commit(bar(S.k_empty[0]));
-        }
-        for (int i = 0; ok && i < n; ++i) {
-            const int st = i % ST, next = (i + 1) % ST;
-            const uint32_t par = (uint32_t)(i / ST) & 1u, npar = (uint32_t)((i + 1) / ST) & 1u;
-            const bool more = i + 1 < n;
-            if (!(ok = wait(S.v_full[st], par) && wait(S.p_full[0], i & 1))) break;
-            tc_fence_after();
-            outputs(0, st, i);
-            if (more) {
-                if (!(ok = wait(S.k_full[next], npar))) break;
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_f16_ts(tmem + tile * 128, p_at + 8 * kk,
+                                   desc(v_low + (uint32_t)(kk / 4) * (D * 128 >> 4) + 2 * (kk % 4)), idesc_o,
+                                   i > 0 || term + kk > 0);
+            };
+            bool ok = wait(S.k_full[0], 0);
+            if (ok) {
                 tc_fence_after();
-                scores(0, next);
+                scores(0, 0);
+                if (two) scores(1, 0);
+                mma_commit(bar(S.k_empty[0]));
             }
-            if (two) {
-                if (!(ok = wait(S.p_full[1], i & 1))) break;
+            for (int i = 0; ok && i < n; ++i) {
+                const int st = i % VS, next = (i + 1) % KS;
+                const uint32_t par = (uint32_t)(i / VS) & 1u, npar = (uint32_t)((i + 1) / KS) & 1u;
+                const bool more = i + 1 < n;
+                if (!(ok = wait(S.v_full[st], par) && wait(S.p_full[0], i & 1))) break;
                 tc_fence_after();
-                outputs(1, st, i);
+                outputs(0, st, i);
+                if (more) {
+                    if (!(ok = wait(S.k_full[next], npar))) break;
+                    tc_fence_after();
+                    scores(0, next);
+                }
+                if (two) {
+                    if (!(ok = wait(S.p_full[1], i & 1))) break;
+                    tc_fence_after();
+                    outputs(1, st, i);
+                }
+                mma_commit(bar(S.v_empty[st]));
+                if (more) {
+                    if (two) scores(1, next);
+                    mma_commit(bar(S.k_empty[next]));
+                }
             }
-            mma_commit(bar(S.v_empty[st]));
-            if (more) {
-                if (two) scores(1, next);
-                mma_commit(bar(S.k_empty[next]));
-            }
+            // Everything issued has completed when these arrive; tensor memory is freed after.
+            mma_commit(bar(S.o_full[0]));
+            mma_commit(bar(S.o_full[1]));
+            wait_for(S.o_full[1], 0, kDrainNs, nullptr);
         }
-        // Everything issued has completed when these arrive; tensor memory is freed after.
-        mma_commit(bar(S.o_full[0]));
-        mma_commit(bar(S.o_full[1]));
-        wait_bounded(bar(S.o_full[1]), 0, kDrainNs, nullptr);
     }
     __syncwarp();
     tc_fence_before();
