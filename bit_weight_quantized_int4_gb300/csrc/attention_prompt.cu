@@ -82,12 +82,39 @@ struct PromptShared {
     uint32_t tmem;
 };
 
-// D (tensor memory) (+)= A B^T, both fp16 operands from shared memory.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMAs are issued by one lane of a warp that runs as a whole, so that addresses and
+// descriptors stay in uniform registers (a lone thread's have to be moved there one by one,
+// which took longer than the MMAs: 100 against 64 clocks each).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t leader;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(leader));
+    return leader;
+}
+// D (tensor memory) (+)= A B^T, both fp16 operands from shared memory.
+__device__ __forceinline__ void mma_f16_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(leader)
+        : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
         : "memory");
 }
 // 8 or 16 columns of this warp's lanes, without waiting for completion.
@@ -148,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
     const q4lin_kv_cache_t& C = g.cache;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ps = g.page_shift;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, ps = g.page_shift;
     const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads);
     const int h = (int)(blockIdx.x % Hkv);
     const int64_t want = blockIdx.x / Hkv;  // which tile pair of the whole call
@@ -282,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = S.tmem;
+    // All of the SM's tensor memory is this CTA's, so it begins at 0.
+    constexpr uint32_t tmem = 0;
     float v_ref = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v_ref = fmaxf(v_ref, S.v_max[w]);
@@ -513,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     } else {
         // ------------------------------------------------------------ MMA issue
         fewer_registers<kIssueRegs>();
-        if (warp == kSoftWarps + kDeqWarps && lane == 0 && n > 0) {
+        if (warp == kSoftWarps + kDeqWarps && n > 0) {
+            const uint32_t leader = elect_one();
             const uint32_t idesc_s = f16_idesc(kQ, kKeys), idesc_o = f16_idesc(kQ, D);
             // Low words of the descriptors; 32 bytes along a swizzled row are 2 in their address
             // field, a block of 64 channels (keys) is kBlock / 16 (the high words are all alike).
@@ -524,61 +553,59 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                 uint32_t k_low = low0 + ((L::k + (uint32_t)(st * L::kBlocks) * L::kBlock) >> 4);
                 uint32_t q_low = low0 + ((L::q + (uint32_t)(tile * QT * L::kBlocks) * L::kBlock) >> 4);
                 const uint32_t d = tmem + kScoreCol + tile * kKeys;
-                fresh(k_low), fresh(q_low);
 #pragma unroll 1
                 for (int term = 0; term < QT; ++term, q_low += L::kBlocks * L::kBlock >> 4)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t at = (uint32_t)(kk / 4) * (L::kBlock >> 4) + 2 * (kk % 4);
-                        mma_f16_ss(d, desc(q_low + at), desc(k_low + at), idesc_s, term + kk > 0);
+                        mma_f16_ss(leader, d, desc(q_low + at), desc(k_low + at), idesc_s, term + kk > 0);
                     }
-                mma_commit(bar(S.s_full[tile]));
+                mma_commit(leader, bar(S.s_full[tile]));
             };
             auto outputs = [&](int tile, int st, int i) {
                 uint32_t v_low = low0 + ((L::v + (uint32_t)st * (2 * D * 128)) >> 4);
                 uint32_t p_at = tmem + kScoreCol + tile * kKeys;
-                fresh(v_low), fresh(p_at);
 #pragma unroll 1
                 for (int term = 0; term < PT; ++term, p_at += 64)
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_f16_ts(tmem + tile * 128, p_at + 8 * kk,
+                        mma_f16_ts(leader, tmem + tile * 128, p_at + 8 * kk,
                                    desc(v_low + (uint32_t)(kk / 4) * (D * 128 >> 4) + 2 * (kk % 4)), idesc_o,
                                    i > 0 || term + kk > 0);
             };
-            bool ok = wait(S.k_full[0], 0);
+            bool ok = __all_sync(0xffffffffu, wait(S.k_full[0], 0));
             if (ok) {
                 tc_fence_after();
                 scores(0, 0);
                 if (two) scores(1, 0);
-                mma_commit(bar(S.k_empty[0]));
+                mma_commit(leader, bar(S.k_empty[0]));
             }
             for (int i = 0; ok && i < n; ++i) {
                 const int st = i % VS, next = (i + 1) % KS;
                 const uint32_t par = (uint32_t)(i / VS) & 1u, npar = (uint32_t)((i + 1) / KS) & 1u;
                 const bool more = i + 1 < n;
-                if (!(ok = wait(S.v_full[st], par) && wait(S.p_full[0], i & 1))) break;
+                if (!(ok = __all_sync(0xffffffffu, wait(S.v_full[st], par) && wait(S.p_full[0], i & 1)))) break;
                 tc_fence_after();
                 outputs(0, st, i);
                 if (more) {
-                    if (!(ok = wait(S.k_full[next], npar))) break;
+                    if (!(ok = __all_sync(0xffffffffu, wait(S.k_full[next], npar)))) break;
                     tc_fence_after();
                     scores(0, next);
                 }
                 if (two) {
-                    if (!(ok = wait(S.p_full[1], i & 1))) break;
+                    if (!(ok = __all_sync(0xffffffffu, wait(S.p_full[1], i & 1)))) break;
                     tc_fence_after();
                     outputs(1, st, i);
                 }
-                mma_commit(bar(S.v_empty[st]));
+                mma_commit(leader, bar(S.v_empty[st]));
                 if (more) {
                     if (two) scores(1, next);
-                    mma_commit(bar(S.k_empty[next]));
+                    mma_commit(leader, bar(S.k_empty[next]));
                 }
             }
             // Everything issued has completed when these arrive; tensor memory is freed after.
-            mma_commit(bar(S.o_full[0]));
-            mma_commit(bar(S.o_full[1]));
+            mma_commit(leader, bar(S.o_full[0]));
+            mma_commit(leader, bar(S.o_full[1]));
             wait_for(S.o_full[1], 0, kDrainNs, nullptr);
         }
     }
