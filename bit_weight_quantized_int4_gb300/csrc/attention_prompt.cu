@@ -4,7 +4,7 @@
 // A row is one query token of one head; the heads that share a key/value head are rows of one
 // list (token-major), so grouped heads fill the MMA's 128 rows and share the keys.  A CTA
 // takes two tiles of 128 rows and walks over 128 keys at a time:
-//   dequantizing warps  codes from global memory into fp16 K and V tiles in shared memory
+//   widening warps      codes from global memory into fp16 K and V tiles in shared memory
 //                       (code - 128 is exact in fp16; both are stored with the axis that the
 //                       product sums over contiguous, 128-byte swizzled),
 //   one issuing thread  S = Q K^T into tensor memory, then O += P V with P read from there,
@@ -34,12 +34,14 @@ using namespace serving;
 
 constexpr int kQ = 128;     // rows per tile (MMA M = lanes of tensor memory)
 constexpr int kKeys = 128;  // keys per step
-// Four warpgroups: two of softmax, one that widens codes, one whose first warp issues MMAs.
-constexpr int kSoftWarps = 8, kDeqWarps = 4, kWarps = 16, kThreads = 32 * kWarps;
-// Registers of their threads: launched with 128 each, 512 a column of four threads.
-constexpr int kSoftRegs = 184, kDeqRegs = 96, kIssueRegs = 48;
-static_assert(2 * kSoftRegs + kDeqRegs + kIssueRegs <= 4 * 128, "registers of the launch");
-constexpr int kScaleSlots = 4;
+// Five warpgroups: two of softmax, one that widens keys, one values, one whose first warp
+// issues the MMAs.
+constexpr int kSoftWarps = 8, kValueWarp = 12, kIssueWarp = 16;
+constexpr int kWarps = 20, kThreads = 32 * kWarps;
+// Registers of their threads: launched with 96 each.
+constexpr int kSoftRegs = 176, kWidenRegs = 48, kIssueRegs = 32;
+static_assert(2 * kSoftRegs + 2 * kWidenRegs + kIssueRegs <= 5 * 96, "registers of the launch");
+constexpr int kScaleSlots = 6;  // steps whose scales are kept: the widening warps are up to four ahead
 constexpr float kBase = 7.f;    // weights are kept as 2^7 p ...
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
 // A score's factor is at least this, so that a masked score (-infinity) stays one.
@@ -59,23 +61,25 @@ struct PromptArgs {
     int64_t wait_ns;
 };
 
+// Shared memory.  A step's K tile is D / 64 blocks of 64 channels, its V tile two blocks of 64
+// keys; both come and go by block through rings, as much as fits (three of each beside 128
+// channels of two terms: half a tile is widened while the other's products run).
 template <int D, int QT>
 struct Layout {
     static constexpr int kBlock = 128 * 128;           // 128 rows of 128 bytes
     static constexpr int kBlocks = D / 64;             // of a Q or K tile
-    // Stages of K and V tiles: what fits (with two terms of 128 channels, one of K).
-    static constexpr int kStages = QT == 2 && D == 128 ? 1 : 2;
-    static constexpr int vStages = 2;
-    static constexpr uint32_t q = 0;                                        // [tile][term][block]
-    static constexpr uint32_t k = q + 2 * QT * kBlocks * kBlock;         // [stage][block]
-    static constexpr uint32_t v = k + kStages * kBlocks * kBlock;           // [stage][2 x D rows of 128 B]
-    static constexpr uint32_t bytes = v + vStages * 2 * D * 128;
+    static constexpr int vBlock = D * 128;
+    static constexpr int kRing = QT == 2 && D == 128 ? 3 : 4, vRing = kRing;
+    static constexpr uint32_t q = 0;                                  // [tile][term][block]
+    static constexpr uint32_t k = q + 2 * QT * kBlocks * kBlock;      // [slot]
+    static constexpr uint32_t v = k + kRing * kBlock;                 // [slot]
+    static constexpr uint32_t bytes = v + vRing * vBlock;
 };
 
 struct PromptShared {
     float factor[2 * kQ];
     float k_scale[kScaleSlots][8], v_log[kScaleSlots][8], v_inv[kScaleSlots][8];  // of 16 keys each
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2];
     float v_max[kWarps];
     int sums[kWarps];
     int found_b, found_tile, failed;
@@ -143,9 +147,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// A value that the compiler computes with anew where it stands: what it would otherwise keep
-// for a whole loop (an address for every piece of a tile) does not fit the registers.
-__device__ __forceinline__ void fresh(uint32_t& x) { asm volatile("" : "+r"(x)); }
 template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -169,7 +170,6 @@ __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
 template <int D, int QT, int PT>
 __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const PromptArgs g) {
     using L = Layout<D, QT>;
-    constexpr int KS = L::kStages, VS = L::vStages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PromptShared S;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -234,18 +234,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
 
     // ---- prologue: barriers, tensor memory, the largest value scale, queries
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&S.k_full[s]), 32 * kDeqWarps);
-            mbar_init(smem_u32(&S.v_full[s]), 32 * kDeqWarps);
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(smem_u32(&S.k_full[s]), 128);
+            mbar_init(smem_u32(&S.v_full[s]), 128);
             mbar_init(smem_u32(&S.k_empty[s]), 1);
             mbar_init(smem_u32(&S.v_empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&S.s_full[s]), 1);
             mbar_init(smem_u32(&S.p_full[s]), kQ);
             mbar_init(smem_u32(&S.o_full[s]), 1);
         }
         mbar_init_fence();
     }
-    if (warp == kSoftWarps + kDeqWarps) tmem_alloc(smem_u32(&S.tmem), kTmemCols);
+    if (warp == kIssueWarp) tmem_alloc(smem_u32(&S.tmem), kTmemCols);
     float v_max = 0.f;
     for (int p = ((step0 * kKeys) >> ps) + tid; p < min(pages, (step1 * kKeys) >> ps); p += kThreads) {
         const int id = __ldg(table + p);
@@ -447,101 +449,105 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             }
             if (in && g.a.lse) g.a.lse[index] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l) - kBase) * kLn2 : -INFINITY;
         }
-    } else if (warp < kSoftWarps + kDeqWarps) {
-        // ------------------------------------------------ codes into fp16 tiles
-        fewer_registers<kDeqRegs>();
-        const uint32_t t = tid - 32 * kSoftWarps;
-        constexpr uint32_t kPieces = kKeys * D / 16 / (32 * kDeqWarps);  // 16-byte pieces per thread
-        constexpr int kRowPieces = D / 16;
-        // Piece j of a thread, p = t + 128 j: 16 channels of key p / (D / 16), or 16 keys of
-        // a channel, page by page.  Either way it lies in group p / D of 16 keys.
-        constexpr int kLogD = D == 64 ? 6 : 7;
-        const int page_shift = kLogD + ps - 4;
-        const uint32_t page_pieces = 1u << page_shift, slot_pieces = 1u << ps >> 4;
-        uint4 kreg[kPieces], vreg[kPieces];
-        // Page of group `lane` of 16 keys of step i, -1 past the end.
-        auto fetch_ids = [&](int i) {
+    } else if (warp < kIssueWarp) {
+        // ------------------------- codes into fp16 blocks: keys, and values, 128 threads each
+        fewer_registers<kWidenRegs>();
+        const bool keys = warp < kValueWarp;
+        const int t = tid & 127;
+        // One ring each, a step's blocks in the order of their use.
+        auto walk = [&](auto&& widen) {
+            if (keys)
+                widen(S.k_full, S.k_empty, base + L::k, L::kBlock, L::kRing, L::kBlocks, C.k_codes);
+            else
+                widen(S.v_full, S.v_empty, base + L::v, L::vBlock, L::vRing, 2, C.v_codes);
+        };
+        // Head's share of the page of group `lane` of 16 keys of step i, -1 past the end.
+        auto fetch_pages = [&](int i) {
             const int p = ((step0 + i) * kKeys + lane * 16) >> ps;
             if (lane >= 8 || i >= n || p >= pages) return -1;
             const int id = __ldg(table + p);
-            return id < 0 || id >= C.num_pages ? 0 : id;
+            return (id < 0 || id >= C.num_pages ? 0 : id) * Hkv + h;
         };
-        auto load = [&](const uint8_t* codes, int ids, uint4* reg) {
-            uint32_t tl = t;
-            fresh(tl);
+        walk([&](uint64_t* full, uint64_t* empty, uint32_t ring, uint32_t block, int depth, int blocks,
+                 const uint8_t* codes) {
+            // A thread's pieces of 16 codes: of a block of keys, 16 channels of key t / 4 + 32 j
+            // (t % 4); of a block of values, 16 keys of a channel, in the order of the page.
+            const int count = keys ? 4 : D / 32;  // pieces per thread and block
+            const uint32_t page_bytes = (uint32_t)D << ps;
+            uint4 reg[4];
+            int pages_now = fetch_pages(0), pages_next = fetch_pages(1);
+            auto load = [&](int page_ids, int blk) {
 #pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-                const uint32_t p = tl + 32 * kDeqWarps * j;
-                const int id = __shfl_sync(0xffffffffu, ids, p / D);
-                const uint32_t at = (p & page_pieces - 1) * 16;
-                reg[j] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-                if (id >= 0) ld_codes(codes + (((int64_t)id * Hkv + h) << ps) * D + at, reg[j]);
-            }
-        };
-        // 16 codes as two 16-byte chunks of fp16, chunks 2 c and 2 c + 1 of the row.
-        auto put = [&](uint32_t block, int row, int c, const uint4& w, int odd) {
-            uint32_t f[8];
-            codes_f16(w.x, &f[0], &f[1]);
-            codes_f16(w.y, &f[2], &f[3]);
-            codes_f16(w.z, &f[4], &f[5]);
-            codes_f16(w.w, &f[6], &f[7]);
-            const uint32_t a = block + swizzled(row, 2 * c), b2 = block + swizzled(row, 2 * c + 1);
-            if (odd) {  // the order of the two stores keeps a quarter-warp off its own banks
-                st_shared_v4(b2, f[4], f[5], f[6], f[7]);
-                st_shared_v4(a, f[0], f[1], f[2], f[3]);
-            } else {
-                st_shared_v4(a, f[0], f[1], f[2], f[3]);
-                st_shared_v4(b2, f[4], f[5], f[6], f[7]);
-            }
-        };
-        int ids = fetch_ids(0), ids_next = fetch_ids(1);
-        load(C.k_codes, ids, kreg);
-        load(C.v_codes, ids, vreg);
-        for (int i = 0; i < n; ++i) {
-            const int kst = i % KS, vst = i % VS;
-            float ks = 0.f, vs = 0.f;
-            if (ids >= 0 && t < 8) {
-                ks = __ldg(C.k_scales + (int64_t)ids * Hkv + h);
-                vs = __ldg(C.v_scales + (int64_t)ids * Hkv + h);
-            }
-            ids = ids_next, ids_next = fetch_ids(i + 2);
-            if (i >= KS && !__all_sync(0xffffffffu, wait(S.k_empty[kst], (uint32_t)(i / KS - 1) & 1u))) break;
-            if (t < 8) {
-                // Far below fp16's range a weight is 0 in the product; in l it counts.
-                const float ratio = fmaxf(vs / v_ref, kLeastRatio);
-                const int slot = i % kScaleSlots;
-                S.k_scale[slot][t] = ks, S.v_log[slot][t] = lg2(ratio), S.v_inv[slot][t] = 1.f / ratio;
-            }
-            const uint32_t kt = base + L::k + (uint32_t)(kst * L::kBlocks) * L::kBlock;
-            uint32_t tk = t;
-            fresh(tk);
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= count) continue;
+                    uint32_t group, at;
+                    if (keys) {
+                        const uint32_t key = t / 4 + 32 * j;
+                        group = key / 16, at = (key & (1u << ps) - 1) * D + blk * 64 + t % 4 * 16;
+                    } else {
+                        const uint32_t q = t + 128 * j;
+                        group = q / D, at = q * 16 & page_bytes - 1;
+                        group += 4 * blk;
+                    }
+                    const int page = __shfl_sync(0xffffffffu, page_ids, group);
+                    reg[j] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+                    if (page >= 0) ld_codes(codes + (uint64_t)(uint32_t)page * page_bytes + at, reg[j]);
+                }
+            };
+            auto store = [&](uint32_t to) {
 #pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-                const uint32_t p = tk + 32 * kDeqWarps * j, token = p / kRowPieces, c = p % kRowPieces;
-                put(kt + (uint32_t)(c / 4) * L::kBlock, token, c % 4, kreg[j], (c / 4) & 1);
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= count) continue;
+                    uint32_t row, c;  // of 128 bytes, and its 32-byte piece
+                    if (keys) {
+                        row = t / 4 + 32 * j, c = t % 4;
+                    } else {
+                        const uint32_t q = t + 128 * j, rem = q & (page_bytes >> 4) - 1;
+                        row = rem >> ps - 4, c = q / D & ~((1u << ps - 4) - 1) | rem & (1u << ps - 4) - 1;
+                    }
+                    uint32_t f[8];
+                    codes_f16(reg[j].x, &f[0], &f[1]);
+                    codes_f16(reg[j].y, &f[2], &f[3]);
+                    codes_f16(reg[j].z, &f[4], &f[5]);
+                    codes_f16(reg[j].w, &f[6], &f[7]);
+                    const uint32_t chunk = to + swizzled(row, 2 * c);
+                    st_shared_v4(chunk, f[0], f[1], f[2], f[3]);
+                    st_shared_v4(chunk ^ 16, f[4], f[5], f[6], f[7]);
+                }
+            };
+            int slot = 0;
+            uint32_t par = 1;  // nothing to wait for in the ring's first round
+            load(pages_now, 0);
+            for (int i = 0; i < n; ++i) {
+                for (int blk = 0; blk < blocks; ++blk) {
+                    // (With the keys: the softmax needs both scales once the scores are there.)
+                    const bool scales = keys && blk == 0 && t < 8;
+                    float ks = 0.f, vs = 0.f;
+                    if (scales && pages_now >= 0) ks = __ldg(C.k_scales + pages_now), vs = __ldg(C.v_scales + pages_now);
+                    if (!__all_sync(0xffffffffu, wait(empty[slot], par))) return;
+                    if (scales) {
+                        // Far below fp16's range a weight is 0 in the product; in l it counts.
+                        const float ratio = fmaxf(vs / v_ref, kLeastRatio);
+                        const int at = i % kScaleSlots;
+                        S.k_scale[at][t] = ks, S.v_log[at][t] = lg2(ratio), S.v_inv[at][t] = 1.f / ratio;
+                    }
+                    store(ring + (uint32_t)slot * block);
+                    fence_async_shared();
+                    mbar_arrive(bar(full[slot]));
+                    if (++slot == depth) slot = 0, par ^= 1u;
+                    if (blk + 1 < blocks) {
+                        load(pages_now, blk + 1);
+                    } else {
+                        load(pages_next, 0);
+                        pages_now = pages_next, pages_next = fetch_pages(i + 2);
+                    }
+                }
             }
-            fence_async_shared();
-            mbar_arrive(bar(S.k_full[kst]));
-            load(C.k_codes, ids, kreg);
-            if (i >= VS && !__all_sync(0xffffffffu, wait(S.v_empty[vst], (uint32_t)(i / VS - 1) & 1u))) break;
-            const uint32_t vt = base + L::v + (uint32_t)vst * (2 * D * 128);
-            uint32_t tv = t;
-            fresh(tv);
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-                // (The divisors are powers of two that depend on the page size.)
-                const uint32_t p = tv + 32 * kDeqWarps * j, pg = p >> page_shift, rem = p & page_pieces - 1;
-                const uint32_t d = rem >> ps - 4, key = (pg << ps) + (rem & slot_pieces - 1) * 16;
-                put(vt + (uint32_t)(key / 64) * (D * 128), d, (key % 64) / 16, vreg[j], 0);
-            }
-            fence_async_shared();
-            mbar_arrive(bar(S.v_full[vst]));
-            load(C.v_codes, ids, vreg);
-        }
+        });
     } else {
         // ------------------------------------------------------------ MMA issue
         fewer_registers<kIssueRegs>();
-        if (warp == kSoftWarps + kDeqWarps && n > 0) {
+        if (warp == kIssueWarp && n > 0) {
             const uint32_t leader = elect_one();
             const uint32_t idesc_s = f16_idesc(kQ, kKeys), idesc_o = f16_idesc(kQ, D);
             // Low words of the descriptors; 32 bytes along a swizzled row are 2 in their address
@@ -549,59 +555,72 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             const uint64_t desc0 = sw128_desc(base);
             const uint32_t high = (uint32_t)(desc0 >> 32), low0 = (uint32_t)desc0;
             auto desc = [&](uint32_t low_word) { return (uint64_t)high << 32 | low_word; };
-            auto scores = [&](int tile, int st) {
-                uint32_t k_low = low0 + ((L::k + (uint32_t)(st * L::kBlocks) * L::kBlock) >> 4);
-                uint32_t q_low = low0 + ((L::q + (uint32_t)(tile * QT * L::kBlocks) * L::kBlock) >> 4);
-                const uint32_t d = tmem + kScoreCol + tile * kKeys;
-#pragma unroll 1
-                for (int term = 0; term < QT; ++term, q_low += L::kBlocks * L::kBlock >> 4)
+            bool ok = true;
+            int k_slot = 0, v_slot = 0;  // of the first block of this step's tile
+            uint32_t k_par = 0, v_par = 0;
+            // One tile's products of a step.  The step's first tile waits for the blocks, its last
+            // one releases them and moves on in the ring.
+            auto scores = [&](int tile, bool first, bool last) {
+                int slot = k_slot;
+                uint32_t par = k_par;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t at = (uint32_t)(kk / 4) * (L::kBlock >> 4) + 2 * (kk % 4);
-                        mma_f16_ss(leader, d, desc(q_low + at), desc(k_low + at), idesc_s, term + kk > 0);
+                for (int kb = 0; kb < L::kBlocks; ++kb) {
+                    if (first) {
+                        ok = ok && __all_sync(0xffffffffu, wait(S.k_full[slot], par));
+                        if (!ok) return;
+                        tc_fence_after();
                     }
+                    const uint32_t k_low = low0 + ((L::k + (uint32_t)slot * L::kBlock) >> 4);
+#pragma unroll
+                    for (int term = 0; term < QT; ++term) {
+                        const uint32_t q_low =
+                            low0 + ((L::q + (uint32_t)((tile * QT + term) * L::kBlocks + kb) * L::kBlock) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_ss(leader, tmem + kScoreCol + tile * kKeys, desc(q_low + 2 * kk),
+                                       desc(k_low + 2 * kk), idesc_s, kb + term + kk > 0);
+                    }
+                    if (last) mma_commit(leader, bar(S.k_empty[slot]));
+                    if (++slot == L::kRing) slot = 0, par ^= 1u;
+                }
+                if (last) k_slot = slot, k_par = par;
                 mma_commit(leader, bar(S.s_full[tile]));
             };
-            auto outputs = [&](int tile, int st, int i) {
-                uint32_t v_low = low0 + ((L::v + (uint32_t)st * (2 * D * 128)) >> 4);
-                uint32_t p_at = tmem + kScoreCol + tile * kKeys;
-#pragma unroll 1
-                for (int term = 0; term < PT; ++term, p_at += 64)
+            auto outputs = [&](int tile, int i, bool first, bool last) {
+                int slot = v_slot;
+                uint32_t par = v_par;
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_f16_ts(leader, tmem + tile * 128, p_at + 8 * kk,
-                                   desc(v_low + (uint32_t)(kk / 4) * (D * 128 >> 4) + 2 * (kk % 4)), idesc_o,
-                                   i > 0 || term + kk > 0);
+                for (int half = 0; half < 2; ++half) {
+                    if (first) {
+                        ok = ok && __all_sync(0xffffffffu, wait(S.v_full[slot], par));
+                        if (!ok) return;
+                    }
+                    if (half == 0) {
+                        ok = ok && __all_sync(0xffffffffu, wait(S.p_full[tile], i & 1));
+                        if (!ok) return;
+                    }
+                    tc_fence_after();
+                    const uint32_t v_low = low0 + ((L::v + (uint32_t)slot * L::vBlock) >> 4);
+#pragma unroll
+                    for (int term = 0; term < PT; ++term)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_ts(leader, tmem + tile * 128,
+                                       tmem + kScoreCol + tile * kKeys + term * 64 + (half * 4 + kk) * 8,
+                                       desc(v_low + 2 * kk), idesc_o, i > 0 || half + term + kk > 0);
+                    if (last) mma_commit(leader, bar(S.v_empty[slot]));
+                    if (++slot == L::vRing) slot = 0, par ^= 1u;
+                }
+                if (last) v_slot = slot, v_par = par;
             };
-            bool ok = __all_sync(0xffffffffu, wait(S.k_full[0], 0));
-            if (ok) {
-                tc_fence_after();
-                scores(0, 0);
-                if (two) scores(1, 0);
-                mma_commit(leader, bar(S.k_empty[0]));
-            }
+            scores(0, true, !two);
+            if (ok && two) scores(1, false, true);
             for (int i = 0; ok && i < n; ++i) {
-                const int st = i % VS, next = (i + 1) % KS;
-                const uint32_t par = (uint32_t)(i / VS) & 1u, npar = (uint32_t)((i + 1) / KS) & 1u;
                 const bool more = i + 1 < n;
-                if (!(ok = __all_sync(0xffffffffu, wait(S.v_full[st], par) && wait(S.p_full[0], i & 1)))) break;
-                tc_fence_after();
-                outputs(0, st, i);
-                if (more) {
-                    if (!(ok = __all_sync(0xffffffffu, wait(S.k_full[next], npar)))) break;
-                    tc_fence_after();
-                    scores(0, next);
-                }
-                if (two) {
-                    if (!(ok = __all_sync(0xffffffffu, wait(S.p_full[1], i & 1)))) break;
-                    tc_fence_after();
-                    outputs(1, st, i);
-                }
-                mma_commit(leader, bar(S.v_empty[st]));
-                if (more) {
-                    if (two) scores(1, next);
-                    mma_commit(leader, bar(S.k_empty[next]));
-                }
+                outputs(0, i, true, !two);
+                if (ok && more) scores(0, true, !two);
+                if (ok && two) outputs(1, i, false, true);
+                if (ok && two && more) scores(1, false, true);
             }
             // Everything issued has completed when these arrive; tensor memory is freed after.
             mma_commit(leader, bar(S.o_full[0]));
@@ -612,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == kSoftWarps + kDeqWarps) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kIssueWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int D, int QT, int PT>

@@ -63,7 +63,7 @@ q4lin_status_t check_cache(const q4lin_kv_cache_t* c, CacheBytes* n) {
         overlaps(c->v_codes, n->codes, c->v_scales, n->scales))
         return Q4LIN_ERR_INVALID_ARG;
     // Grid and index limits of the kernels: positions and page numbers are 32 bits.
-    if (c->kv_heads > 65535 || c->num_pages > 0x7FFFFFFF || c->batch > 0x7FFFFFFF / 8 ||
+    if (c->kv_heads > 65535 || n->scales / 4 > 0x7FFFFFFF || c->batch > 0x7FFFFFFF / 8 ||
         c->pages_per_sequence > (0x7FFFFFFF - 64) / c->page_size)
         return Q4LIN_ERR_TOO_LARGE;
     return Q4LIN_OK;
