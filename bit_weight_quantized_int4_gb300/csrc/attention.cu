@@ -3,13 +3,15 @@
 //
 // Bound: the codes, 2 head_dim bytes per key and key/value head, read once for all query
 // rows of that head.  The keys of all sequences and heads form one list of 64-key tiles that
-// is cut evenly over the CTAs, whatever the sequences' lengths; a CTA's share of one head's
-// keys is a piece.  A CTA's warps take a piece's tiles in turn, each with its own ring of
-// bulk copies (a page's keys or values of one head are contiguous), its own running maximum
-// and sum and its own outputs; they are joined through shared memory at the end of the
-// piece.  A head that is cut joins its pieces through the handle's workspace: every CTA has
-// at most two unfinished pieces (its first and its last), the CTA that arrives last adds
-// them in order, so the result does not depend on the schedule.
+// is cut evenly over the CTAs, whatever the sequences' lengths; a CTA's share of one
+// sequence's keys, for `heads_per` of its key/value heads, is a piece.  The warps of a head
+// take its tiles in turn, each with its own ring of bulk copies (a page's keys or values of
+// one head are contiguous), its own running maximum and sum and its own outputs; they are
+// joined through shared memory at the end of the piece, while the next piece's first copies
+// and queries are on their way.  A head that is cut joins its pieces through the handle's
+// workspace: every CTA has at most two unfinished pieces (its first and its last), the CTA
+// that arrives last adds them in order, so the result does not depend on the schedule.
+// Short lists are not cut at all where the join would cost more than it saves.
 //
 // Products on the tensor cores (m16n8k16, fp16 operands, fp32 sums): codes - 128 are exact
 // in fp16; a query row and a row of probabilities take two of the MMA's 16 rows each, the
@@ -43,6 +45,7 @@ struct SplitArgs {
     int page_shift;
     int64_t rows_max;
     int q_vec;
+    int heads_per;  // key/value heads of a CTA at a time: 1, 2 or 4 (RT * heads_per <= 4)
     float* ws;
     int* tickets;
     int* status;
@@ -56,16 +59,30 @@ struct RowInfo {
     int64_t index;       // token * heads + head, or -1
 };
 
+// Largest heads_per * RT: what the queries' fragments leave of the shared memory.
+__host__ __device__ constexpr int max_group(int D) { return D == 256 ? 2 : 4; }
+
+// A CTA's share of one sequence's keys.
+struct Piece {
+    int b, len, tq, h0, row0, tile, n;  // n tiles from `tile`; first head, first row
+    int units, k0, seg_begin;           // list units of the whole, done before, where it begins
+    int after;                          // list position past the piece
+    int cut;
+    int64_t o0;
+};
+
 template <int D, int RT>
 struct Shared {
-    static constexpr int W = warps_of(D);
-    uint4 q[RT][D / 16][32];  // A fragments
-    RowInfo row[RT * kRows];
+    static constexpr int W = warps_of(D), kGroup = max_group(D);
+    uint4 q[kGroup][D / 16][32];  // A fragments, [head * RT + row tile]
+    RowInfo row[2][kGroup * kRows];  // of this piece and the next
     float m[W][RT * kRows], l[W][RT * kRows];
+    uint32_t merge[W];  // where a warp left its outputs
     uint64_t full[W][kSlots];
+    Piece piece[3];  // this one, the next, and the one after that in the making
     int prefix[kMaxBatch + 1];
-    int sums[W];
-    int limit_min, low_max;
+    int sums[3][W];
+    int limit_min[2][kGroup], low_max[2][kGroup];  // per head of a piece
     int failed, last;
 };
 
@@ -112,19 +129,22 @@ __device__ __forceinline__ void emit(const SplitArgs& g, int64_t index, int D, i
 
 template <int D, int RT>
 __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_split_kernel(const SplitArgs g) {
-    constexpr int W = warps_of(D), T = 32 * W, R = RT * kRows;
+    constexpr int W = warps_of(D), T = 32 * W, R = RT * kRows, kGroup = max_group(D);
     constexpr int kNt = D / 8;
     constexpr uint32_t kHalf = kTile * D;  // bytes of a tile's keys (values)
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared<D, RT> S;
     const uint32_t ring = (smem_u32(smem_raw) + 127u) & ~127u;
-    float* merge = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));  // [W][R][D]
+    uint8_t* ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
     const q4lin_kv_cache_t& C = g.cache;
     const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads), ps = g.page_shift;
     const int ppt = kTile >> ps;  // pages per tile
+    const int hp = g.heads_per, wph = W / hp;  // warps per head
+    const int my_head = warp / wph, my_turn = warp % wph;
 
-    // ---- the list of tiles: an inclusive scan over the sequences
+    // ---- the list: tiles of all sequences, row tiles and groups of heads, or their number
+    // alone where nothing is cut.  First the totals, then an inclusive scan.
     if (tid == 0) {
         S.prefix[0] = 0;
         S.failed = 0;
@@ -132,7 +152,35 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             for (int s = 0; s < kSlots; ++s) mbar_init(smem_u32(&S.full[w][s]), 1);
         mbar_init_fence();
     }
-    const int batch = (int)C.batch;
+    const int batch = (int)C.batch, groups = Hkv / hp;
+    int tiles_all = 0, segments = 0, longest = 0;
+    for (int b = tid; b < batch; b += T) {
+        bool bad;
+        const Sequence s = sequence_of<RT>(g, b, &bad);
+        tiles_all += s.tiles * s.row_tiles * groups, segments += s.row_tiles * groups;
+        if (s.row_tiles) longest = max(longest, s.tiles);
+        if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
+    }
+    tiles_all = __reduce_add_sync(0xffffffffu, tiles_all);
+    segments = __reduce_add_sync(0xffffffffu, segments);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) S.sums[0][warp] = tiles_all, S.sums[1][warp] = segments, S.sums[2][warp] = longest;
+    __syncthreads();
+    tiles_all = segments = longest = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        tiles_all += S.sums[0][w], segments += S.sums[1][w], longest = max(longest, S.sums[2][w]);
+    // Rounds of the warps over a CTA's tiles: cut evenly, a join costs about two; whole, each
+    // CTA takes some heads' tiles to their end.  (Measured: one token over 701 keys, 8 heads
+    // of 64: SHORT.)
+    const int grid = (int)gridDim.x;
+    const int cut_share = max(wph, (tiles_all + grid - 1) / grid);
+    const int whole_share = (segments + grid - 1) / grid;
+    const bool whole = whole_share * ((longest + wph - 1) / wph) <= (cut_share + wph - 1) / wph + 2;
+    const int share = whole ? whole_share : cut_share, total = whole ? segments : tiles_all;
+    const int64_t begin = (int64_t)blockIdx.x * share;
+    const int end = (int)min((int64_t)total, begin + share);
+    if (begin >= end) return;
     int carry = 0;
     for (int b0 = 0; b0 < batch; b0 += T) {
         const int b = b0 + tid;
@@ -140,8 +188,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
         if (b < batch) {
             bool bad;
             const Sequence s = sequence_of<RT>(g, b, &bad);
-            v = s.tiles * s.row_tiles * Hkv;
-            if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
+            v = (whole ? 1 : s.tiles) * s.row_tiles * groups;
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -149,27 +196,20 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             if (lane >= o) v += n;
         }
         __syncthreads();
-        if (lane == 31) S.sums[warp] = v;
+        if (lane == 31) S.sums[0][warp] = v;
         __syncthreads();
         int before = carry;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            if (w < warp) before += S.sums[w];
-            carry += S.sums[w];
+            if (w < warp) before += S.sums[0][w];
+            carry += S.sums[0][w];
         }
         if (b < batch) S.prefix[b + 1] = before + v;
     }
     __syncthreads();
-    const int total = carry;
-    // Shares of at least a tile per warp.
-    const int share = max(W, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-    const int64_t begin = (int64_t)blockIdx.x * share;
-    const int end = (int)min((int64_t)total, begin + share);
-    if (begin >= end) return;
-    uint32_t phase = 0;  // parity bit of each slot's next wait
 
-    for (int pos = (int)begin; pos < end;) {
-        // ---- the piece: tiles [k0, k0 + n) of row tile rt of head h of sequence b
+    // ---- pieces
+    auto make_piece = [&](int pos, Piece& p) {  // one thread
         int lo = 0, hi = batch;  // prefix[lo] <= pos < prefix[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -178,128 +218,180 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             else
                 hi = mid;
         }
-        const int b = lo;
         bool bad;
-        const Sequence s = sequence_of<RT>(g, b, &bad);
-        const int local = pos - S.prefix[b], seg = local / s.tiles;
-        const int k0 = local - seg * s.tiles, h = seg / s.row_tiles, rt0 = seg - h * s.row_tiles;
-        const int n = min(s.tiles - k0, end - pos);
-        const int seg_begin = pos - k0;  // first tile of the whole head in the list
-        pos += n;
-        const int64_t o0 = __ldg(g.a.offsets + b);
+        const Sequence s = sequence_of<RT>(g, lo, &bad);
+        p.b = lo, p.len = s.len, p.tq = s.tq;
+        p.units = whole ? 1 : s.tiles;
+        const int local = pos - S.prefix[lo], seg = local / p.units;
+        p.k0 = local - seg * p.units;
+        p.h0 = seg / s.row_tiles * hp, p.row0 = seg % s.row_tiles * R;
+        p.seg_begin = pos - p.k0;
+        const int units = min(p.units - p.k0, end - pos);
+        p.cut = units < p.units;
+        p.tile = s.tile0 + p.k0, p.n = whole ? s.tiles : units;
+        p.after = pos + units;
+        p.o0 = __ldg(g.a.offsets + lo);
+    };
 
-        // ---- queries: rotated, scaled to fp16's upper range by a power of two, split
-        if (tid == 0) S.limit_min = INT_MAX, S.low_max = 0;
-        __syncthreads();
-        constexpr int kUnitsRow = D / 8;               // lanes per row (8 channels each)
-        constexpr int kPer = T / kUnitsRow;            // rows in flight
-        for (int r0 = 0; r0 < R; r0 += kPer) {
-            const int r = r0 + tid / kUnitsRow, u = tid % kUnitsRow;
-            const int row = rt0 * R + r;
-            const bool in = r < R && row < s.tq * group;
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            const int token = in ? row / group : 0, head = h * group + (in ? row - token * group : 0);
-            const int position = s.len - s.tq + token;
-            bool turned;
-            int cl, ch;
-            rope_channels(g.a.rope, u, &turned, &cl, &ch);
-            if (in) {
-                const int64_t e = (o0 + token) * g.a.q_token_stride + head * g.a.q_head_stride;
-                load_four(g.a.query, g.a.dtype, e + cl, g.q_vec, x);
-                load_four(g.a.query, g.a.dtype, e + ch, g.q_vec, x + 4);
-                if (turned && position >= 0) rope_unit(g.a.rope, position, u, x);
-            }
-            float m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
-#pragma unroll
-            for (int o = kUnitsRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            // 2^up brings the row's largest |x| to [2^14, 2^15); its exponent is kept within
-            // what both 2^up and 2^-up can hold.
-            const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
-            const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-            const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-            if (r < R) {
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int d = w ? ch : cl;  // channels d .. d + 3
-                    uint4 f;
-                    split_f16(x[4 * w] * up, x[4 * w + 1] * up, &f.x, &f.y);
-                    split_f16(x[4 * w + 2] * up, x[4 * w + 3] * up, &f.z, &f.w);
-                    S.q[r / kRows][(d / 64) * 4 + (d % 16) / 4][(r % kRows) * 4 + (d % 64) / 16] = f;
-                }
-                if (u == 0) {
-                    RowInfo i;
-                    i.factor = g.a.scale * kLog2e * down;
-                    i.limit = in && position >= 0 ? (g.a.causal ? position : s.len - 1) : -1;
-                    if (in && !g.a.causal) i.limit = s.len - 1;
-                    const int64_t low = g.a.window > 0 ? (int64_t)position - g.a.window + 1 : 0;
-                    i.low = low > 0 ? (int)low : 0;
-                    i.index = in ? (o0 + token) * g.a.heads + head : -1;
-                    S.row[r] = i;
-                    if (in) {
-                        atomicMin(&S.limit_min, i.limit);
-                        atomicMax(&S.low_max, i.low);
-                    }
-                }
+    // This warp's tiles of a piece: `first`, `first` + wph, ...; with the pages of the next
+    // 32 / ppt of them in the lanes: lane i holds page i % ppt of tile i / ppt.
+    const uint32_t page_bytes = (uint32_t)(D << ps);
+    const int batch_tiles = 32 / ppt;
+    const int32_t* table = nullptr;
+    int first = 0, cnt = 0, pages = 0, head = 0, ids = 0, issued = 0, slot_in = 0, in_flight = 0;
+    auto fetch_ids = [&](int i) {
+        const int tile = first + (i + lane / ppt) * wph, p = tile * ppt + lane % ppt;
+        ids = -1;
+        if (i + lane / ppt < cnt && p < pages) {
+            ids = __ldg(table + p);
+            if (ids < 0 || ids >= C.num_pages) {
+                atomicCAS(g.status, 0, kStatusIndex);
+                ids = 0;  // read something of the cache rather than nothing
             }
         }
-        __syncthreads();
+    };
+    auto enter = [&](const Piece& p) {
+        cnt = p.len > 0 && p.n > my_turn ? (p.n - my_turn + wph - 1) / wph : 0;
+        first = p.tile + my_turn;
+        table = C.page_table + p.b * C.table_stride;
+        pages = (p.len + (1 << ps) - 1) >> ps;
+        head = p.h0 + my_head;
+        issued = 0;
+        fetch_ids(0);
+    };
+    // Next half tile of the piece (keys of a tile, then its values) into the ring.
+    auto issue = [&]() {
+        if (issued >= 2 * cnt) return;
+        const int i = issued >> 1;
+        if ((issued & 1) == 0 && i > 0 && i % batch_tiles == 0) fetch_ids(i);
+        const int id = __shfl_sync(0xffffffffu, ids, (i % batch_tiles) * ppt + lane % ppt);
+        const bool mine = lane < ppt && id >= 0;
+        const int count = __popc(__ballot_sync(0xffffffffu, mine));
+        const uint32_t bar = smem_u32(&S.full[warp][slot_in]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * page_bytes);
+        __syncwarp();
+        if (mine) {
+            const uint8_t* codes = issued & 1 ? C.v_codes : C.k_codes;
+            bulk_load(ring + (uint32_t)(warp * kSlots + slot_in) * kHalf + lane * page_bytes,
+                      codes + ((int64_t)id * Hkv + head) * page_bytes, page_bytes, bar);
+        }
+        ++issued, ++in_flight;
+        slot_in = slot_in + 1 == kSlots ? 0 : slot_in + 1;
+    };
+    // The scales of this lane's 16 keys of tile i (one page each).
+    float sk_next = 0.f, sv_next = 0.f;
+    auto fetch_scales = [&](int i) {
+        const int p = (first + i * wph) * ppt + ((t * 16) >> ps);
+        sk_next = sv_next = 0.f;
+        if (i < cnt && p < pages) {
+            int id = __ldg(table + p);
+            if (id < 0 || id >= C.num_pages) id = 0;
+            sk_next = __ldg(C.k_scales + (int64_t)id * Hkv + head);
+            sv_next = __ldg(C.v_scales + (int64_t)id * Hkv + head);
+        }
+    };
 
-        // ---- this warp's tiles
-        const int cnt = s.len > 0 && n > warp ? (n - warp + W - 1) / W : 0;
-        const int first = s.tile0 + k0 + warp;  // its tiles: first, first + W, ...
-        const int32_t* table = C.page_table + b * C.table_stride;
-        const uint32_t page_bytes = (uint32_t)(D << ps);
-        const int pages = (s.len + (1 << ps) - 1) >> ps;
-        // Pages of the next 32 / ppt tiles: lane i holds page (i % ppt) of tile i / ppt.
-        int ids = 0;
-        auto fetch_ids = [&](int i) {
-            const int tile = first + (i + lane / ppt) * W, p = tile * ppt + lane % ppt;
-            ids = -1;
-            if (i + lane / ppt < cnt && p < pages) {
-                ids = __ldg(table + p);
-                if (ids < 0 || ids >= C.num_pages) {
-                    atomicCAS(g.status, 0, kStatusIndex);
-                    ids = 0;  // read something of the cache rather than nothing
-                }
+    // Queries of a piece: thread (row, unit of 8 channels), kPasses rows one after another.
+    constexpr int kUnitsRow = D / 8, kPer = T / kUnitsRow;
+    constexpr int kPasses = kGroup * kRows / kPer;  // of the most rows
+    const int q_unit = tid % kUnitsRow;
+    auto query_row = [&](const Piece& p, int r, int* token, int* h) {  // r: row of the piece
+        const int row = p.row0 + r % R;
+        const bool in = r < hp * R && row < p.tq * group;
+        *token = in ? row / group : 0;
+        *h = (p.h0 + r / R) * group + (in ? row - *token * group : 0);
+        return in;
+    };
+    bool turned;
+    int cl, ch;
+    rope_channels(g.a.rope, q_unit, &turned, &cl, &ch);
+    auto load_query = [&](const Piece& p, int pass, float (&x)[8]) {
+        int token, h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        if (query_row(p, pass * kPer + tid / kUnitsRow, &token, &h)) {
+            const int64_t e = (p.o0 + token) * g.a.q_token_stride + h * g.a.q_head_stride;
+            load_four(g.a.query, g.a.dtype, e + cl, g.q_vec, x);
+            load_four(g.a.query, g.a.dtype, e + ch, g.q_vec, x + 4);
+        }
+    };
+    // Rotated, scaled to fp16's upper range by a power of two, split into two terms.
+    auto put_query = [&](const Piece& p, int pass, float (&x)[8], int which) {
+        const int r = pass * kPer + tid / kUnitsRow;
+        int token, h;
+        const bool in = query_row(p, r, &token, &h);
+        const int position = p.len - p.tq + token;
+        if (in && turned && position >= 0) rope_unit(g.a.rope, position, q_unit, x);
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+#pragma unroll
+        for (int o = kUnitsRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // 2^up brings the row's largest |x| to [2^14, 2^15); its exponent is kept within what
+        // both 2^up and 2^-up can hold.
+        const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
+        const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+        const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+        if (r >= hp * R) return;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const int d = w ? ch : cl;  // channels d .. d + 3
+            uint4 f;
+            split_f16(x[4 * w] * up, x[4 * w + 1] * up, &f.x, &f.y);
+            split_f16(x[4 * w + 2] * up, x[4 * w + 3] * up, &f.z, &f.w);
+            S.q[r / kRows][(d / 64) * 4 + (d % 16) / 4][(r % kRows) * 4 + (d % 64) / 16] = f;
+        }
+        if (q_unit == 0) {
+            RowInfo i;
+            i.factor = g.a.scale * kLog2e * down;
+            i.limit = !in ? -1 : g.a.causal ? position : p.len - 1;
+            const int64_t low = g.a.window > 0 ? (int64_t)position - g.a.window + 1 : 0;
+            i.low = low > 0 ? (int)low : 0;
+            i.index = in ? (p.o0 + token) * g.a.heads + h : -1;
+            S.row[which][r] = i;
+            if (in) {
+                atomicMin(&S.limit_min[which][r / R], i.limit);
+                atomicMax(&S.low_max[which][r / R], i.low);
             }
-        };
-        const int batch_tiles = 32 / ppt;
-        int issued = 0;
-        // Half tile u (keys of tile u / 2, then its values) into its slot of the ring.
-        auto issue = [&]() {
-            if (issued >= 2 * cnt) return;
-            const int i = issued >> 1, slot = issued % kSlots;
-            if ((issued & 1) == 0 && i % batch_tiles == 0) fetch_ids(i);
-            const int id = __shfl_sync(0xffffffffu, ids, (i % batch_tiles) * ppt + lane % ppt);
-            const bool mine = lane < ppt && id >= 0;
-            const int count = __popc(__ballot_sync(0xffffffffu, mine));
-            const uint32_t bar = smem_u32(&S.full[warp][slot]);
-            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * page_bytes);
-            __syncwarp();
-            if (mine) {
-                const uint8_t* base = issued & 1 ? C.v_codes : C.k_codes;
-                bulk_load(ring + (uint32_t)(warp * kSlots + slot) * kHalf + lane * page_bytes,
-                          base + ((int64_t)id * Hkv + h) * page_bytes, page_bytes, bar);
-            }
-            ++issued;
-        };
-        // The scales of this lane's 16 keys of tile i (one page each).
-        float sk_next = 0.f, sv_next = 0.f;
-        auto fetch_scales = [&](int i) {
-            const int p = (first + i * W) * ppt + ((t * 16) >> ps);
-            sk_next = sv_next = 0.f;
-            if (i < cnt && p < pages) {
-                int id = __ldg(table + p);
-                if (id < 0 || id >= C.num_pages) id = 0;
-                sk_next = __ldg(C.k_scales + (int64_t)id * Hkv + h);
-                sv_next = __ldg(C.v_scales + (int64_t)id * Hkv + h);
-            }
-        };
+        }
+    };
+    auto clear_limits = [&](int which) {
+        if (tid < hp) S.limit_min[which][tid] = INT_MAX, S.low_max[which][tid] = 0;
+    };
 
+    uint32_t phase = 0;  // parity bit of each slot's next wait
+    int slot_out = 0, which = 0;
+    bool ok = true;
+    auto await = [&]() {  // the oldest half tile in flight; its place in the ring
+        const uint32_t bar = smem_u32(&S.full[warp][slot_out]);
+        ok = __all_sync(0xffffffffu, wait_bounded(bar, (phase >> slot_out) & 1u, g.wait_ns, &S.failed));
+        const uint32_t at = ring + (uint32_t)(warp * kSlots + slot_out) * kHalf;
+        if (ok) {
+            phase ^= 1u << slot_out, --in_flight;
+            slot_out = slot_out + 1 == kSlots ? 0 : slot_out + 1;
+        }
+        return at;
+    };
+
+    if (tid == 0) {
+        make_piece((int)begin, S.piece[0]);
+        if (S.piece[0].after < end) make_piece(S.piece[0].after, S.piece[1]);
+    }
+    clear_limits(0);
+    __syncthreads();
+    enter(S.piece[0]);
+    issue();
+    issue();
+    fetch_scales(0);
+    for (int pass = 0; pass < kPasses; ++pass) {
+        float x[8];
+        load_query(S.piece[0], pass, x);
+        put_query(S.piece[0], pass, x, 0);
+    }
+    __syncthreads();
+
+    for (int turn = 0;; turn = turn == 2 ? 0 : turn + 1) {
+        issue();
         float O[RT][kNt][2], m_run[RT], l_run[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -307,29 +399,17 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
 #pragma unroll
             for (int i = 0; i < kNt; ++i) O[rt][i][0] = O[rt][i][1] = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) issue();
-        fetch_scales(0);
-        int waited = 0;
-        bool ok = true;
-        auto await = [&]() {
-            const int slot = waited % kSlots;
-            const uint32_t bar = smem_u32(&S.full[warp][slot]);
-            const bool done = wait_bounded(bar, (phase >> slot) & 1u, g.wait_ns, &S.failed);
-            ok = __all_sync(0xffffffffu, done);
-            if (ok) phase ^= 1u << slot, ++waited;
-        };
-        const RowInfo* rows = S.row;
-        const int limit_min = S.limit_min, low_max = S.low_max;
+        const RowInfo* rows = S.row[which] + my_head * R;
+        const int limit_min = S.limit_min[which][my_head], low_max = S.low_max[which][my_head];
 
         for (int i = 0; i < cnt; ++i) {
             const float sk = sk_next, sv = sv_next;
             fetch_scales(i + 1);
-            const int key0 = (first + i * W) * kTile + t * 16;  // first of this lane's 16 keys
+            const int tile_key = (first + i * wph) * kTile;
+            const int key0 = tile_key + t * 16;  // first of this lane's 16 keys
             // ---- scores: 8 column tiles of 8 keys; key of column c of tile j:
             // (c / 2) 16 + 2 j + c % 2, so that this lane's are key0 .. key0 + 15
-            uint32_t slot_at = ring + (uint32_t)(warp * kSlots + waited % kSlots) * kHalf;
-            await();
+            const uint32_t k_at = await();
             if (!ok) break;
             float sc[RT][8][4];
 #pragma unroll
@@ -344,11 +424,11 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) qf[rt][k] = S.q[rt][4 * c + k][lane];
+                    for (int k = 0; k < 4; ++k) qf[rt][k] = S.q[my_head * RT + rt][4 * c + k][lane];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int key = (gq >> 1) * 16 + 2 * j + (gq & 1);
-                    const uint4 w = ld_shared_v4(slot_at + (uint32_t)(key * D + c * 64 + t * 16));
+                    const uint4 w = ld_shared_v4(k_at + (uint32_t)(key * D + c * 64 + t * 16));
                     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -369,7 +449,6 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
                 sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, 2));
             }
             const float ratio = ppt > 1 ? (sv_max > 0.f ? __fdividef(sv, sv_max) : 0.f) : 1.f;
-            const int tile_key = (first + i * W) * kTile;
             const bool inside = tile_key >= low_max && tile_key + kTile - 1 <= limit_min;
             uint4 pf[RT][4];
             float alpha[RT];
@@ -417,10 +496,9 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             }
 
             // ---- outputs: channel tile nt of 8, the tile's 64 keys in 4 steps
-            slot_at = ring + (uint32_t)(warp * kSlots + waited % kSlots) * kHalf;
-            await();
+            const uint32_t v_at = await() + (uint32_t)((((t * 16) >> ps) * (D << ps)) +
+                                                       ((t * 16) & ((1 << ps) - 1)) + (gq << ps));
             if (!ok) break;
-            const uint32_t v_at = slot_at + (uint32_t)((((t * 16) >> ps) * (D << ps)) + ((t * 16) & ((1 << ps) - 1)) + (gq << ps));
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt) {
                 const uint4 w = ld_shared_v4(v_at + (uint32_t)((nt * 8) << ps));
@@ -446,17 +524,38 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             __syncwarp();
             issue();
         }
-        if (!ok && lane == 0) record_failure(g.status, &S.failed);
-        // Copies still in flight (only after a failed wait) must land before the CTA leaves.
-        for (; waited < issued; ++waited) {
-            const int slot = waited % kSlots;
-            wait_bounded(smem_u32(&S.full[warp][slot]), (phase >> slot) & 1u, kDrainNs, nullptr);
-            phase ^= 1u << slot;
+        if (!ok) {
+            // A wait ran out: copies still in flight must land before the CTA leaves, and it
+            // goes on without any (the tickets have to come out even; outputs are undefined).
+            if (lane == 0) record_failure(g.status, &S.failed);
+            for (; in_flight > 0; --in_flight) {
+                wait_bounded(smem_u32(&S.full[warp][slot_out]), (phase >> slot_out) & 1u, kDrainNs, nullptr);
+                phase ^= 1u << slot_out;
+                slot_out = slot_out + 1 == kSlots ? 0 : slot_out + 1;
+            }
         }
 
-        // ---- join the warps: the ring holds nothing any more.  (After a failed wait, too: the
-        // tickets have to come out even; the outputs are undefined then.)
-        __syncthreads();
+        const Piece& P = S.piece[turn];
+        const int next = turn == 2 ? 0 : turn + 1;
+        const Piece& N = S.piece[next];
+        const bool more = P.after < end;
+        // ---- the next piece's first copies take two of the ring's three slots, this one's
+        // outputs the third
+        const uint32_t keep = (uint32_t)(warp * kSlots + (slot_in + 2) % kSlots) * kHalf;
+        if (more) {
+            enter(N);
+            if (!ok) cnt = 0;
+            issue();
+            issue();
+            fetch_scales(0);
+        }
+        float x[kPasses][8];
+        if (more) {
+#pragma unroll
+            for (int pass = 0; pass < kPasses; ++pass) load_query(N, pass, x[pass]);
+            clear_limits(which ^ 1);
+        }
+        if (lane == 0) S.merge[warp] = keep;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float l = l_run[rt];
@@ -464,43 +563,45 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             l += __shfl_xor_sync(0xffffffffu, l, 2);
             const int r = rt * kRows + gq;
             if (t == 0) S.m[warp][r] = m_run[rt], S.l[warp][r] = l;
+            float* o = reinterpret_cast<float*>(ring_ptr + keep) + r * D + 2 * t;
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt)
-                *reinterpret_cast<float2*>(merge + ((size_t)warp * R + r) * D + nt * 8 + 2 * t) =
-                    make_float2(O[rt][nt][0], O[rt][nt][1]);
+                *reinterpret_cast<float2*>(o + nt * 8) = make_float2(O[rt][nt][0], O[rt][nt][1]);
         }
         __syncthreads();
-        const bool whole = n == s.tiles;
-        // Partial pieces: slot 0 for the CTA's first (begun by an earlier CTA), 1 for its last.
-        constexpr int kPart = R * (D + 2);
-        float* part = g.ws + ((int64_t)blockIdx.x * 2 + (k0 == 0)) * kPart;
-        constexpr int kQuads = R * D / 4;
-        for (int i = tid; i < kQuads; i += T) {
-            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+
+        // ---- join a head's warps.  Partial pieces: slot 0 for the CTA's first (begun by an
+        // earlier CTA), 1 for its last.
+        constexpr int kPart = R * (D + 2), kQuads = R * D / 4;
+        auto part_at = [&](int cta, int place, int hi) {
+            return g.ws + ((int64_t)(cta * 2 + place) * hp + hi) * kPart;
+        };
+        for (int i = tid - my_head * wph * 32; i < kQuads; i += wph * 32) {
+            const int r = i / (D / 4), d = (i % (D / 4)) * 4, w0 = my_head * wph;
             float mx = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < W; ++w) mx = fmaxf(mx, S.m[w][r]);
+            for (int w = w0; w < w0 + wph; ++w) mx = fmaxf(mx, S.m[w][r]);
             const float base = mx == -INFINITY ? 0.f : mx;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             float l = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
+#pragma unroll 2
+            for (int w = w0; w < w0 + wph; ++w) {
                 const float c = ex2(S.m[w][r] - base);
-                const float4 v = *reinterpret_cast<const float4*>(merge + ((size_t)w * R + r) * D + d);
+                const float4 v = *reinterpret_cast<const float4*>(ring_ptr + S.merge[w] + (r * D + d) * 4);
                 o.x = fmaf(v.x, c, o.x), o.y = fmaf(v.y, c, o.y);
                 o.z = fmaf(v.z, c, o.z), o.w = fmaf(v.w, c, o.w);
                 l = fmaf(S.l[w][r], c, l);
             }
-            if (!whole) {
+            if (P.cut) {
+                float* part = part_at(blockIdx.x, P.k0 == 0, my_head);
                 *reinterpret_cast<float4*>(part + r * D + d) = o;
                 if (d == 0) part[R * D + r] = mx, part[R * D + R + r] = l;
-                continue;
+            } else {
+                emit(g, S.row[which][my_head * R + r].index, D, d, o, l, base);
             }
-            emit(g, S.row[r].index, D, d, o, l, base);
         }
-        if (!whole) {
-            // The CTAs that share this head's keys: c0 .. c1.
-            const int c0 = seg_begin / share, c1 = (seg_begin + s.tiles - 1) / share;
+        if (P.cut) {
+            // The CTAs that share these heads' keys: c0 .. c1.
+            const int c0 = P.seg_begin / share, c1 = (P.seg_begin + P.units - 1) / share;
             __syncthreads();
             if (tid == 0) {
                 __threadfence();
@@ -510,19 +611,18 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             }
             __syncthreads();
             if (S.last) {
-                for (int i = tid; i < kQuads; i += T) {
-                    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-                    const int64_t index = S.row[r].index;
+                for (int i = tid; i < hp * kQuads; i += T) {
+                    const int hi = i / kQuads, r = i % kQuads / (D / 4), d = (i % (D / 4)) * 4;
+                    const int64_t index = S.row[which][hi * R + r].index;
                     if (index < 0) continue;
                     float mx = -INFINITY;
-                    for (int c = c0; c <= c1; ++c)
-                        mx = fmaxf(mx, __ldcg(g.ws + ((int64_t)c * 2 + (c == c0)) * kPart + R * D + r));
+                    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(part_at(c, c == c0, hi) + R * D + r));
                     const float base = mx == -INFINITY ? 0.f : mx;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                     float l = 0.f;
 #pragma unroll 4
                     for (int c = c0; c <= c1; ++c) {
-                        const float* src = g.ws + ((int64_t)c * 2 + (c == c0)) * kPart;
+                        const float* src = part_at(c, c == c0, hi);
                         const float4 v = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
                         const float k = ex2(__ldcg(src + R * D + r) - base);
                         o.x = fmaf(v.x, k, o.x), o.y = fmaf(v.y, k, o.y);
@@ -533,7 +633,12 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
                 }
             }
         }
-        // The next piece's copies write where the joined outputs were.
+        if (!more) break;
+        which ^= 1;
+        if (tid == 0 && N.after < end) make_piece(N.after, S.piece[next == 2 ? 0 : next + 1]);
+#pragma unroll
+        for (int pass = 0; pass < kPasses; ++pass) put_query(N, pass, x[pass], which);
+        // The next copies also write where the joined outputs were.
         fence_async_shared();
         __syncthreads();
     }
@@ -575,13 +680,20 @@ cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_at
         g.tickets = c.tickets;
         g.status = c.status_word;
         g.wait_ns = c.wait_limit_ns;
-        // No more CTAs than tiles of the longest possible list; one or two per SM.
+        // One or two CTAs per SM, and no more than the longest possible list has tiles for.
+        const int64_t slots = (int64_t)c.sm_count * ctas_of(D, two ? 2 : 1);
         const int64_t tiles = (cache.pages_per_sequence * cache.page_size + kTile - 1) / kTile;
         const int64_t row_tiles = std::min((a.tokens * group + R - 1) / R + g.cache.batch,
                                            ((rows + R - 1) / R) * g.cache.batch);
         const int64_t grid = std::max<int64_t>(
-            1, std::min<int64_t>((int64_t)c.sm_count * ctas_of(D, two ? 2 : 1),
-                                 (tiles * row_tiles * cache.kv_heads + warps_of(D) - 1) / warps_of(D)));
+            1, std::min<int64_t>(slots, (tiles * row_tiles * cache.kv_heads + warps_of(D) - 1) / warps_of(D)));
+        // More heads at a time leave fewer joins of warps and fewer of them idle at the end of
+        // a piece, as long as every CTA finds a piece of its own.
+        g.heads_per = 1;
+        for (int hp = 2; hp * (two ? 2 : 1) <= max_group(D) && cache.kv_heads % hp == 0 &&
+                         row_tiles * cache.kv_heads / hp >= slots;
+             hp *= 2)
+            g.heads_per = hp;
         switch (D) {
             case 64: err = two ? launch<64, 2>(g, grid, c.stream) : launch<64, 1>(g, grid, c.stream); break;
             case 128: err = two ? launch<128, 2>(g, grid, c.stream) : launch<128, 1>(g, grid, c.stream); break;

@@ -361,50 +361,71 @@ def plan_kernel(handle: Handle, x, qweight, scales, bias, group_size: int, out) 
 
 
 # ------------------------------------------------- operators around the linears (torch)
+# A decode step makes hundreds of these calls, some shorter on the GPU than their checks
+# here: types are compared as objects, and torch is looked up once.
+class _Torch:
+    """torch, its types' codes and its current stream's handle, filled at the first use."""
+    module = None
+    codes: dict = {}
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.float32, cls.int32, cls.empty = torch.float32, torch.int32, torch.empty
+        cls.codes = {torch.float32: Q4LIN_DTYPE_F32, torch.float16: Q4LIN_DTYPE_F16,
+                     torch.bfloat16: Q4LIN_DTYPE_BF16}
+        # The raw handle without a Stream object around it, where torch has that.
+        cls.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        cls.module = torch
+
+
 def _dtype_code(t, what):
-    code = {"torch.float32": Q4LIN_DTYPE_F32, "torch.float16": Q4LIN_DTYPE_F16,
-            "torch.bfloat16": Q4LIN_DTYPE_BF16}.get(str(t.dtype))
+    code = _Torch.codes.get(t.dtype)
     if code is None:
         raise ValueError(f"{what} must be float32, float16 or bfloat16")
     return code
 
 
 def _check_device(handle, *tensors):
+    if _Torch.module is None:
+        _Torch.load()
+    device = handle.device
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != handle.device):
-            raise ValueError(f"every tensor must be on the handle's device, cuda:{handle.device}")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"every tensor must be on the handle's device, cuda:{device}")
 
 
-def _check_vector(t, n, kind, what):
-    """A contiguous one-dimensional tensor of n int32 ("int32") or float32 values."""
-    if str(t.dtype) != "torch." + kind or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {kind} [{n}] tensor")
+def _check_vector(t, n, dtype, what):
+    """A contiguous one-dimensional tensor of n values."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} [{n}] tensor")
     return t.data_ptr()
 
 
-def _check_heads(t, what):
-    """[tokens, heads, head_dim] with contiguous channels."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+def _head_strides(t, what):
+    """Token and head strides of [tokens, heads, head_dim] with contiguous channels."""
+    strides = t.stride()
+    if len(strides) != 3 or strides[2] != 1:
         raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous channels")
+    return strides
 
 
-def _stream_of(stream, t) -> int:
+def _stream_of(stream, handle) -> int:
     if stream is not None:
         return stream
-    import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return _Torch.stream(handle.device)
 
 
 def _rope_args(rope, interleaved):
     if rope is None:
         return q4lin_rope_t()
     cos, sin = rope
-    for t in rope:
-        if str(t.dtype) != "torch.float32" or t.dim() != 2 or not t.is_contiguous() \
-                or t.shape != cos.shape:
-            raise ValueError("rope must be two contiguous float32 [positions, rotated / 2] tensors")
-    return q4lin_rope_t(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1],
-                        int(interleaved))
+    shape = cos.shape
+    if cos.dtype is not _Torch.float32 or sin.dtype is not _Torch.float32 or len(shape) != 2 \
+            or sin.shape != shape or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("rope must be two contiguous float32 [positions, rotated / 2] tensors")
+    return q4lin_rope_t(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], interleaved)
 
 
 class KVCache:
@@ -455,18 +476,18 @@ def kv_append(handle: Handle, cache: KVCache, k, v, offsets, starts, rope=None,
     each and possibly slices of a larger tensor, to the cache: rows offsets[b] ..
     offsets[b + 1] become tokens starts[b], starts[b] + 1, ... of sequence b."""
     c = cache.args
-    _check_device(handle, cache.k_codes, k, v, offsets, starts, *(rope or ()))
-    _check_heads(k, "k")
-    if k.shape != v.shape or k.shape[1] != c.kv_heads or k.shape[2] != c.head_dim or \
-            v.dtype != k.dtype:
+    cos, sin = rope or (None, None)
+    _check_device(handle, cache.k_codes, k, v, offsets, starts, cos, sin)
+    ks, vs, shape = _head_strides(k, "k"), _head_strides(v, "v"), k.shape
+    if v.shape != shape or shape[1] != c.kv_heads or shape[2] != c.head_dim or v.dtype is not k.dtype:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one type, as the cache")
-    _check_heads(v, "v")
-    args = q4lin_kv_append_t(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0),
-                             v.stride(1), _dtype_code(k, "k"), k.shape[0],
-                             _check_vector(offsets, c.batch + 1, "int32", "offsets"),
-                             _check_vector(starts, c.batch, "int32", "starts"),
+    batch, int32 = c.batch, _Torch.int32
+    args = q4lin_kv_append_t(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
+                             _dtype_code(k, "k"), shape[0],
+                             _check_vector(offsets, batch + 1, int32, "offsets"),
+                             _check_vector(starts, batch, int32, "starts"),
                              _rope_args(rope, interleaved))
-    st = _lib.q4lin_run_kv_append(handle.ptr, c, args, _stream_of(stream, k))
+    st = _lib.q4lin_run_kv_append(handle.ptr, c, args, _stream_of(stream, handle))
     if st != Q4LIN_OK:
         raise Q4LinError(st, "q4lin_run_kv_append")
 
@@ -478,28 +499,29 @@ def attention(handle: Handle, cache: KVCache, query, offsets, lengths, scale: fl
     lengths[b] counts sequence b's tokens in the cache, those of its queries included;
     max_query: no sequence has more query tokens (default: all of them).  Returns (out, lse):
     out like query, lse float32 [tokens, heads]."""
-    import torch
     c = cache.args
-    _check_device(handle, cache.k_codes, query, offsets, lengths, out, lse, *(rope or ()))
-    _check_heads(query, "query")
-    tokens, heads, dim = query.shape
+    cos, sin = rope or (None, None)
+    _check_device(handle, cache.k_codes, query, offsets, lengths, out, lse, cos, sin)
+    strides, shape = _head_strides(query, "query"), query.shape
+    tokens, heads, dim = shape
     if dim != c.head_dim or heads % c.kv_heads:
         raise ValueError("query must be [tokens, heads, head_dim], heads a multiple of kv_heads")
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=query.dtype, device=query.device)
-    elif out.shape != query.shape or out.dtype != query.dtype or not out.is_contiguous():
+        out = _Torch.empty(shape, dtype=query.dtype, device=query.device)
+    elif out.shape != shape or out.dtype is not query.dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, with the query's shape and type")
     if lse is None:
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=query.device)
-    elif tuple(lse.shape) != (tokens, heads) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        lse = _Torch.empty((tokens, heads), dtype=_Torch.float32, device=query.device)
+    elif lse.shape != (tokens, heads) or lse.dtype is not _Torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
-    args = q4lin_attention_t(query.data_ptr(), query.stride(0), query.stride(1), out.data_ptr(),
+    batch, int32 = c.batch, _Torch.int32
+    args = q4lin_attention_t(query.data_ptr(), strides[0], strides[1], out.data_ptr(),
                              lse.data_ptr(), _dtype_code(query, "query"), tokens, heads,
                              tokens if max_query is None else max_query,
-                             _check_vector(offsets, c.batch + 1, "int32", "offsets"),
-                             _check_vector(lengths, c.batch, "int32", "lengths"), scale,
-                             int(causal), window, _rope_args(rope, interleaved))
-    st = _lib.q4lin_run_attention(handle.ptr, c, args, _stream_of(stream, query))
+                             _check_vector(offsets, batch + 1, int32, "offsets"),
+                             _check_vector(lengths, batch, int32, "lengths"), scale,
+                             causal, window, _rope_args(rope, interleaved))
+    st = _lib.q4lin_run_attention(handle.ptr, c, args, _stream_of(stream, handle))
     if st != Q4LIN_OK:
         raise Q4LinError(st, "q4lin_run_attention")
     return out, lse
@@ -515,29 +537,30 @@ class LogProbs(NamedTuple):
     top_logprobs: object
 
 
-def _check_logits(t, what):
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+def _row_stride(t, what):
+    strides = t.stride()
+    if len(strides) != 2 or (strides[1] != 1 and t.shape[1] != 1):
         raise ValueError(f"{what} must be [rows, vocabulary] with contiguous rows")
+    return strides[0]
 
 
 def logprobs(handle: Handle, logits, tokens=None, top: int = 0, stream=None) -> LogProbs:
     """Log probability of tokens (int32 [rows], -1 for none), entropy, log-sum-exp and the
     `top` most likely tokens of each row of logits (q4lin_run_logprobs)."""
-    import torch
     _check_device(handle, logits, tokens)
-    _check_logits(logits, "logits")
+    stride = _row_stride(logits, "logits")
     rows, vocabulary = logits.shape
-    small = torch.empty((3, rows), dtype=torch.float32, device=logits.device)
-    logprob, entropy, lse = small.unbind()
+    device, empty, float32 = logits.device, _Torch.empty, _Torch.float32
+    logprob, entropy, lse = (empty(rows, dtype=float32, device=device) for _ in range(3))
     ids = best = None
     if top:
-        ids = torch.empty((rows, top), dtype=torch.int32, device=logits.device)
-        best = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
+        ids = empty((rows, top), dtype=_Torch.int32, device=device)
+        best = empty((rows, top), dtype=float32, device=device)
     args = q4lin_logprobs_t(
-        logits.data_ptr(), logits.stride(0), _dtype_code(logits, "logits"), rows, vocabulary,
-        None if tokens is None else _check_vector(tokens, rows, "int32", "tokens"),
+        logits.data_ptr(), stride, _dtype_code(logits, "logits"), rows, vocabulary,
+        None if tokens is None else _check_vector(tokens, rows, _Torch.int32, "tokens"),
         logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top, _ptr(ids), _ptr(best))
-    st = _lib.q4lin_run_logprobs(handle.ptr, args, _stream_of(stream, logits))
+    st = _lib.q4lin_run_logprobs(handle.ptr, args, _stream_of(stream, handle))
     if st != Q4LIN_OK:
         raise Q4LinError(st, "q4lin_run_logprobs")
     return LogProbs(logprob, entropy, lse, ids, best)
@@ -548,22 +571,21 @@ def logprobs_backward(handle: Handle, logits, tokens, lse, entropy, d_logprob=No
     """Gradient for the logits of logprobs' logprob and entropy, given theirs (float32 [rows]
     or None for zeros) and the lse and entropy that logprobs returned.  out may be the logits
     themselves."""
-    import torch
     _check_device(handle, logits, tokens, lse, entropy, d_logprob, d_entropy, out)
-    _check_logits(logits, "logits")
+    stride = _row_stride(logits, "logits")
     rows, vocabulary = logits.shape
     if out is None:
-        out = torch.empty((rows, vocabulary), dtype=logits.dtype, device=logits.device)
-    elif out.shape != logits.shape or out.dtype != logits.dtype:
+        out = _Torch.empty((rows, vocabulary), dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype is not logits.dtype:
         raise ValueError("out must have the logits' shape and type")
-    _check_logits(out, "out")
-    vector = lambda t, kind, what: None if t is None else _check_vector(t, rows, kind, what)
+    float32 = _Torch.float32
+    vector = lambda t, what: None if t is None else _check_vector(t, rows, float32, what)
     args = q4lin_logprobs_backward_t(
-        logits.data_ptr(), logits.stride(0), _dtype_code(logits, "logits"), rows, vocabulary,
-        vector(tokens, "int32", "tokens"), vector(lse, "float32", "lse"),
-        vector(entropy, "float32", "entropy"), vector(d_logprob, "float32", "d_logprob"),
-        vector(d_entropy, "float32", "d_entropy"), out.data_ptr(), out.stride(0))
-    st = _lib.q4lin_run_logprobs_backward(handle.ptr, args, _stream_of(stream, logits))
+        logits.data_ptr(), stride, _dtype_code(logits, "logits"), rows, vocabulary,
+        None if tokens is None else _check_vector(tokens, rows, _Torch.int32, "tokens"),
+        vector(lse, "lse"), vector(entropy, "entropy"), vector(d_logprob, "d_logprob"),
+        vector(d_entropy, "d_entropy"), out.data_ptr(), _row_stride(out, "out"))
+    st = _lib.q4lin_run_logprobs_backward(handle.ptr, args, _stream_of(stream, handle))
     if st != Q4LIN_OK:
         raise Q4LinError(st, "q4lin_run_logprobs_backward")
     return out
