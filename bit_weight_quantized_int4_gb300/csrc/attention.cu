@@ -32,12 +32,14 @@ using namespace serving;
 constexpr int kTile = 64;        // keys per tile
 constexpr int kRows = 8;         // query rows per MMA tile (two of its 16 rows each)
 constexpr int kSlots = 3;        // half tiles (keys or values) in a warp's ring
-constexpr int kMaxBatch = 2048;  // sequences per launch
+constexpr int kMaxBatch = 1024;  // sequences per launch
 constexpr float kShift = 14.f;   // probabilities are kept as 2^14 p: fp16's range downwards
 constexpr int64_t kDrainNs = 4000000000LL;
 
-__host__ __device__ constexpr int warps_of(int D) { return D == 256 ? 4 : 8; }
-__host__ __device__ constexpr int ctas_of(int D, int RT) { return D == 64 && RT == 1 ? 2 : 1; }
+// CTAs of four warps, as many per SM as their rings and registers allow: while one joins its
+// warps or waits for its first keys, the others stream.
+constexpr int kWarps = 4;
+__host__ __device__ constexpr int ctas_of(int D, int RT) { return D == 256 ? 1 : D == 64 && RT == 1 ? 3 : 2; }
 
 struct SplitArgs {
     q4lin_kv_cache_t cache;
@@ -60,28 +62,34 @@ struct RowInfo {
 };
 
 // Largest heads_per * RT: what the queries' fragments leave of the shared memory.
-__host__ __device__ constexpr int max_group(int D) { return D == 256 ? 2 : 4; }
+__host__ __device__ constexpr int max_group(int D) { return D == 64 ? 4 : 2; }
+
+enum { kCut, kParts, kWhole };  // how the list is shared, see the kernel
+
+struct List {
+    int mode, share, tiles, grid, groups, end;  // end: of this CTA's share
+};
 
 // A CTA's share of one sequence's keys.
 struct Piece {
     int b, len, tq, h0, row0, tile, n;  // n tiles from `tile`; first head, first row
-    int units, k0, seg_begin;           // list units of the whole, done before, where it begins
-    int after;                          // list position past the piece
-    int cut;
+    int after, more;                    // list position past the piece; whether the CTA goes on
+    int cut, later, c0, c1;             // not a head's only piece; not its first; its CTAs
     int64_t o0;
 };
 
 template <int D, int RT>
 struct Shared {
-    static constexpr int W = warps_of(D), kGroup = max_group(D);
+    static constexpr int W = kWarps, kGroup = max_group(D);
     uint4 q[kGroup][D / 16][32];  // A fragments, [head * RT + row tile]
     RowInfo row[2][kGroup * kRows];  // of this piece and the next
     float m[W][RT * kRows], l[W][RT * kRows];
     uint32_t merge[W];  // where a warp left its outputs
     uint64_t full[W][kSlots];
+    List list;
     Piece piece[3];  // this one, the next, and the one after that in the making
     int prefix[kMaxBatch + 1];
-    int sums[3][W];
+    int sums[3][W], scan[2][W];
     int limit_min[2][kGroup], low_max[2][kGroup];  // per head of a piece
     int failed, last;
 };
@@ -111,6 +119,52 @@ __device__ __forceinline__ Sequence sequence_of(const SplitArgs& g, int64_t b, b
     return s;
 }
 
+// A head's parts, one per CTA, in proportion to its tiles.
+__device__ __forceinline__ int parts_of(int tiles, int grid, int all) {
+    return max(1, (int)((int64_t)tiles * grid / max(all, 1)));
+}
+// Units of one head in the list.
+__device__ __forceinline__ int units_of(const List& list, const Sequence& s) {
+    return list.mode == kCut ? s.tiles : list.mode == kParts ? parts_of(s.tiles, list.grid, list.tiles) : 1;
+}
+// What a CTA does from list position pos on, in sequence b that begins at list_begin (one thread).
+template <int RT>
+__device__ __noinline__ void fill_piece(const SplitArgs& g, const List& list, int pos, int b, int list_begin,
+                                        const Sequence& s, Piece& p) {
+    p.b = b, p.len = s.len, p.tq = s.tq;
+    const int of_head = units_of(list, s), local = pos - list_begin, seg = local / of_head;
+    const int unit = local - seg * of_head, done = min(of_head - unit, list.end - pos);
+    p.h0 = seg / s.row_tiles * g.heads_per, p.row0 = seg % s.row_tiles * (RT * kRows);
+    p.after = pos + done;
+    p.more = p.after < list.end;
+    p.cut = done < of_head;
+    int k0 = 0;
+    p.n = s.tiles;
+    if (list.mode == kCut) {
+        k0 = unit, p.n = done;
+    } else if (list.mode == kParts) {
+        const int each = (s.tiles + of_head - 1) / of_head;
+        k0 = unit * each, p.n = max(0, min(each, s.tiles - k0));
+    }
+    p.tile = s.tile0 + k0;
+    p.later = unit > 0;
+    p.c0 = (pos - unit) / list.share, p.c1 = (pos - unit + of_head - 1) / list.share;
+    p.o0 = __ldg(g.a.offsets + b);
+}
+template <int RT>
+__device__ __noinline__ void make_piece(const SplitArgs& g, const List& list, const int* prefix, int pos, Piece& p) {
+    int lo = 0, hi = (int)g.cache.batch;  // prefix[lo] <= pos < prefix[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= pos)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    bool bad;
+    fill_piece<RT>(g, list, pos, lo, prefix[lo], sequence_of<RT>(g, lo, &bad), p);
+}
+
 // Four channels of a query row: the joined sums o and l, both as 2^kShift p, over the maximum
 // `base` (a power of two's exponent).
 __device__ __forceinline__ void emit(const SplitArgs& g, int64_t index, int D, int d, float4 o, float l,
@@ -127,9 +181,58 @@ __device__ __forceinline__ void emit(const SplitArgs& g, int64_t index, int D, i
     if (d == 0 && g.a.lse) g.a.lse[index] = l != 0.f ? (base + lg2(l) - kShift) * kLn2 : -INFINITY;
 }
 
+// A CTA's unfinished piece of one head: [R][D] sums, then R maxima and R sums of weights.
 template <int D, int RT>
-__global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_split_kernel(const SplitArgs g) {
-    constexpr int W = warps_of(D), T = 32 * W, R = RT * kRows, kGroup = max_group(D);
+__device__ __forceinline__ float* part_at(const SplitArgs& g, int cta, int place, int hi) {
+    constexpr int kPart = RT * kRows * (D + 2);
+    return g.ws + ((int64_t)(cta * 2 + place) * g.heads_per + hi) * kPart;
+}
+
+// The parts of a piece's heads, added in their order by one CTA: four channels of a row per
+// thread, kAhead loads in flight (what another SM has just written takes a microsecond or two
+// to come).  Not in line: its registers are not the main loop's.
+template <int D, int RT, int W>
+__device__ __noinline__ void join_parts(const SplitArgs& g, const Piece& P, const RowInfo* rows) {
+    constexpr int R = RT * kRows, T = 32 * W, kAhead = 16;
+    const int group = (int)(g.a.heads / g.cache.kv_heads);
+    const int valid = min(R, P.tq * group - P.row0), count = P.c1 - P.c0 + 1;
+    for (int i = threadIdx.x; i < g.heads_per * valid * (D / 4); i += T) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4, hi = row / valid, r = row - hi * valid;
+        float mx = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < count; c += kAhead) {
+            float pm[kAhead], pl[kAhead];
+            float4 po[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                pm[k] = -INFINITY, pl[k] = 0.f, po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c + k < count) {
+                    const float* src = part_at<D, RT>(g, P.c0 + c + k, c + k == 0, hi);
+                    pm[k] = __ldcg(src + R * D + r), pl[k] = __ldcg(src + R * D + R + r);
+                    po[k] = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
+                }
+            }
+            float top = mx;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) top = fmaxf(top, pm[k]);
+            const float from = top == -INFINITY ? 0.f : top, old = ex2(mx - from);
+            o.x *= old, o.y *= old, o.z *= old, o.w *= old, l *= old;
+            mx = top;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const float w = ex2(pm[k] - from);
+                o.x = fmaf(po[k].x, w, o.x), o.y = fmaf(po[k].y, w, o.y);
+                o.z = fmaf(po[k].z, w, o.z), o.w = fmaf(po[k].w, w, o.w);
+                l = fmaf(pl[k], w, l);
+            }
+        }
+        emit(g, rows[hi * R + r].index, D, d, o, l, mx == -INFINITY ? 0.f : mx);
+    }
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__(32 * kWarps, ctas_of(D, RT)) attention_split_kernel(const SplitArgs g) {
+    constexpr int W = kWarps, T = 32 * W, R = RT * kRows, kGroup = max_group(D);
     constexpr int kNt = D / 8;
     constexpr uint32_t kHalf = kTile * D;  // bytes of a tile's keys (values)
     extern __shared__ uint8_t smem_raw[];
@@ -154,85 +257,90 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
     }
     const int batch = (int)C.batch, groups = Hkv / hp;
     int tiles_all = 0, segments = 0, longest = 0;
+    Sequence mine = {};  // of the thread's last sequence: its only one in most calls
     for (int b = tid; b < batch; b += T) {
         bool bad;
-        const Sequence s = sequence_of<RT>(g, b, &bad);
-        tiles_all += s.tiles * s.row_tiles * groups, segments += s.row_tiles * groups;
-        if (s.row_tiles) longest = max(longest, s.tiles);
+        mine = sequence_of<RT>(g, b, &bad);
+        tiles_all += mine.tiles * mine.row_tiles * groups, segments += mine.row_tiles * groups;
+        if (mine.row_tiles) longest = max(longest, mine.tiles);
         if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
     }
-    tiles_all = __reduce_add_sync(0xffffffffu, tiles_all);
-    segments = __reduce_add_sync(0xffffffffu, segments);
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if (lane == 0) S.sums[0][warp] = tiles_all, S.sums[1][warp] = segments, S.sums[2][warp] = longest;
+    const bool once = batch <= T;
+    {
+        const int a = __reduce_add_sync(0xffffffffu, tiles_all), b = __reduce_add_sync(0xffffffffu, segments);
+        const int c = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) S.sums[0][warp] = a, S.sums[1][warp] = b, S.sums[2][warp] = c;
+    }
     __syncthreads();
     tiles_all = segments = longest = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w)
         tiles_all += S.sums[0][w], segments += S.sums[1][w], longest = max(longest, S.sums[2][w]);
-    // Rounds of the warps over a CTA's tiles: cut evenly, a join costs about two; whole, each
-    // CTA takes some heads' tiles to their end.  (Measured: one token over 701 keys, 8 heads
-    // of 64: SHORT.)
+    // Three ways to share the list, by the rounds that the warps of a CTA then take over its
+    // tiles.  Cut: evenly, wherever that falls; a piece more and a join cost about three rounds.
+    // Parts: every head in parts of its own, one per CTA; a join costs about two.  Whole: some
+    // heads to their end.
     const int grid = (int)gridDim.x;
-    const int cut_share = max(wph, (tiles_all + grid - 1) / grid);
-    const int whole_share = (segments + grid - 1) / grid;
-    const bool whole = whole_share * ((longest + wph - 1) / wph) <= (cut_share + wph - 1) / wph + 2;
-    const int share = whole ? whole_share : cut_share, total = whole ? segments : tiles_all;
+    int parts = 0, part_tiles = 0;
+    for (int b = tid; b < batch; b += T) {
+        bool bad;
+        if (!once) mine = sequence_of<RT>(g, b, &bad);
+        if (!mine.row_tiles) continue;
+        const int n = parts_of(mine.tiles, grid, tiles_all);
+        parts += n * mine.row_tiles * groups;
+        part_tiles = max(part_tiles, (mine.tiles + n - 1) / n);
+    }
+    parts = __reduce_add_sync(0xffffffffu, parts);
+    part_tiles = __reduce_max_sync(0xffffffffu, part_tiles);
+    if (lane == 0) S.scan[0][warp] = parts, S.scan[1][warp] = part_tiles;
+    __syncthreads();
+    parts = part_tiles = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) parts += S.scan[0][w], part_tiles = max(part_tiles, S.scan[1][w]);
+    const int cut_share = max(wph, (tiles_all + grid - 1) / grid), whole_share = (segments + grid - 1) / grid;
+    const int cut_rounds = (cut_share + wph - 1) / wph + 3;
+    const int whole_rounds = whole_share * ((longest + wph - 1) / wph);
+    const int part_rounds = parts <= grid ? (part_tiles + wph - 1) / wph + 2 : INT_MAX;
+    const int rounds = min(cut_rounds, min(whole_rounds, part_rounds));
+    const int mode = rounds == whole_rounds ? kWhole : rounds == part_rounds ? kParts : kCut;
+    const int share = mode == kCut ? cut_share : mode == kParts ? 1 : whole_share;
+    const int total = mode == kCut ? tiles_all : mode == kParts ? parts : segments;
     const int64_t begin = (int64_t)blockIdx.x * share;
     const int end = (int)min((int64_t)total, begin + share);
     if (begin >= end) return;
+    const List list = {mode, share, tiles_all, grid, groups, end};
+    if (tid == 0) S.list = list;
     int carry = 0;
     for (int b0 = 0; b0 < batch; b0 += T) {
         const int b = b0 + tid;
         int v = 0;
         if (b < batch) {
             bool bad;
-            const Sequence s = sequence_of<RT>(g, b, &bad);
-            v = (whole ? 1 : s.tiles) * s.row_tiles * groups;
+            if (!once) mine = sequence_of<RT>(g, b, &bad);
+            v = mine.row_tiles ? units_of(list, mine) * mine.row_tiles * groups : 0;
         }
+        int sum = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += n;
+            const int n = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += n;
         }
         __syncthreads();
-        if (lane == 31) S.sums[0][warp] = v;
+        if (lane == 31) S.scan[0][warp] = sum;
         __syncthreads();
         int before = carry;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            if (w < warp) before += S.sums[0][w];
-            carry += S.sums[0][w];
+            if (w < warp) before += S.scan[0][w];
+            carry += S.scan[0][w];
         }
-        if (b < batch) S.prefix[b + 1] = before + v;
+        before += sum;
+        if (b < batch) S.prefix[b + 1] = before;
+        // The sequence that the CTA's share begins in.
+        if (v && begin >= before - v && begin < before) fill_piece<RT>(g, list, (int)begin, b, before - v, mine, S.piece[0]);
     }
-    __syncthreads();
 
-    // ---- pieces
-    auto make_piece = [&](int pos, Piece& p) {  // one thread
-        int lo = 0, hi = batch;  // prefix[lo] <= pos < prefix[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (S.prefix[mid] <= pos)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        bool bad;
-        const Sequence s = sequence_of<RT>(g, lo, &bad);
-        p.b = lo, p.len = s.len, p.tq = s.tq;
-        p.units = whole ? 1 : s.tiles;
-        const int local = pos - S.prefix[lo], seg = local / p.units;
-        p.k0 = local - seg * p.units;
-        p.h0 = seg / s.row_tiles * hp, p.row0 = seg % s.row_tiles * R;
-        p.seg_begin = pos - p.k0;
-        const int units = min(p.units - p.k0, end - pos);
-        p.cut = units < p.units;
-        p.tile = s.tile0 + p.k0, p.n = whole ? s.tiles : units;
-        p.after = pos + units;
-        p.o0 = __ldg(g.a.offsets + lo);
-    };
-
+    // ---- pieces: S.piece[0] is there after the next barrier
     // This warp's tiles of a piece: `first`, `first` + wph, ...; with the pages of the next
     // 32 / ppt of them in the lanes: lane i holds page i % ppt of tile i / ppt.
     const uint32_t page_bytes = (uint32_t)(D << ps);
@@ -305,7 +413,11 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
     bool turned;
     int cl, ch;
     rope_channels(g.a.rope, q_unit, &turned, &cl, &ch);
-    auto load_query = [&](const Piece& p, int pass, float (&x)[8]) {
+    struct Query {
+        float x[8], c[4], s[4];
+    };
+    auto load_query = [&](const Piece& p, int pass, Query& q) {
+        float(&x)[8] = q.x;
         int token, h;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = 0.f;
@@ -313,15 +425,18 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             const int64_t e = (p.o0 + token) * g.a.q_token_stride + h * g.a.q_head_stride;
             load_four(g.a.query, g.a.dtype, e + cl, g.q_vec, x);
             load_four(g.a.query, g.a.dtype, e + ch, g.q_vec, x + 4);
+            const int position = p.len - p.tq + token;
+            if (turned && position >= 0) rope_load(g.a.rope, position, q_unit, q.c, q.s);
         }
     };
     // Rotated, scaled to fp16's upper range by a power of two, split into two terms.
-    auto put_query = [&](const Piece& p, int pass, float (&x)[8], int which) {
+    auto put_query = [&](const Piece& p, int pass, Query& q, int which) {
+        float(&x)[8] = q.x;
         const int r = pass * kPer + tid / kUnitsRow;
         int token, h;
         const bool in = query_row(p, r, &token, &h);
         const int position = p.len - p.tq + token;
-        if (in && turned && position >= 0) rope_unit(g.a.rope, position, q_unit, x);
+        if (in && turned && position >= 0) rope_apply(g.a.rope, q.c, q.s, x);
         float m = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
@@ -373,25 +488,27 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
         return at;
     };
 
-    if (tid == 0) {
-        make_piece((int)begin, S.piece[0]);
-        if (S.piece[0].after < end) make_piece(S.piece[0].after, S.piece[1]);
-    }
+    const int passes = (hp * R + kPer - 1) / kPer;  // of this call
     clear_limits(0);
     __syncthreads();
-    enter(S.piece[0]);
-    issue();
-    issue();
-    fetch_scales(0);
-    for (int pass = 0; pass < kPasses; ++pass) {
-        float x[8];
-        load_query(S.piece[0], pass, x);
-        put_query(S.piece[0], pass, x, 0);
+    {
+        Query x[kPasses];
+#pragma unroll
+        for (int pass = 0; pass < kPasses; ++pass)
+            if (pass < passes) load_query(S.piece[0], pass, x[pass]);
+        enter(S.piece[0]);
+        issue();
+        issue();
+        issue();
+        fetch_scales(0);
+#pragma unroll
+        for (int pass = 0; pass < kPasses; ++pass)
+            if (pass < passes) put_query(S.piece[0], pass, x[pass], 0);
     }
+    if (tid == T - 1 && S.piece[0].more) make_piece<RT>(g, S.list, S.prefix, S.piece[0].after, S.piece[1]);
     __syncthreads();
 
     for (int turn = 0;; turn = turn == 2 ? 0 : turn + 1) {
-        issue();
         float O[RT][kNt][2], m_run[RT], l_run[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -538,7 +655,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
         const Piece& P = S.piece[turn];
         const int next = turn == 2 ? 0 : turn + 1;
         const Piece& N = S.piece[next];
-        const bool more = P.after < end;
+        const bool more = P.more;
         // ---- the next piece's first copies take two of the ring's three slots, this one's
         // outputs the third
         const uint32_t keep = (uint32_t)(warp * kSlots + (slot_in + 2) % kSlots) * kHalf;
@@ -549,10 +666,11 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             issue();
             fetch_scales(0);
         }
-        float x[kPasses][8];
+        Query x[kPasses];
         if (more) {
 #pragma unroll
-            for (int pass = 0; pass < kPasses; ++pass) load_query(N, pass, x[pass]);
+            for (int pass = 0; pass < kPasses; ++pass)
+                if (pass < passes) load_query(N, pass, x[pass]);
             clear_limits(which ^ 1);
         }
         if (lane == 0) S.merge[warp] = keep;
@@ -572,10 +690,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
 
         // ---- join a head's warps.  Partial pieces: slot 0 for the CTA's first (begun by an
         // earlier CTA), 1 for its last.
-        constexpr int kPart = R * (D + 2), kQuads = R * D / 4;
-        auto part_at = [&](int cta, int place, int hi) {
-            return g.ws + ((int64_t)(cta * 2 + place) * hp + hi) * kPart;
-        };
+        constexpr int kQuads = R * D / 4;
         for (int i = tid - my_head * wph * 32; i < kQuads; i += wph * 32) {
             const int r = i / (D / 4), d = (i % (D / 4)) * 4, w0 = my_head * wph;
             float mx = -INFINITY;
@@ -592,7 +707,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
                 l = fmaf(S.l[w][r], c, l);
             }
             if (P.cut) {
-                float* part = part_at(blockIdx.x, P.k0 == 0, my_head);
+                float* part = part_at<D, RT>(g, blockIdx.x, !P.later, my_head);
                 *reinterpret_cast<float4*>(part + r * D + d) = o;
                 if (d == 0) part[R * D + r] = mx, part[R * D + R + r] = l;
             } else {
@@ -600,8 +715,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
             }
         }
         if (P.cut) {
-            // The CTAs that share these heads' keys: c0 .. c1.
-            const int c0 = P.seg_begin / share, c1 = (P.seg_begin + P.units - 1) / share;
+            const int c0 = P.c0, c1 = P.c1;  // the CTAs that share these heads' keys
             __syncthreads();
             if (tid == 0) {
                 __threadfence();
@@ -610,46 +724,29 @@ __global__ void __launch_bounds__(32 * warps_of(D), ctas_of(D, RT)) attention_sp
                 if (S.last) g.tickets[c0] = 0;
             }
             __syncthreads();
-            if (S.last) {
-                for (int i = tid; i < hp * kQuads; i += T) {
-                    const int hi = i / kQuads, r = i % kQuads / (D / 4), d = (i % (D / 4)) * 4;
-                    const int64_t index = S.row[which][hi * R + r].index;
-                    if (index < 0) continue;
-                    float mx = -INFINITY;
-                    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(part_at(c, c == c0, hi) + R * D + r));
-                    const float base = mx == -INFINITY ? 0.f : mx;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float l = 0.f;
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* src = part_at(c, c == c0, hi);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
-                        const float k = ex2(__ldcg(src + R * D + r) - base);
-                        o.x = fmaf(v.x, k, o.x), o.y = fmaf(v.y, k, o.y);
-                        o.z = fmaf(v.z, k, o.z), o.w = fmaf(v.w, k, o.w);
-                        l = fmaf(__ldcg(src + R * D + R + r), k, l);
-                    }
-                    emit(g, index, D, d, o, l, base);
-                }
-            }
+            if (S.last) join_parts<D, RT, W>(g, P, S.row[which]);
         }
         if (!more) break;
         which ^= 1;
-        if (tid == 0 && N.after < end) make_piece(N.after, S.piece[next == 2 ? 0 : next + 1]);
+        if (tid == T - 1 && N.more)
+            make_piece<RT>(g, S.list, S.prefix, N.after, S.piece[next == 2 ? 0 : next + 1]);
 #pragma unroll
-        for (int pass = 0; pass < kPasses; ++pass) put_query(N, pass, x[pass], which);
+        for (int pass = 0; pass < kPasses; ++pass)
+            if (pass < passes) put_query(N, pass, x[pass], which);
         // The next copies also write where the joined outputs were.
         fence_async_shared();
         __syncthreads();
+        issue();
     }
 }
 
 template <int D, int RT>
 cudaError_t launch(const SplitArgs& g, int64_t grid, cudaStream_t stream) {
-    constexpr int bytes = warps_of(D) * kSlots * kTile * D + 128;
+    constexpr int bytes = kWarps * kSlots * kTile * D + 128;
+    static_assert(ctas_of(D, RT) * (bytes + sizeof(Shared<D, RT>) + 1024) <= 228 * 1024, "shared memory of one SM");
     const cudaError_t e = kernel_smem_once<attention_split_kernel<D, RT>>(bytes);
     if (e != cudaSuccess) return e;
-    attention_split_kernel<D, RT><<<(unsigned)grid, 32 * warps_of(D), bytes, stream>>>(g);
+    attention_split_kernel<D, RT><<<(unsigned)grid, 32 * kWarps, bytes, stream>>>(g);
     return cudaGetLastError();
 }
 
@@ -686,7 +783,7 @@ cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_at
         const int64_t row_tiles = std::min((a.tokens * group + R - 1) / R + g.cache.batch,
                                            ((rows + R - 1) / R) * g.cache.batch);
         const int64_t grid = std::max<int64_t>(
-            1, std::min<int64_t>(slots, (tiles * row_tiles * cache.kv_heads + warps_of(D) - 1) / warps_of(D)));
+            1, std::min<int64_t>(slots, (tiles * row_tiles * cache.kv_heads + kWarps - 1) / kWarps));
         // More heads at a time leave fewer joins of warps and fewer of them idle at the end of
         // a piece, as long as every CTA finds a piece of its own.
         g.heads_per = 1;

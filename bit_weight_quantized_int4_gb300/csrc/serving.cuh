@@ -65,12 +65,17 @@ __device__ __forceinline__ void store_one(void* p, int dtype, int64_t i, float x
 }
 
 // Row `position` of the rotation for the eight channels of unit u (two groups of four, see
-// rope_channels), each product and sum rounded once.
-__device__ __forceinline__ void rope_unit(const q4lin_rope_t& r, int64_t position, int u, float (&x)[8]) {
+// rope_channels): the four cosines and sines.
+__device__ __forceinline__ void rope_load(const q4lin_rope_t& r, int64_t position, int u, float (&c)[4],
+                                          float (&s)[4]) {
     const int64_t at = position * (r.rotated / 2) + 4 * u;
-    float c[4], s[4], y[4], z[4];
     load_four(r.cos, Q4LIN_DTYPE_F32, at, (reinterpret_cast<uintptr_t>(r.cos) & 15) == 0, c);
     load_four(r.sin, Q4LIN_DTYPE_F32, at, (reinterpret_cast<uintptr_t>(r.sin) & 15) == 0, s);
+}
+// The rotation, each product and sum rounded once.
+__device__ __forceinline__ void rope_apply(const q4lin_rope_t& r, const float (&c)[4], const float (&s)[4],
+                                           float (&x)[8]) {
+    float y[4], z[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float a = r.interleaved ? x[2 * e] : x[e], b = r.interleaved ? x[2 * e + 1] : x[4 + e];
@@ -82,6 +87,11 @@ __device__ __forceinline__ void rope_unit(const q4lin_rope_t& r, int64_t positio
         x[2 * e] = r.interleaved ? y[e] : e < 2 ? y[2 * e] : z[2 * e - 4];
         x[2 * e + 1] = r.interleaved ? z[e] : e < 2 ? y[2 * e + 1] : z[2 * e - 3];
     }
+}
+__device__ __forceinline__ void rope_unit(const q4lin_rope_t& r, int64_t position, int u, float (&x)[8]) {
+    float c[4], s[4];
+    rope_load(r, position, u, c, s);
+    rope_apply(r, c, s, x);
 }
 // First channels of the two groups of four of unit u of a head: a rotated pair's two halves
 // where the first half is rotated with the second, else eight consecutive channels.
