@@ -33,24 +33,6 @@ __device__ __forceinline__ int64_t first_slot(const AppendArgs& g, int64_t b) {
     return ((int64_t)__ldg(g.a.offsets + b) >> g.page_shift) + 2 * b;
 }
 
-// The last b in [0, batch) with key(b) <= at, by a 32-way search of one warp.
-template <typename Key>
-__device__ __forceinline__ int64_t find_sequence(int64_t batch, int64_t at, Key key) {
-    const int lane = threadIdx.x & 31;
-    int64_t lo = 0, n = batch;
-    while (true) {
-        const int64_t step = (n + 31) / 32;
-        const int64_t b = lo + lane * step;
-        const bool below = lane * step < n && key(b) <= at;
-        const unsigned m = __ballot_sync(0xffffffffu, below);
-        const int last = m ? 31 - __clz(m) : 0;
-        const int64_t left = n - last * step;
-        lo += last * step;
-        n = left < step ? left : step;
-        if (step == 1) return lo;
-    }
-}
-
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendArgs g) {
     __shared__ float s_amax[THREADS / 32];

@@ -113,6 +113,24 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
+// The last b in [0, batch) with key(b) <= at, by a 32-way search of one warp.
+template <typename Key>
+__device__ __forceinline__ int64_t find_sequence(int64_t batch, int64_t at, Key key) {
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, n = batch;
+    while (true) {
+        const int64_t step = (n + 31) / 32;
+        const int64_t b = lo + lane * step;
+        const bool below = lane * step < n && key(b) <= at;
+        const unsigned m = __ballot_sync(0xffffffffu, below);
+        const int last = m ? 31 - __clz(m) : 0;
+        const int64_t left = n - last * step;
+        lo += last * step;
+        n = left < step ? left : step;
+        if (step == 1) return lo;
+    }
+}
+
 // `bytes` (a multiple of 16) from global to this CTA's shared memory, both 16-byte aligned,
 // completing on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
