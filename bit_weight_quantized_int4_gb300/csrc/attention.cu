@@ -199,22 +199,23 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
     const int batch_tiles = 32 / ppt;
     const int32_t* table = nullptr;
     int first = 0, cnt = 0, pages = 0, head = 0, ids = 0, issued = 0, slot_in = 0, in_flight = 0;
-    auto fetch_ids = [&](int i) {
+    auto load_ids = [&](int i) {
         const int p = (first + i) * ppt + lane;
-        ids = -1;
-        if (i + lane / ppt < cnt && p < pages) {
-            ids = __ldg(table + p);
-            if (ids < 0 || ids >= C.num_pages) {
-                atomicCAS(g.status, 0, kStatusIndex);
-                ids = 0;  // read something of the cache rather than nothing
-            }
+        ids = i + lane / ppt < cnt && p < pages ? __ldg(table + p) : INT_MIN;
+    };
+    auto check_ids = [&]() {
+        if (ids == INT_MIN) {
+            ids = -1;
+        } else if (ids < 0 || ids >= C.num_pages) {
+            atomicCAS(g.status, 0, kStatusIndex);
+            ids = 0;  // read something of the cache rather than nothing
         }
     };
     // Next half tile of the piece (keys of a tile, then its values) into the ring.
     auto issue = [&]() {
         if (issued >= 2 * cnt) return;
         const int i = issued >> 1;
-        if ((issued & 1) == 0 && i > 0 && i % batch_tiles == 0) fetch_ids(i);
+        if ((issued & 1) == 0 && i > 0 && i % batch_tiles == 0) load_ids(i), check_ids();
         const int id = __shfl_sync(0xffffffffu, ids, (i % batch_tiles) * ppt + lane % ppt);
         const bool some = lane < ppt && id >= 0;
         const int count = __popc(__ballot_sync(0xffffffffu, some));
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
         pages = (P.len + (1 << ps) - 1) >> ps;
         head = P.h;
         issued = 0;
+        load_ids(0);
         int limit_min = INT_MAX, low_max = 0;
         {
             constexpr int kUnits = D / 8, kPer = 32 / kUnits, kPasses = R / kPer;
@@ -276,33 +278,36 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
             int cl, ch;
             rope_channels(g.a.rope, unit, &turned, &cl, &ch);
             constexpr int kTogether = kPasses < 4 ? kPasses : 4;  // passes whose loads overlap
+            const int valid = min(R, P.tq * group - P.row0);  // rows (the others stay unread)
+            if (lane >= valid && lane < R) mine.row[lane] = {0.f, -1, 0, -1};
+            const uint32_t token0 = (uint32_t)P.row0 / (uint32_t)group, rest0 = P.row0 - token0 * group;
 #pragma unroll 1
-            for (int p0 = 0; p0 < kPasses; p0 += kTogether) {
+            for (int p0 = 0; p0 * kPer < valid; p0 += kTogether) {
                 float x[kTogether][8], c[kTogether][4], s[kTogether][4];
 #pragma unroll
                 for (int k = 0; k < kTogether; ++k) {
-                    const int row = P.row0 + (p0 + k) * kPer + lane / kUnits, token = row / group;
-                    const int position = P.len - P.tq + token;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-                    if (row < P.tq * group) {
+                    const uint32_t r = (p0 + k) * kPer + lane / kUnits, step = (rest0 + r) / (uint32_t)group;
+                    const int token = token0 + step, position = P.len - P.tq + token;
+                    if (r < valid) {
                         const int64_t e = (o0 + token) * g.a.q_token_stride +
-                                          (P.h * group + row - token * group) * g.a.q_head_stride;
+                                          (P.h * group + (int)(rest0 + r - step * group)) * g.a.q_head_stride;
                         load_four(g.a.query, g.a.dtype, e + cl, g.q_vec, x[k]);
                         load_four(g.a.query, g.a.dtype, e + ch, g.q_vec, x[k] + 4);
                         if (turned && position >= 0) rope_load(g.a.rope, position, unit, c[k], s[k]);
                     }
                 }
                 if (p0 == 0) {
-                    fetch_ids(0);
+                    check_ids();
                     fetch_scales(0);
-                    issue();
+#pragma unroll 1
+                    for (int i = 0; i < kSlots; ++i) issue();
                 }
 #pragma unroll
                 for (int k = 0; k < kTogether; ++k) {
-                    const int r = (p0 + k) * kPer + lane / kUnits, row = P.row0 + r, token = row / group;
-                    const int position = P.len - P.tq + token;
-                    const bool in = row < P.tq * group;
+                    if ((p0 + k) * kPer >= valid) break;
+                    const uint32_t r = (p0 + k) * kPer + lane / kUnits, step = (rest0 + r) / (uint32_t)group;
+                    const int token = token0 + step, position = P.len - P.tq + token;
+                    const bool in = r < valid;
                     if (in && turned && position >= 0) rope_apply(g.a.rope, c[k], s[k], x[k]);
                     float m = 0.f;
 #pragma unroll
@@ -314,6 +319,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
                     const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
                     const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
                     const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+                    if (!in) continue;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         const int d = w ? ch : cl;  // channels d .. d + 3
@@ -324,16 +330,14 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
                     }
                     RowInfo i;
                     i.factor = g.a.scale * kLog2e * down;
-                    i.limit = !in ? -1 : g.a.causal ? position : P.len - 1;
+                    i.limit = g.a.causal ? position : P.len - 1;
                     const int64_t low = g.a.window > 0 ? (int64_t)position - g.a.window + 1 : 0;
                     i.low = low > 0 ? (int)low : 0;
-                    i.index = in ? (int)((o0 + token) * g.a.heads + P.h * group + row - token * group) : -1;
+                    i.index = (int)((o0 + token) * g.a.heads + P.h * group + (rest0 + r - step * group));
                     if (unit == 0) mine.row[r] = i;
-                    if (in) limit_min = min(limit_min, i.limit), low_max = max(low_max, i.low);
+                    limit_min = min(limit_min, i.limit), low_max = max(low_max, i.low);
                 }
             }
-#pragma unroll 1
-            for (int i = 1; i < kSlots; ++i) issue();
             limit_min = __reduce_min_sync(0xffffffffu, limit_min);
             low_max = __reduce_max_sync(0xffffffffu, low_max);
             __syncwarp();
@@ -525,9 +529,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
 }
 
 // The rows of heads that were cut: one CTA per query row, its warps taking parts in turn.
-template <int D, int RT, int kJoinWarps>
+template <int D, int RT, int kJoinWarps, int kAhead>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const SplitArgs g) {
-    constexpr int R = RT * kRows, kAhead = 4, kVec = D == 256 ? 2 : 1;  // 16-byte units per lane
+    constexpr int R = RT * kRows, kVec = D == 256 ? 2 : 1;  // 16-byte units per lane
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
     __shared__ float4 s_o[kJoinWarps][D / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -619,17 +623,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
     if (lane == 0 && g.a.lse) g.a.lse[index] = l != 0.f ? (from + lg2(l) - kShift) * kLn2 : -INFINITY;
 }
 
-constexpr int kManyParts = 16, kFewParts = 2;  // warps of a joining CTA
-
 template <int D, int RT>
-cudaError_t launch(SplitArgs& g, int64_t tiles_most, const LaunchCtx& c) {
+cudaError_t launch(SplitArgs& g, int64_t segments_most, const LaunchCtx& c) {
     constexpr int W = warps_of(D, RT), R = RT * kRows;
     constexpr int bytes = W * kSlots * kTile * D + (int)sizeof(Shared<D, RT>);
     static_assert(bytes <= 227 * 1024, "shared memory of one SM");
     cudaError_t e = kernel_smem_once<attention_split_kernel<D, RT>>(bytes);
     if (e != cudaSuccess) return e;
     // One CTA per SM, and no more than the longest possible list has tiles for.
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(c.sm_count, tiles_most));
+    const int64_t tiles = (g.cache.pages_per_sequence * g.cache.page_size + kTile - 1) / kTile;
+    const int64_t grid = std::min<int64_t>(c.sm_count, segments_most * tiles);
     g.workers = (int)grid * W;
     g.list = reinterpret_cast<int*>(c.ws);
     g.parts = c.ws + kMaxBatch + 4;  // 16-byte aligned
@@ -641,17 +644,25 @@ cudaError_t launch(SplitArgs& g, int64_t tiles_most, const LaunchCtx& c) {
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    // Few rows have many parts each, many rows few.
-    const int64_t rows = g.a.tokens * g.a.heads;
-    const bool few = rows <= 2 * c.sm_count;
+    // Warps per row by the parts that a row may have (64 sequences x 8 heads on 1216 warps: 2 or 3
+    // parts, two warps 113 us for the whole call, four 116; 9 x 4 heads x 3 row tiles on 1064:
+    // about 10, eight warps 21 us, two 24; one sequence x 8 heads: 152).
+    const int64_t parts = g.workers / segments_most;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)rows);
-    cfg.blockDim = dim3(few ? 32 * kManyParts : 32 * kFewParts);
+    cfg.gridDim = dim3((unsigned)(g.a.tokens * g.a.heads));
     cfg.stream = c.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&cfg, attention_join_kernel<D, RT, kManyParts>, g)
-               : cudaLaunchKernelEx(&cfg, attention_join_kernel<D, RT, kFewParts>, g);
+    if (parts <= 4) {
+        cfg.blockDim = dim3(64);
+        return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, RT, 2, 4>, g);
+    }
+    if (parts <= 32) {
+        cfg.blockDim = dim3(256);
+        return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, RT, 8, 4>, g);
+    }
+    cfg.blockDim = dim3(512);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, RT, 16, D == 256 ? 4 : 10>, g);
 }
 
 }  // namespace
@@ -681,12 +692,11 @@ cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_at
         g.wait_ns = c.wait_limit_ns;
         const int64_t row_tiles = std::min((a.tokens * group + R - 1) / R + g.cache.batch,
                                            ((rows + R - 1) / R) * g.cache.batch);
-        const int64_t tiles_most = ((cache.pages_per_sequence * cache.page_size + kTile - 1) / kTile) *
-                                   row_tiles * cache.kv_heads;
+        const int64_t most = row_tiles * cache.kv_heads;  // heads' row tiles in the list
         switch (D) {
-            case 64: err = two ? launch<64, 2>(g, tiles_most, c) : launch<64, 1>(g, tiles_most, c); break;
-            case 128: err = two ? launch<128, 2>(g, tiles_most, c) : launch<128, 1>(g, tiles_most, c); break;
-            default: err = launch<256, 1>(g, tiles_most, c); break;
+            case 64: err = two ? launch<64, 2>(g, most, c) : launch<64, 1>(g, most, c); break;
+            case 128: err = two ? launch<128, 2>(g, most, c) : launch<128, 1>(g, most, c); break;
+            default: err = launch<256, 1>(g, most, c); break;
         }
     }
     return err;
