@@ -1,14 +1,15 @@
 // kv_append.cu -- keys and values appended to the paged 8-bit cache, keys rotated on the way.
 //
-// One CTA per (page that receives tokens, head, keys or values).  It holds the page's new
-// tokens in registers between the two steps of the quantisation (the largest |x|, then the
-// codes), so they are read once; each unit of a thread is eight channels of one token, and a
-// thread's units are eight consecutive tokens of the same channels, so that the transposed
-// values leave as eight consecutive bytes per channel.
+// Two kernels.  Prompts: one CTA per (page that receives tokens, head, keys or values).  It
+// holds the page's new tokens in registers between the two steps of the quantisation (the
+// largest |x|, then the codes), so they are read once; a thread's units are eight consecutive
+// tokens of the same eight channels, so that the transposed values leave as eight consecutive
+// bytes per channel.  Few tokens a sequence: one warp per (page, head, keys or values).
 //
 // Bound: memory traffic (size + 1 bytes per element) for prompts, the chain of dependent
-// loads (offset -> page -> old scale) for single tokens.  The old codes of a page are read
-// and written only where its scale grows.
+// loads (offset -> page -> old scale) for single tokens; what does not depend on the last
+// load is asked for with it.  The old codes of a page are read and written only where its
+// scale grows.
 #include "q4lin_internal.h"
 #include "serving.cuh"
 
@@ -22,108 +23,185 @@ struct AppendArgs {
     q4lin_kv_cache_t cache;
     q4lin_kv_append_t a;
     int page_shift;
-    int by_token;  // blockIdx.x counts tokens (few per sequence), else page slots
     int k_vec, v_vec;
     int* status;
 };
 
 // Page slots of sequence b: offsets[b] / page + 2 b up to the same of b + 1.  A sequence of
 // n tokens touches at most (n - 1) / page + 2 pages, which never exceeds that difference.
-__device__ __forceinline__ int64_t first_slot(const AppendArgs& g, int64_t b) {
-    return ((int64_t)__ldg(g.a.offsets + b) >> g.page_shift) + 2 * b;
+__device__ __forceinline__ int64_t first_slot(const AppendArgs& g, int64_t b, int64_t offset) {
+    return (offset >> g.page_shift) + 2 * b;
 }
 
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendArgs g) {
-    __shared__ float s_amax[THREADS / 32];
-    const q4lin_kv_cache_t& C = g.cache;
-    const int D = (int)C.head_dim, P = (int)C.page_size, units = D / 8;
-    const int h = blockIdx.y;
-    const bool keys = blockIdx.z == 0;
+// New tokens of one page: rows [first, first + n) of the call, positions from p0, slots [at,
+// at + n).  n is 0 where there are none.
+struct Share {
+    int64_t b, first, p0, column;
+    int at, n;
+};
 
-    // Which tokens: rows [first, first + n) of the call, slots [at, at + n) of their page.
-    int64_t b;
-    if (g.by_token) {
-        b = find_sequence(C.batch, blockIdx.x, [&](int64_t i) { return (int64_t)__ldg(g.a.offsets + i); });
-    } else {
-        b = find_sequence(C.batch, blockIdx.x, [&](int64_t i) { return first_slot(g, i); });
+// The share of page slot (or, by token, of the page that token opens for the call) `id`.  The
+// sequence is found by a 32-way search of the warp, which brings its three indices along.
+template <bool BY_TOKEN>
+__device__ __forceinline__ Share find_share(const AppendArgs& g, int64_t id) {
+    const int lane = threadIdx.x & 31, P = 1 << g.page_shift;
+    int64_t lo = 0, n = g.cache.batch, o0 = 0, o1 = 0, start = 0;
+    while (true) {
+        const int64_t step = (n + 31) / 32, b = lo + lane * step;
+        const bool in = lane * step < n;
+        const int64_t o = in ? __ldg(g.a.offsets + b) : 0;
+        const int next = in && step == 1 ? __ldg(g.a.offsets + b + 1) : 0;
+        const int st = in && step == 1 ? __ldg(g.a.starts + b) : 0;
+        const unsigned m = __ballot_sync(0xffffffffu, in && (BY_TOKEN ? o : first_slot(g, b, o)) <= id);
+        const int last = m ? 31 - __clz(m) : 0;
+        lo += last * step;
+        if (step == 1) {
+            o0 = __shfl_sync(0xffffffffu, (int)o, last), o1 = __shfl_sync(0xffffffffu, next, last);
+            start = __shfl_sync(0xffffffffu, st, last);
+            break;
+        }
+        n = n - last * step < step ? n - last * step : step;
     }
-    const int64_t o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1);
-    const int64_t start = __ldg(g.a.starts + b);
+    Share s = {lo, 0, 0, 0, 0, 0};
     if (o0 < 0 || o1 > g.a.tokens || start < 0) {
         if (threadIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
-        return;
+        return s;
     }
-    if (o1 <= o0) return;
     int64_t page0;  // first position of the page
-    if (g.by_token) {
-        const int64_t position = start + blockIdx.x - o0;
-        if (blockIdx.x < o0 || blockIdx.x >= o1) return;
-        if (blockIdx.x != o0 && (position & (P - 1)) != 0) return;  // another token's page
+    if (BY_TOKEN) {
+        if (id < o0 || id >= o1) return s;
+        const int64_t position = start + id - o0;
+        if (id != o0 && (position & (P - 1)) != 0) return s;  // another token's page
         page0 = position & ~(int64_t)(P - 1);
     } else {
-        const int64_t j = blockIdx.x - first_slot(g, b);
-        if (j < 0) return;
+        const int64_t j = id - first_slot(g, lo, o0);
+        if (j < 0) return s;
         page0 = ((start >> g.page_shift) + j) << g.page_shift;
     }
     const int64_t end = start + (o1 - o0);
-    if (page0 >= end) return;
-    const int64_t p0 = page0 > start ? page0 : start;             // first new position
-    const int64_t p1 = page0 + P < end ? page0 + P : end;         // past the last
-    const int at = (int)(p0 - page0), n = (int)(p1 - p0);
-    const int64_t first = o0 + (p0 - start);
-    const int64_t column = page0 >> g.page_shift;
-    const bool turn = keys && g.a.rope.cos != nullptr;
-    int64_t page = -1;
-    if (column < C.pages_per_sequence) page = __ldg(C.page_table + b * C.table_stride + column);
-    if (page < 0 || page >= C.num_pages || (turn && p1 > g.a.rope.positions)) {
+    if (page0 >= end) return s;
+    s.p0 = page0 > start ? page0 : start;                 // first new position
+    const int64_t p1 = page0 + P < end ? page0 + P : end;  // past the last
+    s.at = (int)(s.p0 - page0), s.n = p1 > s.p0 ? (int)(p1 - s.p0) : 0;
+    s.first = o0 + (s.p0 - start);
+    s.column = page0 >> g.page_shift;
+    return s;
+}
+// The share's page, -1 where its index or its positions are out of range.
+__device__ __forceinline__ int64_t page_of(const AppendArgs& g, const Share& s, bool keys) {
+    const q4lin_kv_cache_t& C = g.cache;
+    const int64_t page =
+        s.column < C.pages_per_sequence ? __ldg(C.page_table + s.b * C.table_stride + s.column) : -1;
+    const bool ok = page >= 0 && page < C.num_pages &&
+                    !(keys && g.a.rope.cos && s.p0 + s.n > g.a.rope.positions);
+    return ok ? page : -1;
+}
+
+// The page's scale from that of its earlier tokens (0: none) and the new tokens' largest |x|.
+__device__ __forceinline__ float new_scale(float s0, float amax) {
+    const float s = fmaxf(s0, __fmul_rn(amax, (float)(1.0 / 127.0)));
+    return s >= 1.17549435e-38f ? s : 0.f;
+}
+__device__ __forceinline__ void largest(const float (&x)[8], float& amax, bool& odd) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+        const float m = fabsf(x[d]);
+        const bool finite = m <= 3.4028235e38f;
+        amax = fmaxf(amax, finite ? m : 0.f);
+        odd |= !finite;
+    }
+}
+// Four codes.  x * inv may be an infinity (clamped) or a NaN (code 128).
+__device__ __forceinline__ uint32_t four_codes(const float* x, float inv) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const float y = rintf(__fmul_rn(x[d], inv));
+        const int c = y == y ? (int)fminf(fmaxf(y, -127.f), 127.f) : 0;
+        v |= (uint32_t)(c + 128) << (8 * d);
+    }
+    return v;
+}
+// Codes of the page's first `at` tokens, rounded again to a scale that is 1 / ratio larger: 16
+// bytes at a time, four in flight, by `count` threads of which this is number `id`.
+__device__ __forceinline__ void round_again(const AppendArgs& g, uint8_t* codes, bool keys, int at, float ratio,
+                                            int id, int count) {
+    const int D = (int)g.cache.head_dim, P = 1 << g.page_shift;
+    uint4* units = reinterpret_cast<uint4*>(codes);
+    const int all = keys ? at * D / 16 : D * P / 16;
+    for (int u0 = id; u0 < all; u0 += 4 * count) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (u0 + k * count < all) v[k] = units[u0 + k * count];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int u = u0 + k * count, slot = (16 * u) & (P - 1);  // values: of the first byte
+            if (u >= all || (!keys && slot >= at)) continue;
+            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t now = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = (int)((w[j] >> (8 * e)) & 0xFF);
+                    const bool held = keys || slot + 4 * j + e < at;
+                    const int r = (int)rintf(__fmul_rn((float)(c - 128), ratio)) + 128;
+                    now |= (uint32_t)(held ? r : c) << (8 * e);
+                }
+                w[j] = now;
+            }
+            units[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// Prompts: blockIdx.x is a page slot.
+template <int THREADS, int DT>
+__global__ void __launch_bounds__(THREADS) kv_append_pages_kernel(const AppendArgs g) {
+    __shared__ float s_amax[THREADS / 32];
+    const q4lin_kv_cache_t& C = g.cache;
+    const int D = (int)C.head_dim, units = D / 8, h = blockIdx.y;
+    const bool keys = blockIdx.z == 0;
+    const Share s = find_share<false>(g, blockIdx.x);
+    if (s.n == 0) return;
+    const int64_t page = page_of(g, s, keys);
+
+    // Thread (u, q): channels of unit u, slots 8 q .. 8 q + 7 of the page.
+    const int u = threadIdx.x % units, q = threadIdx.x / units;
+    const void* src = keys ? g.a.k : g.a.v;
+    const int64_t ts = keys ? g.a.k_token_stride : g.a.v_token_stride;
+    const int64_t at0 = s.first * ts + h * (keys ? g.a.k_head_stride : g.a.v_head_stride);
+    const bool vec = keys ? g.k_vec : g.v_vec;
+    bool turned = false;
+    int lo = 8 * u, hi = 8 * u + 4;
+    if (keys) rope_channels(g.a.rope, u, &turned, &lo, &hi);
+    float x[kUnits][8];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+        const int r = q * kUnits + i - s.at;  // new token
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[i][d] = 0.f;
+        if (r >= 0 && r < s.n) {
+            load_four(src, DT, at0 + r * ts + lo, vec, x[i]);
+            load_four(src, DT, at0 + r * ts + hi, vec, x[i] + 4);
+        }
+    }
+    if (page < 0) {
         if (threadIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
         return;
     }
     const int64_t head = page * C.kv_heads + h;
     uint8_t* codes = (keys ? C.k_codes : C.v_codes) + head * ((int64_t)D << g.page_shift);
     float* scale = (keys ? C.k_scales : C.v_scales) + head;
-    const float s0 = at > 0 ? *scale : 0.f;
-
-    // Thread (u, q): channels of unit u, slots 8 q .. 8 q + 7 of the page.
-    const int u = threadIdx.x % units, q = threadIdx.x / units;
-    const void* src = keys ? g.a.k : g.a.v;
-    const int64_t ts = keys ? g.a.k_token_stride : g.a.v_token_stride;
-    const int64_t hs = keys ? g.a.k_head_stride : g.a.v_head_stride;
-    const bool vec = keys ? g.k_vec : g.v_vec;
-    bool turned = false;
-    int lo = 8 * u, hi = 8 * u + 4;
-    if (keys) rope_channels(g.a.rope, u, &turned, &lo, &hi);
-    float x[kUnits][8];
+    const float s0 = s.at > 0 ? *scale : 0.f;
     float amax = 0.f;
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        const int r = q * kUnits + i - at;  // new token
-        const bool in = r >= 0 && r < n;
-        if (in) {
-            const int64_t e = (first + r) * ts + h * hs;
-            float a[4], c[4];
-            load_four(src, g.a.dtype, e + lo, vec, a);
-            load_four(src, g.a.dtype, e + hi, vec, c);
-#pragma unroll
-            for (int d = 0; d < 4; ++d) x[i][d] = a[d], x[i][4 + d] = c[d];
-        } else {
-#pragma unroll
-            for (int d = 0; d < 8; ++d) x[i][d] = 0.f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int r = q * kUnits + i - at;
-        if (turned && r >= 0 && r < n) rope_unit(g.a.rope, p0 + r, u, x[i]);
-#pragma unroll
-        for (int d = 0; d < 8; ++d) {
-            const float m = fabsf(x[i][d]);
-            const bool finite = m <= 3.4028235e38f;
-            amax = fmaxf(amax, finite ? m : 0.f);
-            odd |= !finite;
-        }
+        const int r = q * kUnits + i - s.at;
+        if (turned && r >= 0 && r < s.n) rope_unit(g.a.rope, s.p0 + r, u, x[i]);
+        largest(x[i], amax, odd);
     }
     if (__any_sync(0xffffffffu, odd) && (threadIdx.x & 31) == 0) atomicCAS(g.status, 0, kStatusNonFinite);
 #pragma unroll
@@ -132,61 +210,30 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendArgs g) 
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) amax = fmaxf(amax, s_amax[w]);
-    float s = fmaxf(s0, __fmul_rn(amax, (float)(1.0 / 127.0)));
-    if (!(s >= 1.17549435e-38f)) s = 0.f;
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    const float now = new_scale(s0, amax), inv = now > 0.f ? __frcp_rn(now) : 0.f;
     // (Every thread has read s0; the barrier above orders that before the store.)
-    if (threadIdx.x == 0) *scale = s;
-
-    if (s > s0 && s0 > 0.f) {
-        // Earlier tokens, rounded again to the larger scale, a word of codes at a time.
-        const float ratio = __fdiv_rn(s0, s);
-        uint32_t* words = reinterpret_cast<uint32_t*>(codes);
-        const int count = keys ? at * D / 4 : D << (g.page_shift - 2);
-        for (int w = threadIdx.x; w < count; w += THREADS) {
-            const int slot = (4 * w) & (P - 1);  // values: the slot of the word's first byte
-            if (!keys && slot >= at) continue;
-            const uint32_t old = words[w];
-            uint32_t now = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = (int)((old >> (8 * e)) & 0xFF);
-                const bool held = keys || slot + e < at;
-                const int r = (int)rintf(__fmul_rn((float)(c - 128), ratio)) + 128;
-                now |= (uint32_t)(held ? r : c) << (8 * e);
-            }
-            words[w] = now;
-        }
-        __syncthreads();  // before new codes are stored into the same words
+    if (threadIdx.x == 0) *scale = now;
+    if (now > s0 && s0 > 0.f) {
+        round_again(g, codes, keys, s.at, __fdiv_rn(s0, now), threadIdx.x, THREADS);
+        __syncthreads();  // before new codes are stored into the same 16 bytes
     }
 
-    // Codes.  x * inv may be an infinity (clamped) or a NaN (code 128).
     uint32_t code[kUnits][2];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            uint32_t v = 0;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const float y = rintf(__fmul_rn(x[i][4 * w + d], inv));
-                const int c = y == y ? (int)fminf(fmaxf(y, -127.f), 127.f) : 0;
-                v |= (uint32_t)(c + 128) << (8 * d);
-            }
-            code[i][w] = v;
-        }
+        code[i][0] = four_codes(x[i], inv), code[i][1] = four_codes(x[i] + 4, inv);
     if (keys) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int slot = q * kUnits + i, r = slot - at;
-            if (r < 0 || r >= n) continue;
+            const int slot = q * kUnits + i, r = slot - s.at;
+            if (r < 0 || r >= s.n) continue;
             *reinterpret_cast<uint32_t*>(codes + slot * D + lo) = code[i][0];
             *reinterpret_cast<uint32_t*>(codes + slot * D + hi) = code[i][1];
         }
         return;
     }
     const int slot0 = q * kUnits;
-    const bool whole = slot0 >= at && slot0 + kUnits <= at + n;
+    const bool whole = slot0 >= s.at && slot0 + kUnits <= s.at + s.n;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         if (whole) {
@@ -208,8 +255,8 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendArgs g) 
         } else {
 #pragma unroll
             for (int i = 0; i < kUnits; ++i) {
-                const int r = slot0 + i - at;
-                if (r < 0 || r >= n) continue;
+                const int r = slot0 + i - s.at;
+                if (r < 0 || r >= s.n) continue;
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
                     codes[(((w ? hi : lo) + d) << g.page_shift) + slot0 + i] =
@@ -219,9 +266,107 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(const AppendArgs g) 
     }
 }
 
+// Few tokens a sequence: blockIdx.x is a token; a warp takes a head's keys or values.
+constexpr int kTokenWarps = 4;
+template <int DT>
+__global__ void __launch_bounds__(32 * kTokenWarps) kv_append_tokens_kernel(const AppendArgs g) {
+    const q4lin_kv_cache_t& C = g.cache;
+    const int D = (int)C.head_dim, units = D / 8, per = 32 / units;  // tokens at a time
+    const int lane = threadIdx.x & 31, item = blockIdx.y * kTokenWarps + (threadIdx.x >> 5);
+    const int h = item >> 1;
+    const bool keys = (item & 1) == 0;
+    if (h >= C.kv_heads) return;
+    const Share s = find_share<true>(g, blockIdx.x);
+    if (s.n == 0) return;
+    const int64_t page = page_of(g, s, keys);
+    const int u = lane % units;
+    const void* src = keys ? g.a.k : g.a.v;
+    const int64_t ts = keys ? g.a.k_token_stride : g.a.v_token_stride;
+    const int64_t at0 = s.first * ts + h * (keys ? g.a.k_head_stride : g.a.v_head_stride);
+    const bool vec = keys ? g.k_vec : g.v_vec;
+    bool turned = false;
+    int lo = 8 * u, hi = 8 * u + 4;
+    if (keys) rope_channels(g.a.rope, u, &turned, &lo, &hi);
+    if (turned && s.p0 + s.n > g.a.rope.positions) turned = false;  // reported below
+    float x[8];
+    auto load = [&](int r0) {  // tokens r0 .. r0 + per - 1, rotated
+        const int r = r0 + lane / units;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[d] = 0.f;
+        if (r < s.n) {
+            float c[4], sn[4];
+            if (turned) rope_load(g.a.rope, s.p0 + r, u, c, sn);
+            load_four(src, DT, at0 + r * ts + lo, vec, x);
+            load_four(src, DT, at0 + r * ts + hi, vec, x + 4);
+            if (turned) rope_apply(g.a.rope, c, sn, x);
+        }
+    };
+    load(0);
+    if (page < 0) {
+        if (lane == 0) atomicCAS(g.status, 0, kStatusIndex);
+        return;
+    }
+    const int64_t head = page * C.kv_heads + h;
+    uint8_t* codes = (keys ? C.k_codes : C.v_codes) + head * ((int64_t)D << g.page_shift);
+    float* scale = (keys ? C.k_scales : C.v_scales) + head;
+    const float s0 = s.at > 0 ? *scale : 0.f;
+    float amax = 0.f;
+    bool odd = false;
+    largest(x, amax, odd);
+    for (int r0 = per; r0 < s.n; r0 += per) {
+        load(r0);
+        largest(x, amax, odd);
+    }
+    if (__any_sync(0xffffffffu, odd) && lane == 0) atomicCAS(g.status, 0, kStatusNonFinite);
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // not negative
+    const float now = new_scale(s0, amax), inv = now > 0.f ? __frcp_rn(now) : 0.f;
+    if (lane == 0) *scale = now;
+    if (now > s0 && s0 > 0.f) {
+        round_again(g, codes, keys, s.at, __fdiv_rn(s0, now), lane, 32);
+        __syncwarp();  // before new codes are stored into the same 16 bytes
+    }
+    for (int r0 = 0; r0 < s.n; r0 += per) {
+        if (s.n > per) load(r0);
+        const int r = r0 + lane / units, slot = s.at + r;
+        if (r >= s.n) continue;
+        const uint32_t a = four_codes(x, inv), b = four_codes(x + 4, inv);
+        if (keys) {
+            *reinterpret_cast<uint32_t*>(codes + slot * D + lo) = a;
+            *reinterpret_cast<uint32_t*>(codes + slot * D + hi) = b;
+        } else {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                codes[((lo + d) << g.page_shift) + slot] = (uint8_t)(a >> (8 * d));
+                codes[((hi + d) << g.page_shift) + slot] = (uint8_t)(b >> (8 * d));
+            }
+        }
+    }
+}
+
 bool vector_rows(const void* p, int dtype, int64_t token_stride, int64_t head_stride) {
     return reinterpret_cast<uintptr_t>(p) % (4 * dtype_size(dtype)) == 0 && token_stride % 4 == 0 &&
            head_stride % 4 == 0;
+}
+
+template <int DT>
+cudaError_t launch(const AppendArgs& g, cudaStream_t stream) {
+    // A warp per token and head (of which those that do not open a page's share leave at once)
+    // or a CTA per page slot and head, whichever are fewer.
+    const int64_t slots = g.a.tokens / g.cache.page_size + 2 * g.cache.batch;
+    if (g.a.tokens <= slots) {
+        const dim3 grid((unsigned)g.a.tokens, (unsigned)((2 * g.cache.kv_heads + kTokenWarps - 1) / kTokenWarps));
+        kv_append_tokens_kernel<DT><<<grid, 32 * kTokenWarps, 0, stream>>>(g);
+        return cudaGetLastError();
+    }
+    const dim3 grid((unsigned)slots, (unsigned)g.cache.kv_heads, 2);
+    const int64_t threads = g.cache.head_dim / 8 * (g.cache.page_size / kUnits);
+    if (threads <= 64)
+        kv_append_pages_kernel<64, DT><<<grid, 64, 0, stream>>>(g);
+    else if (threads <= 128)
+        kv_append_pages_kernel<128, DT><<<grid, 128, 0, stream>>>(g);
+    else
+        kv_append_pages_kernel<256, DT><<<grid, 256, 0, stream>>>(g);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -235,19 +380,11 @@ cudaError_t kv_append_launch(const q4lin_kv_cache_t& cache, const q4lin_kv_appen
     g.k_vec = vector_rows(a.k, a.dtype, a.k_token_stride, a.k_head_stride);
     g.v_vec = vector_rows(a.v, a.dtype, a.v_token_stride, a.v_head_stride);
     g.status = c.status_word;
-    // One CTA per token that opens a page's share (every token is looked at), or per page
-    // slot, whichever are fewer.
-    const int64_t slots = a.tokens / cache.page_size + 2 * cache.batch;
-    g.by_token = a.tokens <= slots;
-    const dim3 grid((unsigned)(g.by_token ? a.tokens : slots), (unsigned)cache.kv_heads, 2);
-    const int64_t threads = cache.head_dim / 8 * (cache.page_size / kUnits);
-    if (threads <= 64)
-        kv_append_kernel<64><<<grid, 64, 0, c.stream>>>(g);
-    else if (threads <= 128)
-        kv_append_kernel<128><<<grid, 128, 0, c.stream>>>(g);
-    else
-        kv_append_kernel<256><<<grid, 256, 0, c.stream>>>(g);
-    return cudaGetLastError();
+    switch (a.dtype) {
+        case Q4LIN_DTYPE_F32: return launch<Q4LIN_DTYPE_F32>(g, c.stream);
+        case Q4LIN_DTYPE_F16: return launch<Q4LIN_DTYPE_F16>(g, c.stream);
+        default: return launch<Q4LIN_DTYPE_BF16>(g, c.stream);
+    }
 }
 
 }  // namespace q4lin
