@@ -102,25 +102,35 @@ __device__ __forceinline__ float new_scale(float s0, float amax) {
     const float s = fmaxf(s0, __fmul_rn(amax, (float)(1.0 / 127.0)));
     return s >= 1.17549435e-38f ? s : 0.f;
 }
-__device__ __forceinline__ void largest(const float (&x)[8], float& amax, bool& odd) {
+// Largest |x|, and whether all are finite: 0 x is 0 only then.
+__device__ __forceinline__ void largest(const float (&x)[8], float& amax, float& zero) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) amax = fmaxf(amax, fabsf(x[d])), zero = fmaf(x[d], 0.f, zero);
+}
+__device__ __forceinline__ float largest_finite(const float (&x)[8], float amax) {
 #pragma unroll
     for (int d = 0; d < 8; ++d) {
         const float m = fabsf(x[d]);
-        const bool finite = m <= 3.4028235e38f;
-        amax = fmaxf(amax, finite ? m : 0.f);
-        odd |= !finite;
+        amax = m <= 3.4028235e38f ? fmaxf(amax, m) : amax;
     }
+    return amax;
 }
-// Four codes.  x * inv may be an infinity (clamped) or a NaN (code 128).
-__device__ __forceinline__ uint32_t four_codes(const float* x, float inv) {
-    uint32_t v = 0;
+// Four codes.  Finite x: |x inv| rounds to 127 at most, and adding 1.5 2^23 + 128 rounds it to a
+// whole number, half to even, whose low byte is the code.  Else x inv may be an infinity
+// (clamped) or a NaN (code 128).
+__device__ __forceinline__ uint32_t four_codes(const float* x, float inv, bool finite) {
+    uint32_t c[4];
+    if (finite) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const float y = rintf(__fmul_rn(x[d], inv));
-        const int c = y == y ? (int)fminf(fmaxf(y, -127.f), 127.f) : 0;
-        v |= (uint32_t)(c + 128) << (8 * d);
+        for (int d = 0; d < 4; ++d) c[d] = __float_as_uint(__fadd_rn(__fmul_rn(x[d], inv), 12583040.f));
+    } else {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const float y = __fmul_rn(x[d], inv);
+            c[d] = y == y ? (uint32_t)((int)fminf(fmaxf(rintf(y), -127.f), 127.f) + 128) : 128u;
+        }
     }
-    return v;
+    return ptx::prmt(ptx::prmt(c[0], c[1], 0x0040u), ptx::prmt(c[2], c[3], 0x0040u), 0x5410u);
 }
 // Codes of the page's first `at` tokens, rounded again to a scale that is 1 / ratio larger: 16
 // bytes at a time, four in flight, by `count` threads of which this is number `id`.
@@ -195,17 +205,21 @@ __global__ void __launch_bounds__(THREADS) kv_append_pages_kernel(const AppendAr
     uint8_t* codes = (keys ? C.k_codes : C.v_codes) + head * ((int64_t)D << g.page_shift);
     float* scale = (keys ? C.k_scales : C.v_scales) + head;
     const float s0 = s.at > 0 ? *scale : 0.f;
-    float amax = 0.f;
-    bool odd = false;
+    float amax = 0.f, zero = 0.f;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const int r = q * kUnits + i - s.at;
         if (turned && r >= 0 && r < s.n) rope_unit(g.a.rope, s.p0 + r, u, x[i]);
-        largest(x[i], amax, odd);
+        largest(x[i], amax, zero);
     }
-    if (__any_sync(0xffffffffu, odd) && (threadIdx.x & 31) == 0) atomicCAS(g.status, 0, kStatusNonFinite);
+    const bool finite = !__syncthreads_or(zero != 0.f);
+    if (!finite) {
+        if (threadIdx.x == 0) atomicCAS(g.status, 0, kStatusNonFinite);
+        amax = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int i = 0; i < kUnits; ++i) amax = largest_finite(x[i], amax);
+    }
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // not negative
     if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
     __syncthreads();
 #pragma unroll
@@ -221,7 +235,7 @@ __global__ void __launch_bounds__(THREADS) kv_append_pages_kernel(const AppendAr
     uint32_t code[kUnits][2];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-        code[i][0] = four_codes(x[i], inv), code[i][1] = four_codes(x[i] + 4, inv);
+        code[i][0] = four_codes(x[i], inv, finite), code[i][1] = four_codes(x[i] + 4, inv, finite);
     if (keys) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
@@ -310,14 +324,21 @@ __global__ void __launch_bounds__(32 * kTokenWarps) kv_append_tokens_kernel(cons
     uint8_t* codes = (keys ? C.k_codes : C.v_codes) + head * ((int64_t)D << g.page_shift);
     float* scale = (keys ? C.k_scales : C.v_scales) + head;
     const float s0 = s.at > 0 ? *scale : 0.f;
-    float amax = 0.f;
-    bool odd = false;
-    largest(x, amax, odd);
+    float amax = 0.f, zero = 0.f;
+    largest(x, amax, zero);
     for (int r0 = per; r0 < s.n; r0 += per) {
         load(r0);
-        largest(x, amax, odd);
+        largest(x, amax, zero);
     }
-    if (__any_sync(0xffffffffu, odd) && lane == 0) atomicCAS(g.status, 0, kStatusNonFinite);
+    const bool finite = !__any_sync(0xffffffffu, zero != 0.f);
+    if (!finite) {
+        if (lane == 0) atomicCAS(g.status, 0, kStatusNonFinite);
+        amax = 0.f;
+        for (int r0 = 0; r0 < s.n; r0 += per) {
+            if (s.n > per) load(r0);
+            amax = largest_finite(x, amax);
+        }
+    }
     amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // not negative
     const float now = new_scale(s0, amax), inv = now > 0.f ? __frcp_rn(now) : 0.f;
     if (lane == 0) *scale = now;
@@ -329,7 +350,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps) kv_append_tokens_kernel(cons
         if (s.n > per) load(r0);
         const int r = r0 + lane / units, slot = s.at + r;
         if (r >= s.n) continue;
-        const uint32_t a = four_codes(x, inv), b = four_codes(x + 4, inv);
+        const uint32_t a = four_codes(x, inv, finite), b = four_codes(x + 4, inv, finite);
         if (keys) {
             *reinterpret_cast<uint32_t*>(codes + slot * D + lo) = a;
             *reinterpret_cast<uint32_t*>(codes + slot * D + hi) = b;
