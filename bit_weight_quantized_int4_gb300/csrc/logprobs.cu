@@ -6,9 +6,10 @@
 //
 // One pass keeps, per thread, m = the largest entry so far, l = sum e^(x - m) and
 // t = sum e^(x - m) (x - m): lse = m + ln l, entropy = ln l - t / l.  The top entries cost
-// nothing on the way: of 32 groups of threads, the k-th largest of the groups' maxima bounds
-// the k-th largest entry from below, and only threads whose maximum reaches that bound (about
-// 32 ln(32 / (32 - k)) of the 512 in a row in no order) look at their entries again, from L2.
+// little on the way: each thread notes the maxima of eight stretches of its entries; of 32
+// groups of stretches, the k-th largest of the groups' maxima bounds the k-th largest entry
+// from below, and only stretches whose maximum reaches that bound (about 32 ln(32 / (32 - k))
+// of 2048 in a row in no order) are looked at again, from L2.
 #include <algorithm>
 
 #include "q4lin_internal.h"
@@ -18,10 +19,12 @@ namespace q4lin {
 namespace {
 using namespace serving;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kCtas = 4;  // per SM
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
-constexpr int kMaxSplits = 64;
+constexpr int kStretches = 8;
+constexpr int kMaxSplits = 32;
 // Stands in for differences x - m below it (a mask's lowest value, -infinity): its exponential
 // is 0 in fp32 as theirs is, and its products with sums stay finite.
 constexpr float kNegative = -1.0e4f;
@@ -89,7 +92,7 @@ struct Vec {
 };
 
 // A CTA's entries [begin, end) of a row: `head` single ones up to a 16-byte boundary, then
-// vectors, then single ones.  Thread i takes single entry i, and vectors i, i + 512, ...
+// vectors, then single ones.  Thread i takes single entry i, and vectors i, i + kThreads, ...
 template <int DT>
 struct Span {
     const void* row;
@@ -111,12 +114,13 @@ struct Span {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LpArgs g) {
-    constexpr int N = Vec<DT>::N, kAhead = 4;
+__global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LpArgs g) {
+    constexpr int N = Vec<DT>::N, kAhead = DT == Q4LIN_DTYPE_F32 ? 4 : 2;  // 16 entries a round
     constexpr int kCandidates = 2048;
     __shared__ unsigned long long s_cand[kCandidates], s_key[kMaxSplits], s_thr, s_top[kMaxTop];
-    __shared__ float s_m[kWarps], s_l[kWarps], s_t[kWarps], s_mx[kThreads];
-    __shared__ int s_owner[kThreads], s_owners, s_above, s_ties, s_last;
+    __shared__ float s_bound, s_m[kWarps], s_l[kWarps], s_t[kWarps], s_mx[kStretches][kThreads];
+    __shared__ unsigned short s_owner[kStretches * kThreads];
+    __shared__ int s_owners, s_above, s_ties, s_last;
     const int64_t row = blockIdx.x / g.splits;
     const int split = (int)(blockIdx.x % g.splits);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = (int)g.a.top;
@@ -139,18 +143,35 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LpArgs g) {
         l += e;
         t = fmaf(e, d, t);
     };
-    for (int64_t v = tid; v < span.vecs; v += kThreads * kAhead) {
-        float x[kAhead][N];
+    // A round's vectors are asked for while the round before is added.
+    float ahead[kAhead][N];
+    auto load = [&](int64_t v) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int64_t at = v + i * kThreads;
             if (at < span.vecs) {
-                Vec<DT>::load(base, span.vec0 + at * N, x[i]);
+                Vec<DT>::load(base, span.vec0 + at * N, ahead[i]);
             } else {
 #pragma unroll
-                for (int e = 0; e < N; ++e) x[i][e] = -INFINITY;
+                for (int e = 0; e < N; ++e) ahead[i][e] = -INFINITY;
             }
         }
+    };
+    // A stretch: `per` rounds of a thread.
+    const int rounds = (int)((span.vecs + kThreads * kAhead - 1) / (kThreads * kAhead));
+    const int per = max(1, (rounds + kStretches - 1) / kStretches);
+    float stretch = -INFINITY, *note = &s_mx[0][tid];
+    int left = per;
+#pragma unroll
+    for (int i = 0; i < kStretches; ++i) s_mx[i][tid] = -INFINITY;
+    load(tid);
+    for (int64_t v = tid; v < span.vecs; v += kThreads * kAhead) {
+        float x[kAhead][N];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[i][e] = ahead[i][e];
+        load(v + kThreads * kAhead);
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
@@ -166,17 +187,20 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LpArgs g) {
 #pragma unroll
                 for (int e = 0; e < N; ++e) add(x[i][e]);
         }
+        stretch = fmaxf(stretch, top);
+        if (--left == 0) *note = stretch, note += kThreads, left = per, stretch = -INFINITY;
     }
+    if (left < per) *note = stretch;
     if (tid < span.singles()) {
         const float x = load_one(base, DT, span.single(tid));
         nan |= x != x;
         if (x > m) rescale(x);
         if (m != -INFINITY) add(x);
+        s_mx[0][tid] = fmaxf(s_mx[0][tid], x);  // single entries count with the first stretch
     }
     const bool any_nan = __syncthreads_or(nan);
 
     // ---- the CTA's m, l, t
-    s_mx[tid] = m;
     float rm = m, rl = l, rt = t;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -194,30 +218,39 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LpArgs g) {
     // ---- the CTA's `mine` largest entries (it may hold fewer than K)
     const int mine = (int)min((int64_t)K, span.end - span.begin);
     if (K > 0) {
-        // The bound: group = lane, over the 16 warps.
-        float group = s_mx[lane];
+        // The bound: group = lane, over the warps and stretches.
+        if (warp == 0) {
+            float group = -INFINITY;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) group = fmaxf(group, s_mx[w * 32 + lane]);
-        int rank = 0;
+            for (int i = 0; i < kStretches; ++i)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float other = __shfl_sync(0xffffffffu, group, i);
-            rank += other > group || (other == group && i < lane);
+                for (int w = 0; w < kWarps; ++w) group = fmaxf(group, s_mx[i][w * 32 + lane]);
+            int rank = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float other = __shfl_sync(0xffffffffu, group, i);
+                rank += other > group || (other == group && i < lane);
+            }
+            if (rank == mine - 1) s_bound = group;
         }
-        const unsigned holder = __ballot_sync(0xffffffffu, rank == mine - 1);
-        const float bound = __shfl_sync(0xffffffffu, group, __ffs(holder) - 1);
-        if (m >= bound) s_owner[atomicAdd(&s_owners, 1)] = tid;
+        __syncthreads();
+        const float bound = s_bound;
+#pragma unroll
+        for (int i = 0; i < kStretches; ++i)
+            if (s_mx[i][tid] >= bound) s_owner[atomicAdd(&s_owners, 1)] = (unsigned short)(i * kThreads + tid);
         __syncthreads();
         const int owners = s_owners;
-        const int depth = (int)((span.vecs + kThreads - 1) / kThreads) + 1;  // vectors, and a single
+        const int depth = per * kAhead + 1;  // vectors of a stretch, and a single entry
         // Every entry x (at index `at`) of the owners, in no order.
         auto owned = [&](auto&& f) {
+#pragma unroll 2
             for (int i = tid; i < owners * depth; i += kThreads) {
-                const int o = s_owner[i % owners], r = i / owners;
+                const int r = i / owners, o = s_owner[i - r * owners], th = o % kThreads, st = o / kThreads;
+                const int64_t v = th + ((int64_t)st * per * kAhead + r) * kThreads;
                 if (r == depth - 1) {
-                    if (o < span.singles()) f(load_one(base, DT, span.single(o)), span.single(o));
-                } else if (o + (int64_t)r * kThreads < span.vecs) {
-                    const int64_t at = span.vec0 + (o + (int64_t)r * kThreads) * N;
+                    if (st == 0 && th < span.singles()) f(load_one(base, DT, span.single(th)), span.single(th));
+                } else if (v < span.vecs) {
+                    const int64_t at = span.vec0 + v * N;
                     float x[N];
                     Vec<DT>::load(base, at, x);
 #pragma unroll
@@ -300,9 +333,19 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const LpArgs g) {
         }
         __syncthreads();
         if (!s_last) return;
+        // By every warp alike: a lane per part, then the lanes are joined.
+        static_assert(kMaxSplits <= 32, "a lane each");
         rm = -INFINITY, rl = rt = 0.f;
-        for (int s = 0; s < g.splits; ++s)  // in order, by every thread alike
-            join(rm, rl, rt, __ldcg(&parts[s].m), __ldcg(&parts[s].l), __ldcg(&parts[s].t));
+        if (lane < g.splits) {
+            const LpPart* p = parts + lane;
+            rm = __ldcg(&p->m), rl = __ldcg(&p->l), rt = __ldcg(&p->t);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, rm, o), l2 = __shfl_xor_sync(0xffffffffu, rl, o),
+                        t2 = __shfl_xor_sync(0xffffffffu, rt, o);
+            join(rm, rl, rt, m2, l2, t2);
+        }
         if (K > 0) {
             // The K-th largest of the CTAs' maxima bounds from below, as above; lists of at
             // most kMaxSplits * kMaxTop keys fit the candidates.
@@ -366,7 +409,7 @@ struct LbArgs {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_backward_kernel(const LbArgs g) {
+__global__ void __launch_bounds__(kThreads, kCtas) logprobs_backward_kernel(const LbArgs g) {
     constexpr int N = Vec<DT>::N, kAhead = DT == Q4LIN_DTYPE_F32 ? 4 : 2;
     constexpr int size = (int)dtype_size(DT);
     const int64_t row = blockIdx.x / g.splits;
@@ -444,11 +487,14 @@ cudaError_t logprobs_launch(const q4lin_logprobs_t& a, const LaunchCtx& c) {
     g.ws = c.ws;
     g.tickets = c.tickets;
     g.status = c.status_word;
-    // Rows that fill the GPU by themselves are not cut (and then need neither workspace nor
-    // tickets, whose number the cut rows stay far below).
-    g.splits = a.rows >= 2 * c.sm_count
-                   ? 1
-                   : splits_for(a.rows, a.vocabulary, 2 * c.sm_count, 2 * kThreads, kMaxSplits);
+    // CTAs per row.  A cut costs a join of 2 to 3 us and the time after the entries once more; it
+    // pays on long rows while they are too few for the SMs (128256 fp32 entries, 20 alternatives,
+    // us for 1 / 2 / 4 / 32 CTAs a row: 1 row 15.8 / 13.6 / 10.9 / 9.5, 32 rows 16.5 / 14.6 /
+    // 11.7 / 17.8, 100 rows 17.2 / 18.6 / 16.8 / 40, 300 rows 35.3 / 33.5 / 43 / 109, 400 rows
+    // 40.2 / 56.6; 32000 entries, 1 row: 7.6 / 9.1).
+    g.splits = 1;
+    if (a.vocabulary >= 65536 && a.rows < 2 * c.sm_count)
+        g.splits = a.rows <= 8 ? kMaxSplits : (int)std::min<int64_t>(4, (400 + a.rows - 1) / a.rows);
     g.chunk = ((a.vocabulary + g.splits - 1) / g.splits + 7) / 8 * 8;
     g.splits = (int)((a.vocabulary + g.chunk - 1) / g.chunk);
     const int64_t grid = a.rows * g.splits;
@@ -464,7 +510,7 @@ cudaError_t logprobs_backward_launch(const q4lin_logprobs_backward_t& a, const L
     LbArgs g;
     g.a = a;
     g.status = c.status_word;
-    g.splits = splits_for(a.rows, a.vocabulary, 8 * c.sm_count, 4 * kThreads, 1 << 20);
+    g.splits = splits_for(a.rows, a.vocabulary, 16 * c.sm_count, 8 * kThreads, 1 << 20);
     g.chunk = ((a.vocabulary + g.splits - 1) / g.splits + 7) / 8 * 8;
     g.splits = (int)((a.vocabulary + g.chunk - 1) / g.chunk);
     const int64_t grid = a.rows * g.splits;
