@@ -20,6 +20,9 @@
 // weight of a bf16 output takes one (its 11 bits are finer than the output's 8), and bf16
 // queries that are not rotated are exact in one.
 //
+// Few rows over many keys leave SMs idle: their walks over the keys are then cut into equal
+// parts, one CTA each, that a second kernel joins in the order of the keys.
+//
 // Bound: the products (4 head_dim flops a pair and term) together with the exponentials
 // (16 a clock and SM against 128 x 128 products in 8 clocks).
 #include <algorithm>
@@ -41,7 +44,8 @@ constexpr int kWarps = 20, kThreads = 32 * kWarps;
 // Registers of their threads: launched with 96 each.
 constexpr int kSoftRegs = 176, kWidenRegs = 48, kIssueRegs = 32;
 static_assert(2 * kSoftRegs + 2 * kWidenRegs + kIssueRegs <= 5 * 96, "registers of the launch");
-constexpr int kScaleSlots = 6;  // steps whose scales are kept: the widening warps are up to four ahead
+constexpr int kMaxBatch = 1024;  // sequences per launch
+constexpr int kScaleSlots = 5;  // steps whose scales are kept: the widening warps are up to four ahead
 constexpr float kBase = 7.f;    // weights are kept as 2^7 p ...
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
 // A score's factor is at least this, so that a masked score (-infinity) stays one.
@@ -57,9 +61,42 @@ struct PromptArgs {
     int page_shift;
     int64_t rows_min;  // sequences of more rows than this per key/value head are taken
     int q_vec;
+    int slots, most_parts;  // CTAs that run at a time; parts of a walk at most
+    float* parts;           // [unit][2 kQ (D + 2)]: unfinished walks
+    int* list;              // [batch + 3]: parts, steps of each, pairs, where a sequence's begin
     int* status;
     int64_t wait_ns;
 };
+
+// What one sequence asks of this kernel.
+struct Prompt {
+    int tq, len, pairs;  // pairs of row tiles
+    bool bad;
+};
+__device__ __forceinline__ Prompt prompt_of(const PromptArgs& g, int64_t b) {
+    const int64_t o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1), len = __ldg(g.a.lengths + b);
+    const int64_t rows = (o1 - o0) * (g.a.heads / g.cache.kv_heads);
+    Prompt p;
+    p.bad = o0 < 0 || o1 < o0 || o1 > g.a.tokens || o1 - o0 > g.a.max_query ||
+            len > g.cache.pages_per_sequence << g.page_shift || (g.a.rope.cos && len > g.a.rope.positions);
+    p.tq = (int)(o1 - o0), p.len = (int)(len > 0 ? len : 0);
+    p.pairs = !p.bad && rows > g.rows_min ? (int)((rows + 2 * kQ - 1) / (2 * kQ)) : 0;
+    return p;
+}
+// The steps over keys of a pair of row tiles: 128 first .. 128 last - 1.
+__device__ __forceinline__ void walk_of(const PromptArgs& g, const Prompt& p, int pair, int* first, int* last) {
+    const int group = (int)(g.a.heads / g.cache.kv_heads), rows = p.tq * group, row0 = pair * 2 * kQ;
+    const int first_pos = p.len - p.tq + row0 / group;
+    const int last_pos = p.len - p.tq + (min(rows, row0 + 2 * kQ) - 1) / group;
+    const int last_key = g.a.causal ? last_pos : p.len - 1;
+    const int64_t low = g.a.window > 0 ? (int64_t)first_pos - g.a.window + 1 : 0;
+    *first = low > 0 ? (int)(low / kKeys) : 0;
+    *last = last_key < 0 || p.len == 0 ? *first : max(*first, last_key / kKeys + 1);
+}
+template <int D>
+__device__ __forceinline__ float* part_at(const PromptArgs& g, int64_t unit) {
+    return g.parts + unit * (2 * kQ * (D + 2));
+}
 
 // Shared memory.  A step's K tile is D / 64 blocks of 64 channels, its V tile two blocks of 64
 // keys; both come and go by block through rings, as much as fits (three of each beside 128
@@ -76,13 +113,21 @@ struct Layout {
     static constexpr uint32_t bytes = v + vRing * vBlock;
 };
 
+// What a CTA does, left in shared memory by its prologue: the warpgroups read what each needs
+// into its own registers (values kept across their register shares are spilled, and the issuing
+// warp then waits for local memory behind the codes' loads: 351 against 243 us).
+struct Job {
+    int64_t o0;
+    int b, tq, len, row0, row_end, step0, n, cut;
+};
+
 struct PromptShared {
+    Job job;
     float factor[2 * kQ];
     float k_scale[kScaleSlots][8], v_log[kScaleSlots][8], v_inv[kScaleSlots][8];  // of 16 keys each
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2];
     float v_max[kWarps];
-    int sums[kWarps];
-    int found_b, found_tile, failed;
+    int failed;
     uint32_t tmem;
 };
 
@@ -167,6 +212,67 @@ __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
     return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
+// One CTA, before the prompts' kernel: which pairs there are, and in how many parts their walks
+// are cut.
+constexpr int kPlanThreads = 256;
+__global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(const PromptArgs g, int units_most) {
+    __shared__ int s_longest[kPlanThreads / 32], s_scan[kPlanThreads / 32];
+    griddep_launch_dependents();  // (the prompts' kernel waits for this one's end)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int Hkv = (int)g.cache.kv_heads, group = (int)(g.a.heads / g.cache.kv_heads);
+    int pairs = 0, longest = 0;
+    for (int64_t b0 = 0; b0 < g.cache.batch; b0 += kPlanThreads) {
+        const int64_t b = b0 + tid;
+        int sum = 0;
+        if (b < g.cache.batch) {
+            const Prompt p = prompt_of(g, b);
+            if (p.bad) atomicCAS(g.status, 0, kStatusIndex);
+            sum = p.pairs;
+            if (p.pairs) {
+                int first, last;
+                walk_of(g, p, p.pairs - 1, &first, &last);
+                // Without a window the last pair's walk is the longest; with one, none is longer
+                // than this.
+                const int64_t window = (g.a.window + 2 * kQ / group + kKeys) / kKeys + 1;
+                const int most = g.a.window > 0 ? (int)min((int64_t)p.len / kKeys + 1, window) : last - first;
+                longest = max(longest, most);
+            }
+        }
+        const int own = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += n;
+        }
+        __syncthreads();
+        if (lane == 31) s_scan[warp] = sum;
+        __syncthreads();
+        int before = pairs;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            if (w < warp) before += s_scan[w];
+            pairs += s_scan[w];
+        }
+        if (b < g.cache.batch) g.list[3 + b] = before + sum - own;
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) s_longest[warp] = longest;
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 0; w < kPlanThreads / 32; ++w) longest = max(longest, s_longest[w]);
+    // Walks in `parts` parts of `each` steps where whole ones leave SMs idle: the least rounds of
+    // CTAs times their steps, with 4 more for what comes before and after, 3 for a join.  Lane i
+    // weighs i + 1 and i + 33 parts.
+    uint32_t best = 0xFFFFFFFFu;
+    for (int n = lane + 1; n <= g.most_parts; n += 32) {
+        const int64_t units = (int64_t)n * pairs * Hkv;
+        if (n > 1 && units > units_most) break;
+        const int64_t cost = (units + g.slots - 1) / g.slots * ((longest + n - 1) / n + (n > 1 ? 7 : 4));
+        best = min(best, (uint32_t)min(cost, (int64_t)0x3FFFFFF) << 6 | (uint32_t)(n - 1));
+    }
+    const int parts = (int)(__reduce_min_sync(0xffffffffu, best) & 63u) + 1;
+    if (lane == 0) g.list[0] = parts, g.list[1] = max(1, (longest + parts - 1) / parts), g.list[2] = pairs;
+}
+
 template <int D, int QT, int PT>
 __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const PromptArgs g) {
     using L = Layout<D, QT>;
@@ -178,57 +284,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, ps = g.page_shift;
     const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads);
     const int h = (int)(blockIdx.x % Hkv);
-    const int64_t want = blockIdx.x / Hkv;  // which tile pair of the whole call
-
-    // ---- the CTA's sequence and tile pair: a scan over the sequences
-    if (tid == 0) S.found_b = -1, S.failed = 0;
-    int64_t carry = 0;
-    for (int64_t b0 = 0; b0 < C.batch; b0 += kThreads) {
-        const int64_t b = b0 + tid;
-        int v = 0;
-        if (b < C.batch) {
-            const int64_t o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1);
-            const int64_t len = __ldg(g.a.lengths + b), rows = (o1 - o0) * group;
-            const bool bad = o0 < 0 || o1 < o0 || o1 > g.a.tokens || o1 - o0 > g.a.max_query ||
-                             len > C.pages_per_sequence << ps || (g.a.rope.cos && len > g.a.rope.positions);
-            if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
-            if (!bad && rows > g.rows_min) v = (int)((rows + 2 * kQ - 1) / (2 * kQ));
-        }
-        int sum = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += n;
-        }
-        __syncthreads();
-        if (lane == 31) S.sums[warp] = sum;
-        __syncthreads();
-        int64_t before = carry;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += S.sums[w];
-            carry += S.sums[w];
-        }
-        before += sum - v;
-        if (v && want >= before && want < before + v) {
-            S.found_b = (int)b;
-            S.found_tile = (int)(v - 1 - (want - before));  // the longest walks first
-        }
-    }
-    __syncthreads();
-    if (S.found_b < 0) return;
-    const int64_t b = S.found_b;
+    griddep_launch_dependents();  // (the joining kernel waits for this one's end)
+    griddep_wait();               // for the plan
+    {
+    const int parts = __ldcg(g.list), each = __ldcg(g.list + 1);
+    const int64_t pair = blockIdx.x / Hkv / parts;  // of the whole call
+    if (pair >= __ldcg(g.list + 2)) return;
+    const int part = (int)(blockIdx.x / Hkv) % parts;
+    const int64_t b = find_sequence(C.batch, pair, [&](int64_t i) { return (int64_t)__ldcg(g.list + 3 + i); });
+    const Prompt prompt = prompt_of(g, b);
+    // The longest walks first.
+    const int tile = prompt.pairs - 1 - (int)(pair - __ldcg(g.list + 3 + b));
+    if (tid == 0) S.failed = 0;
     const int64_t o0 = __ldg(g.a.offsets + b);
-    const int tq = (int)(__ldg(g.a.offsets + b + 1) - o0), len = max(__ldg(g.a.lengths + b), 0);
-    const int rows = tq * group, row0 = S.found_tile * 2 * kQ;
+    const int tq = prompt.tq, len = prompt.len;
+    const int rows = tq * group, row0 = tile * 2 * kQ;
     const int row_end = min(rows, row0 + 2 * kQ);
-    const bool two = row_end - row0 > kQ;
-    // Steps over keys [128 step0, 128 step1).
-    const int first_pos = len - tq + row0 / group, last_pos = len - tq + (row_end - 1) / group;
-    const int last_key = g.a.causal ? last_pos : len - 1;
-    const int64_t low64 = g.a.window > 0 ? (int64_t)first_pos - g.a.window + 1 : 0;
-    const int step0 = low64 > 0 ? (int)(low64 / kKeys) : 0;
-    const int step1 = last_key < 0 || len == 0 ? step0 : max(step0, last_key / kKeys + 1);
+    int step0, step1;
+    walk_of(g, prompt, tile, &step0, &step1);
+    step0 = min(step0 + part * each, step1), step1 = min(step0 + each, step1);
     const int n = step1 - step0;
+    if (n == 0 && part > 0) return;  // a shorter walk has fewer parts
+    if (tid == 0) S.job = {o0, (int)b, tq, len, row0, row_end, step0, n, parts > 1};
     const int32_t* table = C.page_table + b * C.table_stride;
     const int pages = (len + (1 << ps) - 1) >> ps;
 
@@ -307,16 +384,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             }
         }
     }
+    }
     fence_async_shared();  // the queries are read by the tensor cores
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     // All of the SM's tensor memory is this CTA's, so it begins at 0.
     constexpr uint32_t tmem = 0;
-    float v_ref = 0.f;
+    const volatile Job& job = S.job;
+    auto value_ref = [&]() {  // the largest value scale of the walk
+        float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v_ref = fmaxf(v_ref, S.v_max[w]);
-    if (!(v_ref > 0.f)) v_ref = 1.f;  // values that are all zero
+        for (int w = 0; w < kWarps; ++w) v = fmaxf(v, const_cast<volatile float&>(S.v_max[w]));
+        return v > 0.f ? v : 1.f;  // 1: values that are all zero
+    };
     volatile int* failed = &S.failed;
     auto bar = [](uint64_t& x) { return smem_u32(&x); };
     // In line (a call would tie the warpgroups' registers together), bounded as everywhere.
@@ -336,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     if (warp < kSoftWarps) {
         // -------------------------------------------------------------- softmax
         more_registers<kSoftRegs>();
+        const int tq = job.tq, len = job.len, row0 = job.row0, row_end = job.row_end;
+        const int n = job.n, step0 = job.step0;
         const int tile = warp >> 2;
         const int r = tile * kQ + (warp & 3) * 32 + lane, row = row0 + r;
         const bool in = row < row_end;
@@ -347,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const float factor = S.factor[r];
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        const int steps = tile == 0 || two ? n : 0;
+        const int steps = tile == 0 || row_end - row0 > kQ ? n : 0;
         for (int i = 0; i < steps; ++i) {
             ok = __all_sync(0xffffffffu, wait(S.s_full[tile], i & 1));
             if (!ok) break;
@@ -422,18 +505,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             tc_fence_after();
         }
         if (ok) {
-            const int64_t index = (o0 + token) * g.a.heads + h * group + (row - token * group);
+            const int64_t index = (job.o0 + token) * g.a.heads + h * group + (row - token * group);
+            const float v_ref = value_ref();
+            const bool cut = job.cut;
             const float inv = l != 0.f ? v_ref / l : 0.f;
+            float* unit = part_at<D>(g, blockIdx.x);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
                 __syncwarp();  // the load is the whole warp's
                 if (steps > 0) tmem_ld32(o_at + 32 * c, x);
                 if (!in) continue;
+                const float f = cut ? v_ref : inv;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = l != 0.f ? __float_as_uint(__uint_as_float(x[e]) * inv) : 0u;
-                if (g.a.dtype == Q4LIN_DTYPE_F32) {
-                    uint4* out = reinterpret_cast<uint4*>(static_cast<float*>(g.a.out) + index * D + 32 * c);
+                for (int e = 0; e < 32; ++e) x[e] = l != 0.f ? __float_as_uint(__uint_as_float(x[e]) * f) : 0u;
+                if (cut || g.a.dtype == Q4LIN_DTYPE_F32) {
+                    uint4* out = reinterpret_cast<uint4*>(cut ? unit + r * D + 32 * c
+                                                              : static_cast<float*>(g.a.out) + index * D + 32 * c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         out[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
@@ -447,11 +535,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                             to_16x2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3]), g.a.dtype));
                 }
             }
-            if (in && g.a.lse) g.a.lse[index] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l) - kBase) * kLn2 : -INFINITY;
+            if (in && cut) {
+                unit[2 * kQ * D + r] = m, unit[2 * kQ * D + 2 * kQ + r] = l;
+            } else if (in && g.a.lse) {
+                g.a.lse[index] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l) - kBase) * kLn2 : -INFINITY;
+            }
         }
     } else if (warp < kIssueWarp) {
         // ------------------------- codes into fp16 blocks: keys, and values, 128 threads each
         fewer_registers<kWidenRegs>();
+        const int n = job.n, step0 = job.step0, pages = (job.len + (1 << ps) - 1) >> ps;
+        const int32_t* table = C.page_table + job.b * C.table_stride;
+        const float v_ref = value_ref();
         const bool keys = warp < kValueWarp;
         const int t = tid & 127;
         // One ring each, a step's blocks in the order of their use.
@@ -547,6 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     } else {
         // ------------------------------------------------------------ MMA issue
         fewer_registers<kIssueRegs>();
+        const int n = job.n;
+        const bool two = job.row_end - job.row0 > kQ;
         if (warp == kIssueWarp && n > 0) {
             const uint32_t leader = elect_one();
             const uint32_t idesc_s = f16_idesc(kQ, kKeys), idesc_o = f16_idesc(kQ, D);
@@ -634,16 +731,109 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     if (warp == kIssueWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
+// The rows of walks that were cut: one warp per query row, a part after another.
+constexpr int kJoinWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_prompt_join_kernel(const PromptArgs g) {
+    constexpr int kAhead = 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t i = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5), token = i / g.a.heads;
+    const int head = (int)(i - token * g.a.heads), group = (int)(g.a.heads / g.cache.kv_heads), h = head / group;
+    if (token >= g.a.tokens) return;
+    const int64_t b = find_sequence(g.cache.batch, token, [&](int64_t k) { return (int64_t)__ldg(g.a.offsets + k); });
+    const int64_t o0 = __ldg(g.a.offsets + b);
+    const Prompt p = prompt_of(g, b);
+    griddep_wait();
+    if (p.pairs == 0 || token < o0 || token >= o0 + p.tq) return;
+    const int parts = __ldcg(g.list), each = __ldcg(g.list + 1);
+    if (parts == 1) return;
+    const int row = (int)(token - o0) * group + head - h * group, pair = row / (2 * kQ), r = row % (2 * kQ);
+    int first, last;
+    walk_of(g, p, pair, &first, &last);
+    const int count = max(1, (last - first + each - 1) / each);
+    const int64_t unit0 = ((int64_t)__ldcg(g.list + 3 + b) + p.pairs - 1 - pair) * parts * g.cache.kv_heads + h;
+    float mx = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool on = lane < D / 4;
+    for (int c = 0; c < count; c += kAhead) {
+        float pm[kAhead], pl[kAhead];
+        float4 po[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            pm[k] = -INFINITY, pl[k] = 0.f, po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c + k < count) {
+                const float* unit = part_at<D>(g, unit0 + (int64_t)(c + k) * g.cache.kv_heads);
+                pm[k] = __ldcg(unit + 2 * kQ * D + r), pl[k] = __ldcg(unit + 2 * kQ * D + 2 * kQ + r);
+                if (on) po[k] = __ldcg(reinterpret_cast<const float4*>(unit + r * D) + lane);
+            }
+        }
+        float top = mx;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, pm[k]);
+        const float from = top == -INFINITY ? 0.f : top, old = ex2(mx - from);
+        o.x *= old, o.y *= old, o.z *= old, o.w *= old, l *= old, mx = top;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float w = ex2(pm[k] - from);
+            o.x = fmaf(po[k].x, w, o.x), o.y = fmaf(po[k].y, w, o.y);
+            o.z = fmaf(po[k].z, w, o.z), o.w = fmaf(po[k].w, w, o.w);
+            l = fmaf(pl[k], w, l);
+        }
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t index = token * g.a.heads + head;
+    if (on && g.a.dtype == Q4LIN_DTYPE_F32)
+        reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + index * D)[lane] =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else if (on)
+        reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D)[lane] =
+            make_uint2(to_16x2(o.x * inv, o.y * inv, g.a.dtype), to_16x2(o.z * inv, o.w * inv, g.a.dtype));
+    if (lane == 0 && g.a.lse)
+        g.a.lse[index] = l != 0.f ? ((mx == -INFINITY ? 0.f : mx) + lg2(l) - kBase) * kLn2 : -INFINITY;
+}
+
 template <int D, int QT, int PT>
-cudaError_t launch(const PromptArgs& g, int64_t grid, cudaStream_t stream) {
+cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     constexpr int bytes = Layout<D, QT>::bytes + 1024;
     static_assert(bytes + sizeof(PromptShared) <= 227 * 1024, "shared memory of one SM");
     // One CTA holds an SM (it takes all of its tensor memory).
     constexpr int asked = bytes > 116 * 1024 ? bytes : 116 * 1024;
-    const cudaError_t e = kernel_smem_once<attention_prompt_kernel<D, QT, PT>>(asked);
+    cudaError_t e = kernel_smem_once<attention_prompt_kernel<D, QT, PT>>(asked);
     if (e != cudaSuccess) return e;
-    attention_prompt_kernel<D, QT, PT><<<(unsigned)grid, kThreads, asked, stream>>>(g);
-    return cudaGetLastError();
+    // Parts only where whole walks leave SMs idle, and as the workspace allows.
+    const int64_t units = std::max<int64_t>(1, pairs_most) * g.cache.kv_heads;
+    const int64_t room = (c.ws_floats - kMaxBatch - 4) / (2 * kQ * (D + 2));
+    g.slots = c.sm_count;
+    g.list = reinterpret_cast<int*>(c.ws);
+    g.parts = c.ws + kMaxBatch + 4;  // 16-byte aligned
+    g.most_parts = units < 2 * c.sm_count ? 64 : 1;
+    const int64_t grid = g.most_parts == 1 ? units : std::min(std::max<int64_t>(units, 2 * c.sm_count), room);
+    if (grid < units) g.most_parts = 1;
+    const int64_t ctas = std::max(grid, units);
+    attention_prompt_plan_kernel<<<1, kPlanThreads, 0, c.stream>>>(g, (int)std::min<int64_t>(ctas, INT32_MAX));
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // The launches of the next kernels overlap the ones before; they wait for their ends on the
+    // device.
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t main = {};
+    main.gridDim = dim3((unsigned)ctas);
+    main.blockDim = dim3(kThreads);
+    main.dynamicSmemBytes = asked;
+    main.stream = c.stream;
+    main.attrs = &attr;
+    main.numAttrs = 1;
+    e = cudaLaunchKernelEx(&main, attention_prompt_kernel<D, QT, PT>, g);
+    if (e != cudaSuccess || g.most_parts == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((g.a.tokens * g.a.heads + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = c.stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attention_prompt_join_kernel<D>, g);
 }
 
 }  // namespace
@@ -652,25 +842,34 @@ bool attention_prompt_eligible(const q4lin_kv_cache_t& cache) { return cache.hea
 
 cudaError_t attention_prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
                                     int64_t rows_min, const LaunchCtx& c) {
-    PromptArgs g;
-    g.cache = cache;
-    g.a = a;
-    g.page_shift = cache.page_size == 16 ? 4 : cache.page_size == 32 ? 5 : 6;
-    g.rows_min = rows_min;
-    g.q_vec = reinterpret_cast<uintptr_t>(a.query) % (4 * dtype_size(a.dtype)) == 0 &&
-              a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;
-    g.status = c.status_word;
-    g.wait_ns = c.wait_limit_ns;
-    // Tile pairs of all sequences at most: each taken one has more than rows_min rows.
     const int64_t rows = a.tokens * (a.heads / cache.kv_heads);
-    const int64_t pairs = rows / (2 * kQ) + std::min(cache.batch, rows / (rows_min + 1));
-    const int64_t grid = std::max<int64_t>(1, pairs) * cache.kv_heads;
-    // One term where it is exact (see the head of this file).
-    if (a.dtype == Q4LIN_DTYPE_BF16 && !a.rope.cos)
-        return cache.head_dim == 64 ? launch<64, 1, 1>(g, grid, c.stream) : launch<128, 1, 1>(g, grid, c.stream);
-    if (a.dtype == Q4LIN_DTYPE_BF16)
-        return cache.head_dim == 64 ? launch<64, 2, 1>(g, grid, c.stream) : launch<128, 2, 1>(g, grid, c.stream);
-    return cache.head_dim == 64 ? launch<64, 2, 2>(g, grid, c.stream) : launch<128, 2, 2>(g, grid, c.stream);
+    cudaError_t e = cudaSuccess;
+    for (int64_t b = 0; b < cache.batch && e == cudaSuccess; b += kMaxBatch) {
+        PromptArgs g;
+        g.cache = cache;
+        g.a = a;
+        g.cache.batch = std::min<int64_t>(kMaxBatch, cache.batch - b);
+        g.cache.page_table += b * cache.table_stride;
+        g.a.offsets += b;
+        g.a.lengths += b;
+        g.page_shift = cache.page_size == 16 ? 4 : cache.page_size == 32 ? 5 : 6;
+        g.rows_min = rows_min;
+        g.q_vec = reinterpret_cast<uintptr_t>(a.query) % (4 * dtype_size(a.dtype)) == 0 &&
+                  a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;
+        g.status = c.status_word;
+        g.wait_ns = c.wait_limit_ns;
+        // Pairs of all sequences at most: each taken one has more than rows_min rows.
+        const int64_t pairs = rows / (2 * kQ) + std::min(g.cache.batch, rows / (rows_min + 1));
+        const bool small = cache.head_dim == 64;
+        // One term where it is exact (see the head of this file).
+        if (a.dtype == Q4LIN_DTYPE_BF16 && !a.rope.cos)
+            e = small ? launch<64, 1, 1>(g, pairs, c) : launch<128, 1, 1>(g, pairs, c);
+        else if (a.dtype == Q4LIN_DTYPE_BF16)
+            e = small ? launch<64, 2, 1>(g, pairs, c) : launch<128, 2, 1>(g, pairs, c);
+        else
+            e = small ? launch<64, 2, 2>(g, pairs, c) : launch<128, 2, 2>(g, pairs, c);
+    }
+    return e;
 }
 
 }  // namespace q4lin
