@@ -63,7 +63,9 @@ struct PromptArgs {
     int q_vec;
     int slots, most_parts;  // CTAs that run at a time; parts of a walk at most
     float* parts;           // [unit][2 kQ (D + 2)]: unfinished walks
-    int* list;              // [batch + 3]: parts, steps of each, pairs, where a sequence's begin
+    int4* plan;             // parts, steps of each, pairs; then of each pair: sequence, tokens,
+                            // length, tile; first and last step, first token
+    int* first_pair;        // [batch]: where a sequence's pairs begin
     int* status;
     int64_t wait_ns;
 };
@@ -118,7 +120,7 @@ struct Layout {
 // warp then waits for local memory behind the codes' loads: 351 against 243 us).
 struct Job {
     int64_t o0;
-    int b, tq, len, row0, row_end, step0, n, cut;
+    int b, h, tq, len, row0, row_end, step0, n, cut;
 };
 
 struct PromptShared {
@@ -187,6 +189,21 @@ __device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t* r) {
         : "r"(addr)
         : "memory");
 }
+// `bytes` from shared to global memory, both 16-byte aligned, and until they have been read.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile(
+        "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+        "cp.async.bulk.commit_group;\n\t"
+        "cp.async.bulk.wait_group 0;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+        "r"(src), "r"(bytes)
+        : "memory");
+}
+// This thread's number, read where it stands.
+__device__ __forceinline__ int thread_number() {
+    int t;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+    return t;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -212,11 +229,84 @@ __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
     return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
+// The queries of a pair of tiles: rotated, scaled to fp16's upper range by a power of two, as
+// QT fp16 terms in swizzled tiles; and what undoes the scaling, with the scores' own scale.
+template <int D, int QT, int DT>
+__device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, float* factor, int64_t o0, int h,
+                                         int tq, int len, int row0, int row_end) {
+    using L = Layout<D, QT>;
+    const int tid = threadIdx.x, group = (int)(g.a.heads / g.cache.kv_heads);
+    constexpr int kUnitsRow = D / 8, kPer = kThreads / kUnitsRow;  // 16 or 8 lanes a row
+    const int u = tid % kUnitsRow;
+    bool turned;
+    int cl, ch;
+    rope_channels(g.a.rope, u, &turned, &cl, &ch);
+    // Rows in batches whose loads are in flight together.
+    constexpr int kPasses = (2 * kQ + kPer - 1) / kPer, kTogether = 4;
+#pragma unroll 1
+    for (int p0 = 0; p0 < kPasses && p0 * kPer < row_end - row0; p0 += kTogether) {
+        float x[kTogether][8], c[kTogether][4], sn[kTogether][4];
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) {
+            const int r = (p0 + k) * kPer + tid / kUnitsRow, row = row0 + r;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+            if (r < 2 * kQ && row < row_end) {
+                const int token = (uint32_t)row / (uint32_t)group, head = h * group + row - token * group;
+                const int64_t e = (o0 + token) * g.a.q_token_stride + head * g.a.q_head_stride;
+                const int position = len - tq + token;
+                load_four(g.a.query, DT, e + cl, g.q_vec, x[k]);
+                load_four(g.a.query, DT, e + ch, g.q_vec, x[k] + 4);
+                if (turned && position >= 0)
+                    rope_load(g.a.rope, position, u, c[k], sn[k]);
+                else
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[k][e] = 1.f, sn[k][e] = 0.f;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[k][e] = 1.f, sn[k][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) {
+            const int r = (p0 + k) * kPer + tid / kUnitsRow;
+            if (turned) rope_apply(g.a.rope, c[k], sn[k], x[k]);
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[k][e]));
+#pragma unroll
+            for (int o = kUnitsRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            // 2^up brings the row's largest |x| to [2^14, 2^15); the scale's sign goes with it,
+            // so that larger scores stay larger after the factor.
+            const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
+            const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), g.a.scale);
+            const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+            if (r < 2 * kQ) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    split_f16(x[k][2 * e] * up, x[k][2 * e + 1] * up, &hi[e], &lo[e]);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int d = w ? ch : cl;  // channels d .. d + 3: half a 16-byte chunk
+                    const uint32_t at = L::q + (uint32_t)((r / kQ) * QT * L::kBlocks + d / 64) * L::kBlock +
+                                        swizzled(r % kQ, (d % 64) / 8) + (d % 8) * 2;
+                    *reinterpret_cast<uint2*>(gbase + at) = make_uint2(hi[2 * w], hi[2 * w + 1]);
+                    if (QT == 2)
+                        *reinterpret_cast<uint2*>(gbase + at + L::kBlocks * L::kBlock) =
+                            make_uint2(lo[2 * w], lo[2 * w + 1]);
+                }
+                if (u == 0) factor[r] = fabsf(g.a.scale) * kLog2e * down;
+            }
+        }
+    }
+}
+
 // One CTA, before the prompts' kernel: which pairs there are, and in how many parts their walks
 // are cut.
 constexpr int kPlanThreads = 256;
 __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(const PromptArgs g, int units_most) {
-    __shared__ int s_longest[kPlanThreads / 32], s_scan[kPlanThreads / 32];
+    __shared__ int s_longest[kPlanThreads / 32], s_scan[kPlanThreads / 32], s_prefix[kMaxBatch + 1];
     griddep_launch_dependents();  // (the prompts' kernel waits for this one's end)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hkv = (int)g.cache.kv_heads, group = (int)(g.a.heads / g.cache.kv_heads);
@@ -252,11 +342,28 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
             if (w < warp) before += s_scan[w];
             pairs += s_scan[w];
         }
-        if (b < g.cache.batch) g.list[3 + b] = before + sum - own;
+        if (b < g.cache.batch) g.first_pair[b] = s_prefix[b] = before + sum - own;
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) s_longest[warp] = longest;
+    if (tid == 0) s_prefix[g.cache.batch] = pairs;
     __syncthreads();
+    for (int i = tid; i < pairs; i += kPlanThreads) {
+        int lo = 0, hi = (int)g.cache.batch;  // prefix[lo] <= i < prefix[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_prefix[mid] <= i)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const Prompt p = prompt_of(g, lo);
+        const int tile = p.pairs - 1 - (i - s_prefix[lo]);  // the longest walks first
+        int first, last;
+        walk_of(g, p, tile, &first, &last);
+        g.plan[1 + 2 * i] = make_int4(lo, p.tq, p.len, tile);
+        g.plan[2 + 2 * i] = make_int4(first, last, __ldg(g.a.offsets + lo), 0);
+    }
     if (warp != 0) return;
     for (int w = 0; w < kPlanThreads / 32; ++w) longest = max(longest, s_longest[w]);
     // Walks in `parts` parts of `each` steps where whole ones leave SMs idle: the least rounds of
@@ -270,10 +377,10 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
         best = min(best, (uint32_t)min(cost, (int64_t)0x3FFFFFF) << 6 | (uint32_t)(n - 1));
     }
     const int parts = (int)(__reduce_min_sync(0xffffffffu, best) & 63u) + 1;
-    if (lane == 0) g.list[0] = parts, g.list[1] = max(1, (longest + parts - 1) / parts), g.list[2] = pairs;
+    if (lane == 0) *g.plan = make_int4(parts, max(1, (longest + parts - 1) / parts), pairs, 0);
 }
 
-template <int D, int QT, int PT>
+template <int D, int QT, int PT, int DT>
 __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const PromptArgs g) {
     using L = Layout<D, QT>;
     extern __shared__ uint8_t smem_raw[];
@@ -287,25 +394,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     griddep_launch_dependents();  // (the joining kernel waits for this one's end)
     griddep_wait();               // for the plan
     {
-    const int parts = __ldcg(g.list), each = __ldcg(g.list + 1);
-    const int64_t pair = blockIdx.x / Hkv / parts;  // of the whole call
-    if (pair >= __ldcg(g.list + 2)) return;
+    const int4 plan = __ldcg(g.plan);
+    const int parts = plan.x, each = plan.y, pair = (int)(blockIdx.x / Hkv) / parts;
+    if (pair >= plan.z) return;
     const int part = (int)(blockIdx.x / Hkv) % parts;
-    const int64_t b = find_sequence(C.batch, pair, [&](int64_t i) { return (int64_t)__ldcg(g.list + 3 + i); });
-    const Prompt prompt = prompt_of(g, b);
-    // The longest walks first.
-    const int tile = prompt.pairs - 1 - (int)(pair - __ldcg(g.list + 3 + b));
+    const int4 j0 = __ldcg(g.plan + 1 + 2 * pair), j1 = __ldcg(g.plan + 2 + 2 * pair);
+    const int b = j0.x, tq = j0.y, len = j0.z, tile = j0.w;
+    const int64_t o0 = j1.z;
     if (tid == 0) S.failed = 0;
-    const int64_t o0 = __ldg(g.a.offsets + b);
-    const int tq = prompt.tq, len = prompt.len;
     const int rows = tq * group, row0 = tile * 2 * kQ;
     const int row_end = min(rows, row0 + 2 * kQ);
-    int step0, step1;
-    walk_of(g, prompt, tile, &step0, &step1);
-    step0 = min(step0 + part * each, step1), step1 = min(step0 + each, step1);
+    const int step0 = min(j1.x + part * each, j1.y), step1 = min(step0 + each, j1.y);
     const int n = step1 - step0;
     if (n == 0 && part > 0) return;  // a shorter walk has fewer parts
-    if (tid == 0) S.job = {o0, (int)b, tq, len, row0, row_end, step0, n, parts > 1};
+    if (tid == 0) S.job = {o0, b, h, tq, len, row0, row_end, step0, n, parts > 1};
     const int32_t* table = C.page_table + b * C.table_stride;
     const int pages = (len + (1 << ps) - 1) >> ps;
 
@@ -336,54 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
 #pragma unroll
     for (int o = 16; o; o >>= 1) v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, o));
     if (lane == 0) S.v_max[warp] = v_max;
-    {
-        constexpr int kUnitsRow = D / 8, kPer = kThreads / kUnitsRow;  // 16 or 8 lanes a row
-        const int u = tid % kUnitsRow;
-        bool turned;
-        int cl, ch;
-        rope_channels(g.a.rope, u, &turned, &cl, &ch);
-        for (int r0 = 0; r0 < 2 * kQ; r0 += kPer) {
-            const int r = r0 + tid / kUnitsRow, row = row0 + r;
-            const bool in = r < 2 * kQ && row < row_end;
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            const int token = in ? row / group : 0, head = h * group + (in ? row - token * group : 0);
-            if (in) {
-                const int64_t e = (o0 + token) * g.a.q_token_stride + head * g.a.q_head_stride;
-                load_four(g.a.query, g.a.dtype, e + cl, g.q_vec, x);
-                load_four(g.a.query, g.a.dtype, e + ch, g.q_vec, x + 4);
-                const int position = len - tq + token;
-                if (turned && position >= 0) rope_unit(g.a.rope, position, u, x);
-            }
-            float m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
-#pragma unroll
-            for (int o = kUnitsRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            // 2^up brings the row's largest |x| to [2^14, 2^15); the scale's sign goes with it,
-            // so that larger scores stay larger after the factor.
-            const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
-            const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), g.a.scale);
-            const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-            if (r < 2 * kQ) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) split_f16(x[2 * e] * up, x[2 * e + 1] * up, &hi[e], &lo[e]);
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int d = w ? ch : cl;  // channels d .. d + 3: half a 16-byte chunk
-                    const uint32_t at = L::q + (uint32_t)((r / kQ) * QT * L::kBlocks + d / 64) * L::kBlock +
-                                        swizzled(r % kQ, (d % 64) / 8) + (d % 8) * 2;
-                    *reinterpret_cast<uint2*>(gbase + at) = make_uint2(hi[2 * w], hi[2 * w + 1]);
-                    if (QT == 2)
-                        *reinterpret_cast<uint2*>(gbase + at + L::kBlocks * L::kBlock) =
-                            make_uint2(lo[2 * w], lo[2 * w + 1]);
-                }
-                if (u == 0) S.factor[r] = fabsf(g.a.scale) * kLog2e * down;
-            }
-        }
-    }
+    put_queries<D, QT, DT>(g, gbase, S.factor, o0, h, tq, len, row0, row_end);
     }
     fence_async_shared();  // the queries are read by the tensor cores
     tc_fence_before();
@@ -426,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const uint32_t s_at = tmem + lanes + kScoreCol + tile * kKeys, o_at = tmem + lanes + tile * 128;
         const int token = row / group, position = len - tq + token;
         const int limit = !in ? -1 : g.a.causal ? position : len - 1;
-        const int64_t low = g.a.window > 0 ? max((int64_t)0, (int64_t)position - g.a.window + 1) : 0;
+        const int low = g.a.window > 0 ? (int)max((int64_t)0, (int64_t)position - g.a.window + 1) : 0;
         const float factor = S.factor[r];
         float m = -INFINITY, l = 0.f;
         bool ok = true;
@@ -436,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             if (!ok) break;
             tc_fence_after();
             const int key0 = (step0 + i) * kKeys, slot = i % kScaleSlots;
-            const int hi = min(limit - key0, kKeys), lo = (int)(low > key0 ? min(low - key0, (int64_t)kKeys) : 0);
+            const int hi = min(limit - key0, kKeys), lo = max(low - key0, 0);
             uint32_t x[kKeys];
             tmem_ld64(s_at, x);
             tmem_ld64(s_at + 64, x + 64);
@@ -504,36 +559,57 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             ok = __all_sync(0xffffffffu, wait(S.o_full[tile], 0));
             tc_fence_after();
         }
-        if (ok) {
-            const int64_t index = (job.o0 + token) * g.a.heads + h * group + (row - token * group);
-            const float v_ref = value_ref();
-            const bool cut = job.cut;
-            const float inv = l != 0.f ? v_ref / l : 0.f;
+        // (A second tile without rows has nothing to store, and the first one's products may
+        // still read the shared memory that the rows go through.)
+        if (ok && (tile == 0 || row_end - row0 > kQ)) {
+            // (Everything about the row anew: the loop has no registers to keep it in.)
+            const int tid = thread_number(), r = tid, row = job.row0 + r;  // threads are rows
+            const bool in = row < job.row_end, cut = job.cut;
+            const int group = (int)(g.a.heads / C.kv_heads), token = row / group;
+            const int64_t index = (job.o0 + token) * g.a.heads + job.h * group + (row - token * group);
+            const float v_ref = value_ref(), inv = l != 0.f ? v_ref / l : 0.f;
+            const uint32_t o_at = ((uint32_t)((tid >> 5) & 3) << 21) + (uint32_t)(r / kQ) * 128;
             float* unit = part_at<D>(g, blockIdx.x);
+            // A thread's row goes through shared memory, where nothing else is wanted any more (its
+            // pitch keeps the rows of a quarter-warp on banks of their own), and leaves by one
+            // bulk copy: rows stored by their threads took 6 us.
+            const bool wide = cut || DT == Q4LIN_DTYPE_F32;
+            const uint32_t row_bytes = wide ? 4 * D : 2 * D, out = base + (uint32_t)r * (4 * D + 16);
+            static_assert(2 * kQ * (4 * D + 16) <= L::bytes, "the rows fit");
+            const float f = l == 0.f ? 0.f : cut ? v_ref : inv;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
                 __syncwarp();  // the load is the whole warp's
-                if (steps > 0) tmem_ld32(o_at + 32 * c, x);
-                if (!in) continue;
-                const float f = cut ? v_ref : inv;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = l != 0.f ? __float_as_uint(__uint_as_float(x[e]) * f) : 0u;
-                if (cut || g.a.dtype == Q4LIN_DTYPE_F32) {
-                    uint4* out = reinterpret_cast<uint4*>(cut ? unit + r * D + 32 * c
-                                                              : static_cast<float*>(g.a.out) + index * D + 32 * c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        out[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                if (steps > 0) {
+                    tmem_ld32(o_at + 32 * c, x);
                 } else {
-                    uint2* out =
-                        reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(l == 0.f ? 0.f : __uint_as_float(x[e]) * f);
+                if (wide) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        out[e] = make_uint2(
-                            to_16x2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]), g.a.dtype),
-                            to_16x2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3]), g.a.dtype));
+                        st_shared_v4(out + 128 * c + 16 * e, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = to_16x2(__uint_as_float(x[8 * e + 2 * j]), __uint_as_float(x[8 * e + 2 * j + 1]),
+                                           DT);
+                        st_shared_v4(out + 64 * c + 16 * e, w[0], w[1], w[2], w[3]);
+                    }
                 }
+            }
+            fence_async_shared();
+            if (in) {
+                void* to = cut ? static_cast<void*>(unit + r * D)
+                               : static_cast<void*>(static_cast<uint8_t*>(g.a.out) + index * row_bytes);
+                bulk_store(to, out, row_bytes);
             }
             if (in && cut) {
                 unit[2 * kQ * D + r] = m, unit[2 * kQ * D + 2 * kQ + r] = l;
@@ -745,13 +821,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_prompt_join_kernel(
     const Prompt p = prompt_of(g, b);
     griddep_wait();
     if (p.pairs == 0 || token < o0 || token >= o0 + p.tq) return;
-    const int parts = __ldcg(g.list), each = __ldcg(g.list + 1);
+    const int parts = __ldcg(g.plan).x, each = __ldcg(g.plan).y;
     if (parts == 1) return;
     const int row = (int)(token - o0) * group + head - h * group, pair = row / (2 * kQ), r = row % (2 * kQ);
     int first, last;
     walk_of(g, p, pair, &first, &last);
     const int count = max(1, (last - first + each - 1) / each);
-    const int64_t unit0 = ((int64_t)__ldcg(g.list + 3 + b) + p.pairs - 1 - pair) * parts * g.cache.kv_heads + h;
+    const int64_t unit0 = ((int64_t)__ldcg(g.first_pair + b) + p.pairs - 1 - pair) * parts * g.cache.kv_heads + h;
     float mx = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool on = lane < D / 4;
@@ -792,20 +868,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_prompt_join_kernel(
         g.a.lse[index] = l != 0.f ? ((mx == -INFINITY ? 0.f : mx) + lg2(l) - kBase) * kLn2 : -INFINITY;
 }
 
-template <int D, int QT, int PT>
+template <int D, int QT, int PT, int DT>
 cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     constexpr int bytes = Layout<D, QT>::bytes + 1024;
     static_assert(bytes + sizeof(PromptShared) <= 227 * 1024, "shared memory of one SM");
     // One CTA holds an SM (it takes all of its tensor memory).
     constexpr int asked = bytes > 116 * 1024 ? bytes : 116 * 1024;
-    cudaError_t e = kernel_smem_once<attention_prompt_kernel<D, QT, PT>>(asked);
+    cudaError_t e = kernel_smem_once<attention_prompt_kernel<D, QT, PT, DT>>(asked);
     if (e != cudaSuccess) return e;
     // Parts only where whole walks leave SMs idle, and as the workspace allows.
     const int64_t units = std::max<int64_t>(1, pairs_most) * g.cache.kv_heads;
-    const int64_t room = (c.ws_floats - kMaxBatch - 4) / (2 * kQ * (D + 2));
+    const int64_t head = kMaxBatch + 4 + 8 * pairs_most;  // floats, a multiple of 4
+    if (head > c.ws_floats / 2) return cudaErrorInvalidValue;
+    const int64_t room = (c.ws_floats - head) / (2 * kQ * (D + 2));
     g.slots = c.sm_count;
-    g.list = reinterpret_cast<int*>(c.ws);
-    g.parts = c.ws + kMaxBatch + 4;  // 16-byte aligned
+    g.first_pair = reinterpret_cast<int*>(c.ws);
+    g.plan = reinterpret_cast<int4*>(c.ws + kMaxBatch);
+    g.parts = c.ws + head;
     g.most_parts = units < 2 * c.sm_count ? 64 : 1;
     const int64_t grid = g.most_parts == 1 ? units : std::min(std::max<int64_t>(units, 2 * c.sm_count), room);
     if (grid < units) g.most_parts = 1;
@@ -825,7 +904,7 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     main.stream = c.stream;
     main.attrs = &attr;
     main.numAttrs = 1;
-    e = cudaLaunchKernelEx(&main, attention_prompt_kernel<D, QT, PT>, g);
+    e = cudaLaunchKernelEx(&main, attention_prompt_kernel<D, QT, PT, DT>, g);
     if (e != cudaSuccess || g.most_parts == 1) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((g.a.tokens * g.a.heads + kJoinWarps - 1) / kJoinWarps));
@@ -862,12 +941,15 @@ cudaError_t attention_prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_a
         const int64_t pairs = rows / (2 * kQ) + std::min(g.cache.batch, rows / (rows_min + 1));
         const bool small = cache.head_dim == 64;
         // One term where it is exact (see the head of this file).
-        if (a.dtype == Q4LIN_DTYPE_BF16 && !a.rope.cos)
-            e = small ? launch<64, 1, 1>(g, pairs, c) : launch<128, 1, 1>(g, pairs, c);
-        else if (a.dtype == Q4LIN_DTYPE_BF16)
-            e = small ? launch<64, 2, 1>(g, pairs, c) : launch<128, 2, 1>(g, pairs, c);
+        constexpr int f32 = Q4LIN_DTYPE_F32, f16 = Q4LIN_DTYPE_F16, bf16 = Q4LIN_DTYPE_BF16;
+        if (a.dtype == bf16 && !a.rope.cos)
+            e = small ? launch<64, 1, 1, bf16>(g, pairs, c) : launch<128, 1, 1, bf16>(g, pairs, c);
+        else if (a.dtype == bf16)
+            e = small ? launch<64, 2, 1, bf16>(g, pairs, c) : launch<128, 2, 1, bf16>(g, pairs, c);
+        else if (a.dtype == f16)
+            e = small ? launch<64, 2, 2, f16>(g, pairs, c) : launch<128, 2, 2, f16>(g, pairs, c);
         else
-            e = small ? launch<64, 2, 2>(g, pairs, c) : launch<128, 2, 2>(g, pairs, c);
+            e = small ? launch<64, 2, 2, f32>(g, pairs, c) : launch<128, 2, 2, f32>(g, pairs, c);
     }
     return e;
 }

@@ -130,9 +130,9 @@ q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cac
     if ((st = check_rope(a->rope, cache->head_dim, &rb)) != Q4LIN_OK) return st;
     if (a->tokens == 0 || cache->batch == 0) return Q4LIN_OK;
     const int64_t size = size_of(a->dtype), D = cache->head_dim;
-    // out is written 4 channels at a time.
+    // out is written 16 bytes at a time.
     if (a->max_query < 1 || !a->query || !a->out || !a->offsets || !a->lengths || !aligned(a->query, size) ||
-        !aligned(a->out, 4 * size) || !aligned(a->lse, 4) || !aligned(a->offsets, 4) || !aligned(a->lengths, 4))
+        !aligned(a->out, 16) || !aligned(a->lse, 4) || !aligned(a->offsets, 4) || !aligned(a->lengths, 4))
         return Q4LIN_ERR_INVALID_ARG;
     if (!extent(a->tokens, a->q_token_stride, a->heads, a->q_head_stride, D, size, &qb) ||
         !mul_ok(a->tokens, a->heads, &t) || !mul_ok(t, D * size, &ob) || !mul_ok(t, a->lse ? 4 : 0, &lb))

@@ -75,17 +75,20 @@ __device__ __forceinline__ void rope_load(const q4lin_rope_t& r, int64_t positio
 // The rotation, each product and sum rounded once.
 __device__ __forceinline__ void rope_apply(const q4lin_rope_t& r, const float (&c)[4], const float (&s)[4],
                                            float (&x)[8]) {
-    float y[4], z[4];
+    if (r.interleaved) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float a = r.interleaved ? x[2 * e] : x[e], b = r.interleaved ? x[2 * e + 1] : x[4 + e];
-        y[e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
-        z[e] = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
-    }
+        for (int e = 0; e < 4; ++e) {
+            const float a = x[2 * e], b = x[2 * e + 1];
+            x[2 * e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
+            x[2 * e + 1] = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
+        }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[2 * e] = r.interleaved ? y[e] : e < 2 ? y[2 * e] : z[2 * e - 4];
-        x[2 * e + 1] = r.interleaved ? z[e] : e < 2 ? y[2 * e + 1] : z[2 * e - 3];
+        for (int e = 0; e < 4; ++e) {
+            const float a = x[e], b = x[4 + e];
+            x[e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
+            x[4 + e] = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
+        }
     }
 }
 __device__ __forceinline__ void rope_unit(const q4lin_rope_t& r, int64_t position, int u, float (&x)[8]) {

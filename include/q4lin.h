@@ -346,7 +346,8 @@ Q4LIN_API q4lin_status_t q4lin_run_kv_append(q4lin_handle_t handle,
 typedef struct q4lin_attention {
     const void* query; /* [tokens, heads, head_dim], channels contiguous */
     int64_t q_token_stride, q_head_stride; /* elements */
-    void* out;              /* [tokens, heads, head_dim], contiguous, of the query's type */
+    void* out;              /* [tokens, heads, head_dim], contiguous, of the query's type,
+                               16-byte aligned */
     float* lse;             /* [tokens, heads], or NULL */
     int dtype;              /* q4lin_dtype_t of query and out */
     int64_t tokens, heads;  /* heads: a multiple of kv_heads */
