@@ -51,6 +51,7 @@ struct SplitArgs {
     int* list;      // [batch + 2]: the share, then where each sequence begins in the list
     int* status;
     int64_t wait_ns;
+    uint32_t missing;  // test hook: bytes that the copies' barriers wait for in vain
 };
 
 // Per query row of a piece.
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
         const bool some = lane < ppt && id >= 0;
         const int count = __popc(__ballot_sync(0xffffffffu, some));
         const uint32_t bar = smem_u32(&S.full[warp][slot_in]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * page_bytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * page_bytes + g.missing);
         __syncwarp();
         if (some) {
             const uint8_t* codes = issued & 1 ? C.v_codes : C.k_codes;
@@ -477,8 +478,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
             // A wait ran out: copies still in flight must land before the CTA leaves, and the
             // warp ends here (outputs are undefined).
             if (lane == 0) record_failure(g.status, &S.failed);
+            const int64_t limit = g.missing ? g.wait_ns : kDrainNs;
             for (; in_flight > 0; --in_flight) {
-                wait_bounded(smem_u32(&S.full[warp][slot_out]), (phase >> slot_out) & 1u, kDrainNs, nullptr);
+                wait_bounded(smem_u32(&S.full[warp][slot_out]), (phase >> slot_out) & 1u, limit, nullptr);
                 phase ^= 1u << slot_out;
                 slot_out = slot_out + 1 == kSlots ? 0 : slot_out + 1;
             }
@@ -690,6 +692,7 @@ cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_at
                   a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;
         g.status = c.status_word;
         g.wait_ns = c.wait_limit_ns;
+        g.missing = c.tc_skip_first_copy ? 16 : 0;
         const int64_t row_tiles = std::min((a.tokens * group + R - 1) / R + g.cache.batch,
                                            ((rows + R - 1) / R) * g.cache.batch);
         const int64_t most = row_tiles * cache.kv_heads;  // heads' row tiles in the list

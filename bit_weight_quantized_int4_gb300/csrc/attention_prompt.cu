@@ -68,6 +68,7 @@ struct PromptArgs {
     int* first_pair;        // [batch]: where a sequence's pairs begin
     int* status;
     int64_t wait_ns;
+    int skip_first_copy;  // test hook: no keys come, and the waits for them run out
 };
 
 // What one sequence asks of this kernel.
@@ -689,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             int slot = 0;
             uint32_t par = 1;  // nothing to wait for in the ring's first round
             load(pages_now, 0);
-            for (int i = 0; i < n; ++i) {
+            for (int i = 0; i < n && !(keys && g.skip_first_copy); ++i) {
                 for (int blk = 0; blk < blocks; ++blk) {
                     // (With the keys: the softmax needs both scales once the scores are there.)
                     const bool scales = keys && blk == 0 && t < 8;
@@ -885,7 +886,7 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     g.first_pair = reinterpret_cast<int*>(c.ws);
     g.plan = reinterpret_cast<int4*>(c.ws + kMaxBatch);
     g.parts = c.ws + head;
-    g.most_parts = units < 2 * c.sm_count ? 64 : 1;
+    g.most_parts = units <= c.sm_count ? 64 : 1;
     const int64_t grid = g.most_parts == 1 ? units : std::min(std::max<int64_t>(units, 2 * c.sm_count), room);
     if (grid < units) g.most_parts = 1;
     const int64_t ctas = std::max(grid, units);
@@ -937,6 +938,7 @@ cudaError_t attention_prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_a
                   a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;
         g.status = c.status_word;
         g.wait_ns = c.wait_limit_ns;
+        g.skip_first_copy = c.tc_skip_first_copy;
         // Pairs of all sequences at most: each taken one has more than rows_min rows.
         const int64_t pairs = rows / (2 * kQ) + std::min(g.cache.batch, rows / (rows_min + 1));
         const bool small = cache.head_dim == 64;

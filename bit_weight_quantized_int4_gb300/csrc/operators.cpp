@@ -14,8 +14,11 @@ using q4lin::overlaps;
 namespace {
 
 // Query rows (tokens x heads) per key/value head up to which a sequence's attention goes
-// through the kernel that splits the keys.
-constexpr int64_t kSplitRows = 64;
+// through the kernel that splits the keys (us, 8 key/value heads of 128, split / prompts' kernel,
+// bf16: one sequence of 8192 keys, 32 rows 28.8 / 26.7, 64 rows 43.0 / 27.9; of 65536, 32 rows
+// 100 / 84, 64 rows 181 / 85; 8 sequences of 2000, 32 rows 35 / 39, 64 rows 45 / 40; 32 of 4000,
+// 32 rows 119 / 148, 64 rows 191 / 147; fp32, 8 of 2000: 31 / 47 and 41 / 48).
+constexpr int64_t kSplitRows = 48;
 
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 bool known_dtype(int dtype) { return dtype >= Q4LIN_DTYPE_F32 && dtype <= Q4LIN_DTYPE_BF16; }

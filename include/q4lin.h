@@ -94,7 +94,7 @@ typedef enum {
     Q4LIN_OPT_NIBBLE_EVEN_HIGH = 2,
     /* Time limit, in nanoseconds of the GPU's global timer, of every bounded
      * device-side wait (mbarrier polls) of the TMA-fed kernels (decode and multi-row
-     * GEMV, tensor-core GEMM, input gradient); <= 0 restores the default (2 s).  When a
+     * GEMV, tensor-core GEMM, input gradient, attention); <= 0 restores the default (2 s).  When a
      * wait runs out the kernel records code 1 in the handle's status word, stops issuing
      * work, lets its own copies (and MMAs) in flight finish, frees its tensor memory and
      * returns; its output is then undefined. */
@@ -104,9 +104,10 @@ typedef enum {
      * preceding kernel must not write this call's qweight or scales. */
     Q4LIN_OPT_PDL = 4,
     /* Test hook, default 0.  1: the tensor-core kernel's copy engine skips the first
-     * pipeline stage, and the multi-row GEMV's copy engine issues nothing, so the barrier
-     * their consumers wait on is never completed and their bounded waits run out
-     * (exercises the timeout path without faulting the GPU). */
+     * pipeline stage, the multi-row GEMV's copy engine issues nothing, and the attention
+     * kernels' barriers expect keys that do not come, so the barrier their consumers wait
+     * on is never completed and their bounded waits run out (exercises the timeout path
+     * without faulting the GPU). */
     Q4LIN_OPT_TC_SKIP_FIRST_COPY = 5,
     /* 1: the tensor-core GEMM multiplies fp16 operands (x and the dequantized weights
      * (code - 8) * scale rounded to IEEE binary16, fp32 accumulation: tcgen05.mma

@@ -125,7 +125,17 @@ PROMPTS = [
 ]
 
 
-@pytest.mark.parametrize("lengths,counts,heads,kv_heads,page,dim,dtype,causal,window", PROMPTS)
+CUT = [
+    # Few rows over many keys: walks in parts, some shorter than others, and a tile without rows.
+    ([5000], [3], 4, 1, 64, 128, "f32", True, 0),
+    ([4097, 130, 1], [40, 40, 1], 4, 2, 16, 64, "bf16", True, 0),
+    ([3000, 2900], [100, 7], 3, 1, 32, 128, "f16", False, 0),
+    ([6000], [150], 2, 1, 64, 64, "f32", True, 2000),
+    ([2500, 0, 700], [2, 3, 300], 8, 2, 64, 128, "bf16", True, 300),
+]
+
+
+@pytest.mark.parametrize("lengths,counts,heads,kv_heads,page,dim,dtype,causal,window", PROMPTS + CUT)
 def test_prompt_kernel(handle, lengths, counts, heads, kv_heads, page, dim, dtype, causal, window):
     """Every size through the prompts' kernel, then the same call by the other one."""
     from bit_weight_quantized_int4_gb300 import q4lin
@@ -156,6 +166,52 @@ def test_values_of_very_different_pages(handle):
 @pytest.mark.parametrize("rotated,interleaved", [(0, False), (32, False), (32, True), (128, True)])
 def test_rotation(handle, rotated, interleaved):
     check(*run(handle, [100, 40], [1, 3], 4, 2, 32, 128, "f32", rotated=rotated, interleaved=interleaved))
+
+
+def test_more_sequences_than_one_launch_takes(handle):
+    """1100 sequences of 0 to 40 tokens, one query each; then prompts among them."""
+    lengths = [i * 7 % 41 for i in range(1100)]
+    check(*run(handle, lengths, [1] * 1100, 2, 1, 16, 64, "f32", max_query=1))
+    counts = [min(n, 30) if i % 100 == 0 else 1 for i, n in enumerate(lengths)]
+    check(*run(handle, lengths, counts, 2, 1, 16, 64, "f32"))
+    assert status(handle) == 0
+
+
+def test_negative_and_zero_scale(handle):
+    """The smallest scores weigh most, or all keys alike; both kernels."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(19)
+    host = ops.Cache(rng, [300], 1, 32, 64)
+    q = ops.to_device(rng.standard_normal((40, 2, 64)).astype(np.float32))
+    offsets = np.array([0, 40], np.int32)
+    for scale in (-0.25, 0.0):
+        for rows in (1, 1 << 40):
+            handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, rows)
+            out, lse = q4lin.attention(handle, host.device(), q, ops.to_device(offsets),
+                                       ops.to_device(np.array([300], np.int32)), scale)
+            handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
+            ref = ops.attention(host, ops.to_host(q), offsets, [300], scale)
+            check(out, lse, (*ref[:3], np.abs(ref[3])), "f32")
+
+
+def test_a_wait_that_runs_out_is_reported(handle):
+    """Keys that do not come: the kernels give up, leave, and work again afterwards."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    host = ops.Cache(np.random.default_rng(20), [3000], 2, 64, 128)
+    cache, q = host.device(), torch.randn(200, 4, 128, device="cuda")
+    n = ops.to_device(np.array([3000], np.int32))
+    for tokens in (1, 200):
+        o = ops.to_device(np.array([0, tokens], np.int32))
+        want = q4lin.attention(handle, cache, q[:tokens], o, n, 0.1)[0]
+        handle.set_option(q4lin.Q4LIN_OPT_WAIT_LIMIT, 1000000)  # 1 ms
+        handle.set_option(q4lin.Q4LIN_OPT_TC_SKIP_FIRST_COPY, 1)
+        q4lin.attention(handle, cache, q[:tokens], o, n, 0.1)
+        handle.set_option(q4lin.Q4LIN_OPT_TC_SKIP_FIRST_COPY, 0)
+        handle.set_option(q4lin.Q4LIN_OPT_WAIT_LIMIT, 0)
+        assert status(handle) == 1
+        assert torch.equal(q4lin.attention(handle, cache, q[:tokens], o, n, 0.1)[0], want)
+        assert status(handle) == 0
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -55,7 +55,8 @@ def check(r, x, tokens, top):
 
 
 SHAPES = [(1, 1, 1), (1, 2, 2), (3, 5, 3), (1, 31, 31), (2, 33, 32), (7, 100, 5), (2, 1000, 20), (5, 1003, 32),
-          (400, 777, 5), (1, 4097, 1), (3, 5000, 0), (1, 128256, 5), (2, 128257, 32), (310, 2049, 20)]
+          (400, 777, 5), (1, 4097, 1), (3, 5000, 0), (1, 128256, 5), (2, 128257, 32), (310, 2049, 20),
+          (40, 70001, 20)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
