@@ -199,10 +199,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
     const uint32_t page_bytes = (uint32_t)(D << ps);
     const int batch_tiles = 32 / ppt;
     const int32_t* table = nullptr;
-    int first = 0, cnt = 0, pages = 0, head = 0, ids = 0, issued = 0, slot_in = 0, in_flight = 0;
+    int first = 0, cnt = 0, page_low = 0, pages = 0, head = 0, ids = 0, issued = 0, slot_in = 0, in_flight = 0;
     auto load_ids = [&](int i) {
         const int p = (first + i) * ppt + lane;
-        ids = i + lane / ppt < cnt && p < pages ? __ldg(table + p) : INT_MIN;
+        ids = i + lane / ppt < cnt && p >= page_low && p < pages ? __ldg(table + p) : INT_MIN;
     };
     auto check_ids = [&]() {
         if (ids == INT_MIN) {
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
     auto fetch_scales = [&](int i) {
         const int p = (first + i) * ppt + ((t * 16) >> ps);
         sk_next = sv_next = 0.f;
-        if (i < cnt && p < pages) {
+        if (i < cnt && p >= page_low && p < pages) {
             int id = __ldg(table + p);
             if (id < 0 || id >= C.num_pages) id = 0;
             sk_next = __ldg(C.k_scales + (int64_t)id * Hkv + head);
@@ -267,6 +267,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
         first = P.tile0 + P.k0;
         table = C.page_table + P.b * C.table_stride;
         pages = (P.len + (1 << ps) - 1) >> ps;
+        // Pages before the window of the piece's first token are not read.
+        page_low = 0;
+        if (g.a.window > 0)
+            page_low = (int)(max((int64_t)P.len - P.tq + P.row0 / group - g.a.window + 1, (int64_t)0) >> ps);
         head = P.h;
         issued = 0;
         load_ids(0);
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
             bool turned;
             int cl, ch;
             rope_channels(g.a.rope, unit, &turned, &cl, &ch);
-            constexpr int kTogether = kPasses < 4 ? kPasses : 4;  // passes whose loads overlap
+            constexpr int kTogether = kPasses < 2 ? kPasses : 2;  // whose loads overlap
             const int valid = min(R, P.tq * group - P.row0);  // rows (the others stay unread)
             if (lane >= valid && lane < R) mine.row[lane] = {0.f, -1, 0, -1};
             const uint32_t token0 = (uint32_t)P.row0 / (uint32_t)group, rest0 = P.row0 - token0 * group;

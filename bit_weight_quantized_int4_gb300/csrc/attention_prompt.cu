@@ -122,6 +122,7 @@ struct Layout {
 struct Job {
     int64_t o0;
     int b, h, tq, len, row0, row_end, step0, n, cut;
+    int page_low;  // the first page that a window leaves
 };
 
 struct PromptShared {
@@ -408,7 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     const int step0 = min(j1.x + part * each, j1.y), step1 = min(step0 + each, j1.y);
     const int n = step1 - step0;
     if (n == 0 && part > 0) return;  // a shorter walk has fewer parts
-    if (tid == 0) S.job = {o0, b, h, tq, len, row0, row_end, step0, n, parts > 1};
+    const int64_t low = g.a.window > 0 ? (int64_t)len - tq + row0 / group - g.a.window + 1 : 0;
+    const int page_low = low > 0 ? (int)(low >> ps) : 0;
+    if (tid == 0) S.job = {o0, b, h, tq, len, row0, row_end, step0, n, parts > 1, page_low};
     const int32_t* table = C.page_table + b * C.table_stride;
     const int pages = (len + (1 << ps) - 1) >> ps;
 
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     }
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&S.tmem), kTmemCols);
     float v_max = 0.f;
-    for (int p = ((step0 * kKeys) >> ps) + tid; p < min(pages, (step1 * kKeys) >> ps); p += kThreads) {
+    for (int p = max((step0 * kKeys) >> ps, page_low) + tid; p < min(pages, (step1 * kKeys) >> ps); p += kThreads) {
         const int id = __ldg(table + p);
         if (id < 0 || id >= C.num_pages)
             atomicCAS(g.status, 0, kStatusIndex);
@@ -622,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         // ------------------------- codes into fp16 blocks: keys, and values, 128 threads each
         fewer_registers<kWidenRegs>();
         const int n = job.n, step0 = job.step0, pages = (job.len + (1 << ps) - 1) >> ps;
+        const int page_low = job.page_low;
         const int32_t* table = C.page_table + job.b * C.table_stride;
         const float v_ref = value_ref();
         const bool keys = warp < kValueWarp;
@@ -633,10 +637,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             else
                 widen(S.v_full, S.v_empty, base + L::v, L::vBlock, L::vRing, 2, C.v_codes);
         };
-        // Head's share of the page of group `lane` of 16 keys of step i, -1 past the end.
+        // Head's share of the page of group `lane` of 16 keys of step i, -1 past the end and
+        // before the window.
         auto fetch_pages = [&](int i) {
             const int p = ((step0 + i) * kKeys + lane * 16) >> ps;
-            if (lane >= 8 || i >= n || p >= pages) return -1;
+            if (lane >= 8 || i >= n || p < page_low || p >= pages) return -1;
             const int id = __ldg(table + p);
             return (id < 0 || id >= C.num_pages ? 0 : id) * Hkv + h;
         };

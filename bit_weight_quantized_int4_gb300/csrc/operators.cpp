@@ -154,11 +154,14 @@ q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cac
             return Q4LIN_ERR_INVALID_ARG;
     if (n.overlap(*cache, a->out, ob) || n.overlap(*cache, a->lse, lb) || overlaps(a->out, ob, a->lse, lb))
         return Q4LIN_ERR_INVALID_ARG;
-    // The kernels count query rows and tiles of 64 keys in 32 bits.
+    // The kernels count query rows and tiles of 64 keys in 32 bits, and the prompts' kernel
+    // keeps 32 bytes for each 256 rows of a key/value head in half of the workspace.
+    constexpr int64_t kRowsMost = int64_t{1} << 27;
+    static_assert(8 * (kRowsMost / 256) <= q4lin::kWsFloats / 3, "the pairs of row tiles fit");
     const int64_t group = a->heads / cache->kv_heads, max_query = std::min(a->max_query, a->tokens);
     const int64_t tiles = cache->pages_per_sequence * cache->page_size / 64 + 1;
     int64_t row_tiles, units;
-    if (t > 0x7FFFFFFF || !mul_ok(max_query, group, &row_tiles)) return Q4LIN_ERR_TOO_LARGE;
+    if (t > 0x7FFFFFFF || t / cache->kv_heads > kRowsMost || !mul_ok(max_query, group, &row_tiles)) return Q4LIN_ERR_TOO_LARGE;
     row_tiles = std::min(row_tiles / 8 + 1, a->tokens * group / 8 + 1);
     const int64_t sequences = std::min<int64_t>(cache->batch, 2048);
     if (!mul_ok(row_tiles, tiles * sequences, &units) || !mul_ok(units, cache->kv_heads, &units) ||

@@ -289,7 +289,8 @@ typedef enum { Q4LIN_DTYPE_F32 = 0, Q4LIN_DTYPE_F16 = 1, Q4LIN_DTYPE_BF16 = 2 } 
  *   k_scales, v_scales  float32 [num_pages, kv_heads]
  *   page_table int32 [batch, table_stride]: entry (b, j) is the page of tokens
  *             [j * page_size, (j + 1) * page_size) of sequence b, j < pages_per_sequence.
- *             Entries past a sequence's length are not read (they may be -1).
+ *             Entries past a sequence's length are not read (they may be -1), nor are
+ *             those wholly before the window of an attention's queries.
  * page_size: 16, 32 or 64.  head_dim: 64, 128 or 256.  A page belongs to one sequence
  * while that sequence is appended to (full pages may be shared). */
 typedef struct q4lin_kv_cache {

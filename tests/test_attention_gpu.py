@@ -194,6 +194,27 @@ def test_negative_and_zero_scale(handle):
             check(out, lse, (*ref[:3], np.abs(ref[3])), "f32")
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("count", [1, 5, 200])
+def test_pages_before_the_window_may_be_gone(handle, count, page):
+    """A window of 50 keys behind each query: the pages before the first query's hold NaN scales
+    and have left the table."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(21)
+    n, window = 500, 50
+    host = ops.Cache(rng, [n], 2, page, 64)
+    gone = host.table[0, :(n - count - window + 1) // page]
+    host.ks[gone], host.vs[gone] = np.nan, np.nan
+    device = host.device()
+    device.page_table[0, :len(gone)] = -1
+    q = ops.to_device(rng.standard_normal((count, 4, 64)).astype(np.float32))
+    offsets = np.array([0, count], np.int32)
+    out, lse = q4lin.attention(handle, device, q, ops.to_device(offsets),
+                               ops.to_device(np.array([n], np.int32)), 0.125, window=window)
+    check(out, lse, ops.attention(host, ops.to_host(q), offsets, [n], 0.125, window=window), "f32")
+    assert status(handle) == 0
+
+
 def test_a_wait_that_runs_out_is_reported(handle):
     """Keys that do not come: the kernels give up, leave, and work again afterwards."""
     import torch
