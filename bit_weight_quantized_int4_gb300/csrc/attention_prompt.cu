@@ -23,8 +23,15 @@
 // Few rows over many keys leave SMs idle: their walks over the keys are then cut into equal
 // parts, one CTA each, that a second kernel joins in the order of the keys.
 //
-// Bound: the products (4 head_dim flops a pair and term) together with the exponentials
-// (16 a clock and SM against 128 x 128 products in 8 clocks).
+// Bound: the products, 2 head_dim flops a pair for each of QT + PT terms.  Measured (8 key/value
+// heads of 128, 4 query heads each, the last 2048 of 8192 tokens): 240 us for rotated bf16
+// queries (QT 2, PT 1: 361 Gflop, 1.5 Pflop/s, 0.79 of a large library product's rate), 363 us
+// for fp32 (two terms of both).  While walks run the tensor pipes are busy for 77 % of the time;
+// the scores' products, which read 8 KB of shared memory for 64 clocks of work, take the rest.
+// (Leaving out the exponentials, or the loads or stores of the widened codes, changed the
+// time by less than 4 %; two threads a row instead of one: 260 us; a share of the exponentials
+// as polynomials on the FMA pipes: 249 us and up.)  Whole walks on 152 SMs leave 16 % of them
+// idle at this size, and each has about 10 us around it: the queries, the first keys, the rows.
 #include <algorithm>
 
 #include "q4lin_internal.h"
@@ -118,7 +125,8 @@ struct Layout {
 
 // What a CTA does, left in shared memory by its prologue: the warpgroups read what each needs
 // into its own registers (values kept across their register shares are spilled, and the issuing
-// warp then waits for local memory behind the codes' loads: 351 against 243 us).
+// warp then waits for local memory behind the codes' loads: 351 against 243 us for the case at
+// the head of this file).
 struct Job {
     int64_t o0;
     int b, h, tq, len, row0, row_end, step0, n, cut;
@@ -576,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             float* unit = part_at<D>(g, blockIdx.x);
             // A thread's row goes through shared memory, where nothing else is wanted any more (its
             // pitch keeps the rows of a quarter-warp on banks of their own), and leaves by one
-            // bulk copy: rows stored by their threads took 6 us.
+            // bulk copy: rows stored by their threads took 6 us more.
             const bool wide = cut || DT == Q4LIN_DTYPE_F32;
             const uint32_t row_bytes = wide ? 4 * D : 2 * D, out = base + (uint32_t)r * (4 * D + 16);
             static_assert(2 * kQ * (4 * D + 16) <= L::bytes, "the rows fit");

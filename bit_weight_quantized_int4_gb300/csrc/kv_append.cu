@@ -10,6 +10,11 @@
 // loads (offset -> page -> old scale) for single tokens; what does not depend on the last
 // load is asked for with it.  The old codes of a page are read and written only where its
 // scale grows.
+//
+// Measured: prompts of 8 k tokens, 48.5 MB, 13.2 us: 3.7 TB/s, 0.54 of a copy's bandwidth: 1344
+// CTAs of one page and head each, loads, maximum, codes and stores one after the other, and
+// too short a launch to overlap them more (smaller units and more CTAs an SM took as long).  One
+// token 2.5 us, one for each of 64 sequences 3.6 us.
 #include "q4lin_internal.h"
 #include "serving.cuh"
 

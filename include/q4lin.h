@@ -22,8 +22,9 @@
  *     synchronizes the device and only enqueues kernels on the given stream.  A handle
  *     owns its options, a 4-byte device status word and 64 MiB of device scratch plus
  *     64 KiB of counters (partial sums of launches that split K or the rows across CTAs:
- *     decode GEMV, tensor-core GEMM, small-M tensor-core GEMM, input gradient; the fp16
- *     copy of x of the fp16 tensor-core path), all allocated by q4lin_create.
+ *     decode GEMV, tensor-core GEMM, small-M tensor-core GEMM, input gradient, attention,
+ *     log probabilities; the fp16 copy of x of the fp16 tensor-core path), all allocated
+ *     by q4lin_create.
  *   - Status codes, never exceptions, aborts or prints.  Arguments are validated before
  *     any launch: a non-OK status from validation means nothing was enqueued.
  *   - All device pointers must be device-accessible memory of the handle's device.
@@ -56,7 +57,8 @@ typedef enum {
     Q4LIN_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed                 */
     Q4LIN_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up (see status word) */
     Q4LIN_ERR_NO_DEVICE = 5,   /* no CUDA device with that ordinal                     */
-    Q4LIN_ERR_TOO_LARGE = 6    /* exceeds a fixed capacity (q4lin_run_static_scratch)  */
+    Q4LIN_ERR_TOO_LARGE = 6    /* exceeds a fixed capacity (q4lin_run_static_scratch),
+                                  or what the operators around the linears can index   */
 } q4lin_status_t;
 
 /* Element type of the scales array. */
@@ -94,14 +96,15 @@ typedef enum {
     Q4LIN_OPT_NIBBLE_EVEN_HIGH = 2,
     /* Time limit, in nanoseconds of the GPU's global timer, of every bounded
      * device-side wait (mbarrier polls) of the TMA-fed kernels (decode and multi-row
-     * GEMV, tensor-core GEMM, input gradient, attention); <= 0 restores the default (2 s).  When a
-     * wait runs out the kernel records code 1 in the handle's status word, stops issuing
+     * GEMV, tensor-core GEMM, input gradient, attention); <= 0 restores the default
+     * (2 s).  When a wait runs out the kernel records code 1 in the handle's status word, stops issuing
      * work, lets its own copies (and MMAs) in flight finish, frees its tensor memory and
      * returns; its output is then undefined. */
     Q4LIN_OPT_WAIT_LIMIT = 3,
     /* 1: launch with programmatic dependent launch, so a kernel may start streaming
      * its weights while the previous kernel on the stream drains (default 0).  The
-     * preceding kernel must not write this call's qweight or scales. */
+     * preceding kernel must not write this call's qweight or scales.  (The linears; the
+     * operators around them start when the previous call has ended.) */
     Q4LIN_OPT_PDL = 4,
     /* Test hook, default 0.  1: the tensor-core kernel's copy engine skips the first
      * pipeline stage, the multi-row GEMV's copy engine issues nothing, and the attention
@@ -275,7 +278,10 @@ Q4LIN_API q4lin_status_t q4lin_run_requant(q4lin_handle_t handle, const float* l
  * only.  An index that points outside its array (a page >= num_pages or < 0, a position
  * past the page table or the rotation table, offsets that decrease or pass `tokens`, a
  * token >= vocabulary) makes the kernel leave out what it would have touched and record
- * code 4 in the handle's status word; nothing out of range is read or written. */
+ * code 4 in the handle's status word; nothing out of range is read or written.
+ *
+ * Sizes whose rows, pages or positions the kernels cannot count (2^31 rows of queries or
+ * logits, 2^27 query rows of one key/value head) return Q4LIN_ERR_TOO_LARGE. */
 
 /* Element type of keys, values, queries, attention outputs and logits. */
 typedef enum { Q4LIN_DTYPE_F32 = 0, Q4LIN_DTYPE_F16 = 1, Q4LIN_DTYPE_BF16 = 2 } q4lin_dtype_t;
