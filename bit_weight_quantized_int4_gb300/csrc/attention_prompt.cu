@@ -32,6 +32,8 @@
 // time by less than 4 %; two threads a row instead of one: 260 us; a share of the exponentials
 // as polynomials on the FMA pipes: 249 us and up.)  Whole walks on 152 SMs leave 16 % of them
 // idle at this size, and each has about 10 us around it: the queries, the first keys, the rows.
+// Cutting the last round's walks so that all SMs end together took as long (239 us, and the
+// joining kernel's time on top): busier SMs were slower ones.
 #include <algorithm>
 
 #include "q4lin_internal.h"
@@ -821,65 +823,87 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     if (warp == kIssueWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// The rows of walks that were cut: one warp per query row, a part after another.
+// The rows of walks that were cut: a warp takes PER rows of a pair of tiles, ROWS at a time with
+// AHEAD parts of each in flight, in the order of the keys.
 constexpr int kJoinWarps = 4;
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) attention_prompt_join_kernel(const PromptArgs g) {
-    constexpr int kAhead = 8;
+template <int D, int PER, int ROWS, int AHEAD>
+__device__ __forceinline__ void join_rows(const PromptArgs& g, int64_t unit0, int stride, int count, int r0, int rows,
+                                          int64_t index0, int head0, int group) {
     const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5), token = i / g.a.heads;
-    const int head = (int)(i - token * g.a.heads), group = (int)(g.a.heads / g.cache.kv_heads), h = head / group;
-    if (token >= g.a.tokens) return;
-    const int64_t b = find_sequence(g.cache.batch, token, [&](int64_t k) { return (int64_t)__ldg(g.a.offsets + k); });
-    const int64_t o0 = __ldg(g.a.offsets + b);
-    const Prompt p = prompt_of(g, b);
-    griddep_wait();
-    if (p.pairs == 0 || token < o0 || token >= o0 + p.tq) return;
-    const int parts = __ldcg(g.plan).x, each = __ldcg(g.plan).y;
-    if (parts == 1) return;
-    const int row = (int)(token - o0) * group + head - h * group, pair = row / (2 * kQ), r = row % (2 * kQ);
-    int first, last;
-    walk_of(g, p, pair, &first, &last);
-    const int count = max(1, (last - first + each - 1) / each);
-    const int64_t unit0 = ((int64_t)__ldcg(g.first_pair + b) + p.pairs - 1 - pair) * parts * g.cache.kv_heads + h;
-    float mx = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool on = lane < D / 4;
-    for (int c = 0; c < count; c += kAhead) {
-        float pm[kAhead], pl[kAhead];
-        float4 po[kAhead];
+#pragma unroll 1
+    for (int r = r0; r < r0 + PER; r += ROWS) {
+        float mx[ROWS], l[ROWS];
+        float4 o[ROWS];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            pm[k] = -INFINITY, pl[k] = 0.f, po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c + k < count) {
-                const float* unit = part_at<D>(g, unit0 + (int64_t)(c + k) * g.cache.kv_heads);
-                pm[k] = __ldcg(unit + 2 * kQ * D + r), pl[k] = __ldcg(unit + 2 * kQ * D + 2 * kQ + r);
-                if (on) po[k] = __ldcg(reinterpret_cast<const float4*>(unit + r * D) + lane);
+        for (int q = 0; q < ROWS; ++q) mx[q] = -INFINITY, l[q] = 0.f, o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < count; c += AHEAD) {
+            float pm[ROWS][AHEAD], pl[ROWS][AHEAD];
+            float4 po[ROWS][AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float* unit = part_at<D>(g, unit0 + (int64_t)(c + k) * stride);
+#pragma unroll
+                for (int q = 0; q < ROWS; ++q) {
+                    pm[q][k] = -INFINITY, pl[q][k] = 0.f, po[q][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c + k < count && r + q < rows) {
+                        pm[q][k] = __ldcg(unit + 2 * kQ * D + r + q), pl[q][k] = __ldcg(unit + 2 * kQ * D + 2 * kQ + r + q);
+                        if (on) po[q][k] = __ldcg(reinterpret_cast<const float4*>(unit + (r + q) * D) + lane);
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < ROWS; ++q) {
+                float top = mx[q];
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) top = fmaxf(top, pm[q][k]);
+                const float from = top == -INFINITY ? 0.f : top, old = ex2(mx[q] - from);
+                o[q].x *= old, o[q].y *= old, o[q].z *= old, o[q].w *= old, l[q] *= old, mx[q] = top;
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const float w = ex2(pm[q][k] - from);
+                    o[q].x = fmaf(po[q][k].x, w, o[q].x), o[q].y = fmaf(po[q][k].y, w, o[q].y);
+                    o[q].z = fmaf(po[q][k].z, w, o[q].z), o[q].w = fmaf(po[q][k].w, w, o[q].w);
+                    l[q] = fmaf(pl[q][k], w, l[q]);
+                }
             }
         }
-        float top = mx;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, pm[k]);
-        const float from = top == -INFINITY ? 0.f : top, old = ex2(mx - from);
-        o.x *= old, o.y *= old, o.z *= old, o.w *= old, l *= old, mx = top;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const float w = ex2(pm[k] - from);
-            o.x = fmaf(po[k].x, w, o.x), o.y = fmaf(po[k].y, w, o.y);
-            o.z = fmaf(po[k].z, w, o.z), o.w = fmaf(po[k].w, w, o.w);
-            l = fmaf(pl[k], w, l);
+        for (int q = 0; q < ROWS; ++q) {
+            if (r + q >= rows) break;
+            const float inv = l[q] != 0.f ? 1.f / l[q] : 0.f;
+            const int at = head0 + r + q, step = at / group;  // tokens from index0's
+            const int64_t index = index0 + step * g.a.heads + (at - step * group);
+            if (on && g.a.dtype == Q4LIN_DTYPE_F32)
+                reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + index * D)[lane] =
+                    make_float4(o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv);
+            else if (on)
+                reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D)[lane] =
+                    make_uint2(to_16x2(o[q].x * inv, o[q].y * inv, g.a.dtype), to_16x2(o[q].z * inv, o[q].w * inv, g.a.dtype));
+            if (lane == 0 && g.a.lse)
+                g.a.lse[index] = l[q] != 0.f ? ((mx[q] == -INFINITY ? 0.f : mx[q]) + lg2(l[q]) - kBase) * kLn2 : -INFINITY;
         }
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    const int64_t index = token * g.a.heads + head;
-    if (on && g.a.dtype == Q4LIN_DTYPE_F32)
-        reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + index * D)[lane] =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    else if (on)
-        reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D)[lane] =
-            make_uint2(to_16x2(o.x * inv, o.y * inv, g.a.dtype), to_16x2(o.z * inv, o.w * inv, g.a.dtype));
-    if (lane == 0 && g.a.lse)
-        g.a.lse[index] = l != 0.f ? ((mx == -INFINITY ? 0.f : mx) + lg2(l) - kBase) * kLn2 : -INFINITY;
+}
+template <int D, int PER, int ROWS, int AHEAD>
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_prompt_join_kernel(const PromptArgs g) {
+    const int i = ((int)blockIdx.x * kJoinWarps + (int)(threadIdx.x >> 5)) * PER;
+    const int Hkv = (int)g.cache.kv_heads, group = (int)(g.a.heads / g.cache.kv_heads);
+    const int u = i / (2 * kQ), r0 = i % (2 * kQ), h = u % Hkv;
+    griddep_wait();
+    // (The launch has no more pairs than the plan has room for: their records come with it.)
+    const int pair = u / Hkv;
+    const int4 plan = __ldcg(g.plan), j0 = __ldcg(g.plan + 1 + 2 * pair), j1 = __ldcg(g.plan + 2 + 2 * pair);
+    const int parts = plan.x, each = plan.y;
+    if (parts == 1 || pair >= plan.z) return;
+    const int row0 = j0.w * 2 * kQ, rows = min(j0.y * group - row0, 2 * kQ);
+    if (r0 >= rows) return;
+    const int count = max(1, (j1.y - j1.x + each - 1) / each);
+    // Row r is head head0 + r of the pair's first token, the heads of a group counted on.
+    const int token = row0 / group, head0 = row0 - token * group;
+    const int64_t index0 = ((int64_t)j1.z + token) * g.a.heads + h * group;
+    join_rows<D, PER, ROWS, AHEAD>(g, (int64_t)pair * parts * Hkv + h, Hkv, count, r0, rows, index0, head0, group);
 }
 
 template <int D, int QT, int PT, int DT>
@@ -920,13 +944,20 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     main.numAttrs = 1;
     e = cudaLaunchKernelEx(&main, attention_prompt_kernel<D, QT, PT, DT>, g);
     if (e != cudaSuccess || g.most_parts == 1) return e;
+    // A row a warp while all of them fit on the SMs at once, more beyond (8 key/value heads of 128,
+    // 4 query heads each, us for 1 / 4 rows a warp: 32 queries on 8192 keys 25.9 / 34.9, 128 40.1 /
+    // 42.8, 300 on 2000 39.4 / 36.6, 512 on 8192 91.4 / 86.8, in fp32 130.5 / 125.5).
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((g.a.tokens * g.a.heads + kJoinWarps - 1) / kJoinWarps));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = c.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_prompt_join_kernel<D>, g);
+    if (g.a.tokens * g.a.heads <= 40 * c.sm_count) {
+        cfg.gridDim = dim3((unsigned)(units * (2 * kQ / kJoinWarps)));
+        return cudaLaunchKernelEx(&cfg, attention_prompt_join_kernel<D, 1, 1, 8>, g);
+    }
+    cfg.gridDim = dim3((unsigned)(units * (2 * kQ / (4 * kJoinWarps))));
+    return cudaLaunchKernelEx(&cfg, attention_prompt_join_kernel<D, 4, 2, 4>, g);
 }
 
 }  // namespace

@@ -148,6 +148,35 @@ def test_prompt_kernel(handle, lengths, counts, heads, kv_heads, page, dim, dtyp
         handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens,window", [(5120, 0), (7700, 0), (7700, 3000), (10000, 0)])
+def test_more_walks_than_sms(handle, tokens, window, dtype):
+    """Whole walks and those of a last round that are cut; rows all over it, the last ones too."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(tokens)
+    heads, dim = 8, 64
+    host = ops.Cache(rng, [tokens], heads, 64, dim)
+    q = ops.to_device(rng.standard_normal((tokens, heads, dim)).astype(np.float32), dtype)
+    offsets = np.array([0, tokens], np.int32)
+    out, lse = q4lin.attention(handle, host.device(), q, ops.to_device(offsets),
+                               ops.to_device(np.array([tokens], np.int32)), 0.125, window=window)
+    rows = np.concatenate([[0, 1, 255, 256, tokens - 1], rng.integers(0, tokens, 120)])
+    at = np.concatenate([np.arange(5) % heads, rng.integers(0, heads, 120)])
+    want = [[], [], [], []]
+    keys = [(host.keys(0, tokens, h), host.values(0, tokens, h)) for h in range(heads)]
+    x = ops.to_host(q)
+    for i, h in zip(rows, at):
+        seen = slice(max(0, i - window + 1) if window else 0, i + 1)
+        k, v = keys[h][0][seen], keys[h][1][seen]
+        s = 0.125 * (k @ x[i, h])
+        p = np.exp(s - s.max())
+        for one, value in zip(want, (p @ v / p.sum(), s.max() + np.log(p.sum()), np.abs(v).max(),
+                                     (0.125 * (np.abs(k) @ np.abs(x[i, h]))).max())):
+            one.append(value)
+    check(out[rows, at], lse[rows, at], [np.array(w) for w in want], dtype)
+    assert status(handle) == 0
+
+
 def test_values_of_very_different_pages(handle):
     """Pages whose values are 2^12 apart, and one of zeros: rows that see only small ones."""
     import torch
