@@ -13,8 +13,8 @@
 // kernel adds in the order of the keys, so the result does not depend on the schedule.
 //
 // Measured (8 key/value heads of 128, 4 query heads each): 64 sequences of up to 8192 tokens,
-// 652 MB, 110 us: 5.9 TB/s, 0.87 of a copy's bandwidth; one sequence of 131071 tokens, 269 MB,
-// 53.6 us: 5.0 TB/s, the start and the join a sixth of it.  One of 701 tokens (0.7 MB) 8.9 us,
+// 652 MB, 110 to 114 us: 5.8 TB/s, 0.86 of a copy's bandwidth; one sequence of 131071 tokens, 269
+// MB, 54 us: 5.0 TB/s, the start and the join a sixth of it.  One of 701 tokens (0.7 MB) 8.9 us,
 // 9 drafts of up to 5 tokens behind a window of 1024 (10 MB, 7 query heads) 21.8 us: the chain of
 // dependent loads, from the offsets to the page table to the first keys, and two launches.
 //

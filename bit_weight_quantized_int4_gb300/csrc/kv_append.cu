@@ -11,10 +11,11 @@
 // load is asked for with it.  The old codes of a page are read and written only where its
 // scale grows.
 //
-// Measured: prompts of 8 k tokens, 48.5 MB, 13.2 us: 3.7 TB/s, 0.54 of a copy's bandwidth: 1344
-// CTAs of one page and head each, loads, maximum, codes and stores one after the other, and
-// too short a launch to overlap them more (smaller units and more CTAs an SM took as long).  One
-// token 2.5 us, one for each of 64 sequences 3.6 us.
+// Measured: prompts of 8 k tokens, 48.5 MB, 13.2 us where the linears have just written them (in
+// L2), 19.2 us from memory: 2.5 TB/s, 0.37 of a copy's bandwidth.  1344 CTAs of one page and head
+// each in three rounds, loads, maximum, codes and stores one after the other.  (Elements in
+// shared memory, six CTAs an SM: 20.8 us; heads side by side: 19.5; angles asked for with
+// the keys: 18.8, but 13.7 from L2.)  One token 2.5 us, one for each of 64 sequences 3.6 us.
 #include "q4lin_internal.h"
 #include "serving.cuh"
 

@@ -15,9 +15,9 @@ namespace {
 
 // Query rows (tokens x heads) per key/value head up to which a sequence's attention goes
 // through the kernel that splits the keys (us, 8 key/value heads of 128, split / prompts' kernel,
-// bf16: one sequence of 8192 keys, 32 rows 28.8 / 26.7, 64 rows 43.0 / 27.9; of 65536, 32 rows
-// 100 / 84, 64 rows 181 / 85; 8 sequences of 2000, 32 rows 35 / 39, 64 rows 45 / 40; 32 of 4000,
-// 32 rows 119 / 148, 64 rows 191 / 147; fp32, 8 of 2000: 31 / 47 and 41 / 48).
+// bf16: one sequence of 8192 keys, 32 rows 27.9 / 28.7, 64 rows 42.2 / 29.5; of 65536, 32 rows
+// 96 / 86, 64 rows 174 / 88; 8 sequences of 2000, 32 rows 34 / 47, 64 rows 44 / 49; 32 of 4000,
+// 32 rows 112 / 149, 64 rows 181 / 147; fp32, 8 of 2000: 31 / 47 and 41 / 48).
 constexpr int64_t kSplitRows = 48;
 
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
