@@ -497,8 +497,9 @@ def attention(handle: Handle, cache: KVCache, query, offsets, lengths, scale: fl
               causal: bool = True, window: int = 0, out=None, lse=None, stream=None):
     """Attention of query [tokens, heads, head_dim] over the cache (q4lin_run_attention).
     lengths[b] counts sequence b's tokens in the cache, those of its queries included;
-    max_query: no sequence has more query tokens (default: all of them).  Returns (out, lse):
-    out like query, lse float32 [tokens, heads]."""
+    max_query: no sequence has more query tokens (default: all of them; 1 for single tokens
+    spares a batch the launches for prompts).  Returns (out, lse): out like query, lse float32
+    [tokens, heads]."""
     c = cache.args
     cos, sin = rope or (None, None)
     _check_device(handle, cache.k_codes, query, offsets, lengths, out, lse, cos, sin)
