@@ -3,19 +3,20 @@
 // Two kernels.  Prompts: one CTA per (page that receives tokens, head, keys or values).  It
 // holds the page's new tokens in registers between the two steps of the quantisation (the
 // largest |x|, then the codes), so they are read once; a thread's units are eight consecutive
-// tokens of the same eight channels, so that the transposed values leave as eight consecutive
-// bytes per channel.  Few tokens a sequence: one warp per (page, head, keys or values).
+// tokens of the same eight channels, so that the values are transposed in registers; a whole
+// page's codes leave through shared memory.  Few tokens a sequence: one warp per (page, head, keys or values).
 //
 // Bound: memory traffic (size + 1 bytes per element) for prompts, the chain of dependent
 // loads (offset -> page -> old scale) for single tokens; what does not depend on the last
 // load is asked for with it.  The old codes of a page are read and written only where its
 // scale grows.
 //
-// Measured: prompts of 8 k tokens, 48.5 MB, 13.2 us where the linears have just written them (in
-// L2), 19.2 us from memory: 2.5 TB/s, 0.37 of a copy's bandwidth.  1344 CTAs of one page and head
-// each in three rounds, loads, maximum, codes and stores one after the other.  (Elements in
-// shared memory, six CTAs an SM: 20.8 us; heads side by side: 19.5; angles asked for with
-// the keys: 18.8, but 13.7 from L2.)  One token 2.5 us, one for each of 64 sequences 3.6 us.
+// Measured: prompts of 8 k tokens, 48.5 MB, 12.7 us where the linears have just written them (in
+// L2), 18.8 us from memory: 2.6 TB/s, 0.38 of a copy's bandwidth.  1344 CTAs of one page and head
+// each in three rounds, loads, maximum, codes and stores one after the other: without the last
+// two 13.2 us from memory, without the angles 3 less.  (Elements in shared memory, six CTAs an
+// SM: 20.8 us; heads side by side: 19.5; angles asked for with the keys: 18.4, but 13.3 from
+// L2; five CTAs an SM: 18.8 and 13.2.)  One token 2.5 us, one for each of 64 sequences 3.6 us.
 #include "q4lin_internal.h"
 #include "serving.cuh"
 
@@ -176,8 +177,9 @@ __device__ __forceinline__ void round_again(const AppendArgs& g, uint8_t* codes,
 template <int THREADS, int DT>
 __global__ void __launch_bounds__(THREADS) kv_append_pages_kernel(const AppendArgs g) {
     __shared__ float s_amax[THREADS / 32];
+    __shared__ uint4 s_codes[THREADS * 4];
     const q4lin_kv_cache_t& C = g.cache;
-    const int D = (int)C.head_dim, units = D / 8, h = blockIdx.y;
+    const int D = (int)C.head_dim, P = 1 << g.page_shift, units = D / 8, h = blockIdx.y;
     const bool keys = blockIdx.z == 0;
     const Share s = find_share<false>(g, blockIdx.x);
     if (s.n == 0) return;
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(THREADS) kv_append_pages_kernel(const AppendAr
     const int64_t at0 = s.first * ts + h * (keys ? g.a.k_head_stride : g.a.v_head_stride);
     const bool vec = keys ? g.k_vec : g.v_vec;
     bool turned = false;
-    int lo = 8 * u, hi = 8 * u + 4;
+    int lo = 4 * u, hi = D / 2 + 4 * u;
     if (keys) rope_channels(g.a.rope, u, &turned, &lo, &hi);
     float x[kUnits][8];
 #pragma unroll
@@ -242,36 +244,75 @@ __global__ void __launch_bounds__(THREADS) kv_append_pages_kernel(const AppendAr
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
         code[i][0] = four_codes(x[i], inv, finite), code[i][1] = four_codes(x[i] + 4, inv, finite);
+    const int slot0 = q * kUnits;
+    const bool whole = slot0 >= s.at && slot0 + kUnits <= s.at + s.n;
+    if (!keys && whole) {
+        // 4 x 4 byte transposes: word i of channel d holds slots 4 i .. 4 i + 3.
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < kUnits; i += 4) {
+                const uint32_t a = code[i][w], b4 = code[i + 1][w], c = code[i + 2][w], d = code[i + 3][w];
+                const uint32_t ab0 = ptx::prmt(a, b4, 0x5140u), ab1 = ptx::prmt(a, b4, 0x7362u);
+                const uint32_t cd0 = ptx::prmt(c, d, 0x5140u), cd1 = ptx::prmt(c, d, 0x7362u);
+                code[i][w] = ptx::prmt(ab0, cd0, 0x5410u), code[i + 1][w] = ptx::prmt(ab0, cd0, 0x7632u);
+                code[i + 2][w] = ptx::prmt(ab1, cd1, 0x5410u), code[i + 3][w] = ptx::prmt(ab1, cd1, 0x7632u);
+            }
+    }
+    if (s.n == P) {
+        // A whole page leaves by 16 bytes a thread, one after the other, through shared memory
+        // (stored from where they are, 4 or 8 bytes at a time, 13.2 and 19.2 us for the prompts at
+        // the head of this file instead of 12.7 and 18.8).
+        // There, 8 slots of a channel (of G such groups) trade places by its number.
+        uint8_t* stage = reinterpret_cast<uint8_t*>(s_codes);
+        const int G = P / kUnits;
+        if (q < G) {
+            if (keys) {
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    *reinterpret_cast<uint32_t*>(stage + (slot0 + i) * D + lo) = code[i][0];
+                    *reinterpret_cast<uint32_t*>(stage + (slot0 + i) * D + hi) = code[i][1];
+                }
+            } else {
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int channel = (w ? hi : lo) + d;
+                        *reinterpret_cast<uint2*>(stage + channel * P + ((q ^ (channel >> 2)) & (G - 1)) * kUnits) =
+                            make_uint2(code[d][w], code[4 + d][w]);
+                    }
+            }
+        }
+        __syncthreads();
+        for (int n = threadIdx.x; n < P * D / 16; n += THREADS) {
+            uint4 v = s_codes[n];
+            if (!keys) {
+                const int channel = (16 * n) >> g.page_shift, k = (channel >> 2) & (G - 1);
+                v = s_codes[n ^ (k >> 1)];
+                if (k & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+            }
+            reinterpret_cast<uint4*>(codes)[n] = v;
+        }
+        return;
+    }
     if (keys) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            const int slot = q * kUnits + i, r = slot - s.at;
+            const int slot = slot0 + i, r = slot - s.at;
             if (r < 0 || r >= s.n) continue;
             *reinterpret_cast<uint32_t*>(codes + slot * D + lo) = code[i][0];
             *reinterpret_cast<uint32_t*>(codes + slot * D + hi) = code[i][1];
         }
         return;
     }
-    const int slot0 = q * kUnits;
-    const bool whole = slot0 >= s.at && slot0 + kUnits <= s.at + s.n;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         if (whole) {
-            // 4 x 4 byte transposes: word i of channel d holds slots 4 i .. 4 i + 3.
-            uint32_t t[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t a = code[4 * i][w], b4 = code[4 * i + 1][w], c = code[4 * i + 2][w],
-                               d = code[4 * i + 3][w];
-                const uint32_t ab0 = ptx::prmt(a, b4, 0x5140u), ab1 = ptx::prmt(a, b4, 0x7362u);
-                const uint32_t cd0 = ptx::prmt(c, d, 0x5140u), cd1 = ptx::prmt(c, d, 0x7362u);
-                t[i][0] = ptx::prmt(ab0, cd0, 0x5410u), t[i][1] = ptx::prmt(ab0, cd0, 0x7632u);
-                t[i][2] = ptx::prmt(ab1, cd1, 0x5410u), t[i][3] = ptx::prmt(ab1, cd1, 0x7632u);
-            }
 #pragma unroll
             for (int d = 0; d < 4; ++d)
                 *reinterpret_cast<uint2*>(codes + (((w ? hi : lo) + d) << g.page_shift) + slot0) =
-                    make_uint2(t[0][d], t[1][d]);
+                    make_uint2(code[d][w], code[4 + d][w]);
         } else {
 #pragma unroll
             for (int i = 0; i < kUnits; ++i) {
