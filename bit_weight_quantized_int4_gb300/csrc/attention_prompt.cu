@@ -25,8 +25,8 @@
 //
 // Bound: the products, 2 head_dim flops a pair for each of QT + PT terms.  Measured (8 key/value
 // heads of 128, 4 query heads each, the last 2048 of 8192 tokens): 240 us for rotated bf16
-// queries (QT 2, PT 1: 361 Gflop, 1.5 Pflop/s, 0.79 of a large library product's rate), 363 us
-// for fp32 (two terms of both).  While walks run the tensor pipes are busy for 77 % of the time;
+// queries (QT 2, PT 1: 361 Gflop, 1.5 Pflop/s, 0.79 of a large library product's rate), 424 us
+// for fp32 (two terms of both, and outputs taken out every 16 steps: 363 without).  While walks run the tensor pipes are busy for 77 % of the time;
 // the scores' products, which read 8 KB of shared memory for 64 clocks of work, take the rest.
 // (Leaving out the exponentials, or the loads or stores of the widened codes, changed the
 // time by less than 4 %; two threads a row instead of one: 260 us; a share of the exponentials
@@ -56,6 +56,10 @@ static_assert(2 * kSoftRegs + 2 * kWidenRegs + kIssueRegs <= 5 * 96, "registers 
 constexpr int kMaxBatch = 1024;  // sequences per launch
 constexpr int kScaleSlots = 5;  // steps whose scales are kept: the widening warps are up to four ahead
 constexpr float kBase = 7.f;    // weights are kept as 2^7 p ...
+// Tensor cores cut off what a product's sum has no room for, so an error of one sign grows with
+// the steps that O adds up there (16384 keys: 3.6e-5 of the norm of fp32 outputs).  fp32 outputs
+// are taken out every kDrain steps and added up with rounding, in their own place in memory.
+constexpr int kDrain = 16;
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
 // A score's factor is at least this, so that a masked score (-infinity) stays one.
 constexpr float kLeastFactor = 1e-37f;
@@ -392,6 +396,34 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
     if (lane == 0) *g.plan = make_int4(parts, max(1, (longest + parts - 1) / parts), pairs, 0);
 }
 
+// Where row `row` of a job (row r of its pair of tiles) has its fp32 outputs, or its sums where
+// the walk is cut.
+template <int D>
+__device__ __forceinline__ float* out_row(const PromptArgs& g, const volatile Job& job, int row, int r) {
+    if (job.cut) return part_at<D>(g, blockIdx.x) + r * D;
+    const int group = (int)(g.a.heads / g.cache.kv_heads), token = row / group;
+    const int64_t index = (job.o0 + token) * g.a.heads + job.h * group + (row - token * group);
+    return static_cast<float*>(g.a.out) + index * D;
+}
+// y += keep * to[0 .. 15] where something is there, and back to it if it is to stay.
+__device__ __forceinline__ void add_16(float* to, uint32_t (&y)[16], float keep, bool there, bool stays) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float4 v = make_float4(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1]), __uint_as_float(y[4 * e + 2]),
+                               __uint_as_float(y[4 * e + 3]));
+        if (there) {
+            const float4 old = reinterpret_cast<const float4*>(to)[e];
+            v.x = fmaf(old.x, keep, v.x), v.y = fmaf(old.y, keep, v.y);
+            v.z = fmaf(old.z, keep, v.z), v.w = fmaf(old.w, keep, v.w);
+        }
+        if (stays)
+            reinterpret_cast<float4*>(to)[e] = v;
+        else
+            y[4 * e] = __float_as_uint(v.x), y[4 * e + 1] = __float_as_uint(v.y), y[4 * e + 2] = __float_as_uint(v.z),
+                  y[4 * e + 3] = __float_as_uint(v.w);
+    }
+}
+
 template <int D, int QT, int PT, int DT>
 __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const PromptArgs g) {
     using L = Layout<D, QT>;
@@ -497,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const int limit = !in ? -1 : g.a.causal ? position : len - 1;
         const int low = g.a.window > 0 ? (int)max((int64_t)0, (int64_t)position - g.a.window + 1) : 0;
         const float factor = S.factor[r];
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, m_out = -INFINITY;  // m_out: of what was taken out
         bool ok = true;
         const int steps = tile == 0 || row_end - row0 > kQ ? n : 0;
         for (int i = 0; i < steps; ++i) {
@@ -541,6 +573,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                         tmem_st16_async(o_at + 16 * c, y);
                     }
                 }
+            }
+            if (DT == Q4LIN_DTYPE_F32 && i > 0 && i % kDrain == 0) {
+                float* to = out_row<D>(g, job, row, r);
+                const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t y[16];
+                    __syncwarp();  // the load is the whole warp's
+                    tmem_ld16(o_at + 16 * c, y);
+                    if (in) add_16(to + 16 * c, y, keep, i > kDrain, true);
+                }
+                __syncwarp();
+                m_out = m;
             }
             const float origin = kBase - (m == -INFINITY ? 0.f : m);
 #pragma unroll
@@ -601,6 +646,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0u;
                 }
+                if (DT == Q4LIN_DTYPE_F32 && steps > kDrain && in) {
+                    const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
+                    float* from = out_row<D>(g, job, row, r) + 32 * c;
+                    add_16(from, *reinterpret_cast<uint32_t(*)[16]>(x), keep, true, false);
+                    add_16(from + 16, *reinterpret_cast<uint32_t(*)[16]>(x + 16), keep, true, false);
+                }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(l == 0.f ? 0.f : __uint_as_float(x[e]) * f);
                 if (wide) {
@@ -619,6 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                     }
                 }
             }
+            // (What was taken out went through the generic proxy to the same place.)
+            if (DT == Q4LIN_DTYPE_F32) asm volatile("fence.proxy.async;" ::: "memory");
             fence_async_shared();
             if (in) {
                 void* to = cut ? static_cast<void*>(unit + r * D)
@@ -796,7 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                         for (int kk = 0; kk < 4; ++kk)
                             mma_f16_ts(leader, tmem + tile * 128,
                                        tmem + kScoreCol + tile * kKeys + term * 64 + (half * 4 + kk) * 8,
-                                       desc(v_low + 2 * kk), idesc_o, i > 0 || half + term + kk > 0);
+                                       desc(v_low + 2 * kk), idesc_o,
+                                       (DT == Q4LIN_DTYPE_F32 ? i % kDrain != 0 : i > 0) || half + term + kk > 0);
                     if (last) mma_commit(leader, bar(S.v_empty[slot]));
                     if (++slot == L::vRing) slot = 0, par ^= 1u;
                 }
@@ -946,7 +1000,8 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     if (e != cudaSuccess || g.most_parts == 1) return e;
     // A row a warp while all of them fit on the SMs at once, more beyond (8 key/value heads of 128,
     // 4 query heads each, us for 1 / 4 rows a warp: 32 queries on 8192 keys 25.9 / 34.9, 128 40.1 /
-    // 42.8, 300 on 2000 39.4 / 36.6, 512 on 8192 91.4 / 86.8, in fp32 130.5 / 125.5).
+    // 42.8, 300 on 2000 39.4 / 36.6, 512 on 8192 91.4 / 86.8, in fp32, without what is taken
+    // out, 130.5 / 125.5).
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = c.stream;

@@ -177,6 +177,30 @@ def test_more_walks_than_sms(handle, tokens, window, dtype):
     assert status(handle) == 0
 
 
+def test_long_fp32_prompt(handle):
+    """Sums over 16384 keys.  The tensor cores cut off instead of rounding: at most 2^-24 of a sum
+    on average for each of the 256 additions (2048 keys in steps of 16, two terms) between two
+    roundings to memory, 1.5e-5 of the outputs' norm."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(31)
+    n, tokens, heads, dim = 16384, 2048, 8, 64
+    host = ops.Cache(rng, [n], heads, 16, dim)
+    q = ops.to_device((rng.standard_normal((tokens, heads, dim)) * 1.2).astype(np.float32))
+    q = q.repeat_interleave(3, 1)  # 192 walks
+    out, _ = q4lin.attention(handle, host.device(), q, ops.to_device(np.array([0, tokens], np.int32)),
+                             ops.to_device(np.array([n], np.int32)), 0.125)
+    x, got, want = ops.to_host(q), ops.to_host(out), []
+    rows = [(int(i), h) for h in range(heads) for i in rng.integers(0, tokens, 6)]
+    for i, h in rows:
+        k, v = host.keys(0, n, h)[:n - tokens + i + 1], host.values(0, n, h)[:n - tokens + i + 1]
+        s = 0.125 * (k @ x[i, 3 * h])
+        p = np.exp(s - s.max())
+        want.append(p @ v / p.sum())
+    want = np.array(want)
+    error = np.array([got[i, 3 * h] for i, h in rows]) - want
+    assert np.linalg.norm(error) <= 1.5e-5 * np.linalg.norm(want)
+
+
 def test_values_of_very_different_pages(handle):
     """Pages whose values are 2^12 apart, and one of zeros: rows that see only small ones."""
     import torch
