@@ -25,8 +25,8 @@
 //
 // Bound: the products, 2 head_dim flops a pair for each of QT + PT terms.  Measured (8 key/value
 // heads of 128, 4 query heads each, the last 2048 of 8192 tokens): 240 us for rotated bf16
-// queries (QT 2, PT 1: 361 Gflop, 1.5 Pflop/s, 0.79 of a large library product's rate), 424 us
-// for fp32 (two terms of both, and outputs taken out every 16 steps: 363 without).  While walks run the tensor pipes are busy for 77 % of the time;
+// queries (QT 2, PT 1: 361 Gflop, 1.5 Pflop/s, 0.79 of a large library product's rate), 483 us
+// for fp32 (two terms of both, and outputs taken out every 8 steps: 363 without).  While walks run the tensor pipes are busy for 77 % of the time;
 // the scores' products, which read 8 KB of shared memory for 64 clocks of work, take the rest.
 // (Leaving out the exponentials, or the loads or stores of the widened codes, changed the
 // time by less than 4 %; two threads a row instead of one: 260 us; a share of the exponentials
@@ -58,8 +58,10 @@ constexpr int kScaleSlots = 5;  // steps whose scales are kept: the widening war
 constexpr float kBase = 7.f;    // weights are kept as 2^7 p ...
 // Tensor cores cut off what a product's sum has no room for, so an error of one sign grows with
 // the steps that O adds up there (16384 keys: 3.6e-5 of the norm of fp32 outputs).  fp32 outputs
-// are taken out every kDrain steps and added up with rounding, in their own place in memory.
-constexpr int kDrain = 16;
+// are taken out every kDrain steps and added up with rounding, in their own place in memory: 3e-6
+// at any length, about what sums in plain fp32 have (every 16 steps: 5e-6, and 424 us instead
+// of 483 for the prompt at the head of this file).
+constexpr int kDrain = 8;
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
 // A score's factor is at least this, so that a masked score (-infinity) stays one.
 constexpr float kLeastFactor = 1e-37f;
