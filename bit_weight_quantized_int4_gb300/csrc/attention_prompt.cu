@@ -579,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             if (DT == Q4LIN_DTYPE_F32 && i > 0 && i % kDrain == 0) {
                 float* to = out_row<D>(g, job, row, r);
                 const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
+                tmem_wait_st();  // O may just have been rescaled; loads do not wait for stores
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t y[16];

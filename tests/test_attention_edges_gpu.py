@@ -1,0 +1,73 @@
+"""Attention over the paged 8-bit cache where its walks, masks and indices are at their limits:
+selected rows against float64, with the tolerance of test_attention_gpu."""
+import numpy as np
+import pytest
+
+from tests import _operators as ops
+from tests.test_attention_gpu import check, status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def handle():
+    from bit_weight_quantized_int4_gb300 import q4lin
+    h = q4lin.Handle(0)
+    yield h
+    h.close()
+
+
+def attend(handle, host, q, counts, lengths, scale, cache=None, **more):
+    from bit_weight_quantized_int4_gb300 import q4lin
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    return q4lin.attention(handle, host.device() if cache is None else cache, q, ops.to_device(offsets),
+                           ops.to_device(np.array(lengths, np.int32)), scale, **more)
+
+
+def check_rows(out, lse, host, q, n, scale, rows, dtype="f32", b=0, first=0, count=None, causal=True, window=0):
+    """Pairs (token, head) of `rows`, of sequence b of n tokens, whose `count` queries begin at row
+    `first`."""
+    x, want = ops.to_host(q), [[], [], [], []]
+    count = q.shape[0] if count is None else count
+    heads, group = q.shape[1], q.shape[1] // host.heads
+    kept = {}
+    for i, h in rows:
+        if h // group not in kept:
+            kept[h // group] = host.keys(b, n, h // group), host.values(b, n, h // group)
+        position = n - count + i
+        seen = slice(max(0, position - window + 1) if window else 0, position + 1 if causal else n)
+        k, v = (a[seen] for a in kept[h // group])
+        s = scale * (k @ x[first + i, h])
+        p = np.exp(s - s.max())
+        for one, value in zip(want, (p @ v / p.sum(), s.max() + np.log(p.sum()), np.abs(v).max(),
+                                     abs(scale) * (np.abs(k) @ np.abs(x[first + i, h])).max())):
+            one.append(value)
+    at = [first + i for i, _ in rows], [h for _, h in rows]
+    check(out[at], lse[at], [np.array(w) for w in want], dtype)
+
+
+def some(rng, count, heads, n=40):
+    """Tokens at both ends and anywhere, of any head."""
+    ends = [(0, 0), (0, heads - 1), (count - 1, 0), (count - 1, heads - 1)]
+    return ends + [(int(rng.integers(count)), int(rng.integers(heads))) for _ in range(n)]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_maxima_that_grow_as_outputs_are_taken_out(handle, dim):
+    """Scores that rise by 14 every 1024 keys, so that a row's maximum moves by far more than 2^8
+    just where fp32 outputs leave tensor memory; whole walks (168 of them)."""
+    rng = np.random.default_rng(41)
+    n, tokens, heads, kv_heads = 5300, 1300, 32, 8
+    host = ops.Cache(rng, [n], kv_heads, 64, dim)
+    way = np.sign(rng.standard_normal(dim))
+    rise = np.arange(host.table.shape[1]) * 64 // 1024
+    for j, page in enumerate(host.table[0, :-(-n // 64)]):
+        host.k[page] = np.clip(100 * way + rng.integers(-9, 10, host.k[page].shape), -127, 127) + 128
+        host.ks[page] = 0.14 * (rise[j] + 1) / dim
+    q = ops.to_device(np.broadcast_to(way, (tokens, heads, dim)).astype(np.float32))
+    out, lse = attend(handle, host, q, [tokens], [n], 1.0)
+    # A row whose last keys are the first few of a higher block weighs both blocks.
+    rows = some(rng, tokens, heads) + [(1024 * j + e - (n - tokens), h) for j in (4, 5) for e in range(-2, 4)
+                                       for h in (0, 7, 31)]
+    check_rows(out, lse, host, q, n, 1.0, rows)
+    assert status(handle) == 0
