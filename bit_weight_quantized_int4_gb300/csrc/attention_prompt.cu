@@ -77,6 +77,7 @@ struct PromptArgs {
     int64_t rows_min;  // sequences of more rows than this per key/value head are taken
     int q_vec;
     int slots, most_parts;  // CTAs that run at a time; parts of a walk at most
+    int pairs_most;         // records that the plan has room for
     float* parts;           // [unit][2 kQ (D + 2)]: unfinished walks
     int4* plan;             // parts, steps of each, pairs; then of each pair: sequence, tokens,
                             // length, tile; first and last step, first token
@@ -362,6 +363,9 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
         }
         if (b < g.cache.batch) g.first_pair[b] = s_prefix[b] = before + sum - own;
     }
+    // Offsets that only rise have no more pairs than there is room for. Where some decrease (which
+    // has been reported above) the others may overlap: then none are taken.
+    if (pairs > g.pairs_most) pairs = 0;
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) s_longest[warp] = longest;
     if (tid == 0) s_prefix[g.cache.batch] = pairs;
@@ -977,6 +981,7 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     if (head > c.ws_floats / 2) return cudaErrorInvalidValue;
     const int64_t room = (c.ws_floats - head) / (2 * kQ * (D + 2));
     g.slots = c.sm_count;
+    g.pairs_most = (int)pairs_most;
     g.first_pair = reinterpret_cast<int*>(c.ws);
     g.plan = reinterpret_cast<int4*>(c.ws + kMaxBatch);
     g.parts = c.ws + head;

@@ -71,3 +71,30 @@ def test_maxima_that_grow_as_outputs_are_taken_out(handle, dim):
                                        for h in (0, 7, 31)]
     check_rows(out, lse, host, q, n, 1.0, rows)
     assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sequences", [3, 64, 1500])
+def test_offsets_that_rise_and_fall(handle, sequences, dtype):
+    """0, n, 0, n, ...: every other sequence looks like all of the tokens.  More row tiles than the
+    call's tokens have are not taken (of three sequences, one or two are), and nothing past the
+    workspace is touched: the call after it is right."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(42)
+    n = 700
+    host = ops.Cache(rng, [n], 1, 64, 64)
+    host.table = np.repeat(host.table, sequences, 0)
+    cache = host.device()
+    q = ops.to_device(rng.standard_normal((n, 8, 64)).astype(np.float32), dtype)
+    offsets = ops.to_device((np.arange(sequences + 1) % 2 * n).astype(np.int32))
+    lengths = ops.to_device(np.full(sequences, n, np.int32))
+    out = torch.full_like(q, 7.0)
+    q4lin.attention(handle, cache, q, offsets, lengths, 0.125, out=out)
+    assert status(handle) == 4
+    if sequences > 3:
+        assert bool((out == 7.0).all())
+    host.table = host.table[:1]
+    got = attend(handle, host, q, [n], [n], 0.125)
+    check_rows(*got, host, q, n, 0.125, some(rng, n, 8), dtype)
+    assert status(handle) == 0
