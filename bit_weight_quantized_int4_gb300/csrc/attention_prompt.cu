@@ -339,12 +339,13 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
             sum = p.pairs;
             if (p.pairs) {
                 int first, last;
-                walk_of(g, p, p.pairs - 1, &first, &last);
-                // Without a window the last pair's walk is the longest; with one, none is longer
-                // than this.
+                // Causal: without a window the last pair's walk is the longest; with one, none is
+                // longer than `window`.  Else all walks end together, and the first pair's begins
+                // before the others.
+                walk_of(g, p, g.a.causal ? p.pairs - 1 : 0, &first, &last);
                 const int64_t window = (g.a.window + 2 * kQ / group + kKeys) / kKeys + 1;
-                const int most = g.a.window > 0 ? (int)min((int64_t)p.len / kKeys + 1, window) : last - first;
-                longest = max(longest, most);
+                const bool behind = g.a.causal && g.a.window > 0;
+                longest = max(longest, behind ? (int)min((int64_t)p.len / kKeys + 1, window) : last - first);
             }
         }
         const int own = sum;

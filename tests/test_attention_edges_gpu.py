@@ -98,3 +98,39 @@ def test_offsets_that_rise_and_fall(handle, sequences, dtype):
     got = attend(handle, host, q, [n], [n], 0.125)
     check_rows(*got, host, q, n, 0.125, some(rng, n, 8), dtype)
     assert status(handle) == 0
+
+
+BEHIND_A_WINDOW = [
+    # tokens, keys, heads, kv heads, dim, dtype, window
+    (600, 600, 4, 1, 64, "f32", 50),
+    (600, 600, 4, 1, 128, "bf16", 1),
+    (600, 900, 3, 1, 128, "f32", 256),
+    (1000, 1000, 1, 1, 64, "f16", 33),
+    (1000, 1000, 4, 1, 64, "f32", 33),
+    (2048, 2048, 1, 1, 64, "bf16", 256),
+    (2048, 2048, 4, 2, 64, "f32", 50),
+    (1024, 3000, 4, 1, 64, "f32", 1),
+    (2048, 2100, 8, 2, 64, "f32", 256),
+    (1100, 1100, 40, 10, 64, "f32", 50),    # whole walks
+    (1100, 1100, 40, 10, 128, "bf16", 256),
+]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("tokens,n,heads,kv_heads,dim,dtype,window", BEHIND_A_WINDOW)
+def test_a_window_without_an_end(handle, tokens, n, heads, kv_heads, dim, dtype, window, causal):
+    """Not causal, a query sees its window and everything after it: walks as long as the queries'
+    count and the window together.  Both kernels; and the causal form of the same sizes."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(43)
+    host = ops.Cache(rng, [n], kv_heads, 32, dim)
+    q = ops.to_device(rng.standard_normal((tokens, heads, dim)).astype(np.float32), dtype)
+    rows, scale = some(rng, tokens, heads), float(np.float32(1 / np.sqrt(dim)))
+    try:
+        for split in (1, 1 << 40):
+            handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, split)
+            out, lse = attend(handle, host, q, [tokens], [n], scale, causal=causal, window=window)
+            check_rows(out, lse, host, q, n, scale, rows, dtype, causal=causal, window=window)
+            assert status(handle) == 0
+    finally:
+        handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
