@@ -169,6 +169,8 @@ q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cac
         return Q4LIN_ERR_TOO_LARGE;
     q4lin_attention_t args = *a;
     args.max_query = max_query;
+    // No sequence has more positions than its pages: a window of as many leaves every key.
+    if (args.window >= cache->pages_per_sequence * cache->page_size) args.window = 0;
     DeviceGuard g(h->device);
     if (!g.ok()) return Q4LIN_ERR_CUDA;
     const q4lin::LaunchCtx c = make_ctx(h, static_cast<cudaStream_t>(stream));

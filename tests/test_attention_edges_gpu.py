@@ -134,3 +134,22 @@ def test_a_window_without_an_end(handle, tokens, n, heads, kv_heads, dim, dtype,
             assert status(handle) == 0
     finally:
         handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("tokens,n,heads,kv_heads", [(1, 3000, 4, 1), (5, 40, 4, 2), (1100, 1100, 40, 10),
+                                                     (700, 1500, 4, 1)])
+def test_windows_wider_than_any_sequence(handle, tokens, n, heads, kv_heads, causal):
+    """As if there were none, up to the largest number that the argument holds."""
+    import torch
+    rng = np.random.default_rng(44)
+    host = ops.Cache(rng, [n], kv_heads, 16, 64)
+    q = ops.to_device(rng.standard_normal((tokens, heads, 64)).astype(np.float32))
+    want = attend(handle, host, q, [tokens], [n], 0.125, causal=causal)
+    check_rows(*want, host, q, n, 0.125, some(rng, tokens, heads), causal=causal)
+    for window in (n, n + 1, n + 100, 2**31, 2**62, 2**63 - 300, 2**63 - 1):
+        got = attend(handle, host, q, [tokens], [n], 0.125, causal=causal, window=window)
+        check_rows(*got, host, q, n, 0.125, some(rng, tokens, heads), causal=causal)
+        if window > n + 16:  # (no page fewer than without)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert status(handle) == 0
