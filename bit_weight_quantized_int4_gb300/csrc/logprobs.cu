@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LpArgs 
                 unsigned long long top = 0;
                 for (int64_t at = span.begin + tid; at < span.end; at += kThreads) {
                     const unsigned long long key = order_key(load_one(base, DT, at), (uint32_t)at);
-                    if (key < below && key > top) top = key;
+                    // (A NaN at index 0 has the largest key there is.)
+                    if ((k == 0 || key < below) && key > top) top = key;
                 }
                 __syncthreads();
                 s_cand[tid] = top;

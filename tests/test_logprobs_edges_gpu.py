@@ -1,0 +1,42 @@
+"""Log probabilities and their gradient where rows hold NaN and infinities, strides say nothing,
+and outputs lie on other streams."""
+import numpy as np
+import pytest
+
+from tests import _operators as ops
+from tests.test_logprobs_gpu import status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def handle():
+    from bit_weight_quantized_int4_gb300 import q4lin
+    h = q4lin.Handle(0)
+    yield h
+    h.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,size,top", [(1, 7, 7), (2, 1, 1), (3, 32, 32), (400, 500, 5), (2, 70001, 20),
+                                           (1, 128256, 32)])
+def test_nan_at_both_ends(handle, rows, size, top, dtype):
+    """A NaN counts as the largest entry wherever it stands, the first and the last place too, and
+    of several the first comes first; one row split over CTAs and not."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(51)
+    x = rng.standard_normal((rows, size)).astype(np.float32)
+    every = np.full((rows, size), np.nan, np.float32)
+    first, both = x.copy(), x.copy()
+    first[:, 0] = np.nan
+    both[:, [0, -1]] = np.nan
+    for y in (first, both, every):
+        y = ops.to_host(ops.to_device(y, dtype))
+        r = q4lin.logprobs(handle, ops.to_device(y.astype(np.float32), dtype),
+                           torch.zeros(rows, dtype=torch.int32, device="cuda"), top=top)
+        order = np.argsort(np.where(np.isnan(y), -np.inf, -y), axis=1, kind="stable")[:, :top]
+        assert np.array_equal(r.top_tokens.cpu().numpy(), order)
+        assert torch.isnan(r.top_logprobs).all() and torch.isnan(r.lse).all()
+        assert torch.isnan(r.entropy).all() and torch.isnan(r.logprob).all()
+    assert status(handle) == 0
