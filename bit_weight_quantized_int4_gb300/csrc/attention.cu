@@ -54,7 +54,7 @@ struct SplitArgs {
     int q_vec;
     int workers;    // warps of the launch
     float* parts;   // [workers][2][R (D + 2)]: a warp's first and last piece, if unfinished
-    int* list;      // [batch + 2]: the share, then where each sequence begins in the list
+    int* list;      // [batch + 1]: the share (0: nothing is run), then each sequence's place in the list
     int* status;
     int64_t wait_ns;
     uint32_t missing;  // test hook: bytes that the copies' barriers wait for in vain
@@ -78,7 +78,7 @@ struct Shared {
     Mine<D, RT> mine[W];
     uint64_t full[W][kSlots];
     int prefix[kMaxBatch + 1];
-    int sums[W];
+    uint32_t sums[W];
     int failed;
 };
 
@@ -138,37 +138,43 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
         mbar_init_fence();
     }
     const int batch = (int)C.batch;
-    int total = 0;
+    uint32_t sum = 0;
+    bool falls = false;
     for (int b0 = 0; b0 < batch; b0 += T) {
         const int b = b0 + tid;
-        int v = 0;
+        uint32_t v = 0;
+        bool decreases = false;
         if (b < batch) {
             bool bad;
             const Sequence s = sequence_of<RT>(g, b, &bad);
             v = s.tiles * s.row_tiles * Hkv;
+            decreases = __ldg(g.a.offsets + b + 1) < __ldg(g.a.offsets + b);
             if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, v, o);
+            const uint32_t n = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += n;
         }
         if (b0 > 0) __syncthreads();
         if (lane == 31) S.sums[warp] = v;
-        __syncthreads();
-        v += total;
+        falls |= __syncthreads_or(decreases);
+        v += sum;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             if (w < warp) v += S.sums[w];
-            total += S.sums[w];
+            sum += S.sums[w];
         }
-        if (b < batch) S.prefix[b + 1] = v;
+        if (b < batch) S.prefix[b + 1] = (int)v;
     }
     __syncthreads();
+    // The host has counted on offsets that rise: where one decreases (reported above), sequences
+    // may overlap and the list outgrow 32 bits.  Then it is empty.
+    const int total = falls ? 0 : (int)sum;
     const int share = max(1, (total + g.workers - 1) / g.workers);
     if (blockIdx.x == 0) {
         for (int b = tid; b < batch; b += T) g.list[1 + b] = S.prefix[b];
-        if (tid == 0) g.list[0] = share;
+        if (tid == 0) g.list[0] = falls ? 0 : share;
     }
     // Neighbouring shares to different SMs: a short list is spread over all of them.
     const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
@@ -560,7 +566,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
     griddep_wait();
     if (token < o0 || token >= o0 + s.tq) return;
     const int row = (int)(token - o0) * group + head - h * group, r = row % R;
-    const int share = __ldcg(g.list), at = __ldcg(g.list + 1 + b) + (h * s.row_tiles + row / R) * s.tiles;
+    const int share = __ldcg(g.list);
+    if (share == 0) return;  // an empty list
+    const int at = __ldcg(g.list + 1 + b) + (h * s.row_tiles + row / R) * s.tiles;
     const int c0 = at / share, c1 = (at + s.tiles - 1) / share;
     if (c0 == c1) return;
     float mx = -INFINITY, l = 0.f;
@@ -637,16 +645,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
     if (lane == 0 && g.a.lse) g.a.lse[index] = l != 0.f ? (from + lg2(l) - kShift) * kLn2 : -INFINITY;
 }
 
+// What a launch may have to do.
+struct SplitSize {
+    bool two;          // row tiles of 16 rows instead of 8
+    int64_t segments;  // row tiles of all key/value heads
+    int64_t tiles;     // of keys, of each
+};
+SplitSize split_size(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max, int64_t batch) {
+    const int64_t group = a.heads / cache.kv_heads, rows = std::min(rows_max, a.max_query * group);
+    SplitSize s;
+    s.two = rows > kRows && cache.head_dim != 256;
+    const int64_t R = s.two ? 2 * kRows : kRows;
+    const int64_t row_tiles =
+        std::min((a.tokens * group + R - 1) / R + batch, ((rows + R - 1) / R) * batch);
+    s.segments = row_tiles * cache.kv_heads;
+    s.tiles = (cache.pages_per_sequence * cache.page_size + kTile - 1) / kTile;
+    return s;
+}
+
 template <int D, int RT>
-cudaError_t launch(SplitArgs& g, int64_t segments_most, const LaunchCtx& c) {
+cudaError_t launch(SplitArgs& g, const SplitSize& size, const LaunchCtx& c) {
     constexpr int W = warps_of(D, RT), R = RT * kRows;
     constexpr int bytes = W * kSlots * kTile * D + (int)sizeof(Shared<D, RT>);
     static_assert(bytes <= 227 * 1024, "shared memory of one SM");
     cudaError_t e = kernel_smem_once<attention_split_kernel<D, RT>>(bytes);
     if (e != cudaSuccess) return e;
     // One CTA per SM, and no more than the longest possible list has tiles for.
-    const int64_t tiles = (g.cache.pages_per_sequence * g.cache.page_size + kTile - 1) / kTile;
-    const int64_t grid = std::min<int64_t>(c.sm_count, segments_most * tiles);
+    const int64_t grid = std::min<int64_t>(c.sm_count, size.segments * size.tiles);
     g.workers = (int)grid * W;
     g.list = reinterpret_cast<int*>(c.ws);
     g.parts = c.ws + kMaxBatch + 4;  // 16-byte aligned
@@ -661,7 +686,7 @@ cudaError_t launch(SplitArgs& g, int64_t segments_most, const LaunchCtx& c) {
     // Warps per row by the parts that a row may have (64 sequences x 8 heads on 1216 warps: 2 or 3
     // parts, two warps 3 us less for the whole call than four; 9 x 4 heads x 3 row tiles on 1064:
     // about 10, eight warps 21 us, two 24; one sequence x 8 heads: 152).
-    const int64_t parts = g.workers / segments_most;
+    const int64_t parts = g.workers / size.segments;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(g.a.tokens * g.a.heads));
     cfg.stream = c.stream;
@@ -681,13 +706,15 @@ cudaError_t launch(SplitArgs& g, int64_t segments_most, const LaunchCtx& c) {
 
 }  // namespace
 
+bool attention_split_countable(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max) {
+    const SplitSize s = split_size(cache, a, rows_max, std::min<int64_t>(kMaxBatch, cache.batch));
+    int64_t units;
+    // (The kernel rounds the list up to its warps, of which there are fewer than 2^16.)
+    return !__builtin_mul_overflow(s.segments, s.tiles, &units) && units <= 0x7FFFFFFF - 0xFFFF;
+}
+
 cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
                                    int64_t rows_max, const LaunchCtx& c) {
-    const int64_t group = a.heads / cache.kv_heads;
-    const int64_t rows = std::min(rows_max, a.max_query * group);
-    const int D = (int)cache.head_dim;
-    const bool two = rows > kRows && D != 256;
-    const int R = two ? 2 * kRows : kRows;
     cudaError_t err = cudaSuccess;
     // Sequences in groups that the kernel's list holds.
     for (int64_t b = 0; b < cache.batch && err == cudaSuccess; b += kMaxBatch) {
@@ -705,13 +732,11 @@ cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_at
         g.status = c.status_word;
         g.wait_ns = c.wait_limit_ns;
         g.missing = c.tc_skip_first_copy ? 16 : 0;
-        const int64_t row_tiles = std::min((a.tokens * group + R - 1) / R + g.cache.batch,
-                                           ((rows + R - 1) / R) * g.cache.batch);
-        const int64_t most = row_tiles * cache.kv_heads;  // heads' row tiles in the list
-        switch (D) {
-            case 64: err = two ? launch<64, 2>(g, most, c) : launch<64, 1>(g, most, c); break;
-            case 128: err = two ? launch<128, 2>(g, most, c) : launch<128, 1>(g, most, c); break;
-            default: err = launch<256, 1>(g, most, c); break;
+        const SplitSize size = split_size(cache, a, rows_max, g.cache.batch);
+        switch (cache.head_dim) {
+            case 64: err = size.two ? launch<64, 2>(g, size, c) : launch<64, 1>(g, size, c); break;
+            case 128: err = size.two ? launch<128, 2>(g, size, c) : launch<128, 1>(g, size, c); break;
+            default: err = launch<256, 1>(g, size, c); break;
         }
     }
     return err;

@@ -154,35 +154,32 @@ q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cac
             return Q4LIN_ERR_INVALID_ARG;
     if (n.overlap(*cache, a->out, ob) || n.overlap(*cache, a->lse, lb) || overlaps(a->out, ob, a->lse, lb))
         return Q4LIN_ERR_INVALID_ARG;
-    // The kernels count query rows and tiles of 64 keys in 32 bits, and the prompts' kernel
-    // keeps 32 bytes for each 256 rows of a key/value head in half of the workspace.
+    // The kernels count query rows in 32 bits, and the prompts' kernel keeps 32 bytes for each 256
+    // rows of a key/value head in half of the workspace.
     constexpr int64_t kRowsMost = int64_t{1} << 27;
     static_assert(8 * (kRowsMost / 256) <= q4lin::kWsFloats / 3, "the pairs of row tiles fit");
     const int64_t group = a->heads / cache->kv_heads, max_query = std::min(a->max_query, a->tokens);
-    const int64_t tiles = cache->pages_per_sequence * cache->page_size / 64 + 1;
-    int64_t row_tiles, units;
-    if (t > 0x7FFFFFFF || t / cache->kv_heads > kRowsMost || !mul_ok(max_query, group, &row_tiles)) return Q4LIN_ERR_TOO_LARGE;
-    row_tiles = std::min(row_tiles / 8 + 1, a->tokens * group / 8 + 1);
-    const int64_t sequences = std::min<int64_t>(cache->batch, 2048);
-    if (!mul_ok(row_tiles, tiles * sequences, &units) || !mul_ok(units, cache->kv_heads, &units) ||
-        units > 0x7FFFFFFF)
+    int64_t rows_longest;
+    if (t > 0x7FFFFFFF || t / cache->kv_heads > kRowsMost || !mul_ok(max_query, group, &rows_longest))
         return Q4LIN_ERR_TOO_LARGE;
+    // One sequence of many rows goes to the prompts' kernel whatever its length; of several, each
+    // kernel takes its own (lengths are on the device).
+    const int64_t split_rows = h->attention_split_rows > 0 ? h->attention_split_rows : kSplitRows;
+    const bool prompts = rows_longest > split_rows && q4lin::attention_prompt_eligible(*cache);
+    const bool split = !prompts || cache->batch > 1;
+    const int64_t split_most = prompts ? split_rows : INT64_MAX;
     q4lin_attention_t args = *a;
     args.max_query = max_query;
     // No sequence has more positions than its pages: a window of as many leaves every key.
     if (args.window >= cache->pages_per_sequence * cache->page_size) args.window = 0;
+    if (split && !q4lin::attention_split_countable(*cache, args, split_most)) return Q4LIN_ERR_TOO_LARGE;
     DeviceGuard g(h->device);
     if (!g.ok()) return Q4LIN_ERR_CUDA;
     const q4lin::LaunchCtx c = make_ctx(h, static_cast<cudaStream_t>(stream));
-    const int64_t split_rows = h->attention_split_rows > 0 ? h->attention_split_rows : kSplitRows;
-    if (max_query * group <= split_rows || !q4lin::attention_prompt_eligible(*cache))
-        return finish(q4lin::attention_split_launch(*cache, args, INT64_MAX, c));
-    // One sequence goes to the prompts' kernel whatever its length; of several, each kernel
-    // takes its own (lengths are on the device).
-    if (cache->batch == 1) return finish(q4lin::attention_prompt_launch(*cache, args, 0, c));
-    const cudaError_t err = q4lin::attention_prompt_launch(*cache, args, split_rows, c);
-    if (err != cudaSuccess) return finish(err);
-    return finish(q4lin::attention_split_launch(*cache, args, split_rows, c));
+    cudaError_t err = cudaSuccess;
+    if (prompts) err = q4lin::attention_prompt_launch(*cache, args, split ? split_rows : 0, c);
+    if (split && err == cudaSuccess) err = q4lin::attention_split_launch(*cache, args, split_most, c);
+    return finish(err);
 }
 
 q4lin_status_t q4lin_run_logprobs(q4lin_handle_t h, const q4lin_logprobs_t* a, void* stream) {

@@ -157,6 +157,8 @@ cudaError_t kv_append_launch(const q4lin_kv_cache_t& cache, const q4lin_kv_appen
 // per key/value head (a row: one query token of one head).
 cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
                                    int64_t rows_max, const LaunchCtx& c);
+// Whether a launch's list of tiles is short enough for it.
+bool attention_split_countable(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max);
 // attention_prompt.cu: sequences of more than `rows_min` query rows per key/value head.
 bool attention_prompt_eligible(const q4lin_kv_cache_t& cache);
 cudaError_t attention_prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,

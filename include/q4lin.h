@@ -281,7 +281,10 @@ Q4LIN_API q4lin_status_t q4lin_run_requant(q4lin_handle_t handle, const float* l
  * code 4 in the handle's status word; nothing out of range is read or written.
  *
  * Sizes whose rows, pages or positions the kernels cannot count (2^31 rows of queries or
- * logits, 2^27 query rows of one key/value head) return Q4LIN_ERR_TOO_LARGE. */
+ * logits, 2^27 query rows of one key/value head; for the attention of up to 256 sequences at
+ * a time that do not go through the prompts' kernel, 2^31 tiles of 64 keys times query rows
+ * in eights times key/value heads, by the width of the page table) return
+ * Q4LIN_ERR_TOO_LARGE. */
 
 /* Element type of keys, values, queries, attention outputs and logits. */
 typedef enum { Q4LIN_DTYPE_F32 = 0, Q4LIN_DTYPE_F16 = 1, Q4LIN_DTYPE_BF16 = 2 } q4lin_dtype_t;

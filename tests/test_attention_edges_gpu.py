@@ -153,3 +153,78 @@ def test_windows_wider_than_any_sequence(handle, tokens, n, heads, kv_heads, cau
         if window > n + 16:  # (no page fewer than without)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert status(handle) == 0
+
+
+def wide_cache(host, width):
+    """The host's cache with a page table of `width` pages a sequence, -1 past what is there."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    narrow = host.device()
+    table = torch.full((host.table.shape[0], width), -1, dtype=torch.int32, device="cuda")
+    table[:, :host.table.shape[1]] = narrow.page_table
+    return q4lin.KVCache(narrow.k_codes, narrow.k_scales, narrow.v_codes, narrow.v_scales, table)
+
+
+MANY = [
+    # new tokens of each sequence (the first, the others), sequences, heads, kv heads, dim, page, pages of a table row
+    (1, 1, 1024, 32, 8, 64, 64, 2048),       # single tokens, and no max_query given
+    (1024, 1, 256, 32, 8, 64, 64, 2048),     # a prompt among single tokens
+    (300, 1, 64, 16, 4, 128, 16, 200000),
+    (2000, 1, 1, 32, 8, 64, 64, 1 << 20),    # one prompt, a table for 2^26 tokens
+    (300, 1, 64, 8, 8, 256, 64, 2048),
+]
+
+
+@pytest.mark.parametrize("first,others,sequences,heads,kv_heads,dim,page,width", MANY)
+def test_many_sequences_and_wide_tables(handle, first, others, sequences, heads, kv_heads, dim, page, width):
+    """Calls whose page table is wide for more than they hold."""
+    rng = np.random.default_rng(45)
+    counts = [first] + [others] * (sequences - 1)
+    lengths = [t + i * 37 % 400 for i, t in enumerate(counts)]
+    host = ops.Cache(rng, lengths, kv_heads, page, dim)
+    q = ops.to_device(rng.standard_normal((sum(counts), heads, dim)).astype(np.float32), "bf16")
+    scale = float(np.float32(1 / np.sqrt(dim)))
+    out, lse = attend(handle, host, q, counts, lengths, scale, cache=wide_cache(host, width))
+    for b in sorted({0, 1 % sequences, 255 % sequences, sequences // 2, sequences - 1}):
+        check_rows(out, lse, host, q, lengths[b], scale, some(rng, counts[b], heads, 8), "bf16", b=b,
+                   first=sum(counts[:b]), count=counts[b])
+    assert status(handle) == 0
+
+
+def test_too_many_tiles_are_refused(handle):
+    """More tiles than the list of the kernel for few rows counts, which with 256 channels takes
+    prompts too; the same call by the prompts' kernel is above."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    host = ops.Cache(np.random.default_rng(46), [4096], 8, 64, 256)
+    q = torch.randn(4096, 32, 256, device="cuda")
+    out = torch.full_like(q, 7.0)
+    with pytest.raises(q4lin.Q4LinError) as e:
+        attend(handle, host, q, [4096], [4096], 0.1, cache=wide_cache(host, 1 << 18), out=out)
+    assert e.value.status == q4lin.Q4LIN_ERR_TOO_LARGE
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all()) and status(handle) == 0
+
+
+@pytest.mark.parametrize("dim", [64, 256])
+def test_overlapping_sequences_do_not_outgrow_the_list(handle, dim):
+    """128 sequences that claim the same tokens, by offsets that rise and fall: with 256 channels
+    2^31 tiles.  Nothing is run, and the next call is right."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(47)
+    tokens, n = (2048, 131072) if dim == 256 else (10, 131072)
+    host = ops.Cache(rng, [64], 8, 64, dim)
+    page = int(host.table[0, 0])
+    host.table = np.full((256, n // 64), page, np.int32)
+    cache = host.device()
+    q = torch.randn(tokens, 32, dim, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((tokens, 32), 7.0, device="cuda")
+    offsets = ops.to_device((np.arange(257) % 2 * tokens).astype(np.int32))
+    q4lin.attention(handle, cache, q, offsets, ops.to_device(np.full(256, n, np.int32)), 0.1, out=out, lse=lse)
+    assert status(handle) == 4
+    assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+    host.table = np.full((1, 2), page, np.int32)
+    got = attend(handle, host, q[:9], [9], [64], 0.125)
+    check_rows(*got, host, q[:9], 64, 0.125, some(rng, 9, 32))
+    assert status(handle) == 0
