@@ -54,7 +54,7 @@ struct SplitArgs {
     int q_vec;
     int workers;    // warps of the launch
     float* parts;   // [workers][2][R (D + 2)]: a warp's first and last piece, if unfinished
-    int* list;      // [batch + 1]: the share (0: nothing is run), then each sequence's place in the list
+    int* list;      // [batch + 1]: the share, then where each sequence begins in the list
     int* status;
     int64_t wait_ns;
     uint32_t missing;  // test hook: bytes that the copies' barriers wait for in vain
@@ -78,7 +78,7 @@ struct Shared {
     Mine<D, RT> mine[W];
     uint64_t full[W][kSlots];
     int prefix[kMaxBatch + 1];
-    uint32_t sums[W];
+    uint2 sums[W];  // of a warp's sequences: tiles, and whether offsets decrease
     int failed;
 };
 
@@ -157,24 +157,27 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
             if (lane >= o) v += n;
         }
         if (b0 > 0) __syncthreads();
-        if (lane == 31) S.sums[warp] = v;
-        falls |= __syncthreads_or(decreases);
+        decreases = __any_sync(0xffffffffu, decreases);
+        if (lane == 31) S.sums[warp] = make_uint2(v, decreases);
+        __syncthreads();
         v += sum;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            if (w < warp) v += S.sums[w];
-            sum += S.sums[w];
+            const uint2 s = S.sums[w];
+            if (w < warp) v += s.x;
+            sum += s.x, falls |= s.y != 0;
         }
         if (b < batch) S.prefix[b + 1] = (int)v;
     }
     __syncthreads();
     // The host has counted on offsets that rise: where one decreases (reported above), sequences
-    // may overlap and the list outgrow 32 bits.  Then it is empty.
+    // may overlap and the list outgrow 32 bits.  Then it is empty, and a share of all numbers tells
+    // the joining kernel that no head was cut.
     const int total = falls ? 0 : (int)sum;
     const int share = max(1, (total + g.workers - 1) / g.workers);
     if (blockIdx.x == 0) {
-        for (int b = tid; b < batch; b += T) g.list[1 + b] = S.prefix[b];
-        if (tid == 0) g.list[0] = falls ? 0 : share;
+        for (int b = tid; b < batch; b += T) g.list[1 + b] = falls ? 0 : S.prefix[b];
+        if (tid == 0) g.list[0] = falls ? INT_MAX : share;
     }
     // Neighbouring shares to different SMs: a short list is spread over all of them.
     const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
@@ -566,9 +569,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
     griddep_wait();
     if (token < o0 || token >= o0 + s.tq) return;
     const int row = (int)(token - o0) * group + head - h * group, r = row % R;
-    const int share = __ldcg(g.list);
-    if (share == 0) return;  // an empty list
-    const int at = __ldcg(g.list + 1 + b) + (h * s.row_tiles + row / R) * s.tiles;
+    const int share = __ldcg(g.list), at = __ldcg(g.list + 1 + b) + (h * s.row_tiles + row / R) * s.tiles;
     const int c0 = at / share, c1 = (at + s.tiles - 1) / share;
     if (c0 == c1) return;
     float mx = -INFINITY, l = 0.f;
