@@ -78,7 +78,7 @@ struct Shared {
     Mine<D, RT> mine[W];
     uint64_t full[W][kSlots];
     int prefix[kMaxBatch + 1];
-    uint2 sums[W];  // of a warp's sequences: tiles, and whether offsets decrease
+    uint32_t sums[W];
     int failed;
 };
 
@@ -87,7 +87,7 @@ struct Sequence {
 };
 
 // What one sequence asks of this kernel; nothing where its indices are bad or its rows are
-// too many for it.
+// too many for it.  tq is -1 where its offsets decrease.
 template <int RT>
 __device__ __forceinline__ Sequence sequence_of(const SplitArgs& g, int64_t b, bool* bad) {
     Sequence s;
@@ -98,7 +98,10 @@ __device__ __forceinline__ Sequence sequence_of(const SplitArgs& g, int64_t b, b
     *bad = o0 < 0 || o1 < o0 || o1 > g.a.tokens || s.tq > g.a.max_query ||
            (int64_t)s.len > g.cache.pages_per_sequence << g.page_shift ||
            (g.a.rope.cos && s.len > g.a.rope.positions);
-    if (*bad || s.tq * group > g.rows_max) s.tq = 0;
+    if (o1 < o0)
+        s.tq = -1;
+    else if (*bad || s.tq * group > g.rows_max)
+        s.tq = 0;
     if (s.len < 0) s.len = 0;
     const int64_t first = g.a.window > 0 ? (int64_t)s.len - s.tq - g.a.window + 1 : 0;
     s.tile0 = first > 0 ? (int)(first / kTile) : 0;
@@ -138,46 +141,44 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
         mbar_init_fence();
     }
     const int batch = (int)C.batch;
+    // Sums stop at kTooMany.  The host has counted on offsets that rise: where one decreases (which
+    // is reported) sequences may overlap and have more tiles than 32 bits hold.
+    constexpr uint32_t kTooMany = 0x7FFFFFFF;
     uint32_t sum = 0;
-    bool falls = false;
     for (int b0 = 0; b0 < batch; b0 += T) {
         const int b = b0 + tid;
         uint32_t v = 0;
-        bool decreases = false;
         if (b < batch) {
             bool bad;
             const Sequence s = sequence_of<RT>(g, b, &bad);
-            v = s.tiles * s.row_tiles * Hkv;
-            decreases = __ldg(g.a.offsets + b + 1) < __ldg(g.a.offsets + b);
+            v = s.tq < 0 ? kTooMany : (uint32_t)(s.tiles * s.row_tiles * Hkv);
             if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t n = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += n;
+            if (lane >= o) v = min(v + n, kTooMany);
         }
         if (b0 > 0) __syncthreads();
-        decreases = __any_sync(0xffffffffu, decreases);
-        if (lane == 31) S.sums[warp] = make_uint2(v, decreases);
+        if (lane == 31) S.sums[warp] = v;
         __syncthreads();
-        v += sum;
+        uint32_t before = sum;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const uint2 s = S.sums[w];
-            if (w < warp) v += s.x;
-            sum += s.x, falls |= s.y != 0;
+            sum = min(sum + S.sums[w], kTooMany);
+            if (w + 1 == warp) before = sum;
         }
-        if (b < batch) S.prefix[b + 1] = (int)v;
+        if (b < batch) S.prefix[b + 1] = (int)min(before + v, kTooMany);
     }
     __syncthreads();
-    // The host has counted on offsets that rise: where one decreases (reported above), sequences
-    // may overlap and the list outgrow 32 bits.  Then it is empty, and a share of all numbers tells
-    // the joining kernel that no head was cut.
-    const int total = falls ? 0 : (int)sum;
+    // A list that would be too long is empty, and a share of all numbers tells the joining kernel
+    // that no head was cut.
+    const bool too_many = sum == kTooMany;
+    const int total = too_many ? 0 : (int)sum;
     const int share = max(1, (total + g.workers - 1) / g.workers);
     if (blockIdx.x == 0) {
-        for (int b = tid; b < batch; b += T) g.list[1 + b] = falls ? 0 : S.prefix[b];
-        if (tid == 0) g.list[0] = falls ? INT_MAX : share;
+        for (int b = tid; b < batch; b += T) g.list[1 + b] = too_many ? 0 : S.prefix[b];
+        if (tid == 0) g.list[0] = too_many ? INT_MAX : share;
     }
     // Neighbouring shares to different SMs: a short list is spread over all of them.
     const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
