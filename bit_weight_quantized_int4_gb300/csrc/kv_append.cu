@@ -40,6 +40,18 @@ __device__ __forceinline__ int64_t first_slot(const AppendArgs& g, int64_t b, in
     return (offset >> g.page_shift) + 2 * b;
 }
 
+// Whether one of the offsets that this CTA looks at (all CTAs of a blockIdx.x range together look
+// at every one) decreases or passes the tokens; the searches below need not come across it.
+__device__ __forceinline__ bool offsets_bad(const AppendArgs& g) {
+    bool bad = false;
+    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < g.cache.batch;
+         b += (int64_t)gridDim.x * blockDim.x) {
+        const int o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1);
+        bad |= o0 < 0 || o1 < o0 || o1 > g.a.tokens;
+    }
+    return bad;
+}
+
 // New tokens of one page: rows [first, first + n) of the call, positions from p0, slots [at,
 // at + n).  n is 0 where there are none.
 struct Share {
@@ -181,6 +193,7 @@ __global__ void __launch_bounds__(THREADS) kv_append_pages_kernel(const AppendAr
     const q4lin_kv_cache_t& C = g.cache;
     const int D = (int)C.head_dim, P = 1 << g.page_shift, units = D / 8, h = blockIdx.y;
     const bool keys = blockIdx.z == 0;
+    if (h == 0 && keys && offsets_bad(g)) atomicCAS(g.status, 0, kStatusIndex);
     const Share s = find_share<false>(g, blockIdx.x);
     if (s.n == 0) return;
     const int64_t page = page_of(g, s, keys);
@@ -336,6 +349,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps) kv_append_tokens_kernel(cons
     const int lane = threadIdx.x & 31, item = blockIdx.y * kTokenWarps + (threadIdx.x >> 5);
     const int h = item >> 1;
     const bool keys = (item & 1) == 0;
+    if (blockIdx.y == 0 && offsets_bad(g)) atomicCAS(g.status, 0, kStatusIndex);
     if (h >= C.kv_heads) return;
     const Share s = find_share<true>(g, blockIdx.x);
     if (s.n == 0) return;
