@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
                     for (int o = kUnits / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                     // 2^up brings the row's largest |x| to [2^14, 2^15); its exponent is kept
                     // within what both 2^up and 2^-up can hold.
-                    const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
+                    const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 254) - 127;
                     const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
                     const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
                     if (!in) continue;

@@ -297,7 +297,7 @@ __device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, fl
             for (int o = kUnitsRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             // 2^up brings the row's largest |x| to [2^14, 2^15); the scale's sign goes with it,
             // so that larger scores stay larger after the factor.
-            const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 250) - 127;
+            const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 254) - 127;
             const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), g.a.scale);
             const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
             if (r < 2 * kQ) {

@@ -228,3 +228,23 @@ def test_overlapping_sequences_do_not_outgrow_the_list(handle, dim):
     got = attend(handle, host, q[:9], [9], [64], 0.125)
     check_rows(*got, host, q[:9], 64, 0.125, some(rng, 9, 32))
     assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_queries_near_the_largest_number(handle, dim, dtype):
+    """Finite queries of up to 2^128, whose scores are of ordinary size by the scale.  Both kernels."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(48)
+    host = ops.Cache(rng, [300], 2, 32, dim)
+    host.ks /= 64
+    q = rng.uniform(-1, 1, (70, 4, dim)) * 2.0**rng.integers(120, 128, (70, 4, 1))
+    q = ops.to_device(q.astype(np.float32), dtype)
+    q[q.isinf()] = 0
+    try:
+        for split in (1, 1 << 40):
+            handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, split)
+            out, lse = attend(handle, host, q, [70], [300], 2.0**-124)
+            check_rows(out, lse, host, q, 300, 2.0**-124, some(rng, 70, 4, 80), dtype)
+    finally:
+        handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
