@@ -296,9 +296,11 @@ __device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, fl
 #pragma unroll
             for (int o = kUnitsRow / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             // 2^up brings the row's largest |x| to [2^14, 2^15); the scale's sign goes with it,
-            // so that larger scores stay larger after the factor.
+            // so that larger scores stay larger after the factor.  With an infinity the whole row
+            // becomes NaN (a lone term of it could give scores of -infinity, as if masked).
             const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 254) - 127;
-            const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), g.a.scale);
+            const uint32_t up_bits = m == INFINITY ? 0x7FC00000u : (uint32_t)(127 + 14 - ex) << 23;
+            const float up = copysignf(__uint_as_float(up_bits), g.a.scale);
             const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
             if (r < 2 * kQ) {
                 uint32_t hi[4], lo[4];

@@ -248,3 +248,36 @@ def test_queries_near_the_largest_number(handle, dim, dtype):
             check_rows(out, lse, host, q, 300, 2.0**-124, some(rng, 70, 4, 80), dtype)
     finally:
         handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,tokens", [(1, 1), (200, 130)])
+def test_an_infinite_query_gives_nan(handle, n, tokens, dim, dtype, rotated):
+    """Also where every key has the same sign in its channel, so that all scores are infinities of
+    one sign.  The other rows are as they were.  Both kernels."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(49)
+    host = ops.Cache(rng, [n], 1, 16, dim)
+    host.k[..., 3] = 1 + host.k[..., 3] % 100    # codes below 128
+    host.k[..., 5] = 255 - host.k[..., 5] % 100  # and above
+    cache = host.device()
+    angle = np.zeros((n, dim // 2), np.float32)
+    rope = (ops.to_device(angle + 1), ops.to_device(angle)) if rotated else None
+    q = ops.to_device(rng.standard_normal((tokens, 4, dim)).astype(np.float32), dtype)
+    try:
+        for split in (1, 1 << 40):
+            handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, split)
+            want, want_lse = attend(handle, host, q, [tokens], [n], 0.1, cache=cache, rope=rope)
+            assert torch.isfinite(want).all() and torch.isfinite(want_lse).all()
+            for channel, value in ((3, float("inf")), (3, -float("inf")), (5, float("inf")), (5, -float("inf"))):
+                x = q.clone()
+                x[-1, 2, channel] = value
+                out, lse = attend(handle, host, x, [tokens], [n], 0.1, cache=cache, rope=rope)
+                assert torch.isnan(out[-1, 2]).all() and torch.isnan(lse[-1, 2])
+                out[-1, 2], lse[-1, 2] = want[-1, 2], want_lse[-1, 2]
+                assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    finally:
+        handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
