@@ -81,7 +81,6 @@ struct PromptArgs {
     float* parts;           // [unit][2 kQ (D + 2)]: unfinished walks
     int4* plan;             // parts, steps of each, pairs; then of each pair: sequence, tokens,
                             // length, tile; first and last step, first token
-    int* first_pair;        // [batch]: where a sequence's pairs begin
     int* status;
     int64_t wait_ns;
     int skip_first_copy;  // test hook: no keys come, and the waits for them run out
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
             if (w < warp) before += s_scan[w];
             pairs += s_scan[w];
         }
-        if (b < g.cache.batch) g.first_pair[b] = s_prefix[b] = before + sum - own;
+        if (b < g.cache.batch) s_prefix[b] = before + sum - own;
     }
     // Offsets that only rise have no more pairs than there is room for. Where some decrease (which
     // has been reported above) the others may overlap: then none are taken.
@@ -980,13 +979,12 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     if (e != cudaSuccess) return e;
     // Parts only where whole walks leave SMs idle, and as the workspace allows.
     const int64_t units = std::max<int64_t>(1, pairs_most) * g.cache.kv_heads;
-    const int64_t head = kMaxBatch + 4 + 8 * pairs_most;  // floats, a multiple of 4
+    const int64_t head = 4 + 8 * pairs_most;  // floats, a multiple of 4
     if (head > c.ws_floats / 2) return cudaErrorInvalidValue;
     const int64_t room = (c.ws_floats - head) / (2 * kQ * (D + 2));
     g.slots = c.sm_count;
     g.pairs_most = (int)pairs_most;
-    g.first_pair = reinterpret_cast<int*>(c.ws);
-    g.plan = reinterpret_cast<int4*>(c.ws + kMaxBatch);
+    g.plan = reinterpret_cast<int4*>(c.ws);
     g.parts = c.ws + head;
     g.most_parts = units <= c.sm_count ? 64 : 1;
     const int64_t grid = g.most_parts == 1 ? units : std::min(std::max<int64_t>(units, 2 * c.sm_count), room);
