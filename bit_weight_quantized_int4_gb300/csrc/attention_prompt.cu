@@ -57,11 +57,18 @@ constexpr int kMaxBatch = 1024;  // sequences per launch
 constexpr int kScaleSlots = 5;  // steps whose scales are kept: the widening warps are up to four ahead
 constexpr float kBase = 7.f;    // weights are kept as 2^7 p ...
 // Tensor cores cut off what a product's sum has no room for, so an error of one sign grows with
-// the steps that O adds up there (16384 keys: 3.6e-5 of the norm of fp32 outputs).  fp32 outputs
-// are taken out every kDrain steps and added up with rounding, in their own place in memory: 3e-6
-// at any length, about what sums in plain fp32 have (every 16 steps: 5e-6, and 424 us instead
-// of 483 for the prompt at the head of this file).
-constexpr int kDrain = 8;
+// the steps that O adds up there (16384 keys: 3.6e-5 of the norm with two-term weights).  Outputs
+// are taken out every `DRAIN` steps and added up with rounding, in memory:
+//   fp32  in their own place or their part's, every 8 steps: 3e-6 at any length, about what sums in
+//         plain fp32 have (every 16 steps: 5e-6);
+//   fp16  in a slot of the workspace, every 64 steps, where the page table has room for more than
+//         kFewKeys: below them the error stays at a third of what the rounding to fp16 leaves
+//         (2.1e-4), at 131072 keys it was 2.6e-4.  (The code for it costs 336 -> 362 us on 2048 of
+//         8192 tokens, 32 heads of 128, which never take anything out; walks of 131072 keys 5.2 -> 5.7 ms.)
+//   bf16  not at all: 1.6e-4 at 131072 keys, against 1.7e-3 of the rounding.
+constexpr int kDrainF32 = 8, kDrainF16 = 64;
+constexpr int64_t kFewKeys = 32768;
+constexpr int kDrainSlots = 256;  // at most; one for each CTA that runs
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
 // A score's factor is at least this, so that a masked score (-infinity) stays one.
 constexpr float kLeastFactor = 1e-37f;
@@ -78,7 +85,9 @@ struct PromptArgs {
     int q_vec;
     int slots, most_parts;  // CTAs that run at a time; parts of a walk at most
     int pairs_most;         // records that the plan has room for
-    float* parts;           // [unit][2 kQ (D + 2)]: unfinished walks
+    float* parts;           // [unit][2 kQ (D + 2)]: unfinished walks; [slot][2 kQ D]: fp16 outputs taken out
+    int* taken;             // [drain_slots]: slots in use
+    int drain_slots;
     int4* plan;             // parts, steps of each, pairs; then of each pair: sequence, tokens,
                             // length, tile; first and last step, first token
     int* status;
@@ -139,6 +148,7 @@ struct Job {
     int64_t o0;
     int b, h, tq, len, row0, row_end, step0, n, cut;
     int page_low;  // the first page that a window leaves
+    int slot;      // for outputs taken out, -1: none
 };
 
 struct PromptShared {
@@ -331,6 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hkv = (int)g.cache.kv_heads, group = (int)(g.a.heads / g.cache.kv_heads);
     int pairs = 0, longest = 0;
+    if (tid < g.drain_slots) g.taken[tid] = 0;
     for (int64_t b0 = 0; b0 < g.cache.batch; b0 += kPlanThreads) {
         const int64_t b = b0 + tid;
         int sum = 0;
@@ -404,11 +415,29 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
     if (lane == 0) *g.plan = make_int4(parts, max(1, (longest + parts - 1) / parts), pairs, 0);
 }
 
-// Where row `row` of a job (row r of its pair of tiles) has its fp32 outputs, or its sums where
-// the walk is cut.
-template <int D>
+// A free slot, for a CTA of a whole walk that outputs of 16 bits are taken out of; -1 for others.
+// There are as many as CTAs run at a time (each holds all of an SM's tensor memory), so one is
+// free; which one does not change the results.  Without (the search is bounded) outputs stay.
+template <int DT, int DRAIN>
+__device__ __forceinline__ int take_slot(const PromptArgs& g, int n, bool cut) {
+    if (DT == Q4LIN_DTYPE_F32 || DRAIN == 0 || cut || n <= DRAIN) return -1;
+    int slot = (int)(blockIdx.x % g.drain_slots);
+    for (int i = 0; i < 64 * kDrainSlots; ++i) {
+        if (atomicCAS(g.taken + slot, 0, 1) == 0) {
+            __threadfence();
+            return slot;
+        }
+        slot = slot + 1 < g.drain_slots ? slot + 1 : 0;
+    }
+    return -1;
+}
+
+// Where row `row` of a job (row r of its pair of tiles) has its fp32 outputs, its sums where the
+// walk is cut, or what was taken out of its fp16 outputs.
+template <int D, int DT>
 __device__ __forceinline__ float* out_row(const PromptArgs& g, const volatile Job& job, int row, int r) {
     if (job.cut) return part_at<D>(g, blockIdx.x) + r * D;
+    if (DT != Q4LIN_DTYPE_F32) return g.parts + ((int64_t)job.slot * 2 * kQ + r) * D;
     const int group = (int)(g.a.heads / g.cache.kv_heads), token = row / group;
     const int64_t index = (job.o0 + token) * g.a.heads + job.h * group + (row - token * group);
     return static_cast<float*>(g.a.out) + index * D;
@@ -432,7 +461,7 @@ __device__ __forceinline__ void add_16(float* to, uint32_t (&y)[16], float keep,
     }
 }
 
-template <int D, int QT, int PT, int DT>
+template <int D, int QT, int PT, int DT, int DRAIN>
 __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const PromptArgs g) {
     using L = Layout<D, QT>;
     extern __shared__ uint8_t smem_raw[];
@@ -461,7 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     if (n == 0 && part > 0) return;  // a shorter walk has fewer parts
     const int64_t low = g.a.window > 0 ? (int64_t)len - tq + row0 / group - g.a.window + 1 : 0;
     const int page_low = low > 0 ? (int)(low >> ps) : 0;
-    if (tid == 0) S.job = {o0, b, h, tq, len, row0, row_end, step0, n, parts > 1, page_low};
+    if (tid == 0)
+        S.job = {o0, b, h, tq, len, row0, row_end, step0, n, parts > 1, page_low, take_slot<DT, DRAIN>(g, n, parts > 1)};
     const int32_t* table = C.page_table + b * C.table_stride;
     const int pages = (len + (1 << ps) - 1) >> ps;
 
@@ -501,6 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     // All of the SM's tensor memory is this CTA's, so it begins at 0.
     constexpr uint32_t tmem = 0;
     const volatile Job& job = S.job;
+    // The first step before which outputs are taken out, so that O begins anew there.
+    auto first_drain = [&]() {
+        return DRAIN > 0 && (DT == Q4LIN_DTYPE_F32 || job.cut || job.slot >= 0) ? DRAIN : INT_MAX;
+    };
     auto value_ref = [&]() {  // the largest value scale of the walk
         float v = 0.f;
 #pragma unroll
@@ -537,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const int limit = !in ? -1 : g.a.causal ? position : len - 1;
         const int low = g.a.window > 0 ? (int)max((int64_t)0, (int64_t)position - g.a.window + 1) : 0;
         const float factor = S.factor[r];
+        int drain = first_drain();
         float m = -INFINITY, l = 0.f, m_out = -INFINITY;  // m_out: of what was taken out
         bool ok = true;
         const int steps = tile == 0 || row_end - row0 > kQ ? n : 0;
@@ -582,16 +617,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                     }
                 }
             }
-            if (DT == Q4LIN_DTYPE_F32 && i > 0 && i % kDrain == 0) {
-                float* to = out_row<D>(g, job, row, r);
-                const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
+            if (DRAIN > 0 && i == drain) {
+                drain += DRAIN;
                 tmem_wait_st();  // O may just have been rescaled; loads do not wait for stores
-#pragma unroll
+                float* to = out_row<D, DT>(g, job, row, r);
+                const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
+#pragma unroll DT == Q4LIN_DTYPE_F32 ? 4 : 8
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t y[16];
                     __syncwarp();  // the load is the whole warp's
                     tmem_ld16(o_at + 16 * c, y);
-                    if (in) add_16(to + 16 * c, y, keep, i > kDrain, true);
+                    if (in) add_16(to + 16 * c, y, keep, i > DRAIN, true);
                 }
                 __syncwarp();
                 m_out = m;
@@ -655,9 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = 0u;
                 }
-                if (DT == Q4LIN_DTYPE_F32 && steps > kDrain && in) {
+                if (DRAIN > 0 && drain > DRAIN && drain < INT_MAX && in) {
                     const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
-                    float* from = out_row<D>(g, job, row, r) + 32 * c;
+                    float* from = out_row<D, DT>(g, job, row, r) + 32 * c;
                     add_16(from, *reinterpret_cast<uint32_t(*)[16]>(x), keep, true, false);
                     add_16(from + 16, *reinterpret_cast<uint32_t(*)[16]>(x + 16), keep, true, false);
                 }
@@ -680,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                 }
             }
             // (What was taken out went through the generic proxy to the same place.)
-            if (DT == Q4LIN_DTYPE_F32) asm volatile("fence.proxy.async;" ::: "memory");
+            if (DRAIN > 0) asm volatile("fence.proxy.async;" ::: "memory");
             fence_async_shared();
             if (in) {
                 void* to = cut ? static_cast<void*>(unit + r * D)
@@ -808,6 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             auto desc = [&](uint32_t low_word) { return (uint64_t)high << 32 | low_word; };
             bool ok = true;
             int k_slot = 0, v_slot = 0;  // of the first block of this step's tile
+            int drain = first_drain();
+            bool begins = true;  // O begins anew at this step
             uint32_t k_par = 0, v_par = 0;
             // One tile's products of a step.  The step's first tile waits for the blocks, its last
             // one releases them and moves on in the ring.
@@ -859,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                             mma_f16_ts(leader, tmem + tile * 128,
                                        tmem + kScoreCol + tile * kKeys + term * 64 + (half * 4 + kk) * 8,
                                        desc(v_low + 2 * kk), idesc_o,
-                                       (DT == Q4LIN_DTYPE_F32 ? i % kDrain != 0 : i > 0) || half + term + kk > 0);
+                                       !begins || half + term + kk > 0);
                     if (last) mma_commit(leader, bar(S.v_empty[slot]));
                     if (++slot == L::vRing) slot = 0, par ^= 1u;
                 }
@@ -869,9 +907,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             if (ok && two) scores(1, false, true);
             for (int i = 0; ok && i < n; ++i) {
                 const bool more = i + 1 < n;
+                if (DRAIN > 0 && i == drain) begins = true, drain += DRAIN;
                 outputs(0, i, true, !two);
                 if (ok && more) scores(0, true, !two);
                 if (ok && two) outputs(1, i, false, true);
+                begins = false;
                 if (ok && two && more) scores(1, false, true);
             }
             // Everything issued has completed when these arrive; tensor memory is freed after.
@@ -884,6 +924,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     tc_fence_before();
     __syncthreads();
     if (warp == kIssueWarp) tmem_dealloc(tmem, kTmemCols);
+    if (DRAIN > 0 && DT != Q4LIN_DTYPE_F32 && thread_number() == 0 && S.job.slot >= 0) {
+        __threadfence();  // (the rows' threads have read what was theirs before the barrier)
+        atomicExch(g.taken + S.job.slot, 0);
+    }
 }
 
 // The rows of walks that were cut: a warp takes PER rows of a pair of tiles, ROWS at a time with
@@ -969,22 +1013,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_prompt_join_kernel(
     join_rows<D, PER, ROWS, AHEAD>(g, (int64_t)pair * parts * Hkv + h, Hkv, count, r0, rows, index0, head0, group);
 }
 
-template <int D, int QT, int PT, int DT>
+template <int D, int QT, int PT, int DT, int DRAIN>
 cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     constexpr int bytes = Layout<D, QT>::bytes + 1024;
     static_assert(bytes + sizeof(PromptShared) <= 227 * 1024, "shared memory of one SM");
     // One CTA holds an SM (it takes all of its tensor memory).
     constexpr int asked = bytes > 116 * 1024 ? bytes : 116 * 1024;
-    cudaError_t e = kernel_smem_once<attention_prompt_kernel<D, QT, PT, DT>>(asked);
+    cudaError_t e = kernel_smem_once<attention_prompt_kernel<D, QT, PT, DT, DRAIN>>(asked);
     if (e != cudaSuccess) return e;
     // Parts only where whole walks leave SMs idle, and as the workspace allows.
     const int64_t units = std::max<int64_t>(1, pairs_most) * g.cache.kv_heads;
-    const int64_t head = 4 + 8 * pairs_most;  // floats, a multiple of 4
+    const int64_t head = kDrainSlots + 4 + 8 * pairs_most;  // floats, a multiple of 4
     if (head > c.ws_floats / 2) return cudaErrorInvalidValue;
     const int64_t room = (c.ws_floats - head) / (2 * kQ * (D + 2));
     g.slots = c.sm_count;
     g.pairs_most = (int)pairs_most;
-    g.plan = reinterpret_cast<int4*>(c.ws);
+    g.taken = reinterpret_cast<int*>(c.ws);
+    g.drain_slots = (int)std::min<int64_t>(room, std::min(kDrainSlots, c.sm_count));
+    g.plan = reinterpret_cast<int4*>(c.ws + kDrainSlots);
     g.parts = c.ws + head;
     g.most_parts = units <= c.sm_count ? 64 : 1;
     const int64_t grid = g.most_parts == 1 ? units : std::min(std::max<int64_t>(units, 2 * c.sm_count), room);
@@ -1005,7 +1051,7 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     main.stream = c.stream;
     main.attrs = &attr;
     main.numAttrs = 1;
-    e = cudaLaunchKernelEx(&main, attention_prompt_kernel<D, QT, PT, DT>, g);
+    e = cudaLaunchKernelEx(&main, attention_prompt_kernel<D, QT, PT, DT, DRAIN>, g);
     if (e != cudaSuccess || g.most_parts == 1) return e;
     // A row a warp while all of them fit on the SMs at once, more beyond (8 key/value heads of 128,
     // 4 query heads each, us for 1 / 4 rows a warp: 32 queries on 8192 keys 25.9 / 34.9, 128 40.1 /
@@ -1052,14 +1098,17 @@ cudaError_t attention_prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_a
         const bool small = cache.head_dim == 64;
         // One term where it is exact (see the head of this file).
         constexpr int f32 = Q4LIN_DTYPE_F32, f16 = Q4LIN_DTYPE_F16, bf16 = Q4LIN_DTYPE_BF16;
+        const bool few = cache.pages_per_sequence * cache.page_size <= kFewKeys;
         if (a.dtype == bf16 && !a.rope.cos)
-            e = small ? launch<64, 1, 1, bf16>(g, pairs, c) : launch<128, 1, 1, bf16>(g, pairs, c);
+            e = small ? launch<64, 1, 1, bf16, 0>(g, pairs, c) : launch<128, 1, 1, bf16, 0>(g, pairs, c);
         else if (a.dtype == bf16)
-            e = small ? launch<64, 2, 1, bf16>(g, pairs, c) : launch<128, 2, 1, bf16>(g, pairs, c);
+            e = small ? launch<64, 2, 1, bf16, 0>(g, pairs, c) : launch<128, 2, 1, bf16, 0>(g, pairs, c);
+        else if (a.dtype == f16 && few)
+            e = small ? launch<64, 2, 2, f16, 0>(g, pairs, c) : launch<128, 2, 2, f16, 0>(g, pairs, c);
         else if (a.dtype == f16)
-            e = small ? launch<64, 2, 2, f16>(g, pairs, c) : launch<128, 2, 2, f16>(g, pairs, c);
+            e = small ? launch<64, 2, 2, f16, kDrainF16>(g, pairs, c) : launch<128, 2, 2, f16, kDrainF16>(g, pairs, c);
         else
-            e = small ? launch<64, 2, 2, f32>(g, pairs, c) : launch<128, 2, 2, f32>(g, pairs, c);
+            e = small ? launch<64, 2, 2, f32, kDrainF32>(g, pairs, c) : launch<128, 2, 2, f32, kDrainF32>(g, pairs, c);
     }
     return e;
 }

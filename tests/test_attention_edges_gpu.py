@@ -281,3 +281,33 @@ def test_an_infinite_query_gives_nan(handle, n, tokens, dim, dtype, rotated):
                 assert torch.equal(out, want) and torch.equal(lse, want_lse)
     finally:
         handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tokens", [5000, 3200])
+def test_sums_over_many_keys_lean_to_neither_side(handle, tokens, dim, dtype):
+    """131072 keys, in whole walks (5000 tokens) and cut ones.  The tensor cores cut off what a sum
+    has no room for: on average 2^-24 of it in each of the 16 additions of a step of 128 keys,
+    an error of one sign that grows with the steps until outputs are taken out (8 steps for fp32,
+    64 for f16).  What the outputs lack along their own direction is at most 16 x 64 x 2^-24 =
+    6.1e-5; the rounding to f16 (1.6e-4 of an output, in no direction) leaves 5 x 1.6e-4 / sqrt(48
+    rows of 64) = 1.5e-5 there."""
+    rng = np.random.default_rng(50)
+    n, heads = 131072, 8
+    host = ops.Cache(rng, [n], 1, 64, dim)
+    q = ops.to_device(rng.standard_normal((tokens, heads, dim)).astype(np.float32), dtype)
+    scale = float(np.float32(1 / np.sqrt(dim)))
+    out, lse = attend(handle, host, q, [tokens], [n], scale)
+    rows = some(rng, tokens, heads, 44)
+    check_rows(out, lse, host, q, n, scale, rows, dtype)
+    x, k, v = ops.to_host(q), host.keys(0, n, 0), host.values(0, n, 0)
+    got, want = [], []
+    for i, h in rows:
+        s = scale * (k[:n - tokens + i + 1] @ x[i, h])
+        p = np.exp(s - s.max())
+        want.append(p @ v[:len(p)] / p.sum())
+        got.append(ops.to_host(out[i, h]))
+    got, want = np.array(got), np.array(want)
+    assert abs(((got - want) * want).sum()) <= (6.1e-5 + (1.5e-5 if dtype == "f16" else 0)) * (want * want).sum()
+    assert status(handle) == 0
