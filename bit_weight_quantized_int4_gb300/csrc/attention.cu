@@ -216,23 +216,25 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
     const int batch_tiles = 32 / ppt;
     const int32_t* table = nullptr;
     int first = 0, cnt = 0, page_low = 0, pages = 0, head = 0, ids = 0, issued = 0, slot_in = 0, in_flight = 0;
+    // (-1 is no page and none of the cache's: it is told apart from one in the table by its place.)
     auto load_ids = [&](int i) {
         const int p = (first + i) * ppt + lane;
-        ids = i + lane / ppt < cnt && p >= page_low && p < pages ? __ldg(table + p) : INT_MIN;
+        ids = i + lane / ppt < cnt && p >= page_low && p < pages ? __ldg(table + p) : -1;
     };
-    auto check_ids = [&]() {
-        if (ids == INT_MIN) {
-            ids = -1;
-        } else if (ids < 0 || ids >= C.num_pages) {
-            atomicCAS(g.status, 0, kStatusIndex);
-            ids = 0;  // read something of the cache rather than nothing
+    auto check_ids = [&](int i) {
+        if ((uint32_t)ids >= (uint32_t)C.num_pages) {
+            const int p = (first + i) * ppt + lane;
+            if (i + lane / ppt < cnt && p >= page_low && p < pages) {
+                atomicCAS(g.status, 0, kStatusIndex);
+                ids = 0;  // read something of the cache rather than nothing
+            }
         }
     };
     // Next half tile of the piece (keys of a tile, then its values) into the ring.
     auto issue = [&]() {
         if (issued >= 2 * cnt) return;
         const int i = issued >> 1;
-        if ((issued & 1) == 0 && i > 0 && i % batch_tiles == 0) load_ids(i), check_ids();
+        if ((issued & 1) == 0 && i > 0 && i % batch_tiles == 0) load_ids(i), check_ids(i);
         const int id = __shfl_sync(0xffffffffu, ids, (i % batch_tiles) * ppt + lane % ppt);
         const bool some = lane < ppt && id >= 0;
         const int count = __popc(__ballot_sync(0xffffffffu, some));
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
                     }
                 }
                 if (p0 == 0) {
-                    check_ids();
+                    check_ids(0);
                     fetch_scales(0);
 #pragma unroll 1
                     for (int i = 0; i < kSlots; ++i) issue();

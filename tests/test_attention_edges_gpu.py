@@ -311,3 +311,21 @@ def test_sums_over_many_keys_lean_to_neither_side(handle, tokens, dim, dtype):
     got, want = np.array(got), np.array(want)
     assert abs(((got - want) * want).sum()) <= (6.1e-5 + (1.5e-5 if dtype == "f16" else 0)) * (want * want).sum()
     assert status(handle) == 0
+
+
+@pytest.mark.parametrize("entry", [-2**31, -1, 2**31 - 1, 3])
+@pytest.mark.parametrize("tokens", [1, 100])
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_every_page_outside_the_cache_is_reported(handle, at, tokens, entry):
+    """Any number that is none of the three pages, and no row of another sequence suffers."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(52)
+    host = ops.Cache(rng, [100], 1, 64, 64, spare=1)
+    host.table = np.stack([host.table[0], host.table[0]])[:, [0, 1, 1]]
+    good = host.table.copy()
+    host.table[0, at] = entry
+    q = ops.to_device(rng.standard_normal((2 * tokens, 2, 64)).astype(np.float32))
+    out, lse = attend(handle, host, q, [tokens] * 2, [180, 100], 0.125)
+    assert status(handle) == 4
+    host.table = good
+    check_rows(out, lse, host, q, 100, 0.125, some(rng, tokens, 2), b=1, first=tokens, count=tokens)
