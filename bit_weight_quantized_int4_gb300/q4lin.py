@@ -325,13 +325,30 @@ def _check_args(x, qweight, scales, bias, group_size):
     return M, N, K, sd
 
 
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream` (a raw handle; None: the current stream).  Memory of the
+    current stream may still be in use there, so on another one the output comes from that
+    stream's, and is not given away before both are done with it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 def linear(handle: Handle, x, qweight, scales, bias, group_size: int, out=None,
            stream=None):
-    """out[M,N] = x @ dequant(qweight)^T (+ bias) on the current (or given) stream."""
+    """out[M,N] = x @ dequant(qweight)^T (+ bias) on the current (or given) stream; another
+    stream's inputs have to be ready there, and kept until it has read them."""
     import torch
     M, N, K, sd = _check_args(x, qweight, scales, bias, group_size)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        out = _empty((M, N), torch.float32, x.device, stream)
     s = stream if stream is not None else torch.cuda.current_stream(x.device).cuda_stream
     st = q4lin_run(handle.ptr, _ptr(x), _ptr(qweight), _ptr(scales), _ptr(bias),
                    _ptr(out), M, N, K, group_size, sd, s)
@@ -363,6 +380,8 @@ def plan_kernel(handle: Handle, x, qweight, scales, bias, group_size: int, out) 
 # ------------------------------------------------- operators around the linears (torch)
 # A decode step makes hundreds of these calls, some shorter on the GPU than their checks
 # here: types are compared as objects, and torch is looked up once.
+# `stream` is a raw handle (default: torch's current stream).  On another stream than theirs,
+# inputs have to be ready there, and kept until it has read them.
 class _Torch:
     """torch, its types' codes and its current stream's handle, filled at the first use."""
     module = None
@@ -409,6 +428,12 @@ def _head_strides(t, what):
     if len(strides) != 3 or strides[2] != 1:
         raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous channels")
     return strides
+
+
+def _new(shape, dtype, device, stream):
+    if stream is None:
+        return _Torch.empty(shape, dtype=dtype, device=device)
+    return _empty(shape, dtype, device, stream)
 
 
 def _stream_of(stream, handle) -> int:
@@ -508,11 +533,11 @@ def attention(handle: Handle, cache: KVCache, query, offsets, lengths, scale: fl
     if dim != c.head_dim or heads % c.kv_heads:
         raise ValueError("query must be [tokens, heads, head_dim], heads a multiple of kv_heads")
     if out is None:
-        out = _Torch.empty(shape, dtype=query.dtype, device=query.device)
+        out = _new(shape, query.dtype, query.device, stream)
     elif out.shape != shape or out.dtype is not query.dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, with the query's shape and type")
     if lse is None:
-        lse = _Torch.empty((tokens, heads), dtype=_Torch.float32, device=query.device)
+        lse = _new((tokens, heads), _Torch.float32, query.device, stream)
     elif lse.shape != (tokens, heads) or lse.dtype is not _Torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor")
     batch, int32 = c.batch, _Torch.int32
@@ -551,12 +576,12 @@ def logprobs(handle: Handle, logits, tokens=None, top: int = 0, stream=None) -> 
     _check_device(handle, logits, tokens)
     stride = _row_stride(logits, "logits")
     rows, vocabulary = logits.shape
-    device, empty, float32 = logits.device, _Torch.empty, _Torch.float32
-    logprob, entropy, lse = (empty(rows, dtype=float32, device=device) for _ in range(3))
+    device, float32 = logits.device, _Torch.float32
+    logprob, entropy, lse = (_new(rows, float32, device, stream) for _ in range(3))
     ids = best = None
     if top:
-        ids = empty((rows, top), dtype=_Torch.int32, device=device)
-        best = empty((rows, top), dtype=float32, device=device)
+        ids = _new((rows, top), _Torch.int32, device, stream)
+        best = _new((rows, top), float32, device, stream)
     args = q4lin_logprobs_t(
         logits.data_ptr(), stride, _dtype_code(logits, "logits"), rows, vocabulary,
         None if tokens is None else _check_vector(tokens, rows, _Torch.int32, "tokens"),
@@ -576,7 +601,7 @@ def logprobs_backward(handle: Handle, logits, tokens, lse, entropy, d_logprob=No
     stride = _row_stride(logits, "logits")
     rows, vocabulary = logits.shape
     if out is None:
-        out = _Torch.empty((rows, vocabulary), dtype=logits.dtype, device=logits.device)
+        out = _new((rows, vocabulary), logits.dtype, logits.device, stream)
     elif out.shape != logits.shape or out.dtype is not logits.dtype:
         raise ValueError("out must have the logits' shape and type")
     float32 = _Torch.float32
