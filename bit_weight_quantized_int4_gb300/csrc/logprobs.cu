@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LpArgs 
 
     // ---- results
     const float ll = logf(rl);
-    const float lse = rm == -INFINITY ? -INFINITY : rm == INFINITY ? INFINITY : rm + ll;
+    // (An infinite maximum has left l = 0, or NaN where the row holds one of those too.)
+    const float lse = rm == -INFINITY ? -INFINITY : rm == INFINITY && rl == 0.f ? INFINITY : rm + ll;
     if (tid == 0) {
         if (g.a.lse) g.a.lse[row] = lse;
         if (g.a.entropy) g.a.entropy[row] = rm == -INFINITY ? 0.f : ll - rt / rl;

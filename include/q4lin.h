@@ -411,8 +411,9 @@ typedef struct q4lin_logprobs {
  * descending order (equal ones: lowest index first) with their log probabilities.
  * -infinity stands for an excluded entry (p = 0, no part in the entropy).  A row of
  * nothing else has lse = -infinity, logprob and top_logprobs -infinity and entropy 0.  A
- * row with a NaN or a +infinity has lse NaN or +infinity, and entropy NaN; the order of
- * the top entries takes a NaN as the largest. */
+ * row with a NaN has lse NaN, one with a +infinity and no NaN has lse +infinity; in both,
+ * entropy, logprob and top_logprobs are NaN (but -infinity for an excluded entry where
+ * there is no NaN).  The order of the top entries takes a NaN as the largest. */
 Q4LIN_API q4lin_status_t q4lin_run_logprobs(q4lin_handle_t handle, const q4lin_logprobs_t* args,
                                             void* stream);
 

@@ -40,3 +40,30 @@ def test_nan_at_both_ends(handle, rows, size, top, dtype):
         assert torch.isnan(r.top_logprobs).all() and torch.isnan(r.lse).all()
         assert torch.isnan(r.entropy).all() and torch.isnan(r.logprob).all()
     assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,size", [(1, 40), (3, 5000), (400, 1000), (1, 128256), (20, 70001)])
+def test_infinities_and_nan_in_one_row(handle, rows, size, dtype):
+    """+infinity alone: lse is +infinity; with a NaN before or after it, near or far: NaN."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(53)
+    x = ops.to_device(rng.standard_normal((rows, size)).astype(np.float32), dtype)
+    tokens = torch.full((rows,), 3, dtype=torch.int32, device="cuda")
+    for at, nan in ((5, None), (0, 1), (1, 0), (5, size - 1), (size - 1, 5), (size // 2, size // 2 + 1)):
+        y = x.clone()
+        y[:, at] = float("inf")
+        if nan is not None:
+            y[:, nan] = float("nan")
+        r = q4lin.logprobs(handle, y, tokens, top=3)
+        assert torch.isnan(r.lse).all() if nan is not None else bool((r.lse == float("inf")).all())
+        assert torch.isnan(r.entropy).all() and torch.isnan(r.logprob).all()
+        assert torch.isnan(r.top_logprobs).all()
+        assert bool((r.top_tokens[:, 0] == (at if nan is None else nan)).all())
+    # An excluded token's log probability is -infinity beside +infinity too, but not beside a NaN.
+    y = x.clone()
+    y[:, 3], y[:, 7] = -float("inf"), float("inf")
+    assert bool((q4lin.logprobs(handle, y, tokens).logprob == -float("inf")).all())
+    y[:, 8] = float("nan")
+    assert torch.isnan(q4lin.logprobs(handle, y, tokens).logprob).all()
