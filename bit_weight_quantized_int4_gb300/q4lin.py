@@ -567,7 +567,7 @@ def _row_stride(t, what):
     strides = t.stride()
     if len(strides) != 2 or (strides[1] != 1 and t.shape[1] != 1):
         raise ValueError(f"{what} must be [rows, vocabulary] with contiguous rows")
-    return strides[0]
+    return strides[0] if t.shape[0] > 1 else t.shape[1]  # (one row's may be anything)
 
 
 def logprobs(handle: Handle, logits, tokens=None, top: int = 0, stream=None) -> LogProbs:

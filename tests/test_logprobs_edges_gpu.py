@@ -67,3 +67,23 @@ def test_infinities_and_nan_in_one_row(handle, rows, size, dtype):
     assert bool((q4lin.logprobs(handle, y, tokens).logprob == -float("inf")).all())
     y[:, 8] = float("nan")
     assert torch.isnan(q4lin.logprobs(handle, y, tokens).logprob).all()
+
+
+def test_one_row_has_no_stride(handle):
+    """One row as a transposed column or a broadcast row, whose strides are 1 and 0: logits, the
+    gradient, and both in one place."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    x = torch.randn(1, 1003, device="cuda")
+    tokens, d = torch.tensor([7], dtype=torch.int32, device="cuda"), torch.ones(1, device="cuda")
+    want = q4lin.logprobs(handle, x, tokens, top=5)
+    gradient = q4lin.logprobs_backward(handle, x, tokens, want.lse, want.entropy, d, d)
+    column = torch.empty(1003, 1, device="cuda").copy_(x.t()).t()
+    assert column.stride() == (1, 1)
+    for y in (column, x[0].expand(1, -1), x.as_strided((1, 1003), (0, 1))):
+        assert all(torch.equal(a, b) for a, b in zip(q4lin.logprobs(handle, y, tokens, top=5), want))
+        for out in (None, torch.empty(1003, 1, device="cuda").t(), torch.empty(1, 1003, device="cuda")):
+            got = q4lin.logprobs_backward(handle, y, tokens, want.lse, want.entropy, d, d, out=out)
+            assert torch.equal(got, gradient)
+    got = q4lin.logprobs_backward(handle, column, tokens, want.lse, want.entropy, d, d, out=column)
+    assert got is column and torch.equal(column, gradient)
