@@ -82,7 +82,13 @@ template <int DT>
 struct Vec {
     static constexpr int N = DT == Q4LIN_DTYPE_F32 ? 4 : 8;
     static __device__ __forceinline__ void load(const void* p, int64_t i, float* x) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * dtype_size(DT)));
+        widen(__ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * dtype_size(DT))), x);
+    }
+    // Where the same kernel writes to the place afterwards.
+    static __device__ __forceinline__ void load_before_store(const void* p, int64_t i, float* x) {
+        widen(*reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * dtype_size(DT)), x);
+    }
+    static __device__ __forceinline__ void widen(const uint4& v, float* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -447,23 +453,28 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_backward_kernel(cons
         if (at == token && !empty) d += d_lp;
         return d;
     };
+    // (The logits' place may be the gradient's: no read-only loads.)
+    auto load_entry = [&](int64_t at) {
+        if (DT == Q4LIN_DTYPE_F32) return reinterpret_cast<const float*>(x_row)[at];
+        return unpack2(reinterpret_cast<const unsigned short*>(x_row)[at], DT).x;
+    };
     const Span<DT> span(x_row, begin, end);
     // Vectors where input and output are aligned alike, else single entries.
     const bool alike = ((reinterpret_cast<uintptr_t>(x_row) ^ reinterpret_cast<uintptr_t>(d_row)) & 15) == 0;
     if (!alike) {
         for (int64_t at = begin + tid; at < end; at += kThreads)
-            store_one(d_row, DT, at, value(load_one(x_row, DT, at), at));
+            store_one(d_row, DT, at, value(load_entry(at), at));
         return;
     }
     if (tid < span.singles()) {
         const int64_t at = span.single(tid);
-        store_one(d_row, DT, at, value(load_one(x_row, DT, at), at));
+        store_one(d_row, DT, at, value(load_entry(at), at));
     }
     for (int64_t v = tid; v < span.vecs; v += kThreads * kAhead) {
         float x[kAhead][N];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (v + i * kThreads < span.vecs) Vec<DT>::load(x_row, span.vec0 + (v + i * kThreads) * N, x[i]);
+            if (v + i * kThreads < span.vecs) Vec<DT>::load_before_store(x_row, span.vec0 + (v + i * kThreads) * N, x[i]);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (v + i * kThreads >= span.vecs) continue;
