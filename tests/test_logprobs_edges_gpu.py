@@ -87,3 +87,64 @@ def test_one_row_has_no_stride(handle):
             assert torch.equal(got, gradient)
     got = q4lin.logprobs_backward(handle, column, tokens, want.lse, want.entropy, d, d, out=column)
     assert got is column and torch.equal(column, gradient)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,size", [(1, 128257), (300, 20001), (2, 37)])
+def test_gradient_in_place_is_the_same(handle, rows, size, dtype):
+    """Over all CTAs of a row and all rows at once, vectors and single entries."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    x = torch.randn(rows, size, device="cuda").to(ops.torch_dtype(dtype))
+    tokens = torch.randint(size, (rows,), device="cuda", dtype=torch.int32)
+    d = torch.randn(rows, device="cuda")
+    r = q4lin.logprobs(handle, x, tokens)
+    want = q4lin.logprobs_backward(handle, x, tokens, r.lse, r.entropy, d, d)
+    assert torch.equal(q4lin.logprobs_backward(handle, x, tokens, r.lse, r.entropy, d, d, out=x), want)
+
+
+def test_refusals_of_the_c_entries(handle):
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    x = torch.randn(4, 100, device="cuda")
+    f, i = torch.zeros(40, device="cuda"), torch.zeros(40, dtype=torch.int32, device="cuda")
+    top = torch.zeros(4, 3, device="cuda")
+    d = torch.zeros(4, 100, device="cuda")
+    at = lambda t, k=0: t.data_ptr() + 4 * k
+    inv, large = q4lin.Q4LIN_ERR_INVALID_ARG, q4lin.Q4LIN_ERR_TOO_LARGE
+
+    def forward(**change):
+        a = q4lin.q4lin_logprobs_t(at(x), 100, 0, 4, 100, at(i), at(f), at(f, 4), at(f, 8), 3, at(i, 8), at(top))
+        for n, v in change.items():
+            setattr(a, n, v)
+        return q4lin.q4lin_run_logprobs(handle.ptr, a, 0)
+
+    def backward(**change):
+        a = q4lin.q4lin_logprobs_backward_t(at(x), 100, 0, 4, 100, at(i), at(f), at(f, 4), at(f, 8), at(f, 12),
+                                            at(d), 100)
+        for n, v in change.items():
+            setattr(a, n, v)
+        return q4lin.q4lin_run_logprobs_backward(handle.ptr, a, 0)
+
+    assert forward() == q4lin.Q4LIN_OK and backward() == q4lin.Q4LIN_OK
+    assert forward(tokens=None, logprob=None, entropy=None, lse=None) == q4lin.Q4LIN_OK
+    assert forward(rows=0) == q4lin.Q4LIN_OK and backward(rows=0) == q4lin.Q4LIN_OK
+    for change in (dict(logits=None), dict(dtype=3), dict(dtype=-1), dict(rows=-1), dict(vocabulary=0),
+                   dict(row_stride=-1), dict(top=-1), dict(top=33), dict(vocabulary=2), dict(top_tokens=None),
+                   dict(top_logprobs=None), dict(logits=at(x) + 2), dict(tokens=at(i) + 1), dict(lse=at(f) + 2),
+                   dict(entropy=at(f)), dict(lse=at(f, 1)), dict(logprob=at(x, 399)), dict(lse=at(i)),
+                   dict(top_tokens=at(i, 2)), dict(row_stride=1 << 61)):
+        assert forward(**change) == inv, change
+    none = dict(tokens=None, logprob=None, entropy=None, lse=None, top=0)
+    assert forward(vocabulary=1 << 31, rows=1, **none) == large  # (no output can overlap so many)
+    for change in (dict(logits=None), dict(d_logits=None), dict(lse=None), dict(tokens=None), dict(entropy=None),
+                   dict(dtype=7), dict(rows=-1), dict(vocabulary=0), dict(row_stride=-1), dict(d_row_stride=99),
+                   dict(d_logits=at(d) + 2), dict(d_logits=at(x, 1)), dict(d_logits=at(x), d_row_stride=101),
+                   dict(lse=at(d, 9)), dict(d_entropy=at(d, 399)), dict(d_row_stride=1 << 61)):
+        assert backward(**change) == inv, change
+    assert q4lin.q4lin_run_logprobs(None, q4lin.q4lin_logprobs_t(), 0) == inv
+    assert q4lin.q4lin_run_logprobs(handle.ptr, None, 0) == inv
+    assert q4lin.q4lin_run_logprobs_backward(None, q4lin.q4lin_logprobs_backward_t(), 0) == inv
+    assert q4lin.q4lin_run_logprobs_backward(handle.ptr, None, 0) == inv
+    torch.cuda.synchronize()
+    assert status(handle) == 0
