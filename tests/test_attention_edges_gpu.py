@@ -329,3 +329,25 @@ def test_every_page_outside_the_cache_is_reported(handle, at, tokens, entry):
     assert status(handle) == 4
     host.table = good
     check_rows(out, lse, host, q, 100, 0.125, some(rng, tokens, 2), b=1, first=tokens, count=tokens)
+
+
+def test_a_sequence_alone_and_in_a_batch(handle):
+    """Where a walk is cut goes by everything that a call is given, so a sequence's rows may differ
+    in their last bits with the rest of the batch; both are within the tolerance of the exact."""
+    rng = np.random.default_rng(54)
+    counts, lengths = [1, 70, 3, 1], [3000, 900, 1500, 64]
+    host = ops.Cache(rng, lengths, 2, 32, 128)
+    table = host.table
+    q = ops.to_device(rng.standard_normal((75, 8, 128)).astype(np.float32))
+    out, lse = attend(handle, host, q, counts, lengths, 0.1)
+    scale = float(np.float32(0.1))
+    for b in range(4):
+        first = sum(counts[:b])
+        rows = some(rng, counts[b], 8, 20)
+        check_rows(out, lse, host, q, lengths[b], scale, rows, b=b, first=first, count=counts[b])
+        host.table = table[b:b + 1]
+        x = q[first:first + counts[b]]
+        alone = attend(handle, host, x, counts[b:b + 1], lengths[b:b + 1], 0.1)
+        check_rows(*alone, host, x, lengths[b], scale, rows)
+        host.table = table
+    assert status(handle) == 0
