@@ -351,3 +351,24 @@ def test_a_sequence_alone_and_in_a_batch(handle):
         check_rows(*alone, host, x, lengths[b], scale, rows)
         host.table = table
     assert status(handle) == 0
+
+
+@pytest.mark.parametrize("window", [0, 2, 5])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_queries_before_the_sequence_that_are_not_causal(handle, dtype, window):
+    """More queries than tokens: the first ones have negative positions and see what their window
+    leaves, like any other; those of an empty sequence see nothing.  Both kernels."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(55)
+    lengths, counts = [3, 0, 20], [7, 2, 30]
+    host = ops.Cache(rng, lengths, 1, 16, 64)
+    q = ops.to_device(rng.standard_normal((39, 2, 64)).astype(np.float32), dtype)
+    offsets = np.array([0, 7, 9, 39], np.int32)
+    want = ops.attention(host, ops.to_host(q), offsets, lengths, 0.125, causal=False, window=window)
+    try:
+        for split in (1, 1 << 40):
+            handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, split)
+            check(*attend(handle, host, q, counts, lengths, 0.125, causal=False, window=window), want, dtype)
+            assert status(handle) == 0
+    finally:
+        handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
