@@ -1,12 +1,12 @@
 // attention.cu -- attention of a few query rows per key/value head over the paged 8-bit
 // cache: single tokens, draft tokens, short chunks.
 //
-// Bound: the codes, 2 head_dim bytes per key and key/value head, read once for all query
-// rows of that head.  The keys of all sequences and heads form one list of 64-key tiles that
+// Bound: the codes, 2 head_dim bytes per key and key/value head, read once for up to 16 query
+// rows of that head (8 with 256 channels; more rows walk over them again, from L2).  The keys of all sequences and heads form one list of 64-key tiles that
 // is cut evenly over all warps of the GPU, whatever the sequences' lengths; a warp's share of
 // one head's keys is a piece.  A warp works alone: it has its own ring of bulk copies (a
 // page's keys or values of one head are contiguous), its own queries, running maximum, sum
-// and outputs, and the next piece's copies are on their way while it stores the last one.
+// and outputs, and a piece's first copies are on their way while its queries are rotated.
 // (CTAs that joined their warps after every piece spent 5 to 8 us on each: the latencies of
 // a loaded memory system, one after another, with nothing in flight.)  Heads that lie in one
 // share are stored at once; the others leave sums in the handle's workspace, which a second
@@ -14,8 +14,8 @@
 //
 // Measured (8 key/value heads of 128, 4 query heads each): 64 sequences of up to 8192 tokens,
 // 652 MB, 110 to 114 us: 5.8 TB/s, 0.86 of a copy's bandwidth; one sequence of 131071 tokens, 269
-// MB, 54 us: 5.0 TB/s, the start and the join a sixth of it.  One of 701 tokens (0.7 MB) 8.9 us,
-// 9 drafts of up to 5 tokens behind a window of 1024 (10 MB, 7 query heads) 21.8 us: the chain of
+// MB, 56 us: 4.8 TB/s, the start and the join a sixth of it.  One of 701 tokens (0.7 MB) 8.9 us,
+// 9 drafts of up to 5 tokens behind a window of 1024 (10 MB, 7 query heads) 22.0 us: the chain of
 // dependent loads, from the offsets to the page table to the first keys, and two launches.
 //
 // Products on the tensor cores (m16n8k16, fp16 operands, fp32 sums): codes - 128 are exact
@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
             bool turned;
             int cl, ch;
             rope_channels(g.a.rope, unit, &turned, &cl, &ch);
-            // Passes whose loads overlap (four of them spill with 128 channels: 113 against 110 us
-            // for 64 sequences, 22.5 against 21.8 for drafts).
+            // Passes whose loads overlap (with four, 128 channels spill in the kernel of 8 rows: 113
+            // against 110 us for 64 sequences; drafts 22.5 against 21.8, where 16 rows spill 108 bytes
+            // all the same, as 56 do with 256 channels).
             constexpr int kTogether = kPasses < 2 ? kPasses : 2;
             const int valid = min(R, P.tq * group - P.row0);  // rows (the others stay unread)
             if (lane >= valid && lane < R) mine.row[lane] = {0.f, -1, 0, -1};

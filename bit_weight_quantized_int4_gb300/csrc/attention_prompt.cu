@@ -25,9 +25,10 @@
 //
 // Bound: the products, 2 head_dim flops a pair for each of QT + PT terms.  Measured (8 key/value
 // heads of 128, 4 query heads each, the last 2048 of 8192 tokens): 240 us for rotated bf16
-// queries (QT 2, PT 1: 361 Gflop, 1.5 Pflop/s, 0.79 of a large library product's rate), 483 us
-// for fp32 (two terms of both, and outputs taken out every 8 steps: 363 without).  While walks run the tensor pipes are busy for 77 % of the time;
-// the scores' products, which read 8 KB of shared memory for 64 clocks of work, take the rest.
+// queries (QT 2, PT 1: 361 Gflop, 1.5 Pflop/s, 0.79 of a large library product's rate), 336 us
+// for fp16 (two terms of both), 479 us for fp32 (the same, and outputs taken out every 8 steps).
+// While walks run the tensor pipes are busy for 77 % of the time; the scores' products, which read
+// 8 KB of shared memory for 64 clocks of work, take the rest.
 // (Leaving out the exponentials, or the loads or stores of the widened codes, changed the
 // time by less than 4 %; two threads a row instead of one: 260 us; a share of the exponentials
 // as polynomials on the FMA pipes: 249 us and up.)  Whole walks on 152 SMs leave 16 % of them

@@ -381,7 +381,8 @@ def plan_kernel(handle: Handle, x, qweight, scales, bias, group_size: int, out) 
 # A decode step makes hundreds of these calls, some shorter on the GPU than their checks
 # here: types are compared as objects, and torch is looked up once.
 # `stream` is a raw handle (default: torch's current stream).  On another stream than theirs,
-# inputs have to be ready there, and kept until it has read them.
+# inputs have to be ready there, and kept until it has read them.  None of these calls is seen by
+# autograd: gradients are calls of their own (logprobs_backward, q4lin_run_backward_dx).
 class _Torch:
     """torch, its types' codes and its current stream's handle, filled at the first use."""
     module = None

@@ -377,17 +377,21 @@ typedef struct q4lin_attention {
  * h / (heads / kv_heads):
  *   x_j = scale * sum_d q_d K[j,d],  out_d = sum_j e^(x_j) V[j,d] / sum_j e^(x_j),
  *   lse = ln sum_j e^(x_j).
- * A query that sees no key (an empty sequence, a negative position) gets out = 0 and
- * lse = -infinity; a query with a NaN or an infinity gets NaN.  Codes are exact in the
- * tensor cores' fp16 operands; queries and probabilities enter them as two fp16 terms (22
- * bits), and everything is summed in fp32.  Sequences with many query rows go through a
- * tcgen05 kernel (whose bfloat16 outputs take probabilities of one fp16 term, 11 bits, and
- * which reads values relative to the largest value scale that its tile of queries sees),
- * the others through one that splits the keys evenly over the SMs (partial
+ * A query that sees no key (an empty sequence; causal and a negative position) gets out = 0
+ * and lse = -infinity; another one with a NaN or an infinity gets NaN.  Queries at negative
+ * positions are not rotated.  Codes are exact in the tensor cores' fp16 operands; queries and
+ * probabilities enter them as two fp16 terms (22 bits), and everything is summed in fp32.
+ * Sequences with many query rows go through a tcgen05 kernel (whose bfloat16 outputs take
+ * probabilities of one fp16 term, 11 bits; which reads values relative to the largest value
+ * scale of the keys that its 256 rows read; and whose sums cut off what fp32 has no room for:
+ * about 4e-6 of the outputs' norm for float32, 6e-5 for float16 and, at 131072 keys, 2e-4
+ * for bfloat16), the others through one that splits the keys evenly over the SMs (partial
  * results joined in a fixed order through the handle's workspace), so a batch may mix
- * prompts and single tokens (Q4LIN_OPT_ATTENTION_SPLIT_ROWS).  tokens == 0 or
- * batch == 0 is Q4LIN_OK.  Sequences of more than max_query tokens record code 4, and
- * their outputs are not written. */
+ * prompts and single tokens (Q4LIN_OPT_ATTENTION_SPLIT_ROWS).  The same call gives the same
+ * bits; where a walk is cut goes by the whole call, so a sequence's last bits may differ with
+ * the rest of its batch.  tokens == 0 or batch == 0 is Q4LIN_OK.  Sequences of more than
+ * max_query tokens record code 4, and their outputs are not written; where offsets decrease,
+ * other sequences' outputs may not be written either. */
 Q4LIN_API q4lin_status_t q4lin_run_attention(q4lin_handle_t handle,
                                              const q4lin_kv_cache_t* cache,
                                              const q4lin_attention_t* args, void* stream);
