@@ -39,6 +39,8 @@ constexpr int kRows = 8;         // query rows per MMA tile (two of its 16 rows 
 constexpr int kSlots = 3;        // half tiles (keys or values) in a warp's ring
 constexpr int kMaxBatch = 256;   // sequences per launch
 constexpr float kShift = 14.f;   // probabilities are kept as 2^14 p: fp16's range downwards
+// Undone before a logarithm, whose error grows with its distance from 0.
+constexpr float kUnshift = 1.f / 16384.f;
 constexpr int64_t kDrainNs = 4000000000LL;
 
 // Warps of the one CTA on an SM: what registers, rings and queries leave room for.
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
                         to_16x2(O[rt][nt][0] * inv, O[rt][nt][1] * inv, g.a.dtype);
             }
             if (t == 0 && g.a.lse)
-                g.a.lse[index] = l != 0.f ? ((m_run[rt] == -INFINITY ? 0.f : m_run[rt]) + lg2(l) - kShift) * kLn2
+                g.a.lse[index] = l != 0.f ? ((m_run[rt] == -INFINITY ? 0.f : m_run[rt]) + lg2(l * kUnshift)) * kLn2
                                           : -INFINITY;
         }
         pos += P.n;
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
             *reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D + d) =
                 make_uint2(to_16x2(a.x * inv, a.y * inv, g.a.dtype), to_16x2(a.z * inv, a.w * inv, g.a.dtype));
     }
-    if (lane == 0 && g.a.lse) g.a.lse[index] = l != 0.f ? (from + lg2(l) - kShift) * kLn2 : -INFINITY;
+    if (lane == 0 && g.a.lse) g.a.lse[index] = l != 0.f ? (from + lg2(l * kUnshift)) * kLn2 : -INFINITY;
 }
 
 // What a launch may have to do.

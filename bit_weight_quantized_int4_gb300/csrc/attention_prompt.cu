@@ -71,6 +71,8 @@ constexpr int kDrainF32 = 8, kDrainF16 = 64;
 constexpr int64_t kFewKeys = 32768;
 constexpr int kDrainSlots = 256;  // at most; one for each CTA that runs
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
+// Undone before a logarithm, whose error grows with its distance from 0.
+constexpr float kUnbase = 1.f / 128.f;
 // A score's factor is at least this, so that a masked score (-infinity) stays one.
 constexpr float kLeastFactor = 1e-37f;
 constexpr float kLeastRatio = 5.421010862427522e-20f;  // 2^-64
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             if (in && cut) {
                 unit[2 * kQ * D + r] = m, unit[2 * kQ * D + 2 * kQ + r] = l;
             } else if (in && g.a.lse) {
-                g.a.lse[index] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l) - kBase) * kLn2 : -INFINITY;
+                g.a.lse[index] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l * kUnbase)) * kLn2 : -INFINITY;
             }
         }
     } else if (warp < kIssueWarp) {
@@ -990,7 +992,7 @@ __device__ __forceinline__ void join_rows(const PromptArgs& g, int64_t unit0, in
                 reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D)[lane] =
                     make_uint2(to_16x2(o[q].x * inv, o[q].y * inv, g.a.dtype), to_16x2(o[q].z * inv, o[q].w * inv, g.a.dtype));
             if (lane == 0 && g.a.lse)
-                g.a.lse[index] = l[q] != 0.f ? ((mx[q] == -INFINITY ? 0.f : mx[q]) + lg2(l[q]) - kBase) * kLn2 : -INFINITY;
+                g.a.lse[index] = l[q] != 0.f ? ((mx[q] == -INFINITY ? 0.f : mx[q]) + lg2(l[q] * kUnbase)) * kLn2 : -INFINITY;
         }
     }
 }

@@ -372,3 +372,28 @@ def test_queries_before_the_sequence_that_are_not_causal(handle, dtype, window):
             assert status(handle) == 0
     finally:
         handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_log_sums_of_a_few_keys(handle, dim, dtype):
+    """Small scores of 1 to 20 keys: a log sum's own error, without the scores' share.  The logarithm
+    of a sum up to 32 is off by 5 x 2^-22 in powers of two, or 2^-20.2 in its own unit, and each
+    of the three roundings after it by 2^-24 of at most 8: 2^-20 + 2^-22 in all, beside 2^-20 of
+    the scores' sums of products.  Both kernels."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(56)
+    lengths = [1 + i % 20 for i in range(120)]
+    host = ops.Cache(rng, lengths, 2, 16, dim)
+    q = ops.to_device((rng.standard_normal((240, 8, dim)) * 0.05).astype(np.float32), dtype)
+    offsets = np.arange(121, dtype=np.int32) * 2
+    want = ops.attention(host, ops.to_host(q), offsets, lengths, 0.125)
+    some_key = ~np.isneginf(want[1])
+    try:
+        for split in (1, 1 << 40):
+            handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, split)
+            _, lse = attend(handle, host, q, [2] * 120, lengths, 0.125)
+            error = np.abs(ops.to_host(lse)[some_key] - want[1][some_key])
+            assert np.all(error <= (2.0**-20 * want[3] + 2.0**-20 + 2.0**-22)[some_key])
+    finally:
+        handle.set_option(q4lin.Q4LIN_OPT_ATTENTION_SPLIT_ROWS, 0)
