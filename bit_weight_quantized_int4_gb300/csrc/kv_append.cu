@@ -82,7 +82,7 @@ __device__ __forceinline__ Share find_share(const AppendArgs& g, int64_t id) {
         n = n - last * step < step ? n - last * step : step;
     }
     Share s = {lo, 0, 0, 0, 0, 0};
-    if (o0 < 0 || o1 > g.a.tokens || start < 0) {
+    if (o0 < 0 || o1 > g.a.tokens || (start < 0 && o1 > o0)) {
         if (threadIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
         return s;
     }

@@ -51,3 +51,21 @@ def test_offsets_outside_the_tokens_are_reported(handle, tokens, wrong):
         q4lin.kv_append(handle, cache, k, k, ops.to_device(offsets), ops.to_device(np.zeros(100, np.int32)))
         assert status(handle) == 4
         same(cache, host)
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 300])
+def test_a_sequence_without_new_tokens_may_start_anywhere(handle, tokens):
+    """A place in the batch that nobody holds, with a start of -1 or past its pages: nothing is
+    written for it, and nothing reported, whichever kernel runs."""
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(63)
+    counts = [0, tokens, 0, 0, tokens, 0]
+    host = ops.Cache(rng, [0, tokens + 5, 0, 0, tokens, 0], 2, 16, 64)
+    cache = host.device()
+    starts = np.array([-1, 5, -1, 1 << 30, 0, -2**31], np.int32)
+    k, v = (rng.standard_normal((2 * tokens, 2, 64)).astype(np.float32) for _ in range(2))
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    ops.append(host, k, v, offsets, starts)
+    q4lin.kv_append(handle, cache, ops.to_device(k), ops.to_device(v), ops.to_device(offsets), ops.to_device(starts))
+    same(cache, host)
+    assert status(handle) == 0
