@@ -1,5 +1,6 @@
-// operators.cpp -- C-ABI host layer of the operators around the linears: the paged 8-bit
-// key/value cache, attention over it, log probabilities and their gradient.  Everything that
+// operators.cpp -- C-ABI host layer of the operators around the linears: the paged 8-bit and
+// 4-bit key/value caches, attention over them, normalised and rotated queries and keys, log
+// probabilities and their gradient.  Everything that
 // the host can see is checked here before anything is enqueued; index arrays live on the
 // device and are checked by the kernels.
 #include <algorithm>
@@ -42,7 +43,8 @@ struct CacheBytes {
     }
 };
 
-q4lin_status_t check_cache(const q4lin_kv_cache_t* c, CacheBytes* n) {
+// bits: of a code. 8: one scale for a page and head, 4: one for each token of them.
+q4lin_status_t check_cache(const q4lin_kv_cache_t* c, CacheBytes* n, int bits = 8) {
     if (!c || c->num_pages < 1 || c->kv_heads < 1 || c->batch < 0 || c->pages_per_sequence < 1 ||
         c->table_stride < c->pages_per_sequence)
         return Q4LIN_ERR_INVALID_ARG;
@@ -50,12 +52,13 @@ q4lin_status_t check_cache(const q4lin_kv_cache_t* c, CacheBytes* n) {
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return Q4LIN_ERR_UNSUPPORTED;
     if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales || (c->batch > 0 && !c->page_table))
         return Q4LIN_ERR_INVALID_ARG;
-    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 4) ||
-        !aligned(c->v_scales, 4) || !aligned(c->page_table, 4))
+    const int64_t scale_bytes = bits == 8 ? 4 : 4 * c->page_size, scale_align = bits == 8 ? 4 : 16;
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, scale_align) ||
+        !aligned(c->v_scales, scale_align) || !aligned(c->page_table, 4))
         return Q4LIN_ERR_INVALID_ARG;
-    int64_t t;
-    if (!mul_ok(c->num_pages, c->kv_heads, &t) || !mul_ok(t, 4, &n->scales) ||
-        !mul_ok(t, c->page_size * c->head_dim, &n->codes) ||
+    int64_t t, page_heads;
+    if (!mul_ok(c->num_pages, c->kv_heads, &page_heads) || !mul_ok(page_heads, scale_bytes, &n->scales) ||
+        !mul_ok(page_heads, c->page_size * c->head_dim * bits / 8, &n->codes) ||
         !mul_ok(c->batch, c->table_stride, &t) || !mul_ok(t, 4, &n->table))
         return Q4LIN_ERR_INVALID_ARG;
     if (overlaps(c->k_codes, n->codes, c->v_codes, n->codes) ||
@@ -66,7 +69,7 @@ q4lin_status_t check_cache(const q4lin_kv_cache_t* c, CacheBytes* n) {
         overlaps(c->v_codes, n->codes, c->v_scales, n->scales))
         return Q4LIN_ERR_INVALID_ARG;
     // Grid and index limits of the kernels: positions and page numbers are 32 bits.
-    if (c->kv_heads > 65535 || n->scales / 4 > 0x7FFFFFFF || c->batch > 0x7FFFFFFF / 8 ||
+    if (c->kv_heads > 65535 || page_heads > 0x7FFFFFFF || c->batch > 0x7FFFFFFF / 8 ||
         c->pages_per_sequence > (0x7FFFFFFF - 64) / c->page_size)
         return Q4LIN_ERR_TOO_LARGE;
     return Q4LIN_OK;
@@ -87,15 +90,13 @@ q4lin_status_t finish(cudaError_t err) {
     return err == cudaSuccess ? Q4LIN_OK : Q4LIN_ERR_CUDA;
 }
 
-}  // namespace
-
-extern "C" {
-
-q4lin_status_t q4lin_run_kv_append(q4lin_handle_t h, const q4lin_kv_cache_t* cache,
-                                   const q4lin_kv_append_t* a, void* stream) {
+// An append to a cache of `bits` bits, by `launch`.
+template <typename Launch>
+q4lin_status_t run_append(q4lin_handle_t h, const q4lin_kv_cache_t* cache, const q4lin_kv_append_t* a,
+                          void* stream, int bits, Launch launch) {
     if (!h || !a) return Q4LIN_ERR_INVALID_ARG;
     CacheBytes n;
-    q4lin_status_t st = check_cache(cache, &n);
+    q4lin_status_t st = check_cache(cache, &n, bits);
     if (st != Q4LIN_OK) return st;
     if (!known_dtype(a->dtype) || a->tokens < 0) return Q4LIN_ERR_INVALID_ARG;
     int64_t kb, vb, rb;
@@ -117,21 +118,24 @@ q4lin_status_t q4lin_run_kv_append(q4lin_handle_t h, const q4lin_kv_cache_t* cac
     if (a->tokens > 0x7FFFFFFF) return Q4LIN_ERR_TOO_LARGE;
     DeviceGuard g(h->device);
     if (!g.ok()) return Q4LIN_ERR_CUDA;
-    return finish(q4lin::kv_append_launch(*cache, *a, make_ctx(h, static_cast<cudaStream_t>(stream))));
+    return finish(launch(*cache, *a, make_ctx(h, static_cast<cudaStream_t>(stream))));
 }
 
-q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cache,
-                                   const q4lin_attention_t* a, void* stream) {
+// Everything that the host can see of an attention's arguments; *idle: there is nothing to do.
+q4lin_status_t check_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cache, const q4lin_attention_t* a, int bits,
+                               bool* idle) {
+    *idle = false;
     if (!h || !a) return Q4LIN_ERR_INVALID_ARG;
     CacheBytes n;
-    q4lin_status_t st = check_cache(cache, &n);
+    q4lin_status_t st = check_cache(cache, &n, bits);
     if (st != Q4LIN_OK) return st;
     if (!known_dtype(a->dtype) || a->tokens < 0 || a->heads < 1 || a->heads % cache->kv_heads != 0 ||
         a->window < 0 || (a->causal != 0 && a->causal != 1))
         return Q4LIN_ERR_INVALID_ARG;
     int64_t qb, ob, lb, rb, t;
     if ((st = check_rope(a->rope, cache->head_dim, &rb)) != Q4LIN_OK) return st;
-    if (a->tokens == 0 || cache->batch == 0) return Q4LIN_OK;
+    *idle = a->tokens == 0 || cache->batch == 0;
+    if (*idle) return Q4LIN_OK;
     const int64_t size = size_of(a->dtype), D = cache->head_dim;
     // out is written 16 bytes at a time.
     if (a->max_query < 1 || !a->query || !a->out || !a->offsets || !a->lengths || !aligned(a->query, size) ||
@@ -154,6 +158,100 @@ q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cac
             return Q4LIN_ERR_INVALID_ARG;
     if (n.overlap(*cache, a->out, ob) || n.overlap(*cache, a->lse, lb) || overlaps(a->out, ob, a->lse, lb))
         return Q4LIN_ERR_INVALID_ARG;
+    return Q4LIN_OK;
+}
+
+// [tokens, heads, head_dim] with contiguous channels, in bytes; strides of axes of length one (or
+// none) are those of a contiguous array.
+struct Rows {
+    const void* p = nullptr;
+    int64_t bytes = 0, token = 0, head = 0;
+    int64_t span = 0;  // of one token's heads
+    bool same(const Rows& o) const { return p == o.p && token == o.token && head == o.head; }
+    // Whether no element lies in both: in ranges of their own, or in parts of their own of rows of
+    // one length (slices of one array).
+    bool apart(const Rows& o) const {
+        if (!overlaps(p, bytes, o.p, o.bytes)) return true;
+        if (token != o.token || span > token || o.span > token) return false;
+        const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(o.p) - reinterpret_cast<uintptr_t>(p)) % token;
+        const int64_t at = d < 0 ? d + token : d;
+        return at >= span && at + o.span <= token;
+    }
+};
+// False where pointer, strides or sizes are no array's.
+bool rows_of(const void* p, int64_t tokens, int64_t token_stride, int64_t heads, int64_t head_stride, int64_t dim,
+             int dtype, Rows* r) {
+    *r = Rows();
+    if (tokens == 0 || heads == 0) return true;
+    const int64_t size = size_of(dtype);
+    if (!p || !aligned(p, size)) return false;
+    if (heads == 1) head_stride = dim;
+    int64_t span;
+    if (head_stride < 0 || !mul_ok(heads - 1, head_stride, &span) || __builtin_add_overflow(span, dim, &span)) return false;
+    if (tokens == 1) token_stride = span;
+    if (!extent(tokens, token_stride, heads, head_stride, dim, size, &r->bytes)) return false;
+    if (!mul_ok(token_stride, size, &r->token) || !mul_ok(head_stride, size, &r->head)) return false;
+    r->p = p, r->span = span * size;
+    return true;
+}
+// Whether every element has a place of its own.
+bool distinct(const Rows& r, int64_t tokens, int64_t heads, int64_t row) {
+    if (!r.p) return true;
+    if (r.head >= row && r.token >= r.span) return true;
+    int64_t column;
+    return r.token >= row && mul_ok(tokens - 1, r.token, &column) && r.head >= column + row;
+}
+// Whether `y` may be written while `x` is read row by row: it is x, or apart from it.
+bool written_apart(const Rows& y, const Rows& x) { return y.same(x) || y.apart(x); }
+
+struct NormRows {
+    Rows x[2], y[2];  // queries, keys
+    int64_t rope;
+};
+q4lin_status_t check_norm_rope(const q4lin_norm_rope_t& a, NormRows* n) {
+    if (!known_dtype(a.dtype) || a.tokens < 0 || a.heads < 0 || a.kv_heads < 0 || a.heads + a.kv_heads < 1 ||
+        !(a.eps >= 0.f) || a.eps > 3.4028235e38f)
+        return Q4LIN_ERR_INVALID_ARG;
+    if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return Q4LIN_ERR_UNSUPPORTED;
+    const q4lin_status_t st = check_rope(a.rope, a.head_dim, &n->rope);
+    if (st != Q4LIN_OK) return st;
+    const int64_t D = a.head_dim, wb = D * 4, row = D * size_of(a.dtype);
+    if (!aligned(a.q_weight, 4) || !aligned(a.k_weight, 4) || !aligned(a.positions, 4) ||
+        !rows_of(a.q, a.tokens, a.q_token_stride, a.heads, a.q_head_stride, D, a.dtype, &n->x[0]) ||
+        !rows_of(a.k, a.tokens, a.k_token_stride, a.kv_heads, a.k_head_stride, D, a.dtype, &n->x[1]) ||
+        !rows_of(a.q_out, a.tokens, a.q_out_token_stride, a.heads, a.q_out_head_stride, D, a.dtype, &n->y[0]) ||
+        !rows_of(a.k_out, a.tokens, a.k_out_token_stride, a.kv_heads, a.k_out_head_stride, D, a.dtype, &n->y[1]) ||
+        !distinct(n->y[0], a.tokens, a.heads, row) || !distinct(n->y[1], a.tokens, a.kv_heads, row) ||
+        (a.rope.cos && a.tokens > 0 && !a.positions))
+        return Q4LIN_ERR_INVALID_ARG;
+    int64_t pb;
+    if (!mul_ok(a.tokens, 4, &pb)) return Q4LIN_ERR_INVALID_ARG;
+    if (!n->y[0].apart(n->y[1]) || !n->y[0].apart(n->x[1]) || !n->y[1].apart(n->x[0])) return Q4LIN_ERR_INVALID_ARG;
+    for (const Rows& y : n->y)
+        if (overlaps(y.p, y.bytes, a.q_weight, wb) || overlaps(y.p, y.bytes, a.k_weight, wb) ||
+            (a.rope.cos && (overlaps(y.p, y.bytes, a.positions, pb) || overlaps(y.p, y.bytes, a.rope.cos, n->rope) ||
+                            overlaps(y.p, y.bytes, a.rope.sin, n->rope))))
+            return Q4LIN_ERR_INVALID_ARG;
+    // Heads and rows are counted in 64 bits; a token's heads in an int.
+    if (a.heads > 0x7FFFFFF || a.kv_heads > 0x7FFFFFF || a.tokens > 0x7FFFFFFF) return Q4LIN_ERR_TOO_LARGE;
+    return Q4LIN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+q4lin_status_t q4lin_run_kv_append(q4lin_handle_t h, const q4lin_kv_cache_t* cache,
+                                   const q4lin_kv_append_t* a, void* stream) {
+    return run_append(h, cache, a, stream, 8, q4lin::kv_append_launch);
+}
+
+q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cache,
+                                   const q4lin_attention_t* a, void* stream) {
+    bool idle;
+    const q4lin_status_t st = check_attention(h, cache, a, 8, &idle);
+    if (st != Q4LIN_OK || idle) return st;
+    const int64_t t = a->tokens * a->heads;
     // The kernels count query rows in 32 bits, and the prompts' kernel keeps 32 bytes for each 256
     // rows of a key/value head in half of the workspace.
     constexpr int64_t kRowsMost = int64_t{1} << 27;
@@ -241,6 +339,94 @@ q4lin_status_t q4lin_run_logprobs_backward(q4lin_handle_t h, const q4lin_logprob
     DeviceGuard g(h->device);
     if (!g.ok()) return Q4LIN_ERR_CUDA;
     return finish(q4lin::logprobs_backward_launch(*a, make_ctx(h, static_cast<cudaStream_t>(stream))));
+}
+
+q4lin_status_t q4lin_run_kv4_append(q4lin_handle_t h, const q4lin_kv4_cache_t* cache,
+                                    const q4lin_kv_append_t* a, void* stream) {
+    return run_append(h, cache, a, stream, 4, q4lin::kv4_append_launch);
+}
+
+q4lin_status_t q4lin_run_kv4_read(q4lin_handle_t h, const q4lin_kv4_cache_t* cache, const q4lin_kv_read_t* a,
+                                  void* stream) {
+    if (!h || !a) return Q4LIN_ERR_INVALID_ARG;
+    CacheBytes n;
+    q4lin_status_t st = check_cache(cache, &n, 4);
+    if (st != Q4LIN_OK) return st;
+    if (!known_dtype(a->dtype) || a->tokens < 0) return Q4LIN_ERR_INVALID_ARG;
+    if (a->tokens == 0 || cache->batch == 0) return Q4LIN_OK;
+    int64_t ob;
+    if ((!a->k && !a->v) || !a->offsets || !a->starts || !aligned(a->k, 16) || !aligned(a->v, 16) ||
+        !aligned(a->offsets, 4) || !aligned(a->starts, 4) ||
+        !mul_ok(a->tokens, cache->kv_heads * cache->head_dim * size_of(a->dtype), &ob))
+        return Q4LIN_ERR_INVALID_ARG;
+    for (const void* out : {a->k, a->v})
+        if (n.overlap(*cache, out, ob) || overlaps(out, ob, cache->page_table, n.table) ||
+            overlaps(out, ob, a->offsets, (cache->batch + 1) * 4) || overlaps(out, ob, a->starts, cache->batch * 4))
+            return Q4LIN_ERR_INVALID_ARG;
+    if (overlaps(a->k, ob, a->v, ob)) return Q4LIN_ERR_INVALID_ARG;
+    if (a->tokens > 0x7FFFFFFF) return Q4LIN_ERR_TOO_LARGE;
+    DeviceGuard g(h->device);
+    if (!g.ok()) return Q4LIN_ERR_CUDA;
+    return finish(q4lin::kv4_read_launch(*cache, *a, make_ctx(h, static_cast<cudaStream_t>(stream))));
+}
+
+q4lin_status_t q4lin_run_kv4_attention(q4lin_handle_t h, const q4lin_kv4_cache_t* cache,
+                                       const q4lin_attention_t* a, void* stream) {
+    bool idle;
+    const q4lin_status_t st = check_attention(h, cache, a, 4, &idle);
+    if (st != Q4LIN_OK || idle) return st;
+    if (a->tokens * a->heads > 0x7FFFFFFF) return Q4LIN_ERR_TOO_LARGE;
+    DeviceGuard g(h->device);
+    if (!g.ok()) return Q4LIN_ERR_CUDA;
+    q4lin_attention_t args = *a;
+    // No sequence has more positions than its pages: a window of as many leaves every key.
+    if (args.window >= cache->pages_per_sequence * cache->page_size) args.window = 0;
+    return finish(q4lin::kv4_attention_launch(*cache, args, make_ctx(h, static_cast<cudaStream_t>(stream))));
+}
+
+q4lin_status_t q4lin_run_norm_rope(q4lin_handle_t h, const q4lin_norm_rope_t* a, void* stream) {
+    if (!h || !a) return Q4LIN_ERR_INVALID_ARG;
+    NormRows n;
+    const q4lin_status_t st = check_norm_rope(*a, &n);
+    if (st != Q4LIN_OK || a->tokens == 0) return st;
+    if (!written_apart(n.y[0], n.x[0]) || !written_apart(n.y[1], n.x[1])) return Q4LIN_ERR_INVALID_ARG;
+    DeviceGuard g(h->device);
+    if (!g.ok()) return Q4LIN_ERR_CUDA;
+    return finish(q4lin::norm_rope_launch(*a, make_ctx(h, static_cast<cudaStream_t>(stream))));
+}
+
+q4lin_status_t q4lin_run_norm_rope_backward(q4lin_handle_t h, const q4lin_norm_rope_backward_t* b, void* stream) {
+    if (!h || !b) return Q4LIN_ERR_INVALID_ARG;
+    const q4lin_norm_rope_t& a = b->forward;
+    NormRows n;
+    q4lin_status_t st = check_norm_rope(a, &n);
+    if (st != Q4LIN_OK) return st;
+    if (!aligned(b->d_q_weight, 4) || !aligned(b->d_k_weight, 4)) return Q4LIN_ERR_INVALID_ARG;
+    const int64_t wb = a.head_dim * 4;
+    Rows d[2];
+    if (!rows_of(b->d_q_out, a.tokens, b->d_q_out_token_stride, a.heads, b->d_q_out_head_stride, a.head_dim, a.dtype, &d[0]) ||
+        !rows_of(b->d_k_out, a.tokens, b->d_k_out_token_stride, a.kv_heads, b->d_k_out_head_stride, a.head_dim, a.dtype, &d[1]) ||
+        overlaps(b->d_q_weight, wb, b->d_k_weight, wb))
+        return Q4LIN_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i) {
+        if (!written_apart(n.y[i], n.x[i]) || !written_apart(n.y[i], d[i]) || !n.y[i].apart(d[1 - i]))
+            return Q4LIN_ERR_INVALID_ARG;
+        float* dw = i ? b->d_k_weight : b->d_q_weight;
+        for (const Rows* r : {&n.x[0], &n.x[1], &n.y[0], &n.y[1], &d[0], &d[1]})
+            if (overlaps(dw, wb, r->p, r->bytes)) return Q4LIN_ERR_INVALID_ARG;
+        if (overlaps(dw, wb, a.q_weight, wb) || overlaps(dw, wb, a.k_weight, wb) ||
+            (a.rope.cos && (overlaps(dw, wb, a.positions, a.tokens * 4) || overlaps(dw, wb, a.rope.cos, n.rope) ||
+                            overlaps(dw, wb, a.rope.sin, n.rope))))
+            return Q4LIN_ERR_INVALID_ARG;
+    }
+    DeviceGuard g(h->device);
+    if (!g.ok()) return Q4LIN_ERR_CUDA;
+    const q4lin::LaunchCtx c = make_ctx(h, static_cast<cudaStream_t>(stream));
+    if (a.tokens > 0) return finish(q4lin::norm_rope_backward_launch(*b, c));
+    cudaError_t e = cudaSuccess;
+    if (b->d_q_weight) e = cudaMemsetAsync(b->d_q_weight, 0, wb, c.stream);
+    if (b->d_k_weight && e == cudaSuccess) e = cudaMemsetAsync(b->d_k_weight, 0, wb, c.stream);
+    return finish(e);
 }
 
 }  // extern "C"

@@ -64,6 +64,23 @@ __device__ __forceinline__ void store_one(void* p, int dtype, int64_t i, float x
         static_cast<unsigned short*>(p)[i] = to_16(x, dtype);
 }
 
+// Four consecutive elements; `vec`: the address is aligned to the four of them.
+__device__ __forceinline__ void store_four(void* p, int dtype, int64_t i, bool vec, const float* x) {
+    if (!vec) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_one(p, dtype, i + e, x[e]);
+    } else if (dtype == Q4LIN_DTYPE_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<unsigned short*>(p) + i) =
+            make_uint2(to_16x2(x[0], x[1], dtype), to_16x2(x[2], x[3], dtype));
+    }
+}
+// Whether groups of four elements of rows with these strides are aligned for load_four and store_four.
+inline bool fours_aligned(const void* p, int dtype, int64_t stride0, int64_t stride1) {
+    return reinterpret_cast<uintptr_t>(p) % (4 * dtype_size(dtype)) == 0 && stride0 % 4 == 0 && stride1 % 4 == 0;
+}
+
 // Row `position` of the rotation for the eight channels of unit u (two groups of four, see
 // rope_channels): the four cosines and sines.
 __device__ __forceinline__ void rope_load(const q4lin_rope_t& r, int64_t position, int u, float (&c)[4],

@@ -117,6 +117,28 @@ class q4lin_attention_t(ctypes.Structure):
                 ("rope", q4lin_rope_t)]
 
 
+class q4lin_kv_read_t(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("dtype", _i32), ("tokens", _i64), ("offsets", _vp),
+                ("starts", _vp)]
+
+
+class q4lin_norm_rope_t(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("q_token_stride", _i64), ("q_head_stride", _i64),
+                ("k_token_stride", _i64), ("k_head_stride", _i64), ("q_weight", _vp),
+                ("k_weight", _vp), ("q_out", _vp), ("k_out", _vp), ("q_out_token_stride", _i64),
+                ("q_out_head_stride", _i64), ("k_out_token_stride", _i64),
+                ("k_out_head_stride", _i64), ("dtype", _i32), ("tokens", _i64), ("heads", _i64),
+                ("kv_heads", _i64), ("head_dim", _i64), ("positions", _vp),
+                ("rope", q4lin_rope_t), ("eps", ctypes.c_float)]
+
+
+class q4lin_norm_rope_backward_t(ctypes.Structure):
+    _fields_ = [("forward", q4lin_norm_rope_t), ("d_q_out", _vp), ("d_k_out", _vp),
+                ("d_q_out_token_stride", _i64), ("d_q_out_head_stride", _i64),
+                ("d_k_out_token_stride", _i64), ("d_k_out_head_stride", _i64),
+                ("d_q_weight", _vp), ("d_k_weight", _vp)]
+
+
 class q4lin_logprobs_t(ctypes.Structure):
     _fields_ = [("logits", _vp), ("row_stride", _i64), ("dtype", _i32), ("rows", _i64),
                 ("vocabulary", _i64), ("tokens", _vp), ("logprob", _vp), ("entropy", _vp),
@@ -132,6 +154,11 @@ class q4lin_logprobs_backward_t(ctypes.Structure):
 
 for _name, _types in (("q4lin_run_kv_append", (q4lin_kv_cache_t, q4lin_kv_append_t)),
                       ("q4lin_run_attention", (q4lin_kv_cache_t, q4lin_attention_t)),
+                      ("q4lin_run_kv4_append", (q4lin_kv_cache_t, q4lin_kv_append_t)),
+                      ("q4lin_run_kv4_read", (q4lin_kv_cache_t, q4lin_kv_read_t)),
+                      ("q4lin_run_kv4_attention", (q4lin_kv_cache_t, q4lin_attention_t)),
+                      ("q4lin_run_norm_rope", (q4lin_norm_rope_t,)),
+                      ("q4lin_run_norm_rope_backward", (q4lin_norm_rope_backward_t,)),
                       ("q4lin_run_logprobs", (q4lin_logprobs_t,)),
                       ("q4lin_run_logprobs_backward", (q4lin_logprobs_backward_t,))):
     _f = getattr(_lib, _name)
@@ -271,6 +298,31 @@ def q4lin_run_logprobs(handle, args, stream) -> int:
 def q4lin_run_logprobs_backward(handle, args, stream) -> int:
     """args: q4lin_logprobs_backward_t."""
     return _lib.q4lin_run_logprobs_backward(handle, args, stream)
+
+
+def q4lin_run_kv4_append(handle, cache, args, stream) -> int:
+    """cache: q4lin_kv_cache_t of 4-bit codes; args: q4lin_kv_append_t."""
+    return _lib.q4lin_run_kv4_append(handle, cache, args, stream)
+
+
+def q4lin_run_kv4_read(handle, cache, args, stream) -> int:
+    """cache: q4lin_kv_cache_t of 4-bit codes; args: q4lin_kv_read_t."""
+    return _lib.q4lin_run_kv4_read(handle, cache, args, stream)
+
+
+def q4lin_run_kv4_attention(handle, cache, args, stream) -> int:
+    """cache: q4lin_kv_cache_t of 4-bit codes; args: q4lin_attention_t."""
+    return _lib.q4lin_run_kv4_attention(handle, cache, args, stream)
+
+
+def q4lin_run_norm_rope(handle, args, stream) -> int:
+    """args: q4lin_norm_rope_t."""
+    return _lib.q4lin_run_norm_rope(handle, args, stream)
+
+
+def q4lin_run_norm_rope_backward(handle, args, stream) -> int:
+    """args: q4lin_norm_rope_backward_t."""
+    return _lib.q4lin_run_norm_rope_backward(handle, args, stream)
 
 
 # ---------------------------------------------------------------- torch convenience
@@ -426,7 +478,7 @@ def _check_vector(t, n, dtype, what):
 def _head_strides(t, what):
     """Token and head strides of [tokens, heads, head_dim] with contiguous channels."""
     strides = t.stride()
-    if len(strides) != 3 or strides[2] != 1:
+    if len(strides) != 3 or (strides[2] != 1 and t.numel()):
         raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous channels")
     return strides
 
@@ -454,22 +506,15 @@ def _rope_args(rope, interleaved):
     return q4lin_rope_t(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], interleaved)
 
 
-class KVCache:
-    """The tensors of a paged 8-bit key/value cache (q4lin_kv_cache_t).
-
-    k_codes uint8 [num_pages, kv_heads, page_size, head_dim], v_codes uint8 [num_pages,
-    kv_heads, head_dim, page_size], k_scales and v_scales float32 [num_pages, kv_heads],
-    page_table int32 [batch, pages per sequence].  The tensors stay the caller's; the page
-    table's contents may change between calls."""
+class _PagedCache:
+    """What the paged caches share: `shapes` gives the codes' and scales' shapes."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, page_table):
-        if k_codes.dim() != 4:
-            raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim]")
-        pages, heads, page, dim = k_codes.shape
-        for t, shape, kind, what in ((k_codes, (pages, heads, page, dim), "uint8", "k_codes"),
-                                     (v_codes, (pages, heads, dim, page), "uint8", "v_codes"),
-                                     (k_scales, (pages, heads), "float32", "k_scales"),
-                                     (v_scales, (pages, heads), "float32", "v_scales")):
+        pages, heads, page, dim = self.sizes(k_codes)
+        shapes = self.shapes(pages, heads, page, dim)
+        for t, shape, kind, what in zip((k_codes, v_codes, k_scales, v_scales), shapes,
+                                        ("uint8", "uint8", "float32", "float32"),
+                                        ("k_codes", "v_codes", "k_scales", "v_scales")):
             if tuple(t.shape) != shape or str(t.dtype) != "torch." + kind or not t.is_contiguous():
                 raise ValueError(f"{what} must be a contiguous {kind} {list(shape)} tensor")
         if page_table.dim() != 2 or str(page_table.dtype) != "torch.int32" or \
@@ -490,17 +535,63 @@ class KVCache:
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, page_table):
         """A cache with nothing in it, on the page table's device."""
         import torch
-        new = lambda *shape: torch.full(shape, 128, dtype=torch.uint8, device=page_table.device)
-        scales = lambda: torch.zeros(num_pages, kv_heads, device=page_table.device)
-        return cls(new(num_pages, kv_heads, page_size, head_dim), scales(),
-                   new(num_pages, kv_heads, head_dim, page_size), scales(), page_table)
+        k, v, ks, vs = cls.shapes(num_pages, kv_heads, page_size, head_dim)
+        codes = lambda shape: torch.full(shape, cls.zero, dtype=torch.uint8, device=page_table.device)
+        scales = lambda shape: torch.zeros(shape, device=page_table.device)
+        return cls(codes(k), scales(ks), codes(v), scales(vs), page_table)
 
 
-def kv_append(handle: Handle, cache: KVCache, k, v, offsets, starts, rope=None,
+class KVCache(_PagedCache):
+    """The tensors of a paged 8-bit key/value cache (q4lin_kv_cache_t).
+
+    k_codes uint8 [num_pages, kv_heads, page_size, head_dim], v_codes uint8 [num_pages,
+    kv_heads, head_dim, page_size], k_scales and v_scales float32 [num_pages, kv_heads],
+    page_table int32 [batch, pages per sequence].  The tensors stay the caller's; the page
+    table's contents may change between calls."""
+    zero = 128  # the bytes that stand for 0
+    run_append, run_attention = _lib.q4lin_run_kv_append, _lib.q4lin_run_attention
+
+    @staticmethod
+    def sizes(k_codes):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim]")
+        return tuple(k_codes.shape)
+
+    @staticmethod
+    def shapes(pages, heads, page, dim):
+        return ((pages, heads, page, dim), (pages, heads, dim, page), (pages, heads), (pages, heads))
+
+
+class KVCache4(_PagedCache):
+    """The tensors of a paged 4-bit key/value cache (q4lin_kv4_cache_t), for kv_append, kv_read
+    and attention.
+
+    k_codes and v_codes uint8 [num_pages, kv_heads, page_size, head_dim / 2] (the even channel
+    in the low four bits), k_scales and v_scales float32 [num_pages, kv_heads, page_size],
+    page_table as in KVCache."""
+    zero = 0x88
+    run_append, run_attention = _lib.q4lin_run_kv4_append, _lib.q4lin_run_kv4_attention
+
+    @staticmethod
+    def sizes(k_codes):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim / 2]")
+        pages, heads, page, half = k_codes.shape
+        return pages, heads, page, 2 * half
+
+    @staticmethod
+    def shapes(pages, heads, page, dim):
+        if dim % 2:
+            raise ValueError("head_dim must be even")
+        codes, scales = (pages, heads, page, dim // 2), (pages, heads, page)
+        return codes, codes, scales, scales
+
+
+def kv_append(handle: Handle, cache, k, v, offsets, starts, rope=None,
               interleaved: bool = False, stream=None) -> None:
     """Append k (rotated by rope = (cos, sin) on the way) and v, [tokens, kv_heads, head_dim]
-    each and possibly slices of a larger tensor, to the cache: rows offsets[b] ..
-    offsets[b + 1] become tokens starts[b], starts[b] + 1, ... of sequence b."""
+    each and possibly slices of a larger tensor, to the cache (KVCache or KVCache4): rows
+    offsets[b] .. offsets[b + 1] become tokens starts[b], starts[b] + 1, ... of sequence b."""
     c = cache.args
     cos, sin = rope or (None, None)
     _check_device(handle, cache.k_codes, k, v, offsets, starts, cos, sin)
@@ -513,15 +604,49 @@ def kv_append(handle: Handle, cache: KVCache, k, v, offsets, starts, rope=None,
                              _check_vector(offsets, batch + 1, int32, "offsets"),
                              _check_vector(starts, batch, int32, "starts"),
                              _rope_args(rope, interleaved))
-    st = _lib.q4lin_run_kv_append(handle.ptr, c, args, _stream_of(stream, handle))
+    run = cache.run_append
+    st = run(handle.ptr, c, args, _stream_of(stream, handle))
     if st != Q4LIN_OK:
-        raise Q4LinError(st, "q4lin_run_kv_append")
+        raise Q4LinError(st, run.__name__)
 
 
-def attention(handle: Handle, cache: KVCache, query, offsets, lengths, scale: float,
+def kv_read(handle: Handle, cache: KVCache4, offsets, starts, tokens: int, dtype=None, k=None,
+            v=None, stream=None):
+    """Tokens of a 4-bit cache as dense keys and values [tokens, kv_heads, head_dim] of `dtype`
+    (default float32): token starts[b] + i of sequence b becomes row offsets[b] + i; `tokens` rows
+    in all.  k and v: outputs to use (rows of no sequence are left as they are there)."""
+    c = cache.args
+    if not isinstance(cache, KVCache4):
+        raise ValueError("cache must be a KVCache4")
+    _check_device(handle, cache.k_codes, offsets, starts, k, v)
+    given = k if k is not None else v
+    if dtype is None:
+        dtype = _Torch.float32 if given is None else given.dtype
+    code = _Torch.codes.get(dtype)
+    if code is None:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    shape = tokens, c.kv_heads, c.head_dim
+    for t, what in ((k, "k"), (v, "v")):
+        if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} tensor")
+    device = cache.k_codes.device
+    k = _new(shape, dtype, device, stream) if k is None else k
+    v = _new(shape, dtype, device, stream) if v is None else v
+    batch, int32 = c.batch, _Torch.int32
+    args = q4lin_kv_read_t(k.data_ptr(), v.data_ptr(), code, tokens,
+                           _check_vector(offsets, batch + 1, int32, "offsets"),
+                           _check_vector(starts, batch, int32, "starts"))
+    st = _lib.q4lin_run_kv4_read(handle.ptr, c, args, _stream_of(stream, handle))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st, "q4lin_run_kv4_read")
+    return k, v
+
+
+def attention(handle: Handle, cache, query, offsets, lengths, scale: float,
               max_query: Optional[int] = None, rope=None, interleaved: bool = False,
               causal: bool = True, window: int = 0, out=None, lse=None, stream=None):
-    """Attention of query [tokens, heads, head_dim] over the cache (q4lin_run_attention).
+    """Attention of query [tokens, heads, head_dim] over the cache (q4lin_run_attention, or
+    q4lin_run_kv4_attention for a KVCache4).
     lengths[b] counts sequence b's tokens in the cache, those of its queries included;
     max_query: no sequence has more query tokens (default: all of them; 1 for single tokens
     spares a batch the launches for prompts).  Returns (out, lse): out like query, lse float32
@@ -548,10 +673,86 @@ def attention(handle: Handle, cache: KVCache, query, offsets, lengths, scale: fl
                              _check_vector(offsets, batch + 1, int32, "offsets"),
                              _check_vector(lengths, batch, int32, "lengths"), scale,
                              causal, window, _rope_args(rope, interleaved))
-    st = _lib.q4lin_run_attention(handle.ptr, c, args, _stream_of(stream, handle))
+    run = cache.run_attention
+    st = run(handle.ptr, c, args, _stream_of(stream, handle))
     if st != Q4LIN_OK:
-        raise Q4LinError(st, "q4lin_run_attention")
+        raise Q4LinError(st, run.__name__)
     return out, lse
+
+
+def _norm_args(handle, q, k, q_weight, k_weight, positions, rope, eps, interleaved, q_out, k_out,
+               stream):
+    """(q4lin_norm_rope_t, q_out, k_out); the outputs are made where they are not given."""
+    cos, sin = rope or (None, None)
+    _check_device(handle, q, k, q_weight, k_weight, positions, cos, sin, q_out, k_out)
+    qs, ks = _head_strides(q, "q"), _head_strides(k, "k")
+    tokens, heads, dim = q.shape
+    if k.shape[0] != tokens or k.shape[2] != dim or k.dtype is not q.dtype:
+        raise ValueError("q and k must be [tokens, heads, head_dim] and [tokens, kv_heads, head_dim] of one type")
+    outs = []
+    for t, x, what in ((q_out, q, "q"), (k_out, k, "k")):
+        if t is None:
+            t = _new(x.shape, x.dtype, x.device, stream)
+        elif t.shape != x.shape or t.dtype is not x.dtype:
+            raise ValueError(f"the output for {what} must have its shape and type")
+        outs.append((t, _head_strides(t, f"the output for {what}")))
+    weight = lambda w, what: None if w is None else _check_vector(w, dim, _Torch.float32, what)
+    if rope is not None and positions is None:
+        raise ValueError("a rotation needs positions")
+    (qo, qos), (ko, kos) = outs
+    args = q4lin_norm_rope_t(
+        q.data_ptr(), k.data_ptr(), qs[0], qs[1], ks[0], ks[1], weight(q_weight, "q_weight"),
+        weight(k_weight, "k_weight"), qo.data_ptr(), ko.data_ptr(), qos[0], qos[1], kos[0], kos[1],
+        _dtype_code(q, "q"), tokens, heads, k.shape[1], dim,
+        None if positions is None else _check_vector(positions, tokens, _Torch.int32, "positions"),
+        _rope_args(rope, interleaved), eps)
+    return args, qo, ko
+
+
+def norm_rope(handle: Handle, q, k, q_weight=None, k_weight=None, positions=None, rope=None,
+              eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """q [tokens, heads, head_dim] and k [tokens, kv_heads, head_dim], possibly slices of a larger
+    tensor, normalised per head, times their weights (float32 [head_dim], None for ones), and
+    rotated by rope = (cos, sin) at positions (int32 [tokens]).  q_out and k_out: outputs to use,
+    q and k themselves among them.  Returns (q_out, k_out)."""
+    args, q_out, k_out = _norm_args(handle, q, k, q_weight, k_weight, positions, rope, eps,
+                                    interleaved, q_out, k_out, stream)
+    st = _lib.q4lin_run_norm_rope(handle.ptr, args, _stream_of(stream, handle))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st, "q4lin_run_norm_rope")
+    return q_out, k_out
+
+
+class NormRopeGradients(NamedTuple):
+    """Results of norm_rope_backward: like q and k, and float32 [head_dim] each (None where the
+    weight was None)."""
+    d_q: object
+    d_k: object
+    d_q_weight: object
+    d_k_weight: object
+
+
+def norm_rope_backward(handle: Handle, q, k, q_weight, k_weight, positions, rope, d_q_out, d_k_out,
+                       eps: float = 1e-6, interleaved: bool = False, d_q=None, d_k=None,
+                       stream=None) -> NormRopeGradients:
+    """Gradients of norm_rope for q, k and the weights, given its inputs and the gradients for
+    its outputs (of any strides).  d_q and d_k: outputs to use; d_q may be q or d_q_out, d_k may be
+    k or d_k_out."""
+    forward, d_q, d_k = _norm_args(handle, q, k, q_weight, k_weight, positions, rope, eps,
+                                   interleaved, d_q, d_k, stream)
+    _check_device(handle, d_q_out, d_k_out)
+    if d_q_out.shape != q.shape or d_k_out.shape != k.shape or d_q_out.dtype is not q.dtype \
+            or d_k_out.dtype is not q.dtype:
+        raise ValueError("d_q_out and d_k_out must have the shapes and the type of q and k")
+    dqs, dks = _head_strides(d_q_out, "d_q_out"), _head_strides(d_k_out, "d_k_out")
+    new = lambda w: None if w is None else _new(w.shape, w.dtype, w.device, stream)
+    dqw, dkw = new(q_weight), new(k_weight)
+    args = q4lin_norm_rope_backward_t(forward, d_q_out.data_ptr(), d_k_out.data_ptr(), dqs[0], dqs[1],
+                                      dks[0], dks[1], _ptr(dqw), _ptr(dkw))
+    st = _lib.q4lin_run_norm_rope_backward(handle.ptr, args, _stream_of(stream, handle))
+    if st != Q4LIN_OK:
+        raise Q4LinError(st, "q4lin_run_norm_rope_backward")
+    return NormRopeGradients(d_q, d_k, dqw, dkw)
 
 
 class LogProbs(NamedTuple):

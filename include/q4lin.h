@@ -444,6 +444,108 @@ Q4LIN_API q4lin_status_t q4lin_run_logprobs_backward(q4lin_handle_t handle,
                                                      const q4lin_logprobs_backward_t* args,
                                                      void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * A decoder layer over a cache in 4 bits: queries and keys normalised per head and rotated,
+ * keys and values quantised into the cache, read back, and attended to.  Index arrays are
+ * read and checked on the device as above. */
+
+/* Norm of each head of queries and keys, and the position rotation, in one pass:
+ *   r = 1 / sqrt(sum_d x_d^2 / head_dim + eps),   y = rotation(x r w),
+ * the rotation as in q4lin_rope_t, by the token's entry of `positions`.  Everything is fp32
+ * up to the one rounding to the type.  Rows whose squares pass fp32's range are scaled by a
+ * power of two first, so finite rows have finite norms. */
+typedef struct q4lin_norm_rope {
+    const void* q; /* [tokens, heads, head_dim], channels contiguous */
+    const void* k; /* [tokens, kv_heads, head_dim] */
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride; /* elements */
+    const float* q_weight; /* [head_dim], or NULL for ones */
+    const float* k_weight;
+    void* q_out; /* as q and k; may be them (same pointer and strides) */
+    void* k_out;
+    int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+    int dtype;                      /* q4lin_dtype_t of all four */
+    int64_t tokens, heads, kv_heads; /* either number of heads may be 0 */
+    int64_t head_dim;               /* 64, 128 or 256 */
+    const int32_t* positions;       /* [tokens]; not read without a rotation */
+    q4lin_rope_t rope;
+    float eps; /* finite, >= 0 */
+} q4lin_norm_rope_t;
+
+/* No two elements of an output may share memory, nor an output with an input or the other
+ * output, but q_out with q and k_out with k.  A token whose position is outside the rotation
+ * table records code 4 and its outputs are not written.  tokens == 0 is Q4LIN_OK. */
+Q4LIN_API q4lin_status_t q4lin_run_norm_rope(q4lin_handle_t handle, const q4lin_norm_rope_t* args,
+                                             void* stream);
+
+typedef struct q4lin_norm_rope_backward {
+    q4lin_norm_rope_t forward; /* its inputs; q_out, k_out and their strides are d_q and d_k, the
+                                  gradients for q and k */
+    const void* d_q_out; /* gradients for q_out and k_out, of the same shapes and type; any strides */
+    const void* d_k_out; /* (0 for a gradient that is the same for all tokens or heads) */
+    int64_t d_q_out_token_stride, d_q_out_head_stride, d_k_out_token_stride, d_k_out_head_stride;
+    float* d_q_weight; /* [head_dim], or NULL */
+    float* d_k_weight;
+} q4lin_norm_rope_backward_t;
+
+/* Gradients of q4lin_run_norm_rope.  With g the rotation undone on a row of d_q_out (d_k_out)
+ * and u = x r:
+ *   d_w = sum over tokens and heads of g u,   d_x = r (g w - u sum_d(g w u) / head_dim).
+ * Sums are fp32 in a fixed order (the same call gives the same bits).  d_q may be q or
+ * d_q_out (same pointer and strides), d_k may be k or d_k_out; no other memory may be shared.
+ * A token whose position is outside the rotation table records code 4, has no part in d_w
+ * and its d_q and d_k are not written.  tokens == 0 writes zeros to d_q_weight and
+ * d_k_weight.  Uses the handle's workspace. */
+Q4LIN_API q4lin_status_t q4lin_run_norm_rope_backward(q4lin_handle_t handle,
+                                                      const q4lin_norm_rope_backward_t* args,
+                                                      void* stream);
+
+/* A key/value cache of 4-bit codes in pages of page_size tokens, with a scale for each token
+ * and head.  The members of q4lin_kv_cache_t, which mean here:
+ *   k_codes, v_codes    uint8 [num_pages, kv_heads, page_size, head_dim / 2], 16-byte aligned;
+ *             the low four bits are the even channel's (as in packed weights), and a code c
+ *             stands for (c - 8) * scale
+ *   k_scales, v_scales  float32 [num_pages, kv_heads, page_size], 16-byte aligned, >= 0
+ * page_table, page_size (16, 32 or 64) and head_dim (64, 128 or 256) as there.  Slots of a
+ * page behind a sequence's length are never read as numbers: their codes and scales may be
+ * anything. */
+typedef q4lin_kv_cache_t q4lin_kv4_cache_t;
+
+/* Append keys (rotated on the way, if args->rope says so) and values.  Of each new token and
+ * head, with amax the largest finite |x| of its head_dim channels (keys after the rotation):
+ *   s    = amax * fl(1/7.5)                            (a scale below 2^-126 is 0)
+ *   code = clamp(rint(x * fl(1/s)), -8, 7) + 8, or 8 when s is 0.
+ * All 16 codes are used and no finite x is further than about s / 2 from what its code stands
+ * for.  Rounding as in q4lin_run_kv_append: the bytes are determined by the inputs.  An
+ * infinity becomes code 15 or 0, a NaN 8, and either records code 3 in the status word.
+ * Tokens that the cache held before are not touched.  The arguments, their checks and the
+ * lengths as there. */
+Q4LIN_API q4lin_status_t q4lin_run_kv4_append(q4lin_handle_t handle,
+                                              const q4lin_kv4_cache_t* cache,
+                                              const q4lin_kv_append_t* args, void* stream);
+
+typedef struct q4lin_kv_read {
+    void* k; /* [tokens, kv_heads, head_dim], contiguous, 16-byte aligned; or NULL */
+    void* v;
+    int dtype;              /* q4lin_dtype_t of k and v */
+    int64_t tokens;         /* tokens read, of all sequences */
+    const int32_t* offsets; /* [batch + 1]: sequence b's are rows offsets[b] .. offsets[b+1] */
+    const int32_t* starts;  /* [batch]: the first token of sequence b that is read */
+} q4lin_kv_read_t;
+
+/* Read tokens back: (code - 8) * scale in fp32, rounded once to the type.  Token
+ * starts[b] + i of sequence b becomes row offsets[b] + i; rows of no sequence are left as they
+ * are.  A token without a page in the table records code 4 and its row is left as well.
+ * tokens == 0 or batch == 0 is Q4LIN_OK.  No output may overlap an input or the other one. */
+Q4LIN_API q4lin_status_t q4lin_run_kv4_read(q4lin_handle_t handle, const q4lin_kv4_cache_t* cache,
+                                            const q4lin_kv_read_t* args, void* stream);
+
+/* Attention over a 4-bit cache: as q4lin_run_attention in its arguments, checks, masks and
+ * results.  Codes are exact in the tensor cores' fp16 operands here too; the keys' scales
+ * multiply the scores and the values' scales the probabilities, in fp32. */
+Q4LIN_API q4lin_status_t q4lin_run_kv4_attention(q4lin_handle_t handle,
+                                                 const q4lin_kv4_cache_t* cache,
+                                                 const q4lin_attention_t* args, void* stream);
+
 /* The path q4lin_run would take for these arguments (no launch, no device access);
  * *path_out receives a q4lin_path_t other than AUTO.  Same validation and status codes
  * as q4lin_run.  For M == 0 or N == 0, *path_out is Q4LIN_PATH_AUTO (nothing runs). */
