@@ -1,131 +1,574 @@
-// kv4_attention.cu -- attention over the paged cache of 4-bit codes.
+// kv4_attention.cu -- attention of a few query rows per key/value head over the paged 4-bit
+// cache: single tokens, draft tokens, short chunks.
 //
-// One CTA for a query row (token and head): its threads take keys in turn for the scores, then
-// channels for the outputs, 256 keys at a time, with the running maximum and sum of a softmax.
-#include <algorithm>
-
-#include "q4lin_internal.h"
-#include "serving.cuh"
+// The keys of all sequences and heads are one list of 64-key tiles, cut evenly over the GPU's warps
+// (attention_split.cuh); a warp works alone, with its own ring of copies.
+//
+// Bound: the codes and scales, head_dim + 8 bytes per key and key/value head.  At half the bytes
+// of an 8-bit cache the instructions that widen codes and feed the products come as close to the
+// limit as the memory does.
+//
+// Products on the tensor cores (m16n8k16, fp16 operands, fp32 sums) as over the 8-bit cache: a query
+// row and a row of weights take two of the MMA's 16 rows each, the rounded value and what the
+// rounding left (22 bits), and codes - 8 are exact.  A token's scales multiply its score and its
+// weight in fp32.  Both kinds lie in memory as rows of a token's codes, so a page is copied as it
+// is, by tensor copies that swizzle 16-byte chunks: a lane reads its keys' chunks, and the values
+// come by ldmatrix.trans, which pairs the same four channels of neighbouring keys, without bank
+// conflicts.  A masked nibble is widened by one addition: 0x6400 | c is 1024 + c in fp16, 0x6400 |
+// 16 c is 1024 + 16 c.  Channels are permuted alike in queries and keys so that the nibbles of a word
+// that are eight bits apart are neighbours along the summed axis.
+#include "attention_split.cuh"
 
 namespace q4lin {
 namespace {
-using namespace serving;
 
-constexpr int kThreads = 256;
+__host__ __device__ constexpr int warps_of(int D, int RT) {
+    return D == 256 ? 8 : D == 64 ? (RT == 1 ? 16 : 8) : (RT == 1 ? 12 : 8);
+}
 
-struct Args {
-    q4lin_kv4_cache_t cache;
-    q4lin_attention_t a;
-    int page_shift;
-    int* status;
+struct KvMaps {
+    CUtensorMap k, v;  // [page and head][token][bytes of a token]
 };
 
-__global__ void __launch_bounds__(kThreads) kv4_attention_kernel(const Args g) {
-    __shared__ float q[256], p[kThreads], part[8], o_part[kThreads];
-    __shared__ int64_t place[kThreads];
+template <int D, int RT>
+struct Mine {  // of one warp
+    uint4 q[RT][D / 16][32];  // A fragments
+    RowInfo row[RT * kRows];
+};
+template <int D, int RT>
+struct Layout {
+    static constexpr int W = warps_of(D, RT);
+    static constexpr uint32_t codes = kTile * D / 2, scales = kTile * 4;  // of half a tile: keys or values
+    static constexpr int room = 226 * 1024 - 2048 - 1024 - W * (int)(sizeof(Mine<D, RT>) + 64);
+    // Half tiles in a warp's ring, as many as fit.
+    static constexpr int slots = room / (int)(W * (codes + scales)) < 8 ? room / (int)(W * (codes + scales)) : 8;
+    static_assert(slots >= 2, "a tile's keys and values fit");
+};
+template <int D, int RT>
+struct Shared {
+    using L = Layout<D, RT>;
+    float scales[L::W][L::slots][kTile];
+    Mine<D, RT> mine[L::W];
+    uint64_t full[L::W][L::slots];
+    int prefix[kMaxBatch + 1];
+    uint32_t sums[L::W];
+    int failed;
+};
+
+// Nibbles n and n + 4 (b0: n = 0, b1: 1, b2: 2, b3: 3) of a word, as exact fp16 pairs of code - 8.
+__device__ __forceinline__ void nibbles_f16(uint32_t w, uint32_t& b0, uint32_t& b1, uint32_t& b2, uint32_t& b3) {
+    const uint32_t v = w >> 8;
+    auto low = [](uint32_t x) {
+        uint32_t y;
+        asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(y) : "r"(x));
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6408)));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    auto high = [](uint32_t x) {
+        uint32_t y;
+        asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(y) : "r"(x));
+        // (1024 + 16 c) / 16 - 72
+        const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x2c00)),
+                                  __half2half2(__ushort_as_half(0xd480)));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    b0 = low(w), b1 = high(w), b2 = low(v), b3 = high(v);
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void ld_words(uint32_t addr, uint32_t (&w)[N]) {
+    if constexpr (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    else
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+}
+__device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+// Byte of 16-byte chunk `chunk` of token `row` of a tile, as the tensor copies lay it down: rows of
+// D / 2 bytes, chunks swizzled within spans of as many.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
+    constexpr int kChunks = D / 32, kShiftRow = D == 64 ? 2 : D == 128 ? 1 : 0;
+    return (uint32_t)(row * (D / 2) + ((chunk ^ ((row >> kShiftRow) & (kChunks - 1))) << 4));
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
+    kv4_attention_kernel(const __grid_constant__ KvMaps maps, const SplitArgs g) {
+    using L = Layout<D, RT>;
+    constexpr int W = L::W, T = 32 * W, R = RT * kRows, kSlots = L::slots;
+    constexpr int kLaneWords = D / 32;                                    // of a key, a lane's
+    constexpr int kWords = D == 64 || RT == 2 ? 2 : 4;                    // taken at a time
+    constexpr int kChunks = D / 32;                                       // of a token's codes
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    Shared<D, RT>& S = *reinterpret_cast<Shared<D, RT>*>(smem_raw + (base - smem_u32(smem_raw)) + W * kSlots * L::codes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
+    const uint32_t ring = base + (uint32_t)(warp * kSlots) * L::codes;
+    const uint32_t scale_ring = smem_u32(S.scales[warp]);
+    Mine<D, RT>& mine = S.mine[warp];
     const q4lin_kv4_cache_t& C = g.cache;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = (int)C.head_dim, ps = g.page_shift;
-    const int64_t token = blockIdx.x / g.a.heads, head = blockIdx.x - token * g.a.heads;
-    const int64_t h = head / (g.a.heads / C.kv_heads);
-    if (blockIdx.x == 0)
-        for (int64_t b = tid; b < C.batch; b += kThreads) {
-            const int o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1);
-            if (o0 < 0 || o1 < o0 || o1 > g.a.tokens) atomicCAS(g.status, 0, kStatusIndex);
-        }
-    const int64_t b = find_sequence(C.batch, token, [&](int64_t i) { return (int64_t)__ldg(g.a.offsets + i); });
-    const int64_t o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1);
-    int64_t len = __ldg(g.a.lengths + b);
-    if (token < o0 || token >= o1) return;
-    if (o0 < 0 || o1 > g.a.tokens || o1 - o0 > g.a.max_query || len > C.pages_per_sequence << ps ||
-        (g.a.rope.cos && len > g.a.rope.positions)) {
-        if (tid == 0) atomicCAS(g.status, 0, kStatusIndex);
-        return;
+    const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads), ps = g.page_shift;
+    const int ppt = kTile >> ps;  // pages per tile
+    griddep_launch_dependents();  // (the joining kernel waits for this one's end)
+
+    if (tid == 0) {
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+        S.prefix[0] = 0;
+        S.failed = 0;
+        for (int w = 0; w < W; ++w)
+            for (int s = 0; s < kSlots; ++s) mbar_init(smem_u32(&S.full[w][s]), 1);
+        mbar_init_fence();
     }
-    if (len < 0) len = 0;
-    const int64_t position = len - (o1 - o0) + (token - o0);
-    if (tid < D / 8) {
-        bool turned;
-        int lo, hi;
-        float x[8];
-        rope_channels(g.a.rope, tid, &turned, &lo, &hi);
-        const int64_t at = token * g.a.q_token_stride + head * g.a.q_head_stride;
-        load_four(g.a.query, g.a.dtype, at + lo, false, x);
-        load_four(g.a.query, g.a.dtype, at + hi, false, x + 4);
-        if (turned && position >= 0) rope_unit(g.a.rope, position, tid, x);
-        for (int e = 0; e < 8; ++e) q[e < 4 ? lo + e : hi + e - 4] = x[e];
+    const int batch = (int)C.batch;
+    const uint32_t sum = scan_tiles<RT, W>(g, S.prefix, S.sums);
+    // A list that would be too long is empty, and a share of all numbers tells the joining kernel
+    // that no head was cut.
+    const bool too_many = sum == kTooMany;
+    const int total = too_many ? 0 : (int)sum;
+    const int share = max(1, (total + g.workers - 1) / g.workers);
+    if (blockIdx.x == 0) {
+        for (int b = tid; b < batch; b += T) g.list[1 + b] = too_many ? 0 : S.prefix[b];
+        if (tid == 0) g.list[0] = too_many ? INT_MAX : share;
     }
-    __syncthreads();
-    int64_t end = g.a.causal ? position + 1 : len, low = g.a.window > 0 ? position - g.a.window + 1 : 0;
-    end = max((int64_t)0, min(end, len)), low = max((int64_t)0, low);
-    // A power of two keeps the sums of products in fp32's range.
-    float most = 0.f;
-    for (int i = 0; i < D; ++i) most = fmaxf(most, fabsf(q[i]));
-    const int ex = min(max((int)(__float_as_uint(most) >> 23), 30), 254) - 127;
-    // (With an infinity all scores become NaN: one of -infinity would look masked.)
-    const float up = most == INFINITY ? NAN : __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-    const float factor = g.a.scale * kLog2e * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    const int groups = kThreads / D, d = tid % D;  // groups of keys for the outputs
-    for (int64_t k0 = low; k0 < end; k0 += kThreads) {
-        const int64_t key = k0 + tid;
-        float s = -INFINITY;
-        place[tid] = -1;
-        if (key < end) {
-            int64_t page = __ldg(C.page_table + b * C.table_stride + (key >> ps));
-            if (page < 0 || page >= C.num_pages) {
+    // Neighbouring shares to different SMs: a short list is spread over all of them.
+    const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
+    const int64_t begin = (int64_t)worker * share;
+    const int end = (int)min((int64_t)total, begin + share);
+    if (begin >= end) return;
+
+    // The piece's tiles `first`, first + 1, ...; with the pages of the next 32 / ppt of them in
+    // the lanes: lane i holds page i % ppt of tile i / ppt.
+    const uint32_t page_bytes = (uint32_t)(D / 2) << ps, page_scales = 4u << ps;
+    const int batch_tiles = 32 / ppt;
+    const int32_t* table = nullptr;
+    int first = 0, cnt = 0, page_low = 0, pages = 0, head = 0, ids = 0, issued = 0, slot_in = 0, in_flight = 0;
+    // (-1 is no page and none of the cache's: it is told apart from one in the table by its place.)
+    auto load_ids = [&](int i) {
+        const int p = (first + i) * ppt + lane;
+        ids = i + lane / ppt < cnt && p >= page_low && p < pages ? __ldg(table + p) : -1;
+    };
+    auto check_ids = [&](int i) {
+        if ((uint32_t)ids >= (uint32_t)C.num_pages) {
+            const int p = (first + i) * ppt + lane;
+            if (i + lane / ppt < cnt && p >= page_low && p < pages) {
                 atomicCAS(g.status, 0, kStatusIndex);
-                page = 0;
+                ids = 0;  // read something of the cache rather than nothing
             }
-            const int64_t row = ((page * C.kv_heads + h) << ps) + (key & ((1 << ps) - 1));
-            place[tid] = row;
-            const uint8_t* codes = C.k_codes + row * (D / 2);
-            float dot = 0.f;
-            for (int c = 0; c < D / 2; ++c) {
-                const int w = __ldg(codes + c);
-                dot = fmaf(q[2 * c] * up, (float)((w & 15) - 8), dot);
-                dot = fmaf(q[2 * c + 1] * up, (float)((w >> 4) - 8), dot);
+        }
+    };
+    // Next half tile of the piece (keys of a tile, then its values) into the ring: the first lanes
+    // copy a page's codes each, the next ones its scales.
+    auto issue = [&]() {
+        if (issued >= 2 * cnt) return;
+        const int i = issued >> 1;
+        if ((issued & 1) == 0 && i > 0 && i % batch_tiles == 0) load_ids(i), check_ids(i);
+        const int at = lane % ppt, id = __shfl_sync(0xffffffffu, ids, (i % batch_tiles) * ppt + at);
+        const int count = __popc(__ballot_sync(0xffffffffu, lane < ppt && id >= 0));
+        const uint32_t bar = smem_u32(&S.full[warp][slot_in]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * (page_bytes + page_scales) + g.missing);
+        __syncwarp();
+        if (lane < 2 * ppt && id >= 0) {
+            const int page = id * Hkv + head;
+            if (lane < ppt)
+                tma_load_3d(ring + (uint32_t)slot_in * L::codes + at * page_bytes, issued & 1 ? &maps.v : &maps.k, 0, 0,
+                            page, bar);
+            else
+                bulk_load(scale_ring + (uint32_t)slot_in * L::scales + at * page_scales,
+                          (issued & 1 ? C.v_scales : C.k_scales) + ((int64_t)page << ps), page_scales, bar);
+        }
+        ++issued, ++in_flight;
+        slot_in = slot_in + 1 == kSlots ? 0 : slot_in + 1;
+    };
+    uint32_t phase = 0;  // parity bit of each slot's next wait
+    int slot_out = 0;
+    bool ok = true;
+    auto await = [&]() {  // the oldest half tile in flight; its slot
+        const uint32_t bar = smem_u32(&S.full[warp][slot_out]);
+        ok = __all_sync(0xffffffffu, wait_bounded(bar, (phase >> slot_out) & 1u, g.wait_ns, &S.failed));
+        const uint32_t at = (uint32_t)slot_out;
+        if (ok) {
+            phase ^= 1u << slot_out, --in_flight;
+            slot_out = slot_out + 1 == kSlots ? 0 : slot_out + 1;
+        }
+        return at;
+    };
+
+    int pos = (int)begin;
+    Piece P = piece_of<RT>(g, S.prefix, pos, end);
+    while (true) {
+        // ---- queries: rotated, scaled to fp16's upper range by a power of two, split into two
+        // terms.  A lane holds 8 channels of a row, kPer rows at a time.  Their loads and the
+        // pages' go first: behind the rings of all SMs they would wait for microseconds.
+        cnt = P.len > 0 ? P.n : 0;
+        first = P.tile0 + P.k0;
+        table = C.page_table + P.b * C.table_stride;
+        pages = (P.len + (1 << ps) - 1) >> ps;
+        // Pages before the window of the piece's first token are not read.
+        page_low = 0;
+        if (g.a.window > 0)
+            page_low = (int)(max((int64_t)P.len - P.tq + P.row0 / group - g.a.window + 1, (int64_t)0) >> ps);
+        head = P.h;
+        issued = 0;
+        load_ids(0);
+        int limit_min = INT_MAX, low_max = 0;
+        {
+            constexpr int kUnits = D / 8, kPer = 32 / kUnits, kPasses = R / kPer;
+            const int unit = lane % kUnits;
+            const int64_t o0 = __ldg(g.a.offsets + P.b);
+            bool turned;
+            int cl, ch;
+            rope_channels(g.a.rope, unit, &turned, &cl, &ch);
+            constexpr int kTogether = kPasses < 2 ? kPasses : 2;  // passes whose loads overlap
+            const int valid = min(R, P.tq * group - P.row0);  // rows (the others stay unread)
+            if (lane >= valid && lane < R) mine.row[lane] = {0.f, -1, 0, -1};
+            const uint32_t token0 = (uint32_t)P.row0 / (uint32_t)group, rest0 = P.row0 - token0 * group;
+#pragma unroll 1
+            for (int p0 = 0; p0 * kPer < valid; p0 += kTogether) {
+                float x[kTogether][8], c[kTogether][4], s[kTogether][4];
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) {
+                    const uint32_t r = (p0 + k) * kPer + lane / kUnits, step = (rest0 + r) / (uint32_t)group;
+                    const int token = token0 + step, position = P.len - P.tq + token;
+                    if (r < valid) {
+                        const int64_t e = (o0 + token) * g.a.q_token_stride +
+                                          (P.h * group + (int)(rest0 + r - step * group)) * g.a.q_head_stride;
+                        load_four(g.a.query, g.a.dtype, e + cl, g.q_vec, x[k]);
+                        load_four(g.a.query, g.a.dtype, e + ch, g.q_vec, x[k] + 4);
+                        if (turned && position >= 0) rope_load(g.a.rope, position, unit, c[k], s[k]);
+                    }
+                }
+                if (p0 == 0) {
+                    check_ids(0);
+#pragma unroll 1
+                    for (int i = 0; i < kSlots; ++i) issue();
+                }
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) {
+                    if ((p0 + k) * kPer >= valid) break;
+                    const uint32_t r = (p0 + k) * kPer + lane / kUnits, step = (rest0 + r) / (uint32_t)group;
+                    const int token = token0 + step, position = P.len - P.tq + token;
+                    const bool in = r < valid;
+                    if (in && turned && position >= 0) rope_apply(g.a.rope, c[k], s[k], x[k]);
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[k][e]));
+#pragma unroll
+                    for (int o = kUnits / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    // 2^up brings the row's largest |x| to [2^14, 2^15), with its exponent kept within
+                    // what both 2^up and 2^-up can hold; the scale's sign goes with it, so that
+                    // larger scores stay larger after the factor.
+                    const int ex = min(max((int)(__float_as_uint(m) >> 23), 30), 254) - 127;
+                    const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), g.a.scale);
+                    const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+                    if (!in) continue;
+                    // Channel n of a word of eight is in the lower half of its pair for n < 4, in the
+                    // upper one for n >= 4; pair n % 4 of a word is half n % 2 of MMA n % 4 / 2.
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int d = (e < 4 ? cl : ch) + e % 4, word = d / 8;
+                        const float v = x[k][e] * up;
+                        const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+                        __half* f = reinterpret_cast<__half*>(
+                            &mine.q[r / kRows][2 * (word % kLaneWords) + e % 4 / 2][(r % kRows) * 4 + word / kLaneWords]);
+                        f[e % 2 * 4 + (d >> 2 & 1)] = hi, f[e % 2 * 4 + 2 + (d >> 2 & 1)] = lo;
+                    }
+                    RowInfo i;
+                    // At least this, so that a masked score of -infinity stays one.
+                    i.factor = fmaxf(fabsf(g.a.scale) * kLog2e * down, 1e-37f);
+                    i.limit = g.a.causal ? position : P.len - 1;
+                    const int64_t low = g.a.window > 0 ? (int64_t)position - g.a.window + 1 : 0;
+                    i.low = low > 0 ? (int)low : 0;
+                    i.index = (int)((o0 + token) * g.a.heads + P.h * group + (rest0 + r - step * group));
+                    if (unit == 0) mine.row[r] = i;
+                    limit_min = min(limit_min, i.limit), low_max = max(low_max, i.low);
+                }
             }
-            s = dot * __ldg(C.k_scales + row) * factor;
+            limit_min = __reduce_min_sync(0xffffffffu, limit_min);
+            low_max = __reduce_max_sync(0xffffffffu, low_max);
+            __syncwarp();
         }
-        float mx = s;
-        for (int i = 16; i; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-        if (lane == 0) part[warp] = mx;
-        __syncthreads();
-        mx = m;
-        for (int i = 0; i < kThreads / 32; ++i) mx = fmaxf(mx, part[i]);
-        const float base = mx == -INFINITY ? 0.f : mx, alpha = exp2f(m - base);
-        m = mx;
-        p[tid] = key < end ? exp2f(s - base) : 0.f;
-        __syncthreads();
-        l *= alpha, o *= alpha;
-        const int n = (int)min((int64_t)kThreads, end - k0);
-        for (int i = 0; i < n; ++i) l += p[i];
-        for (int i = tid / D; i < n; i += groups) {
-            const int w = __ldg(C.v_codes + place[i] * (D / 2) + d / 2);
-            o = fmaf(p[i] * __ldg(C.v_scales + place[i]), (float)((d & 1 ? w >> 4 : w & 15) - 8), o);
+
+        // O: of channel 32 c + 8 t + 4 e + n in [4 c + n][e].
+        float O[RT][4 * kChunks][2], m_run[RT], l_run[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            m_run[rt] = -INFINITY, l_run[rt] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4 * kChunks; ++i) O[rt][i][0] = O[rt][i][1] = 0.f;
         }
-        __syncthreads();
+        const RowInfo* rows = mine.row;
+        for (int i = 0; i < cnt; ++i) {
+            const int tile_key = (first + i) * kTile;
+            // Slots that were not copied, and those behind the sequence, may hold anything.
+            const bool whole = tile_key + kTile <= P.len && tile_key >= page_low << ps;
+            auto held = [&](int key) { return key < P.len && key >= page_low << ps; };
+            // ---- scores: 8 column tiles of 8 keys; this lane's are 8 j + 2 t + e
+            const uint32_t k_slot = await();
+            if (!ok) break;
+            float sc[RT][8][4];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[rt][j][e] = 0.f;
+            const uint32_t k_at = ring + k_slot * L::codes;
+#pragma unroll
+            for (int c = 0; c < kLaneWords / kWords; ++c) {
+                uint4 qf[RT][2 * kWords];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int k = 0; k < 2 * kWords; ++k) qf[rt][k] = mine.q[rt][2 * kWords * c + k][lane];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int byte = t * kLaneWords * 4 + c * kWords * 4;  // of key 8 j + gq
+                    uint32_t w[kWords];
+                    ld_words(k_at + chunk_at<D>(8 * j + gq, byte >> 4) + (byte & 15), w);
+#pragma unroll
+                    for (int k = 0; k < kWords; ++k) {
+                        uint32_t b0, b1, b2, b3;
+                        nibbles_f16(w[k], b0, b1, b2, b3);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            mma_f16(sc[rt][j], qf[rt][2 * k], b0, b1);
+                            mma_f16(sc[rt][j], qf[rt][2 * k + 1], b2, b3);
+                        }
+                    }
+                }
+            }
+            float2 sk[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sk[j] = ld_shared_f2(scale_ring + k_slot * L::scales + (8 * j + 2 * t) * 4);
+                if (!whole) {
+                    const int key = tile_key + 8 * j + 2 * t;
+                    sk[j].x = held(key) ? sk[j].x : 0.f, sk[j].y = held(key + 1) ? sk[j].y : 0.f;
+                }
+            }
+            __syncwarp();
+            issue();  // the slot of the keys is free
+
+            // ---- softmax: running maximum and sum; weights times the values' scales over a power of
+            // two near the tile's largest, as two fp16 terms
+            const uint32_t v_slot = await();
+            if (!ok) break;
+            float2 sv[8];
+            float sv_max = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sv[j] = ld_shared_f2(scale_ring + v_slot * L::scales + (8 * j + 2 * t) * 4);
+                if (!whole) {
+                    const int key = tile_key + 8 * j + 2 * t;
+                    sv[j].x = held(key) ? sv[j].x : 0.f, sv[j].y = held(key + 1) ? sv[j].y : 0.f;
+                }
+                sv_max = fmaxf(sv_max, fmaxf(sv[j].x, sv[j].y));
+            }
+            sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, 1));
+            sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, 2));
+            const uint32_t sv_ex = min(max(__float_as_uint(sv_max) >> 23, 1u), 253u);
+            const float sv_unit = __uint_as_float(sv_ex << 23), sv_inv = __uint_as_float((254u - sv_ex) << 23);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sv[j] = fmul2(sv[j], make_float2(sv_inv, sv_inv));
+            const bool inside = tile_key >= low_max && tile_key + kTile - 1 <= limit_min;
+            uint4 pf[RT][4];
+            float alpha[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const RowInfo& row = rows[rt * kRows + gq];
+                float2 p[8];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    p[j] = fmul2(fadd2(make_float2(sc[rt][j][0], sc[rt][j][1]), make_float2(sc[rt][j][2], sc[rt][j][3])),
+                                 sk[j]);
+                if (!inside) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int key = tile_key + 8 * j + 2 * t;
+                        if (key < row.low || key > row.limit) p[j].x = -INFINITY;
+                        if (key + 1 < row.low || key + 1 > row.limit) p[j].y = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(p[j].x, p[j].y));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                mx = fmaxf(mx * row.factor, m_run[rt]);
+                const float from = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing yet
+                alpha[rt] = ex2(m_run[rt] - from);
+                m_run[rt] = mx;
+                const float2 f2 = make_float2(row.factor, row.factor), off = make_float2(kShift - from, kShift - from);
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    p[j] = ffma2(p[j], f2, off);
+                    p[j].x = ex2(p[j].x), p[j].y = ex2(p[j].y);
+                    sum = fadd2(sum, p[j]);
+                    p[j] = fmul2(p[j], sv[j]);
+                }
+                l_run[rt] = fmaf(l_run[rt], alpha[rt], sum.x + sum.y);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    split_f16(p[2 * k].x, p[2 * k].y, &pf[rt][k].x, &pf[rt][k].y);
+                    split_f16(p[2 * k + 1].x, p[2 * k + 1].y, &pf[rt][k].z, &pf[rt][k].w);
+                }
+            }
+
+            // ---- outputs: 32 channels at a time, the tile's 64 keys in 4 steps
+            const uint32_t v_at = ring + v_slot * L::codes;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                float acc[RT][4][4];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[rt][n][e] = 0.f;
+#pragma unroll
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    uint32_t w[4];  // of keys 32 k2 + 8 i + 2 t, + 1: channels 4 gq .. 4 gq + 3 of the chunk
+                    ldmatrix_trans(v_at + chunk_at<D>(32 * k2 + lane, c), w);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t b0[4], b1[4];
+                        nibbles_f16(w[2 * k], b0[0], b0[1], b0[2], b0[3]);
+                        nibbles_f16(w[2 * k + 1], b1[0], b1[1], b1[2], b1[3]);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) mma_f16(acc[rt][n], pf[rt][2 * k2 + k], b0[n], b1[n]);
+                    }
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            O[rt][4 * c + n][e] =
+                                fmaf(acc[rt][n][e] + acc[rt][n][2 + e], sv_unit, O[rt][4 * c + n][e] * alpha[rt]);
+            }
+            __syncwarp();
+            issue();
+        }
+        if (!ok) {
+            // A wait ran out: copies still in flight must land before the CTA leaves, and the
+            // warp ends here (outputs are undefined).
+            if (lane == 0) record_failure(g.status, &S.failed);
+            const int64_t limit = g.missing ? g.wait_ns : kDrainNs;
+            for (; in_flight > 0; --in_flight) {
+                wait_bounded(smem_u32(&S.full[warp][slot_out]), (phase >> slot_out) & 1u, limit, nullptr);
+                phase ^= 1u << slot_out;
+                slot_out = slot_out + 1 == kSlots ? 0 : slot_out + 1;
+            }
+            return;
+        }
+
+        // ---- results: this lane has 8 channels of each chunk of rows rt 8 + gq
+        const bool complete = P.n == P.tiles;
+        float* part = part_at<D, RT>(g, worker, P.k0 == 0);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float l = l_run[rt];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int r = rt * kRows + gq;
+            const int64_t index = rows[r].index;
+            if (index < 0) continue;
+            const float f = !complete ? 1.f : l != 0.f ? 1.f / l : 0.f;  // l == 0: the row sees no key
+            const bool wide = !complete || g.a.dtype == Q4LIN_DTYPE_F32;
+            float* to = complete ? static_cast<float*>(g.a.out) + index * D : part + r * D;
+            unsigned short* to16 = static_cast<unsigned short*>(g.a.out) + index * D;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = O[rt][4 * c + e % 4][e / 4] * f;
+                if (wide) {
+                    *reinterpret_cast<float4*>(to + 32 * c + 8 * t) = make_float4(x[0], x[1], x[2], x[3]);
+                    *reinterpret_cast<float4*>(to + 32 * c + 8 * t + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                } else {
+                    *reinterpret_cast<uint4*>(to16 + 32 * c + 8 * t) =
+                        make_uint4(to_16x2(x[0], x[1], g.a.dtype), to_16x2(x[2], x[3], g.a.dtype),
+                                   to_16x2(x[4], x[5], g.a.dtype), to_16x2(x[6], x[7], g.a.dtype));
+                }
+            }
+            if (t != 0) continue;
+            if (!complete)
+                part[R * D + r] = m_run[rt], part[R * D + R + r] = l;
+            else if (g.a.lse)
+                g.a.lse[index] = l != 0.f ? ((m_run[rt] == -INFINITY ? 0.f : m_run[rt]) + lg2(l * kUnshift)) * kLn2
+                                          : -INFINITY;
+        }
+        pos += P.n;
+        if (pos >= end) return;
+        P = piece_of<RT>(g, S.prefix, pos, end);
+        __syncwarp();  // every lane has read the queries and rows of this piece
     }
-    o_part[tid] = o;
-    __syncthreads();
-    if (tid >= D) return;
-    for (int i = 1; i < groups; ++i) o += o_part[i * D + tid];
-    const int64_t row = token * g.a.heads + head;
-    store_one(g.a.out, g.a.dtype, row * D + tid, l > 0.f ? o / l : l == 0.f ? 0.f : NAN);
-    if (tid == 0 && g.a.lse)
-        g.a.lse[row] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// A map of the codes: boxes of one page of one head, 16-byte chunks of a token's codes swizzled.
+bool map_codes(CUtensorMap* map, const q4lin_kv4_cache_t& C, const uint8_t* codes) {
+    EncodeTiledFn encode = tensor_map_encoder();
+    if (!encode) return false;
+    const cuuint64_t row = (cuuint64_t)C.head_dim / 2;
+    const cuuint64_t dims[3] = {row, (cuuint64_t)C.page_size, (cuuint64_t)(C.num_pages * C.kv_heads)};
+    const cuuint64_t strides[2] = {row, row * (cuuint64_t)C.page_size};
+    const cuuint32_t box[3] = {(cuuint32_t)row, (cuuint32_t)C.page_size, 1}, steps[3] = {1, 1, 1};
+    const CUtensorMapSwizzle swizzle = row == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                       : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                   : CU_TENSOR_MAP_SWIZZLE_128B;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int RT>
+cudaError_t launch(SplitArgs& g, const SplitSize& size, const KvMaps& maps, const LaunchCtx& c) {
+    using L = Layout<D, RT>;
+    constexpr int R = RT * kRows;
+    constexpr int bytes = L::W * L::slots * (int)L::codes + (int)sizeof(Shared<D, RT>) + 1024;
+    static_assert(bytes <= 227 * 1024, "shared memory of one SM");
+    cudaError_t e = kernel_smem_once<kv4_attention_kernel<D, RT>>(bytes);
+    if (e != cudaSuccess) return e;
+    // One CTA per SM, and no more than the longest possible list has tiles for.
+    const int64_t grid = std::min<int64_t>(c.sm_count, size.segments * size.tiles);
+    g.workers = (int)grid * L::W;
+    g.list = reinterpret_cast<int*>(c.ws);
+    g.parts = c.ws + kMaxBatch + 4;  // 16-byte aligned
+    if ((int64_t)g.workers * 2 * R * (D + 2) + kMaxBatch + 4 > c.ws_floats) return cudaErrorInvalidValue;
+    kv4_attention_kernel<D, RT><<<(unsigned)grid, 32 * L::W, bytes, c.stream>>>(maps, g);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return join_launch<D, RT>(g, size, c);
 }
 
 }  // namespace
 
-cudaError_t kv4_attention_launch(const q4lin_kv4_cache_t& cache, const q4lin_attention_t& a, const LaunchCtx& c) {
-    Args g;
-    g.cache = cache;
-    g.a = a;
-    g.page_shift = cache.page_size == 16 ? 4 : cache.page_size == 32 ? 5 : 6;
-    g.status = c.status_word;
-    kv4_attention_kernel<<<(unsigned)(a.tokens * a.heads), kThreads, 0, c.stream>>>(g);
-    return cudaGetLastError();
+cudaError_t kv4_attention_split_launch(const q4lin_kv4_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max,
+                                       const LaunchCtx& c) {
+    KvMaps maps;
+    if (!map_codes(&maps.k, cache, cache.k_codes) || !map_codes(&maps.v, cache, cache.v_codes))
+        return cudaErrorInvalidValue;
+    return in_groups(cache, a, rows_max, c, [&](SplitArgs& g, const SplitSize& size) {
+        switch (cache.head_dim) {
+            case 64: return size.two ? launch<64, 2>(g, size, maps, c) : launch<64, 1>(g, size, maps, c);
+            case 128: return size.two ? launch<128, 2>(g, size, maps, c) : launch<128, 1>(g, size, maps, c);
+            default: return launch<256, 1>(g, size, maps, c);
+        }
+    });
 }
 
 }  // namespace q4lin
