@@ -31,6 +31,7 @@ namespace {
 using namespace ptx;
 using namespace serving;
 
+constexpr int kRows = 8;   // query rows per MMA tile (two of its 16 rows each)
 constexpr int kSlots = 3;  // half tiles (keys or values) in a warp's ring
 
 // Warps of the one CTA on an SM: what registers, rings and queries leave room for.
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
         mbar_init_fence();
     }
     const int batch = (int)C.batch;
-    const uint32_t sum = scan_tiles<RT, W>(g, S.prefix, S.sums);
+    const uint32_t sum = scan_tiles<R, W>(g, S.prefix, S.sums);
     // A list that would be too long is empty, and a share of all numbers tells the joining kernel
     // that no head was cut.
     const bool too_many = sum == kTooMany;
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
     const int end = (int)min((int64_t)total, begin + share);
     if (begin >= end) return;
 
-    auto piece_at = [&](int pos) { return piece_of<RT>(g, S.prefix, pos, end); };
+    auto piece_at = [&](int pos) { return piece_of<R>(g, S.prefix, pos, end); };
 
     // The piece's tiles `first`, first + 1, ...; with the pages of the next 32 / ppt of them in
     // the lanes: lane i holds page i % ppt of tile i / ppt.
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1) attention_split_kerne
 
         // ---- results: lane (gq, t) holds channels 8 nt + 2 t, + 1 of rows rt 8 + gq
         const bool whole = P.n == P.tiles;
-        float* part = part_at<D, RT>(g, worker, P.k0 == 0);
+        float* part = part_at<D, R>(g, worker, P.k0 == 0);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float l = l_run[rt];
@@ -456,24 +457,21 @@ cudaError_t launch(SplitArgs& g, const SplitSize& size, const LaunchCtx& c) {
     attention_split_kernel<D, RT><<<(unsigned)grid, 32 * W, bytes, c.stream>>>(g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return join_launch<D, RT>(g, size, c);
+    return join_launch<D, R>(g, size, c);
 }
 
 }  // namespace
 
 bool attention_split_countable(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max) {
-    const SplitSize s = split_size(cache, a, rows_max, std::min<int64_t>(kMaxBatch, cache.batch));
-    int64_t units;
-    // (The kernel rounds the list up to its warps, of which there are fewer than 2^16.)
-    return !__builtin_mul_overflow(s.segments, s.tiles, &units) && units <= 0x7FFFFFFF - 0xFFFF;
+    return split_countable(cache, a, rows_max, kRows);
 }
 
 cudaError_t attention_split_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
                                    int64_t rows_max, const LaunchCtx& c) {
-    return in_groups(cache, a, rows_max, c, [&](SplitArgs& g, const SplitSize& size) {
+    return in_groups(cache, a, rows_max, kRows, c, [&](SplitArgs& g, const SplitSize& size) {
         switch (cache.head_dim) {
-            case 64: return size.two ? launch<64, 2>(g, size, c) : launch<64, 1>(g, size, c);
-            case 128: return size.two ? launch<128, 2>(g, size, c) : launch<128, 1>(g, size, c);
+            case 64: return size.rows > kRows ? launch<64, 2>(g, size, c) : launch<64, 1>(g, size, c);
+            case 128: return size.rows > kRows ? launch<128, 2>(g, size, c) : launch<128, 1>(g, size, c);
             default: return launch<256, 1>(g, size, c);
         }
     });

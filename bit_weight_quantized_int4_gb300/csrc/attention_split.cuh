@@ -15,7 +15,6 @@ using namespace ptx;
 using namespace serving;
 
 constexpr int kTile = 64;        // keys per tile
-constexpr int kRows = 8;         // query rows per MMA tile (two of its 16 rows each)
 constexpr int kMaxBatch = 256;   // sequences per launch
 constexpr float kShift = 14.f;   // probabilities are kept as 2^14 p: fp16's range downwards
 // Undone before a logarithm, whose error grows with its distance from 0.
@@ -50,7 +49,7 @@ struct Sequence {
 
 // What one sequence asks of this kernel; nothing where its indices are bad or its rows are
 // too many for it.  tq is -1 where its offsets decrease.
-template <int RT>
+template <int R>
 __device__ __forceinline__ Sequence sequence_of(const SplitArgs& g, int64_t b, bool* bad) {
     Sequence s;
     const int64_t o0 = __ldg(g.a.offsets + b), o1 = __ldg(g.a.offsets + b + 1);
@@ -68,14 +67,14 @@ __device__ __forceinline__ Sequence sequence_of(const SplitArgs& g, int64_t b, b
     const int64_t first = g.a.window > 0 ? (int64_t)s.len - s.tq - g.a.window + 1 : 0;
     s.tile0 = first > 0 ? (int)(first / kTile) : 0;
     s.tiles = max((s.len + kTile - 1) / kTile - s.tile0, 1);
-    s.row_tiles = (int)((s.tq * group + RT * kRows - 1) / (RT * kRows));
+    s.row_tiles = (int)((s.tq * group + R - 1) / R);
     return s;
 }
 
 // An unfinished piece: [R][D] sums, then R maxima and R sums of weights.
-template <int D, int RT>
+template <int D, int R>
 __device__ __forceinline__ float* part_at(const SplitArgs& g, int worker, bool begins) {
-    constexpr int kPart = RT * kRows * (D + 2);
+    constexpr int kPart = R * (D + 2);
     return g.parts + ((int64_t)worker * 2 + begins) * kPart;
 }
 
@@ -83,7 +82,7 @@ __device__ __forceinline__ float* part_at(const SplitArgs& g, int worker, bool b
 // in the list, and the result its length.  prefix[0] is 0 already.  Sums stop at kTooMany: the host
 // has counted on offsets that rise, and where one decreases (which is reported) sequences may
 // overlap and have more tiles than 32 bits hold.
-template <int RT, int W>
+template <int R, int W>
 __device__ __forceinline__ uint32_t scan_tiles(const SplitArgs& g, int* prefix, uint32_t* sums) {
     constexpr int T = 32 * W;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -94,7 +93,7 @@ __device__ __forceinline__ uint32_t scan_tiles(const SplitArgs& g, int* prefix, 
         uint32_t v = 0;
         if (b < batch) {
             bool bad;
-            const Sequence s = sequence_of<RT>(g, b, &bad);
+            const Sequence s = sequence_of<R>(g, b, &bad);
             v = s.tq < 0 ? kTooMany : (uint32_t)(s.tiles * s.row_tiles * Hkv);
             if (bad && blockIdx.x == 0) atomicCAS(g.status, 0, kStatusIndex);
         }
@@ -124,9 +123,8 @@ struct Piece {
     int b, len, tq, h, row0, k0, n, tiles, tile0;
 };
 // The piece that begins at `pos` of the list and goes no further than `end`.
-template <int RT>
+template <int R>
 __device__ __forceinline__ Piece piece_of(const SplitArgs& g, const int* prefix, int pos, int end) {
-    constexpr int R = RT * kRows;
     const int batch = (int)g.cache.batch;
     int lo = 0, hi = batch;  // prefix[lo] <= pos < prefix[hi]
     while (hi - lo > 1) {
@@ -137,7 +135,7 @@ __device__ __forceinline__ Piece piece_of(const SplitArgs& g, const int* prefix,
             hi = mid;
     }
     bool bad;
-    const Sequence s = sequence_of<RT>(g, lo, &bad);
+    const Sequence s = sequence_of<R>(g, lo, &bad);
     const int local = pos - prefix[lo], seg = local / s.tiles;
     Piece p;
     p.b = lo, p.len = s.len, p.tq = s.tq, p.tiles = s.tiles, p.tile0 = s.tile0;
@@ -148,9 +146,9 @@ __device__ __forceinline__ Piece piece_of(const SplitArgs& g, const int* prefix,
 }
 
 // The rows of heads that were cut: one CTA per query row, its warps taking parts in turn.
-template <int D, int RT, int kJoinWarps, int kAhead>
+template <int D, int R, int kJoinWarps, int kAhead>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const SplitArgs g) {
-    constexpr int R = RT * kRows, kVec = D == 256 ? 2 : 1;  // 16-byte units per lane
+    constexpr int kVec = D == 256 ? 2 : 1;  // 16-byte units per lane
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
     __shared__ float4 s_o[kJoinWarps][D / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -160,7 +158,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
     // (Offsets and lengths are the caller's inputs, not the first kernel's results.)
     const int64_t b = find_sequence(g.cache.batch, token, [&](int64_t i) { return (int64_t)__ldg(g.a.offsets + i); });
     bool bad;
-    const Sequence s = sequence_of<RT>(g, b, &bad);
+    const Sequence s = sequence_of<R>(g, b, &bad);
     const int64_t o0 = __ldg(g.a.offsets + b);
     griddep_wait();
     if (token < o0 || token >= o0 + s.tq) return;
@@ -181,7 +179,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
             const int w = c + k * kJoinWarps;
             pm[k] = -INFINITY, pl[k] = 0.f;
             if (w <= c1) {
-                const float* src = part_at<D, RT>(g, w, w == c0);
+                const float* src = part_at<D, R>(g, w, w == c0);
                 pm[k] = __ldcg(src + R * D + r), pl[k] = __ldcg(src + R * D + R + r);
 #pragma unroll
                 for (int v = 0; v < kVec; ++v)
@@ -244,24 +242,36 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
 
 // What a launch may have to do.
 struct SplitSize {
-    bool two;          // row tiles of 16 rows instead of 8
+    int rows;          // query rows of a row tile
     int64_t segments;  // row tiles of all key/value heads
     int64_t tiles;     // of keys, of each
 };
-SplitSize split_size(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max, int64_t batch) {
+// Row tiles of `least` rows, or twice, four times as many up to 16 (8 with 256 channels) where a
+// sequence may have more.
+inline SplitSize split_size(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max, int64_t batch,
+                            int least) {
     const int64_t group = a.heads / cache.kv_heads, rows = std::min(rows_max, a.max_query * group);
+    const int most = cache.head_dim == 256 ? 8 : 16;
     SplitSize s;
-    s.two = rows > kRows && cache.head_dim != 256;
-    const int64_t R = s.two ? 2 * kRows : kRows;
+    s.rows = least;
+    while (s.rows < most && s.rows < rows) s.rows *= 2;
+    const int64_t R = s.rows;
     const int64_t row_tiles =
         std::min((a.tokens * group + R - 1) / R + batch, ((rows + R - 1) / R) * batch);
     s.segments = row_tiles * cache.kv_heads;
     s.tiles = (cache.pages_per_sequence * cache.page_size + kTile - 1) / kTile;
     return s;
 }
+// Whether a launch's list of tiles is short enough for 32 bits.
+inline bool split_countable(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max, int least) {
+    const SplitSize s = split_size(cache, a, rows_max, std::min<int64_t>(kMaxBatch, cache.batch), least);
+    int64_t units;
+    // (The kernel rounds the list up to its warps, of which there are fewer than 2^16.)
+    return !__builtin_mul_overflow(s.segments, s.tiles, &units) && units <= 0x7FFFFFFF - 0xFFFF;
+}
 
 // The joining kernel, behind the one that left the parts.
-template <int D, int RT>
+template <int D, int R>
 cudaError_t join_launch(const SplitArgs& g, const SplitSize& size, const LaunchCtx& c) {
     // The second kernel's launch overlaps the first's work; it waits for its end on the device.
     cudaLaunchAttribute attr = {};
@@ -278,20 +288,20 @@ cudaError_t join_launch(const SplitArgs& g, const SplitSize& size, const LaunchC
     cfg.numAttrs = 1;
     if (parts <= 4) {
         cfg.blockDim = dim3(64);
-        return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, RT, 2, 4>, g);
+        return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, R, 2, 4>, g);
     }
     if (parts <= 32) {
         cfg.blockDim = dim3(256);
-        return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, RT, 8, 4>, g);
+        return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, R, 8, 4>, g);
     }
     cfg.blockDim = dim3(512);
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, RT, 16, D == 256 ? 4 : 10>, g);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<D, R, 16, D == 256 ? 4 : 10>, g);
 }
 
 // run(arguments, size) for sequences in groups that a launch's list holds.
 template <typename Run>
-cudaError_t in_groups(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max, const LaunchCtx& c,
-                      Run run) {
+cudaError_t in_groups(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max, int least,
+                      const LaunchCtx& c, Run run) {
     cudaError_t err = cudaSuccess;
     for (int64_t b = 0; b < cache.batch && err == cudaSuccess; b += kMaxBatch) {
         SplitArgs g;
@@ -308,7 +318,7 @@ cudaError_t in_groups(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
         g.status = c.status_word;
         g.wait_ns = c.wait_limit_ns;
         g.missing = c.tc_skip_first_copy ? 16 : 0;
-        err = run(g, split_size(cache, a, rows_max, g.cache.batch));
+        err = run(g, split_size(cache, a, rows_max, g.cache.batch, least));
     }
     return err;
 }

@@ -8,47 +8,49 @@
 // of an 8-bit cache the instructions that widen codes and feed the products come as close to the
 // limit as the memory does.
 //
-// Products on the tensor cores (m16n8k16, fp16 operands, fp32 sums) as over the 8-bit cache: a query
-// row and a row of weights take two of the MMA's 16 rows each, the rounded value and what the
-// rounding left (22 bits), and codes - 8 are exact.  A token's scales multiply its score and its
-// weight in fp32.  Both kinds lie in memory as rows of a token's codes, so a page is copied as it
-// is, by tensor copies that swizzle 16-byte chunks: a lane reads its keys' chunks, and the values
-// come by ldmatrix.trans, which pairs the same four channels of neighbouring keys, without bank
-// conflicts.  A masked nibble is widened by one addition: 0x6400 | c is 1024 + c in fp16, 0x6400 |
-// 16 c is 1024 + 16 c.  Channels are permuted alike in queries and keys so that the nibbles of a word
-// that are eight bits apart are neighbours along the summed axis.
+// Products on the tensor cores (m16n8k16, fp16 operands, fp32 sums), transposed: keys (channels of
+// the values) are the MMA's 16 rows, and a query row takes two of its 8 columns, the rounded value
+// and what the rounding left (22 bits).  So four query rows, a key head's in most models, fill a
+// tile, where as the MMA's rows they would fill half of one.  Codes - 8 are exact in fp16; a token's
+// scales multiply its score and its weight in fp32.  Both kinds lie in memory as rows of a token's
+// codes, so a page is copied as it is, by tensor copies that swizzle 16-byte chunks: a lane reads
+// its keys' chunks, and the values come by ldmatrix.trans, which pairs the same four channels of
+// neighbouring keys, without bank conflicts.  A masked nibble is widened by one addition: 0x6400 | c
+// is 1024 + c in fp16, 0x6400 | 16 c is 1024 + 16 c.  Channels are permuted alike in queries and keys
+// so that the nibbles of a word that lie 16 bits apart are neighbours along the summed axis.
 #include "attention_split.cuh"
 
 namespace q4lin {
 namespace {
 
-__host__ __device__ constexpr int warps_of(int D, int RT) {
-    return D == 256 ? 8 : D == 64 ? (RT == 1 ? 16 : 8) : (RT == 1 ? 12 : 8);
+// CT tiles of 8 columns, 4 query rows each.
+__host__ __device__ constexpr int warps_of(int D, int CT) {
+    return D == 64 ? (CT == 1 ? 20 : CT == 2 ? 16 : 12) : D == 128 ? (CT == 1 ? 16 : CT == 2 ? 12 : 8) : 8;
 }
 
 struct KvMaps {
     CUtensorMap k, v;  // [page and head][token][bytes of a token]
 };
 
-template <int D, int RT>
+template <int D, int CT>
 struct Mine {  // of one warp
-    uint4 q[RT][D / 16][32];  // A fragments
-    RowInfo row[RT * kRows];
+    uint2 q[CT][D / 16][32];  // B fragments
+    RowInfo row[CT * 4];
 };
-template <int D, int RT>
+template <int D, int CT>
 struct Layout {
-    static constexpr int W = warps_of(D, RT);
+    static constexpr int W = warps_of(D, CT);
     static constexpr uint32_t codes = kTile * D / 2, scales = kTile * 4;  // of half a tile: keys or values
-    static constexpr int room = 226 * 1024 - 2048 - 1024 - W * (int)(sizeof(Mine<D, RT>) + 64);
+    static constexpr int room = 226 * 1024 - 2048 - 1024 - W * (int)(sizeof(Mine<D, CT>) + 64);
     // Half tiles in a warp's ring, as many as fit.
     static constexpr int slots = room / (int)(W * (codes + scales)) < 8 ? room / (int)(W * (codes + scales)) : 8;
     static_assert(slots >= 2, "a tile's keys and values fit");
 };
-template <int D, int RT>
+template <int D, int CT>
 struct Shared {
-    using L = Layout<D, RT>;
+    using L = Layout<D, CT>;
     float scales[L::W][L::slots][kTile];
-    Mine<D, RT> mine[L::W];
+    Mine<D, CT> mine[L::W];
     uint64_t full[L::W][L::slots];
     int prefix[kMaxBatch + 1];
     uint32_t sums[L::W];
@@ -80,6 +82,12 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) 
                  : "r"(addr)
                  : "memory");
 }
+// The 8 x 8 matrix of which lane 4 i + j holds elements 2 j and 2 j + 1 of row i, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 template <int N>
 __device__ __forceinline__ void ld_words(uint32_t addr, uint32_t (&w)[N]) {
     if constexpr (N == 2)
@@ -87,9 +95,9 @@ __device__ __forceinline__ void ld_words(uint32_t addr, uint32_t (&w)[N]) {
     else
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
 }
-__device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+__device__ __forceinline__ float ld_shared_f(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
 // Byte of 16-byte chunk `chunk` of token `row` of a tile, as the tensor copies lay it down: rows of
@@ -100,21 +108,23 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     return (uint32_t)(row * (D / 2) + ((chunk ^ ((row >> kShiftRow) & (kChunks - 1))) << 4));
 }
 
-template <int D, int RT>
-__global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
+template <int D, int CT>
+__global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
     kv4_attention_kernel(const __grid_constant__ KvMaps maps, const SplitArgs g) {
-    using L = Layout<D, RT>;
-    constexpr int W = L::W, T = 32 * W, R = RT * kRows, kSlots = L::slots;
-    constexpr int kLaneWords = D / 32;                                    // of a key, a lane's
-    constexpr int kWords = D == 64 || RT == 2 ? 2 : 4;                    // taken at a time
-    constexpr int kChunks = D / 32;                                       // of a token's codes
+    using L = Layout<D, CT>;
+    constexpr int W = L::W, T = 32 * W, R = 4 * CT, kSlots = L::slots;
+    constexpr int kLaneWords = D / 32;                  // of a key, a lane's
+    constexpr int kWords = kLaneWords < 4 ? kLaneWords : 4;  // read at a time
+    constexpr int kChunks = D / 32;                     // of a token's codes
+    constexpr int kSteps = D / 16;                      // MMAs along the channels
+    constexpr bool kHeld = CT * kSteps <= 16;           // queries stay in registers
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    Shared<D, RT>& S = *reinterpret_cast<Shared<D, RT>*>(smem_raw + (base - smem_u32(smem_raw)) + W * kSlots * L::codes);
+    Shared<D, CT>& S = *reinterpret_cast<Shared<D, CT>*>(smem_raw + (base - smem_u32(smem_raw)) + W * kSlots * L::codes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
     const uint32_t ring = base + (uint32_t)(warp * kSlots) * L::codes;
     const uint32_t scale_ring = smem_u32(S.scales[warp]);
-    Mine<D, RT>& mine = S.mine[warp];
+    Mine<D, CT>& mine = S.mine[warp];
     const q4lin_kv4_cache_t& C = g.cache;
     const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads), ps = g.page_shift;
     const int ppt = kTile >> ps;  // pages per tile
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
         mbar_init_fence();
     }
     const int batch = (int)C.batch;
-    const uint32_t sum = scan_tiles<RT, W>(g, S.prefix, S.sums);
+    const uint32_t sum = scan_tiles<R, W>(g, S.prefix, S.sums);
     // A list that would be too long is empty, and a share of all numbers tells the joining kernel
     // that no head was cut.
     const bool too_many = sum == kTooMany;
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
     };
 
     int pos = (int)begin;
-    Piece P = piece_of<RT>(g, S.prefix, pos, end);
+    Piece P = piece_of<R>(g, S.prefix, pos, end);
     while (true) {
         // ---- queries: rotated, scaled to fp16's upper range by a power of two, split into two
         // terms.  A lane holds 8 channels of a row, kPer rows at a time.  Their loads and the
@@ -272,15 +282,16 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
                     const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
                     if (!in) continue;
                     // Channel n of a word of eight is in the lower half of its pair for n < 4, in the
-                    // upper one for n >= 4; pair n % 4 of a word is half n % 2 of MMA n % 4 / 2.
+                    // upper one for n >= 4; pair n % 4 of a word is half n % 2 of step n % 4 / 2.
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int d = (e < 4 ? cl : ch) + e % 4, word = d / 8;
                         const float v = x[k][e] * up;
                         const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+                        // Columns 2 r and 2 r + 1 of row r: lanes 4 columns apart.
                         __half* f = reinterpret_cast<__half*>(
-                            &mine.q[r / kRows][2 * (word % kLaneWords) + e % 4 / 2][(r % kRows) * 4 + word / kLaneWords]);
-                        f[e % 2 * 4 + (d >> 2 & 1)] = hi, f[e % 2 * 4 + 2 + (d >> 2 & 1)] = lo;
+                            &mine.q[r / 4][2 * (word % kLaneWords) + e % 4 / 2][r % 4 * 8 + word / kLaneWords]);
+                        f[e % 2 * 2 + (d >> 2 & 1)] = hi, f[16 + e % 2 * 2 + (d >> 2 & 1)] = lo;
                     }
                     RowInfo i;
                     // At least this, so that a masked score of -infinity stays one.
@@ -298,64 +309,82 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
             __syncwarp();
         }
 
-        // O: of channel 32 c + 8 t + 4 e + n in [4 c + n][e].
-        float O[RT][4 * kChunks][2], m_run[RT], l_run[RT];
+        // Lane (gq, t) has row 4 ct + t of everything.  O: channels 32 c + 4 gq + 2 n, + 1 in [2 c + n].
+        float2 O[CT][2 * kChunks];
+        float m_run[CT], l_run[CT], factor[CT];
+        int limit[CT], low[CT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            m_run[rt] = -INFINITY, l_run[rt] = 0.f;
+        for (int ct = 0; ct < CT; ++ct) {
+            m_run[ct] = -INFINITY, l_run[ct] = 0.f;
+            const RowInfo& row = mine.row[4 * ct + t];
+            factor[ct] = row.factor, limit[ct] = row.limit, low[ct] = row.low;
 #pragma unroll
-            for (int i = 0; i < 4 * kChunks; ++i) O[rt][i][0] = O[rt][i][1] = 0.f;
+            for (int i = 0; i < 2 * kChunks; ++i) O[ct][i] = make_float2(0.f, 0.f);
         }
-        const RowInfo* rows = mine.row;
+        uint2 held_q[CT][kHeld ? kSteps : 1];
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) held_q[ct][k] = mine.q[ct][k][lane];
+        }
         for (int i = 0; i < cnt; ++i) {
             const int tile_key = (first + i) * kTile;
             // Slots that were not copied, and those behind the sequence, may hold anything.
             const bool whole = tile_key + kTile <= P.len && tile_key >= page_low << ps;
-            auto held = [&](int key) { return key < P.len && key >= page_low << ps; };
-            // ---- scores: 8 column tiles of 8 keys; this lane's are 8 j + 2 t + e
+            // Scales of this lane's keys, 16 m + gq and + 8.
+            auto scales_of = [&](uint32_t slot, float2 (&s)[4]) {
+                const uint32_t at = scale_ring + slot * L::scales + gq * 4;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    s[m] = make_float2(ld_shared_f(at + m * 64), ld_shared_f(at + m * 64 + 32));
+                    if (!whole) {
+                        const int key = tile_key + 16 * m + gq;
+                        if (key >= P.len || key < page_low << ps) s[m].x = 0.f;
+                        if (key + 8 >= P.len || key + 8 < page_low << ps) s[m].y = 0.f;
+                    }
+                }
+            };
+            // ---- scores
             const uint32_t k_slot = await();
             if (!ok) break;
-            float sc[RT][8][4];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[rt][j][e] = 0.f;
             const uint32_t k_at = ring + k_slot * L::codes;
+            float sc[CT][4][4];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[ct][m][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < kLaneWords / kWords; ++c) {
-                uint4 qf[RT][2 * kWords];
+                const int byte = t * kLaneWords * 4 + c * kWords * 4;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int k = 0; k < 2 * kWords; ++k) qf[rt][k] = mine.q[rt][2 * kWords * c + k][lane];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int byte = t * kLaneWords * 4 + c * kWords * 4;  // of key 8 j + gq
-                    uint32_t w[kWords];
-                    ld_words(k_at + chunk_at<D>(8 * j + gq, byte >> 4) + (byte & 15), w);
+                for (int m = 0; m < 4; ++m) {
+                    uint32_t w[2][kWords];
+                    ld_words(k_at + chunk_at<D>(16 * m + gq, byte >> 4) + (byte & 15), w[0]);
+                    ld_words(k_at + chunk_at<D>(16 * m + 8 + gq, byte >> 4) + (byte & 15), w[1]);
 #pragma unroll
                     for (int k = 0; k < kWords; ++k) {
-                        uint32_t b0, b1, b2, b3;
-                        nibbles_f16(w[k], b0, b1, b2, b3);
+                        uint4 a, b;
+                        nibbles_f16(w[0][k], a.x, a.z, b.x, b.z);
+                        nibbles_f16(w[1][k], a.y, a.w, b.y, b.w);
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            mma_f16(sc[rt][j], qf[rt][2 * k], b0, b1);
-                            mma_f16(sc[rt][j], qf[rt][2 * k + 1], b2, b3);
+                        for (int ct = 0; ct < CT; ++ct) {
+                            const int step = 2 * (c * kWords + k);
+                            uint2 q0, q1;
+                            if constexpr (kHeld)
+                                q0 = held_q[ct][step], q1 = held_q[ct][step + 1];
+                            else
+                                q0 = mine.q[ct][step][lane], q1 = mine.q[ct][step + 1][lane];
+                            mma_f16(sc[ct][m], a, q0.x, q0.y);
+                            mma_f16(sc[ct][m], b, q1.x, q1.y);
                         }
                     }
                 }
             }
-            float2 sk[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sk[j] = ld_shared_f2(scale_ring + k_slot * L::scales + (8 * j + 2 * t) * 4);
-                if (!whole) {
-                    const int key = tile_key + 8 * j + 2 * t;
-                    sk[j].x = held(key) ? sk[j].x : 0.f, sk[j].y = held(key + 1) ? sk[j].y : 0.f;
-                }
-            }
+            float2 sk[4];
+            scales_of(k_slot, sk);
             __syncwarp();
             issue();  // the slot of the keys is free
 
@@ -363,102 +392,97 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
             // two near the tile's largest, as two fp16 terms
             const uint32_t v_slot = await();
             if (!ok) break;
-            float2 sv[8];
+            float2 sv[4];
+            scales_of(v_slot, sv);
             float sv_max = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sv[j] = ld_shared_f2(scale_ring + v_slot * L::scales + (8 * j + 2 * t) * 4);
-                if (!whole) {
-                    const int key = tile_key + 8 * j + 2 * t;
-                    sv[j].x = held(key) ? sv[j].x : 0.f, sv[j].y = held(key + 1) ? sv[j].y : 0.f;
-                }
-                sv_max = fmaxf(sv_max, fmaxf(sv[j].x, sv[j].y));
-            }
-            sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, 1));
-            sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, 2));
+            for (int m = 0; m < 4; ++m) sv_max = fmaxf(sv_max, fmaxf(sv[m].x, sv[m].y));
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, o));
             const uint32_t sv_ex = min(max(__float_as_uint(sv_max) >> 23, 1u), 253u);
             const float sv_unit = __uint_as_float(sv_ex << 23), sv_inv = __uint_as_float((254u - sv_ex) << 23);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sv[j] = fmul2(sv[j], make_float2(sv_inv, sv_inv));
+            for (int m = 0; m < 4; ++m) sv[m] = fmul2(sv[m], make_float2(sv_inv, sv_inv));
             const bool inside = tile_key >= low_max && tile_key + kTile - 1 <= limit_min;
-            uint4 pf[RT][4];
-            float alpha[RT];
+            uint2 pf[CT][4];  // B fragments
+            float alpha[CT];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const RowInfo& row = rows[rt * kRows + gq];
-                float2 p[8];
+            for (int ct = 0; ct < CT; ++ct) {
+                float2 p[4];
                 float mx = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    p[j] = fmul2(fadd2(make_float2(sc[rt][j][0], sc[rt][j][1]), make_float2(sc[rt][j][2], sc[rt][j][3])),
-                                 sk[j]);
+                for (int m = 0; m < 4; ++m)
+                    p[m] = fmul2(fadd2(make_float2(sc[ct][m][0], sc[ct][m][2]), make_float2(sc[ct][m][1], sc[ct][m][3])),
+                                 sk[m]);
                 if (!inside) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int key = tile_key + 8 * j + 2 * t;
-                        if (key < row.low || key > row.limit) p[j].x = -INFINITY;
-                        if (key + 1 < row.low || key + 1 > row.limit) p[j].y = -INFINITY;
+                    for (int m = 0; m < 4; ++m) {
+                        const int key = tile_key + 16 * m + gq;
+                        if (key < low[ct] || key > limit[ct]) p[m].x = -INFINITY;
+                        if (key + 8 < low[ct] || key + 8 > limit[ct]) p[m].y = -INFINITY;
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(p[j].x, p[j].y));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                mx = fmaxf(mx * row.factor, m_run[rt]);
+                for (int m = 0; m < 4; ++m) mx = fmaxf(mx, fmaxf(p[m].x, p[m].y));
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                mx = fmaxf(mx * factor[ct], m_run[ct]);
                 const float from = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing yet
-                alpha[rt] = ex2(m_run[rt] - from);
-                m_run[rt] = mx;
-                const float2 f2 = make_float2(row.factor, row.factor), off = make_float2(kShift - from, kShift - from);
+                alpha[ct] = ex2(m_run[ct] - from);
+                m_run[ct] = mx;
+                const float2 f2 = make_float2(factor[ct], factor[ct]), off = make_float2(kShift - from, kShift - from);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    p[j] = ffma2(p[j], f2, off);
-                    p[j].x = ex2(p[j].x), p[j].y = ex2(p[j].y);
-                    sum = fadd2(sum, p[j]);
-                    p[j] = fmul2(p[j], sv[j]);
+                for (int m = 0; m < 4; ++m) {
+                    p[m] = ffma2(p[m], f2, off);
+                    p[m].x = ex2(p[m].x), p[m].y = ex2(p[m].y);
+                    sum = fadd2(sum, p[m]);
+                    p[m] = fmul2(p[m], sv[m]);
+                    // Rows of a transposed fragment: both terms of a key's weight.
+                    uint32_t hi, lo;
+                    split_f16(p[m].x, p[m].y, &hi, &lo);
+                    pf[ct][m].x = transposed(prmt(hi, lo, 0x5410u));
+                    pf[ct][m].y = transposed(prmt(hi, lo, 0x7632u));
                 }
-                l_run[rt] = fmaf(l_run[rt], alpha[rt], sum.x + sum.y);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    split_f16(p[2 * k].x, p[2 * k].y, &pf[rt][k].x, &pf[rt][k].y);
-                    split_f16(p[2 * k + 1].x, p[2 * k + 1].y, &pf[rt][k].z, &pf[rt][k].w);
-                }
+                l_run[ct] = fmaf(l_run[ct], alpha[ct], sum.x + sum.y);
             }
 
             // ---- outputs: 32 channels at a time, the tile's 64 keys in 4 steps
             const uint32_t v_at = ring + v_slot * L::codes;
+            const float2 unit2 = make_float2(sv_unit, sv_unit);
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-                float acc[RT][4][4];
+                float acc[CT][2][4];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[rt][n][e] = 0.f;
+                        for (int e = 0; e < 4; ++e) acc[ct][n][e] = 0.f;
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) {
                     uint32_t w[4];  // of keys 32 k2 + 8 i + 2 t, + 1: channels 4 gq .. 4 gq + 3 of the chunk
                     ldmatrix_trans(v_at + chunk_at<D>(32 * k2 + lane, c), w);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        uint32_t b0[4], b1[4];
-                        nibbles_f16(w[2 * k], b0[0], b0[1], b0[2], b0[3]);
-                        nibbles_f16(w[2 * k + 1], b1[0], b1[1], b1[2], b1[3]);
+                        uint4 a, b;  // channels 4 gq, + 1; 4 gq + 2, + 3
+                        nibbles_f16(w[2 * k], a.x, a.y, b.x, b.y);
+                        nibbles_f16(w[2 * k + 1], a.z, a.w, b.z, b.w);
 #pragma unroll
-                        for (int n = 0; n < 4; ++n)
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) mma_f16(acc[rt][n], pf[rt][2 * k2 + k], b0[n], b1[n]);
+                        for (int ct = 0; ct < CT; ++ct) {
+                            mma_f16(acc[ct][0], a, pf[ct][2 * k2 + k].x, pf[ct][2 * k2 + k].y);
+                            mma_f16(acc[ct][1], b, pf[ct][2 * k2 + k].x, pf[ct][2 * k2 + k].y);
+                        }
                     }
                 }
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            O[rt][4 * c + n][e] =
-                                fmaf(acc[rt][n][e] + acc[rt][n][2 + e], sv_unit, O[rt][4 * c + n][e] * alpha[rt]);
+                    for (int n = 0; n < 2; ++n) {
+                        const float2 v = fadd2(make_float2(acc[ct][n][0], acc[ct][n][2]),
+                                               make_float2(acc[ct][n][1], acc[ct][n][3]));
+                        O[ct][2 * c + n] = ffma2(v, unit2, fmul2(O[ct][2 * c + n], make_float2(alpha[ct], alpha[ct])));
+                    }
             }
             __syncwarp();
             issue();
@@ -476,16 +500,16 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
             return;
         }
 
-        // ---- results: this lane has 8 channels of each chunk of rows rt 8 + gq
+        // ---- results: this lane has 4 channels of each chunk of rows 4 ct + t
         const bool complete = P.n == P.tiles;
-        float* part = part_at<D, RT>(g, worker, P.k0 == 0);
+        float* part = part_at<D, R>(g, worker, P.k0 == 0);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float l = l_run[rt];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            const int r = rt * kRows + gq;
-            const int64_t index = rows[r].index;
+        for (int ct = 0; ct < CT; ++ct) {
+            float l = l_run[ct];
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+            const int r = 4 * ct + t;
+            const int64_t index = mine.row[r].index;
             if (index < 0) continue;
             const float f = !complete ? 1.f : l != 0.f ? 1.f / l : 0.f;  // l == 0: the row sees no key
             const bool wide = !complete || g.a.dtype == Q4LIN_DTYPE_F32;
@@ -493,28 +517,23 @@ __global__ void __launch_bounds__(32 * warps_of(D, RT), 1)
             unsigned short* to16 = static_cast<unsigned short*>(g.a.out) + index * D;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = O[rt][4 * c + e % 4][e / 4] * f;
-                if (wide) {
-                    *reinterpret_cast<float4*>(to + 32 * c + 8 * t) = make_float4(x[0], x[1], x[2], x[3]);
-                    *reinterpret_cast<float4*>(to + 32 * c + 8 * t + 4) = make_float4(x[4], x[5], x[6], x[7]);
-                } else {
-                    *reinterpret_cast<uint4*>(to16 + 32 * c + 8 * t) =
-                        make_uint4(to_16x2(x[0], x[1], g.a.dtype), to_16x2(x[2], x[3], g.a.dtype),
-                                   to_16x2(x[4], x[5], g.a.dtype), to_16x2(x[6], x[7], g.a.dtype));
-                }
+                const float2 x = fmul2(O[ct][2 * c], make_float2(f, f)), y = fmul2(O[ct][2 * c + 1], make_float2(f, f));
+                if (wide)
+                    *reinterpret_cast<float4*>(to + 32 * c + 4 * gq) = make_float4(x.x, x.y, y.x, y.y);
+                else
+                    *reinterpret_cast<uint2*>(to16 + 32 * c + 4 * gq) =
+                        make_uint2(to_16x2(x.x, x.y, g.a.dtype), to_16x2(y.x, y.y, g.a.dtype));
             }
-            if (t != 0) continue;
+            if (gq != 0) continue;
             if (!complete)
-                part[R * D + r] = m_run[rt], part[R * D + R + r] = l;
+                part[R * D + r] = m_run[ct], part[R * D + R + r] = l;
             else if (g.a.lse)
-                g.a.lse[index] = l != 0.f ? ((m_run[rt] == -INFINITY ? 0.f : m_run[rt]) + lg2(l * kUnshift)) * kLn2
+                g.a.lse[index] = l != 0.f ? ((m_run[ct] == -INFINITY ? 0.f : m_run[ct]) + lg2(l * kUnshift)) * kLn2
                                           : -INFINITY;
         }
         pos += P.n;
         if (pos >= end) return;
-        P = piece_of<RT>(g, S.prefix, pos, end);
+        P = piece_of<R>(g, S.prefix, pos, end);
         __syncwarp();  // every lane has read the queries and rows of this piece
     }
 }
@@ -535,13 +554,13 @@ bool map_codes(CUtensorMap* map, const q4lin_kv4_cache_t& C, const uint8_t* code
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int RT>
+template <int D, int CT>
 cudaError_t launch(SplitArgs& g, const SplitSize& size, const KvMaps& maps, const LaunchCtx& c) {
-    using L = Layout<D, RT>;
-    constexpr int R = RT * kRows;
-    constexpr int bytes = L::W * L::slots * (int)L::codes + (int)sizeof(Shared<D, RT>) + 1024;
+    using L = Layout<D, CT>;
+    constexpr int R = 4 * CT;
+    constexpr int bytes = L::W * L::slots * (int)L::codes + (int)sizeof(Shared<D, CT>) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of one SM");
-    cudaError_t e = kernel_smem_once<kv4_attention_kernel<D, RT>>(bytes);
+    cudaError_t e = kernel_smem_once<kv4_attention_kernel<D, CT>>(bytes);
     if (e != cudaSuccess) return e;
     // One CTA per SM, and no more than the longest possible list has tiles for.
     const int64_t grid = std::min<int64_t>(c.sm_count, size.segments * size.tiles);
@@ -549,25 +568,33 @@ cudaError_t launch(SplitArgs& g, const SplitSize& size, const KvMaps& maps, cons
     g.list = reinterpret_cast<int*>(c.ws);
     g.parts = c.ws + kMaxBatch + 4;  // 16-byte aligned
     if ((int64_t)g.workers * 2 * R * (D + 2) + kMaxBatch + 4 > c.ws_floats) return cudaErrorInvalidValue;
-    kv4_attention_kernel<D, RT><<<(unsigned)grid, 32 * L::W, bytes, c.stream>>>(maps, g);
+    kv4_attention_kernel<D, CT><<<(unsigned)grid, 32 * L::W, bytes, c.stream>>>(maps, g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return join_launch<D, RT>(g, size, c);
+    return join_launch<D, R>(g, size, c);
 }
 
 }  // namespace
+
+bool kv4_attention_split_countable(const q4lin_kv4_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max) {
+    return split_countable(cache, a, rows_max, 4);
+}
 
 cudaError_t kv4_attention_split_launch(const q4lin_kv4_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max,
                                        const LaunchCtx& c) {
     KvMaps maps;
     if (!map_codes(&maps.k, cache, cache.k_codes) || !map_codes(&maps.v, cache, cache.v_codes))
         return cudaErrorInvalidValue;
-    return in_groups(cache, a, rows_max, c, [&](SplitArgs& g, const SplitSize& size) {
-        switch (cache.head_dim) {
-            case 64: return size.two ? launch<64, 2>(g, size, maps, c) : launch<64, 1>(g, size, maps, c);
-            case 128: return size.two ? launch<128, 2>(g, size, maps, c) : launch<128, 1>(g, size, maps, c);
-            default: return launch<256, 1>(g, size, maps, c);
-        }
+    return in_groups(cache, a, rows_max, 4, c, [&](SplitArgs& g, const SplitSize& size) {
+        auto rows = [&](auto dim) {
+            constexpr int D = decltype(dim)::value;
+            if constexpr (D < 256)
+                if (size.rows > 8) return launch<D, 4>(g, size, maps, c);
+            return size.rows > 4 ? launch<D, 2>(g, size, maps, c) : launch<D, 1>(g, size, maps, c);
+        };
+        if (cache.head_dim == 64) return rows(std::integral_constant<int, 64>{});
+        if (cache.head_dim == 128) return rows(std::integral_constant<int, 128>{});
+        return rows(std::integral_constant<int, 256>{});
     });
 }
 

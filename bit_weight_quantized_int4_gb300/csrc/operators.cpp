@@ -380,7 +380,7 @@ q4lin_status_t q4lin_run_kv4_attention(q4lin_handle_t h, const q4lin_kv4_cache_t
     args.max_query = std::min(a->max_query, a->tokens);
     // No sequence has more positions than its pages: a window of as many leaves every key.
     if (args.window >= cache->pages_per_sequence * cache->page_size) args.window = 0;
-    if (!q4lin::attention_split_countable(*cache, args, INT64_MAX)) return Q4LIN_ERR_TOO_LARGE;
+    if (!q4lin::kv4_attention_split_countable(*cache, args, INT64_MAX)) return Q4LIN_ERR_TOO_LARGE;
     DeviceGuard g(h->device);
     if (!g.ok()) return Q4LIN_ERR_CUDA;
     return finish(q4lin::kv4_attention_split_launch(*cache, args, INT64_MAX, make_ctx(h, static_cast<cudaStream_t>(stream))));
