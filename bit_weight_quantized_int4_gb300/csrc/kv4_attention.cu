@@ -23,9 +23,10 @@
 namespace q4lin {
 namespace {
 
-// CT tiles of 8 columns, 4 query rows each.
+// CT tiles of 8 columns, 4 query rows each.  Warps in fours: one too many for a scheduler holds all of
+// them up (64 sequences, 8 / 10 / 12 / 14 / 16 warps: 90, 99, 82, 94, 86 us; two tiles 120, 151, 128).
 __host__ __device__ constexpr int warps_of(int D, int CT) {
-    return D == 64 ? (CT == 1 ? 20 : CT == 2 ? 16 : 12) : D == 128 ? (CT == 1 ? 16 : CT == 2 ? 12 : 8) : 8;
+    return D == 64 ? (CT == 1 ? 20 : CT == 2 ? 16 : 12) : D == 128 ? (CT == 1 ? 12 : 8) : 8;
 }
 
 struct KvMaps {
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
     Mine<D, CT>& mine = S.mine[warp];
     const q4lin_kv4_cache_t& C = g.cache;
     const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads), ps = g.page_shift;
-    const int ppt = kTile >> ps;  // pages per tile
+    const int tile_shift = 6 - ps, ppt = 1 << tile_shift;  // pages per tile
     griddep_launch_dependents();  // (the joining kernel waits for this one's end)
 
     if (tid == 0) {
@@ -159,18 +160,18 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
     // The piece's tiles `first`, first + 1, ...; with the pages of the next 32 / ppt of them in
     // the lanes: lane i holds page i % ppt of tile i / ppt.
     const uint32_t page_bytes = (uint32_t)(D / 2) << ps, page_scales = 4u << ps;
-    const int batch_tiles = 32 / ppt;
+    const int batch_tiles = 32 >> tile_shift, page_of_lane = lane & (ppt - 1), tile_of_lane = lane >> tile_shift;
     const int32_t* table = nullptr;
     int first = 0, cnt = 0, page_low = 0, pages = 0, head = 0, ids = 0, issued = 0, slot_in = 0, in_flight = 0;
     // (-1 is no page and none of the cache's: it is told apart from one in the table by its place.)
     auto load_ids = [&](int i) {
-        const int p = (first + i) * ppt + lane;
-        ids = i + lane / ppt < cnt && p >= page_low && p < pages ? __ldg(table + p) : -1;
+        const int p = ((first + i) << tile_shift) + lane;
+        ids = i + tile_of_lane < cnt && p >= page_low && p < pages ? __ldg(table + p) : -1;
     };
     auto check_ids = [&](int i) {
         if ((uint32_t)ids >= (uint32_t)C.num_pages) {
-            const int p = (first + i) * ppt + lane;
-            if (i + lane / ppt < cnt && p >= page_low && p < pages) {
+            const int p = ((first + i) << tile_shift) + lane;
+            if (i + tile_of_lane < cnt && p >= page_low && p < pages) {
                 atomicCAS(g.status, 0, kStatusIndex);
                 ids = 0;  // read something of the cache rather than nothing
             }
@@ -180,9 +181,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
     // copy a page's codes each, the next ones its scales.
     auto issue = [&]() {
         if (issued >= 2 * cnt) return;
-        const int i = issued >> 1;
-        if ((issued & 1) == 0 && i > 0 && i % batch_tiles == 0) load_ids(i), check_ids(i);
-        const int at = lane % ppt, id = __shfl_sync(0xffffffffu, ids, (i % batch_tiles) * ppt + at);
+        const int i = issued >> 1, in_batch = i & (batch_tiles - 1);
+        if ((issued & 1) == 0 && i > 0 && in_batch == 0) load_ids(i), check_ids(i);
+        const int id = __shfl_sync(0xffffffffu, ids, (in_batch << tile_shift) + page_of_lane);
         const int count = __popc(__ballot_sync(0xffffffffu, lane < ppt && id >= 0));
         const uint32_t bar = smem_u32(&S.full[warp][slot_in]);
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * (page_bytes + page_scales) + g.missing);
@@ -190,10 +191,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
         if (lane < 2 * ppt && id >= 0) {
             const int page = id * Hkv + head;
             if (lane < ppt)
-                tma_load_3d(ring + (uint32_t)slot_in * L::codes + at * page_bytes, issued & 1 ? &maps.v : &maps.k, 0, 0,
-                            page, bar);
+                tma_load_3d(ring + (uint32_t)slot_in * L::codes + page_of_lane * page_bytes,
+                            issued & 1 ? &maps.v : &maps.k, 0, 0, page, bar);
             else
-                bulk_load(scale_ring + (uint32_t)slot_in * L::scales + at * page_scales,
+                bulk_load(scale_ring + (uint32_t)slot_in * L::scales + page_of_lane * page_scales,
                           (issued & 1 ? C.v_scales : C.k_scales) + ((int64_t)page << ps), page_scales, bar);
         }
         ++issued, ++in_flight;
@@ -356,31 +357,36 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[ct][m][e] = 0.f;
+            // (Steps of the four blocks of 16 keys side by side: a block's own wait for one another.)
 #pragma unroll
             for (int c = 0; c < kLaneWords / kWords; ++c) {
                 const int byte = t * kLaneWords * 4 + c * kWords * 4;
+                uint32_t w[8][kWords];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    uint32_t w[2][kWords];
-                    ld_words(k_at + chunk_at<D>(16 * m + gq, byte >> 4) + (byte & 15), w[0]);
-                    ld_words(k_at + chunk_at<D>(16 * m + 8 + gq, byte >> 4) + (byte & 15), w[1]);
+                for (int j = 0; j < 8; ++j) ld_words(k_at + chunk_at<D>(8 * j + gq, byte >> 4) + (byte & 15), w[j]);
 #pragma unroll
-                    for (int k = 0; k < kWords; ++k) {
-                        uint4 a, b;
-                        nibbles_f16(w[0][k], a.x, a.z, b.x, b.z);
-                        nibbles_f16(w[1][k], a.y, a.w, b.y, b.w);
+                for (int k = 0; k < kWords; ++k) {
+                    const int step = 2 * (c * kWords + k);
+                    uint2 q0[CT], q1[CT];
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            const int step = 2 * (c * kWords + k);
-                            uint2 q0, q1;
-                            if constexpr (kHeld)
-                                q0 = held_q[ct][step], q1 = held_q[ct][step + 1];
-                            else
-                                q0 = mine.q[ct][step][lane], q1 = mine.q[ct][step + 1][lane];
-                            mma_f16(sc[ct][m], a, q0.x, q0.y);
-                            mma_f16(sc[ct][m], b, q1.x, q1.y);
-                        }
+                    for (int ct = 0; ct < CT; ++ct) {
+                        if constexpr (kHeld)
+                            q0[ct] = held_q[ct][step], q1[ct] = held_q[ct][step + 1];
+                        else
+                            q0[ct] = mine.q[ct][step][lane], q1[ct] = mine.q[ct][step + 1][lane];
                     }
+                    uint4 a[4], b[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        nibbles_f16(w[2 * m][k], a[m].x, a[m].z, b[m].x, b[m].z);
+                        nibbles_f16(w[2 * m + 1][k], a[m].y, a[m].w, b[m].y, b[m].w);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) mma_f16(sc[ct][m], a[m], q0[ct].x, q0[ct].y);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) mma_f16(sc[ct][m], b[m], q1[ct].x, q1[ct].y);
                 }
             }
             float2 sk[4];
@@ -412,8 +418,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                 float mx = -INFINITY;
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
-                    p[m] = fmul2(fadd2(make_float2(sc[ct][m][0], sc[ct][m][2]), make_float2(sc[ct][m][1], sc[ct][m][3])),
-                                 sk[m]);
+                    p[m] = fmul2(make_float2(sc[ct][m][0] + sc[ct][m][1], sc[ct][m][2] + sc[ct][m][3]), sk[m]);
                 if (!inside) {
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
@@ -447,41 +452,44 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                 l_run[ct] = fmaf(l_run[ct], alpha[ct], sum.x + sum.y);
             }
 
-            // ---- outputs: 32 channels at a time, the tile's 64 keys in 4 steps
+            // ---- outputs: 64 channels at a time, the tile's 64 keys in 4 steps
             const uint32_t v_at = ring + v_slot * L::codes;
             const float2 unit2 = make_float2(sv_unit, sv_unit);
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                float acc[CT][2][4];
+            for (int c0 = 0; c0 < kChunks; c0 += 2) {
+                float acc[CT][4][4];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < 4; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[ct][n][e] = 0.f;
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) {
-                    uint32_t w[4];  // of keys 32 k2 + 8 i + 2 t, + 1: channels 4 gq .. 4 gq + 3 of the chunk
-                    ldmatrix_trans(v_at + chunk_at<D>(32 * k2 + lane, c), w);
+                    uint32_t w[2][4];  // of keys 32 k2 + 8 i + 2 t, + 1: channels 4 gq .. 4 gq + 3 of the chunk
+                    ldmatrix_trans(v_at + chunk_at<D>(32 * k2 + lane, c0), w[0]);
+                    ldmatrix_trans(v_at + chunk_at<D>(32 * k2 + lane, c0 + 1), w[1]);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        uint4 a, b;  // channels 4 gq, + 1; 4 gq + 2, + 3
-                        nibbles_f16(w[2 * k], a.x, a.y, b.x, b.y);
-                        nibbles_f16(w[2 * k + 1], a.z, a.w, b.z, b.w);
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            mma_f16(acc[ct][0], a, pf[ct][2 * k2 + k].x, pf[ct][2 * k2 + k].y);
-                            mma_f16(acc[ct][1], b, pf[ct][2 * k2 + k].x, pf[ct][2 * k2 + k].y);
+                        for (int c = 0; c < 2; ++c) {
+                            uint4 a, b;  // channels 4 gq, + 1; 4 gq + 2, + 3
+                            nibbles_f16(w[c][2 * k], a.x, a.y, b.x, b.y);
+                            nibbles_f16(w[c][2 * k + 1], a.z, a.w, b.z, b.w);
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct) {
+                                mma_f16(acc[ct][2 * c], a, pf[ct][2 * k2 + k].x, pf[ct][2 * k2 + k].y);
+                                mma_f16(acc[ct][2 * c + 1], b, pf[ct][2 * k2 + k].x, pf[ct][2 * k2 + k].y);
+                            }
                         }
                     }
                 }
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float2 v = fadd2(make_float2(acc[ct][n][0], acc[ct][n][2]),
-                                               make_float2(acc[ct][n][1], acc[ct][n][3]));
-                        O[ct][2 * c + n] = ffma2(v, unit2, fmul2(O[ct][2 * c + n], make_float2(alpha[ct], alpha[ct])));
+                    for (int n = 0; n < 4; ++n) {
+                        const float2 v = make_float2(acc[ct][n][0] + acc[ct][n][1], acc[ct][n][2] + acc[ct][n][3]);
+                        O[ct][2 * c0 + n] = ffma2(v, unit2, fmul2(O[ct][2 * c0 + n], make_float2(alpha[ct], alpha[ct])));
                     }
             }
             __syncwarp();
