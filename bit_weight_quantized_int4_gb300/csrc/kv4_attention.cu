@@ -58,25 +58,6 @@ struct Shared {
     int failed;
 };
 
-// Nibbles n and n + 4 (b0: n = 0, b1: 1, b2: 2, b3: 3) of a word, as exact fp16 pairs of code - 8.
-__device__ __forceinline__ void nibbles_f16(uint32_t w, uint32_t& b0, uint32_t& b1, uint32_t& b2, uint32_t& b3) {
-    const uint32_t v = w >> 8;
-    auto low = [](uint32_t x) {
-        uint32_t y;
-        asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(y) : "r"(x));
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x6408)));
-        return *reinterpret_cast<const uint32_t*>(&h);
-    };
-    auto high = [](uint32_t x) {
-        uint32_t y;
-        asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(y) : "r"(x));
-        // (1024 + 16 c) / 16 - 72
-        const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&y), __half2half2(__ushort_as_half(0x2c00)),
-                                  __half2half2(__ushort_as_half(0xd480)));
-        return *reinterpret_cast<const uint32_t*>(&h);
-    };
-    b0 = low(w), b1 = high(w), b2 = low(v), b3 = high(v);
-}
 __device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])

@@ -237,19 +237,12 @@ q4lin_status_t check_norm_rope(const q4lin_norm_rope_t& a, NormRows* n) {
     return Q4LIN_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-q4lin_status_t q4lin_run_kv_append(q4lin_handle_t h, const q4lin_kv_cache_t* cache,
-                                   const q4lin_kv_append_t* a, void* stream) {
-    return run_append(h, cache, a, stream, 8, q4lin::kv_append_launch);
-}
-
-q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cache,
-                                   const q4lin_attention_t* a, void* stream) {
+// Attention over a cache of `bits` bits by its kernels.
+template <typename Countable, typename Prompt, typename Split>
+q4lin_status_t run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cache, const q4lin_attention_t* a, void* stream,
+                             int bits, Countable countable, Prompt prompt_launch, Split split_launch) {
     bool idle;
-    const q4lin_status_t st = check_attention(h, cache, a, 8, &idle);
+    const q4lin_status_t st = check_attention(h, cache, a, bits, &idle);
     if (st != Q4LIN_OK || idle) return st;
     const int64_t t = a->tokens * a->heads;
     // The kernels count query rows in 32 bits, and the prompts' kernel keeps 32 bytes for each 256
@@ -270,14 +263,29 @@ q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cac
     args.max_query = max_query;
     // No sequence has more positions than its pages: a window of as many leaves every key.
     if (args.window >= cache->pages_per_sequence * cache->page_size) args.window = 0;
-    if (split && !q4lin::attention_split_countable(*cache, args, split_most)) return Q4LIN_ERR_TOO_LARGE;
+    if (split && !countable(*cache, args, split_most)) return Q4LIN_ERR_TOO_LARGE;
     DeviceGuard g(h->device);
     if (!g.ok()) return Q4LIN_ERR_CUDA;
     const q4lin::LaunchCtx c = make_ctx(h, static_cast<cudaStream_t>(stream));
     cudaError_t err = cudaSuccess;
-    if (prompts) err = q4lin::attention_prompt_launch(*cache, args, split ? split_rows : 0, c);
-    if (split && err == cudaSuccess) err = q4lin::attention_split_launch(*cache, args, split_most, c);
+    if (prompts) err = prompt_launch(*cache, args, split ? split_rows : 0, c);
+    if (split && err == cudaSuccess) err = split_launch(*cache, args, split_most, c);
     return finish(err);
+}
+
+}  // namespace
+
+extern "C" {
+
+q4lin_status_t q4lin_run_kv_append(q4lin_handle_t h, const q4lin_kv_cache_t* cache,
+                                   const q4lin_kv_append_t* a, void* stream) {
+    return run_append(h, cache, a, stream, 8, q4lin::kv_append_launch);
+}
+
+q4lin_status_t q4lin_run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cache,
+                                   const q4lin_attention_t* a, void* stream) {
+    return run_attention(h, cache, a, stream, 8, q4lin::attention_split_countable, q4lin::attention_prompt_launch,
+                         q4lin::attention_split_launch);
 }
 
 q4lin_status_t q4lin_run_logprobs(q4lin_handle_t h, const q4lin_logprobs_t* a, void* stream) {
@@ -372,18 +380,8 @@ q4lin_status_t q4lin_run_kv4_read(q4lin_handle_t h, const q4lin_kv4_cache_t* cac
 
 q4lin_status_t q4lin_run_kv4_attention(q4lin_handle_t h, const q4lin_kv4_cache_t* cache,
                                        const q4lin_attention_t* a, void* stream) {
-    bool idle;
-    const q4lin_status_t st = check_attention(h, cache, a, 4, &idle);
-    if (st != Q4LIN_OK || idle) return st;
-    if (a->tokens * a->heads > 0x7FFFFFFF) return Q4LIN_ERR_TOO_LARGE;
-    q4lin_attention_t args = *a;
-    args.max_query = std::min(a->max_query, a->tokens);
-    // No sequence has more positions than its pages: a window of as many leaves every key.
-    if (args.window >= cache->pages_per_sequence * cache->page_size) args.window = 0;
-    if (!q4lin::kv4_attention_split_countable(*cache, args, INT64_MAX)) return Q4LIN_ERR_TOO_LARGE;
-    DeviceGuard g(h->device);
-    if (!g.ok()) return Q4LIN_ERR_CUDA;
-    return finish(q4lin::kv4_attention_split_launch(*cache, args, INT64_MAX, make_ctx(h, static_cast<cudaStream_t>(stream))));
+    return run_attention(h, cache, a, stream, 4, q4lin::kv4_attention_split_countable,
+                         q4lin::kv4_attention_prompt_launch, q4lin::kv4_attention_split_launch);
 }
 
 q4lin_status_t q4lin_run_norm_rope(q4lin_handle_t h, const q4lin_norm_rope_t* a, void* stream) {

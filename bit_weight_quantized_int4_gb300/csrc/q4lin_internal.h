@@ -166,6 +166,8 @@ cudaError_t attention_prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_a
 // The same over a 4-bit cache (kv4_attention.cu).
 cudaError_t kv4_attention_split_launch(const q4lin_kv4_cache_t& cache, const q4lin_attention_t& a,
                                        int64_t rows_max, const LaunchCtx& c);
+cudaError_t kv4_attention_prompt_launch(const q4lin_kv4_cache_t& cache, const q4lin_attention_t& a,
+                                        int64_t rows_min, const LaunchCtx& c);
 bool kv4_attention_split_countable(const q4lin_kv4_cache_t& cache, const q4lin_attention_t& a, int64_t rows_max);
 cudaError_t kv4_append_launch(const q4lin_kv4_cache_t& cache, const q4lin_kv_append_t& a, const LaunchCtx& c);
 cudaError_t kv4_read_launch(const q4lin_kv4_cache_t& cache, const q4lin_kv_read_t& a, const LaunchCtx& c);
