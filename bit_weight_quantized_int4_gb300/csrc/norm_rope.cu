@@ -1,9 +1,9 @@
 // norm_rope.cu -- queries and keys normalised per head and rotated in one pass, and the gradient
 // of that.
 //
-// A warp takes heads of one token, `PASSES` x 32 / (D / 8) of them at a time; a lane holds eight
-// channels of a head (the two groups of four that the rotation pairs), and the token's angles and
-// the weights of its channels for all of the warp's heads.
+// A warp takes heads of one token (a part of them where tokens are few), `PASSES` x 32 / (D / 8) of
+// them in flight; a lane holds eight channels of a head (the two groups of four that the rotation
+// pairs), and the token's angles and the weights of its channels for all of the warp's heads.
 //
 // Forward, y = R(x r w) with r = 1 / sqrt(mean x^2 + eps); backward, with g = R^T dy and u = x r:
 // dw = sum g u, dx = r (g w - u mean(g w u)).  R turns pairs by an angle, so R^T turns them back.
@@ -17,15 +17,18 @@ namespace {
 using namespace ptx;
 using namespace serving;
 
-constexpr int kWarps = 4;
+// Passes in flight of a warp, as many as registers leave warps for (8192 tokens of 40 heads of 128 in
+// bf16: forward 1 / 2 / 3 / 4 passes 38.9, 34.2, 33.8, 35.0 us).
+constexpr int kAhead = 3, kBackAhead = 4;
+constexpr int kWarps = 4, kBackWarps = 8;
 
 struct NormArgs {
     q4lin_norm_rope_t a;
     const void *dq, *dk;  // backward: the gradients that come in
     int64_t dq_token, dq_head, dk_token, dk_head;
     float* parts;  // backward: [kind][CTA][D] sums of the weights' gradients
-    int q_vec, k_vec, q_out_vec, k_out_vec, dq_vec, dk_vec;
-    int64_t q_chunks, chunks;  // of a token's heads
+    bool vec;            // groups of four elements of all arrays are aligned
+    int64_t part_heads;  // of a token's heads, queries' and keys', in a part
     int* status;
 };
 
@@ -36,7 +39,6 @@ struct Side {
     const void* d;
     const float* w;
     int64_t xt, xh, yt, yh, dt, dh, heads;
-    bool x_vec, y_vec, d_vec;
 };
 __device__ __forceinline__ Side side_of(const NormArgs& g, bool keys) {
     Side s;
@@ -47,11 +49,13 @@ __device__ __forceinline__ Side side_of(const NormArgs& g, bool keys) {
     s.yh = keys ? g.a.k_out_head_stride : g.a.q_out_head_stride;
     s.dt = keys ? g.dk_token : g.dq_token, s.dh = keys ? g.dk_head : g.dq_head;
     s.heads = keys ? g.a.kv_heads : g.a.heads;
-    s.x_vec = keys ? g.k_vec : g.q_vec, s.y_vec = keys ? g.k_out_vec : g.q_out_vec;
-    s.d_vec = keys ? g.dk_vec : g.dq_vec;
     return s;
 }
 
+// A lane's eight channels: two groups of four, as pairs.
+struct Eight {
+    float2 v[4];
+};
 // Sum over the U lanes of a head.
 template <int U>
 __device__ __forceinline__ float head_sum(float v) {
@@ -59,222 +63,320 @@ __device__ __forceinline__ float head_sum(float v) {
     for (int o = U / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+template <int U>
+__device__ __forceinline__ float dot(const Eight& a, const Eight& b) {
+    float2 sum = fmul2(a.v[0], b.v[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) sum = ffma2(a.v[e], b.v[e], sum);
+    return head_sum<U>(sum.x + sum.y);
+}
+__device__ __forceinline__ void scale_by(Eight& x, float f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x.v[e] = fmul2(x.v[e], make_float2(f, f));
+}
 // x becomes u = x r; the result is r.  Where the squares pass fp32's range, x is scaled by 2^-70
 // first (whole warp: the sums need every lane).
 template <int D>
-__device__ __forceinline__ float normalise(float (&x)[8], float eps) {
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-    sum = head_sum<D / 8>(sum);
-    float r = __frsqrt_rn(fmaf(sum, 1.f / D, eps)), back = 1.f;
+__device__ __forceinline__ float normalise(Eight& x, float eps) {
+    const float sum = dot<D / 8>(x, x);
+    float r = rsqrtf(fmaf(sum, 1.f / D, eps)), back = 1.f;
     if (__any_sync(0xffffffffu, sum > 3e38f)) {
         constexpr float kDown = 8.470329472543003e-22f;  // 2^-70
         const bool far = sum > 3e38f;
-        float again = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float y = x[e] * kDown;
-            again = fmaf(y, y, again);
-            if (far) x[e] = y;
-        }
-        again = head_sum<D / 8>(again);
-        if (far) r = __frsqrt_rn(fmaf(again, 1.f / D, eps * kDown * kDown)), back = kDown;
+        if (far) scale_by(x, kDown);
+        const float again = dot<D / 8>(x, x);
+        if (far) r = rsqrtf(fmaf(again, 1.f / D, eps * kDown * kDown)), back = kDown;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= r;
+    scale_by(x, r);
     return r * back;
 }
-__device__ __forceinline__ void load_weight(const float* w, int lo, int hi, float (&v)[8]) {
+template <bool VEC>
+__device__ __forceinline__ Eight load_weight(const float* w, int lo, int hi) {
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = w ? __ldg(w + (e < 4 ? lo + e : hi + e - 4)) : 1.f;
+    for (int e = 0; e < 8; ++e) v[e] = 1.f;
+    if (w) {
+        load_four(w, Q4LIN_DTYPE_F32, lo, VEC, v);
+        load_four(w, Q4LIN_DTYPE_F32, hi, VEC, v + 4);
+    }
+    return {make_float2(v[0], v[1]), make_float2(v[2], v[3]), make_float2(v[4], v[5]), make_float2(v[6], v[7])};
 }
 
-// Four consecutive elements by ordinary loads: outputs may lie where the inputs are.
-__device__ __forceinline__ void read_four(const void* p, int dtype, int64_t i, bool vec, float* x) {
-    if (dtype == Q4LIN_DTYPE_F32) {
-        const float* f = static_cast<const float*>(p) + i;
-        if (vec) {
-            const float4 v = *reinterpret_cast<const float4*>(f);
-            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+// A lane's eight elements as they lie in memory, by ordinary loads: outputs may lie where the inputs
+// are.  VEC: groups of four are aligned.
+template <int DT, bool VEC>
+struct Raw {
+    uint2 w[DT == Q4LIN_DTYPE_F32 ? 4 : 2];
+
+    __device__ __forceinline__ void load(const void* p, int64_t lo, int64_t hi) {
+        if constexpr (DT == Q4LIN_DTYPE_F32) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t* f = static_cast<const uint32_t*>(p) + (g ? hi : lo);
+                if constexpr (VEC) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(f);
+                    w[2 * g] = make_uint2(v.x, v.y), w[2 * g + 1] = make_uint2(v.z, v.w);
+                } else {
+                    w[2 * g] = make_uint2(f[0], f[1]), w[2 * g + 1] = make_uint2(f[2], f[3]);
+                }
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = f[e];
+            for (int g = 0; g < 2; ++g) {
+                const unsigned short* b = static_cast<const unsigned short*>(p) + (g ? hi : lo);
+                if constexpr (VEC)
+                    w[g] = *reinterpret_cast<const uint2*>(b);
+                else
+                    w[g] = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+            }
         }
-        return;
     }
-    const unsigned short* b = static_cast<const unsigned short*>(p) + i;
-    uint2 v;
-    if (vec)
-        v = *reinterpret_cast<const uint2*>(b);
-    else
-        v = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
-    const float2 lo = unpack2(v.x, dtype), hi = unpack2(v.y, dtype);
-    x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+    __device__ __forceinline__ Eight unpack() const {
+        Eight x;
+        if constexpr (DT == Q4LIN_DTYPE_F32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x.v[e] = make_float2(__uint_as_float(w[e].x), __uint_as_float(w[e].y));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x.v[2 * e] = unpack2(w[e].x, DT), x.v[2 * e + 1] = unpack2(w[e].y, DT);
+        }
+        return x;
+    }
+};
+
+// The token's position, and whether it is in the table (else reported, and one that is).
+__device__ __forceinline__ int64_t position_of(const NormArgs& g, int64_t token, bool* good) {
+    *good = true;
+    if (!g.a.rope.cos) return 0;
+    const int64_t position = __ldg(g.a.positions + token);
+    *good = position >= 0 && position < g.a.rope.positions;
+    if (!*good && (threadIdx.x & 31) == 0) atomicCAS(g.status, 0, kStatusIndex);
+    return *good ? position : 0;
 }
 
-// The token's position; false where it is outside the table (reported).
-__device__ __forceinline__ bool position_of(const NormArgs& g, int64_t token, int64_t* position) {
-    if (!g.a.rope.cos) return true;
-    *position = __ldg(g.a.positions + token);
-    if (*position >= 0 && *position < g.a.rope.positions) return true;
-    if ((threadIdx.x & 31) == 0) atomicCAS(g.status, 0, kStatusIndex);
-    return false;
+// The rotation by the four angles of a lane, of pairs (channel, channel half the rotated ones further)
+// or of neighbours.
+struct Angles {
+    float2 c[2], s[2];
+};
+__device__ __forceinline__ void turn(const q4lin_rope_t& r, const Angles& a, Eight& x) {
+    if (r.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float c = e % 2 ? a.c[e / 2].y : a.c[e / 2].x, s = e % 2 ? a.s[e / 2].y : a.s[e / 2].x;
+            const float2 v = x.v[e];
+            x.v[e] = make_float2(fmaf(v.x, c, -(v.y * s)), fmaf(v.y, c, v.x * s));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 p = x.v[e], q = x.v[2 + e], minus = make_float2(-a.s[e].x, -a.s[e].y);
+            x.v[e] = ffma2(p, a.c[e], fmul2(q, minus)), x.v[2 + e] = ffma2(q, a.c[e], fmul2(p, a.s[e]));
+        }
+    }
+}
+__device__ __forceinline__ Angles angles_of(const q4lin_rope_t& r, int64_t position, int u, float sign) {
+    float c[4], s[4];
+    rope_load(r, position, u, c, s);
+    return {{make_float2(c[0], c[1]), make_float2(c[2], c[3])},
+            {make_float2(sign * s[0], sign * s[1]), make_float2(sign * s[2], sign * s[3])}};
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_row(void* p, int64_t at, int lo, int hi, const Eight& x) {
+    const float y[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
+    store_four(p, DT, at + lo, VEC, y);
+    store_four(p, DT, at + hi, VEC, y + 4);
 }
 
-template <int D, int DT, int PASSES>
+// A part's heads: queries [q0, q1) and keys [k0, k1).
+struct Heads {
+    int64_t q0, q1, k0, k1;
+};
+__device__ __forceinline__ Heads heads_of(const NormArgs& g, int part) {
+    const int64_t all = g.a.heads + g.a.kv_heads, h0 = part * g.part_heads, h1 = min(h0 + g.part_heads, all);
+    const int64_t n = g.a.heads;
+    return {min(h0, n), min(h1, n), max(h0, n) - n, max(h1, n) - n};
+}
+
+template <int D, int DT, int AHEAD, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormArgs g) {
     constexpr int U = D / 8, R = 32 / U;
-    const int lane = threadIdx.x & 31, u = lane % U;
-    bool turned;
+    const int lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
+    const int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (token >= g.a.tokens) return;
+    bool turned, good = true, first = true;
     int lo, hi;
     rope_channels(g.a.rope, u, &turned, &lo, &hi);
-    const int64_t items = g.a.tokens * g.chunks;
-    for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items; i += (int64_t)gridDim.x * kWarps) {
-        const int64_t token = i / g.chunks, chunk = i - token * g.chunks;
-        const bool keys = chunk >= g.q_chunks;
-        const Side s = side_of(g, keys);
-        const int64_t h0 = (keys ? chunk - g.q_chunks : chunk) * (PASSES * R) + lane / U;
-        float x[PASSES][8], c[4], sn[4], w[8];
+    const Heads heads = heads_of(g, blockIdx.y);
+    Angles angles;
+    auto rows = [&](auto keys) {
+        const Side s = side_of(g, decltype(keys)::value);
+        const int begin = (int)(decltype(keys)::value ? heads.k0 : heads.q0);
+        const int end = (int)(decltype(keys)::value ? heads.k1 : heads.q1);
+        if (begin >= end) return;
+        Raw<DT, VEC> raw[AHEAD];
+        auto fetch = [&](Raw<DT, VEC>& r, int h0) {
+            const int64_t at = token * s.xt + min(h0 + sub, end - 1) * s.xh;
+            r.load(s.x, at + lo, at + hi);
+        };
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
+        for (int p = 0; p < AHEAD; ++p)
+            if (begin + p * R < end) fetch(raw[p], begin + p * R);
+        const Eight w = load_weight<VEC>(s.w, lo, hi);
+        if (first) {  // (behind the first rows' loads)
+            const int64_t position = position_of(g, token, &good);
+            if (turned) angles = angles_of(g.a.rope, position, u, 1.f);
+            first = false;
+        }
+#pragma unroll 1
+        for (int h0 = begin; h0 < end; h0 += AHEAD * R) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[p][e] = 0.f;
-            const int64_t h = h0 + p * R, at = token * s.xt + h * s.xh;
-            if (h < s.heads) {
-                read_four(s.x, DT, at + lo, s.x_vec, x[p]);
-                read_four(s.x, DT, at + hi, s.x_vec, x[p] + 4);
+            for (int p = 0; p < AHEAD; ++p) {
+                const int hp = h0 + p * R, h = hp + sub;
+                if (hp >= end) break;
+                Eight x = raw[p].unpack();
+                if (hp + AHEAD * R < end) fetch(raw[p], hp + AHEAD * R);
+                normalise<D>(x, g.a.eps);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x.v[e] = fmul2(x.v[e], w.v[e]);
+                if (turned) turn(g.a.rope, angles, x);
+                if (h < end && good) store_row<DT, VEC>(s.y, token * s.yt + h * s.yh, lo, hi, x);
             }
         }
-        load_weight(s.w, lo, hi, w);
-        int64_t position = 0;
-        if (!position_of(g, token, &position)) continue;
-        if (turned) rope_load(g.a.rope, position, u, c, sn);
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int64_t h = h0 + p * R, at = token * s.yt + h * s.yh;
-            normalise<D>(x[p], g.a.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[p][e] *= w[e];
-            if (turned) rope_apply(g.a.rope, c, sn, x[p]);
-            if (h < s.heads) {
-                store_four(s.y, DT, at + lo, s.y_vec, x[p]);
-                store_four(s.y, DT, at + hi, s.y_vec, x[p] + 4);
-            }
-        }
-    }
+    };
+    rows(std::false_type{});
+    rows(std::true_type{});
 }
 
-// CTAs of a kind (queries, keys) walk over its items with the weights' sums in registers.
-template <int D, int DT, int PASSES>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_backward_kernel(const NormArgs g) {
+// CTAs walk over tokens with the weights' sums in registers.
+template <int D, int DT, int AHEAD, bool VEC>
+__global__ void __launch_bounds__(32 * kBackWarps) norm_rope_backward_kernel(const NormArgs g) {
     constexpr int U = D / 8, R = 32 / U;
-    __shared__ float sums[kWarps * R][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U;
+    __shared__ float sums[kBackWarps * R][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
     griddep_launch_dependents();  // (the kernel that joins the sums waits for this one's end)
     bool turned;
     int lo, hi;
     rope_channels(g.a.rope, u, &turned, &lo, &hi);
+    const Heads heads = heads_of(g, blockIdx.y);
+    auto rows = [&](auto keys) {
+        constexpr bool kKeys = decltype(keys)::value;
+        const Side s = side_of(g, kKeys);
+        const int begin = (int)(kKeys ? heads.k0 : heads.q0), end = (int)(kKeys ? heads.k1 : heads.q1);
+        const Eight w = load_weight<VEC>(s.w, lo, hi);
+        Eight dw;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dw.v[e] = make_float2(0.f, 0.f);
 #pragma unroll 1
-    for (int kind = 0; kind < 2; ++kind) {
-        const Side s = side_of(g, kind == 1);
-        const int64_t chunks = kind ? g.chunks - g.q_chunks : g.q_chunks, items = g.a.tokens * chunks;
-        float w[8], dw[8];
-        load_weight(s.w, lo, hi, w);
+        for (int64_t token = (int64_t)blockIdx.x * kBackWarps + warp; token < g.a.tokens && begin < end;
+             token += (int64_t)gridDim.x * kBackWarps) {
+            Raw<DT, VEC> raw_x[AHEAD], raw_d[AHEAD];
+            auto fetch = [&](int p, int h0) {
+                const int h = min(h0 + sub, end - 1);
+                const int64_t at = token * s.xt + h * s.xh, dat = token * s.dt + h * s.dh;
+                raw_x[p].load(s.x, at + lo, at + hi);
+                raw_d[p].load(s.d, dat + lo, dat + hi);
+            };
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[e] = 0.f;
-        for (int64_t i = (int64_t)blockIdx.x * kWarps + warp; i < items; i += (int64_t)gridDim.x * kWarps) {
-            const int64_t token = i / chunks, h0 = (i - token * chunks) * (PASSES * R) + lane / U;
-            float x[PASSES][8], d[PASSES][8], c[4], sn[4];
+            for (int p = 0; p < AHEAD; ++p)
+                if (begin + p * R < end) fetch(p, begin + p * R);
+            Angles angles;
+            bool good;
+            const int64_t position = position_of(g, token, &good);  // (behind the first rows' loads)
+            if (turned) angles = angles_of(g.a.rope, position, u, -1.f);  // back
+#pragma unroll 1
+            for (int h0 = begin; h0 < end; h0 += AHEAD * R) {
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
+                for (int p = 0; p < AHEAD; ++p) {
+                    const int hp = h0 + p * R, h = hp + sub;
+                    if (hp >= end) break;
+                    const bool in = h < end && good;
+                    Eight x = raw_x[p].unpack(), d = raw_d[p].unpack();
+                    if (hp + AHEAD * R < end) fetch(p, hp + AHEAD * R);
+                    const float r = normalise<D>(x, g.a.eps);
+                    if (turned) turn(g.a.rope, angles, d);
+                    if (in) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[p][e] = d[p][e] = 0.f;
-                const int64_t h = h0 + p * R, at = token * s.xt + h * s.xh, dat = token * s.dt + h * s.dh;
-                if (h < s.heads) {
-                    read_four(s.x, DT, at + lo, s.x_vec, x[p]);
-                    read_four(s.x, DT, at + hi, s.x_vec, x[p] + 4);
-                    read_four(s.d, DT, dat + lo, s.d_vec, d[p]);
-                    read_four(s.d, DT, dat + hi, s.d_vec, d[p] + 4);
-                }
-            }
-            int64_t position = 0;
-            if (!position_of(g, token, &position)) continue;
-            if (turned) {
-                rope_load(g.a.rope, position, u, c, sn);
+                        for (int e = 0; e < 4; ++e) dw.v[e] = ffma2(d.v[e], x.v[e], dw.v[e]);
+                    }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sn[e] = -sn[e];  // back
-            }
+                    for (int e = 0; e < 4; ++e) d.v[e] = fmul2(d.v[e], w.v[e]);
+                    const float mean = dot<U>(d, x) * (-1.f / D);
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                const int64_t h = h0 + p * R, at = token * s.yt + h * s.yh;
-                const float r = normalise<D>(x[p], g.a.eps);
-                if (turned) rope_apply(g.a.rope, c, sn, d[p]);
-                float dot = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (h < s.heads) dw[e] = fmaf(d[p][e], x[p][e], dw[e]);
-                    d[p][e] *= w[e];
-                    dot = fmaf(d[p][e], x[p][e], dot);
-                }
-                dot = head_sum<U>(dot) * (1.f / D);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[p][e] = r * fmaf(-x[p][e], dot, d[p][e]);
-                if (h < s.heads) {
-                    store_four(s.y, DT, at + lo, s.y_vec, x[p]);
-                    store_four(s.y, DT, at + hi, s.y_vec, x[p] + 4);
+                    for (int e = 0; e < 4; ++e) x.v[e] = ffma2(x.v[e], make_float2(mean, mean), d.v[e]);
+                    scale_by(x, r);
+                    if (in) store_row<DT, VEC>(s.y, token * s.yt + h * s.yh, lo, hi, x);
                 }
             }
         }
         // The CTA's sums, the warps' and their rows' in order.
-        if (kind) __syncthreads();
+        if (kKeys) __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sums[warp * R + lane / U][e < 4 ? lo + e : hi + e - 4] = dw[e];
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<float2*>(&sums[warp * R + sub][(e < 2 ? lo : hi) + e % 2 * 2]) = dw.v[e];
         __syncthreads();
-        for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
+        const int64_t cta = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, ctas = (int64_t)gridDim.x * gridDim.y;
+        for (int d = threadIdx.x; d < D; d += 32 * kBackWarps) {
             float v = 0.f;
-            for (int j = 0; j < kWarps * R; ++j) v += sums[j][d];
-            g.parts[((int64_t)kind * gridDim.x + blockIdx.x) * D + d] = v;
+#pragma unroll
+            for (int j = 0; j < kBackWarps * R; ++j) v += sums[j][d];
+            g.parts[(kKeys * ctas + cta) * D + d] = v;
         }
-    }
+    };
+    rows(std::false_type{});
+    rows(std::true_type{});
 }
 
-// One CTA for 32 channels of a kind: the CTAs' sums, 8 stretches of them at a time.
-__global__ void __launch_bounds__(256) norm_rope_join_kernel(const float* parts, int ctas, int D, float* dqw, float* dkw) {
-    __shared__ float sums[8][32];
+// One CTA for 32 channels of a kind: the CTAs' sums, every 32nd of them by a warp.
+__global__ void __launch_bounds__(1024) norm_rope_join_kernel(const float* parts, int ctas, int D, float* dqw, float* dkw) {
+    __shared__ float sums[32][33];
     const int kind = blockIdx.y, column = threadIdx.x & 31, stretch = threadIdx.x >> 5, d = blockIdx.x * 32 + column;
     float* to = kind ? dkw : dqw;
     griddep_wait();
     if (!to) return;
     float v = 0.f;
-    for (int i = stretch; i < ctas; i += 8) v += __ldcg(parts + ((int64_t)kind * ctas + i) * D + d);
+#pragma unroll 8
+    for (int i = stretch; i < ctas; i += 32) v += __ldcg(parts + ((int64_t)kind * ctas + i) * D + d);
     sums[stretch][column] = v;
     __syncthreads();
-    if (stretch) return;
+    v = sums[column][stretch];  // of channel `stretch`
 #pragma unroll
-    for (int j = 1; j < 8; ++j) v += sums[j][column];
-    to[d] = v;
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (column == 0) to[blockIdx.x * 32 + stretch] = v;
+}
+
+// Parts of a token's heads, whole rows of lanes each, so that there are `warps` warps where the
+// heads allow.
+unsigned parts_of(NormArgs& g, int64_t row_heads, int64_t warps) {
+    const int64_t rows = (g.a.heads + g.a.kv_heads + row_heads - 1) / row_heads;
+    const int64_t parts = std::max<int64_t>(1, std::min(std::min(rows, (warps + g.a.tokens - 1) / g.a.tokens), (int64_t)65535));
+    const int64_t each = (rows + parts - 1) / parts;
+    g.part_heads = each * row_heads;
+    return (unsigned)((rows + each - 1) / each);
 }
 
 template <int D, int DT>
 cudaError_t forward(NormArgs& g, const LaunchCtx& c) {
-    constexpr int kPasses = 1, kHeads = kPasses * 32 / (D / 8);
-    g.q_chunks = (g.a.heads + kHeads - 1) / kHeads;
-    g.chunks = g.q_chunks + (g.a.kv_heads + kHeads - 1) / kHeads;
-    const int64_t blocks = (g.a.tokens * g.chunks + kWarps - 1) / kWarps;
-    norm_rope_kernel<D, DT, kPasses><<<(unsigned)std::min<int64_t>(blocks, 1 << 30), 32 * kWarps, 0, c.stream>>>(g);
+    const unsigned parts = parts_of(g, 32 / (D / 8), 64 * c.sm_count);
+    const dim3 grid((unsigned)((g.a.tokens + kWarps - 1) / kWarps), parts);
+    if (g.vec)
+        norm_rope_kernel<D, DT, kAhead, true><<<grid, 32 * kWarps, 0, c.stream>>>(g);
+    else
+        norm_rope_kernel<D, DT, 1, false><<<grid, 32 * kWarps, 0, c.stream>>>(g);
     return cudaGetLastError();
 }
 template <int D, int DT>
 cudaError_t backward(NormArgs& g, float* dqw, float* dkw, const LaunchCtx& c) {
-    constexpr int kPasses = 1, kHeads = kPasses * 32 / (D / 8);
-    g.q_chunks = (g.a.heads + kHeads - 1) / kHeads;
-    g.chunks = g.q_chunks + (g.a.kv_heads + kHeads - 1) / kHeads;
-    const int64_t blocks = (g.a.tokens * std::max(g.q_chunks, g.chunks - g.q_chunks) + kWarps - 1) / kWarps;
-    const unsigned grid = (unsigned)std::min<int64_t>(blocks, 8 * c.sm_count);
-    if ((int64_t)2 * grid * D > c.ws_floats) return cudaErrorInvalidValue;
+    const unsigned parts = parts_of(g, 32 / (D / 8), 16 * c.sm_count);
+    const int64_t most = std::max<int64_t>(1, 2 * c.sm_count / parts);
+    const dim3 grid((unsigned)std::min((g.a.tokens + kBackWarps - 1) / kBackWarps, most), parts);
+    const int64_t ctas = (int64_t)grid.x * grid.y;
+    if (2 * ctas * D > c.ws_floats) return cudaErrorInvalidValue;
     g.parts = c.ws;
-    norm_rope_backward_kernel<D, DT, kPasses><<<grid, 32 * kWarps, 0, c.stream>>>(g);
+    if (g.vec)
+        norm_rope_backward_kernel<D, DT, kBackAhead, true><<<grid, 32 * kBackWarps, 0, c.stream>>>(g);
+    else
+        norm_rope_backward_kernel<D, DT, 1, false><<<grid, 32 * kBackWarps, 0, c.stream>>>(g);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!dqw && !dkw)) return e;
     // Its launch overlaps the first kernel; it waits for that one's end on the device.
@@ -283,20 +385,24 @@ cudaError_t backward(NormArgs& g, float* dqw, float* dkw, const LaunchCtx& c) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(D / 32, 2);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(1024);
     cfg.stream = c.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_rope_join_kernel, (const float*)g.parts, (int)grid, D, dqw, dkw);
+    return cudaLaunchKernelEx(&cfg, norm_rope_join_kernel, (const float*)g.parts, (int)ctas, D, dqw, dkw);
 }
 
 NormArgs args_of(const q4lin_norm_rope_t& a, const LaunchCtx& c) {
     NormArgs g = {};
     g.a = a;
-    g.q_vec = fours_aligned(a.q, a.dtype, a.q_token_stride, a.q_head_stride);
-    g.k_vec = fours_aligned(a.k, a.dtype, a.k_token_stride, a.k_head_stride);
-    g.q_out_vec = fours_aligned(a.q_out, a.dtype, a.q_out_token_stride, a.q_out_head_stride);
-    g.k_out_vec = fours_aligned(a.k_out, a.dtype, a.k_out_token_stride, a.k_out_head_stride);
+    auto aligned_rows = [&](const void* p, int64_t t, int64_t h, int64_t heads) {
+        return heads == 0 || fours_aligned(p, a.dtype, t, h);
+    };
+    g.vec = aligned_rows(a.q, a.q_token_stride, a.q_head_stride, a.heads) &&
+            aligned_rows(a.k, a.k_token_stride, a.k_head_stride, a.kv_heads) &&
+            aligned_rows(a.q_out, a.q_out_token_stride, a.q_out_head_stride, a.heads) &&
+            aligned_rows(a.k_out, a.k_out_token_stride, a.k_out_head_stride, a.kv_heads) &&
+            reinterpret_cast<uintptr_t>(a.q_weight) % 16 == 0 && reinterpret_cast<uintptr_t>(a.k_weight) % 16 == 0;
     g.status = c.status_word;
     return g;
 }
@@ -327,8 +433,8 @@ cudaError_t norm_rope_backward_launch(const q4lin_norm_rope_backward_t& b, const
     g.dq = b.d_q_out, g.dk = b.d_k_out;
     g.dq_token = b.d_q_out_token_stride, g.dq_head = b.d_q_out_head_stride;
     g.dk_token = b.d_k_out_token_stride, g.dk_head = b.d_k_out_head_stride;
-    g.dq_vec = fours_aligned(g.dq, g.a.dtype, g.dq_token, g.dq_head);
-    g.dk_vec = fours_aligned(g.dk, g.a.dtype, g.dk_token, g.dk_head);
+    g.vec = g.vec && (g.a.heads == 0 || fours_aligned(g.dq, g.a.dtype, g.dq_token, g.dq_head)) &&
+            (g.a.kv_heads == 0 || fours_aligned(g.dk, g.a.dtype, g.dk_token, g.dk_head));
     if (g.a.head_dim == 64) return backward_typed<64>(g, b.d_q_weight, b.d_k_weight, c);
     if (g.a.head_dim == 128) return backward_typed<128>(g, b.d_q_weight, b.d_k_weight, c);
     return backward_typed<256>(g, b.d_q_weight, b.d_k_weight, c);
