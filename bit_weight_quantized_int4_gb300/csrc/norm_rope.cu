@@ -18,8 +18,9 @@ using namespace ptx;
 using namespace serving;
 
 // Passes in flight of a warp, as many as registers leave warps for (8192 tokens of 40 heads of 128 in
-// bf16: forward 1 / 2 / 3 / 4 passes 38.9, 34.2, 33.8, 35.0 us).
-constexpr int kAhead = 3, kBackAhead = 4;
+// bf16: forward 2 / 3 / 4 passes 33.3, 32.8, 31.8 us; backward with two CTAs an SM 54.6 us, with three,
+// whose registers hold less, 92 and up).
+constexpr int kAhead = 4, kBackAhead = 4, kBackCtas = 2;
 constexpr int kWarps = 4, kBackWarps = 8;
 
 struct NormArgs {
@@ -74,21 +75,38 @@ __device__ __forceinline__ void scale_by(Eight& x, float f) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x.v[e] = fmul2(x.v[e], make_float2(f, f));
 }
-// x becomes u = x r; the result is r.  Where the squares pass fp32's range, x is scaled by 2^-70
-// first (whole warp: the sums need every lane).
+// Sums of x x and of x y.
+template <int U>
+__device__ __forceinline__ float2 two_sums(const Eight& x, const Eight& y) {
+    float2 a = fmul2(x.v[0], x.v[0]), b = fmul2(x.v[0], y.v[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) a = ffma2(x.v[e], x.v[e], a), b = ffma2(x.v[e], y.v[e], b);
+    float2 v = make_float2(a.x + a.y, b.x + b.y);
+#pragma unroll
+    for (int o = U / 2; o; o >>= 1)
+        v = fadd2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+    return v;
+}
+// r = 1 / sqrt(sum / D + eps) of a row whose squares add up to `sum`.  Where they pass fp32's range, x is
+// scaled by 2^-70 first (whole warp: the sums need every lane): r is then that of the scaled x, *back
+// what it was scaled by, and *mean the mean of x y anew.
 template <int D>
-__device__ __forceinline__ float normalise(Eight& x, float eps) {
-    const float sum = dot<D / 8>(x, x);
-    float r = rsqrtf(fmaf(sum, 1.f / D, eps)), back = 1.f;
+__device__ __forceinline__ void scales_of(Eight& x, const Eight& y, float sum, float eps, float* mean, float* r, float* back) {
+    *r = rsqrtf(fmaf(sum, 1.f / D, eps)), *back = 1.f;
     if (__any_sync(0xffffffffu, sum > 3e38f)) {
         constexpr float kDown = 8.470329472543003e-22f;  // 2^-70
         const bool far = sum > 3e38f;
         if (far) scale_by(x, kDown);
-        const float again = dot<D / 8>(x, x);
-        if (far) r = rsqrtf(fmaf(again, 1.f / D, eps * kDown * kDown)), back = kDown;
+        const float2 again = two_sums<D / 8>(x, y);
+        if (far) *r = rsqrtf(fmaf(again.x, 1.f / D, eps * kDown * kDown)), *back = kDown, *mean = again.y * (1.f / D);
     }
+}
+// x becomes x r.
+template <int D>
+__device__ __forceinline__ void normalise(Eight& x, float eps) {
+    float r, back, mean;
+    scales_of<D>(x, x, dot<D / 8>(x, x), eps, &mean, &r, &back);
     scale_by(x, r);
-    return r * back;
 }
 template <bool VEC>
 __device__ __forceinline__ Eight load_weight(const float* w, int lo, int hi) {
@@ -108,26 +126,26 @@ template <int DT, bool VEC>
 struct Raw {
     uint2 w[DT == Q4LIN_DTYPE_F32 ? 4 : 2];
 
-    __device__ __forceinline__ void load(const void* p, int64_t lo, int64_t hi) {
-        if constexpr (DT == Q4LIN_DTYPE_F32) {
+    // Groups at p + lo and p + hi (bytes); zeros where the lane has no row.
+    __device__ __forceinline__ void load(const char* p, int lo, int hi, bool in) {
+        constexpr int kGroup = DT == Q4LIN_DTYPE_F32 ? 2 : 1;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const uint32_t* f = static_cast<const uint32_t*>(p) + (g ? hi : lo);
-                if constexpr (VEC) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(f);
-                    w[2 * g] = make_uint2(v.x, v.y), w[2 * g + 1] = make_uint2(v.z, v.w);
-                } else {
-                    w[2 * g] = make_uint2(f[0], f[1]), w[2 * g + 1] = make_uint2(f[2], f[3]);
-                }
-            }
-        } else {
+        for (int g = 0; g < 2; ++g) {
+            const char* from = p + (g ? hi : lo);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const unsigned short* b = static_cast<const unsigned short*>(p) + (g ? hi : lo);
-                if constexpr (VEC)
-                    w[g] = *reinterpret_cast<const uint2*>(b);
-                else
-                    w[g] = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+            for (int e = 0; e < kGroup; ++e) w[g * kGroup + e] = make_uint2(0u, 0u);
+            if (!in) continue;
+            if constexpr (VEC && DT == Q4LIN_DTYPE_F32) {
+                const uint4 v = *reinterpret_cast<const uint4*>(from);
+                w[2 * g] = make_uint2(v.x, v.y), w[2 * g + 1] = make_uint2(v.z, v.w);
+            } else if constexpr (VEC) {
+                w[g] = *reinterpret_cast<const uint2*>(from);
+            } else if constexpr (DT == Q4LIN_DTYPE_F32) {
+                const uint32_t* f = reinterpret_cast<const uint32_t*>(from);
+                w[2 * g] = make_uint2(f[0], f[1]), w[2 * g + 1] = make_uint2(f[2], f[3]);
+            } else {
+                const unsigned short* b = reinterpret_cast<const unsigned short*>(from);
+                w[g] = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
             }
         }
     }
@@ -182,10 +200,10 @@ __device__ __forceinline__ Angles angles_of(const q4lin_rope_t& r, int64_t posit
             {make_float2(sign * s[0], sign * s[1]), make_float2(sign * s[2], sign * s[3])}};
 }
 template <int DT, bool VEC>
-__device__ __forceinline__ void store_row(void* p, int64_t at, int lo, int hi, const Eight& x) {
+__device__ __forceinline__ void store_row(char* p, int lo, int hi, const Eight& x) {
     const float y[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
-    store_four(p, DT, at + lo, VEC, y);
-    store_four(p, DT, at + hi, VEC, y + 4);
+    store_four(p + lo, DT, 0, VEC, y);
+    store_four(p + hi, DT, 0, VEC, y + 4);
 }
 
 // A part's heads: queries [q0, q1) and keys [k0, k1).
@@ -200,13 +218,14 @@ __device__ __forceinline__ Heads heads_of(const NormArgs& g, int part) {
 
 template <int D, int DT, int AHEAD, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormArgs g) {
-    constexpr int U = D / 8, R = 32 / U;
+    constexpr int U = D / 8, R = 32 / U, kSize = (int)dtype_size(DT);
     const int lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
     const int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (token >= g.a.tokens) return;
     bool turned, good = true, first = true;
     int lo, hi;
     rope_channels(g.a.rope, u, &turned, &lo, &hi);
+    const int lo_at = lo * kSize, hi_at = hi * kSize;
     const Heads heads = heads_of(g, blockIdx.y);
     Angles angles;
     auto rows = [&](auto keys) {
@@ -215,13 +234,15 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormArgs g
         const int end = (int)(decltype(keys)::value ? heads.k1 : heads.q1);
         if (begin >= end) return;
         Raw<DT, VEC> raw[AHEAD];
-        auto fetch = [&](Raw<DT, VEC>& r, int h0) {
-            const int64_t at = token * s.xt + min(h0 + sub, end - 1) * s.xh;
-            r.load(s.x, at + lo, at + hi);
+        const char* x_at = static_cast<const char*>(s.x) + (token * s.xt + (begin + sub) * s.xh) * kSize;
+        char* y_at = static_cast<char*>(s.y) + (token * s.yt + (begin + sub) * s.yh) * kSize;
+        const int64_t x_step = R * s.xh * kSize, y_step = R * s.yh * kSize;
+        auto fetch = [&](Raw<DT, VEC>& r, int h) {
+            r.load(x_at, lo_at, hi_at, h < end);
+            x_at += x_step;
         };
 #pragma unroll
-        for (int p = 0; p < AHEAD; ++p)
-            if (begin + p * R < end) fetch(raw[p], begin + p * R);
+        for (int p = 0; p < AHEAD; ++p) fetch(raw[p], begin + sub + p * R);
         const Eight w = load_weight<VEC>(s.w, lo, hi);
         if (first) {  // (behind the first rows' loads)
             const int64_t position = position_of(g, token, &good);
@@ -235,12 +256,13 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormArgs g
                 const int hp = h0 + p * R, h = hp + sub;
                 if (hp >= end) break;
                 Eight x = raw[p].unpack();
-                if (hp + AHEAD * R < end) fetch(raw[p], hp + AHEAD * R);
+                fetch(raw[p], h + AHEAD * R);
                 normalise<D>(x, g.a.eps);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x.v[e] = fmul2(x.v[e], w.v[e]);
                 if (turned) turn(g.a.rope, angles, x);
-                if (h < end && good) store_row<DT, VEC>(s.y, token * s.yt + h * s.yh, lo, hi, x);
+                if (h < end && good) store_row<DT, VEC>(y_at, lo_at, hi_at, x);
+                y_at += y_step;
             }
         }
     };
@@ -250,20 +272,22 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormArgs g
 
 // CTAs walk over tokens with the weights' sums in registers.
 template <int D, int DT, int AHEAD, bool VEC>
-__global__ void __launch_bounds__(32 * kBackWarps) norm_rope_backward_kernel(const NormArgs g) {
-    constexpr int U = D / 8, R = 32 / U;
+__global__ void __launch_bounds__(32 * kBackWarps, kBackCtas) norm_rope_backward_kernel(const NormArgs g) {
+    constexpr int U = D / 8, R = 32 / U, kSize = (int)dtype_size(DT);
     __shared__ float sums[kBackWarps * R][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
     griddep_launch_dependents();  // (the kernel that joins the sums waits for this one's end)
     bool turned;
     int lo, hi;
     rope_channels(g.a.rope, u, &turned, &lo, &hi);
+    const int lo_at = lo * kSize, hi_at = hi * kSize;
     const Heads heads = heads_of(g, blockIdx.y);
     auto rows = [&](auto keys) {
         constexpr bool kKeys = decltype(keys)::value;
         const Side s = side_of(g, kKeys);
         const int begin = (int)(kKeys ? heads.k0 : heads.q0), end = (int)(kKeys ? heads.k1 : heads.q1);
         const Eight w = load_weight<VEC>(s.w, lo, hi);
+        const int64_t x_step = R * s.xh * kSize, d_step = R * s.dh * kSize, y_step = R * s.yh * kSize;
         Eight dw;
 #pragma unroll
         for (int e = 0; e < 4; ++e) dw.v[e] = make_float2(0.f, 0.f);
@@ -271,15 +295,16 @@ __global__ void __launch_bounds__(32 * kBackWarps) norm_rope_backward_kernel(con
         for (int64_t token = (int64_t)blockIdx.x * kBackWarps + warp; token < g.a.tokens && begin < end;
              token += (int64_t)gridDim.x * kBackWarps) {
             Raw<DT, VEC> raw_x[AHEAD], raw_d[AHEAD];
-            auto fetch = [&](int p, int h0) {
-                const int h = min(h0 + sub, end - 1);
-                const int64_t at = token * s.xt + h * s.xh, dat = token * s.dt + h * s.dh;
-                raw_x[p].load(s.x, at + lo, at + hi);
-                raw_d[p].load(s.d, dat + lo, dat + hi);
+            const char* x_at = static_cast<const char*>(s.x) + (token * s.xt + (begin + sub) * s.xh) * kSize;
+            const char* d_at = static_cast<const char*>(s.d) + (token * s.dt + (begin + sub) * s.dh) * kSize;
+            char* y_at = static_cast<char*>(s.y) + (token * s.yt + (begin + sub) * s.yh) * kSize;
+            auto fetch = [&](int p, int h) {
+                raw_x[p].load(x_at, lo_at, hi_at, h < end);
+                raw_d[p].load(d_at, lo_at, hi_at, h < end);
+                x_at += x_step, d_at += d_step;
             };
 #pragma unroll
-            for (int p = 0; p < AHEAD; ++p)
-                if (begin + p * R < end) fetch(p, begin + p * R);
+            for (int p = 0; p < AHEAD; ++p) fetch(p, begin + sub + p * R);
             Angles angles;
             bool good;
             const int64_t position = position_of(g, token, &good);  // (behind the first rows' loads)
@@ -292,20 +317,27 @@ __global__ void __launch_bounds__(32 * kBackWarps) norm_rope_backward_kernel(con
                     if (hp >= end) break;
                     const bool in = h < end && good;
                     Eight x = raw_x[p].unpack(), d = raw_d[p].unpack();
-                    if (hp + AHEAD * R < end) fetch(p, hp + AHEAD * R);
-                    const float r = normalise<D>(x, g.a.eps);
+                    fetch(p, h + AHEAD * R);
                     if (turned) turn(g.a.rope, angles, d);
+                    Eight gw;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) gw.v[e] = fmul2(d.v[e], w.v[e]);
+                    // Both sums at once; with u = x r, the second is that of g w u over r.
+                    float r, back;
+                    const float2 both = two_sums<U>(x, gw);
+                    float mean = both.y * (1.f / D);
+                    scales_of<D>(x, gw, both.x, g.a.eps, &mean, &r, &back);
+                    scale_by(x, r);
+                    mean *= -r;
                     if (in) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) dw.v[e] = ffma2(d.v[e], x.v[e], dw.v[e]);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d.v[e] = fmul2(d.v[e], w.v[e]);
-                    const float mean = dot<U>(d, x) * (-1.f / D);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x.v[e] = ffma2(x.v[e], make_float2(mean, mean), d.v[e]);
-                    scale_by(x, r);
-                    if (in) store_row<DT, VEC>(s.y, token * s.yt + h * s.yh, lo, hi, x);
+                    for (int e = 0; e < 4; ++e) x.v[e] = ffma2(x.v[e], make_float2(mean, mean), gw.v[e]);
+                    scale_by(x, r * back);
+                    if (in) store_row<DT, VEC>(y_at, lo_at, hi_at, x);
+                    y_at += y_step;
                 }
             }
         }
@@ -368,7 +400,7 @@ cudaError_t forward(NormArgs& g, const LaunchCtx& c) {
 template <int D, int DT>
 cudaError_t backward(NormArgs& g, float* dqw, float* dkw, const LaunchCtx& c) {
     const unsigned parts = parts_of(g, 32 / (D / 8), 16 * c.sm_count);
-    const int64_t most = std::max<int64_t>(1, 2 * c.sm_count / parts);
+    const int64_t most = std::max<int64_t>(1, kBackCtas * c.sm_count / parts);
     const dim3 grid((unsigned)std::min((g.a.tokens + kBackWarps - 1) / kBackWarps, most), parts);
     const int64_t ctas = (int64_t)grid.x * grid.y;
     if (2 * ctas * D > c.ws_floats) return cudaErrorInvalidValue;
