@@ -16,8 +16,10 @@
 // The pages' scales stay out of the operands: a key page's multiplies its columns of S, a
 // value page's (over the largest of the walk) joins the exponent of its weights.  O is
 // only rescaled when a row's maximum has grown by 2^8 since the last time, which fp16's range
-// leaves room for.  4-bit codes have a scale for each token: a key's multiplies its column of S,
-// and a value's (over the largest of the walk) its weights, 128 of each read from shared memory.
+// leaves room for.  4-bit codes have a scale for each token: a key's multiplies its column of S, read
+// from shared memory by every softmax warp.  A value's (over the largest of the walk) multiplies
+// its weights in the same way where those have two terms; for bf16 outputs, where they have one,
+// code - 8 times the scale is rounded to fp16 once as it is widened (11 bits as the weight's).
 // Queries and weights enter as QT and PT fp16 terms, the rounded value and
 // what the rounding left (22 bits), each term a product of its own: two of both in general; a
 // weight of a bf16 output takes one (its 11 bits are finer than the output's 8), and bf16
@@ -80,6 +82,8 @@ constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp
 constexpr float kUnbase = 1.f / 128.f;
 // A score's factor is at least this, so that a masked score (-infinity) stays one.
 constexpr float kLeastFactor = 1e-37f;
+// (4 bits) Weights of a step that add up to no more than this are below fp16's 65504 each.
+constexpr float kMostSum = 65000.f;
 constexpr float kLeastRatio = 5.421010862427522e-20f;  // 2^-64
 constexpr int64_t kDrainNs = 4000000000LL;
 constexpr uint32_t kTmemCols = 512;
@@ -136,14 +140,14 @@ __device__ __forceinline__ float* part_at(const PromptArgs& g, int64_t unit) {
 // Shared memory.  A step's K tile is D / 64 blocks of 64 channels, its V tile two blocks of 64
 // keys; both come and go by block through rings, as much as fits (three of each beside 128
 // channels of two terms: half a tile is widened while the other's products run).
-template <int D, int QT, int BITS>
+template <int D, int QT, bool KEYED>
 struct Layout {
     static constexpr int kBlock = 128 * 128;           // 128 rows of 128 bytes
     static constexpr int kBlocks = D / 64;             // of a Q or K tile
     static constexpr int vBlock = D * 128;
     static constexpr bool kTight = QT == 2 && D == 128;
-    // (The scales of 4-bit codes take the place of a block of values.)
-    static constexpr int kRing = kTight ? 3 : 4, vRing = kTight && BITS == 4 ? 2 : kRing;
+    // (KEYED: scales of each key and value take the place of a block of values.)
+    static constexpr int kRing = kTight ? 3 : 4, vRing = kTight && KEYED ? 2 : kRing;
     static constexpr uint32_t q = 0;                                  // [tile][term][block]
     static constexpr uint32_t k = q + 2 * QT * kBlocks * kBlock;      // [slot]
     static constexpr uint32_t v = k + kRing * kBlock;                 // [slot]
@@ -162,25 +166,25 @@ struct Job {
 };
 
 // Scales of the steps between widening and softmax.  8 bits: of 16 keys each, with the values' as
-// logarithms and inverses; 4 bits: of each key, the values' as ratios.  K blocks of up to two steps
+// logarithms and inverses; KEYED: of each key, the values' as ratios.  K blocks of up to two steps
 // more are widened while a step's scores are read, of four with 64 channels (kScaleSlots).
-template <int D, int BITS>
+template <int D, bool KEYED>
 struct StepScales {
     static constexpr int kSlots = kScaleSlots;
     float k_scale[kSlots][8], v_log[kSlots][8], v_inv[kSlots][8];
 };
 template <int D>
-struct StepScales<D, 4> {
+struct StepScales<D, true> {
     static constexpr int kSlots = D == 64 ? kScaleSlots : 3;
     alignas(16) float k_scale[kSlots][kKeys];
     alignas(16) float v_ratio[kSlots][kKeys];
 };
 
-template <int D, int BITS>
+template <int D, bool KEYED>
 struct PromptShared {
     Job job;
     float factor[2 * kQ];
-    StepScales<D, BITS> scales;
+    StepScales<D, KEYED> scales;
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2];
     float v_max[kWarps];
     int failed;
@@ -243,6 +247,20 @@ __device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t* r) {
         : "r"(addr)
         : "memory");
 }
+// 32 columns of this warp's lanes, without waiting; and the wait for them, which the registers go
+// through so that no use of them is scheduled before it.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
 // `bytes` from shared to global memory, both 16-byte aligned, and until they have been read.
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
     asm volatile(
@@ -281,6 +299,12 @@ __device__ __forceinline__ void ld_codes(const uint8_t* p, uint4& v) {
 __device__ __forceinline__ void ld_word(const uint8_t* p, uint32_t& v) {
     asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
 }
+// Pairs times pairs of scales of two terms, rounded once to fp16 (but for the lower term's product).
+__device__ __forceinline__ uint32_t scaled_f16(uint32_t x, uint32_t hi, uint32_t lo) {
+    const __half2 v = *reinterpret_cast<const __half2*>(&x);
+    const __half2 y = __hfma2(v, *reinterpret_cast<const __half2*>(&hi), __hmul2(v, *reinterpret_cast<const __half2*>(&lo)));
+    return *reinterpret_cast<const uint32_t*>(&y);
+}
 // Byte of 16-byte chunk `chunk` of row `row` in a 128-byte-swizzled block.
 __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
     return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
@@ -291,7 +315,7 @@ __device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
 template <int D, int QT, int DT, int BITS>
 __device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, float* factor, int64_t o0, int h,
                                          int tq, int len, int row0, int row_end) {
-    using L = Layout<D, QT, BITS>;
+    using L = Layout<D, QT, false>;  // (where the queries are is the same with KEYED)
     const int tid = threadIdx.x, group = (int)(g.a.heads / g.cache.kv_heads);
     constexpr int kUnitsRow = D / 8, kPer = kThreads / kUnitsRow;  // 16 or 8 lanes a row
     const int u = tid % kUnitsRow;
@@ -382,9 +406,7 @@ __device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, fl
                                 make_uint2(lo[2 * w], lo[2 * w + 1]);
                     }
                 }
-                // (Not so small that a masked score would not stay -infinity; 8 bits: with the scale below.)
-                const float f = fabsf(g.a.scale) * kLog2e * down;
-                if (u == 0) factor[r] = BITS == 4 ? fmaxf(f, kLeastFactor) : f;
+                if (u == 0) factor[r] = fabsf(g.a.scale) * kLog2e * down;
             }
         }
     }
@@ -521,9 +543,11 @@ __device__ __forceinline__ void add_16(float* to, uint32_t (&y)[16], float keep,
 
 template <int D, int QT, int PT, int DT, int DRAIN, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const PromptArgs g) {
-    using L = Layout<D, QT, BITS>;
+    constexpr bool kKeyed = BITS == 4, kFolded = BITS == 4 && PT == 1;  // what becomes of scales
+    using L = Layout<D, QT, kKeyed>;
+    using Scales = StepScales<D, kKeyed>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ PromptShared<D, BITS> S;
+    __shared__ PromptShared<D, kKeyed> S;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
     const q4lin_kv_cache_t& C = g.cache;
@@ -577,13 +601,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         else if constexpr (BITS == 8)
             v_max = fmaxf(v_max, __ldg(C.v_scales + (int64_t)id * Hkv + h));
         else {
-            const float* s = C.v_scales + (((int64_t)id * Hkv + h) << ps);
+            const int64_t at = ((int64_t)id * Hkv + h) << ps;
             const int left = len - (p << ps);  // (what is behind the sequence may be anything)
+            auto largest = [&](const float* s, int e, float old) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(s + at + e));
+                return fmaxf(old, fmaxf(fmaxf(e < left ? v.x : 0.f, e + 1 < left ? v.y : 0.f),
+                                        fmaxf(e + 2 < left ? v.z : 0.f, e + 3 < left ? v.w : 0.f)));
+            };
 #pragma unroll 4
             for (int e = 0; e < 1 << ps; e += 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(s + e));
-                v_max = fmaxf(v_max, fmaxf(fmaxf(e < left ? v.x : 0.f, e + 1 < left ? v.y : 0.f),
-                                           fmaxf(e + 2 < left ? v.z : 0.f, e + 3 < left ? v.w : 0.f)));
+                v_max = largest(C.v_scales, e, v_max);
             }
         }
     }
@@ -603,10 +630,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     auto first_drain = [&]() {
         return DRAIN > 0 && (DT == Q4LIN_DTYPE_F32 || job.cut || job.slot >= 0) ? DRAIN : INT_MAX;
     };
-    auto value_ref = [&]() {  // the largest value scale of the walk
+    // What the values' scales are taken relative to: the largest of the walk, folded ones a power of
+    // two that brings it to [2^11, 2^12), so that codes times scales fill fp16's range.
+    auto value_ref = [&]() {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v = fmaxf(v, const_cast<volatile float&>(S.v_max[w]));
+        if constexpr (kFolded) return __uint_as_float(min(max((int)(__float_as_uint(v) >> 23) - 11, 1), 253) << 23);
         return v > 0.f ? v : 1.f;  // 1: values that are all zero
     };
     volatile int* failed = &S.failed;
@@ -638,7 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const int token = row / group, position = len - tq + token;
         const int limit = !in ? -1 : g.a.causal ? position : len - 1;
         const int low = g.a.window > 0 ? (int)max((int64_t)0, (int64_t)position - g.a.window + 1) : 0;
-        const float factor = S.factor[r];
+        // (4 bits: not so small that a masked score would not stay -infinity; 8 bits: with the scale below.)
+        float factor = S.factor[r];
+        if constexpr (BITS == 4) factor = fmaxf(factor, kLeastFactor);
         int drain = first_drain();
         float m = -INFINITY, l = 0.f, m_out = -INFINITY;  // m_out: of what was taken out
         bool ok = true;
@@ -647,106 +679,189 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             ok = __all_sync(0xffffffffu, wait(S.s_full[tile], i & 1));
             if (!ok) break;
             tc_fence_after();
-            const int key0 = (step0 + i) * kKeys, slot = i % StepScales<D, BITS>::kSlots;
+            const int key0 = (step0 + i) * kKeys, slot = i % Scales::kSlots;
             const int hi = min(limit - key0, kKeys), lo = max(low - key0, 0);
-            uint32_t x[kKeys];
-            tmem_ld64(s_at, x);
-            tmem_ld64(s_at + 64, x + 64);
-            if constexpr (BITS == 4) {
+            if constexpr (kFolded) {
+                // The scores in quarters, the next one on its way.  The weights by the maximum that there
+                // is: as long as their sum stays in fp16's range, so does each of them, and no maximum is
+                // looked for.  They wait in registers until that is known; rows that have seen nothing yet
+                // and those whose sum has grown too far (each for itself) get a new maximum first.
                 const float4* ks = reinterpret_cast<const float4*>(S.scales.k_scale[slot]);
+                const float2 factor2 = make_float2(factor, factor), least2 = make_float2(kLeastFactor, kLeastFactor);
+                const bool masked = __any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0);
+                auto quarters = [&](auto&& take) {  // take(quarter, its 32 scores)
+                    uint32_t x[2][32];
+                    tmem_ld32_async(s_at, x[0]);
 #pragma unroll
-                for (int e = 0; e < kKeys / 4; ++e) {
-                    const float4 s = ks[e];
-                    const float2 a = fmul2(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), make_float2(s.x, s.y));
-                    const float2 b = fmul2(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), make_float2(s.z, s.w));
-                    x[4 * e] = __float_as_uint(a.x), x[4 * e + 1] = __float_as_uint(a.y);
-                    x[4 * e + 2] = __float_as_uint(b.x), x[4 * e + 3] = __float_as_uint(b.y);
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld32(x[c % 2]);
+                        if (c < 3) tmem_ld32_async(s_at + 32 * (c + 1), x[(c + 1) % 2]);
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * c + e > hi || 32 * c + e < lo) x[c % 2][e] = 0xFF800000u;
+                        }
+                        take(c, x[c % 2]);
+                    }
+                };
+                auto column_factors = [&](int e, float2& a, float2& b) {  // of columns 4 e .. 4 e + 3
+                    const float4 k = ks[e];
+                    a = ffma2(make_float2(k.x, k.y), factor2, least2), b = ffma2(make_float2(k.z, k.w), factor2, least2);
+                };
+                uint32_t p[kKeys / 2];
+                float2 sum;
+                bool need = in && m == -INFINITY;
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    if (__any_sync(0xffffffffu, need)) {
+                        float top = -INFINITY;
+                        quarters([&](int c, const uint32_t (&x)[32]) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float2 a, b;
+                                column_factors(8 * c + e, a, b);
+                                a = fmul2(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), a);
+                                b = fmul2(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), b);
+                                top = max3(max3(top, a.x, a.y), b.x, b.y);
+                            }
+                        });
+                        const float now = need ? fmaxf(m, top) : m, alpha = now == -INFINITY ? 1.f : ex2(m - now);
+                        m = now, l *= alpha;
+                        if (i > 0) {
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t y[16];
+                                tmem_ld16(o_at + 16 * c, y);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+                                tmem_st16_async(o_at + 16 * c, y);
+                            }
+                        }
+                    }
+                    const float origin = kBase - (m == -INFINITY ? 0.f : m);
+                    const float2 off2 = make_float2(origin, origin);
+                    sum = make_float2(0.f, 0.f);
+                    quarters([&](int c, const uint32_t (&x)[32]) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float2 w[2];
+                            column_factors(8 * c + e, w[0], w[1]);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                w[h] = ffma2(make_float2(__uint_as_float(x[4 * e + 2 * h]), __uint_as_float(x[4 * e + 2 * h + 1])), w[h], off2);
+                                w[h].x = ex2(w[h].x), w[h].y = ex2(w[h].y);
+                                sum = fadd2(sum, w[h]);
+                                const __half2 v = __floats2half2_rn(w[h].x, w[h].y);
+                                p[16 * c + 2 * e + h] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                        }
+                    });
+                    need = sum.x + sum.y > kMostSum;
+                    if (!__any_sync(0xffffffffu, need)) break;
                 }
-            }
-            // Columns [lo, hi] of the step are seen; all of them in most steps.
-            if (__any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0)) {
+                l += sum.x + sum.y;
 #pragma unroll
-                for (int e = 0; e < kKeys; ++e)
-                    if (e > hi || e < lo) x[e] = 0xFF800000u;
-            }
-            float top = -INFINITY;
+                for (int c = 0; c < 8; ++c) tmem_st8_async(s_at + 8 * c, *reinterpret_cast<uint32_t(*)[8]>(p + 8 * c));
+            } else {
+                uint32_t x[kKeys];
+                tmem_ld64(s_at, x);
+                tmem_ld64(s_at + 64, x + 64);
+                if constexpr (kKeyed) {
+                    const float4* ks = reinterpret_cast<const float4*>(S.scales.k_scale[slot]);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                float mx = max3(__uint_as_float(x[16 * c]), __uint_as_float(x[16 * c + 1]), __uint_as_float(x[16 * c + 2]));
+                    for (int e = 0; e < kKeys / 4; ++e) {
+                        const float4 s = ks[e];
+                        const float2 a = fmul2(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), make_float2(s.x, s.y));
+                        const float2 b = fmul2(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), make_float2(s.z, s.w));
+                        x[4 * e] = __float_as_uint(a.x), x[4 * e + 1] = __float_as_uint(a.y);
+                        x[4 * e + 2] = __float_as_uint(b.x), x[4 * e + 3] = __float_as_uint(b.y);
+                    }
+                }
+                // Columns [lo, hi] of the step are seen; all of them in most steps.
+                if (__any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0)) {
 #pragma unroll
-                for (int e = 3; e < 15; e += 2)
-                    mx = max3(mx, __uint_as_float(x[16 * c + e]), __uint_as_float(x[16 * c + e + 1]));
-                mx = fmaxf(mx, __uint_as_float(x[16 * c + 15]));
-                if constexpr (BITS == 8)
-                    top = fmaxf(top, mx * fmaxf(factor * S.scales.k_scale[slot][c], kLeastFactor));
-                else
-                    top = fmaxf(top, mx);
-            }
-            if constexpr (BITS == 4) top *= factor;
-            if (__any_sync(0xffffffffu, top > m + kSlack)) {
-                // Some row's maximum grew too far: O and l over to the new one.  (The product
-                // that read the last weights is complete: this step's scores came after it.)
-                const float now = fmaxf(m, top);
-                const float alpha = now == -INFINITY ? 1.f : ex2(m - now);
-                m = now, l *= alpha;
-                if (i > 0) {
+                    for (int e = 0; e < kKeys; ++e)
+                        if (e > hi || e < lo) x[e] = 0xFF800000u;
+                }
+                float top = -INFINITY;
 #pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float mx = max3(__uint_as_float(x[16 * c]), __uint_as_float(x[16 * c + 1]), __uint_as_float(x[16 * c + 2]));
+#pragma unroll
+                    for (int e = 3; e < 15; e += 2)
+                        mx = max3(mx, __uint_as_float(x[16 * c + e]), __uint_as_float(x[16 * c + e + 1]));
+                    mx = fmaxf(mx, __uint_as_float(x[16 * c + 15]));
+                    if constexpr (BITS == 8)
+                        top = fmaxf(top, mx * fmaxf(factor * S.scales.k_scale[slot][c], kLeastFactor));
+                    else
+                        top = fmaxf(top, mx);
+                }
+                if constexpr (BITS == 4) top *= factor;
+                if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                    // Some row's maximum grew too far: O and l over to the new one.  (The product
+                    // that read the last weights is complete: this step's scores came after it.)
+                    const float now = fmaxf(m, top);
+                    const float alpha = now == -INFINITY ? 1.f : ex2(m - now);
+                    m = now, l *= alpha;
+                    if (i > 0) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t y[16];
+                            tmem_ld16(o_at + 16 * c, y);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+                            tmem_st16_async(o_at + 16 * c, y);
+                        }
+                    }
+                }
+                if (DRAIN > 0 && i == drain) {
+                    drain += DRAIN;
+                    tmem_wait_st();  // O may just have been rescaled; loads do not wait for stores
+                    float* to = out_row<D, DT>(g, job, row, r);
+                    const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
+#pragma unroll DT == Q4LIN_DTYPE_F32 ? 4 : 8
                     for (int c = 0; c < D / 16; ++c) {
                         uint32_t y[16];
+                        __syncwarp();  // the load is the whole warp's
                         tmem_ld16(o_at + 16 * c, y);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
-                        tmem_st16_async(o_at + 16 * c, y);
+                        if (in) add_16(to + 16 * c, y, keep, i > DRAIN, true);
                     }
+                    __syncwarp();
+                    m_out = m;
                 }
-            }
-            if (DRAIN > 0 && i == drain) {
-                drain += DRAIN;
-                tmem_wait_st();  // O may just have been rescaled; loads do not wait for stores
-                float* to = out_row<D, DT>(g, job, row, r);
-                const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
-#pragma unroll DT == Q4LIN_DTYPE_F32 ? 4 : 8
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t y[16];
-                    __syncwarp();  // the load is the whole warp's
-                    tmem_ld16(o_at + 16 * c, y);
-                    if (in) add_16(to + 16 * c, y, keep, i > DRAIN, true);
-                }
-                __syncwarp();
-                m_out = m;
-            }
-            const float origin = kBase - (m == -INFINITY ? 0.f : m);
+                const float origin = kBase - (m == -INFINITY ? 0.f : m);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                float f = factor, off = origin;
-                if constexpr (BITS == 8)
-                    f = fmaxf(factor * S.scales.k_scale[slot][c], kLeastFactor), off = origin + S.scales.v_log[slot][c];
-                const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-                float2 sum = make_float2(0.f, 0.f);
-                float4 ratio = make_float4(0.f, 0.f, 0.f, 0.f);
-                uint32_t p[8], rest[8];
+                for (int c = 0; c < 8; ++c) {
+                    float f = factor, off = origin;
+                    if constexpr (BITS == 8)
+                        f = fmaxf(factor * S.scales.k_scale[slot][c], kLeastFactor), off = origin + S.scales.v_log[slot][c];
+                    const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+                    float2 sum = make_float2(0.f, 0.f);
+                    [[maybe_unused]] float4 ratio = make_float4(0.f, 0.f, 0.f, 0.f);
+                    uint32_t p[8], rest[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float2 y = ffma2(make_float2(__uint_as_float(x[16 * c + 2 * e]), __uint_as_float(x[16 * c + 2 * e + 1])), f2, off2);
-                    y.x = ex2(y.x), y.y = ex2(y.y);
-                    sum = fadd2(sum, y);
-                    if constexpr (BITS == 4) {
-                        if (e % 2 == 0) ratio = *reinterpret_cast<const float4*>(&S.scales.v_ratio[slot][16 * c + 2 * e]);
-                        y = fmul2(y, e % 2 ? make_float2(ratio.z, ratio.w) : make_float2(ratio.x, ratio.y));
+                    for (int e = 0; e < 8; ++e) {
+                        float2 y = ffma2(make_float2(__uint_as_float(x[16 * c + 2 * e]), __uint_as_float(x[16 * c + 2 * e + 1])), f2, off2);
+                        y.x = ex2(y.x), y.y = ex2(y.y);
+                        sum = fadd2(sum, y);
+                        if constexpr (kKeyed) {
+                            if (e % 2 == 0) ratio = *reinterpret_cast<const float4*>(&S.scales.v_ratio[slot][16 * c + 2 * e]);
+                            y = fmul2(y, e % 2 ? make_float2(ratio.z, ratio.w) : make_float2(ratio.x, ratio.y));
+                        }
+                        if (PT == 2) {
+                            split_f16(y.x, y.y, &p[e], &rest[e]);
+                        } else {
+                            const __half2 v = __floats2half2_rn(y.x, y.y);
+                            p[e] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
                     }
-                    if (PT == 2) {
-                        split_f16(y.x, y.y, &p[e], &rest[e]);
-                    } else {
-                        const __half2 v = __floats2half2_rn(y.x, y.y);
-                        p[e] = *reinterpret_cast<const uint32_t*>(&v);
-                    }
+                    if constexpr (BITS == 8)
+                        l = fmaf(sum.x + sum.y, S.scales.v_inv[slot][c], l);
+                    else
+                        l += sum.x + sum.y;
+                    tmem_st8_async(s_at + 8 * c, p);  // over the scores
+                    if (PT == 2) tmem_st8_async(s_at + 64 + 8 * c, rest);
                 }
-                if constexpr (BITS == 8)
-                    l = fmaf(sum.x + sum.y, S.scales.v_inv[slot][c], l);
-                else
-                    l += sum.x + sum.y;
-                tmem_st8_async(s_at + 8 * c, p);  // over the scores
-                if (PT == 2) tmem_st8_async(s_at + 64 + 8 * c, rest);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -828,8 +943,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const int n = job.n, step0 = job.step0, pages = (job.len + (1 << ps) - 1) >> ps;
         const int page_low = job.page_low;
         const int32_t* table = C.page_table + job.b * C.table_stride;
-        const float v_ref = value_ref();
         const bool keys = warp < kValueWarp;
+        const float ref = value_ref();
         const int t = tid & 127;
         // One ring each, a step's blocks in the order of their use.
         auto walk = [&](auto&& widen) {
@@ -854,7 +969,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             // 8 channels (t / 8) of 8 keys (t % 8), so that stores of a channel lie on all banks.
             [[maybe_unused]] const int count = keys ? 4 : D / 32;  // (8 bits) pieces per thread and block
             const uint32_t page_bytes = (uint32_t)(D * BITS / 8) << ps;
+            [[maybe_unused]] const float inverse = 1.f / ref;
             uint4 reg[BITS == 4 ? 2 : 4];
+            [[maybe_unused]] float scale[kFolded ? 8 : 1];  // of the eight values
             int pages_now = fetch_pages(0), pages_next = fetch_pages(1);
             auto load = [&](int page_ids, int blk) {
                 if constexpr (BITS == 4) {
@@ -882,6 +999,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                             for (int j = 0; j < 8; ++j) ld_word(from + j * kRow, w[j]);
                         }
                         reg[0] = make_uint4(w[0], w[1], w[2], w[3]), reg[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        if constexpr (kFolded) {
+                            uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                            if (page >= 0) {
+                                const uint8_t* from = reinterpret_cast<const uint8_t*>(C.v_scales + ((int64_t)page << ps) + (key & (1u << ps) - 1));
+                                ld_codes(from, a);
+                                ld_codes(from + 16, b);
+                            }
+                            const uint32_t s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) scale[j] = __uint_as_float(s[j]);
+                        }
                     }
                 } else {
 #pragma unroll
@@ -902,7 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                     }
                 }
             };
-            auto store = [&](uint32_t to) {
+            // (first: the block's first key, for scales that are behind the sequence.)
+            auto store = [&](uint32_t to, [[maybe_unused]] int first) {
                 if constexpr (BITS == 4) {
                     if (keys) {
 #pragma unroll
@@ -919,12 +1048,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                         // Halves of the words of neighbouring keys side by side: their nibbles are the
                         // same four channels.
                         const uint32_t w[8] = {reg[0].x, reg[0].y, reg[0].z, reg[0].w, reg[1].x, reg[1].y, reg[1].z, reg[1].w};
+                        [[maybe_unused]] uint32_t hi[4], lo[4];
+                        if constexpr (kFolded) {
+                            const int left = job.len - first - t % 8 * 8;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                split_f16(2 * j < left ? scale[2 * j] * inverse : 0.f,
+                                          2 * j + 1 < left ? scale[2 * j + 1] * inverse : 0.f, &hi[j], &lo[j]);
+                        }
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             uint32_t f[4][4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
+                            for (int j = 0; j < 4; ++j) {
                                 nibbles_f16(prmt(w[2 * j], w[2 * j + 1], half ? 0x7632u : 0x5410u), f[0][j], f[1][j], f[2][j], f[3][j]);
+                                if constexpr (kFolded) {
+#pragma unroll
+                                    for (int n = 0; n < 4; ++n) f[n][j] = scaled_f16(f[n][j], hi[j], lo[j]);
+                                }
+                            }
 #pragma unroll
                             for (int n = 0; n < 4; ++n)
                                 st_shared_v4(to + swizzled(t / 8 * 8 + half * 4 + n, t % 8), f[n][0], f[n][1], f[n][2], f[n][3]);
@@ -960,13 +1102,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                     // (With the keys: the softmax needs both scales once the scores are there.)
                     const bool scales = keys && blk == 0 && (BITS == 4 || t < 8);
                     float ks = 0.f, vs = 0.f;
-                    if constexpr (BITS == 4) {
+                    if constexpr (kKeyed) {
                         // Key t of the step; 0 for those behind the sequence and before the window.
                         if (keys && blk == 0) {
                             const int page = __shfl_sync(0xffffffffu, pages_now, t / 16), key = (step0 + i) * kKeys + t;
                             if (page >= 0 && key < job.len) {
                                 const int64_t at = ((int64_t)page << ps) + (key & (1 << ps) - 1);
-                                ks = __ldg(C.k_scales + at), vs = __ldg(C.v_scales + at);
+                                ks = __ldg(C.k_scales + at);
+                                if constexpr (!kFolded) vs = __ldg(C.v_scales + at);
                             }
                         }
                     } else if (scales && pages_now >= 0) {
@@ -975,15 +1118,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                     if (!__all_sync(0xffffffffu, wait(empty[slot], par))) return;
                     if (scales) {
                         // Far below fp16's range a weight is 0 in the product; in l it counts.
-                        const int at = i % StepScales<D, BITS>::kSlots;
-                        if constexpr (BITS == 4) {
-                            S.scales.k_scale[at][t] = ks, S.scales.v_ratio[at][t] = vs / v_ref;
-                        } else {
-                            const float ratio = fmaxf(vs / v_ref, kLeastRatio);
+                        const int at = i % Scales::kSlots;
+                        if constexpr (kKeyed) {
+                            S.scales.k_scale[at][t] = ks;
+                            if constexpr (!kFolded) S.scales.v_ratio[at][t] = vs / ref;
+                        } else if constexpr (BITS == 8) {
+                            const float ratio = fmaxf(vs / ref, kLeastRatio);
                             S.scales.k_scale[at][t] = ks, S.scales.v_log[at][t] = lg2(ratio), S.scales.v_inv[at][t] = 1.f / ratio;
                         }
                     }
-                    store(ring + (uint32_t)slot * block);
+                    store(ring + (uint32_t)slot * block, (step0 + i) * kKeys + 64 * blk);
                     fence_async_shared();
                     mbar_arrive(bar(full[slot]));
                     if (++slot == depth) slot = 0, par ^= 1u;
@@ -1182,8 +1326,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_prompt_join_kernel(
 
 template <int D, int QT, int PT, int DT, int DRAIN, int BITS>
 cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
-    constexpr int bytes = Layout<D, QT, BITS>::bytes + 1024;
-    static_assert(bytes + sizeof(PromptShared<D, BITS>) <= 227 * 1024, "shared memory of one SM");
+    constexpr bool kKeyed = BITS == 4;
+    constexpr int bytes = Layout<D, QT, kKeyed>::bytes + 1024;
+    static_assert(bytes + sizeof(PromptShared<D, kKeyed>) <= 227 * 1024, "shared memory of one SM");
     // One CTA holds an SM (it takes all of its tensor memory).
     constexpr int asked = bytes > 116 * 1024 ? bytes : 116 * 1024;
     cudaError_t e = kernel_smem_once<attention_prompt_kernel<D, QT, PT, DT, DRAIN, BITS>>(asked);
