@@ -296,9 +296,6 @@ __device__ __forceinline__ void ld_codes(const uint8_t* p, uint4& v) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
 }
-__device__ __forceinline__ void ld_word(const uint8_t* p, uint32_t& v) {
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-}
 // Pairs times pairs of scales of two terms, rounded once to fp16 (but for the lower term's product).
 __device__ __forceinline__ uint32_t scaled_f16(uint32_t x, uint32_t hi, uint32_t lo) {
     const __half2 v = *reinterpret_cast<const __half2*>(&x);
@@ -965,13 +962,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                  const uint8_t* codes) {
             // 8 bits: a thread's pieces of 16 codes: of a block of keys, 16 channels of key t / 4 + 32 j
             // (t % 4); of a block of values, 16 keys of a channel, in the order of the page.
-            // 4 bits: of a block of keys, 32 channels of key t / 2 + 64 j (t % 2); of a block of values,
-            // 8 channels (t / 8) of 8 keys (t % 8), so that stores of a channel lie on all banks.
+            // 4 bits: pieces of 32 codes: of a block of keys, of key t / 2 + 64 j (t % 2); of a block of
+            // values, of whole tokens, in the order of the page.
             [[maybe_unused]] const int count = keys ? 4 : D / 32;  // (8 bits) pieces per thread and block
             const uint32_t page_bytes = (uint32_t)(D * BITS / 8) << ps;
             [[maybe_unused]] const float inverse = 1.f / ref;
             uint4 reg[BITS == 4 ? 2 : 4];
-            [[maybe_unused]] float scale[kFolded ? 8 : 1];  // of the eight values
+            // 16-byte chunks of a token's 4-bit codes; values' rows of a block that a thread has a chunk of.
+            [[maybe_unused]] constexpr int kChunks = D / 32, kValueRows = D / 64;
+            [[maybe_unused]] float scale[2];  // of the values
             int pages_now = fetch_pages(0), pages_next = fetch_pages(1);
             auto load = [&](int page_ids, int blk) {
                 if constexpr (BITS == 4) {
@@ -987,28 +986,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                                              blk * 32 + t % 2 * 16, reg[j]);
                         }
                     } else {
-                        const uint32_t key = 64 * blk + t % 8 * 8;
-                        const int page = __shfl_sync(0xffffffffu, page_ids, key / 16);
-                        uint32_t w[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) w[j] = 0x88888888u;
-                        if (page >= 0 && t / 8 * 4 < (int)kRow) {
-                            const uint8_t* from = codes + (uint64_t)(uint32_t)page * page_bytes +
-                                                  (key & (1u << ps) - 1) * kRow + t / 8 * 4;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) ld_word(from + j * kRow, w[j]);
-                        }
-                        reg[0] = make_uint4(w[0], w[1], w[2], w[3]), reg[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        if constexpr (kFolded) {
-                            uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                        for (int j = 0; j < kValueRows; ++j) {
+                            const uint32_t key = 64 * blk + t / kChunks + 128 / kChunks * j;
+                            const int page = __shfl_sync(0xffffffffu, page_ids, key / 16);
+                            const uint32_t in_page = key & (1u << ps) - 1;
+                            reg[j] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                            if constexpr (kFolded) scale[j] = 0.f;
                             if (page >= 0) {
-                                const uint8_t* from = reinterpret_cast<const uint8_t*>(C.v_scales + ((int64_t)page << ps) + (key & (1u << ps) - 1));
-                                ld_codes(from, a);
-                                ld_codes(from + 16, b);
+                                ld_codes(codes + (uint64_t)(uint32_t)page * page_bytes + in_page * kRow + t % kChunks * 16, reg[j]);
+                                if constexpr (kFolded) scale[j] = __ldg(C.v_scales + ((int64_t)page << ps) + in_page);
                             }
-                            const uint32_t s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) scale[j] = __uint_as_float(s[j]);
                         }
                     }
                 } else {
@@ -1044,32 +1032,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                                 st_shared_v4(to + swizzled(t / 2 + 64 * j, t % 2 * 4 + c), f[0], f[1], f[2], f[3]);
                             }
                         }
-                    } else if (t / 8 * 8 < D) {
-                        // Halves of the words of neighbouring keys side by side: their nibbles are the
-                        // same four channels.
-                        const uint32_t w[8] = {reg[0].x, reg[0].y, reg[0].z, reg[0].w, reg[1].x, reg[1].y, reg[1].z, reg[1].w};
-                        [[maybe_unused]] uint32_t hi[4], lo[4];
-                        if constexpr (kFolded) {
-                            const int left = job.len - first - t % 8 * 8;
+                    } else {
+                        // Rows of a key's 64 channels, as the products take them with this operand the other
+                        // way round; the second half of the channels in rows of their own behind the first,
+                        // written in another order so that all banks are.
+                        const int chunk = t % kChunks, half = chunk / 2;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                split_f16(2 * j < left ? scale[2 * j] * inverse : 0.f,
-                                          2 * j + 1 < left ? scale[2 * j + 1] * inverse : 0.f, &hi[j], &lo[j]);
-                        }
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t f[4][4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                nibbles_f16(prmt(w[2 * j], w[2 * j + 1], half ? 0x7632u : 0x5410u), f[0][j], f[1][j], f[2][j], f[3][j]);
-                                if constexpr (kFolded) {
-#pragma unroll
-                                    for (int n = 0; n < 4; ++n) f[n][j] = scaled_f16(f[n][j], hi[j], lo[j]);
-                                }
+                        for (int j = 0; j < kValueRows; ++j) {
+                            const int row = t / kChunks + 128 / kChunks * j;
+                            const uint32_t w[4] = {half ? reg[j].z : reg[j].x, half ? reg[j].w : reg[j].y,
+                                                   half ? reg[j].x : reg[j].z, half ? reg[j].y : reg[j].w};
+                            [[maybe_unused]] uint32_t hi, lo;
+                            if constexpr (kFolded) {
+                                const float s = first + row < job.len ? scale[j] * inverse : 0.f;
+                                split_f16(s, s, &hi, &lo);
                             }
 #pragma unroll
-                            for (int n = 0; n < 4; ++n)
-                                st_shared_v4(to + swizzled(t / 8 * 8 + half * 4 + n, t % 8), f[n][0], f[n][1], f[n][2], f[n][3]);
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t f[4];
+                                nibbles_f16(w[c], f[0], f[1], f[2], f[3]);
+                                if constexpr (kFolded) {
+#pragma unroll
+                                    for (int n = 0; n < 4; ++n) f[n] = scaled_f16(f[n], hi, lo);
+                                }
+                                st_shared_v4(to + half * (64 * 128) + swizzled(row, chunk % 2 * 4 + (c ^ 2 * half)),
+                                             prmt(f[0], f[1], 0x5410u), prmt(f[2], f[3], 0x5410u),
+                                             prmt(f[0], f[1], 0x7632u), prmt(f[2], f[3], 0x7632u));
+                            }
                         }
                     }
                 } else {
@@ -1147,7 +1136,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const bool two = job.row_end - job.row0 > kQ;
         if (warp == kIssueWarp && n > 0) {
             const uint32_t leader = elect_one();
-            const uint32_t idesc_s = f16_idesc(kQ, kKeys), idesc_o = f16_idesc(kQ, D);
+            // (4 bits: values as rows of channels, so that the summed axis is the other one.)
+            const uint32_t idesc_s = f16_idesc(kQ, kKeys), idesc_o = f16_idesc(kQ, D) | (BITS == 4 ? 1u << 16 : 0u);
             // Low words of the descriptors; 32 bytes along a swizzled row are 2 in their address
             // field, a block of 64 channels (keys) is kBlock / 16 (the high words are all alike).
             const uint64_t desc0 = sw128_desc(base);
@@ -1200,14 +1190,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                         if (!ok) return;
                     }
                     tc_fence_after();
-                    const uint32_t v_low = low0 + ((L::v + (uint32_t)slot * L::vBlock) >> 4);
+                    // Of 16 keys: 32 bytes of a channel's row; or 16 rows, with the second half of the
+                    // channels (in the descriptor, where rows along the summed axis have a 1) 8 KB away.
+                    constexpr uint32_t kStep = BITS == 4 ? 16 * 128 / 16 : 2, kOther = BITS == 4 ? 64 * 128 / 16 - 1 : 0;
+                    const uint32_t v_low = low0 + (kOther << 16) + ((L::v + (uint32_t)slot * L::vBlock) >> 4);
 #pragma unroll
                     for (int term = 0; term < PT; ++term)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma_f16_ts(leader, tmem + tile * 128,
                                        tmem + kScoreCol + tile * kKeys + term * 64 + (half * 4 + kk) * 8,
-                                       desc(v_low + 2 * kk), idesc_o,
+                                       desc(v_low + kStep * kk), idesc_o,
                                        !begins || half + term + kk > 0);
                     if (last) mma_commit(leader, bar(S.v_empty[slot]));
                     if (++slot == L::vRing) slot = 0, par ^= 1u;
