@@ -29,6 +29,11 @@ __host__ __device__ constexpr int warps_of(int D, int CT) {
     return D == 64 ? (CT == 1 ? 20 : CT == 2 ? 16 : 12) : D == 128 ? (CT == 1 ? 12 : 8) : 8;
 }
 
+// Weights are kept as 2^4 p, p by a maximum that scores may have passed by up to 2^10: in a product
+// with a value's scale, below 2, they stay below fp16's 65504, and what two terms leave is 2^-28 of the
+// largest weight.
+constexpr float kFewBits = 4.f, kUnfew = 1.f / 16.f, kMostWeight = 16384.f;
+
 struct KvMaps {
     CUtensorMap k, v;  // [page and head][token][bytes of a token]
 };
@@ -37,20 +42,20 @@ template <int D, int CT>
 struct Mine {  // of one warp
     uint2 q[CT][D / 16][32];  // B fragments
     RowInfo row[CT * 4];
+    float scales[2][kTile];  // of a tile's keys and values (these over a power of two near the largest)
 };
 template <int D, int CT>
 struct Layout {
     static constexpr int W = warps_of(D, CT);
-    static constexpr uint32_t codes = kTile * D / 2, scales = kTile * 4;  // of half a tile: keys or values
+    static constexpr uint32_t codes = kTile * D / 2;  // of half a tile: keys or values
     static constexpr int room = 226 * 1024 - 2048 - 1024 - W * (int)(sizeof(Mine<D, CT>) + 64);
     // Half tiles in a warp's ring, as many as fit.
-    static constexpr int slots = room / (int)(W * (codes + scales)) < 8 ? room / (int)(W * (codes + scales)) : 8;
+    static constexpr int slots = room / (int)(W * codes) < 8 ? room / (int)(W * codes) : 8;
     static_assert(slots >= 2, "a tile's keys and values fit");
 };
 template <int D, int CT>
 struct Shared {
     using L = Layout<D, CT>;
-    float scales[L::W][L::slots][kTile];
     Mine<D, CT> mine[L::W];
     uint64_t full[L::W][L::slots];
     int prefix[kMaxBatch + 1];
@@ -105,7 +110,6 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
     Shared<D, CT>& S = *reinterpret_cast<Shared<D, CT>*>(smem_raw + (base - smem_u32(smem_raw)) + W * kSlots * L::codes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
     const uint32_t ring = base + (uint32_t)(warp * kSlots) * L::codes;
-    const uint32_t scale_ring = smem_u32(S.scales[warp]);
     Mine<D, CT>& mine = S.mine[warp];
     const q4lin_kv4_cache_t& C = g.cache;
     const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads), ps = g.page_shift;
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
 
     // The piece's tiles `first`, first + 1, ...; with the pages of the next 32 / ppt of them in
     // the lanes: lane i holds page i % ppt of tile i / ppt.
-    const uint32_t page_bytes = (uint32_t)(D / 2) << ps, page_scales = 4u << ps;
+    const uint32_t page_bytes = (uint32_t)(D / 2) << ps;
     const int batch_tiles = 32 >> tile_shift, page_of_lane = lane & (ppt - 1), tile_of_lane = lane >> tile_shift;
     const int32_t* table = nullptr;
     int first = 0, cnt = 0, page_low = 0, pages = 0, head = 0, ids = 0, issued = 0, slot_in = 0, in_flight = 0;
@@ -158,28 +162,39 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
             }
         }
     };
-    // Next half tile of the piece (keys of a tile, then its values) into the ring: the first lanes
-    // copy a page's codes each, the next ones its scales.
+    // Next half tile of the piece (keys of a tile, then its values) into the ring, a page a lane.
     auto issue = [&]() {
         if (issued >= 2 * cnt) return;
         const int i = issued >> 1, in_batch = i & (batch_tiles - 1);
         if ((issued & 1) == 0 && i > 0 && in_batch == 0) load_ids(i), check_ids(i);
         const int id = __shfl_sync(0xffffffffu, ids, (in_batch << tile_shift) + page_of_lane);
-        const int count = __popc(__ballot_sync(0xffffffffu, lane < ppt && id >= 0));
+        const bool some = lane < ppt && id >= 0;
+        const int count = __popc(__ballot_sync(0xffffffffu, some));
         const uint32_t bar = smem_u32(&S.full[warp][slot_in]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * (page_bytes + page_scales) + g.missing);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)count * page_bytes + g.missing);
         __syncwarp();
-        if (lane < 2 * ppt && id >= 0) {
-            const int page = id * Hkv + head;
-            if (lane < ppt)
-                tma_load_3d(ring + (uint32_t)slot_in * L::codes + page_of_lane * page_bytes,
-                            issued & 1 ? &maps.v : &maps.k, 0, 0, page, bar);
-            else
-                bulk_load(scale_ring + (uint32_t)slot_in * L::scales + page_of_lane * page_scales,
-                          (issued & 1 ? C.v_scales : C.k_scales) + ((int64_t)page << ps), page_scales, bar);
-        }
+        if (some)
+            tma_load_3d(ring + (uint32_t)slot_in * L::codes + page_of_lane * page_bytes, issued & 1 ? &maps.v : &maps.k, 0, 0,
+                        id * Hkv + head, bar);
         ++issued, ++in_flight;
         slot_in = slot_in + 1 == kSlots ? 0 : slot_in + 1;
+    };
+    // Four scales a lane, keys' in the lower half of the warp and values' in the upper one, on their way
+    // a tile ahead, their page's index two.
+    const int scale_key = (lane & 15) * 4;
+    const float* const scale_base = lane < 16 ? C.k_scales : C.v_scales;
+    int scale_page = -1;
+    float4 scales_next = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto fetch_page = [&](int i) {
+        const int p = ((first + i) << tile_shift) + (scale_key >> ps);
+        scale_page = i < cnt && p >= page_low && p < pages ? __ldg(table + p) : -1;
+        if ((uint32_t)scale_page >= (uint32_t)C.num_pages && i < cnt && p >= page_low && p < pages) scale_page = 0;  // (reported)
+    };
+    auto fetch_scales = [&]() {
+        scales_next = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (scale_page >= 0)
+            scales_next = __ldg(reinterpret_cast<const float4*>(
+                scale_base + (((int64_t)scale_page * Hkv + head) << ps) + (scale_key & ((1 << ps) - 1))));
     };
     uint32_t phase = 0;  // parity bit of each slot's next wait
     int slot_out = 0;
@@ -212,6 +227,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
         head = P.h;
         issued = 0;
         load_ids(0);
+        fetch_page(0);
         int limit_min = INT_MAX, low_max = 0;
         {
             constexpr int kUnits = D / 8, kPer = 32 / kUnits, kPasses = R / kPer;
@@ -241,6 +257,8 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                 }
                 if (p0 == 0) {
                     check_ids(0);
+                    fetch_scales();
+                    fetch_page(1);
 #pragma unroll 1
                     for (int i = 0; i < kSlots; ++i) issue();
                 }
@@ -312,20 +330,28 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
         }
         for (int i = 0; i < cnt; ++i) {
             const int tile_key = (first + i) * kTile;
-            // Slots that were not copied, and those behind the sequence, may hold anything.
-            const bool whole = tile_key + kTile <= P.len && tile_key >= page_low << ps;
-            // Scales of this lane's keys, 16 m + gq and + 8.
-            auto scales_of = [&](uint32_t slot, float2 (&s)[4]) {
-                const uint32_t at = scale_ring + slot * L::scales + gq * 4;
+            // The tile's scales, through shared memory to the lanes that want them; 0 for keys behind the
+            // sequence, whose slots may hold anything.  Values' over a power of two: sv_unit.
+            float sv_unit;
+            {
+                const int left = P.len - tile_key - scale_key;
+                float4 v = scales_next;
+                v.x = left > 0 ? v.x : 0.f, v.y = left > 1 ? v.y : 0.f, v.z = left > 2 ? v.z : 0.f, v.w = left > 3 ? v.w : 0.f;
+                const float most = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+                const uint32_t ex = min(max(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(most)) >> 23, 1u), 253u);
+                sv_unit = __uint_as_float(ex << 23);
+                const float inverse = lane < 16 ? 1.f : __uint_as_float((254u - ex) << 23);
+                v.x *= inverse, v.y *= inverse, v.z *= inverse, v.w *= inverse;
+                *reinterpret_cast<float4*>(&mine.scales[lane >> 4][scale_key]) = v;
+                fetch_scales();
+                fetch_page(i + 2);
+                __syncwarp();
+            }
+            // Of this lane's keys, 16 m + gq and + 8.
+            auto scales_of = [&](int kind, float2 (&s)[4]) {
+                const uint32_t at = smem_u32(mine.scales[kind]) + gq * 4;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    s[m] = make_float2(ld_shared_f(at + m * 64), ld_shared_f(at + m * 64 + 32));
-                    if (!whole) {
-                        const int key = tile_key + 16 * m + gq;
-                        if (key >= P.len || key < page_low << ps) s[m].x = 0.f;
-                        if (key + 8 >= P.len || key + 8 < page_low << ps) s[m].y = 0.f;
-                    }
-                }
+                for (int m = 0; m < 4; ++m) s[m] = make_float2(ld_shared_f(at + m * 64), ld_shared_f(at + m * 64 + 32));
             };
             // ---- scores
             const uint32_t k_slot = await();
@@ -370,58 +396,58 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                         for (int ct = 0; ct < CT; ++ct) mma_f16(sc[ct][m], b[m], q1[ct].x, q1[ct].y);
                 }
             }
-            float2 sk[4];
-            scales_of(k_slot, sk);
             __syncwarp();
             issue();  // the slot of the keys is free
 
-            // ---- softmax: running maximum and sum; weights times the values' scales over a power of
-            // two near the tile's largest, as two fp16 terms
-            const uint32_t v_slot = await();
-            if (!ok) break;
-            float2 sv[4];
-            scales_of(v_slot, sv);
-            float sv_max = 0.f;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) sv_max = fmaxf(sv_max, fmaxf(sv[m].x, sv[m].y));
-#pragma unroll
-            for (int o = 4; o < 32; o *= 2) sv_max = fmaxf(sv_max, __shfl_xor_sync(0xffffffffu, sv_max, o));
-            const uint32_t sv_ex = min(max(__float_as_uint(sv_max) >> 23, 1u), 253u);
-            const float sv_unit = __uint_as_float(sv_ex << 23), sv_inv = __uint_as_float((254u - sv_ex) << 23);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) sv[m] = fmul2(sv[m], make_float2(sv_inv, sv_inv));
+            // ---- softmax: weights by the maximum that there is, as long as they stay in fp16's range; a row
+            // that has seen nothing yet or whose scores have grown too far gets a new maximum first.  Then
+            // times the values' scales, as two fp16 terms.
+            float2 sk[4], sv[4];
+            scales_of(0, sk);
+            scales_of(1, sv);
             const bool inside = tile_key >= low_max && tile_key + kTile - 1 <= limit_min;
             uint2 pf[CT][4];  // B fragments
-            float alpha[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                float2 p[4];
-                float mx = -INFINITY;
+                float2 x[4], p[4];
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
-                    p[m] = fmul2(make_float2(sc[ct][m][0] + sc[ct][m][1], sc[ct][m][2] + sc[ct][m][3]), sk[m]);
+                    x[m] = fmul2(make_float2(sc[ct][m][0] + sc[ct][m][1], sc[ct][m][2] + sc[ct][m][3]), sk[m]);
                 if (!inside) {
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
                         const int key = tile_key + 16 * m + gq;
-                        if (key < low[ct] || key > limit[ct]) p[m].x = -INFINITY;
-                        if (key + 8 < low[ct] || key + 8 > limit[ct]) p[m].y = -INFINITY;
+                        if (key < low[ct] || key > limit[ct]) x[m].x = -INFINITY;
+                        if (key + 8 < low[ct] || key + 8 > limit[ct]) x[m].y = -INFINITY;
                     }
                 }
+                const float2 f2 = make_float2(factor[ct], factor[ct]);
+                auto weights = [&]() {
+                    const float off = kFewBits - (m_run[ct] == -INFINITY ? 0.f : m_run[ct]);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) mx = fmaxf(mx, fmaxf(p[m].x, p[m].y));
+                    for (int m = 0; m < 4; ++m) {
+                        p[m] = ffma2(x[m], f2, make_float2(off, off));
+                        p[m].x = ex2(p[m].x), p[m].y = ex2(p[m].y);
+                    }
+                };
+                weights();
+                float most = fmaxf(fmaxf(fmaxf(p[0].x, p[0].y), fmaxf(p[1].x, p[1].y)), fmaxf(fmaxf(p[2].x, p[2].y), fmaxf(p[3].x, p[3].y)));
+                const unsigned far = __ballot_sync(0xffffffffu, most > kMostWeight || m_run[ct] == -INFINITY);
+                if (far) {  // (each row for itself)
+                    float mx = fmaxf(fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y)), fmaxf(fmaxf(x[2].x, x[2].y), fmaxf(x[3].x, x[3].y)));
 #pragma unroll
-                for (int o = 4; o < 32; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                mx = fmaxf(mx * factor[ct], m_run[ct]);
-                const float from = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing yet
-                alpha[ct] = ex2(m_run[ct] - from);
-                m_run[ct] = mx;
-                const float2 f2 = make_float2(factor[ct], factor[ct]), off = make_float2(kShift - from, kShift - from);
+                    for (int o = 4; o < 32; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const float old = m_run[ct];
+                    if (far & 0x11111111u << t) m_run[ct] = fmaxf(mx * factor[ct], old);
+                    const float alpha = m_run[ct] == -INFINITY ? 1.f : ex2(old - m_run[ct]);
+                    l_run[ct] *= alpha;
+#pragma unroll
+                    for (int n = 0; n < 2 * kChunks; ++n) O[ct][n] = fmul2(O[ct][n], make_float2(alpha, alpha));
+                    weights();
+                }
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    p[m] = ffma2(p[m], f2, off);
-                    p[m].x = ex2(p[m].x), p[m].y = ex2(p[m].y);
                     sum = fadd2(sum, p[m]);
                     p[m] = fmul2(p[m], sv[m]);
                     // Rows of a transposed fragment: both terms of a key's weight.
@@ -430,8 +456,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                     pf[ct][m].x = transposed(prmt(hi, lo, 0x5410u));
                     pf[ct][m].y = transposed(prmt(hi, lo, 0x7632u));
                 }
-                l_run[ct] = fmaf(l_run[ct], alpha[ct], sum.x + sum.y);
+                l_run[ct] += sum.x + sum.y;
             }
+            const uint32_t v_slot = await();
+            if (!ok) break;
 
             // ---- outputs: 64 channels at a time, the tile's 64 keys in 4 steps
             const uint32_t v_at = ring + v_slot * L::codes;
@@ -470,7 +498,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         const float2 v = make_float2(acc[ct][n][0] + acc[ct][n][1], acc[ct][n][2] + acc[ct][n][3]);
-                        O[ct][2 * c0 + n] = ffma2(v, unit2, fmul2(O[ct][2 * c0 + n], make_float2(alpha[ct], alpha[ct])));
+                        O[ct][2 * c0 + n] = ffma2(v, unit2, O[ct][2 * c0 + n]);
                     }
             }
             __syncwarp();
@@ -514,10 +542,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                         make_uint2(to_16x2(x.x, x.y, g.a.dtype), to_16x2(y.x, y.y, g.a.dtype));
             }
             if (gq != 0) continue;
-            if (!complete)
-                part[R * D + r] = m_run[ct], part[R * D + R + r] = l;
+            if (!complete)  // (the joining kernel takes weights as 2^kShift p)
+                part[R * D + r] = m_run[ct] + (kShift - kFewBits), part[R * D + R + r] = l;
             else if (g.a.lse)
-                g.a.lse[index] = l != 0.f ? ((m_run[ct] == -INFINITY ? 0.f : m_run[ct]) + lg2(l * kUnshift)) * kLn2
+                g.a.lse[index] = l != 0.f ? ((m_run[ct] == -INFINITY ? 0.f : m_run[ct]) + lg2(l * kUnfew)) * kLn2
                                           : -INFINITY;
         }
         pos += P.n;
