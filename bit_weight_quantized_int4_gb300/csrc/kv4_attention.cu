@@ -4,9 +4,12 @@
 // The keys of all sequences and heads are one list of 64-key tiles, cut evenly over the GPU's warps
 // (attention_split.cuh); a warp works alone, with its own ring of copies.
 //
-// Bound: the codes and scales, head_dim + 8 bytes per key and key/value head.  At half the bytes
-// of an 8-bit cache the instructions that widen codes and feed the products come as close to the
-// limit as the memory does.
+// Bound: the codes and scales, head_dim + 8 bytes per key and key/value head; at half the bytes of an
+// 8-bit cache also the instructions of a tile, about 1100 a warp, 576 of which widen codes.  Measured (8
+// key/value heads of 128, 4 query heads each): 64 sequences of up to 8192 tokens, 347 MB, 73 us: 4.8
+// TB/s, 0.70 of a copy's bandwidth (without widening any code 62 us); one sequence of 131071 tokens, 143
+// MB, 38.5 us, 8 of it the start and the join; one of 701 tokens 8.6 us.  Heads of 64 / 256: 50 us (0.54)
+// and 127 us (0.78); eight and sixteen query heads a key head 108 and 220 us.
 //
 // Products on the tensor cores (m16n8k16, fp16 operands, fp32 sums), transposed: keys (channels of
 // the values) are the MMA's 16 rows, and a query row takes two of its 8 columns, the rounded value
@@ -24,9 +27,11 @@ namespace q4lin {
 namespace {
 
 // CT tiles of 8 columns, 4 query rows each.  Warps in fours: one too many for a scheduler holds all of
-// them up (64 sequences, 8 / 10 / 12 / 14 / 16 warps: 90, 99, 82, 94, 86 us; two tiles 120, 151, 128).
+// them up (64 sequences as above, 8 / 12 / 16 warps: 78, 73, 77 us, 10 and 14 more than any; two tiles, 8
+// and 12: 108, 133; heads of 64, 12 / 16 / 20: 54, 54, 62, two tiles 74 with 12, 79 with 16, four 121 with
+// 8, 167 with 12).
 __host__ __device__ constexpr int warps_of(int D, int CT) {
-    return D == 64 ? (CT == 1 ? 20 : CT == 2 ? 16 : 12) : D == 128 ? (CT == 1 ? 12 : 8) : 8;
+    return D == 64 ? (CT <= 2 ? 12 : 8) : D == 128 && CT == 1 ? 12 : 8;
 }
 
 // Weights are kept as 2^4 p, p by a maximum that scores may have passed by up to 2^10: in a product
@@ -48,9 +53,11 @@ template <int D, int CT>
 struct Layout {
     static constexpr int W = warps_of(D, CT);
     static constexpr uint32_t codes = kTile * D / 2;  // of half a tile: keys or values
-    static constexpr int room = 226 * 1024 - 2048 - 1024 - W * (int)(sizeof(Mine<D, CT>) + 64);
-    // Half tiles in a warp's ring, as many as fit.
-    static constexpr int slots = room / (int)(W * codes) < 8 ? room / (int)(W * codes) : 8;
+    static constexpr int other = W * ((int)sizeof(Mine<D, CT>) + 4) + 4 * (kMaxBatch + 1) + 64 + 1024;
+    // Half tiles in a warp's ring: three, where they fit (with more the first copies of all warps hold one
+    // another up: one sequence of 131071 tokens 38.6 us, with four 40.6; 64 sequences of heads of 64 with
+    // 2, 3, 4, 8: 50.7, 50.3, 50.5, 53.6).
+    static constexpr int fit = (227 * 1024 - other) / (W * (int)(codes + 8)), slots = fit < 3 ? fit : 3;
     static_assert(slots >= 2, "a tile's keys and values fit");
 };
 template <int D, int CT>
@@ -432,7 +439,8 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                 };
                 weights();
                 float most = fmaxf(fmaxf(fmaxf(p[0].x, p[0].y), fmaxf(p[1].x, p[1].y)), fmaxf(fmaxf(p[2].x, p[2].y), fmaxf(p[3].x, p[3].y)));
-                const unsigned far = __ballot_sync(0xffffffffu, most > kMostWeight || m_run[ct] == -INFINITY);
+                const bool sees = limit[ct] >= tile_key && low[ct] < tile_key + kTile;
+                const unsigned far = __ballot_sync(0xffffffffu, most > kMostWeight || (m_run[ct] == -INFINITY && sees));
                 if (far) {  // (each row for itself)
                     float mx = fmaxf(fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y)), fmaxf(fmaxf(x[2].x, x[2].y), fmaxf(x[3].x, x[3].y)));
 #pragma unroll

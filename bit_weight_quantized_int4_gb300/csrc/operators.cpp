@@ -20,6 +20,11 @@ namespace {
 // 96 / 86, 64 rows 174 / 88; 8 sequences of 2000, 32 rows 34 / 47, 64 rows 44 / 49; 32 of 4000,
 // 32 rows 112 / 149, 64 rows 181 / 147; fp32, 8 of 2000: 31 / 47 and 41 / 48).
 constexpr int64_t kSplitRows = 48;
+// Over a 4-bit cache the prompts' kernel is ahead earlier with bf16, whose products have one term
+// each (the same sizes: one sequence of 8192 keys, 32 rows 28.5 / 29.4, 48 rows 42.5 / 31.5; of 65536, 24
+// rows 88 / 88, 48 rows 124 / 88; 8 of 2000, 32 rows 41 / 52, 48 rows 64 / 56; 32 of 4000, 32 rows 165 /
+// 189, 48 rows 230 / 200; fp32, 48 rows: 41 / 38, 121 / 152, 61 / 70, 228 / 327).
+constexpr int64_t kSplitRows4Bf16 = 32;
 
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 bool known_dtype(int dtype) { return dtype >= Q4LIN_DTYPE_F32 && dtype <= Q4LIN_DTYPE_BF16; }
@@ -255,7 +260,8 @@ q4lin_status_t run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cache, co
         return Q4LIN_ERR_TOO_LARGE;
     // One sequence of many rows goes to the prompts' kernel whatever its length; of several, each
     // kernel takes its own (lengths are on the device).
-    const int64_t split_rows = h->attention_split_rows > 0 ? h->attention_split_rows : kSplitRows;
+    const int64_t by_rule = bits == 4 && a->dtype == Q4LIN_DTYPE_BF16 ? kSplitRows4Bf16 : kSplitRows;
+    const int64_t split_rows = h->attention_split_rows > 0 ? h->attention_split_rows : by_rule;
     const bool prompts = rows_longest > split_rows && q4lin::attention_prompt_eligible(*cache);
     const bool split = !prompts || cache->batch > 1;
     const int64_t split_most = prompts ? split_rows : INT64_MAX;
