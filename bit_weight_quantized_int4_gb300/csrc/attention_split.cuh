@@ -29,6 +29,7 @@ struct SplitArgs {
     int64_t rows_max;
     int q_vec;
     int workers;    // warps of the launch
+    int64_t join_each;  // tokens of a sequence that the joining kernel has CTAs for; 0: one for every token
     float* parts;   // [workers][2][R (D + 2)]: a warp's first and last piece, if unfinished
     int* list;      // [batch + 1]: the share, then where each sequence begins in the list
     int* status;
@@ -152,14 +153,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
     __shared__ float4 s_o[kJoinWarps][D / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t token = blockIdx.x / g.a.heads;
-    const int head = (int)(blockIdx.x - token * g.a.heads);
+    const int64_t at_token = blockIdx.x / g.a.heads;
+    const int head = (int)(blockIdx.x - at_token * g.a.heads);
     const int group = (int)(g.a.heads / g.cache.kv_heads), h = head / group;
     // (Offsets and lengths are the caller's inputs, not the first kernel's results.)
-    const int64_t b = find_sequence(g.cache.batch, token, [&](int64_t i) { return (int64_t)__ldg(g.a.offsets + i); });
+    int64_t b;
+    if (g.join_each)
+        b = at_token / g.join_each;
+    else
+        b = find_sequence(g.cache.batch, at_token, [&](int64_t i) { return (int64_t)__ldg(g.a.offsets + i); });
     bool bad;
     const Sequence s = sequence_of<R>(g, b, &bad);
-    const int64_t o0 = __ldg(g.a.offsets + b);
+    const int64_t o0 = __ldg(g.a.offsets + b), token = g.join_each ? o0 + at_token - b * g.join_each : at_token;
     griddep_wait();
     if (token < o0 || token >= o0 + s.tq) return;
     const int row = (int)(token - o0) * group + head - h * group, r = row % R;
@@ -272,7 +277,12 @@ inline bool split_countable(const q4lin_kv_cache_t& cache, const q4lin_attention
 
 // The joining kernel, behind the one that left the parts.
 template <int D, int R>
-cudaError_t join_launch(const SplitArgs& g, const SplitSize& size, const LaunchCtx& c) {
+cudaError_t join_launch(SplitArgs& g, const SplitSize& size, const LaunchCtx& c) {
+    // CTAs for the tokens that a sequence of this kernel may have, or for every token, whichever are
+    // fewer (among 2403 tokens of three prompts, none of them this kernel's, 77000 idle CTAs took 140 us).
+    const int64_t each = std::min(g.a.max_query, std::max<int64_t>(1, g.rows_max / (g.a.heads / g.cache.kv_heads)));
+    g.join_each = each <= g.a.tokens / g.cache.batch ? each : 0;
+    const int64_t rows = g.join_each ? each * g.cache.batch : g.a.tokens;
     // The second kernel's launch overlaps the first's work; it waits for its end on the device.
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -282,7 +292,7 @@ cudaError_t join_launch(const SplitArgs& g, const SplitSize& size, const LaunchC
     // about 10, eight warps 21 us, two 24; one sequence x 8 heads: 152).
     const int64_t parts = g.workers / size.segments;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(g.a.tokens * g.a.heads));
+    cfg.gridDim = dim3((unsigned)(rows * g.a.heads));
     cfg.stream = c.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
