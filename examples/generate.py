@@ -2,13 +2,17 @@
 gradient of what it generated back to its last hidden states.
 
     python examples/generate.py [--layers 16 --hidden 2048 --heads 32 --kv-heads 8 ...]
+    python examples/generate.py --cache-bits 4 --head-norm 1
 
 The weights are random (the shapes are what counts here), activations are fp32.  Every layer
-keeps its keys and values in a paged 8-bit cache; all layers share one page table.
+keeps its keys and values in a paged 8-bit cache (or a 4-bit one); all layers share one page
+table.
 
     prompts    one call for all of them: kv_append rotates and stores the keys, attention
                reads them back (many query rows per sequence)
-    steps      the same two calls with one token per sequence
+               (with --head-norm, norm_rope normalises queries and keys per head and rotates
+               both beforehand, in their own place)
+    steps      the same calls with one token per sequence
     logits     logprobs gives the alternatives that the next token is drawn from, and the
                log probability of the drawn one
     learning   logprobs_backward turns advantages into the logits' gradient (in the logits'
@@ -38,6 +42,8 @@ class Config:
     inner: int = 4096
     vocabulary: int = 32000
     page: int = 32
+    cache_bits: int = 8  # or 4
+    head_norm: int = 0   # 1: queries and keys are normalised per head
 
 
 class Linear:
@@ -87,6 +93,9 @@ class Model:
         rate = 10000.0 ** (-torch.arange(0, c.head_dim, 2, device=device) / c.head_dim)
         angle = torch.arange(positions, device=device)[:, None] * rate
         self.rope = angle.cos().contiguous(), angle.sin().contiguous()
+        # Weights of the norms of queries and of keys, of each layer.
+        self.head_norms = [torch.randn(2, c.head_dim, device=device, generator=g) * 0.1 + 1
+                           for _ in range(c.layers if c.head_norm else 0)]
 
     def caches(self, sequences, tokens):
         """Empty caches of all layers, with room for `tokens` tokens of each sequence."""
@@ -94,7 +103,8 @@ class Model:
         pages = -(-tokens // c.page)
         table = torch.randperm(sequences * pages, device=self.embedding.device)
         table = table.to(torch.int32).view(sequences, pages)
-        return [q4lin.KVCache.empty(sequences * pages, c.kv_heads, c.page, c.head_dim, table)
+        kind = {8: q4lin.KVCache, 4: q4lin.KVCache4}[c.cache_bits]
+        return [kind.empty(sequences * pages, c.kv_heads, c.page, c.head_dim, table)
                 for _ in self.layers]
 
     def hidden(self, caches, tokens, offsets, held, most):
@@ -104,12 +114,21 @@ class Model:
         c, handle = self.config, self.handle
         lengths = held + offsets[1:] - offsets[:-1]
         x = self.embedding[tokens]
-        for cache, (qkv, o, up, down) in zip(caches, self.layers):
+        rope, positions = self.rope, None
+        if c.head_norm:  # (which rotates as well)
+            rope = None
+            counts = (offsets[1:] - offsets[:-1]).long()
+            positions = torch.repeat_interleave(held - offsets[:-1], counts, output_size=len(tokens))
+            positions += torch.arange(len(tokens), dtype=torch.int32, device=x.device)
+        for layer, (cache, (qkv, o, up, down)) in enumerate(zip(caches, self.layers)):
             y = qkv(handle, norm(x)).view(-1, c.heads + 2 * c.kv_heads, c.head_dim)
             q, k, v = y.split([c.heads, c.kv_heads, c.kv_heads], 1)
-            q4lin.kv_append(handle, cache, k, v, offsets, held, rope=self.rope)
+            if c.head_norm:
+                q4lin.norm_rope(handle, q, k, *self.head_norms[layer], positions, self.rope,
+                                q_out=q, k_out=k)
+            q4lin.kv_append(handle, cache, k, v, offsets, held, rope=rope)
             y, _ = q4lin.attention(handle, cache, q, offsets, lengths, c.head_dim**-0.5,
-                                   max_query=most, rope=self.rope)
+                                   max_query=most, rope=rope)
             x = x + o(handle, y.view(-1, c.heads * c.head_dim))
             gate, value = up(handle, norm(x)).chunk(2, 1)
             x = x + down(handle, torch.nn.functional.silu(gate) * value)
