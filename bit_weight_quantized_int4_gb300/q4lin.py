@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq4lin.so")
@@ -495,15 +496,19 @@ def _stream_of(stream, handle) -> int:
     return _Torch.stream(handle.device)
 
 
+def _rope_members(cos, sin, interleaved):
+    """The members of q4lin_rope_t."""
+    shape, float32 = cos.shape, _Torch.float32
+    if cos.dtype is not float32 or sin.dtype is not float32 or len(shape) != 2 \
+            or sin.shape != shape or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("rope must be two contiguous float32 [positions, rotated / 2] tensors")
+    return cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], interleaved
+
+
 def _rope_args(rope, interleaved):
     if rope is None:
         return q4lin_rope_t()
-    cos, sin = rope
-    shape = cos.shape
-    if cos.dtype is not _Torch.float32 or sin.dtype is not _Torch.float32 or len(shape) != 2 \
-            or sin.shape != shape or not cos.is_contiguous() or not sin.is_contiguous():
-        raise ValueError("rope must be two contiguous float32 [positions, rotated / 2] tensors")
-    return q4lin_rope_t(cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], interleaved)
+    return q4lin_rope_t(*_rope_members(*rope, interleaved))
 
 
 class _PagedCache:
@@ -680,33 +685,52 @@ def attention(handle: Handle, cache, query, offsets, lengths, scale: float,
     return out, lse
 
 
+# q4lin_norm_rope_t and what q4lin_norm_rope_backward_t has behind it, packed: a ctypes structure of
+# as many members takes five times as long to fill as these calls' kernels to launch.
+_NORM_ROPE = struct.Struct("PPqqqqPPPPqqqqi4xqqqqPPPqqi4xf4x")
+_NORM_ROPE_MORE = struct.Struct("PPqqqqPP")
+_run_norm_rope = _lib["q4lin_run_norm_rope"]
+_run_norm_rope_backward = _lib["q4lin_run_norm_rope_backward"]
+for _f, _t in ((_run_norm_rope, q4lin_norm_rope_t), (_run_norm_rope_backward, q4lin_norm_rope_backward_t)):
+    _f.argtypes, _f.restype = [_vp, ctypes.c_char_p, _vp], _i32
+assert _NORM_ROPE.size == ctypes.sizeof(q4lin_norm_rope_t)
+assert _NORM_ROPE.size + _NORM_ROPE_MORE.size == ctypes.sizeof(q4lin_norm_rope_backward_t)
+
+
 def _norm_args(handle, q, k, q_weight, k_weight, positions, rope, eps, interleaved, q_out, k_out,
                stream):
-    """(q4lin_norm_rope_t, q_out, k_out); the outputs are made where they are not given."""
-    cos, sin = rope or (None, None)
+    """(a packed q4lin_norm_rope_t, q_out, k_out); the outputs are made where they are not given."""
+    cos, sin = rope if rope is not None else (None, None)
     _check_device(handle, q, k, q_weight, k_weight, positions, cos, sin, q_out, k_out)
     qs, ks = _head_strides(q, "q"), _head_strides(k, "k")
-    tokens, heads, dim = q.shape
-    if k.shape[0] != tokens or k.shape[2] != dim or k.dtype is not q.dtype:
+    q_shape, k_shape, dtype = q.shape, k.shape, q.dtype
+    tokens, heads, dim = q_shape
+    if k_shape[0] != tokens or k_shape[2] != dim or k.dtype is not dtype:
         raise ValueError("q and k must be [tokens, heads, head_dim] and [tokens, kv_heads, head_dim] of one type")
-    outs = []
-    for t, x, what in ((q_out, q, "q"), (k_out, k, "k")):
-        if t is None:
-            t = _new(x.shape, x.dtype, x.device, stream)
-        elif t.shape != x.shape or t.dtype is not x.dtype:
-            raise ValueError(f"the output for {what} must have its shape and type")
-        outs.append((t, _head_strides(t, f"the output for {what}")))
-    weight = lambda w, what: None if w is None else _check_vector(w, dim, _Torch.float32, what)
-    if rope is not None and positions is None:
+    code = _dtype_code(q, "q")
+    if q_out is None:
+        q_out = _new(q_shape, dtype, q.device, stream)
+    elif q_out.shape != q_shape or q_out.dtype is not dtype:
+        raise ValueError("the output for q must have its shape and type")
+    if k_out is None:
+        k_out = _new(k_shape, dtype, k.device, stream)
+    elif k_out.shape != k_shape or k_out.dtype is not dtype:
+        raise ValueError("the output for k must have its shape and type")
+    qos, kos = _head_strides(q_out, "the output for q"), _head_strides(k_out, "the output for k")
+    float32 = _Torch.float32
+    qw = 0 if q_weight is None else _check_vector(q_weight, dim, float32, "q_weight")
+    kw = 0 if k_weight is None else _check_vector(k_weight, dim, float32, "k_weight")
+    at = 0 if positions is None else _check_vector(positions, tokens, _Torch.int32, "positions")
+    if rope is None:
+        turn = 0, 0, 0, 0, 0
+    elif positions is None:
         raise ValueError("a rotation needs positions")
-    (qo, qos), (ko, kos) = outs
-    args = q4lin_norm_rope_t(
-        q.data_ptr(), k.data_ptr(), qs[0], qs[1], ks[0], ks[1], weight(q_weight, "q_weight"),
-        weight(k_weight, "k_weight"), qo.data_ptr(), ko.data_ptr(), qos[0], qos[1], kos[0], kos[1],
-        _dtype_code(q, "q"), tokens, heads, k.shape[1], dim,
-        None if positions is None else _check_vector(positions, tokens, _Torch.int32, "positions"),
-        _rope_args(rope, interleaved), eps)
-    return args, qo, ko
+    else:
+        turn = _rope_members(cos, sin, interleaved)
+    args = _NORM_ROPE.pack(q.data_ptr(), k.data_ptr(), qs[0], qs[1], ks[0], ks[1], qw, kw,
+                           q_out.data_ptr(), k_out.data_ptr(), qos[0], qos[1], kos[0], kos[1], code,
+                           tokens, heads, k_shape[1], dim, at, *turn, eps)
+    return args, q_out, k_out
 
 
 def norm_rope(handle: Handle, q, k, q_weight=None, k_weight=None, positions=None, rope=None,
@@ -717,7 +741,7 @@ def norm_rope(handle: Handle, q, k, q_weight=None, k_weight=None, positions=None
     q and k themselves among them.  Returns (q_out, k_out)."""
     args, q_out, k_out = _norm_args(handle, q, k, q_weight, k_weight, positions, rope, eps,
                                     interleaved, q_out, k_out, stream)
-    st = _lib.q4lin_run_norm_rope(handle.ptr, args, _stream_of(stream, handle))
+    st = _run_norm_rope(handle.ptr, args, _stream_of(stream, handle))
     if st != Q4LIN_OK:
         raise Q4LinError(st, "q4lin_run_norm_rope")
     return q_out, k_out
@@ -736,7 +760,7 @@ def norm_rope_backward(handle: Handle, q, k, q_weight, k_weight, positions, rope
                        eps: float = 1e-6, interleaved: bool = False, d_q=None, d_k=None,
                        stream=None) -> NormRopeGradients:
     """Gradients of norm_rope for q, k and the weights, given its inputs and the gradients for
-    its outputs (of any strides).  d_q and d_k: outputs to use; d_q may be q or d_q_out, d_k may be
+    its outputs (of any token and head strides).  d_q and d_k: outputs to use; d_q may be q or d_q_out, d_k may be
     k or d_k_out."""
     forward, d_q, d_k = _norm_args(handle, q, k, q_weight, k_weight, positions, rope, eps,
                                    interleaved, d_q, d_k, stream)
@@ -745,11 +769,12 @@ def norm_rope_backward(handle: Handle, q, k, q_weight, k_weight, positions, rope
             or d_k_out.dtype is not q.dtype:
         raise ValueError("d_q_out and d_k_out must have the shapes and the type of q and k")
     dqs, dks = _head_strides(d_q_out, "d_q_out"), _head_strides(d_k_out, "d_k_out")
-    new = lambda w: None if w is None else _new(w.shape, w.dtype, w.device, stream)
-    dqw, dkw = new(q_weight), new(k_weight)
-    args = q4lin_norm_rope_backward_t(forward, d_q_out.data_ptr(), d_k_out.data_ptr(), dqs[0], dqs[1],
-                                      dks[0], dks[1], _ptr(dqw), _ptr(dkw))
-    st = _lib.q4lin_run_norm_rope_backward(handle.ptr, args, _stream_of(stream, handle))
+    dqw = None if q_weight is None else _new(q_weight.shape, _Torch.float32, q.device, stream)
+    dkw = None if k_weight is None else _new(k_weight.shape, _Torch.float32, q.device, stream)
+    args = forward + _NORM_ROPE_MORE.pack(d_q_out.data_ptr(), d_k_out.data_ptr(), dqs[0], dqs[1], dks[0],
+                                          dks[1], 0 if dqw is None else dqw.data_ptr(),
+                                          0 if dkw is None else dkw.data_ptr())
+    st = _run_norm_rope_backward(handle.ptr, args, _stream_of(stream, handle))
     if st != Q4LIN_OK:
         raise Q4LinError(st, "q4lin_run_norm_rope_backward")
     return NormRopeGradients(d_q, d_k, dqw, dkw)
