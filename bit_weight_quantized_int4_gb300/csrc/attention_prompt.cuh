@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const int low = g.a.window > 0 ? (int)max((int64_t)0, (int64_t)position - g.a.window + 1) : 0;
         // (4 bits: not so small that a masked score would not stay -infinity; 8 bits: with the scale below.)
         float factor = S.factor[r];
-        if constexpr (BITS == 4) factor = fmaxf(factor, kLeastFactor);
+        if constexpr (BITS == 4) factor = factor < kLeastFactor ? kLeastFactor : factor;  // (a NaN stays one)
         int drain = first_drain();
         float m = -INFINITY, l = 0.f, m_out = -INFINITY;  // m_out: of what was taken out
         bool ok = true;

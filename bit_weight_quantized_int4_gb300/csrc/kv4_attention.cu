@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                         f[e % 2 * 2 + (d >> 2 & 1)] = hi, f[16 + e % 2 * 2 + (d >> 2 & 1)] = lo;
                     }
                     RowInfo i;
-                    // At least this, so that a masked score of -infinity stays one.
-                    i.factor = fmaxf(fabsf(g.a.scale) * kLog2e * down, 1e-37f);
+                    // At least this, so that a masked score of -infinity stays one (and a NaN one).
+                    const float f = fabsf(g.a.scale) * kLog2e * down;
+                    i.factor = f < 1e-37f ? 1e-37f : f;
                     i.limit = g.a.causal ? position : P.len - 1;
                     const int64_t low = g.a.window > 0 ? (int64_t)position - g.a.window + 1 : 0;
                     i.low = low > 0 ? (int)low : 0;

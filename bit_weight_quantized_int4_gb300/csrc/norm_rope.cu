@@ -87,18 +87,19 @@ __device__ __forceinline__ float2 two_sums(const Eight& x, const Eight& y) {
         v = fadd2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
     return v;
 }
-// r = 1 / sqrt(sum / D + eps) of a row whose squares add up to `sum`.  Where they pass fp32's range, x is
-// scaled by 2^-70 first (whole warp: the sums need every lane): r is then that of the scaled x, *back
-// what it was scaled by, and *mean the mean of x y anew.
+// r = 1 / sqrt(sum / D + eps) of a row whose squares add up to `sum`.  Where they pass fp32's range, or
+// are lost below it and eps does not hide that, x is scaled by a power of two first (whole warp: the
+// sums need every lane): r is then that of the scaled x, *back what it was scaled by, and *mean the
+// mean of x y anew.
 template <int D>
 __device__ __forceinline__ void scales_of(Eight& x, const Eight& y, float sum, float eps, float* mean, float* r, float* back) {
     *r = rsqrtf(fmaf(sum, 1.f / D, eps)), *back = 1.f;
-    if (__any_sync(0xffffffffu, sum > 3e38f)) {
-        constexpr float kDown = 8.470329472543003e-22f;  // 2^-70
-        const bool far = sum > 3e38f;
-        if (far) scale_by(x, kDown);
+    const bool far = sum > 3e38f || (eps < 1e-30f && sum < 1e-30f);
+    if (__any_sync(0xffffffffu, far)) {
+        const float by = sum > 3e38f ? 8.470329472543003e-22f : 1.2676506002282294e30f;  // 2^-70, 2^100
+        if (far) scale_by(x, by);
         const float2 again = two_sums<D / 8>(x, y);
-        if (far) *r = rsqrtf(fmaf(again.x, 1.f / D, eps * kDown * kDown)), *back = kDown, *mean = again.y * (1.f / D);
+        if (far) *r = rsqrtf(fmaf(again.x, 1.f / D, eps * by * by)), *back = by, *mean = again.y * (1.f / D);
     }
 }
 // x becomes x r.

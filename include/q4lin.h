@@ -452,8 +452,9 @@ Q4LIN_API q4lin_status_t q4lin_run_logprobs_backward(q4lin_handle_t handle,
 /* Norm of each head of queries and keys, and the position rotation, in one pass:
  *   r = 1 / sqrt(sum_d x_d^2 / head_dim + eps),   y = rotation(x r w),
  * the rotation as in q4lin_rope_t, by the token's entry of `positions`.  Everything is fp32
- * up to the one rounding to the type.  Rows whose squares pass fp32's range are scaled by a
- * power of two first, so finite rows have finite norms. */
+ * up to the one rounding to the type.  Rows whose squares leave fp32's range are scaled by a
+ * power of two first, so finite rows have finite results (but for zeros with eps 0, which are
+ * NaN).  A NaN or an infinity stays in its row. */
 typedef struct q4lin_norm_rope {
     const void* q; /* [tokens, heads, head_dim], channels contiguous */
     const void* k; /* [tokens, kv_heads, head_dim] */

@@ -419,6 +419,62 @@ def test_other_stream_nothing_to_do_and_graph(handle):
     assert attend(handle, host, q[:0], [0, 0], [100, 900], 0.1)[0].shape == (0, 4, 64)
 
 
+def test_a_wait_that_runs_out_is_reported(handle):
+    """Keys that do not come: the kernels give up, leave, and work again afterwards."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    host = kv4.Cache(np.random.default_rng(20), [3000], 2, 64, 128)
+    cache = host.device()
+    for dtype in (torch.float32, torch.bfloat16):
+        for tokens in (1, 200):
+            q = torch.randn(tokens, 4, 128, device="cuda").to(dtype)
+            want = attend(handle, host, q, [tokens], [3000], 0.1, cache=cache)[0]
+            handle.set_option(q4lin.Q4LIN_OPT_WAIT_LIMIT, 1000000)  # 1 ms
+            handle.set_option(q4lin.Q4LIN_OPT_TC_SKIP_FIRST_COPY, 1)
+            attend(handle, host, q, [tokens], [3000], 0.1, cache=cache)
+            handle.set_option(q4lin.Q4LIN_OPT_TC_SKIP_FIRST_COPY, 0)
+            handle.set_option(q4lin.Q4LIN_OPT_WAIT_LIMIT, 0)
+            assert status(handle) == 1
+            assert torch.equal(attend(handle, host, q, [tokens], [3000], 0.1, cache=cache)[0], want)
+            assert status(handle) == 0
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf")])
+def test_a_scale_that_is_no_number(handle, split, scale):
+    """Every row becomes NaN; the next call is right."""
+    import torch
+    host = kv4.Cache(np.random.default_rng(21), [200], 1, 32, 64)
+    for dtype in (torch.float32, torch.bfloat16):
+        q = torch.randn(100, 2, 64, device="cuda").to(dtype)
+        for rows in BOTH:
+            split(rows)
+            out, lse = attend(handle, host, q, [100], [200], scale)
+            assert torch.isnan(out).all() and torch.isnan(lse).all()
+            assert torch.isfinite(attend(handle, host, q, [100], [200], 0.1)[0]).all()
+
+
+def test_two_heads_apart_and_padded_batches(handle):
+    """One query head a key head, a batch with sequences of no queries among others, rows behind the last
+    sequence left as they were, and offsets that do not begin at 0."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng = np.random.default_rng(22)
+    lengths, counts = [40, 300, 0, 129, 7], [1, 0, 0, 100, 7]
+    for heads, dim, dtype in ((3, 64, "f32"), (6, 128, "bf16"), (3, 256, "f16")):
+        host = kv4.Cache(rng, lengths, 3, 16, dim)
+        q = ops.to_device(rng.standard_normal((120, heads, dim)).astype(np.float32), dtype)
+        offsets = np.concatenate([[2], 2 + np.cumsum(counts)]).astype(np.int32)
+        out, lse = torch.full_like(q, 7.0), torch.full((120, heads), 7.0, device="cuda")
+        q4lin.attention(handle, host.device(), q, ops.to_device(offsets), ops.to_device(np.array(lengths, np.int32)),
+                        0.125, out=out, lse=lse)
+        want = ops.attention(host, ops.to_host(q), offsets, lengths, 0.125)
+        rows = slice(2, offsets[-1])
+        check(out[rows], lse[rows], [w[rows] for w in want], dtype)
+        for edge in (slice(0, 2), slice(offsets[-1], None)):
+            assert bool((out[edge] == 7).all()) and bool((lse[edge] == 7).all())
+        assert status(handle) == 0
+
+
 def test_a_layer(handle):
     """Norm and rotation, append, attention token by token and in one call, as a decoder runs them,
     against float64 over what the cache then holds; the whole captured into a graph."""

@@ -143,9 +143,21 @@ def test_sizes_of_numbers(handle, dim):
     near(got.d_q[fine], want, 2.0**-19 * size + 2e-37)
     assert torch.isnan(out[4, 1]).all() and torch.isfinite(out[4, 0]).all()
     assert torch.isnan(got.d_q[4, 1]).all() and torch.isfinite(got.d_q[4, 0]).all()
-    # Rows as large as the type holds, rotated: finite.
-    big = torch.full((2, 2, dim), 3e38, device="cuda")
-    assert torch.isfinite(q4lin.norm_rope(handle, big, big, eps=0.0)[0]).all()
+    # Without eps, rows as large as the type holds and as small as fp32 does: like any other.
+    x = rng.standard_normal((5, 2, dim)) * np.array([3e37, 1e-18, 1e-25, 1e-38, 1])[:, None, None]
+    q = ops.to_device(x.astype(np.float32))
+    out, _ = q4lin.norm_rope(handle, q, q[:, :1], eps=0.0)
+    x = ops.to_host(q)
+    want, size = kv4.norm_rope(x, np.ones(dim), None, None, 0.0, False)
+    near(out, want, 2.0**-20 * size)
+    d = torch.ones_like(q) * torch.tensor([1e10, 1e-10, 1e-10, 1e-10, 1], device="cuda")[:, None, None]
+    got = q4lin.norm_rope_backward(handle, q, q[:, :1], None, None, None, None, d, d[:, :1], eps=0.0)
+    want, _, size, _ = kv4.norm_rope_backward(x, np.ones(dim), None, None, 0.0, False, ops.to_host(d))
+    near(got.d_q, want, 2.0**-19 * size + 1e-37)
+    # An infinity: its row alone.
+    q[4, 0, 3] = float("inf")
+    out, _ = q4lin.norm_rope(handle, q, q[:, :1], eps=EPS)
+    assert torch.isnan(out[4, 0, 3]) and torch.isfinite(out[4, 1]).all() and torch.isfinite(out[:4]).all()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
