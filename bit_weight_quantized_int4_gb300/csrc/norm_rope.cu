@@ -1,9 +1,15 @@
 // norm_rope.cu -- queries and keys normalised per head and rotated in one pass, and the gradient
 // of that.
 //
-// A warp takes heads of one token (a part of them where tokens are few), `PASSES` x 32 / (D / 8) of
-// them in flight; a lane holds eight channels of a head (the two groups of four that the rotation
-// pairs), and the token's angles and the weights of its channels for all of the warp's heads.
+// A pass of a warp takes 32 / (D / 8) heads of one token; a lane holds eight channels of a head (the two
+// groups of four that the rotation pairs), and keeps the token's angles and the weights of its channels.
+// Forward, a warp takes a token's heads (a part of them where tokens are few); backward, where a warp's
+// sums over its rows cost a join, as many CTAs as fit share all passes out evenly.
+//
+// Bound: memory, for the gradient with bf16 the instructions beside it (half of a warp scheduler's slots).
+// Measured: 8192 tokens of 40 heads of 128 in bf16 normalised and rotated in 32 us, 0.79 of a copy's
+// bandwidth; their gradient in 52 us, 0.73; of 4096 tokens in fp32 31.6 and 43.7 us, 0.79 and 0.86; one
+// token 2.6 and 5.6 us, one launch and two.
 //
 // Forward, y = R(x r w) with r = 1 / sqrt(mean x^2 + eps); backward, with g = R^T dy and u = x r:
 // dw = sum g u, dx = r (g w - u mean(g w u)).  R turns pairs by an angle, so R^T turns them back.
@@ -17,17 +23,24 @@ namespace {
 using namespace ptx;
 using namespace serving;
 
-// Passes in flight of a warp, as many as registers leave warps for (8192 tokens of 40 heads of 128 in
-// bf16: forward 2 / 3 / 4 passes 33.3, 32.8, 31.8 us; backward with two CTAs an SM 54.6 us, with three,
-// whose registers hold less, 92 and up).
-constexpr int kAhead = 4, kBackAhead = 4, kBackCtas = 2;
+// Passes in flight of a warp.  Forward, in registers (8192 tokens of 40 heads of 128 in bf16): 2 / 3 / 4
+// passes 33.3, 32.8, 31.8 us.  Backward, slots of the ring for two bytes an element, the CTA's warps and the
+// CTAs of an SM (the same, and 4096 tokens in fp32): 6, 8 and 2 51.8 and 43.7 us; 6, 8 and 3, whose registers
+// do not hold a row's work, 65 and 49; 6, 6 and 3 52.7 and 44.5; 8, 4 and 5 52.9 and 44.4; 12, 4 and 4 56 and 44.6.
+// With rows in registers, as forward, 55 and 76 us.
+constexpr int kAhead = 4, kBackSlots = 6, kBackCtas = 2;
 constexpr int kWarps = 4, kBackWarps = 8;
 
+// Bytes from a head to the one that a warp takes next.
+struct Steps {
+    int64_t x, d, y;
+};
 struct NormArgs {
     q4lin_norm_rope_t a;
     const void *dq, *dk;  // backward: the gradients that come in
     int64_t dq_token, dq_head, dk_token, dk_head;
-    float* parts;  // backward: [kind][CTA][D] sums of the weights' gradients
+    Steps steps[2];  // backward: of queries, of keys
+    float* parts;    // backward: [kind][CTA][D] sums of the weights' gradients
     bool vec;            // groups of four elements of all arrays are aligned
     int64_t part_heads;  // of a token's heads, queries' and keys', in a part
     int* status;
@@ -271,90 +284,175 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormArgs g
     rows(std::true_type{});
 }
 
-// CTAs walk over tokens with the weights' sums in registers.
-template <int D, int DT, int AHEAD, bool VEC>
+// Rows of x and dy on their way to a lane: copies to a ring in shared memory that only the lane reads
+// (VEC), so that many rows of a warp are in flight without a register for any.  Else the next row's
+// elements in registers: there is no copy of two bytes.
+template <int DT, bool VEC>
+struct Rows {
+    static constexpr int kSlots = VEC ? kBackSlots / (DT == Q4LIN_DTYPE_F32 ? 2 : 1) : 1, kGroup = DT == Q4LIN_DTYPE_F32 ? 16 : 8;
+    static constexpr int kBytes = VEC ? kSlots * 4 * kGroup * 32 * kBackWarps : 0;
+    uint32_t ring;  // the lane's first group of the slot read next; groups lie 32 lanes apart
+    int slot;
+    Raw<DT, VEC> x, d;
+
+    __device__ __forceinline__ void init(void* shared) {
+        if constexpr (VEC) {
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+            ring = smem_u32(shared) + (warp * kSlots * 4 * 32 + lane) * kGroup;
+            slot = 0;
+        }
+    }
+    // Into slot `to`.
+    __device__ __forceinline__ void fetch(int to, const char* px, const char* pd, int lo, int hi, bool in) {
+        if constexpr (VEC) {
+            const uint32_t at = ring + to * (4 * 32 * kGroup);
+            if (in) {
+                cp_async_ca<kGroup>(at, px + lo);
+                cp_async_ca<kGroup>(at + 32 * kGroup, px + hi);
+                cp_async_ca<kGroup>(at + 64 * kGroup, pd + lo);
+                cp_async_ca<kGroup>(at + 96 * kGroup, pd + hi);
+            }
+            cp_async_commit();
+        } else {
+            x.load(px, lo, hi, in), d.load(pd, lo, hi, in);
+        }
+    }
+    __device__ __forceinline__ void read(int from, Eight& ex, Eight& ed) {
+        if constexpr (VEC) {
+            cp_async_wait_group<kSlots - 2>();
+            const uint32_t at = ring + from * (4 * 32 * kGroup);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                lds_group(x, g, at + g * 32 * kGroup);
+                lds_group(d, g, at + (2 + g) * 32 * kGroup);
+            }
+        }
+        ex = x.unpack(), ed = d.unpack();
+    }
+    static __device__ __forceinline__ void lds_group(Raw<DT, VEC>& r, int g, uint32_t at) {
+        if constexpr (DT == Q4LIN_DTYPE_F32)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r.w[2 * g].x), "=r"(r.w[2 * g].y), "=r"(r.w[2 * g + 1].x), "=r"(r.w[2 * g + 1].y)
+                         : "r"(at)
+                         : "memory");
+        else
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.w[g].x), "=r"(r.w[g].y) : "r"(at) : "memory");
+    }
+};
+
+// A warp takes a stretch of the (token, R heads) of queries, then of keys, all warps equally many, with
+// the weights' sums in registers.
+template <int D, int DT, bool VEC>
 __global__ void __launch_bounds__(32 * kBackWarps, kBackCtas) norm_rope_backward_kernel(const NormArgs g) {
     constexpr int U = D / 8, R = 32 / U, kSize = (int)dtype_size(DT);
-    __shared__ float sums[kBackWarps * R][D];
+    using Ring = Rows<DT, VEC>;
+    constexpr int kSums = kBackWarps * R * D * 4;
+    __shared__ __align__(16) char shared[Ring::kBytes > kSums ? Ring::kBytes : kSums];
+    float(*sums)[D] = reinterpret_cast<float(*)[D]>(shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
     griddep_launch_dependents();  // (the kernel that joins the sums waits for this one's end)
     bool turned;
     int lo, hi;
     rope_channels(g.a.rope, u, &turned, &lo, &hi);
     const int lo_at = lo * kSize, hi_at = hi * kSize;
-    const Heads heads = heads_of(g, blockIdx.y);
+    Ring ring;
+    ring.init(shared);
     auto rows = [&](auto keys) {
         constexpr bool kKeys = decltype(keys)::value;
         const Side s = side_of(g, kKeys);
-        const int begin = (int)(kKeys ? heads.k0 : heads.q0), end = (int)(kKeys ? heads.k1 : heads.q1);
+        const int heads = (int)s.heads, each = (heads + R - 1) / R;  // passes of a token
+        const int64_t all = g.a.tokens * each, warps = (int64_t)gridDim.x * kBackWarps;
+        const int64_t w0 = (int64_t)blockIdx.x * kBackWarps + warp;
+        const int64_t share = all / warps, more = all % warps;
+        int left = (int)(share + (w0 < more));
         const Eight w = load_weight<VEC>(s.w, lo, hi);
-        const int64_t x_step = R * s.xh * kSize, d_step = R * s.dh * kSize, y_step = R * s.yh * kSize;
         Eight dw;
 #pragma unroll
         for (int e = 0; e < 4; ++e) dw.v[e] = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int64_t token = (int64_t)blockIdx.x * kBackWarps + warp; token < g.a.tokens && begin < end;
-             token += (int64_t)gridDim.x * kBackWarps) {
-            Raw<DT, VEC> raw_x[AHEAD], raw_d[AHEAD];
-            const char* x_at = static_cast<const char*>(s.x) + (token * s.xt + (begin + sub) * s.xh) * kSize;
-            const char* d_at = static_cast<const char*>(s.d) + (token * s.dt + (begin + sub) * s.dh) * kSize;
-            char* y_at = static_cast<char*>(s.y) + (token * s.yt + (begin + sub) * s.yh) * kSize;
-            auto fetch = [&](int p, int h) {
-                raw_x[p].load(x_at, lo_at, hi_at, h < end);
-                raw_d[p].load(d_at, lo_at, hi_at, h < end);
-                x_at += x_step, d_at += d_step;
+        if (left > 0) {
+            const int64_t first = w0 * share + min(w0, more);
+            int64_t token = first / each, next_token = token;  // of the row worked on, of the one fetched next
+            int h = (int)(first - token * each) * R + sub, next_h = h, to_fetch = left;
+            const Steps& step = g.steps[kKeys];  // from R heads to the next
+            const char *x_at, *d_at;
+            char* y_at;
+            auto place = [&](const void* p, int64_t t, int64_t at, int64_t hs, int head) {
+                return static_cast<const char*>(p) + (t * at + head * hs) * kSize;
             };
+            x_at = place(s.x, token, s.xt, s.xh, h), d_at = place(s.d, token, s.dt, s.dh, h);
+            y_at = const_cast<char*>(place(s.y, token, s.yt, s.yh, h));
+            auto fetch = [&](int to) {
+                ring.fetch(to, x_at, d_at, lo_at, hi_at, to_fetch > 0 && next_h < heads);
+                --to_fetch, next_h += R, x_at += step.x, d_at += step.d;
+                if (next_h >= each * R) {
+                    next_h = sub, ++next_token;
+                    x_at = place(s.x, next_token, s.xt, s.xh, sub), d_at = place(s.d, next_token, s.dt, s.dh, sub);
+                }
+            };
+            constexpr int kFirst = VEC ? Ring::kSlots - 1 : 1;
 #pragma unroll
-            for (int p = 0; p < AHEAD; ++p) fetch(p, begin + sub + p * R);
+            for (int p = 0; p < kFirst; ++p) fetch(p);
+            int slot = 0, into = kFirst;
+            bool good = true, next_good = true;
+            int next = (int)position_of(g, token, &next_good);
             Angles angles;
-            bool good;
-            const int64_t position = position_of(g, token, &good);  // (behind the first rows' loads)
-            if (turned) angles = angles_of(g.a.rope, position, u, -1.f);  // back
+            bool begins = true;
 #pragma unroll 1
-            for (int h0 = begin; h0 < end; h0 += AHEAD * R) {
+            for (; left > 0; --left) {
+                if (begins) {
+                    if (turned) angles = angles_of(g.a.rope, next, u, -1.f);  // back
+                    good = next_good, begins = false;
+                    ++token;
+                    if (token < g.a.tokens) next = (int)position_of(g, token, &next_good);
+                }
+                const bool in = h < heads && good;
+                Eight x, d;
+                ring.read(slot, x, d);
+                // (The slot written to is the one read last time, whose row has been stored since.)
+                fetch(into);
+                if constexpr (VEC) {
+                    into = slot, slot = slot + 1 == Ring::kSlots ? 0 : slot + 1;
+                }
+                if (turned) turn(g.a.rope, angles, d);
+                Eight gw;
 #pragma unroll
-                for (int p = 0; p < AHEAD; ++p) {
-                    const int hp = h0 + p * R, h = hp + sub;
-                    if (hp >= end) break;
-                    const bool in = h < end && good;
-                    Eight x = raw_x[p].unpack(), d = raw_d[p].unpack();
-                    fetch(p, h + AHEAD * R);
-                    if (turned) turn(g.a.rope, angles, d);
-                    Eight gw;
+                for (int e = 0; e < 4; ++e) gw.v[e] = fmul2(d.v[e], w.v[e]);
+                // Both sums at once; with u = x r, the second is that of g w u over r.
+                float r, back;
+                const float2 both = two_sums<U>(x, gw);
+                float mean = both.y * (1.f / D);
+                scales_of<D>(x, gw, both.x, g.a.eps, &mean, &r, &back);
+                scale_by(x, r);
+                mean *= -r;
+                if (in) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) gw.v[e] = fmul2(d.v[e], w.v[e]);
-                    // Both sums at once; with u = x r, the second is that of g w u over r.
-                    float r, back;
-                    const float2 both = two_sums<U>(x, gw);
-                    float mean = both.y * (1.f / D);
-                    scales_of<D>(x, gw, both.x, g.a.eps, &mean, &r, &back);
-                    scale_by(x, r);
-                    mean *= -r;
-                    if (in) {
+                    for (int e = 0; e < 4; ++e) dw.v[e] = ffma2(d.v[e], x.v[e], dw.v[e]);
+                }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) dw.v[e] = ffma2(d.v[e], x.v[e], dw.v[e]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x.v[e] = ffma2(x.v[e], make_float2(mean, mean), gw.v[e]);
-                    scale_by(x, r * back);
-                    if (in) store_row<DT, VEC>(y_at, lo_at, hi_at, x);
-                    y_at += y_step;
+                for (int e = 0; e < 4; ++e) x.v[e] = ffma2(x.v[e], make_float2(mean, mean), gw.v[e]);
+                scale_by(x, r * back);
+                if (in) store_row<DT, VEC>(y_at, lo_at, hi_at, x);
+                h += R, y_at += step.y;
+                if (h >= each * R) {
+                    h = sub, begins = true;
+                    y_at = const_cast<char*>(place(s.y, token, s.yt, s.yh, sub));
                 }
             }
         }
-        // The CTA's sums, the warps' and their rows' in order.
-        if (kKeys) __syncthreads();
+        // The CTA's sums, the warps' and their rows' in order (where the rings were).
+        if constexpr (VEC) cp_async_wait_all();
+        __syncthreads();
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             *reinterpret_cast<float2*>(&sums[warp * R + sub][(e < 2 ? lo : hi) + e % 2 * 2]) = dw.v[e];
         __syncthreads();
-        const int64_t cta = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, ctas = (int64_t)gridDim.x * gridDim.y;
         for (int d = threadIdx.x; d < D; d += 32 * kBackWarps) {
             float v = 0.f;
 #pragma unroll
             for (int j = 0; j < kBackWarps * R; ++j) v += sums[j][d];
-            g.parts[(kKeys * ctas + cta) * D + d] = v;
+            g.parts[(kKeys * (int64_t)gridDim.x + blockIdx.x) * D + d] = v;
         }
+        if (!kKeys) __syncthreads();
     };
     rows(std::false_type{});
     rows(std::true_type{});
@@ -400,16 +498,17 @@ cudaError_t forward(NormArgs& g, const LaunchCtx& c) {
 }
 template <int D, int DT>
 cudaError_t backward(NormArgs& g, float* dqw, float* dkw, const LaunchCtx& c) {
-    const unsigned parts = parts_of(g, 32 / (D / 8), 16 * c.sm_count);
-    const int64_t most = std::max<int64_t>(1, kBackCtas * c.sm_count / parts);
-    const dim3 grid((unsigned)std::min((g.a.tokens + kBackWarps - 1) / kBackWarps, most), parts);
-    const int64_t ctas = (int64_t)grid.x * grid.y;
+    constexpr int kHeads = 32 / (D / 8), kStep = kHeads * (int)dtype_size(DT);
+    g.steps[0] = {kStep * g.a.q_head_stride, kStep * g.dq_head, kStep * g.a.q_out_head_stride};
+    g.steps[1] = {kStep * g.a.k_head_stride, kStep * g.dk_head, kStep * g.a.k_out_head_stride};
+    const int64_t passes = g.a.tokens * ((std::max(g.a.heads, g.a.kv_heads) + kHeads - 1) / kHeads);
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>((passes + kBackWarps - 1) / kBackWarps, kBackCtas * c.sm_count));
     if (2 * ctas * D > c.ws_floats) return cudaErrorInvalidValue;
     g.parts = c.ws;
     if (g.vec)
-        norm_rope_backward_kernel<D, DT, kBackAhead, true><<<grid, 32 * kBackWarps, 0, c.stream>>>(g);
+        norm_rope_backward_kernel<D, DT, true><<<(unsigned)ctas, 32 * kBackWarps, 0, c.stream>>>(g);
     else
-        norm_rope_backward_kernel<D, DT, 1, false><<<grid, 32 * kBackWarps, 0, c.stream>>>(g);
+        norm_rope_backward_kernel<D, DT, false><<<(unsigned)ctas, 32 * kBackWarps, 0, c.stream>>>(g);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!dqw && !dkw)) return e;
     // Its launch overlaps the first kernel; it waits for that one's end on the device.
