@@ -121,7 +121,6 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
     const q4lin_kv4_cache_t& C = g.cache;
     const int Hkv = (int)C.kv_heads, group = (int)(g.a.heads / C.kv_heads), ps = g.page_shift;
     const int tile_shift = 6 - ps, ppt = 1 << tile_shift;  // pages per tile
-    griddep_launch_dependents();  // (the joining kernel waits for this one's end)
 
     if (tid == 0) {
         prefetch_tensormap(&maps.k);
@@ -132,6 +131,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
             for (int s = 0; s < kSlots; ++s) mbar_init(smem_u32(&S.full[w][s]), 1);
         mbar_init_fence();
     }
+    follow_stream();  // (the joining kernel, launched next, waits for this one's end)
     const int batch = (int)C.batch;
     const uint32_t sum = scan_tiles<R, W>(g, S.prefix, S.sums);
     // A list that would be too long is empty, and a share of all numbers tells the joining kernel
@@ -594,8 +594,7 @@ cudaError_t launch(SplitArgs& g, const SplitSize& size, const KvMaps& maps, cons
     g.list = reinterpret_cast<int*>(c.ws);
     g.parts = c.ws + kMaxBatch + 4;  // 16-byte aligned
     if ((int64_t)g.workers * 2 * R * (D + 2) + kMaxBatch + 4 > c.ws_floats) return cudaErrorInvalidValue;
-    kv4_attention_kernel<D, CT><<<(unsigned)grid, 32 * L::W, bytes, c.stream>>>(maps, g);
-    e = cudaGetLastError();
+    e = launch_early(kv4_attention_kernel<D, CT>, dim3((unsigned)grid), 32 * L::W, bytes, c.stream, maps, g);
     if (e != cudaSuccess) return e;
     return join_launch<D, R>(g, size, c);
 }

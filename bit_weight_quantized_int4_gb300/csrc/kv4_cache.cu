@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_append_kernel(const AppendArg
     constexpr int U = D / 8, R = 32 / U;  // lanes of a head, heads of a warp
     const q4lin_kv4_cache_t& C = g.cache;
     const int lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
+    follow_stream();
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && offsets_bad(g.a.offsets, C.batch, g.a.tokens))
         atomicCAS(g.status, 0, kStatusIndex);
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * g.tokens_each;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_read_kernel(const ReadArgs g)
     constexpr int U = D / 8, R = 32 / U;
     const q4lin_kv4_cache_t& C = g.cache;
     const int lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
+    follow_stream();
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && offsets_bad(g.a.offsets, C.batch, g.a.tokens))
         atomicCAS(g.status, 0, kStatusIndex);
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * g.tokens_each;
@@ -265,11 +267,8 @@ cudaError_t append(AppendArgs& g, bool vec, const LaunchCtx& c) {
     g.tokens_each = tokens_each(g.a.tokens, 2 * chunks, 32 * c.sm_count);
     const int64_t groups = (g.a.tokens + g.tokens_each - 1) / g.tokens_each;
     const dim3 grid((unsigned)((groups + kWarps - 1) / kWarps), chunks, 2);
-    if (vec)
-        kv4_append_kernel<D, DT, true><<<grid, 32 * kWarps, 0, c.stream>>>(g);
-    else
-        kv4_append_kernel<D, DT, false><<<grid, 32 * kWarps, 0, c.stream>>>(g);
-    return cudaGetLastError();
+    if (vec) return launch_early(kv4_append_kernel<D, DT, true>, grid, 32 * kWarps, 0, c.stream, g);
+    return launch_early(kv4_append_kernel<D, DT, false>, grid, 32 * kWarps, 0, c.stream, g);
 }
 template <int D, int DT>
 cudaError_t read(ReadArgs& g, const LaunchCtx& c) {
@@ -278,8 +277,7 @@ cudaError_t read(ReadArgs& g, const LaunchCtx& c) {
     g.tokens_each = tokens_each(g.a.tokens, kinds * chunks, 64 * c.sm_count);
     const int64_t groups = (g.a.tokens + g.tokens_each - 1) / g.tokens_each;
     const dim3 grid((unsigned)((groups + kWarps - 1) / kWarps), chunks, kinds);
-    kv4_read_kernel<D, DT><<<grid, 32 * kWarps, 0, c.stream>>>(g);
-    return cudaGetLastError();
+    return launch_early(kv4_read_kernel<D, DT>, grid, 32 * kWarps, 0, c.stream, g);
 }
 // f(head_dim, dtype) with both as types.
 template <typename F>

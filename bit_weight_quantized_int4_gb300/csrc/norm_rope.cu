@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormArgs g
     constexpr int U = D / 8, R = 32 / U, kSize = (int)dtype_size(DT);
     const int lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
     const int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    follow_stream();
     if (token >= g.a.tokens) return;
     bool turned, good = true, first = true;
     int lo, hi;
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(32 * kBackWarps, kBackCtas) norm_rope_backward
     __shared__ __align__(16) char shared[Ring::kBytes > kSums ? Ring::kBytes : kSums];
     float(*sums)[D] = reinterpret_cast<float(*)[D]>(shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = lane % U, sub = lane / U;
-    griddep_launch_dependents();  // (the kernel that joins the sums waits for this one's end)
+    follow_stream();  // (so does the kernel that joins the sums)
     bool turned;
     int lo, hi;
     rope_channels(g.a.rope, u, &turned, &lo, &hi);
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(1024) norm_rope_join_kernel(const float* parts
     __shared__ float sums[32][33];
     const int kind = blockIdx.y, column = threadIdx.x & 31, stretch = threadIdx.x >> 5, d = blockIdx.x * 32 + column;
     float* to = kind ? dkw : dqw;
-    griddep_wait();
+    follow_stream();
     if (!to) return;
     float v = 0.f;
 #pragma unroll 8
@@ -490,11 +491,8 @@ template <int D, int DT>
 cudaError_t forward(NormArgs& g, const LaunchCtx& c) {
     const unsigned parts = parts_of(g, 32 / (D / 8), 64 * c.sm_count);
     const dim3 grid((unsigned)((g.a.tokens + kWarps - 1) / kWarps), parts);
-    if (g.vec)
-        norm_rope_kernel<D, DT, kAhead, true><<<grid, 32 * kWarps, 0, c.stream>>>(g);
-    else
-        norm_rope_kernel<D, DT, 1, false><<<grid, 32 * kWarps, 0, c.stream>>>(g);
-    return cudaGetLastError();
+    if (g.vec) return launch_early(norm_rope_kernel<D, DT, kAhead, true>, grid, 32 * kWarps, 0, c.stream, g);
+    return launch_early(norm_rope_kernel<D, DT, 1, false>, grid, 32 * kWarps, 0, c.stream, g);
 }
 template <int D, int DT>
 cudaError_t backward(NormArgs& g, float* dqw, float* dkw, const LaunchCtx& c) {
@@ -505,23 +503,10 @@ cudaError_t backward(NormArgs& g, float* dqw, float* dkw, const LaunchCtx& c) {
     const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>((passes + kBackWarps - 1) / kBackWarps, kBackCtas * c.sm_count));
     if (2 * ctas * D > c.ws_floats) return cudaErrorInvalidValue;
     g.parts = c.ws;
-    if (g.vec)
-        norm_rope_backward_kernel<D, DT, true><<<(unsigned)ctas, 32 * kBackWarps, 0, c.stream>>>(g);
-    else
-        norm_rope_backward_kernel<D, DT, false><<<(unsigned)ctas, 32 * kBackWarps, 0, c.stream>>>(g);
-    cudaError_t e = cudaGetLastError();
+    const auto kernel = g.vec ? norm_rope_backward_kernel<D, DT, true> : norm_rope_backward_kernel<D, DT, false>;
+    const cudaError_t e = launch_early(kernel, dim3((unsigned)ctas), 32 * kBackWarps, 0, c.stream, g);
     if (e != cudaSuccess || (!dqw && !dkw)) return e;
-    // Its launch overlaps the first kernel; it waits for that one's end on the device.
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(D / 32, 2);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = c.stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_rope_join_kernel, (const float*)g.parts, (int)ctas, D, dqw, dkw);
+    return launch_early(norm_rope_join_kernel, dim3(D / 32, 2), 1024, 0, c.stream, (const float*)g.parts, (int)ctas, D, dqw, dkw);
 }
 
 NormArgs args_of(const q4lin_norm_rope_t& a, const LaunchCtx& c) {

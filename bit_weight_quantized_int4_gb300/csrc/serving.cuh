@@ -7,6 +7,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "../../include/q4lin.h"
 #include "ptx.cuh"
 
@@ -120,6 +122,30 @@ __device__ __forceinline__ void rope_channels(const q4lin_rope_t& r, int u, bool
     const bool halves = *turned && !r.interleaved;
     *lo = halves ? 4 * u : 8 * u;
     *hi = halves ? (int)(r.rotated / 2) + 4 * u : 8 * u + 4;
+}
+
+// Launch a kernel that may begin before the stream's last one has ended, and waits for that on the device
+// (follow_stream) before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t shared, cudaStream_t stream, A&&... args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+// The wait of such a kernel, by all of its threads (one that ended without it could end before what it
+// follows).  The next one may begin then, and no sooner: what comes before this kernel in the stream has
+// ended for it, too, which kernels that read their constant inputs before their own wait rely on.
+__device__ __forceinline__ void follow_stream() {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
 }
 
 __device__ __forceinline__ float ex2(float x) {
