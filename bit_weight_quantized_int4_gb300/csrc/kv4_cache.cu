@@ -10,10 +10,10 @@
 // rotation pairs).  More tokens a warp are fewer lookups, more warps hide more latency.
 //
 // Bound: memory, 4 and 4 1/2 bytes an element with fp32 for both.  Measured: 7 prompts of up to 2047
-// tokens (4510 in all, 8 heads of 128, fp32, rotated) appended in 12 us and read back in 12, a floor of 6
-// each: the lookups, the rotation and the codes of short launches; 65531 tokens read in bf16 in 57 us,
-// 340 MB, 0.88 of a copy's bandwidth (four heads a warp 75 us, one token a warp 92).  64 single
-// tokens 3.1 us for each: a launch.
+// tokens (4510 in all, 8 heads of 128, fp32, rotated) appended and read back in 23 us, a floor of 6
+// each: the lookups, the rotation and the codes of short launches; 65531 tokens read in bf16 in 56 us,
+// 340 MB, 0.89 of a copy's bandwidth (four heads a warp 75 us, one token a warp 92).  64 single
+// tokens 2.8 us for each: a launch.
 #include <algorithm>
 
 #include "q4lin_internal.h"
