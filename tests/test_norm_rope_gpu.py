@@ -266,3 +266,37 @@ def test_other_stream_and_graph(handle):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+@pytest.mark.parametrize("tokens,heads,kv_heads,dim,dtype,rotated,shift", [
+    (5003, 6, 2, 64, "bf16", 64, 0),     # rows of a pass that are not all heads
+    (2500, 7, 5, 128, "f32", 32, 0),     # an odd last pass of every token
+    (2600, 3, 1, 256, "f16", 256, 0),    # a pass a head
+    (5003, 6, 2, 64, "bf16", 64, 1),     # rows that no copy takes
+    (2500, 7, 5, 128, "f32", 0, 1),
+])
+def test_gradient_of_many_tokens(handle, tokens, heads, kv_heads, dim, dtype, rotated, shift):
+    """Shares of a warp that begin and end inside a token, some positions out of range among them."""
+    import torch
+    from bit_weight_quantized_int4_gb300 import q4lin
+    rng, q, k, weights, positions, rope = inputs(tokens, heads, kv_heads, dim, dtype, rotated)
+    if shift:
+        wide = torch.zeros(tokens, heads + kv_heads, dim + shift, dtype=q.dtype, device="cuda")
+        wide[..., shift:] = torch.cat([q, k], 1)
+        q, k = wide[:, :heads, shift:], wide[:, heads:, shift:]
+    d = [ops.to_device(rng.standard_normal(x.shape).astype(np.float32), dtype) for x in (q, k)]
+    kept = np.ones(tokens, bool)
+    if rope:
+        kept[[0, 7, tokens // 2, tokens - 1]] = False
+    at = np.where(kept, positions, 300).astype(np.int32)
+    outs = [torch.full(x.shape, 7.0, dtype=x.dtype, device="cuda") for x in (q, k)]
+    got = q4lin.norm_rope_backward(handle, q, k, *map(ops.to_device, weights), ops.to_device(at),
+                                   rope and tuple(map(ops.to_device, rope)), *d, eps=EPS, d_q=outs[0], d_k=outs[1])
+    for x, w, dy, dx, dw in zip((q, k), weights, d, got[:2], got[2:]):
+        x, dy, dx = ops.to_host(x), ops.to_host(dy), ops.to_host(dx)
+        assert np.all(dx[~kept] == 7)  # nothing is written for a position that is not in the table
+        want, want_w, size, size_w = kv4.norm_rope_backward(x[kept], w.astype(np.float64), positions[kept], rope, EPS,
+                                                            False, dy[kept])
+        near(torch.from_numpy(dx[kept]), want, 2.0**-19 * size + ops.ROUND[dtype] * np.abs(want) + ops.TINY[dtype])
+        near(dw, want_w, 400 * 2.0**-24 * size_w)
+    assert (status(handle) != 0) == (rope is not None)
