@@ -25,8 +25,9 @@
 // weight of a bf16 output takes one (its 11 bits are finer than the output's 8), and bf16
 // queries that are not rotated are exact in one.
 //
-// Few rows over many keys leave SMs idle: their walks over the keys are then cut into equal
-// parts, one CTA each, that a second kernel joins in the order of the keys.
+// Few rows over many keys leave SMs idle (and, over 4 bits, few more walks than SMs the last round's): their
+// walks over the keys are then cut into equal parts, one CTA each, that a second kernel joins in the order of
+// the keys.
 //
 // Bound: the products, 2 head_dim flops a pair for each of QT + PT terms.  Measured (8 key/value
 // heads of 128, 4 query heads each, the last 2048 of 8192 tokens): 240 us for rotated bf16
@@ -414,6 +415,12 @@ __device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, fl
     }
 }
 
+// What walks of `longest` steps cost in n parts: rounds of CTAs times their steps, with 4 more for what comes
+// before and after, 3 for a join.
+__host__ __device__ inline int64_t cost_of(int64_t walks, int64_t slots, int64_t longest, int64_t n) {
+    return (n * walks + slots - 1) / slots * ((longest + n - 1) / n + (n > 1 ? 7 : 4));
+}
+
 // One CTA, before the prompts' kernel: which pairs there are, and in how many parts their walks
 // are cut.
 constexpr int kPlanThreads = 256;
@@ -483,14 +490,13 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
     }
     if (warp != 0) return;
     for (int w = 0; w < kPlanThreads / 32; ++w) longest = max(longest, s_longest[w]);
-    // Walks in `parts` parts of `each` steps where whole ones leave SMs idle: the least rounds of
-    // CTAs times their steps, with 4 more for what comes before and after, 3 for a join.  Lane i
-    // weighs i + 1 and i + 33 parts.
+    // Walks in `parts` parts of `each` steps where whole ones leave SMs idle.  Lane i weighs i + 1 and
+    // i + 33 parts.
     uint32_t best = 0xFFFFFFFFu;
     for (int n = lane + 1; n <= g.most_parts; n += 32) {
         const int64_t units = (int64_t)n * pairs * Hkv;
         if (n > 1 && units > units_most) break;
-        const int64_t cost = (units + g.slots - 1) / g.slots * ((longest + n - 1) / n + (n > 1 ? 7 : 4));
+        const int64_t cost = cost_of((int64_t)pairs * Hkv, g.slots, longest, n);
         best = min(best, (uint32_t)min(cost, (int64_t)0x3FFFFFF) << 6 | (uint32_t)(n - 1));
     }
     const int parts = (int)(__reduce_min_sync(0xffffffffu, best) & 63u) + 1;
@@ -1343,7 +1349,18 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     g.plan = reinterpret_cast<int4*>(c.ws + kDrainSlots);
     g.parts = c.ws + head;
     g.most_parts = units <= c.sm_count ? 64 : 1;
-    const int64_t grid = g.most_parts == 1 ? units : std::min(std::max<int64_t>(units, 2 * c.sm_count), room);
+    int64_t grid = g.most_parts == 1 ? units : std::min(std::max<int64_t>(units, 2 * c.sm_count), room);
+    if (BITS == 4 && units > c.sm_count) {
+        // Where few more walks than SMs leave most SMs idle in the last round, too (1280 tokens, 4 heads on each
+        // of 8 of 128, 160 walks: after 6912 others in bf16 277 -> 254 us, in fp32 538 -> 432, after 64000
+        // 2300 -> 1618), if walks as long as the page table allows would be cut: the launch costs 3 us where the
+        // plan then finds that they are too short.
+        const int64_t longest = g.cache.pages_per_sequence * g.cache.page_size / kKeys + 1;
+        int64_t best = 1;
+        for (int64_t n = 2; n <= 64 && n * units <= room; ++n)
+            if (cost_of(units, g.slots, longest, n) < cost_of(units, g.slots, longest, best)) best = n;
+        g.most_parts = best > 1 ? 64 : 1, grid = best * units;
+    }
     if (grid < units) g.most_parts = 1;
     const int64_t ctas = std::max(grid, units);
     attention_prompt_plan_kernel<<<1, kPlanThreads, 0, c.stream>>>(g, (int)std::min<int64_t>(ctas, INT32_MAX));

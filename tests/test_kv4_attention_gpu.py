@@ -516,3 +516,18 @@ def test_a_layer(handle):
     torch.cuda.synchronize()
     assert torch.equal(held, out)
     assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype,window", [("f16", 0), ("f32", 9001), ("bf16", 0)])
+def test_walks_cut_where_the_last_round_is_short(handle, dtype, window):
+    """More walks than SMs, by few, over so many keys that they are cut; another sequence beside them."""
+    rng = np.random.default_rng(34)
+    lengths, counts = [34000, 300], [5100, 200]
+    host = kv4.Cache(rng, lengths, 8, 64, 64)
+    q = ops.to_device(rng.standard_normal((5300, 8, 64)).astype(np.float32), dtype)
+    out, lse = attend(handle, host, q, counts, lengths, 0.125, window=window)
+    check_rows(out, lse, host, q, 34000, 0.125, some(rng, 5100, 8, 30), dtype, count=5100, window=window)
+    check_rows(out, lse, host, q, 300, 0.125, some(rng, 200, 8, 30), dtype, b=1, first=5100, count=200, window=window)
+    again = attend(handle, host, q, counts, lengths, 0.125, window=window)
+    assert out.equal(again[0]) and lse.equal(again[1])
+    assert status(handle) == 0
