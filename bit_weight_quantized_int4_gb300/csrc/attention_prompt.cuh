@@ -41,7 +41,7 @@
 // idle at this size, and each has about 10 us around it: the queries, the first keys, the rows.
 // Cutting the last round's walks so that all SMs end together took as long (239 us, and the
 // joining kernel's time on top): busier SMs were slower ones.
-// Over 4 bits, the same prompt: 280 us for bf16 queries as they are (QT 1), 327 us rotated, 398 us for
+// Over 4 bits, the same prompt: 270 us for bf16 queries as they are (QT 1), 308 us rotated, 402 us for
 // fp16, 567 us for fp32; heads of 64, bf16, 211 us.  The tensor pipes are busy for 35 % of the first:
 // a tile's steps are a chain of softmax, values' product and next scores, and a scale for each key
 // lengthens the softmax.  (With the values' scales multiplied into the weights, as for the other types, 305
@@ -65,9 +65,17 @@ constexpr int kKeys = 128;  // keys per step
 // issues the MMAs.
 constexpr int kSoftWarps = 8, kValueWarp = 12, kIssueWarp = 16;
 constexpr int kWarps = 20, kThreads = 32 * kWarps;
-// Registers of their threads: launched with 96 each.
-constexpr int kSoftRegs = 176, kWidenRegs = 48, kIssueRegs = 32;
-static_assert(2 * kSoftRegs + 2 * kWidenRegs + kIssueRegs <= 5 * 96, "registers of the launch");
+// Registers of their threads: launched with 96 each.  Where values are multiplied by their scales as they are
+// widened and heads have 128 channels, the widening warps need more (softmax / widening 176 / 48, 168 / 56, 160 /
+// 64, 152 / 72, 2048 of 8192 tokens: 279, 272, 269, 310 us, rotated 326, 312, 306, 317; heads of 64 212, 214,
+// 220, 220; two terms of weights, fp16, 400, 405, 414).
+constexpr int kIssueRegs = 32;
+__host__ __device__ constexpr int soft_regs(int D, bool folded) { return folded && D == 128 ? 160 : 176; }
+__host__ __device__ constexpr int widen_regs(int D, bool folded) { return folded && D == 128 ? 64 : 48; }
+constexpr bool regs_fit(int D, bool folded) {
+    return 2 * soft_regs(D, folded) + 2 * widen_regs(D, folded) + kIssueRegs <= 5 * 96;
+}
+static_assert(regs_fit(128, true) && regs_fit(128, false), "registers of the launch");
 constexpr int kMaxBatch = 1024;  // sequences per launch
 constexpr int kScaleSlots = 5;  // steps whose scales are kept: the widening warps are up to four ahead
 constexpr float kBase = 7.f;    // weights are kept as 2^7 p ...
@@ -666,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
 
     if (warp < kSoftWarps) {
         // -------------------------------------------------------------- softmax
-        more_registers<kSoftRegs>();
+        more_registers<soft_regs(D, kFolded)>();
         const int tq = job.tq, len = job.len, row0 = job.row0, row_end = job.row_end;
         const int n = job.n, step0 = job.step0;
         const int tile = warp >> 2;
@@ -948,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         }
     } else if (warp < kIssueWarp) {
         // ------------------------- codes into fp16 blocks: keys, and values, 128 threads each
-        fewer_registers<kWidenRegs>();
+        fewer_registers<widen_regs(D, kFolded)>();
         const int n = job.n, step0 = job.step0, pages = (job.len + (1 << ps) - 1) >> ps;
         const int page_low = job.page_low;
         const int32_t* table = C.page_table + job.b * C.table_stride;
