@@ -43,10 +43,10 @@
 // joining kernel's time on top): busier SMs were slower ones.
 // Over 4 bits, the same prompt: 270 us for bf16 queries as they are (QT 1), 308 us rotated, 402 us for
 // fp16, 567 us for fp32; heads of 64, bf16, 211 us.  The tensor pipes are busy for 35 % of the first:
-// a tile's steps are a chain of softmax, values' product and next scores, and a scale for each key
-// lengthens the softmax.  (With the values' scales multiplied into the weights, as for the other types, 305
-// us; that without the keys' scales 267, without any 213.  Four rows a thread, by loads of 16 rows, with an
-// eighth of the reads of scales: 276 us, heads of 64 220.)
+// the softmax, with a scale for each key, and the widening take longer.  (With the values' scales multiplied
+// into the weights, as for the other types, 305 us; that without the keys' scales 267, without any 213.  Four
+// rows a thread, by loads of 16 rows, with an eighth of the reads of scales, against 279: 276 us, heads of 64
+// 220 against 211; with that, half steps whose next scores are computed meanwhile: 286.)
 #pragma once
 
 #include <algorithm>
