@@ -11,7 +11,8 @@
 //   one issuing thread  S = Q K^T into tensor memory, then O += P V with P read from there,
 //   softmax warps       one thread per row: the running maximum and sum in fp32, the weights
 //                       back into tensor memory over the scores that they came from.
-// The two tiles take turns: one's products run while the other's softmax does.
+// The two tiles take turns: one's products run while the other's softmax does.  (Heads of 256, over 4 bits:
+// one tile, whose outputs take the tensor memory of two.)
 //
 // The pages' scales stay out of the operands: a key page's multiplies its columns of S, a
 // value page's (over the largest of the walk) joins the exponent of its weights.  O is
@@ -42,7 +43,8 @@
 // Cutting the last round's walks so that all SMs end together took as long (239 us, and the
 // joining kernel's time on top): busier SMs were slower ones.
 // Over 4 bits, the same prompt: 270 us for bf16 queries as they are (QT 1), 308 us rotated, 402 us for
-// fp16, 567 us for fp32; heads of 64, bf16, 211 us.  The tensor pipes are busy for 35 % of the first:
+// fp16, 567 us for fp32; heads of 64, bf16, 211 us; the last 820 of 8192 tokens with heads of 256 359, 438,
+// 531 and 685 us (on the kernel for few rows 1570).  The tensor pipes are busy for 35 % of the first:
 // the softmax, with a scale for each key, and the widening take longer.  (With the values' scales multiplied
 // into the weights, as for the other types, 305 us; that without the keys' scales 267, without any 213.  Four
 // rows a thread, by loads of 16 rows, with an eighth of the reads of scales, against 279: 276 us, heads of 64
@@ -70,8 +72,8 @@ constexpr int kWarps = 20, kThreads = 32 * kWarps;
 // 64, 152 / 72, 2048 of 8192 tokens: 279, 272, 269, 310 us, rotated 326, 312, 306, 317; heads of 64 212, 214,
 // 220, 220; two terms of weights, fp16, 400, 405, 414).
 constexpr int kIssueRegs = 32;
-__host__ __device__ constexpr int soft_regs(int D, bool folded) { return folded && D == 128 ? 160 : 176; }
-__host__ __device__ constexpr int widen_regs(int D, bool folded) { return folded && D == 128 ? 64 : 48; }
+__host__ __device__ constexpr int soft_regs(int D, bool folded) { return D == 256 || (folded && D == 128) ? 160 : 176; }
+__host__ __device__ constexpr int widen_regs(int D, bool folded) { return D == 256 || (folded && D == 128) ? 64 : 48; }
 constexpr bool regs_fit(int D, bool folded) {
     return 2 * soft_regs(D, folded) + 2 * widen_regs(D, folded) + kIssueRegs <= 5 * 96;
 }
@@ -104,10 +106,13 @@ constexpr int64_t kDrainNs = 4000000000LL;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScoreCol = 256;  // O of the two tiles in columns 0 and 128, S from here
 
+// Rows of a CTA, a pair of tiles: of heads of 256 channels, whose outputs fill the columns of two, one tile.
+__host__ __device__ constexpr int pair_rows_of(int64_t D) { return D == 256 ? kQ : 2 * kQ; }
+
 struct PromptArgs {
     q4lin_kv_cache_t cache;
     q4lin_attention_t a;
-    int page_shift;
+    int page_shift, pair_rows;
     int64_t rows_min;  // sequences of more rows than this per key/value head are taken
     int q_vec;
     int slots, most_parts;  // CTAs that run at a time; parts of a walk at most
@@ -134,14 +139,14 @@ __device__ __forceinline__ Prompt prompt_of(const PromptArgs& g, int64_t b) {
     p.bad = o0 < 0 || o1 < o0 || o1 > g.a.tokens || o1 - o0 > g.a.max_query ||
             len > g.cache.pages_per_sequence << g.page_shift || (g.a.rope.cos && len > g.a.rope.positions);
     p.tq = (int)(o1 - o0), p.len = (int)(len > 0 ? len : 0);
-    p.pairs = !p.bad && rows > g.rows_min ? (int)((rows + 2 * kQ - 1) / (2 * kQ)) : 0;
+    p.pairs = !p.bad && rows > g.rows_min ? (int)((rows + g.pair_rows - 1) / g.pair_rows) : 0;
     return p;
 }
 // The steps over keys of a pair of row tiles: 128 first .. 128 last - 1.
 __device__ __forceinline__ void walk_of(const PromptArgs& g, const Prompt& p, int pair, int* first, int* last) {
-    const int group = (int)(g.a.heads / g.cache.kv_heads), rows = p.tq * group, row0 = pair * 2 * kQ;
+    const int group = (int)(g.a.heads / g.cache.kv_heads), rows = p.tq * group, row0 = pair * g.pair_rows;
     const int first_pos = p.len - p.tq + row0 / group;
-    const int last_pos = p.len - p.tq + (min(rows, row0 + 2 * kQ) - 1) / group;
+    const int last_pos = p.len - p.tq + (min(rows, row0 + g.pair_rows) - 1) / group;
     const int last_key = g.a.causal ? last_pos : p.len - 1;
     const int64_t low = g.a.window > 0 ? (int64_t)first_pos - g.a.window + 1 : 0;
     *first = low > 0 ? (int)(low / kKeys) : 0;
@@ -149,22 +154,24 @@ __device__ __forceinline__ void walk_of(const PromptArgs& g, const Prompt& p, in
 }
 template <int D>
 __device__ __forceinline__ float* part_at(const PromptArgs& g, int64_t unit) {
-    return g.parts + unit * (2 * kQ * (D + 2));
+    return g.parts + unit * (pair_rows_of(D) * (D + 2));
 }
 
 // Shared memory.  A step's K tile is D / 64 blocks of 64 channels, its V tile two blocks of 64
 // keys; both come and go by block through rings, as much as fits (three of each beside 128
-// channels of two terms: half a tile is widened while the other's products run).
+// channels of two terms: half a tile is widened while the other's products run; of heads of 256 one
+// block of values).
 template <int D, int QT, bool KEYED>
 struct Layout {
     static constexpr int kBlock = 128 * 128;           // 128 rows of 128 bytes
     static constexpr int kBlocks = D / 64;             // of a Q or K tile
     static constexpr int vBlock = D * 128;
-    static constexpr bool kTight = QT == 2 && D == 128;
+    static constexpr bool kTight = QT == 2 && D >= 128;
     // (KEYED: scales of each key and value take the place of a block of values.)
-    static constexpr int kRing = kTight ? 3 : 4, vRing = kTight && KEYED ? 2 : kRing;
+    static constexpr int kRing = kTight ? 3 : 4;
+    static constexpr int vRing = D == 256 ? (kTight ? 1 : 2) : kTight && KEYED ? 2 : kRing;
     static constexpr uint32_t q = 0;                                  // [tile][term][block]
-    static constexpr uint32_t k = q + 2 * QT * kBlocks * kBlock;      // [slot]
+    static constexpr uint32_t k = q + pair_rows_of(D) / kQ * QT * kBlocks * kBlock;      // [slot]
     static constexpr uint32_t v = k + kRing * kBlock;                 // [slot]
     static constexpr uint32_t bytes = v + vRing * vBlock;
 };
@@ -335,7 +342,7 @@ __device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, fl
     int cl, ch;
     rope_channels(g.a.rope, u, &turned, &cl, &ch);
     // Rows in batches whose loads are in flight together.
-    constexpr int kPasses = (2 * kQ + kPer - 1) / kPer, kTogether = 4;
+    constexpr int kRows = pair_rows_of(D), kPasses = (kRows + kPer - 1) / kPer, kTogether = 4;
 #pragma unroll 1
     for (int p0 = 0; p0 < kPasses && p0 * kPer < row_end - row0; p0 += kTogether) {
         float x[kTogether][8], c[kTogether][4], sn[kTogether][4];
@@ -344,7 +351,7 @@ __device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, fl
             const int r = (p0 + k) * kPer + tid / kUnitsRow, row = row0 + r;
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-            if (r < 2 * kQ && row < row_end) {
+            if (r < kRows && row < row_end) {
                 const int token = (uint32_t)row / (uint32_t)group, head = h * group + row - token * group;
                 const int64_t e = (o0 + token) * g.a.q_token_stride + head * g.a.q_head_stride;
                 const int position = len - tq + token;
@@ -376,7 +383,7 @@ __device__ __noinline__ void put_queries(const PromptArgs& g, uint8_t* gbase, fl
             const uint32_t up_bits = m == INFINITY ? 0x7FC00000u : (uint32_t)(127 + 14 - ex) << 23;
             const float up = copysignf(__uint_as_float(up_bits), g.a.scale);
             const float down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-            if (r < 2 * kQ) {
+            if (r < kRows) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_prompt_plan_kernel(con
                 // longer than `window`.  Else all walks end together, and the first pair's begins
                 // before the others.
                 walk_of(g, p, g.a.causal ? p.pairs - 1 : 0, &first, &last);
-                const int64_t window = (g.a.window + 2 * kQ / group + kKeys) / kKeys + 1;
+                const int64_t window = (g.a.window + g.pair_rows / group + kKeys) / kKeys + 1;
                 const bool behind = g.a.causal && g.a.window > 0;
                 longest = max(longest, behind ? (int)min((int64_t)p.len / kKeys + 1, window) : last - first);
             }
@@ -534,7 +541,7 @@ __device__ __forceinline__ int take_slot(const PromptArgs& g, int n, bool cut) {
 template <int D, int DT>
 __device__ __forceinline__ float* out_row(const PromptArgs& g, const volatile Job& job, int row, int r) {
     if (job.cut) return part_at<D>(g, blockIdx.x) + r * D;
-    if (DT != Q4LIN_DTYPE_F32) return g.parts + ((int64_t)job.slot * 2 * kQ + r) * D;
+    if (DT != Q4LIN_DTYPE_F32) return g.parts + ((int64_t)job.slot * pair_rows_of(D) + r) * D;
     const int group = (int)(g.a.heads / g.cache.kv_heads), token = row / group;
     const int64_t index = (job.o0 + token) * g.a.heads + job.h * group + (row - token * group);
     return static_cast<float*>(g.a.out) + index * D;
@@ -582,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     const int b = j0.x, tq = j0.y, len = j0.z, tile = j0.w;
     const int64_t o0 = j1.z;
     if (tid == 0) S.failed = 0;
-    const int rows = tq * group, row0 = tile * 2 * kQ;
-    const int row_end = min(rows, row0 + 2 * kQ);
+    const int rows = tq * group, row0 = tile * pair_rows_of(D);
+    const int row_end = min(rows, row0 + pair_rows_of(D));
     const int step0 = min(j1.x + part * each, j1.y), step1 = min(step0 + each, j1.y);
     const int n = step1 - step0;
     if (n == 0 && part > 0) return;  // a shorter walk has fewer parts
@@ -904,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             // bulk copy: rows stored by their threads took 6 us more.
             const bool wide = cut || DT == Q4LIN_DTYPE_F32;
             const uint32_t row_bytes = wide ? 4 * D : 2 * D, out = base + (uint32_t)r * (4 * D + 16);
-            static_assert(2 * kQ * (4 * D + 16) <= L::bytes, "the rows fit");
+            static_assert(pair_rows_of(D) * (4 * D + 16) <= L::bytes, "the rows fit");
             const float f = l == 0.f ? 0.f : cut ? v_ref : inv;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -949,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                 bulk_store(to, out, row_bytes);
             }
             if (in && cut) {
-                unit[2 * kQ * D + r] = m, unit[2 * kQ * D + 2 * kQ + r] = l;
+                unit[pair_rows_of(D) * D + r] = m, unit[pair_rows_of(D) * (D + 1) + r] = l;
             } else if (in && g.a.lse) {
                 g.a.lse[index] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l * kUnbase)) * kLn2 : -INFINITY;
             }
@@ -987,10 +994,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             [[maybe_unused]] const int count = keys ? 4 : D / 32;  // (8 bits) pieces per thread and block
             const uint32_t page_bytes = (uint32_t)(D * BITS / 8) << ps;
             [[maybe_unused]] const float inverse = 1.f / ref;
-            uint4 reg[BITS == 4 ? 2 : 4];
+            uint4 reg[BITS == 4 && D < 256 ? 2 : 4];
             // 16-byte chunks of a token's 4-bit codes; values' rows of a block that a thread has a chunk of.
             [[maybe_unused]] constexpr int kChunks = D / 32, kValueRows = D / 64;
-            [[maybe_unused]] float scale[2];  // of the values
+            [[maybe_unused]] float scale[D == 256 ? 4 : 2];  // of the values
             int pages_now = fetch_pages(0), pages_next = fetch_pages(1);
             auto load = [&](int page_ids, int blk) {
                 if constexpr (BITS == 4) {
@@ -1054,14 +1061,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                         }
                     } else {
                         // Rows of a key's 64 channels, as the products take them with this operand the other
-                        // way round; the second half of the channels in rows of their own behind the first,
-                        // written in another order so that all banks are.
-                        const int chunk = t % kChunks, half = chunk / 2;
+                        // way round; every further 64 channels in rows of their own behind the first, every
+                        // second 64 written in another order so that all banks are.
+                        const int chunk = t % kChunks, half = chunk / 2, odd = half % 2;
 #pragma unroll
                         for (int j = 0; j < kValueRows; ++j) {
                             const int row = t / kChunks + 128 / kChunks * j;
-                            const uint32_t w[4] = {half ? reg[j].z : reg[j].x, half ? reg[j].w : reg[j].y,
-                                                   half ? reg[j].x : reg[j].z, half ? reg[j].y : reg[j].w};
+                            const uint32_t w[4] = {odd ? reg[j].z : reg[j].x, odd ? reg[j].w : reg[j].y,
+                                                   odd ? reg[j].x : reg[j].z, odd ? reg[j].y : reg[j].w};
                             [[maybe_unused]] uint32_t hi, lo;
                             if constexpr (kFolded) {
                                 const float s = first + row < job.len ? scale[j] * inverse : 0.f;
@@ -1075,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
 #pragma unroll
                                     for (int n = 0; n < 4; ++n) f[n] = scaled_f16(f[n], hi, lo);
                                 }
-                                st_shared_v4(to + half * (64 * 128) + swizzled(row, chunk % 2 * 4 + (c ^ 2 * half)),
+                                st_shared_v4(to + half * (64 * 128) + swizzled(row, chunk % 2 * 4 + (c ^ 2 * odd)),
                                              prmt(f[0], f[1], 0x5410u), prmt(f[2], f[3], 0x5410u),
                                              prmt(f[0], f[1], 0x7632u), prmt(f[2], f[3], 0x7632u));
                             }
@@ -1211,7 +1218,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                     }
                     tc_fence_after();
                     // Of 16 keys: 32 bytes of a channel's row; or 16 rows, with the second half of the
-                    // channels (in the descriptor, where rows along the summed axis have a 1) 8 KB away.
+                    // channels (in the descriptor, where rows along the summed axis have a 1) 8 KB away, and so on.
                     constexpr uint32_t kStep = BITS == 4 ? 16 * 128 / 16 : 2, kOther = BITS == 4 ? 64 * 128 / 16 - 1 : 0;
                     const uint32_t v_low = low0 + (kOther << 16) + ((L::v + (uint32_t)slot * L::vBlock) >> 4);
 #pragma unroll
@@ -1262,8 +1269,10 @@ __device__ __forceinline__ void join_rows(const PromptArgs& g, int64_t unit0, in
                                           int64_t index0, int head0, int group) {
     const int lane = threadIdx.x & 31;
     const bool on = lane < D / 4;
+    // (128 channels at a time.)
 #pragma unroll 1
-    for (int r = r0; r < r0 + PER; r += ROWS) {
+    for (int v = 0; v < PER * (D == 256 ? 2 : 1); v += ROWS) {
+        const int r = r0 + v % PER, unit4 = v / PER * 32 + lane;
         float mx[ROWS], l[ROWS];
         float4 o[ROWS];
 #pragma unroll
@@ -1279,8 +1288,8 @@ __device__ __forceinline__ void join_rows(const PromptArgs& g, int64_t unit0, in
                 for (int q = 0; q < ROWS; ++q) {
                     pm[q][k] = -INFINITY, pl[q][k] = 0.f, po[q][k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (c + k < count && r + q < rows) {
-                        pm[q][k] = __ldcg(unit + 2 * kQ * D + r + q), pl[q][k] = __ldcg(unit + 2 * kQ * D + 2 * kQ + r + q);
-                        if (on) po[q][k] = __ldcg(reinterpret_cast<const float4*>(unit + (r + q) * D) + lane);
+                        pm[q][k] = __ldcg(unit + pair_rows_of(D) * D + r + q), pl[q][k] = __ldcg(unit + pair_rows_of(D) * (D + 1) + r + q);
+                        if (on) po[q][k] = __ldcg(reinterpret_cast<const float4*>(unit + (r + q) * D) + unit4);
                     }
                 }
             }
@@ -1307,12 +1316,12 @@ __device__ __forceinline__ void join_rows(const PromptArgs& g, int64_t unit0, in
             const int at = head0 + r + q, step = at / group;  // tokens from index0's
             const int64_t index = index0 + step * g.a.heads + (at - step * group);
             if (on && g.a.dtype == Q4LIN_DTYPE_F32)
-                reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + index * D)[lane] =
+                reinterpret_cast<float4*>(static_cast<float*>(g.a.out) + index * D)[unit4] =
                     make_float4(o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv);
             else if (on)
-                reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D)[lane] =
+                reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D)[unit4] =
                     make_uint2(to_16x2(o[q].x * inv, o[q].y * inv, g.a.dtype), to_16x2(o[q].z * inv, o[q].w * inv, g.a.dtype));
-            if (lane == 0 && g.a.lse)
+            if (unit4 == 0 && g.a.lse)
                 g.a.lse[index] = l[q] != 0.f ? ((mx[q] == -INFINITY ? 0.f : mx[q]) + lg2(l[q] * kUnbase)) * kLn2 : -INFINITY;
         }
     }
@@ -1321,14 +1330,14 @@ template <int D, int PER, int ROWS, int AHEAD>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_prompt_join_kernel(const PromptArgs g) {
     const int i = ((int)blockIdx.x * kJoinWarps + (int)(threadIdx.x >> 5)) * PER;
     const int Hkv = (int)g.cache.kv_heads, group = (int)(g.a.heads / g.cache.kv_heads);
-    const int u = i / (2 * kQ), r0 = i % (2 * kQ), h = u % Hkv;
+    const int u = i / pair_rows_of(D), r0 = i % pair_rows_of(D), h = u % Hkv;
     griddep_wait();
     // (The launch has no more pairs than the plan has room for: their records come with it.)
     const int pair = u / Hkv;
     const int4 plan = __ldcg(g.plan), j0 = __ldcg(g.plan + 1 + 2 * pair), j1 = __ldcg(g.plan + 2 + 2 * pair);
     const int parts = plan.x, each = plan.y;
     if (parts == 1 || pair >= plan.z) return;
-    const int row0 = j0.w * 2 * kQ, rows = min(j0.y * group - row0, 2 * kQ);
+    const int row0 = j0.w * pair_rows_of(D), rows = min(j0.y * group - row0, pair_rows_of(D));
     if (r0 >= rows) return;
     const int count = max(1, (j1.y - j1.x + each - 1) / each);
     // Row r is head head0 + r of the pair's first token, the heads of a group counted on.
@@ -1350,7 +1359,7 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     const int64_t units = std::max<int64_t>(1, pairs_most) * g.cache.kv_heads;
     const int64_t head = kDrainSlots + 4 + 8 * pairs_most;  // floats, a multiple of 4
     if (head > c.ws_floats / 2) return cudaErrorInvalidValue;
-    const int64_t room = (c.ws_floats - head) / (2 * kQ * (D + 2));
+    const int64_t room = (c.ws_floats - head) / (pair_rows_of(D) * (D + 2));
     g.slots = c.sm_count;
     g.pairs_most = (int)pairs_most;
     g.taken = reinterpret_cast<int*>(c.ws);
@@ -1399,10 +1408,10 @@ cudaError_t launch(PromptArgs& g, int64_t pairs_most, const LaunchCtx& c) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     if (g.a.tokens * g.a.heads <= 40 * c.sm_count) {
-        cfg.gridDim = dim3((unsigned)(units * (2 * kQ / kJoinWarps)));
+        cfg.gridDim = dim3((unsigned)(units * (pair_rows_of(D) / kJoinWarps)));
         return cudaLaunchKernelEx(&cfg, attention_prompt_join_kernel<D, 1, 1, 8>, g);
     }
-    cfg.gridDim = dim3((unsigned)(units * (2 * kQ / (4 * kJoinWarps))));
+    cfg.gridDim = dim3((unsigned)(units * (pair_rows_of(D) / (4 * kJoinWarps))));
     return cudaLaunchKernelEx(&cfg, attention_prompt_join_kernel<D, 4, 2, 4>, g);
 }
 
@@ -1428,21 +1437,24 @@ cudaError_t prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t
         g.wait_ns = c.wait_limit_ns;
         g.skip_first_copy = c.tc_skip_first_copy;
         // Pairs of all sequences at most: each taken one has more than rows_min rows.
-        const int64_t pairs = rows / (2 * kQ) + std::min(g.cache.batch, rows / (rows_min + 1));
-        const bool small = cache.head_dim == 64;
-        // One term where it is exact (see the head of this file).
-        constexpr int f32 = Q4LIN_DTYPE_F32, f16 = Q4LIN_DTYPE_F16, bf16 = Q4LIN_DTYPE_BF16;
+        g.pair_rows = pair_rows_of(cache.head_dim);
+        const int64_t pairs = rows / g.pair_rows + std::min(g.cache.batch, rows / (rows_min + 1));
         const bool few = cache.pages_per_sequence * cache.page_size <= kFewKeys;
-        if (a.dtype == bf16 && !a.rope.cos)
-            e = small ? launch<64, 1, 1, bf16, 0, BITS>(g, pairs, c) : launch<128, 1, 1, bf16, 0, BITS>(g, pairs, c);
-        else if (a.dtype == bf16)
-            e = small ? launch<64, 2, 1, bf16, 0, BITS>(g, pairs, c) : launch<128, 2, 1, bf16, 0, BITS>(g, pairs, c);
-        else if (a.dtype == f16 && few)
-            e = small ? launch<64, 2, 2, f16, 0, BITS>(g, pairs, c) : launch<128, 2, 2, f16, 0, BITS>(g, pairs, c);
-        else if (a.dtype == f16)
-            e = small ? launch<64, 2, 2, f16, kDrainF16, BITS>(g, pairs, c) : launch<128, 2, 2, f16, kDrainF16, BITS>(g, pairs, c);
-        else
-            e = small ? launch<64, 2, 2, f32, kDrainF32, BITS>(g, pairs, c) : launch<128, 2, 2, f32, kDrainF32, BITS>(g, pairs, c);
+        auto typed = [&](auto dim) {
+            // One term where it is exact (see the head of this file).
+            constexpr int f32 = Q4LIN_DTYPE_F32, f16 = Q4LIN_DTYPE_F16, bf16 = Q4LIN_DTYPE_BF16, D = decltype(dim)::value;
+            if (a.dtype == bf16 && !a.rope.cos) return launch<D, 1, 1, bf16, 0, BITS>(g, pairs, c);
+            if (a.dtype == bf16) return launch<D, 2, 1, bf16, 0, BITS>(g, pairs, c);
+            if (a.dtype == f16 && few) return launch<D, 2, 2, f16, 0, BITS>(g, pairs, c);
+            if (a.dtype == f16) return launch<D, 2, 2, f16, kDrainF16, BITS>(g, pairs, c);
+            return launch<D, 2, 2, f32, kDrainF32, BITS>(g, pairs, c);
+        };
+        if (cache.head_dim == 64)
+            e = typed(std::integral_constant<int, 64>{});
+        else if (cache.head_dim == 128)
+            e = typed(std::integral_constant<int, 128>{});
+        else if constexpr (BITS == 4)
+            e = typed(std::integral_constant<int, 256>{});
     }
     return e;
 }

@@ -23,7 +23,8 @@ constexpr int64_t kSplitRows = 48;
 // Over a 4-bit cache the prompts' kernel is ahead earlier with bf16, whose products have one term
 // each (the same sizes: one sequence of 8192 keys, 32 rows 28.5 / 29.4, 48 rows 42.5 / 31.5; of 65536, 24
 // rows 88 / 88, 48 rows 124 / 88; 8 of 2000, 32 rows 41 / 52, 48 rows 64 / 56; 32 of 4000, 32 rows 165 /
-// 189, 48 rows 230 / 200; fp32, 48 rows: 41 / 38, 121 / 152, 61 / 70, 228 / 327).
+// 189, 48 rows 230 / 200; fp32, 48 rows: 41 / 38, 121 / 152, 61 / 70, 228 / 327; heads of 256, bf16, 32 rows 35 /
+// 39, 147 / 132, 63 / 58, 48 rows 52 / 41, 209 / 134, 89 / 61; fp32, 48 rows 48 / 52, 206 / 225, 84 / 82).
 constexpr int64_t kSplitRows4Bf16 = 32;
 
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
@@ -262,7 +263,10 @@ q4lin_status_t run_attention(q4lin_handle_t h, const q4lin_kv_cache_t* cache, co
     // kernel takes its own (lengths are on the device).
     const int64_t by_rule = bits == 4 && a->dtype == Q4LIN_DTYPE_BF16 ? kSplitRows4Bf16 : kSplitRows;
     const int64_t split_rows = h->attention_split_rows > 0 ? h->attention_split_rows : by_rule;
-    const bool prompts = rows_longest > split_rows && q4lin::attention_prompt_eligible(*cache);
+    // (Heads of 256 have a record for each 128 rows: where those would not fit, the other kernel takes all.)
+    const bool eligible = bits == 4 ? cache->head_dim <= 128 || t / cache->kv_heads <= kRowsMost / 2
+                                    : q4lin::attention_prompt_eligible(*cache);
+    const bool prompts = rows_longest > split_rows && eligible;
     const bool split = !prompts || cache->batch > 1;
     const int64_t split_most = prompts ? split_rows : INT64_MAX;
     q4lin_attention_t args = *a;

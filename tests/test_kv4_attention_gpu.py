@@ -531,3 +531,40 @@ def test_walks_cut_where_the_last_round_is_short(handle, dtype, window):
     again = attend(handle, host, q, counts, lengths, 0.125, window=window)
     assert out.equal(again[0]) and lse.equal(again[1])
     assert status(handle) == 0
+
+
+WIDE = [  # heads of 256 in the prompts' kernel: lengths, counts, heads, kv heads, page, dtype, rotated, causal, window
+    ([130, 700, 64], [130, 333, 64], 6, 2, 16, "f32", 256, True, 0),
+    ([401, 5, 130], [129, 5, 130], 8, 8, 64, "bf16", 0, True, 0),
+    ([900, 0, 333], [64, 0, 200], 7, 1, 32, "f16", 64, True, 100),
+    ([257, 1], [100, 1], 4, 4, 64, "bf16", 256, False, 0),
+    ([3000], [70], 4, 1, 64, "bf16", 0, True, 0),       # walks that are cut
+    ([3100], [40], 8, 2, 16, "f32", 128, True, 2500),
+    ([2500], [129], 2, 1, 32, "f16", 0, True, 0),
+    ([1300, 1200], [50, 1200], 2, 2, 64, "f32", 0, True, 0),  # outputs taken out on the way
+]
+
+
+@pytest.mark.parametrize("lengths,counts,heads,kv_heads,page,dtype,rotated,causal,window", WIDE)
+def test_prompts_of_wide_heads(handle, split, lengths, counts, heads, kv_heads, page, dtype, rotated, causal, window):
+    results = []
+    for rows in BOTH:
+        split(rows)
+        results.append(run(handle, lengths, counts, heads, kv_heads, page, 256, dtype, rotated=rotated, causal=causal,
+                           window=window))
+        check(*results[-1])
+        assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype,n,tokens", [("f16", 34000, 90), ("f32", 9000, 2600), ("bf16", 9000, 2600)])
+def test_many_keys_of_wide_heads(handle, split, dtype, n, tokens):
+    """Few walks in parts, and more walks than SMs; with outputs taken out."""
+    split(1)
+    rng = np.random.default_rng(n)
+    host = kv4.Cache(rng, [n], 8, 64, 256)
+    q = ops.to_device(rng.standard_normal((tokens, 8, 256)).astype(np.float32), dtype)
+    out, lse = attend(handle, host, q, [tokens], [n], 0.0625)
+    check_rows(out, lse, host, q, n, 0.0625, some(rng, tokens, 8, 30), dtype)
+    again = attend(handle, host, q, [tokens], [n], 0.0625)
+    assert out.equal(again[0]) and lse.equal(again[1])
+    assert status(handle) == 0
