@@ -544,7 +544,7 @@ Q4LIN_API q4lin_status_t q4lin_run_kv4_read(q4lin_handle_t handle, const q4lin_k
  * results.  Codes are exact in the tensor cores' fp16 operands here too; the keys' scales
  * multiply the scores and the values' scales the probabilities, in fp32.  One exception:
  * where bfloat16 outputs come from the kernel for many query rows, a value times its scale
- * (over the largest of the keys that its 256 rows read, at most a power of two more) is
+ * (over the largest of the keys that its 256 rows, 128 of heads of 256, read, at most a power of two more) is
  * rounded to fp16 once, 11 bits like the probability that it meets. */
 Q4LIN_API q4lin_status_t q4lin_run_kv4_attention(q4lin_handle_t handle,
                                                  const q4lin_kv4_cache_t* cache,
