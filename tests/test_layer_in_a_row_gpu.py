@@ -86,8 +86,10 @@ def test_steps_without_a_pause(handle, heads, kv_heads, dim, dtype, lengths):
     assert all(bool(torch.isfinite(t).all()) for t in want[-1])
 
 
-def test_weights_that_were_just_written(handle):
-    """A linear whose codes the stream wrote two kernels ago, a norm between them."""
+@pytest.mark.parametrize("early", [0, 1])
+def test_weights_that_were_just_written(handle, early):
+    """A linear whose codes the stream wrote two kernels ago, a norm between them; the linear may begin
+    while the norm runs, but not before the codes are there."""
     import torch
     from bit_weight_quantized_int4_gb300 import q4lin
     torch.manual_seed(2)
@@ -109,8 +111,12 @@ def test_weights_that_were_just_written(handle):
 
     want = [step(latent, torch.cuda.synchronize) for latent in latents]
     assert not torch.equal(*want)
-    for i in range(60):
-        assert torch.equal(step(latents[i % 2], lambda: None), want[i % 2])
+    handle.set_option(q4lin.Q4LIN_OPT_PDL, early)
+    try:
+        got = [step(latents[i % 2], lambda: None) for i in range(60)]
+    finally:
+        handle.set_option(q4lin.Q4LIN_OPT_PDL, 0)
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
 
 
 def test_binding_refuses(handle):
