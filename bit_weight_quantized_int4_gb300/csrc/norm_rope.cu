@@ -292,18 +292,16 @@ template <int DT, bool VEC>
 struct Rows {
     static constexpr int kSlots = VEC ? kBackSlots / (DT == Q4LIN_DTYPE_F32 ? 2 : 1) : 1, kGroup = DT == Q4LIN_DTYPE_F32 ? 16 : 8;
     static constexpr int kBytes = VEC ? kSlots * 4 * kGroup * 32 * kBackWarps : 0;
-    uint32_t ring;  // the lane's first group of the slot read next; groups lie 32 lanes apart
-    int slot;
+    uint32_t ring;  // the lane's first group of slot 0; groups lie 32 lanes apart
     Raw<DT, VEC> x, d;
 
     __device__ __forceinline__ void init(void* shared) {
         if constexpr (VEC) {
             const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
             ring = smem_u32(shared) + (warp * kSlots * 4 * 32 + lane) * kGroup;
-            slot = 0;
         }
     }
-    // Into slot `to`.
+    // Into slot `to` (rows that there are not leave what was there, which nobody uses).
     __device__ __forceinline__ void fetch(int to, const char* px, const char* pd, int lo, int hi, bool in) {
         if constexpr (VEC) {
             const uint32_t at = ring + to * (4 * 32 * kGroup);
