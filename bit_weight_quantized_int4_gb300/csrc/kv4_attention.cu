@@ -345,8 +345,9 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                 const int left = P.len - tile_key - scale_key;
                 float4 v = scales_next;
                 v.x = left > 0 ? v.x : 0.f, v.y = left > 1 ? v.y : 0.f, v.z = left > 2 ? v.z : 0.f, v.w = left > 3 ? v.w : 0.f;
+                // (The largest by their bits, where a -0 would pass for more than any.)
                 const float most = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-                const uint32_t ex = min(max(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(most)) >> 23, 1u), 253u);
+                const uint32_t ex = min(max(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(fabsf(most))) >> 23, 1u), 253u);
                 sv_unit = __uint_as_float(ex << 23);
                 const float inverse = lane < 16 ? 1.f : __uint_as_float((254u - ex) << 23);
                 v.x *= inverse, v.y *= inverse, v.z *= inverse, v.w *= inverse;
