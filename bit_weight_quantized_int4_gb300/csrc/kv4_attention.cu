@@ -34,9 +34,10 @@ __host__ __device__ constexpr int warps_of(int D, int CT) {
     return D == 64 ? (CT <= 2 ? 12 : 8) : D == 128 && CT == 1 ? 12 : 8;
 }
 
-// Weights are kept as 2^4 p, p by a maximum that scores may have passed by up to 2^10: in a product
-// with a value's scale, below 2, they stay below fp16's 65504, and what two terms leave is 2^-28 of the
-// largest weight.
+// Weights are kept as 2^4 p, p by a maximum that scores may have passed by up to 2^10.  For the product
+// with the values' codes a row's, times the values' scales, are brought to fp16's upper range by a power
+// of two for each tile: of the largest of them, in which only keys that the row sees have a part, so that
+// two terms leave 2^-22 of that however small a value is beside those that the row does not see.
 constexpr float kFewBits = 4.f, kUnfew = 1.f / 16.f, kMostWeight = 16384.f;
 
 struct KvMaps {
@@ -47,7 +48,7 @@ template <int D, int CT>
 struct Mine {  // of one warp
     uint2 q[CT][D / 16][32];  // B fragments
     RowInfo row[CT * 4];
-    float scales[2][kTile];  // of a tile's keys and values (these over a power of two near the largest)
+    float scales[2][kTile];  // of a tile's keys and values
 };
 template <int D, int CT>
 struct Layout {
@@ -339,18 +340,11 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
         for (int i = 0; i < cnt; ++i) {
             const int tile_key = (first + i) * kTile;
             // The tile's scales, through shared memory to the lanes that want them; 0 for keys behind the
-            // sequence, whose slots may hold anything.  Values' over a power of two: sv_unit.
-            float sv_unit;
+            // sequence, whose slots may hold anything.
             {
                 const int left = P.len - tile_key - scale_key;
                 float4 v = scales_next;
                 v.x = left > 0 ? v.x : 0.f, v.y = left > 1 ? v.y : 0.f, v.z = left > 2 ? v.z : 0.f, v.w = left > 3 ? v.w : 0.f;
-                // (The largest by their bits, where a -0 would pass for more than any.)
-                const float most = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-                const uint32_t ex = min(max(__reduce_max_sync(0xffffffffu, lane < 16 ? 0u : __float_as_uint(fabsf(most))) >> 23, 1u), 253u);
-                sv_unit = __uint_as_float(ex << 23);
-                const float inverse = lane < 16 ? 1.f : __uint_as_float((254u - ex) << 23);
-                v.x *= inverse, v.y *= inverse, v.z *= inverse, v.w *= inverse;
                 *reinterpret_cast<float4*>(&mine.scales[lane >> 4][scale_key]) = v;
                 fetch_scales();
                 fetch_page(i + 2);
@@ -416,6 +410,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
             scales_of(1, sv);
             const bool inside = tile_key >= low_max && tile_key + kTile - 1 <= limit_min;
             uint2 pf[CT][4];  // B fragments
+            float unit[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 float2 x[4], p[4];
@@ -456,10 +451,22 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                     weights();
                 }
                 float2 sum = make_float2(0.f, 0.f);
+                most = 0.f;
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     sum = fadd2(sum, p[m]);
                     p[m] = fmul2(p[m], sv[m]);
+                    most = fmaxf(fmaxf(most, fabsf(p[m].x)), fabsf(p[m].y));
+                }
+                // The largest of the row (a lane's other columns are other rows) to [2^14, 2^15).
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                const uint32_t ex = min(max(__float_as_uint(most) >> 23, 15u), 254u);
+                const float up = __uint_as_float((268u - ex) << 23);
+                unit[ct] = __uint_as_float((ex - 14u) << 23);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    p[m] = fmul2(p[m], make_float2(up, up));
                     // Rows of a transposed fragment: both terms of a key's weight.
                     uint32_t hi, lo;
                     split_f16(p[m].x, p[m].y, &hi, &lo);
@@ -473,7 +480,6 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
 
             // ---- outputs: 64 channels at a time, the tile's 64 keys in 4 steps
             const uint32_t v_at = ring + v_slot * L::codes;
-            const float2 unit2 = make_float2(sv_unit, sv_unit);
 #pragma unroll
             for (int c0 = 0; c0 < kChunks; c0 += 2) {
                 float acc[CT][4][4];
@@ -508,7 +514,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         const float2 v = make_float2(acc[ct][n][0] + acc[ct][n][1], acc[ct][n][2] + acc[ct][n][3]);
-                        O[ct][2 * c0 + n] = ffma2(v, unit2, O[ct][2 * c0 + n]);
+                        O[ct][2 * c0 + n] = ffma2(v, make_float2(unit[ct], unit[ct]), O[ct][2 * c0 + n]);
                     }
             }
             __syncwarp();

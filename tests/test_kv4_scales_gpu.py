@@ -8,9 +8,10 @@ import pytest
 from tests import _kv4 as kv4
 from tests import _operators as ops
 from tests.test_attention_gpu import check, status
-from tests.test_kv4_attention_gpu import BOTH, attend, handle, split  # noqa: F401 (fixtures)
+from tests.test_kv4_attention_gpu import BOTH, attend, check_rows, handle, some, split  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
+KERNELS = 1 << 40,  # as BOTH: the one for few rows
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -34,4 +35,65 @@ def test_scales_of_minus_zero(handle, split, tokens, dim, dtype):
             check(*results[-1], want, dtype)
     for plus, minus in zip(results[:2], results[2:]):
         assert all(torch.equal(a, b) for a, b in zip(plus, minus))
+    assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("apart", [12, 20, 30, 60])
+@pytest.mark.parametrize("tokens,n,window", [(300, 300, 1), (40, 300, 2), (300, 300, 8), (3, 200, 2), (9, 130, 3)])
+def test_rows_that_see_small_values_only(handle, split, tokens, n, window, apart, dim, dtype):
+    """Every other four tokens' values are 2^apart smaller, so that some rows' windows see those only."""
+    rng = np.random.default_rng(72)
+    host = kv4.Cache(rng, [n], 1, 32, dim)
+    small = np.arange(host.vs.shape[2]) // 4 % 2 == 0
+    host.vs[..., small] *= np.float32(2.0**-apart)
+    q = ops.to_device(rng.standard_normal((tokens, 2, dim)).astype(np.float32), dtype)
+    want = ops.attention(host, ops.to_host(q), [0, tokens], [n], 0.125, window=window)
+    for rows in KERNELS:
+        split(rows)
+        check(*attend(handle, host, q, [tokens], [n], 0.125, window=window), want, dtype)
+    assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("apart", [9, 20, 30, 60])
+@pytest.mark.parametrize("tokens", [7, 300])
+def test_small_values_before_large_ones(handle, split, tokens, apart, dim, dtype):
+    """A prompt whose first half has small values: its rows must not depend on the ones behind them."""
+    rng = np.random.default_rng(73)
+    host = kv4.Cache(rng, [tokens], 2, 16, dim)
+    slots = host.table[0, :-(-tokens // 16)]
+    at = np.arange(len(slots) * 16).reshape(len(slots), 1, 16)
+    host.vs[slots] *= np.where(at < tokens // 2, 2.0**-apart, 1.0).astype(np.float32)
+    host.vs[slots] *= np.where(at % 11 == 5, 0.0, 1.0).astype(np.float32)
+    q = ops.to_device(rng.standard_normal((tokens, 6, dim)).astype(np.float32), dtype)
+    want = ops.attention(host, ops.to_host(q), [0, tokens], [tokens], 0.125)
+    for rows in KERNELS:
+        split(rows)
+        check(*attend(handle, host, q, [tokens], [tokens], 0.125), want, dtype)
+    assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype,dim,tokens,n,heads", [
+    ("f32", 64, 3000, 3000, 16), ("bf16", 64, 3000, 3000, 16), ("f16", 128, 300, 3000, 4),  # whole walks, cut ones
+    ("bf16", 128, 300, 3000, 4), ("f32", 256, 40, 5000, 2), ("bf16", 256, 40, 5000, 2)])
+def test_values_that_grow(handle, split, dtype, dim, tokens, n, heads):
+    """Values that grow by 2^50 along the sequence, so that every row's largest one is among its last; and
+    shrink, so that the last rows' windows see small ones."""
+    rng = np.random.default_rng(74)
+    host = kv4.Cache(rng, [n], heads, 64, dim)
+    slots = host.table[0, :-(-n // 64)]
+    at = np.arange(len(slots) * 64).reshape(len(slots), 1, 64)
+    base = host.vs.copy()
+    q = ops.to_device(rng.standard_normal((tokens, heads, dim)).astype(np.float32), dtype)
+    pairs = some(rng, tokens, heads, 40)
+    for grows, window in ((True, 0), (False, 60), (True, 60)):
+        power = at / n * 50 - 50 if grows else -at / n * 50
+        host.vs[slots] = base[slots] * (2.0**power).astype(np.float32)
+        for rows in KERNELS:
+            split(rows)
+            out, lse = attend(handle, host, q, [tokens], [n], 0.125, window=window)
+            check_rows(out, lse, host, q, n, 0.125, pairs, dtype, window=window)
     assert status(handle) == 0
