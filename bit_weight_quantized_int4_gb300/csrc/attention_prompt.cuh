@@ -20,7 +20,8 @@
 // leaves room for.  4-bit codes have a scale for each token: a key's multiplies its column of S, read
 // from shared memory by every softmax warp.  A value's (over the largest of the walk) multiplies
 // its weights in the same way where those have two terms; for bf16 outputs, where they have one,
-// code - 8 times the scale is rounded to fp16 once as it is widened (11 bits as the weight's).
+// code - 8 times the scale is rounded to fp16 once as it is widened (11 bits as the weight's).  Walks whose values' scales
+// are so far apart that fp16 would lose small ones (kWideFolded) take the scales' exponents into the weights'.
 // Queries and weights enter as QT and PT fp16 terms, the rounded value and
 // what the rounding left (22 bits), each term a product of its own: two of both in general; a
 // weight of a bf16 output takes one (its 11 bits are finer than the output's 8), and bf16
@@ -52,6 +53,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "q4lin_internal.h"
 #include "serving.cuh"
@@ -102,6 +104,16 @@ constexpr float kLeastFactor = 1e-37f;
 // (4 bits) Weights of a step that add up to no more than this are below fp16's 65504 each.
 constexpr float kMostSum = 65000.f;
 constexpr float kLeastRatio = 5.421010862427522e-20f;  // 2^-64
+// (4 bits) A walk whose values' scales are further apart than this is wide.  fp16 has room for two terms
+// of weights down to 2^-32 of the largest, and for folded values' 11 bits down to 2^-25 of the largest scale.
+// Beyond, a row that sees only small values beside large ones behind it, or before its window, would lose them.
+// In a wide walk the exponents of the values' scales join those of the weights, so that a row's maximum, a
+// whole number there, is that of the products, which have the upper end of fp16's range; and values are not
+// folded.  What is below 2^-80 of the walk's largest scale counts as that in the maximum, so that the sum of
+// the weights alone stays in fp32's range.  (Such walks take 1.4 to 3.5 times as long: 2048 of 8192 tokens in
+// bf16 819 us, in fp32 1026.)
+constexpr float kWideFolded = 16777216.f, kWideWeights = 1024.f;  // 2^24, 2^10
+constexpr int kLeastExponent = -80;
 constexpr int64_t kDrainNs = 4000000000LL;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScoreCol = 256;  // O of the two tiles in columns 0 and 128, S from here
@@ -208,7 +220,7 @@ struct PromptShared {
     float factor[2 * kQ];
     StepScales<D, KEYED> scales;
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2];
-    float v_max[kWarps];
+    float v_max[kWarps], v_min[kWarps];  // (4 bits) v_min: of those above 0
     int failed;
     uint32_t tmem;
 };
@@ -291,6 +303,26 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
         "cp.async.bulk.wait_group 0;" ::"l"(reinterpret_cast<uint64_t>(dst)),
         "r"(src), "r"(bytes)
         : "memory");
+}
+// Values' scales over the walk's reference, taken apart: exponent, 2^-exponent, and what that leaves, at most 1.
+struct Apart2 {
+    float2 exponent, inverse, rest;
+};
+__device__ __forceinline__ Apart2 apart2(float2 ratio) {
+    auto exponent = [](float r) { return min(max((int)(__float_as_uint(r) >> 23 & 255u) - 126, kLeastExponent), 126); };
+    const int a = exponent(ratio.x), b = exponent(ratio.y);
+    Apart2 p;
+    p.exponent = make_float2((float)a, (float)b);
+    p.inverse = make_float2(__uint_as_float((uint32_t)(127 - a) << 23), __uint_as_float((uint32_t)(127 - b) << 23));
+    p.rest = fmul2(ratio, p.inverse);
+    return p;
+}
+// m + log2(l); the exponent of an l far from 1 (of weights whose values' scales are far apart) is added apart,
+// as lg2's result would be rounded where m cancels it.
+__device__ __forceinline__ float log2_sum(float m, float l) {
+    if (!(l >= 4294967296.f && l <= 3.4028235e38f)) return m + lg2(l);
+    const uint32_t bits = __float_as_uint(l);
+    return m + (float)((int)(bits >> 23) - 127) + lg2(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
 }
 // This thread's number, read where it stands.
 __device__ __forceinline__ int thread_number() {
@@ -618,29 +650,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     }
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&S.tmem), kTmemCols);
     float v_max = 0.f;
-    for (int p = max((step0 * kKeys) >> ps, page_low) + tid; p < min(pages, (step1 * kKeys) >> ps); p += kThreads) {
-        const int id = __ldg(table + p);
-        if (id < 0 || id >= C.num_pages)
-            atomicCAS(g.status, 0, kStatusIndex);
-        else if constexpr (BITS == 8)
-            v_max = fmaxf(v_max, __ldg(C.v_scales + (int64_t)id * Hkv + h));
-        else {
-            const int64_t at = ((int64_t)id * Hkv + h) << ps;
-            const int left = len - (p << ps);  // (what is behind the sequence may be anything)
-            auto largest = [&](const float* s, int e, float old) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(s + at + e));
-                return fmaxf(old, fmaxf(fmaxf(e < left ? v.x : 0.f, e + 1 < left ? v.y : 0.f),
-                                        fmaxf(e + 2 < left ? v.z : 0.f, e + 3 < left ? v.w : 0.f)));
-            };
+    [[maybe_unused]] float v_min = INFINITY;
+    const int page_first = max((step0 * kKeys) >> ps, page_low), page_last = min(pages, (step1 * kKeys) >> ps);
+    if constexpr (BITS == 8) {
+        for (int p = page_first + tid; p < page_last; p += kThreads) {
+            const int id = __ldg(table + p);
+            if (id < 0 || id >= C.num_pages)
+                atomicCAS(g.status, 0, kStatusIndex);
+            else
+                v_max = fmaxf(v_max, __ldg(C.v_scales + (int64_t)id * Hkv + h));
+        }
+    } else {
+        // Four tokens' scales a thread.
+        const int fours = ps - 2;
 #pragma unroll 4
-            for (int e = 0; e < 1 << ps; e += 4) {
-                v_max = largest(C.v_scales, e, v_max);
+        for (int i = (page_first << fours) + tid; i < page_last << fours; i += kThreads) {
+            const int p = i >> fours, e = (i & ((1 << fours) - 1)) * 4, id = __ldg(table + p);
+            const int left = len - (p << ps) - e;  // (what is behind the sequence may be anything)
+            if (id < 0 || id >= C.num_pages) {
+                atomicCAS(g.status, 0, kStatusIndex);
+            } else {
+                const float4 s = __ldg(reinterpret_cast<const float4*>(C.v_scales + (((int64_t)id * Hkv + h) << ps) + e));
+                const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float x = n < left ? v[n] : 0.f;
+                    v_max = fmaxf(v_max, x), v_min = fminf(v_min, x > 0.f ? x : INFINITY);
+                }
             }
         }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) v_max = fmaxf(v_max, __shfl_xor_sync(0xffffffffu, v_max, o));
     if (lane == 0) S.v_max[warp] = v_max;
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v_min = fminf(v_min, __shfl_xor_sync(0xffffffffu, v_min, o));
+        if (lane == 0) S.v_min[warp] = v_min;
+    }
     put_queries<D, QT, DT, BITS>(g, gbase, S.factor, o0, h, tq, len, row0, row_end);
     }
     fence_async_shared();  // the queries are read by the tensor cores
@@ -662,6 +709,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         for (int w = 0; w < kWarps; ++w) v = fmaxf(v, const_cast<volatile float&>(S.v_max[w]));
         if constexpr (kFolded) return __uint_as_float(min(max((int)(__float_as_uint(v) >> 23) - 11, 1), 253) << 23);
         return v > 0.f ? v : 1.f;  // 1: values that are all zero
+    };
+    // (By a whole warp; positive floats are ordered as their bits.)
+    auto wide_walk = [&]() {
+        if constexpr (BITS == 8) return false;
+        const uint32_t most = __reduce_max_sync(0xffffffffu, lane < kWarps ? __float_as_uint(S.v_max[lane]) : 0u);
+        const uint32_t least = __reduce_min_sync(0xffffffffu, lane < kWarps ? __float_as_uint(S.v_min[lane]) : 0x7F800000u);
+        return __uint_as_float(least) * (kFolded ? kWideFolded : kWideWeights) < __uint_as_float(most);
     };
     volatile int* failed = &S.failed;
     auto bar = [](uint64_t& x) { return smem_u32(&x); };
@@ -699,57 +753,220 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         float m = -INFINITY, l = 0.f, m_out = -INFINITY;  // m_out: of what was taken out
         bool ok = true;
         const int steps = tile == 0 || row_end - row0 > kQ ? n : 0;
-        for (int i = 0; i < steps; ++i) {
-            ok = __all_sync(0xffffffffu, wait(S.s_full[tile], i & 1));
-            if (!ok) break;
-            tc_fence_after();
-            const int key0 = (step0 + i) * kKeys, slot = i % Scales::kSlots;
-            const int hi = min(limit - key0, kKeys), lo = max(low - key0, 0);
-            if constexpr (kFolded) {
-                // The scores in quarters, the next one on its way.  The weights by the maximum that there
-                // is: as long as their sum stays in fp16's range, so does each of them, and no maximum is
-                // looked for.  They wait in registers until that is known; rows that have seen nothing yet
-                // and those whose sum has grown too far (each for itself) get a new maximum first.
-                const float4* ks = reinterpret_cast<const float4*>(S.scales.k_scale[slot]);
-                const float2 factor2 = make_float2(factor, factor), least2 = make_float2(kLeastFactor, kLeastFactor);
-                const bool masked = __any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0);
-                auto quarters = [&](auto&& take) {  // take(quarter, its 32 scores)
-                    uint32_t x[2][32];
-                    tmem_ld32_async(s_at, x[0]);
+        [[maybe_unused]] auto ratios_of = [&](int slot) -> const float2* {
+            if constexpr (kKeyed)
+                return reinterpret_cast<const float2*>(S.scales.v_ratio[slot]);
+            else
+                return nullptr;
+        };
+        auto walk = [&](auto is_wide) {
+            constexpr bool kWide = decltype(is_wide)::value;
+            for (int i = 0; i < steps; ++i) {
+                ok = __all_sync(0xffffffffu, wait(S.s_full[tile], i & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const int key0 = (step0 + i) * kKeys, slot = i % Scales::kSlots;
+                const int hi = min(limit - key0, kKeys), lo = max(low - key0, 0);
+                if constexpr (kKeyed && kWide) {
+                    // Sixteen scores at a time, twice, in little code: unrolled, it made ordinary walks, which do not
+                    // run it, 12 % slower.
+                    auto sixteen = [&](int c, const uint32_t (&x)[16], float from, auto&& take) {  // take(pair, exponents, scales)
+                        const float2* ks = reinterpret_cast<const float2*>(S.scales.k_scale[slot]) + 8 * c;
+                        const float2* ratios = ratios_of(slot) + 8 * c;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait_ld32(x[c % 2]);
-                        if (c < 3) tmem_ld32_async(s_at + 32 * (c + 1), x[(c + 1) % 2]);
-                        if (masked) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (32 * c + e > hi || 32 * c + e < lo) x[c % 2][e] = 0xFF800000u;
+                        for (int e = 0; e < 8; ++e) {
+                            const int key = 16 * c + 2 * e;
+                            const float2 s = make_float2(key > hi || key < lo ? -INFINITY : __uint_as_float(x[2 * e]),
+                                                         key + 1 > hi || key + 1 < lo ? -INFINITY : __uint_as_float(x[2 * e + 1]));
+                            const float2 f = ffma2(ks[e], make_float2(factor, factor), make_float2(kLeastFactor, kLeastFactor));
+                            const Apart2 v = apart2(ratios[e]);
+                            take(e, ffma2(s, f, fadd2(make_float2(from, from), v.exponent)), v);
                         }
-                        take(c, x[c % 2]);
-                    }
-                };
-                auto column_factors = [&](int e, float2& a, float2& b) {  // of columns 4 e .. 4 e + 3
-                    const float4 k = ks[e];
-                    a = ffma2(make_float2(k.x, k.y), factor2, least2), b = ffma2(make_float2(k.z, k.w), factor2, least2);
-                };
-                uint32_t p[kKeys / 2];
-                float2 sum;
-                bool need = in && m == -INFINITY;
+                    };
+                    float top = -INFINITY;
 #pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
-                    if (__any_sync(0xffffffffu, need)) {
-                        float top = -INFINITY;
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t x[16];
+                        tmem_ld16(s_at + 16 * c, x);
+                        sixteen(c, x, 0.f, [&](int, float2 t, const Apart2&) { top = max3(top, t.x, t.y); });
+                    }
+                    top = ceilf(top);
+                    if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                        const float now = fmaxf(m, top), alpha = now == -INFINITY ? 1.f : ex2(m - now);
+                        m = now, l *= alpha;
+#pragma unroll 1
+                        for (int c = 0; c < (i > 0 ? D / 16 : 0); ++c) {
+                            uint32_t y[16];
+                            tmem_ld16(o_at + 16 * c, y);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+                            tmem_st16_async(o_at + 16 * c, y);
+                        }
+                    }
+                    if (DRAIN > 0 && i == drain) {
+                        drain += DRAIN;
+                        tmem_wait_st();  // as below
+                        float* to = out_row<D, DT>(g, job, row, r);
+                        const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t y[16];
+                            __syncwarp();
+                            tmem_ld16(o_at + 16 * c, y);
+                            if (in) add_16(to + 16 * c, y, keep, i > DRAIN, true);
+                        }
+                        __syncwarp();
+                        m_out = m;
+                    }
+                    const float origin = kBase - (m == -INFINITY ? 0.f : m);
+                    float2 sum = make_float2(0.f, 0.f);
+                    auto weigh = [&](int c, const uint32_t (&x)[16]) {
+                        uint32_t p[8], rest[8];
+                        sixteen(c, x, origin, [&](int e, float2 t, const Apart2& v) {
+                            const float2 y = make_float2(ex2(t.x), ex2(t.y)), w = fmul2(y, v.rest);
+                            sum = ffma2(y, v.inverse, sum);
+                            split_f16(w.x, w.y, &p[e], &rest[e]);
+                        });
+                        tmem_st8_async(s_at + 8 * c, p);
+                        if (PT == 2) tmem_st8_async(s_at + 64 + 8 * c, rest);
+                    };
+                    // Weights go over scores that have been read.  Their lower terms lie from column 64 on, so with two
+                    // terms those scores are taken first (32 of them) or from the end.
+                    [[maybe_unused]] uint32_t kept[2][16];
+                    if constexpr (PT == 2) {
+                        tmem_ld16(s_at + 64, kept[0]);
+                        tmem_ld16(s_at + 80, kept[1]);
+                    }
+#pragma unroll 1
+                    for (int k = 0; k < (PT == 2 ? 6 : 8); ++k) {
+                        const int c = PT == 2 && k >= 4 ? 11 - k : k;
+                        uint32_t x[16];
+                        tmem_ld16(s_at + 16 * c, x);
+                        weigh(c, x);
+                    }
+                    if constexpr (PT == 2) weigh(4, kept[0]), weigh(5, kept[1]);
+                    l += sum.x + sum.y;
+                } else if constexpr (kFolded) {
+                    // The scores in quarters, the next one on its way.  The weights by the maximum that there
+                    // is: as long as their sum stays in fp16's range, so does each of them, and no maximum is
+                    // looked for.  They wait in registers until that is known; rows that have seen nothing yet
+                    // and those whose sum has grown too far (each for itself) get a new maximum first.
+                    const float4* ks = reinterpret_cast<const float4*>(S.scales.k_scale[slot]);
+                    const float2 factor2 = make_float2(factor, factor), least2 = make_float2(kLeastFactor, kLeastFactor);
+                    const bool masked = __any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0);
+                    auto quarters = [&](auto&& take) {  // take(quarter, its 32 scores)
+                        uint32_t x[2][32];
+                        tmem_ld32_async(s_at, x[0]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_wait_ld32(x[c % 2]);
+                            if (c < 3) tmem_ld32_async(s_at + 32 * (c + 1), x[(c + 1) % 2]);
+                            if (masked) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (32 * c + e > hi || 32 * c + e < lo) x[c % 2][e] = 0xFF800000u;
+                            }
+                            take(c, x[c % 2]);
+                        }
+                    };
+                    auto column_factors = [&](int e, float2& a, float2& b) {  // of columns 4 e .. 4 e + 3
+                        const float4 k = ks[e];
+                        a = ffma2(make_float2(k.x, k.y), factor2, least2), b = ffma2(make_float2(k.z, k.w), factor2, least2);
+                    };
+                    uint32_t p[kKeys / 2];
+                    float2 sum;
+                    bool need = in && m == -INFINITY;
+#pragma unroll 1
+                    for (int pass = 0; pass < 2; ++pass) {
+                        if (__any_sync(0xffffffffu, need)) {
+                            float top = -INFINITY;
+                            quarters([&](int c, const uint32_t (&x)[32]) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    float2 a, b;
+                                    column_factors(8 * c + e, a, b);
+                                    a = fmul2(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), a);
+                                    b = fmul2(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), b);
+                                    top = max3(max3(top, a.x, a.y), b.x, b.y);
+                                }
+                            });
+                            const float now = need ? fmaxf(m, top) : m, alpha = now == -INFINITY ? 1.f : ex2(m - now);
+                            m = now, l *= alpha;
+                            if (i > 0) {
+#pragma unroll
+                                for (int c = 0; c < D / 16; ++c) {
+                                    uint32_t y[16];
+                                    tmem_ld16(o_at + 16 * c, y);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+                                    tmem_st16_async(o_at + 16 * c, y);
+                                }
+                            }
+                        }
+                        const float origin = kBase - (m == -INFINITY ? 0.f : m);
+                        const float2 off2 = make_float2(origin, origin);
+                        sum = make_float2(0.f, 0.f);
                         quarters([&](int c, const uint32_t (&x)[32]) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                float2 a, b;
-                                column_factors(8 * c + e, a, b);
-                                a = fmul2(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), a);
-                                b = fmul2(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), b);
-                                top = max3(max3(top, a.x, a.y), b.x, b.y);
+                                float2 w[2];
+                                column_factors(8 * c + e, w[0], w[1]);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    w[h] = ffma2(make_float2(__uint_as_float(x[4 * e + 2 * h]), __uint_as_float(x[4 * e + 2 * h + 1])), w[h], off2);
+                                    w[h].x = ex2(w[h].x), w[h].y = ex2(w[h].y);
+                                    sum = fadd2(sum, w[h]);
+                                    const __half2 v = __floats2half2_rn(w[h].x, w[h].y);
+                                    p[16 * c + 2 * e + h] = *reinterpret_cast<const uint32_t*>(&v);
+                                }
                             }
                         });
-                        const float now = need ? fmaxf(m, top) : m, alpha = now == -INFINITY ? 1.f : ex2(m - now);
+                        need = sum.x + sum.y > kMostSum;
+                        if (!__any_sync(0xffffffffu, need)) break;
+                    }
+                    l += sum.x + sum.y;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) tmem_st8_async(s_at + 8 * c, *reinterpret_cast<uint32_t(*)[8]>(p + 8 * c));
+                } else {
+                    uint32_t x[kKeys];
+                    tmem_ld64(s_at, x);
+                    tmem_ld64(s_at + 64, x + 64);
+                    if constexpr (kKeyed) {
+                        const float4* ks = reinterpret_cast<const float4*>(S.scales.k_scale[slot]);
+#pragma unroll
+                        for (int e = 0; e < kKeys / 4; ++e) {
+                            const float4 s = ks[e];
+                            const float2 a = fmul2(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), make_float2(s.x, s.y));
+                            const float2 b = fmul2(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), make_float2(s.z, s.w));
+                            x[4 * e] = __float_as_uint(a.x), x[4 * e + 1] = __float_as_uint(a.y);
+                            x[4 * e + 2] = __float_as_uint(b.x), x[4 * e + 3] = __float_as_uint(b.y);
+                        }
+                    }
+                    // Columns [lo, hi] of the step are seen; all of them in most steps.
+                    if (__any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0)) {
+#pragma unroll
+                        for (int e = 0; e < kKeys; ++e)
+                            if (e > hi || e < lo) x[e] = 0xFF800000u;
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float mx = max3(__uint_as_float(x[16 * c]), __uint_as_float(x[16 * c + 1]), __uint_as_float(x[16 * c + 2]));
+#pragma unroll
+                        for (int e = 3; e < 15; e += 2)
+                            mx = max3(mx, __uint_as_float(x[16 * c + e]), __uint_as_float(x[16 * c + e + 1]));
+                        mx = fmaxf(mx, __uint_as_float(x[16 * c + 15]));
+                        if constexpr (BITS == 8)
+                            top = fmaxf(top, mx * fmaxf(factor * S.scales.k_scale[slot][c], kLeastFactor));
+                        else
+                            top = fmaxf(top, mx);
+                    }
+                    if constexpr (BITS == 4) top *= factor;
+                    if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                        // Some row's maximum grew too far: O and l over to the new one.  (The product
+                        // that read the last weights is complete: this step's scores came after it.)
+                        const float now = fmaxf(m, top);
+                        const float alpha = now == -INFINITY ? 1.f : ex2(m - now);
                         m = now, l *= alpha;
                         if (i > 0) {
 #pragma unroll
@@ -762,135 +979,64 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                             }
                         }
                     }
-                    const float origin = kBase - (m == -INFINITY ? 0.f : m);
-                    const float2 off2 = make_float2(origin, origin);
-                    sum = make_float2(0.f, 0.f);
-                    quarters([&](int c, const uint32_t (&x)[32]) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float2 w[2];
-                            column_factors(8 * c + e, w[0], w[1]);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                w[h] = ffma2(make_float2(__uint_as_float(x[4 * e + 2 * h]), __uint_as_float(x[4 * e + 2 * h + 1])), w[h], off2);
-                                w[h].x = ex2(w[h].x), w[h].y = ex2(w[h].y);
-                                sum = fadd2(sum, w[h]);
-                                const __half2 v = __floats2half2_rn(w[h].x, w[h].y);
-                                p[16 * c + 2 * e + h] = *reinterpret_cast<const uint32_t*>(&v);
-                            }
-                        }
-                    });
-                    need = sum.x + sum.y > kMostSum;
-                    if (!__any_sync(0xffffffffu, need)) break;
-                }
-                l += sum.x + sum.y;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) tmem_st8_async(s_at + 8 * c, *reinterpret_cast<uint32_t(*)[8]>(p + 8 * c));
-            } else {
-                uint32_t x[kKeys];
-                tmem_ld64(s_at, x);
-                tmem_ld64(s_at + 64, x + 64);
-                if constexpr (kKeyed) {
-                    const float4* ks = reinterpret_cast<const float4*>(S.scales.k_scale[slot]);
-#pragma unroll
-                    for (int e = 0; e < kKeys / 4; ++e) {
-                        const float4 s = ks[e];
-                        const float2 a = fmul2(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), make_float2(s.x, s.y));
-                        const float2 b = fmul2(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), make_float2(s.z, s.w));
-                        x[4 * e] = __float_as_uint(a.x), x[4 * e + 1] = __float_as_uint(a.y);
-                        x[4 * e + 2] = __float_as_uint(b.x), x[4 * e + 3] = __float_as_uint(b.y);
-                    }
-                }
-                // Columns [lo, hi] of the step are seen; all of them in most steps.
-                if (__any_sync(0xffffffffu, hi < kKeys - 1 || lo > 0)) {
-#pragma unroll
-                    for (int e = 0; e < kKeys; ++e)
-                        if (e > hi || e < lo) x[e] = 0xFF800000u;
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float mx = max3(__uint_as_float(x[16 * c]), __uint_as_float(x[16 * c + 1]), __uint_as_float(x[16 * c + 2]));
-#pragma unroll
-                    for (int e = 3; e < 15; e += 2)
-                        mx = max3(mx, __uint_as_float(x[16 * c + e]), __uint_as_float(x[16 * c + e + 1]));
-                    mx = fmaxf(mx, __uint_as_float(x[16 * c + 15]));
-                    if constexpr (BITS == 8)
-                        top = fmaxf(top, mx * fmaxf(factor * S.scales.k_scale[slot][c], kLeastFactor));
-                    else
-                        top = fmaxf(top, mx);
-                }
-                if constexpr (BITS == 4) top *= factor;
-                if (__any_sync(0xffffffffu, top > m + kSlack)) {
-                    // Some row's maximum grew too far: O and l over to the new one.  (The product
-                    // that read the last weights is complete: this step's scores came after it.)
-                    const float now = fmaxf(m, top);
-                    const float alpha = now == -INFINITY ? 1.f : ex2(m - now);
-                    m = now, l *= alpha;
-                    if (i > 0) {
-#pragma unroll
+                    if (DRAIN > 0 && i == drain) {
+                        drain += DRAIN;
+                        tmem_wait_st();  // O may just have been rescaled; loads do not wait for stores
+                        float* to = out_row<D, DT>(g, job, row, r);
+                        const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
+#pragma unroll DT == Q4LIN_DTYPE_F32 ? 4 : 8
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t y[16];
+                            __syncwarp();  // the load is the whole warp's
                             tmem_ld16(o_at + 16 * c, y);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
-                            tmem_st16_async(o_at + 16 * c, y);
+                            if (in) add_16(to + 16 * c, y, keep, i > DRAIN, true);
                         }
+                        __syncwarp();
+                        m_out = m;
+                    }
+                    const float origin = kBase - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float f = factor, off = origin;
+                        if constexpr (BITS == 8)
+                            f = fmaxf(factor * S.scales.k_scale[slot][c], kLeastFactor), off = origin + S.scales.v_log[slot][c];
+                        const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
+                        float2 sum = make_float2(0.f, 0.f);
+                        [[maybe_unused]] float4 ratio = make_float4(0.f, 0.f, 0.f, 0.f);
+                        uint32_t p[8], rest[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float2 y = ffma2(make_float2(__uint_as_float(x[16 * c + 2 * e]), __uint_as_float(x[16 * c + 2 * e + 1])), f2, off2);
+                            y.x = ex2(y.x), y.y = ex2(y.y);
+                            sum = fadd2(sum, y);
+                            if constexpr (kKeyed) {
+                                if (e % 2 == 0) ratio = *reinterpret_cast<const float4*>(&S.scales.v_ratio[slot][16 * c + 2 * e]);
+                                y = fmul2(y, e % 2 ? make_float2(ratio.z, ratio.w) : make_float2(ratio.x, ratio.y));
+                            }
+                            if (PT == 2) {
+                                split_f16(y.x, y.y, &p[e], &rest[e]);
+                            } else {
+                                const __half2 v = __floats2half2_rn(y.x, y.y);
+                                p[e] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                        }
+                        if constexpr (BITS == 8)
+                            l = fmaf(sum.x + sum.y, S.scales.v_inv[slot][c], l);
+                        else
+                            l += sum.x + sum.y;
+                        tmem_st8_async(s_at + 8 * c, p);  // over the scores
+                        if (PT == 2) tmem_st8_async(s_at + 64 + 8 * c, rest);
                     }
                 }
-                if (DRAIN > 0 && i == drain) {
-                    drain += DRAIN;
-                    tmem_wait_st();  // O may just have been rescaled; loads do not wait for stores
-                    float* to = out_row<D, DT>(g, job, row, r);
-                    const float keep = m_out == -INFINITY ? 0.f : ex2(m_out - m);
-#pragma unroll DT == Q4LIN_DTYPE_F32 ? 4 : 8
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t y[16];
-                        __syncwarp();  // the load is the whole warp's
-                        tmem_ld16(o_at + 16 * c, y);
-                        if (in) add_16(to + 16 * c, y, keep, i > DRAIN, true);
-                    }
-                    __syncwarp();
-                    m_out = m;
-                }
-                const float origin = kBase - (m == -INFINITY ? 0.f : m);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float f = factor, off = origin;
-                    if constexpr (BITS == 8)
-                        f = fmaxf(factor * S.scales.k_scale[slot][c], kLeastFactor), off = origin + S.scales.v_log[slot][c];
-                    const float2 f2 = make_float2(f, f), off2 = make_float2(off, off);
-                    float2 sum = make_float2(0.f, 0.f);
-                    [[maybe_unused]] float4 ratio = make_float4(0.f, 0.f, 0.f, 0.f);
-                    uint32_t p[8], rest[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float2 y = ffma2(make_float2(__uint_as_float(x[16 * c + 2 * e]), __uint_as_float(x[16 * c + 2 * e + 1])), f2, off2);
-                        y.x = ex2(y.x), y.y = ex2(y.y);
-                        sum = fadd2(sum, y);
-                        if constexpr (kKeyed) {
-                            if (e % 2 == 0) ratio = *reinterpret_cast<const float4*>(&S.scales.v_ratio[slot][16 * c + 2 * e]);
-                            y = fmul2(y, e % 2 ? make_float2(ratio.z, ratio.w) : make_float2(ratio.x, ratio.y));
-                        }
-                        if (PT == 2) {
-                            split_f16(y.x, y.y, &p[e], &rest[e]);
-                        } else {
-                            const __half2 v = __floats2half2_rn(y.x, y.y);
-                            p[e] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
-                    }
-                    if constexpr (BITS == 8)
-                        l = fmaf(sum.x + sum.y, S.scales.v_inv[slot][c], l);
-                    else
-                        l += sum.x + sum.y;
-                    tmem_st8_async(s_at + 8 * c, p);  // over the scores
-                    if (PT == 2) tmem_st8_async(s_at + 64 + 8 * c, rest);
-                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(S.p_full[tile]));
             }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar(S.p_full[tile]));
-        }
+        };
+        if (kKeyed && wide_walk())
+            walk(std::bool_constant<kKeyed>{});
+        else
+            walk(std::false_type{});
         if (ok && steps > 0) {
             ok = __all_sync(0xffffffffu, wait(S.o_full[tile], 0));
             tc_fence_after();
@@ -958,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             if (in && cut) {
                 unit[pair_rows_of(D) * D + r] = m, unit[pair_rows_of(D) * (D + 1) + r] = l;
             } else if (in && g.a.lse) {
-                g.a.lse[index] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + lg2(l * kUnbase)) * kLn2 : -INFINITY;
+                g.a.lse[index] = l != 0.f ? log2_sum(m == -INFINITY ? 0.f : m, l * kUnbase) * kLn2 : -INFINITY;
             }
         }
     } else if (warp < kIssueWarp) {
@@ -969,6 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const int32_t* table = C.page_table + job.b * C.table_stride;
         const bool keys = warp < kValueWarp;
         const float ref = value_ref();
+        [[maybe_unused]] const bool wide = wide_walk();
         const int t = tid & 127;
         // One ring each, a step's blocks in the order of their use.
         auto walk = [&](auto&& widen) {
@@ -993,7 +1140,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             // values, of whole tokens, in the order of the page.
             [[maybe_unused]] const int count = keys ? 4 : D / 32;  // (8 bits) pieces per thread and block
             const uint32_t page_bytes = (uint32_t)(D * BITS / 8) << ps;
-            [[maybe_unused]] const float inverse = 1.f / ref;
+            // A value's scale over the reference; 1 in wide walks.
+            [[maybe_unused]] const float inverse = wide ? 0.f : 1.f / ref, one = wide ? 1.f : 0.f;
             uint4 reg[BITS == 4 && D < 256 ? 2 : 4];
             // 16-byte chunks of a token's 4-bit codes; values' rows of a block that a thread has a chunk of.
             [[maybe_unused]] constexpr int kChunks = D / 32, kValueRows = D / 64;
@@ -1071,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                                                    odd ? reg[j].x : reg[j].z, odd ? reg[j].y : reg[j].w};
                             [[maybe_unused]] uint32_t hi, lo;
                             if constexpr (kFolded) {
-                                const float s = first + row < job.len ? scale[j] * inverse : 0.f;
+                                const float s = first + row < job.len ? fmaf(scale[j], inverse, one) : 0.f;
                                 split_f16(s, s, &hi, &lo);
                             }
 #pragma unroll
@@ -1125,7 +1273,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                             if (page >= 0 && key < job.len) {
                                 const int64_t at = ((int64_t)page << ps) + (key & (1 << ps) - 1);
                                 ks = __ldg(C.k_scales + at);
-                                if constexpr (!kFolded) vs = __ldg(C.v_scales + at);
+                                if (!kFolded || wide) vs = __ldg(C.v_scales + at);
                             }
                         }
                     } else if (scales && pages_now >= 0) {
@@ -1137,7 +1285,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                         const int at = i % Scales::kSlots;
                         if constexpr (kKeyed) {
                             S.scales.k_scale[at][t] = ks;
-                            if constexpr (!kFolded) S.scales.v_ratio[at][t] = vs / ref;
+                            if (!kFolded || wide) S.scales.v_ratio[at][t] = vs / ref;
                         } else if constexpr (BITS == 8) {
                             const float ratio = fmaxf(vs / ref, kLeastRatio);
                             S.scales.k_scale[at][t] = ks, S.scales.v_log[at][t] = lg2(ratio), S.scales.v_inv[at][t] = 1.f / ratio;
@@ -1322,7 +1470,7 @@ __device__ __forceinline__ void join_rows(const PromptArgs& g, int64_t unit0, in
                 reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D)[unit4] =
                     make_uint2(to_16x2(o[q].x * inv, o[q].y * inv, g.a.dtype), to_16x2(o[q].z * inv, o[q].w * inv, g.a.dtype));
             if (unit4 == 0 && g.a.lse)
-                g.a.lse[index] = l[q] != 0.f ? ((mx[q] == -INFINITY ? 0.f : mx[q]) + lg2(l[q] * kUnbase)) * kLn2 : -INFINITY;
+                g.a.lse[index] = l[q] != 0.f ? log2_sum(mx[q] == -INFINITY ? 0.f : mx[q], l[q] * kUnbase) * kLn2 : -INFINITY;
         }
     }
 }

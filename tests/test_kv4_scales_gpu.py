@@ -11,7 +11,6 @@ from tests.test_attention_gpu import check, status
 from tests.test_kv4_attention_gpu import BOTH, attend, check_rows, handle, some, split  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
-KERNELS = 1 << 40,  # as BOTH: the one for few rows
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -50,7 +49,7 @@ def test_rows_that_see_small_values_only(handle, split, tokens, n, window, apart
     host.vs[..., small] *= np.float32(2.0**-apart)
     q = ops.to_device(rng.standard_normal((tokens, 2, dim)).astype(np.float32), dtype)
     want = ops.attention(host, ops.to_host(q), [0, tokens], [n], 0.125, window=window)
-    for rows in KERNELS:
+    for rows in BOTH:
         split(rows)
         check(*attend(handle, host, q, [tokens], [n], 0.125, window=window), want, dtype)
     assert status(handle) == 0
@@ -70,7 +69,7 @@ def test_small_values_before_large_ones(handle, split, tokens, apart, dim, dtype
     host.vs[slots] *= np.where(at % 11 == 5, 0.0, 1.0).astype(np.float32)
     q = ops.to_device(rng.standard_normal((tokens, 6, dim)).astype(np.float32), dtype)
     want = ops.attention(host, ops.to_host(q), [0, tokens], [tokens], 0.125)
-    for rows in KERNELS:
+    for rows in BOTH:
         split(rows)
         check(*attend(handle, host, q, [tokens], [tokens], 0.125), want, dtype)
     assert status(handle) == 0
@@ -92,8 +91,24 @@ def test_values_that_grow(handle, split, dtype, dim, tokens, n, heads):
     for grows, window in ((True, 0), (False, 60), (True, 60)):
         power = at / n * 50 - 50 if grows else -at / n * 50
         host.vs[slots] = base[slots] * (2.0**power).astype(np.float32)
-        for rows in KERNELS:
+        for rows in BOTH:
             split(rows)
             out, lse = attend(handle, host, q, [tokens], [n], 0.125, window=window)
             check_rows(out, lse, host, q, n, 0.125, pairs, dtype, window=window)
+    assert status(handle) == 0
+
+
+def test_small_values_and_outputs_taken_out(handle, split):
+    """fp16 rows over a table so long that their outputs are taken out on the way, in whole walks."""
+    split(1)
+    rng = np.random.default_rng(75)
+    n, tokens, heads = 33000, 2600, 16
+    host = kv4.Cache(rng, [n], heads, 64, 64)
+    slots = host.table[0, :-(-n // 64)]
+    at = np.arange(len(slots) * 64).reshape(len(slots), 1, 64)
+    host.vs[slots] *= np.where(at // 1000 % 2 == 0, 2.0**-30, 1.0).astype(np.float32)
+    host.vs[slots] *= np.where(at < 31500, 2.0**-12, 1.0).astype(np.float32)
+    q = ops.to_device(rng.standard_normal((tokens, heads, 64)).astype(np.float32), "f16")
+    out, lse = attend(handle, host, q, [tokens], [n], 0.125)
+    check_rows(out, lse, host, q, n, 0.125, some(rng, tokens, heads, 40), "f16")
     assert status(handle) == 0
