@@ -901,6 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                                     for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
                                     tmem_st16_async(o_at + 16 * c, y);
                                 }
+                                tmem_wait_st();  // a second pass may read them; loads do not wait for stores
                             }
                         }
                         const float origin = kBase - (m == -INFINITY ? 0.f : m);

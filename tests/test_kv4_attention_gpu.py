@@ -568,3 +568,26 @@ def test_many_keys_of_wide_heads(handle, split, dtype, n, tokens):
     again = attend(handle, host, q, [tokens], [n], 0.0625)
     assert out.equal(again[0]) and lse.equal(again[1])
     assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rotated", [False, True])
+def test_rows_that_begin_while_others_maxima_grow(handle, split, dim, rotated):
+    """bf16 prompts with a window, whose rows first see a key in a step in which scores of others grow by
+    2^12 and more: outputs are rescaled twice there."""
+    split(1)
+    rng = np.random.default_rng(61)
+    n, window = 600, 150
+    host = kv4.Cache(rng, [n], 2, 32, dim)
+    slots = host.table[0, :-(-n // 32)]
+    at = np.arange(len(slots) * 32).reshape(len(slots), 1, 32)
+    host.k[..., 0], host.ks[slots] = 15, np.where(at % 128 < 40, 0.02, 2.0)
+    host.ks[slots] *= (1 + at / 200).astype(np.float32)
+    q = rng.standard_normal((n, 2, dim)) * 0.1
+    q[..., 0] = 4
+    q = ops.to_device(q.astype(np.float32), "bf16")
+    angle = np.zeros((n, dim // 2), np.float32)
+    rope = (ops.to_device(angle + 1), ops.to_device(angle)) if rotated else None
+    want = ops.attention(host, ops.to_host(q), [0, n], [n], 0.125, window=window)
+    check(*attend(handle, host, q, [n], [n], 0.125, window=window, rope=rope), want, "bf16")
+    assert status(handle) == 0
