@@ -100,26 +100,32 @@ __device__ __forceinline__ float2 two_sums(const Eight& x, const Eight& y) {
         v = fadd2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
     return v;
 }
-// r = 1 / sqrt(sum / D + eps) of a row whose squares add up to `sum`.  Where they pass fp32's range, or
-// are lost below it and eps does not hide that, x is scaled by a power of two first (whole warp: the
-// sums need every lane): r is then that of the scaled x, *back what it was scaled by, and *mean the
-// mean of x y anew.
+// Whether the squares of a row, which add up to `sum`, pass fp32's range, or are lost below it where eps
+// does not hide that.
+__device__ __forceinline__ bool is_far(float sum, float eps) { return sum > 3e38f || (eps < 1e-30f && sum < 1e-30f); }
+// Such a row's x scaled by a power of two (*back), and r = 1 / sqrt(mean x^2 + eps) of that.  By a whole warp:
+// the sum needs every lane.
 template <int D>
-__device__ __forceinline__ void scales_of(Eight& x, const Eight& y, float sum, float eps, float* mean, float* r, float* back) {
-    *r = rsqrtf(fmaf(sum, 1.f / D, eps)), *back = 1.f;
-    const bool far = sum > 3e38f || (eps < 1e-30f && sum < 1e-30f);
-    if (__any_sync(0xffffffffu, far)) {
-        const float by = sum > 3e38f ? 8.470329472543003e-22f : 1.2676506002282294e30f;  // 2^-70, 2^100
-        if (far) scale_by(x, by);
-        const float2 again = two_sums<D / 8>(x, y);
-        if (far) *r = rsqrtf(fmaf(again.x, 1.f / D, eps * by * by)), *back = by, *mean = again.y * (1.f / D);
-    }
+__device__ __forceinline__ void scale_far(Eight& x, bool far, float sum, float eps, float* r, float* back) {
+    const float by = sum > 3e38f ? 8.470329472543003e-22f : 1.2676506002282294e30f;  // 2^-70, 2^100
+    if (far) scale_by(x, by);
+    const float again = dot<D / 8>(x, x);
+    if (far) *r = rsqrtf(fmaf(again, 1.f / D, eps * by * by)), *back = by;
+}
+// Whether one of a lane's elements is not 0.
+__device__ __forceinline__ bool any_of(const Eight& x) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bits |= __float_as_uint(x.v[e].x) | __float_as_uint(x.v[e].y);
+    return bits << 1 != 0;
 }
 // x becomes x r.
 template <int D>
 __device__ __forceinline__ void normalise(Eight& x, float eps) {
-    float r, back, mean;
-    scales_of<D>(x, x, dot<D / 8>(x, x), eps, &mean, &r, &back);
+    const float sum = dot<D / 8>(x, x);
+    float r = rsqrtf(fmaf(sum, 1.f / D, eps)), back;
+    const bool far = is_far(sum, eps);
+    if (__any_sync(0xffffffffu, far)) scale_far<D>(x, far, sum, eps, &r, &back);
     scale_by(x, r);
 }
 template <bool VEC>
@@ -416,13 +422,22 @@ __global__ void __launch_bounds__(32 * kBackWarps, kBackCtas) norm_rope_backward
                 Eight gw;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) gw.v[e] = fmul2(d.v[e], w.v[e]);
-                // Both sums at once; with u = x r, the second is that of g w u over r.
-                float r, back;
+                // Both sums at once; with u = x r, the second is that of g w u over r.  Where x is to be scaled, or
+                // the sum leaves fp32's range, or terms may be lost below it, it is taken anew with u.
                 const float2 both = two_sums<U>(x, gw);
-                float mean = both.y * (1.f / D);
-                scales_of<D>(x, gw, both.x, g.a.eps, &mean, &r, &back);
+                float r = rsqrtf(fmaf(both.x, 1.f / D, g.a.eps)), back = 1.f, mean = both.y * (1.f / D) * r;
+                const bool far = is_far(both.x, g.a.eps);
+                const bool lost = in && (far || !(fabsf(both.y) <= 3e38f) || fabsf(both.y) < 1e-30f);
+                // (Padding's gradients are zeros, and so is their sum.)
+                if (__any_sync(0xffffffffu, lost) && __any_sync(0xffffffffu, lost && (far || any_of(gw)))) {
+                    scale_far<D>(x, far, both.x, g.a.eps, &r, &back);
+                    Eight u = x;
+                    scale_by(u, r);
+                    const float again = dot<U>(u, gw);
+                    if (lost) mean = again * (1.f / D);
+                }
                 scale_by(x, r);
-                mean *= -r;
+                mean = -mean;
                 if (in) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) dw.v[e] = ffma2(d.v[e], x.v[e], dw.v[e]);
