@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(32 * kBackWarps, kBackCtas) norm_rope_backward
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x.v[e] = ffma2(x.v[e], make_float2(mean, mean), gw.v[e]);
-                scale_by(x, r * back);
+                scale_by(x, r);
+                if (back != 1.f) scale_by(x, back);  // (their product may have no room where a zero has)
                 if (in) store_row<DT, VEC>(y_at, lo_at, hi_at, x);
                 h += R, y_at += step.y;
                 if (h >= each * R) {

@@ -40,3 +40,20 @@ def test_products_that_leave_the_range(handle, dim, aligned):
     x[5], d[5, 1] = 1e-3, 0
     d[:, 2, 5:] = 0  # one lane's channels alone
     compare(handle, x, d, 1e-31, aligned)
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_of_the_smallest_numbers(handle, dim, aligned):
+    """Rows below 2^-126, without eps: zeros where the gradient that comes in is, ordinary numbers where it
+    is small."""
+    rng = np.random.default_rng(92)
+    x, d = rng.standard_normal((4, 2, dim)) * 1e-42, rng.standard_normal((4, 2, dim)) * 1e-25
+    x[x == 0] = 1e-42
+    d[1] = 0
+    x[2] *= 1e-2
+    x[2, :, 0] = 1.5e-45
+    d[3] = 0
+    x[3] *= 1e60
+    got = compare(handle, x, d, 0.0, aligned)
+    assert bool((got[[1, 3]] == 0).all())
