@@ -99,7 +99,7 @@ constexpr int kDrainSlots = 256;  // at most; one for each CTA that runs
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
 // Undone before a logarithm, whose error grows with its distance from 0.
 constexpr float kUnbase = 1.f / 128.f;
-// A score's factor is at least this, so that a masked score (-infinity) stays one.
+// A score's factor, its key's scale included, is at least about this, so that a masked score (-infinity) stays one.
 constexpr float kLeastFactor = 1e-37f;
 // (4 bits) Weights of a step that add up to no more than this are below fp16's 65504 each.
 constexpr float kMostSum = 65000.f;
@@ -220,7 +220,7 @@ struct PromptShared {
     float factor[2 * kQ];
     StepScales<D, KEYED> scales;
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2];
-    float v_max[kWarps], v_min[kWarps];  // (4 bits) v_min: of those above 0
+    float v_max[kWarps], v_min[kWarps], k_max[kWarps];  // (4 bits) v_min: of those above 0
     int failed;
     uint32_t tmem;
 };
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     }
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&S.tmem), kTmemCols);
     float v_max = 0.f;
-    [[maybe_unused]] float v_min = INFINITY;
+    [[maybe_unused]] float v_min = INFINITY, k_max = 0.f;
     const int page_first = max((step0 * kKeys) >> ps, page_low), page_last = min(pages, (step1 * kKeys) >> ps);
     if constexpr (BITS == 8) {
         for (int p = page_first + tid; p < page_last; p += kThreads) {
@@ -670,8 +670,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             if (id < 0 || id >= C.num_pages) {
                 atomicCAS(g.status, 0, kStatusIndex);
             } else {
-                const float4 s = __ldg(reinterpret_cast<const float4*>(C.v_scales + (((int64_t)id * Hkv + h) << ps) + e));
+                const int64_t at = (((int64_t)id * Hkv + h) << ps) + e;
+                const float4 s = __ldg(reinterpret_cast<const float4*>(C.v_scales + at));
                 const float v[4] = {s.x, s.y, s.z, s.w};
+                if constexpr (!kFolded) {
+                    const float4 k = __ldg(reinterpret_cast<const float4*>(C.k_scales + at));
+                    k_max = fmaxf(k_max, fmaxf(fmaxf(0 < left ? k.x : 0.f, 1 < left ? k.y : 0.f), fmaxf(2 < left ? k.z : 0.f, 3 < left ? k.w : 0.f)));
+                }
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const float x = n < left ? v[n] : 0.f;
@@ -687,6 +692,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
 #pragma unroll
         for (int o = 16; o; o >>= 1) v_min = fminf(v_min, __shfl_xor_sync(0xffffffffu, v_min, o));
         if (lane == 0) S.v_min[warp] = v_min;
+        if constexpr (!kFolded) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) k_max = fmaxf(k_max, __shfl_xor_sync(0xffffffffu, k_max, o));
+            if (lane == 0) S.k_max[warp] = k_max;
+        }
     }
     put_queries<D, QT, DT, BITS>(g, gbase, S.factor, o0, h, tq, len, row0, row_end);
     }
@@ -709,6 +719,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         for (int w = 0; w < kWarps; ++w) v = fmaxf(v, const_cast<volatile float&>(S.v_max[w]));
         if constexpr (kFolded) return __uint_as_float(min(max((int)(__float_as_uint(v) >> 23) - 11, 1), 253) << 23);
         return v > 0.f ? v : 1.f;  // 1: values that are all zero
+    };
+    // What the keys' scales are taken relative to where they multiply scores before the row's factor does: 1, or for
+    // scales above 2^64 a power of two that brings the largest there, as a score may be an ordinary one where neither
+    // that nor the factor is.
+    auto key_ref = [&]() {
+        if constexpr (kFolded || BITS == 8) return 1.f;
+        const uint32_t most = __reduce_max_sync(0xffffffffu, lane < kWarps ? __float_as_uint(S.k_max[lane]) : 0u);
+        return __uint_as_float((max(most >> 23, 127u + 64u) - 64u) << 23);
     };
     // (By a whole warp; positive floats are ordered as their bits.)
     auto wide_walk = [&]() {
@@ -746,9 +764,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const int token = row / group, position = len - tq + token;
         const int limit = !in ? -1 : g.a.causal ? position : len - 1;
         const int low = g.a.window > 0 ? (int)max((int64_t)0, (int64_t)position - g.a.window + 1) : 0;
-        // (4 bits: not so small that a masked score would not stay -infinity; 8 bits: with the scale below.)
         float factor = S.factor[r];
-        if constexpr (BITS == 4) factor = factor < kLeastFactor ? kLeastFactor : factor;  // (a NaN stays one)
+        if constexpr (kKeyed && !kFolded) {  // (not so small that a masked score would not stay -infinity)
+            factor *= key_ref();
+            factor = factor < kLeastFactor ? kLeastFactor : factor;  // (a NaN stays one)
+        }
         int drain = first_drain();
         float m = -INFINITY, l = 0.f, m_out = -INFINITY;  // m_out: of what was taken out
         bool ok = true;
@@ -1117,6 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
         const bool keys = warp < kValueWarp;
         const float ref = value_ref();
         [[maybe_unused]] const bool wide = wide_walk();
+        [[maybe_unused]] const float key_inverse = 1.f / key_ref();
         const int t = tid & 127;
         // One ring each, a step's blocks in the order of their use.
         auto walk = [&](auto&& widen) {
@@ -1285,7 +1306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
                         // Far below fp16's range a weight is 0 in the product; in l it counts.
                         const int at = i % Scales::kSlots;
                         if constexpr (kKeyed) {
-                            S.scales.k_scale[at][t] = ks;
+                            S.scales.k_scale[at][t] = kFolded ? ks : ks * key_inverse;
                             if (!kFolded || wide) S.scales.v_ratio[at][t] = vs / ref;
                         } else if constexpr (BITS == 8) {
                             const float ratio = fmaxf(vs / ref, kLeastRatio);

@@ -302,9 +302,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                         f[e % 2 * 2 + (d >> 2 & 1)] = hi, f[16 + e % 2 * 2 + (d >> 2 & 1)] = lo;
                     }
                     RowInfo i;
-                    // At least this, so that a masked score of -infinity stays one (and a NaN one).
-                    const float f = fabsf(g.a.scale) * kLog2e * down;
-                    i.factor = f < 1e-37f ? 1e-37f : f;
+                    i.factor = fabsf(g.a.scale) * kLog2e * down;
                     i.limit = g.a.causal ? position : P.len - 1;
                     const int64_t low = g.a.window > 0 ? (int64_t)position - g.a.window + 1 : 0;
                     i.low = low > 0 ? (int)low : 0;
@@ -414,9 +412,11 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 float2 x[4], p[4];
+                // (Factors and keys' scales first: a score may be an ordinary one where neither is.)
+                const float2 f2 = make_float2(factor[ct], factor[ct]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
-                    x[m] = fmul2(make_float2(sc[ct][m][0] + sc[ct][m][1], sc[ct][m][2] + sc[ct][m][3]), sk[m]);
+                    x[m] = fmul2(make_float2(sc[ct][m][0] + sc[ct][m][1], sc[ct][m][2] + sc[ct][m][3]), fmul2(sk[m], f2));
                 if (!inside) {
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
@@ -425,12 +425,11 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                         if (key + 8 < low[ct] || key + 8 > limit[ct]) x[m].y = -INFINITY;
                     }
                 }
-                const float2 f2 = make_float2(factor[ct], factor[ct]);
                 auto weights = [&]() {
                     const float off = kFewBits - (m_run[ct] == -INFINITY ? 0.f : m_run[ct]);
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
-                        p[m] = ffma2(x[m], f2, make_float2(off, off));
+                        p[m] = fadd2(x[m], make_float2(off, off));
                         p[m].x = ex2(p[m].x), p[m].y = ex2(p[m].y);
                     }
                 };
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
 #pragma unroll
                     for (int o = 4; o < 32; o *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     const float old = m_run[ct];
-                    if (far & 0x11111111u << t) m_run[ct] = fmaxf(mx * factor[ct], old);
+                    if (far & 0x11111111u << t) m_run[ct] = fmaxf(mx, old);
                     const float alpha = m_run[ct] == -INFINITY ? 1.f : ex2(old - m_run[ct]);
                     l_run[ct] *= alpha;
 #pragma unroll
