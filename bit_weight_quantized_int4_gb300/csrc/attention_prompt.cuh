@@ -99,6 +99,8 @@ constexpr int kDrainSlots = 256;  // at most; one for each CTA that runs
 constexpr float kSlack = 8.f;   // ... with p up to 2^8 before O is rescaled (fp16: below 2^16)
 // Undone before a logarithm, whose error grows with its distance from 0.
 constexpr float kUnbase = 1.f / 128.f;
+// (4 bits) A part's sums of values above 2^32 are kept over 2^32, so that those near fp32's largest have room.
+constexpr float kLessBits = 32.f, kLess = 2.3283064365386963e-10f;
 // A score's factor, its key's scale included, is at least about this, so that a masked score (-infinity) stays one.
 constexpr float kLeastFactor = 1e-37f;
 // (4 bits) Weights of a step that add up to no more than this are below fp16's 65504 each.
@@ -1079,7 +1081,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             const bool wide = cut || DT == Q4LIN_DTYPE_F32;
             const uint32_t row_bytes = wide ? 4 * D : 2 * D, out = base + (uint32_t)r * (4 * D + 16);
             static_assert(pair_rows_of(D) * (4 * D + 16) <= L::bytes, "the rows fit");
-            const float f = l == 0.f ? 0.f : cut ? v_ref : inv;
+            float f = l == 0.f ? 0.f : cut ? v_ref : inv;
+            if (BITS == 4 && cut && v_ref > 4294967296.f) {
+                // (What the maximum loses as it is rounded goes into the sums.)
+                const float more = m + kLessBits, by = fmaf((more - kLessBits) - m, -kLn2, 1.f) * kLess;
+                if (m != -INFINITY) m = more, l *= by, f *= by;
+            }
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];

@@ -29,6 +29,7 @@ struct SplitArgs {
     int64_t rows_max;
     int q_vec;
     int workers;    // warps of the launch
+    float unshift;      // of the parts' sums of weights, before a logarithm
     int64_t join_each;  // tokens of a sequence that the joining kernel has CTAs for; 0: one for every token
     float* parts;   // [workers][2][R (D + 2)]: a warp's first and last piece, if unfinished
     int* list;      // [batch + 1]: the share, then where each sequence begins in the list
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const S
             *reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D + d) =
                 make_uint2(to_16x2(a.x * inv, a.y * inv, g.a.dtype), to_16x2(a.z * inv, a.w * inv, g.a.dtype));
     }
-    if (lane == 0 && g.a.lse) g.a.lse[index] = l != 0.f ? (from + lg2(l * kUnshift)) * kLn2 : -INFINITY;
+    if (lane == 0 && g.a.lse) g.a.lse[index] = l != 0.f ? (from + lg2(l * g.unshift)) * kLn2 : -INFINITY;
 }
 
 // What a launch may have to do.
@@ -323,6 +324,7 @@ cudaError_t in_groups(const q4lin_kv_cache_t& cache, const q4lin_attention_t& a,
         g.a.lengths += b;
         g.page_shift = cache.page_size == 16 ? 4 : cache.page_size == 32 ? 5 : 6;
         g.rows_max = rows_max;
+        g.unshift = kUnshift;
         g.q_vec = reinterpret_cast<uintptr_t>(a.query) % (4 * dtype_size(a.dtype)) == 0 &&
                   a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;
         g.status = c.status_word;

@@ -34,11 +34,12 @@ __host__ __device__ constexpr int warps_of(int D, int CT) {
     return D == 64 ? (CT <= 2 ? 12 : 8) : D == 128 && CT == 1 ? 12 : 8;
 }
 
-// Weights are kept as 2^4 p, p by a maximum that scores may have passed by up to 2^10.  For the product
-// with the values' codes a row's, times the values' scales, are brought to fp16's upper range by a power
-// of two for each tile: of the largest of them, in which only keys that the row sees have a part, so that
-// two terms leave 2^-22 of that however small a value is beside those that the row does not see.
-constexpr float kFewBits = 4.f, kUnfew = 1.f / 16.f, kMostWeight = 16384.f;
+// Weights are 2 to the power of scores less a maximum that they may have passed by up to 2^10.  For the product
+// with the values' codes a row's, times the values' scales, are brought to fp16's upper range by a power of two
+// for each tile: of the largest of them, in which only keys that the row sees have a part, so that two terms
+// leave 2^-22 of that however small a value is beside those that the row does not see.  Sums of values are kept
+// over 2^20, so that those near fp32's largest have room.
+constexpr float kMostWeight = 1024.f, kLess = 1.f / 1048576.f, kMore = 1048576.f;
 
 struct KvMaps {
     CUtensorMap k, v;  // [page and head][token][bytes of a token]
@@ -48,7 +49,7 @@ template <int D, int CT>
 struct Mine {  // of one warp
     uint2 q[CT][D / 16][32];  // B fragments
     RowInfo row[CT * 4];
-    float scales[2][kTile];  // of a tile's keys and values
+    float scales[2][kTile];  // of a tile's keys, and values over 2^20
 };
 template <int D, int CT>
 struct Layout {
@@ -343,6 +344,8 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                 const int left = P.len - tile_key - scale_key;
                 float4 v = scales_next;
                 v.x = left > 0 ? v.x : 0.f, v.y = left > 1 ? v.y : 0.f, v.z = left > 2 ? v.z : 0.f, v.w = left > 3 ? v.w : 0.f;
+                const float less = lane < 16 ? 1.f : kLess;
+                v.x *= less, v.y *= less, v.z *= less, v.w *= less;
                 *reinterpret_cast<float4*>(&mine.scales[lane >> 4][scale_key]) = v;
                 fetch_scales();
                 fetch_page(i + 2);
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                     }
                 }
                 auto weights = [&]() {
-                    const float off = kFewBits - (m_run[ct] == -INFINITY ? 0.f : m_run[ct]);
+                    const float off = m_run[ct] == -INFINITY ? 0.f : -m_run[ct];
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
                         p[m] = fadd2(x[m], make_float2(off, off));
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
             const int r = 4 * ct + t;
             const int64_t index = mine.row[r].index;
             if (index < 0) continue;
-            const float f = !complete ? 1.f : l != 0.f ? 1.f / l : 0.f;  // l == 0: the row sees no key
+            const float f = !complete ? 1.f : l != 0.f ? kMore / l : 0.f;  // l == 0: the row sees no key
             const bool wide = !complete || g.a.dtype == Q4LIN_DTYPE_F32;
             float* to = complete ? static_cast<float*>(g.a.out) + index * D : part + r * D;
             unsigned short* to16 = static_cast<unsigned short*>(g.a.out) + index * D;
@@ -557,10 +560,10 @@ __global__ void __launch_bounds__(32 * warps_of(D, CT), 1)
                         make_uint2(to_16x2(x.x, x.y, g.a.dtype), to_16x2(y.x, y.y, g.a.dtype));
             }
             if (gq != 0) continue;
-            if (!complete)  // (the joining kernel takes weights as 2^kShift p)
-                part[R * D + r] = m_run[ct] + (kShift - kFewBits), part[R * D + R + r] = l;
+            if (!complete)
+                part[R * D + r] = m_run[ct], part[R * D + R + r] = l * kLess;
             else if (g.a.lse)
-                g.a.lse[index] = l != 0.f ? ((m_run[ct] == -INFINITY ? 0.f : m_run[ct]) + lg2(l * kUnfew)) * kLn2
+                g.a.lse[index] = l != 0.f ? ((m_run[ct] == -INFINITY ? 0.f : m_run[ct]) + lg2(l)) * kLn2
                                           : -INFINITY;
         }
         pos += P.n;
@@ -617,6 +620,7 @@ cudaError_t kv4_attention_split_launch(const q4lin_kv4_cache_t& cache, const q4l
     if (!map_codes(&maps.k, cache, cache.k_codes) || !map_codes(&maps.v, cache, cache.v_codes))
         return cudaErrorInvalidValue;
     return in_groups(cache, a, rows_max, 4, c, [&](SplitArgs& g, const SplitSize& size) {
+        g.unshift = kMore;
         auto rows = [&](auto dim) {
             constexpr int D = decltype(dim)::value;
             if constexpr (D < 256)

@@ -6,7 +6,7 @@ import pytest
 from tests import _kv4 as kv4
 from tests import _operators as ops
 from tests.test_attention_gpu import check, status
-from tests.test_kv4_attention_gpu import BOTH, attend, handle, split  # noqa: F401 (fixtures)
+from tests.test_kv4_attention_gpu import BOTH, attend, check_rows, handle, some, split  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -45,4 +45,21 @@ def test_large_keys_that_are_not_seen(handle, split, dim, dtype):
     for plain, large in zip(results[:2], results[2:]):
         check(*plain, want, dtype)
         check(*large, want, dtype)
+    assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n,tokens", [(300, 70), (5000, 3), (5000, 40)])
+@pytest.mark.parametrize("power", [-100, 100, 126])
+def test_values_near_the_ends_of_the_range(handle, split, power, n, tokens, dim, dtype):
+    """Values up to 2^127, and of 2^-100: whole walks and cut ones."""
+    rng = np.random.default_rng(82)
+    host = kv4.Cache(rng, [n], 2, 32, dim)
+    host.vs *= np.float32(2.0**power)
+    q = ops.to_device(rng.standard_normal((tokens, 4, dim)).astype(np.float32), dtype)
+    for rows in BOTH:
+        split(rows)
+        out, lse = attend(handle, host, q, [tokens], [n], 0.125)
+        check_rows(out, lse, host, q, n, 0.125, some(rng, tokens, 4, 40), dtype)
     assert status(handle) == 0
