@@ -1,6 +1,6 @@
-// serving.cuh -- device helpers shared by the operators around the linears (kv_append.cu,
-// attention.cu, logprobs.cu): typed loads and stores, the position rotation, one-instruction
-// exp2 and log2, untiled bulk copies, the warp-level fp16 MMA.
+// serving.cuh -- device helpers shared by the operators around the linears (the caches' kernels,
+// attention, norms, log probabilities): typed loads and stores, the position rotation, one-instruction
+// exp2 and log2, untiled bulk copies, the warp-level fp16 MMA, widened codes.
 #pragma once
 
 #include <cuda_bf16.h>

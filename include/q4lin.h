@@ -103,8 +103,12 @@ typedef enum {
     Q4LIN_OPT_WAIT_LIMIT = 3,
     /* 1: launch with programmatic dependent launch, so a kernel may start streaming
      * its weights while the previous kernel on the stream drains (default 0).  The
-     * preceding kernel must not write this call's qweight or scales.  (The linears; the
-     * operators around them start when the previous call has ended.) */
+     * preceding kernel must not write this call's qweight or scales.  This is the linears'
+     * option.  Of the operators around them the norms, their gradient, the 4-bit cache's
+     * append and read and its attention of few query rows may always begin while the previous
+     * kernel drains, whatever it says: they wait for that kernel's end on the device before
+     * they touch memory, and let the next one begin no sooner than after that wait.  The
+     * others start when the previous call has ended. */
     Q4LIN_OPT_PDL = 4,
     /* Test hook, default 0.  1: the tensor-core kernel's copy engine skips the first
      * pipeline stage, the multi-row GEMV's copy engine issues nothing, and the attention
@@ -542,10 +546,14 @@ Q4LIN_API q4lin_status_t q4lin_run_kv4_read(q4lin_handle_t handle, const q4lin_k
 
 /* Attention over a 4-bit cache: as q4lin_run_attention in its arguments, checks, masks and
  * results.  Codes are exact in the tensor cores' fp16 operands here too; the keys' scales
- * multiply the scores and the values' scales the probabilities, in fp32.  One exception:
- * where bfloat16 outputs come from the kernel for many query rows, a value times its scale
- * (over the largest of the keys that its 256 rows, 128 of heads of 256, read, at most a power of two more) is
- * rounded to fp16 once, 11 bits like the probability that it meets. */
+ * multiply the scores and the values' scales the probabilities, in fp32, and these products
+ * enter as two terms that leave 2^-22 of the largest one among keys that the row sees: neither
+ * the scales of keys that it does not see nor those of values that are zero matter.  (In the
+ * kernel for many query rows, down to 2^-80 of the largest value scale among the keys that its
+ * 256 rows, 128 of heads of 256, read.)  One exception: where bfloat16 outputs come from that
+ * kernel, probabilities take one term, 11 bits, and while those value scales are within 2^24 of
+ * one another a value times its scale (over a power of two near the largest) is rounded to fp16
+ * once, 11 bits too. */
 Q4LIN_API q4lin_status_t q4lin_run_kv4_attention(q4lin_handle_t handle,
                                                  const q4lin_kv4_cache_t* cache,
                                                  const q4lin_attention_t* args, void* stream);
