@@ -126,7 +126,7 @@ __host__ __device__ constexpr int pair_rows_of(int64_t D) { return D == 256 ? kQ
 struct PromptArgs {
     q4lin_kv_cache_t cache;
     q4lin_attention_t a;
-    int page_shift, pair_rows;
+    int page_shift, pair_rows, bits;
     int64_t rows_min;  // sequences of more rows than this per key/value head are taken
     int q_vec;
     int slots, most_parts;  // CTAs that run at a time; parts of a walk at most
@@ -319,10 +319,10 @@ __device__ __forceinline__ Apart2 apart2(float2 ratio) {
     p.rest = fmul2(ratio, p.inverse);
     return p;
 }
-// m + log2(l); the exponent of an l far from 1 (of weights whose values' scales are far apart) is added apart,
-// as lg2's result would be rounded where m cancels it.
-__device__ __forceinline__ float log2_sum(float m, float l) {
-    if (!(l >= 4294967296.f && l <= 3.4028235e38f)) return m + lg2(l);
+// m + log2(l); over 4 bits with the exponent of an l above 2 (far above, where values' scales are far apart) added
+// apart, as lg2's result would be rounded where m cancels it.
+__device__ __forceinline__ float log2_sum(float m, float l, bool apart) {
+    if (!(apart && l >= 2.f && l <= 3.4028235e38f)) return m + lg2(l);
     const uint32_t bits = __float_as_uint(l);
     return m + (float)((int)(bits >> 23) - 127) + lg2(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
 }
@@ -1132,7 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
             if (in && cut) {
                 unit[pair_rows_of(D) * D + r] = m, unit[pair_rows_of(D) * (D + 1) + r] = l;
             } else if (in && g.a.lse) {
-                g.a.lse[index] = l != 0.f ? log2_sum(m == -INFINITY ? 0.f : m, l * kUnbase) * kLn2 : -INFINITY;
+                g.a.lse[index] = l != 0.f ? log2_sum(m == -INFINITY ? 0.f : m, l * kUnbase, BITS == 4) * kLn2 : -INFINITY;
             }
         }
     } else if (warp < kIssueWarp) {
@@ -1499,7 +1499,7 @@ __device__ __forceinline__ void join_rows(const PromptArgs& g, int64_t unit0, in
                 reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.a.out) + index * D)[unit4] =
                     make_uint2(to_16x2(o[q].x * inv, o[q].y * inv, g.a.dtype), to_16x2(o[q].z * inv, o[q].w * inv, g.a.dtype));
             if (unit4 == 0 && g.a.lse)
-                g.a.lse[index] = l[q] != 0.f ? log2_sum(mx[q] == -INFINITY ? 0.f : mx[q], l[q] * kUnbase) * kLn2 : -INFINITY;
+                g.a.lse[index] = l[q] != 0.f ? log2_sum(mx[q] == -INFINITY ? 0.f : mx[q], l[q] * kUnbase, g.bits == 4) * kLn2 : -INFINITY;
         }
     }
 }
@@ -1607,6 +1607,7 @@ cudaError_t prompt_launch(const q4lin_kv_cache_t& cache, const q4lin_attention_t
         g.a.offsets += b;
         g.a.lengths += b;
         g.page_shift = cache.page_size == 16 ? 4 : cache.page_size == 32 ? 5 : 6;
+        g.bits = BITS;
         g.rows_min = rows_min;
         g.q_vec = reinterpret_cast<uintptr_t>(a.query) % (4 * dtype_size(a.dtype)) == 0 &&
                   a.q_token_stride % 4 == 0 && a.q_head_stride % 4 == 0;

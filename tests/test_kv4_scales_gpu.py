@@ -112,3 +112,21 @@ def test_small_values_and_outputs_taken_out(handle, split):
     out, lse = attend(handle, host, q, [tokens], [n], 0.125)
     check_rows(out, lse, host, q, n, 0.125, some(rng, tokens, heads, 40), "f16")
     assert status(handle) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("seed", range(4))
+def test_log_sums_of_few_keys_with_values_far_apart(handle, split, seed, dim, dtype):
+    """Each row sees one key, whose value is up to 2^40 smaller than the largest, in whole walks and cut ones."""
+    rng = np.random.default_rng(76 + seed)
+    n = (300, 77, 500, 230)[seed]
+    host = kv4.Cache(rng, [n], 1, 32, dim)
+    host.vs *= (2.0**rng.integers(-40, 1, host.vs.shape)).astype(np.float32)
+    host.ks *= np.float32(0.3)
+    q = ops.to_device((rng.standard_normal((n, 7, dim)) * (1, 0.3, 0.1, 0.05)[seed]).astype(np.float32), dtype)
+    want = ops.attention(host, ops.to_host(q), [0, n], [n], dim**-0.5, window=1)
+    for rows in BOTH:
+        split(rows)
+        check(*attend(handle, host, q, [n], [n], dim**-0.5, window=1), want, dtype)
+    assert status(handle) == 0
