@@ -43,9 +43,9 @@
 // idle at this size, and each has about 10 us around it: the queries, the first keys, the rows.
 // Cutting the last round's walks so that all SMs end together took as long (239 us, and the
 // joining kernel's time on top): busier SMs were slower ones.
-// Over 4 bits, the same prompt: 270 us for bf16 queries as they are (QT 1), 308 us rotated, 402 us for
-// fp16, 567 us for fp32; heads of 64, bf16, 211 us; the last 820 of 8192 tokens with heads of 256 359, 438,
-// 531 and 685 us (on the kernel for few rows 1570).  The tensor pipes are busy for 35 % of the first:
+// Over 4 bits, the same prompt: 271 us for bf16 queries as they are (QT 1), 316 us rotated, 407 us for
+// fp16, 564 us for fp32; heads of 64, bf16, 215 us; the last 820 of 8192 tokens with heads of 256 365, 439,
+// 540 and 705 us (on the kernel for few rows 1570).  The tensor pipes are busy for 35 % of the first:
 // the softmax, with a scale for each key, and the widening take longer.  (With the values' scales multiplied
 // into the weights, as for the other types, 305 us; that without the keys' scales 267, without any 213.  Four
 // rows a thread, by loads of 16 rows, with an eighth of the reads of scales, against 279: 276 us, heads of 64

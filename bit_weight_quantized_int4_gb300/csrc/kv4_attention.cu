@@ -5,11 +5,11 @@
 // (attention_split.cuh); a warp works alone, with its own ring of copies.
 //
 // Bound: the codes and scales, head_dim + 8 bytes per key and key/value head; at half the bytes of an
-// 8-bit cache also the instructions of a tile, about 1100 a warp, 576 of which widen codes.  Measured (8
-// key/value heads of 128, 4 query heads each): 64 sequences of up to 8192 tokens, 347 MB, 73 us: 4.8
-// TB/s, 0.70 of a copy's bandwidth (without widening any code 62 us); one sequence of 131071 tokens, 143
-// MB, 38.6 us, 8 of it the start and the join; one of 701 tokens 8.7 us.  Heads of 64 / 256: 50 us (0.54)
-// and 127 us (0.78); eight and sixteen query heads a key head 109 and 194 us.
+// 8-bit cache also the instructions of a tile, about 1150 a warp, 576 of which widen codes.  Measured (8
+// key/value heads of 128, 4 query heads each): 64 sequences of up to 8192 tokens, 347 MB, 74.5 us: 4.7
+// TB/s, 0.69 of a copy's bandwidth (without widening any code 11 us less); one sequence of 131071 tokens, 143
+// MB, 39.3 us, 8 of it the start and the join; one of 701 tokens 8.7 us.  Heads of 64 / 256: 51 us (0.53)
+// and 127 us (0.78); eight and sixteen query heads a key head 108 and 205 us.
 //
 // Products on the tensor cores (m16n8k16, fp16 operands, fp32 sums), transposed: keys (channels of
 // the values) are the MMA's 16 rows, and a query row takes two of its 8 columns, the rounded value

@@ -253,7 +253,10 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_read_kernel(const ReadArgs g)
     }
 }
 
-// Tokens of a warp, up to eight: as many as leave `warps` warps.
+// Tokens of a warp, up to eight: as many as leave `warps` warps.  Measured, 8 heads of 128, one token a warp and as
+// many as leave 64, 32, 16, 8 warps an SM: append of 700 tokens in fp32 4.8, 4.8, 4.8, 4.3, 4.2 us, of 4510 17.1, 13.0,
+// 11.7, 11.6, 11.6, of 65536 in bf16 219, then 109; read of 700 in fp32 4.2, 4.2, 4.2, 4.6, 4.8, of 4510 16.4, 12.7,
+// 13.1, 13.7, 13.5 (in bf16 14.4, 8.9, 6.9, 6.9, 6.9), of 65536 in bf16 175, then 57.
 int tokens_each(int64_t tokens, int64_t warps_per_token, int64_t warps) {
     int each = 1;
     while (each < 8 && tokens * warps_per_token > 2 * each * warps) each *= 2;

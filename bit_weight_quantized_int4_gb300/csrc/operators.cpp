@@ -21,10 +21,17 @@ namespace {
 // 32 rows 112 / 149, 64 rows 181 / 147; fp32, 8 of 2000: 31 / 47 and 41 / 48).
 constexpr int64_t kSplitRows = 48;
 // Over a 4-bit cache the prompts' kernel is ahead earlier with bf16, whose products have one term
-// each (the same sizes: one sequence of 8192 keys, 32 rows 28.5 / 29.4, 48 rows 42.5 / 31.5; of 65536, 24
-// rows 88 / 88, 48 rows 124 / 88; 8 of 2000, 32 rows 41 / 52, 48 rows 64 / 56; 32 of 4000, 32 rows 165 /
-// 189, 48 rows 230 / 200; fp32, 48 rows: 41 / 38, 121 / 152, 61 / 70, 228 / 327; heads of 256, bf16, 32 rows 35 /
-// 39, 147 / 132, 63 / 58, 48 rows 52 / 41, 209 / 134, 89 / 61; fp32, 48 rows 48 / 52, 206 / 225, 84 / 82).
+// each.  Kernel for few rows / for prompts, us, one sequence of 8192 keys, one of 65536, 8 of 2000, 32 of 4000:
+//   bf16, 32 rows   heads of 64 21 / 25, 62 / 74, 30 / 44, 105 / 152   128 29 / 31, 97 / 89, 41 / 51, 175 / 183
+//                   256 36 / 43, 148 / 139, 64 / 62, 294 / 285
+//   bf16, 40 rows   64 31 / 26, 83 / 76, 44 / 46, 146 / 154   128 42 / 32, 129 / 90, 64 / 53, 238 / 187
+//                   256 48 / 44, 179 / 140, 76 / 63, 366 / 284
+//   fp16, 48 rows   64 32 / 29, 85 / 108, 46 / 53, 148 / 221   128 44 / 38, 131 / 146, 64 / 65, 245 / 283
+//                   256 52 / 49, 210 / 217, 90 / 77, 422 / 401
+//   fp16, 56 rows   64 30 / 29, 103 / 108, 42 / 54, 197 / 221   128 41 / 38, 161 / 147, 66 / 65, 317 / 284
+//                   256 52 / 50, 240 / 217, 87 / 78, 488 / 401
+//   fp32, 48 rows   64 30 / 31, 83 / 118, 44 / 56, 147 / 242   128 42 / 40, 128 / 157, 62 / 67, 243 / 312
+//                   256 49 / 53, 206 / 234, 83 / 84, 416 / 494
 constexpr int64_t kSplitRows4Bf16 = 32;
 
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
