@@ -653,7 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_prompt_kernel(const Pro
     if (warp == kIssueWarp) tmem_alloc(smem_u32(&S.tmem), kTmemCols);
     float v_max = 0.f;
     [[maybe_unused]] float v_min = INFINITY, k_max = 0.f;
-    const int page_first = max((step0 * kKeys) >> ps, page_low), page_last = min(pages, (step1 * kKeys) >> ps);
+    const int page_first = max((step0 * kKeys) >> ps, page_low);
+    const int page_last = (int)min((int64_t)pages, ((int64_t)step1 * kKeys) >> ps);  // (the last step may end past 2^31)
     if constexpr (BITS == 8) {
         for (int p = page_first + tid; p < page_last; p += kThreads) {
             const int id = __ldg(table + p);
